@@ -222,7 +222,6 @@ rq_status rq_decode_attention_noalloc(const rq_shape* shape, const rq_cache* cac
                                       const uint16_t* pending_kv, const int32_t* ctx_lens,
                                       int32_t max_ctx, uint16_t* out, void* stream);
 
-/* Human-readable name of a status. */
 /* Serving step support (rit.work summary, "How each pass's KV cache is reconstructed": the
  * current token's loops are encoded once its final loop ends, then it joins the cache).
  * Adds n to every ctx_lens[b] on the device, capped at capacity, so that a captured CUDA graph
@@ -232,6 +231,104 @@ rq_status rq_decode_attention_noalloc(const rq_shape* shape, const rq_cache* cac
 rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t capacity,
                          void* stream);
 
+/* Chunk attention: attention of several new tokens per sequence over the packed cache, one
+ * loop per call -- prompt chunks, verification of drafted tokens, and with n_new = 1 the
+ * single-token step of a caller that collects attention weights.  (rit.work summary, "How each
+ * pass's KV cache is reconstructed": loop l attends over loop l's rebuilt K/V while the new
+ * tokens' states are still BF16; the pages state the step for one token, this is the same step
+ * for a chunk.)  New token j of sequence b attends over the ctx_lens[b] cached tokens and the
+ * chunk's tokens 0..j.
+ *   q          bf16, element (b, j, hq, i) at b*q_strides[0] + j*q_strides[1] +
+ *              hq*q_strides[2] + i (strides in elements, non-negative)
+ *   loop       0 <= loop < n_loops
+ *   kv_new     the chunk's states, as rq_encode_append takes them: bf16 element
+ *              (b, j, kv, l, h, i) at b*kv_strides[0] + j*kv_strides[1] + kv*kv_strides[2] +
+ *              l*kv_strides[3] + h*kv_strides[4] + i; loop `loop` is read
+ *   n_lens     device int32 [B]: new tokens of each sequence, 0..n_new (a padded batch; what
+ *              lies behind a sequence's last token is never used), or NULL: n_new each
+ *   n_new      >= 0 (0: nothing enqueued)
+ *   ctx_lens, max_ctx  as in rq_decode_attention (max_ctx may be 0)
+ *   out        bf16 [B][n_new][Hq][d]; rows behind a sequence's last token are left as they were
+ *   weights    fp32 [B][Hkv][capacity], or NULL: the softmax weights of the last `window` new
+ *              tokens of each sequence (all of them if it has fewer), summed over their query
+ *              heads of the kv-head, are added: weights[b][h][t] += sum P for cached slots
+ *              t < ctx, and at t = ctx + j' for chunk token j' (the slot rq_encode_append gives
+ *              it; slots at or above capacity are dropped).  Sums are fp32 in a fixed order.
+ *   window     1..n_new with weights; 0 if and only if weights is NULL
+ *   ws         at least rq_chunk_workspace_bytes(...) bytes, 256-byte aligned; its first uint32
+ *              is the call's error word, as in rq_decode_attention: nonzero after a device-side
+ *              ctx_len outside [0, max_ctx], an n_len outside [0, n_new] (taken as n_new), a bad
+ *              block-table entry, or a pipeline wait that gave up.  The call's outputs are then
+ *              NaN, and its weights not to be used.  Calls that share a workspace must not
+ *              overlap on the GPU.
+ * A chunk token whose K or V row of the loop is not finite, or beyond fp16's largest number
+ * (the states' range everywhere in this library), makes the outputs of its own and of the
+ * sequence's later tokens NaN for the query heads of its kv-head; earlier tokens never see it.
+ * Scores, softmax statistics and accumulators are fp32. */
+size_t rq_chunk_workspace_bytes(const rq_shape* shape, int32_t loop, int32_t n_new,
+                                int32_t max_ctx, int32_t window);
+rq_status rq_chunk_attention(const rq_shape* shape, const rq_cache* cache, const uint16_t* q,
+                             const int64_t q_strides[3], int32_t loop, const uint16_t* kv_new,
+                             const int64_t kv_strides[5], const int32_t* n_lens, int32_t n_new,
+                             const int32_t* ctx_lens, int32_t max_ctx, uint16_t* out,
+                             float* weights, int32_t window, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* rq_chunk_attention on a paged cache (weights stay [B][Hkv][capacity], by logical slot). */
+rq_status rq_paged_chunk_attention(const rq_shape* shape, const rq_cache* cache,
+                                   const rq_paging* paging, const uint16_t* q,
+                                   const int64_t q_strides[3], int32_t loop,
+                                   const uint16_t* kv_new, const int64_t kv_strides[5],
+                                   const int32_t* n_lens, int32_t n_new, const int32_t* ctx_lens,
+                                   int32_t max_ctx, uint16_t* out, float* weights, int32_t window,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated attention weight (an interface choice: the pages shrink each token,
+ * not the number of tokens).  rq_evict_select names the slots of each (sequence, kv-head) to
+ * keep, rq_evict_compact moves their rows, of every loop, to the front of a cache.
+ *
+ * rq_evict_select: of the ctx = ctx_lens[b] slots of a (sequence, kv-head) kept_lens[b] =
+ * min(ctx, budget) are kept: the first n_first, the last n_last, then those of the largest
+ * weights; equal weights go to the lowest slot, +0 equals -0, NaN counts above every number.
+ *   weights    fp32 [batch][n_kv_heads][capacity]
+ *   budget     >= 1; n_first, n_last >= 0, n_first + n_last <= budget
+ *   keep       int32 [batch][n_kv_heads][budget]: the kept slots, ascending; entries at and
+ *              behind kept_lens[b] are left as they were
+ *   kept_lens  int32 [batch]: also the new ctx_lens after rq_evict_compact.  A ctx_len outside
+ *              [0, capacity] gives -1 and no entries (a decode call refuses that length). */
+rq_status rq_evict_select(const float* weights, int32_t batch, int32_t n_kv_heads,
+                          int32_t capacity, const int32_t* ctx_lens, int32_t budget,
+                          int32_t n_first, int32_t n_last, int32_t* keep, int32_t* kept_lens,
+                          void* stream);
+
+/* rq_evict_compact: row keep[b][h][t] of `cache` becomes row t of `to`, for t < kept_lens[b],
+ * every section (codes, step/offset, a).  `to_shape` equals `shape` but for capacity (and the
+ * query heads and softmax scale, which do not matter here); to's rotation signs are not written.
+ *   `to` may be the same cache (the same data pointer and capacity): then keep must ascend, as
+ *              rq_evict_select leaves it; other overlaps of the two buffers are not allowed.
+ *   keep       int32 [B][Hkv][budget], 1 <= budget; an entry outside [0, capacity) is never
+ *              dereferenced: its row is left as it was
+ *   kept_lens  int32 [B]; clamped to [0, min(budget, to_shape->capacity)]
+ *   weights, to_weights  fp32 [B][Hkv][capacity] of the two caches, or both NULL:
+ *              to_weights[t] = weights[keep[t]], and 0 from kept_lens[b] to to's capacity, so
+ *              that a new token starts at 0.  They are the same array exactly if the caches are.
+ * Rows of `to` behind kept_lens[b] are left as they were. */
+rq_status rq_evict_compact(const rq_shape* shape, const rq_cache* cache, const rq_shape* to_shape,
+                           const rq_cache* to, const int32_t* keep, int32_t budget,
+                           const int32_t* kept_lens, const float* weights, float* to_weights,
+                           void* stream);
+
+/* The same on paged caches.  In place: the same data, block table and page count (the pages
+ * behind the kept rows are then free); pages that several sequences share must not be
+ * compacted in place.  A block-table entry outside [0, n_pages) is never dereferenced: its rows
+ * are left as they were. */
+rq_status rq_paged_evict_compact(const rq_shape* shape, const rq_cache* cache,
+                                 const rq_paging* paging, const rq_shape* to_shape,
+                                 const rq_cache* to, const rq_paging* to_paging,
+                                 const int32_t* keep, int32_t budget, const int32_t* kept_lens,
+                                 const float* weights, float* to_weights, void* stream);
+
+/* Human-readable name of a status. */
 const char* rq_status_str(rq_status status);
 
 #ifdef __cplusplus

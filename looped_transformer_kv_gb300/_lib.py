@@ -19,7 +19,9 @@ EXPORTS = ("rq_cache_bytes", "rq_record_bytes", "rq_encode_append", "rq_decode_w
            "rq_decode_attention_noalloc", "rq_paged_cache_bytes", "rq_paged_encode_append",
            "rq_paged_decode_attention", "rq_advance_ctx",
            "rq_test_decode_attention_wait_runs_out", "rq_ablation_encode_append",
-           "rq_ablation_decode_attention")
+           "rq_ablation_decode_attention", "rq_chunk_workspace_bytes", "rq_chunk_attention",
+           "rq_paged_chunk_attention", "rq_evict_select", "rq_evict_compact",
+           "rq_paged_evict_compact")
 
 
 class RqShape(ctypes.Structure):
@@ -101,6 +103,20 @@ def lib():
     L.rq_ablation_decode_attention.restype = i32
     L.rq_advance_ctx.argtypes = [_P, i32, i32, i32, _P]
     L.rq_advance_ctx.restype = i32
+    I = ctypes.POINTER(i64)
+    L.rq_chunk_workspace_bytes.argtypes = [S, i32, i32, i32, i32]
+    L.rq_chunk_workspace_bytes.restype = sz
+    chunk = [_P, I, i32, _P, I, _P, i32, _P, i32, _P, _P, i32, _P, sz, _P]
+    L.rq_chunk_attention.argtypes = [S, C] + chunk
+    L.rq_chunk_attention.restype = i32
+    L.rq_paged_chunk_attention.argtypes = [S, C, G] + chunk
+    L.rq_paged_chunk_attention.restype = i32
+    L.rq_evict_select.argtypes = [_P, i32, i32, i32, _P, i32, i32, i32, _P, _P, _P]
+    L.rq_evict_select.restype = i32
+    L.rq_evict_compact.argtypes = [S, C, S, C, _P, i32, _P, _P, _P, _P]
+    L.rq_evict_compact.restype = i32
+    L.rq_paged_evict_compact.argtypes = [S, C, G, S, C, G, _P, i32, _P, _P, _P, _P]
+    L.rq_paged_evict_compact.restype = i32
     L.rq_status_str.argtypes = [i32]
     L.rq_status_str.restype = ctypes.c_char_p
     P = ctypes.POINTER(RqSynthParams)

@@ -131,6 +131,107 @@ rq_status decode_common(const rq_shape* shape, const rq_cache* cache, const rq_p
   }
 }
 
+// Strides of a chunk call's q or kv_new: non-negative, and every element's offset in 63 bits.
+bool strides_ok(const int64_t* strides, const int64_t* extents, int n) {
+  int64_t last = 0;
+  for (int i = 0; i < n; ++i) {
+    if (strides[i] < 0) return false;
+    const int64_t steps = extents[i] > 0 ? extents[i] - 1 : 0;
+    if (steps > 0 && strides[i] > (INT64_MAX / 4 - last) / steps) return false;
+    last += steps * strides[i];
+  }
+  return true;
+}
+
+// Sizes a chunk call may have, without its pointers.
+rq_status check_chunk_sizes(const rq_shape* s, int32_t loop, int32_t n_new, int32_t max_ctx,
+                            int32_t window) {
+  if (loop < 0 || loop >= s->n_loops || n_new < 0) return RQ_ERR_INVALID_ARG;
+  if (max_ctx < 0 || max_ctx > s->capacity) return RQ_ERR_INVALID_ARG;
+  if (window < 0 || window > n_new) return RQ_ERR_INVALID_ARG;
+  if (int64_t(max_ctx) + n_new > (int64_t(1) << 30)) return RQ_ERR_UNSUPPORTED;
+  if (int64_t(s->batch) * s->n_q_heads * (n_new > 0 ? n_new : 1) > (int64_t(1) << 31))
+    return RQ_ERR_UNSUPPORTED;
+  return RQ_OK;
+}
+
+rq_status chunk_common(const rq_shape* shape, const rq_cache* cache, const rq_paging* paging,
+                       const rq::ChunkCall& c, void* ws, size_t ws_bytes, void* stream) {
+  rq_status st = check_shape(shape);
+  if (st != RQ_OK) return st;
+  if ((st = check_cache(shape, cache)) != RQ_OK) return st;
+  if (paging && (st = check_paging(shape, paging)) != RQ_OK) return st;
+  if (!c.ctx_lens || (c.n_new != 0 && (!c.q || !c.kv_new || !c.out))) return RQ_ERR_INVALID_ARG;
+  if ((c.weights != nullptr) != (c.window > 0) && c.n_new > 0) return RQ_ERR_INVALID_ARG;
+  if ((st = check_chunk_sizes(shape, c.loop, c.n_new, c.max_ctx, c.window)) != RQ_OK) return st;
+  const int64_t qe[3] = {shape->batch, c.n_new, shape->n_q_heads};
+  const int64_t ke[5] = {shape->batch, c.n_new, 2, shape->n_loops, shape->n_kv_heads};
+  if (!strides_ok(c.q_strides, qe, 3) || !strides_ok(c.kv_strides, ke, 5)) return RQ_ERR_INVALID_ARG;
+  if (c.n_new == 0) return RQ_OK;
+  if (!ws || ws_bytes < rq_chunk_workspace_bytes(shape, c.loop, c.n_new, c.max_ctx, c.window))
+    return RQ_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RQ_ERR_WORKSPACE;
+  try {
+    return from_cuda(rq::launch_chunk(*shape, *cache, paging, c, ws, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return RQ_ERR_INTERNAL;
+  }
+}
+
+bool make_chunk_call(rq::ChunkCall& c, const uint16_t* q, const int64_t* q_strides, int32_t loop,
+                     const uint16_t* kv_new, const int64_t* kv_strides, const int32_t* n_lens,
+                     int32_t n_new, const int32_t* ctx_lens, int32_t max_ctx, uint16_t* out,
+                     float* weights, int32_t window) {
+  if (!q_strides || !kv_strides) return false;
+  c = {q, {}, loop, kv_new, {}, n_lens, n_new, ctx_lens, max_ctx, out, weights, window};
+  for (int i = 0; i < 3; ++i) c.q_strides[i] = q_strides[i];
+  for (int i = 0; i < 5; ++i) c.kv_strides[i] = kv_strides[i];
+  return true;
+}
+
+rq_status compact_common(const rq_shape* shape, const rq_cache* cache, const rq_paging* paging,
+                         const rq_shape* to_shape, const rq_cache* to, const rq_paging* to_paging,
+                         const int32_t* keep, int32_t budget, const int32_t* kept_lens,
+                         const float* weights, float* to_weights, void* stream) {
+  rq_status st = check_shape(shape);
+  if (st != RQ_OK) return st;
+  if ((st = check_shape(to_shape)) != RQ_OK) return st;
+  if ((st = check_cache(shape, cache)) != RQ_OK) return st;
+  if ((st = check_cache(to_shape, to)) != RQ_OK) return st;
+  if (paging && ((st = check_paging(shape, paging)) != RQ_OK ||
+                 (st = check_paging(to_shape, to_paging)) != RQ_OK))
+    return st;
+  if (!keep || !kept_lens || budget < 1) return RQ_ERR_INVALID_ARG;
+  if (shape->batch != to_shape->batch || shape->n_kv_heads != to_shape->n_kv_heads ||
+      shape->head_dim != to_shape->head_dim || shape->n_loops != to_shape->n_loops)
+    return RQ_ERR_INVALID_ARG;
+  for (int l = 0; l < shape->n_loops - 1; ++l)
+    if (shape->res_bits[l] != to_shape->res_bits[l]) return RQ_ERR_INVALID_ARG;
+  bool in_place = cache->data == to->data && shape->capacity == to_shape->capacity;
+  if (paging) {
+    in_place = in_place && paging->block_table == to_paging->block_table &&
+               paging->n_pages == to_paging->n_pages;
+  } else if (!in_place) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(cache->data), a1 = a0 + rq_cache_bytes(shape);
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(to->data), b1 = b0 + rq_cache_bytes(to_shape);
+    if (a0 < b1 && b0 < a1) return RQ_ERR_INVALID_ARG;
+  }
+  if ((weights != nullptr) != (to_weights != nullptr)) return RQ_ERR_INVALID_ARG;
+  if (weights) {
+    const size_t per = sizeof(float) * shape->batch * size_t(shape->n_kv_heads);
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(weights), a1 = a0 + per * shape->capacity;
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(to_weights), b1 = b0 + per * to_shape->capacity;
+    if (in_place ? a0 != b0 : (a0 < b1 && b0 < a1)) return RQ_ERR_INVALID_ARG;
+  }
+  try {
+    return from_cuda(rq::launch_evict_compact(*shape, *cache, paging, *to_shape, *to, to_paging,
+                                              in_place, keep, budget, kept_lens, weights, to_weights,
+                                              static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return RQ_ERR_INTERNAL;
+  }
+}
+
 }  // namespace
 
 namespace rq {
@@ -277,6 +378,75 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
   advance_ctx_kernel<<<(batch + 127) / 128, 128, 0, static_cast<cudaStream_t>(stream)>>>(
       ctx_lens, batch, n, capacity);
   return from_cuda(cudaGetLastError());
+}
+
+size_t rq_chunk_workspace_bytes(const rq_shape* s, int32_t loop, int32_t n_new, int32_t max_ctx,
+                                int32_t window) {
+  if (check_shape(s) != RQ_OK || check_chunk_sizes(s, loop, n_new, max_ctx, window) != RQ_OK) return 0;
+  return rq::chunk_workspace_bytes(*s, loop, n_new, max_ctx, window);
+}
+
+rq_status rq_chunk_attention(const rq_shape* shape, const rq_cache* cache, const uint16_t* q,
+                             const int64_t q_strides[3], int32_t loop, const uint16_t* kv_new,
+                             const int64_t kv_strides[5], const int32_t* n_lens, int32_t n_new,
+                             const int32_t* ctx_lens, int32_t max_ctx, uint16_t* out,
+                             float* weights, int32_t window, void* ws, size_t ws_bytes,
+                             void* stream) {
+  rq::ChunkCall c;
+  if (!make_chunk_call(c, q, q_strides, loop, kv_new, kv_strides, n_lens, n_new, ctx_lens, max_ctx,
+                       out, weights, window))
+    return RQ_ERR_INVALID_ARG;
+  return chunk_common(shape, cache, nullptr, c, ws, ws_bytes, stream);
+}
+
+rq_status rq_paged_chunk_attention(const rq_shape* shape, const rq_cache* cache,
+                                   const rq_paging* paging, const uint16_t* q,
+                                   const int64_t q_strides[3], int32_t loop,
+                                   const uint16_t* kv_new, const int64_t kv_strides[5],
+                                   const int32_t* n_lens, int32_t n_new, const int32_t* ctx_lens,
+                                   int32_t max_ctx, uint16_t* out, float* weights, int32_t window,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  rq::ChunkCall c;
+  if (!paging || !make_chunk_call(c, q, q_strides, loop, kv_new, kv_strides, n_lens, n_new, ctx_lens,
+                                  max_ctx, out, weights, window))
+    return RQ_ERR_INVALID_ARG;
+  return chunk_common(shape, cache, paging, c, ws, ws_bytes, stream);
+}
+
+rq_status rq_evict_select(const float* weights, int32_t batch, int32_t n_kv_heads,
+                          int32_t capacity, const int32_t* ctx_lens, int32_t budget,
+                          int32_t n_first, int32_t n_last, int32_t* keep, int32_t* kept_lens,
+                          void* stream) {
+  if (!weights || !ctx_lens || !keep || !kept_lens) return RQ_ERR_INVALID_ARG;
+  if (batch <= 0 || n_kv_heads <= 0 || capacity <= 0 || budget < 1 || n_first < 0 || n_last < 0 ||
+      int64_t(n_first) + n_last > budget)
+    return RQ_ERR_INVALID_ARG;
+  if (capacity > (1 << 30) || int64_t(batch) * n_kv_heads > (1 << 27)) return RQ_ERR_UNSUPPORTED;
+  try {
+    return from_cuda(rq::launch_evict_select(weights, batch, n_kv_heads, capacity, ctx_lens, budget,
+                                             n_first, n_last, keep, kept_lens,
+                                             static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return RQ_ERR_INTERNAL;
+  }
+}
+
+rq_status rq_evict_compact(const rq_shape* shape, const rq_cache* cache, const rq_shape* to_shape,
+                           const rq_cache* to, const int32_t* keep, int32_t budget,
+                           const int32_t* kept_lens, const float* weights, float* to_weights,
+                           void* stream) {
+  return compact_common(shape, cache, nullptr, to_shape, to, nullptr, keep, budget, kept_lens,
+                        weights, to_weights, stream);
+}
+
+rq_status rq_paged_evict_compact(const rq_shape* shape, const rq_cache* cache,
+                                 const rq_paging* paging, const rq_shape* to_shape,
+                                 const rq_cache* to, const rq_paging* to_paging,
+                                 const int32_t* keep, int32_t budget, const int32_t* kept_lens,
+                                 const float* weights, float* to_weights, void* stream) {
+  if (!paging || !to_paging) return RQ_ERR_INVALID_ARG;
+  return compact_common(shape, cache, paging, to_shape, to, to_paging, keep, budget, kept_lens,
+                        weights, to_weights, stream);
 }
 
 const char* rq_status_str(rq_status s) {

@@ -1,0 +1,216 @@
+// Chunk attention (rq_chunk_attention): host side, combine and weights.
+//
+// A row is one (new token j, query head g) of a kv-head: row = j * heads + g.  The rows take the
+// decode kernel's chunk variants (rq_decode_mma.cuh): the cache is streamed once per block of 8
+// rows, and the combine below merges the splits and adds the chunk's own tokens, causally.
+#include "rq_common.cuh"
+#include "rq_kernels.h"
+
+namespace rq {
+namespace {
+
+constexpr float kStateMax = 65504.f;   // largest fp16: the states' range
+
+struct TailArgs {
+  const uint16_t* q;
+  const uint16_t* kv_new;    // K rows of the call's loop; V rows at + kv_v
+  int64_t qs0, qs1, qs2, ks0, ks1, kv_v, ks_h;
+  const int32_t* n_lens;
+  const int32_t* ctx_lens;
+  const int8_t* vsigns;      // null: final loop (no residual part)
+  const float* part;
+  const unsigned* err;
+  uint16_t* out;
+  float* scores;             // [B][H][window * heads][score_stride], or null
+  float* lse;                // [B][H][window * heads], log2 units
+  float* weights;
+  int64_t score_stride;
+  int B, H, heads, n_new, n_splits, window, cap, max_ctx;
+  float scale_log2;
+};
+
+// One warp per row: merge the split partials, then the chunk's tokens 0..j one by one (online
+// softmax), undo the rotation, store bf16.  Rows whose weights are asked for also store the
+// chunk tokens' scores and their log2-sum-exp.  Latency-bound: j + 1 dependent dot products.
+template <int D>
+__global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constant__ TailArgs a) {
+  constexpr int P = D / 32;
+  constexpr int rec = 4 + 2 * D;
+  const int lane = threadIdx.x & 31;
+  const int rows = a.n_new * a.heads;
+  const int64_t wid = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (wid >= int64_t(a.B) * a.H * rows) return;
+  const int row = int(wid % rows), h = int(wid / rows % a.H), b = int(wid / rows / a.H);
+  const int j = row / a.heads, g = row % a.heads;
+  int n_len = a.n_lens ? a.n_lens[b] : a.n_new;
+  bool bad = *a.err != 0u;
+  if (n_len < 0 || n_len > a.n_new) {   // (the error word is set: every row of the sequence)
+    n_len = a.n_new;
+    bad = true;
+  }
+  if (j >= n_len) return;
+  uint16_t* o = a.out + ((int64_t(b) * a.n_new + j) * a.H * a.heads + h * a.heads + g) * D + lane * P;
+  const int first = max(0, n_len - a.window) * a.heads;
+  const int64_t wrow = (int64_t(b) * a.H + h) * a.window * a.heads + row - first;
+  const bool voted = a.scores && row >= first;
+  float M = -INFINITY, ell = 0.f, ar[P], ae[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) ar[i] = ae[i] = 0.f;
+  if (!bad) {
+    const float* part = a.part + wid * a.n_splits * rec;
+    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, part[int64_t(s) * rec]);
+    for (int s = 0; s < a.n_splits; ++s) {
+      const float* ps = part + int64_t(s) * rec;
+      if (ps[0] == -INFINITY) continue;
+      const float f = exp2f(ps[0] - M);
+      ell = fmaf(f, ps[1], ell);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        ar[i] = fmaf(f, ps[4 + lane * P + i], ar[i]);
+        ae[i] = fmaf(f, ps[4 + D + lane * P + i], ae[i]);
+      }
+    }
+    float qv[P];
+    const uint16_t* qp = a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.heads + g) * a.qs2 + lane * P;
+#pragma unroll
+    for (int i = 0; i < P; ++i) qv[i] = bf16_bits_to_float(qp[i]) * a.scale_log2;
+    for (int t = 0; t <= j; ++t) {
+      const uint16_t* kp = a.kv_new + b * a.ks0 + t * a.ks1 + h * a.ks_h + lane * P;
+      const uint16_t* vp = kp + a.kv_v;
+      float s = 0.f, v[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float k = bf16_bits_to_float(kp[i]);
+        v[i] = bf16_bits_to_float(vp[i]);
+        bad |= !(fabsf(k) <= kStateMax) || !(fabsf(v[i]) <= kStateMax);
+        s = fmaf(qv[i], k, s);
+      }
+      s = warp_sum(s);
+      if (voted && lane == 0) a.scores[wrow * a.score_stride + a.ctx_lens[b] + t] = s;
+      const float m = fmaxf(M, s), f0 = exp2f(M - m), f1 = exp2f(s - m);   // (s is finite)
+      ell = fmaf(ell, f0, f1);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        ar[i] = fmaf(ar[i], f0, f1 * v[i]);
+        ae[i] *= f0;
+      }
+      M = m;
+    }
+    bad = __any_sync(RQ_FULL_MASK, bad);
+  }
+  if (a.vsigns) {
+    warp_fwht<P>(ae, lane);
+    const float inv_sqrt_d = (D == 128) ? 0.08838834764831845f : 0.125f;
+    const int8_t* sg = a.vsigns + int64_t(h) * D + lane * P;
+#pragma unroll
+    for (int i = 0; i < P; ++i) ar[i] = fmaf(ae[i] * inv_sqrt_d, float(sg[i]), ar[i]);
+  }
+  const float nan = __int_as_float(0x7fc00000);
+  const float inv = bad ? nan : 1.f / ell;
+#pragma unroll
+  for (int i = 0; i < P; ++i) o[i] = float_to_bf16_bits(ar[i] * inv);
+  if (voted && lane == 0) a.lse[wrow] = bad ? nan : M + log2f(ell);
+}
+
+// One thread per slot: the weights of the window's rows, in row order.
+__global__ void __launch_bounds__(128) chunk_weights_kernel(const __grid_constant__ TailArgs a) {
+  const int t = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int n_len = a.n_lens ? a.n_lens[b] : a.n_new, ctx = a.ctx_lens[b];
+  if (n_len < 0 || n_len > a.n_new || ctx < 0 || ctx > a.max_ctx) return;   // (flagged)
+  if (t >= ctx + n_len || t >= a.cap) return;
+  const int first = max(0, n_len - a.window);
+  const int64_t base = (int64_t(b) * a.H + h) * a.window * a.heads;
+  const int n = (n_len - first) * a.heads;
+  const int from = t < ctx ? 0 : max(0, t - ctx - first) * a.heads;   // chunk token t - ctx: rows j >= it
+  float w = 0.f;
+  for (int r = from; r < n; ++r)
+    w += exp2f(a.scores[(base + r) * a.score_stride + t] - a.lse[base + r]);
+  a.weights[(int64_t(b) * a.H + h) * a.cap + t] += w;
+}
+
+// Workspace of a call with few rows: header, partial records, then (with weights) the scores and
+// log2-sum-exps of the window's rows.
+struct RowsLayout {
+  SplitPlan plan;
+  size_t part, scores, lse, total;
+  int64_t score_stride;
+};
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
+  RowsLayout l;
+  const int heads = s.n_q_heads / s.n_kv_heads;
+  l.plan = plan_splits_chunk(s, loop, heads * n_new, max_ctx);
+  const size_t units = size_t(s.batch) * s.n_kv_heads;
+  size_t o = kWsHeaderBytes;
+  l.part = o;
+  o = round256(o + units * heads * n_new * l.plan.n_splits * partial_floats(s) * sizeof(float));
+  l.score_stride = (int64_t(max_ctx) + n_new + 31) / 32 * 32;
+  l.scores = o;
+  o = round256(o + units * heads * window * size_t(l.score_stride) * sizeof(float));
+  l.lse = o;
+  o = round256(o + units * heads * window * sizeof(float));
+  l.total = o;
+  return l;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
+  return rows_layout(s, loop, n_new, max_ctx, window).total;
+}
+
+cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                         const ChunkCall& c, void* ws, cudaStream_t stream) {
+  char* const w = static_cast<char*>(ws);
+  unsigned* err = reinterpret_cast<unsigned*>(w);
+  cudaError_t e = cudaMemsetAsync(w, 0, kWsHeaderBytes, stream);
+  if (e != cudaSuccess) return e;
+  const RowsLayout l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window);
+  float* const scores = c.weights ? reinterpret_cast<float*>(w + l.scores) : nullptr;
+  e = launch_chunk_mma(s, cache, paging, c, l.plan, reinterpret_cast<float*>(w + l.part), scores,
+                       l.score_stride, err, stream);
+  if (e != cudaSuccess) return e;
+  TailArgs a;
+  a.q = c.q;
+  a.kv_new = c.kv_new + c.loop * c.kv_strides[3];
+  a.qs0 = c.q_strides[0];
+  a.qs1 = c.q_strides[1];
+  a.qs2 = c.q_strides[2];
+  a.ks0 = c.kv_strides[0];
+  a.ks1 = c.kv_strides[1];
+  a.kv_v = c.kv_strides[2];
+  a.ks_h = c.kv_strides[4];
+  a.n_lens = c.n_lens;
+  a.ctx_lens = c.ctx_lens;
+  a.vsigns = c.loop < s.n_loops - 1 ? cache.rot_signs[1] : nullptr;
+  a.part = reinterpret_cast<const float*>(w + l.part);
+  a.err = err;
+  a.out = c.out;
+  a.scores = scores;
+  a.lse = reinterpret_cast<float*>(w + l.lse);
+  a.weights = c.weights;
+  a.score_stride = l.score_stride;
+  a.B = s.batch;
+  a.H = s.n_kv_heads;
+  a.heads = s.n_q_heads / s.n_kv_heads;
+  a.n_new = c.n_new;
+  a.n_splits = l.plan.n_splits;
+  a.window = c.window;
+  a.cap = s.capacity;
+  a.max_ctx = c.max_ctx;
+  const float scale = s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim));
+  a.scale_log2 = scale * kLog2e;
+  const int64_t warps = int64_t(s.batch) * s.n_q_heads * c.n_new;
+  if (s.head_dim == 128)
+    chunk_combine_kernel<128><<<unsigned((warps + 3) / 4), 128, 0, stream>>>(a);
+  else
+    chunk_combine_kernel<64><<<unsigned((warps + 3) / 4), 128, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || !c.weights) return e;
+  const dim3 grid((c.max_ctx + c.n_new + 127) / 128, s.n_kv_heads, s.batch);
+  chunk_weights_kernel<<<grid, 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace rq

@@ -198,6 +198,111 @@ SplitPlan plan_splits_rq(const rq_shape& s, int loop_begin, int loop_count, int 
   return plan_splits_for(s, max_ctx, ctas > 0 ? ctas : 1, kT);
 }
 
+// ---------------------------------------------------------------------------- chunk calls
+// Few rows: blocks of at most 8 rows, each with its own CTAs over the cache's splits.
+
+namespace {
+
+KernelFn pick_chunk_any(int D, bool res4, int nr, bool paged, int pk) {
+  return paged ? pick_chunk_paged(D, res4, nr, pk) : pick_chunk(D, res4, nr, pk);
+}
+
+cudaError_t prepare_chunk_kernels() {
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaSuccess;
+    for (int D : {64, 128})
+      for (int kind = 0; kind < 3; ++kind)   // the final loop, a 2-bit and a 4-bit residual loop
+        for (int v = 0; v < 6; ++v) {
+          cudaError_t e = cudaFuncSetAttribute(pick_chunk_any(D, kind == 2, kind > 0, v >= 3, v % 3),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               200 * 1024);
+          if (e != cudaSuccess) err[dev] = e;
+        }
+  });
+  return err[dev];
+}
+
+// The block of rows every launch of a chunk call repeats.
+QueryBlock chunk_block(const rq_shape& s, int loop, int rows) {
+  QueryBlock bq;
+  bq.gi0 = 0;
+  bq.gw = 1;
+  while (bq.gw < rows && bq.gw < kNQ) bq.gw <<= 1;
+  bq.lb = loop;
+  bq.nl = 1;
+  bq.r0 = loop;
+  bq.nr = loop < s.n_loops - 1 ? 1 : 0;
+  return bq;
+}
+
+}  // namespace
+
+SplitPlan plan_splits_chunk(const rq_shape& s, int loop, int rows, int max_ctx) {
+  const QueryBlock bq = chunk_block(s, loop, rows);
+  rq_cache dummy;
+  memset(&dummy, 0, sizeof(dummy));
+  BlockLaunch bl;
+  int ctas = 1;
+  if (build_block(s, dummy, bq, 0, bl))
+    ctas = resident_ctas(s.head_dim, bl.res4, bq.nr, block_packing(bq), bl.smem);
+  rq_shape units = s;   // every block of rows is a unit of its own
+  units.n_kv_heads *= (rows + bq.gw - 1) / bq.gw;
+  return plan_splits_for(units, max_ctx, ctas, kT);
+}
+
+cudaError_t launch_chunk_mma(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                             const ChunkCall& c, const SplitPlan& plan, float* part, float* scores,
+                             int64_t score_stride, unsigned* err, cudaStream_t stream) {
+  cudaError_t e = prepare_chunk_kernels();
+  if (e != cudaSuccess) return e;
+  const int heads = s.n_q_heads / s.n_kv_heads, rows = heads * c.n_new;
+  const QueryBlock bq = chunk_block(s, c.loop, rows);
+  const int n_pg = paging ? plan.tokens_per_split / kT : 0;
+  BlockLaunch bl;
+  if (!build_block(s, cache, bq, n_pg, bl)) return cudaErrorInvalidConfiguration;
+  MmaArgs& a = bl.a;
+  a.bt = paging ? paging->block_table : nullptr;
+  a.max_pages = paging ? paging->max_pages : 0;
+  a.n_pages = paging ? paging->n_pages : 0;
+  a.ksigns = cache.rot_signs[0];
+  a.vsigns = cache.rot_signs[1];
+  a.q = c.q;
+  a.ctx_lens = c.ctx_lens;
+  a.part = part;
+  a.err = err;
+  a.B = s.batch;
+  a.Hq = s.n_kv_heads * rows;
+  a.H = s.n_kv_heads;
+  a.L = s.n_loops;
+  a.cap = s.capacity;
+  a.g = rows;
+  a.loop_begin = c.loop;
+  a.loop_count = 1;
+  a.n_splits = plan.n_splits;
+  a.tokens_per_split = plan.tokens_per_split;
+  const float scale = s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim));
+  a.scale_log2 = scale * kLog2e;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.n_blocks = (rows + bq.gw - 1) / bq.gw;
+  a.heads = heads;
+  a.n_new = c.n_new;
+  a.window = c.window;
+  a.max_ctx = c.max_ctx;
+  a.qs0 = c.q_strides[0];
+  a.qs1 = c.q_strides[1];
+  a.qs2 = c.q_strides[2];
+  a.n_lens = c.n_lens;
+  a.scores = scores;
+  a.score_stride = score_stride;
+  dim3 grid(unsigned(plan.n_splits) * a.n_blocks, s.n_kv_heads, s.batch);
+  pick_chunk_any(s.head_dim, bl.res4, bq.nr, paging != nullptr, block_packing(bq))<<<grid, kW * 32, bl.smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_rq_decode_mma(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
                                  const uint16_t* q, int loop_begin, int loop_count,
                                  const int32_t* ctx_lens, int n_splits, int tokens_per_split,

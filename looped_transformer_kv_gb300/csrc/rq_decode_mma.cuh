@@ -80,6 +80,14 @@ struct MmaArgs {
   int off_kc, off_km, off_vc, off_vm;
   int off_krc[kMaxResPerBlock], off_krm[kMaxResPerBlock], off_ka[kMaxResPerBlock];
   int off_vrc[kMaxResPerBlock], off_vrm[kMaxResPerBlock], off_va[kMaxResPerBlock];
+  // chunk variants (CHUNK): the query columns of a kv-head are the rows (new token j, query
+  // head gi of the kv-head), row = j * heads + gi; blk is the launch's first block, and every
+  // block of blk.gw rows has its own CTAs
+  int n_blocks, heads, n_new, window, max_ctx;
+  int64_t qs0, qs1, qs2;       // element strides of q
+  const int32_t* n_lens;       // new tokens of each sequence, or null (n_new each)
+  float* scores;               // [B][H][window * heads][score_stride] (log2 units), or null
+  int64_t score_stride;
 };
 
 using KernelFn = void (*)(MmaArgs);
@@ -216,7 +224,9 @@ __device__ __forceinline__ void weights_to_b_packed(float w00, float w01, float 
 // 0 = the method; 1 = a fixed at 1 (the a rows are not read); 2 = direct quantisation of the
 // loop (the reference is neither copied nor read: the score and the value are the loop's own
 // codes alone, a = 0).
-template <int D, bool RES4, int NRT, bool PAGED, int PK, int MODE = 0>
+// CHUNK: the columns are the rows of a chunk call (MmaArgs), one loop, no in-kernel combine; the
+// scores of the rows whose weights are asked for are stored as well.
+template <int D, bool RES4, int NRT, bool PAGED, int PK, int MODE = 0, bool CHUNK = false>
 __global__ void __launch_bounds__(kW * 32, (NRT == 0 || (PK == 2 && !RES4)) ? 4 : 3) rq_mma_kernel(const __grid_constant__ MmaArgs a) {
   constexpr int NG = D / 32;
   constexpr int NQ = kNQ;
@@ -236,8 +246,19 @@ __global__ void __launch_bounds__(kW * 32, (NRT == 0 || (PK == 2 && !RES4)) ? 4 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const QueryBlock blk = a.blk;
+  const int split = CHUNK ? blockIdx.x / a.n_blocks : blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  QueryBlock blk = a.blk;
+  int n_len = 0;               // CHUNK: new tokens of the sequence
+  if constexpr (CHUNK) {
+    blk.gi0 += (blockIdx.x % a.n_blocks) * blk.gw;
+    n_len = a.n_lens ? a.n_lens[b] : a.n_new;
+    const int n_ctx = a.ctx_lens[b];
+    if (n_len < 0 || n_len > a.n_new || n_ctx < 0 || n_ctx > a.max_ctx) {
+      if (threadIdx.x == 0) atomicOr(a.err, 1u);
+      return;
+    }
+    if (n_len * a.heads <= blk.gi0) return;   // no row of the block is a token's
+  }
   const int nr = NRT >= 0 ? NRT : blk.nr;
 
   // Stage layout (byte offsets within a stage, the order of the cache's tile records): K
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(kW * 32, (NRT == 0 || (PK == 2 && !RES4)) ? 4 
   // combine kernel: for them the fence at every CTA's end and the combine on the tail cost
   // more than the launch it saves.
   auto combine_if_last = [&]() {
-    if constexpr (!SC) return;
+    if constexpr (!SC || CHUNK) return;
     if (!a.tickets) return;   // (a call with other blocks: the combine kernel merges)
     __syncthreads();
     bool last = false;
@@ -383,13 +404,18 @@ __global__ void __launch_bounds__(kW * 32, (NRT == 0 || (PK == 2 && !RES4)) ? 4 
   auto prep_column = [&](int n, float (&v)[P], float (&rr)[P]) {
     const int li = n / blk.gw;
     const int gi = blk.gi0 + n % blk.gw;
-    const bool real = li < blk.nl && gi < a.g;
+    const bool real = li < blk.nl && (CHUNK ? gi < n_len * a.heads : gi < a.g);
     const int l = blk.lb + li;
     const int8_t* sg = a.ksigns + int64_t(h) * D + lane * P;
     if (real) {
-      const uint16_t* qp =
-          a.q + ((int64_t(b) * a.Hq + int64_t(h) * a.g + gi) * a.loop_count + (l - a.loop_begin)) * D +
-          lane * P;
+      const uint16_t* qp;
+      if constexpr (CHUNK)
+        qp = a.q + b * a.qs0 + (gi / a.heads) * a.qs1 + (int64_t(h) * a.heads + gi % a.heads) * a.qs2 +
+             lane * P;
+      else
+        qp = a.q +
+             ((int64_t(b) * a.Hq + int64_t(h) * a.g + gi) * a.loop_count + (l - a.loop_begin)) * D +
+             lane * P;
 #pragma unroll
       for (int j = 0; j < P; ++j) v[j] = bf16_bits_to_float(qp[j]) * a.scale_log2;
     } else {
@@ -882,6 +908,22 @@ __global__ void __launch_bounds__(kW * 32, (NRT == 0 || (PK == 2 && !RES4)) ? 4 
         }
       }
 
+      if constexpr (CHUNK) {   // the scores of the rows whose weights are asked for
+        if (a.scores) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int n = SC ? e : 2 * c + e;
+            if ((SC && (e > 0 || c > 0)) || (HL && !SC && n >= 4) || n >= blk.gw) continue;
+            const int row = blk.gi0 + n, first = max(0, n_len - a.window) * a.heads;
+            if (row < first || row >= n_len * a.heads) continue;
+            float* o = a.scores +
+                       ((int64_t(b) * a.H + h) * a.window * a.heads + (row - first)) * a.score_stride + t0;
+            if (v0) o[tr0] = sc[e];
+            if (v1) o[tr1] = sc[2 + e];
+          }
+        }
+      }
+
       // ---------------------------------------------------------------- online softmax
       float p[4];
       {
@@ -1370,5 +1412,27 @@ KernelFn pick_pg(int D, bool res4, int nr) {
 
 // kernel of the paged-cache variants (rq_decode_mma_paged.cu)
 KernelFn pick_paged(int D, bool res4, int nr, int pk);
+
+// kernels of the chunk calls (rq_chunk_mma.cu: contiguous cache, rq_chunk_mma_paged.cu: paged);
+// nr: 0 (the final loop) or 1
+template <bool PG, int PK>
+KernelFn pick_chunk_pk(int D, bool res4, int nr) {
+  if constexpr (PK == 2) {
+    if (!has_single_column_variant(D, res4, nr)) return pick_chunk_pk<PG, 1>(D, res4, nr);
+    return nr == 0 ? rq_mma_kernel<128, false, 0, PG, 2, 0, true>
+                   : (res4 ? rq_mma_kernel<128, true, 1, PG, 2, 0, true>
+                           : rq_mma_kernel<128, false, 1, PG, 2, 0, true>);
+  } else {
+    if (D == 128)
+      return nr == 0 ? rq_mma_kernel<128, false, 0, PG, PK, 0, true>
+                     : (res4 ? rq_mma_kernel<128, true, 1, PG, PK, 0, true>
+                             : rq_mma_kernel<128, false, 1, PG, PK, 0, true>);
+    return nr == 0 ? rq_mma_kernel<64, false, 0, PG, PK, 0, true>
+                   : (res4 ? rq_mma_kernel<64, true, 1, PG, PK, 0, true>
+                           : rq_mma_kernel<64, false, 1, PG, PK, 0, true>);
+  }
+}
+KernelFn pick_chunk(int D, bool res4, int nr, int pk);
+KernelFn pick_chunk_paged(int D, bool res4, int nr, int pk);
 
 }  // namespace rq

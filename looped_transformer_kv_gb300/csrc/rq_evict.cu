@@ -1,0 +1,511 @@
+// Eviction by accumulated attention weight: the slots to keep (rq_evict_select) and the move of
+// their rows to the front of a cache (rq_evict_compact).
+#include <cooperative_groups.h>
+
+#include "rq_common.cuh"
+#include "rq_kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace rq {
+namespace {
+
+// ------------------------------------------------------------------------------ select
+//
+// The k-th largest of a row's weights by radix selection: weights become 32-bit keys of the
+// same order, three passes over 11, 11 and 10 key bits count the digits of the keys that still
+// match, and fix the digit of the k-th one.  One more pass in slot order takes every key above
+// the k-th and, of its equals, the first ones.  A row is shared by a cluster of CTAs (each holds
+// its part of the keys in shared memory, the counts are added over the cluster).
+// Bytes: 4 per slot read once, 4 per kept slot written; what bounds it is the latency of the
+// passes' barriers (short rows) and the shared-memory atomics of the first pass (long ones).
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSelMaxCluster = 8;
+constexpr int kSelKeys = 48 * 1024;     // keys a CTA holds in shared memory (192 KB)
+constexpr uint32_t kHeld = 0xffffffffu; // key of a slot that is kept whatever its weight
+
+// Same order as the weights; NaN above every number, -0 as +0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xfffffffeu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+struct SelArgs {
+  const float* weights;
+  const int32_t* ctx_lens;
+  int32_t* keep;
+  int32_t* kept_lens;
+  int H, cap, budget, n_first, n_last, slice;   // slice: keys of shared memory, 0: none
+};
+
+__device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(RQ_FULL_MASK, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const int s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ SelArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int bh = blockIdx.x / C, b = bh / a.H;
+  const int n = a.ctx_lens[b];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[2][kBins];          // alternating passes
+  __shared__ int warp_sums[kSelWarps];
+  __shared__ int found[2], counts[2];     // (digit, its rank from above); (above, equal) of this CTA
+  const bool bad = n < 0 || n > a.cap;
+  const int k = bad ? -1 : min(n, a.budget);
+  if (rank == 0 && bh % a.H == 0 && threadIdx.x == 0) a.kept_lens[b] = k;
+  if (bad) return;                        // (the same for the whole cluster)
+  int32_t* const out = a.keep + int64_t(bh) * a.budget;
+  if (n <= a.budget) {                    // everything stays
+    for (int t = rank * kSelThreads + threadIdx.x; t < n; t += C * kSelThreads) out[t] = t;
+    return;
+  }
+  // this CTA's slots [t0, t1): a multiple of 32 per warp
+  const int per_warp = ((n + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32;
+  const int t0 = min(n, rank * kSelWarps * per_warp), t1 = min(n, t0 + kSelWarps * per_warp);
+  const float* const row = a.weights + int64_t(bh) * a.cap;
+  const int held_from = n - a.n_last;
+  auto fresh_key = [&](int t) {
+    return (t < a.n_first || t >= held_from) ? kHeld : weight_key(row[t]);
+  };
+  const bool stored = t1 - t0 <= a.slice;
+  for (int i = threadIdx.x; i < 2 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  auto key_at = [&](int t) { return stored ? keys[t - t0] : fresh_key(t); };
+
+  uint32_t prefix = 0;                    // the k-th key's digits so far
+  int need = k;                           // its rank among the keys that match them
+  const int shift[3] = {21, 10, 0};
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int sh = shift[pass];
+    const uint32_t digits = pass == 2 ? 1024u : 2048u;
+    int* const h = hist[pass & 1];
+    for (int t = t0 + threadIdx.x; t - threadIdx.x < t1; t += kSelThreads) {
+      uint32_t key = 0;
+      bool mine = t < t1;
+      if (mine) {
+        if (pass == 0) {
+          key = fresh_key(t);
+          if (stored) keys[t - t0] = key;
+        } else {
+          key = key_at(t);
+          mine = (key >> (sh + (pass == 2 ? 10 : 11))) == prefix;
+        }
+      }
+      const uint32_t d = (key >> sh) & (digits - 1u);
+      // a warp whose keys share a digit (equal weights) adds once
+      const unsigned active = __ballot_sync(RQ_FULL_MASK, mine);
+      if (active == 0u) continue;
+      const uint32_t d0 = __shfl_sync(RQ_FULL_MASK, d, __ffs(active) - 1);
+      if (__all_sync(RQ_FULL_MASK, !mine || d == d0)) {
+        if (lane == 0) atomicAdd(&h[d0], __popc(active));
+      } else if (mine) {
+        atomicAdd(&h[d], 1);
+      }
+    }
+    cluster.sync();
+    // counts of the cluster, four digits per thread, from the highest digit down
+    int c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = kBins - 1 - (int(threadIdx.x) * 4 + i);
+      c[i] = 0;
+      for (int r = 0; r < C; ++r) c[i] += cluster.map_shared_rank(h, r)[d];
+      sum += c[i];
+    }
+    int total;
+    int above = block_exclusive_scan(sum, warp_sums, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < need && need <= above + c[i]) {
+        found[0] = kBins - 1 - (int(threadIdx.x) * 4 + i);
+        found[1] = need - above;
+      }
+      above += c[i];
+    }
+    __syncthreads();
+    prefix = (prefix << (pass == 2 ? 10 : 11)) | uint32_t(found[0]);
+    need = found[1];
+    cluster.sync();   // the counts of this pass have been read by everyone
+    if (pass == 0) {  // (the last pass counts in this array again)
+      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[0][i] = 0;
+      __syncthreads();
+    }
+  }
+  // prefix: the k-th key; `need` of its equals are kept, the lowest slots
+  const int w0 = t0 + warp * per_warp, w1 = min(t1, w0 + per_warp);
+  int above = 0, equal = 0;
+  for (int t = w0 + lane; t - lane < w1; t += 32) {
+    const uint32_t key = t < w1 ? key_at(t) : 0u;
+    above += __popc(__ballot_sync(RQ_FULL_MASK, t < w1 && key > prefix));
+    equal += __popc(__ballot_sync(RQ_FULL_MASK, t < w1 && key == prefix));
+  }
+  int total;
+  const int above_before = block_exclusive_scan(lane == 0 ? above : 0, warp_sums, total);
+  if (threadIdx.x == 0) counts[0] = total;
+  const int equal_before = block_exclusive_scan(lane == 0 ? equal : 0, warp_sums, total);
+  if (threadIdx.x == 0) counts[1] = total;
+  cluster.sync();
+  int A = __shfl_sync(RQ_FULL_MASK, above_before, 0), E = __shfl_sync(RQ_FULL_MASK, equal_before, 0);
+  for (int r = 0; r < rank; ++r) {
+    A += cluster.map_shared_rank(counts, r)[0];
+    E += cluster.map_shared_rank(counts, r)[1];
+  }
+  for (int t = w0 + lane; t - lane < w1; t += 32) {
+    const uint32_t key = t < w1 ? key_at(t) : 0u;
+    const bool is_above = t < w1 && key > prefix, is_equal = t < w1 && key == prefix;
+    const unsigned ma = __ballot_sync(RQ_FULL_MASK, is_above);
+    const unsigned me = __ballot_sync(RQ_FULL_MASK, is_equal);
+    const unsigned lower = (1u << lane) - 1u;
+    const int a_here = A + __popc(ma & lower), e_here = E + __popc(me & lower);
+    if (is_above || (is_equal && e_here < need)) out[a_here + min(e_here, need)] = t;
+    A += __popc(ma);
+    E += __popc(me);
+  }
+  cluster.sync();   // (no CTA leaves while its counts may be read)
+}
+
+// ------------------------------------------------------------------------------ compact
+//
+// A 64-row tile of one section of `to` is made of units of at most 16 bytes; a thread loads the
+// sources of its units into registers and stores them.  K rows, steps and offsets are contiguous
+// per row; V code words hold two tokens, so a unit (4 words of a pair) takes the matching
+// 16-bit halves of two source pairs.  Bound by HBM: every kept byte is read and written once (V
+// codes of a kept token whose pair neighbour is not kept cost twice their bytes).
+// In place, a row only moves to a lower slot.  A cluster of CTAs takes the tiles of one (sequence,
+// kv-head, section) in ascending waves: all rows of a wave are read before any is written
+// (cluster barrier), and later waves read only rows at or above their own tiles.
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnits = 3;      // units of a section's tile per thread, at most (768 / 256)
+constexpr int kMoveCluster = 8;
+
+struct MoveArgs {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t rec_bytes;
+  const int32_t* src_bt;
+  const int32_t* dst_bt;
+  int src_max_pages, src_n_pages, dst_max_pages, dst_n_pages;
+  const int32_t* keep;
+  const int32_t* kept_lens;
+  const float* weights;
+  float* to_weights;
+  int H, L, budget, src_cap, dst_cap, tiles;
+  int8_t res_bits[RQ_MAX_LOOPS];
+};
+
+// One unit: what it is and where it starts within the section.
+struct Unit {
+  int off;        // byte offset of the unit in a tile's section (K-like kinds: of row 0)
+  int row;        // row, or first row of the pair
+  int bytes;      // 16, 8 or 2; 0: no unit
+  int row_bytes;
+  int chunk;      // K codes: 16-byte chunk of the row; V codes: group of 4 units
+  bool v_codes;
+};
+
+template <int D>
+__device__ __forceinline__ Unit unit_of(int i, int bits, bool residual) {
+  constexpr int NG = D / 32;
+  const int rb = D * bits / 8, chunks = rb / 16;
+  const int nc = kTile * chunks, per = nc + kTile + (residual ? kTile : 0);
+  const int side = kTile * (rb + NG * 4 + (residual ? 2 : 0));
+  Unit u;
+  u.v_codes = false;
+  const bool v = i >= per;
+  if (v) i -= per;
+  const int base = v ? side : 0;
+  u.bytes = 0;
+  if (i >= per) return u;
+  if (i < nc) {
+    u.bytes = 16;
+    u.off = base;
+    u.chunk = i % chunks;
+    if (v) {   // a pair's words: 2 rb bytes, `chunks` * 2 units of 16 bytes
+      u.v_codes = true;
+      u.chunk = i % (2 * chunks);
+      u.row = i / (2 * chunks) * 2;
+    } else {
+      u.row = i / chunks;
+    }
+    u.row_bytes = rb;
+  } else if (i < nc + kTile) {
+    u.row = i - nc;
+    u.chunk = 0;
+    u.off = base + kTile * rb;
+    u.row_bytes = u.bytes = NG * 4;
+  } else {
+    u.row = i - nc - kTile;
+    u.chunk = 0;
+    u.off = base + kTile * (rb + NG * 4);
+    u.row_bytes = u.bytes = 2;
+  }
+  return u;
+}
+
+template <int D, bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __grid_constant__ MoveArgs a) {
+  const int sect = blockIdx.y;                       // 0: reference, 1 + l: loop l
+  const int per_bh = IN_PLACE ? kMoveCluster : a.tiles;
+  const int64_t bh = blockIdx.x / per_bh;
+  const int first_tile = blockIdx.x % per_bh;
+  const int b = int(bh / a.H), h = int(bh % a.H);
+  const int kept = max(0, min(a.kept_lens[b], min(a.budget, a.dst_cap)));
+  const int n_tiles = (kept + kTile - 1) / kTile;
+  const int bits = sect == 0 ? 4 : a.res_bits[sect - 1];
+  const int sec_off = sect == 0 ? 0 : loop_section_offset(D, a.res_bits, sect - 1);
+  const int32_t* const keep = a.keep + bh * a.budget;
+  __shared__ int64_t from[kTile];                    // record offset of each row's source, -1: none
+  __shared__ int from_row[kTile];
+
+  // offset of the record of a tile, -1 where the block table has no page for it
+  auto record = [&](int tile, const int32_t* bt, int max_pages, int n_pages, int cap) -> int64_t {
+    int64_t rec;
+    if (bt) {
+      const int pg = bt[int64_t(b) * max_pages + tile];
+      if (pg < 0 || pg >= n_pages) return -1;
+      rec = int64_t(pg) * a.H + h;
+    } else {
+      rec = bh * (cap / kTile) + tile;
+    }
+    return rec * a.rec_bytes + sec_off;
+  };
+
+  const int waves = IN_PLACE ? (n_tiles + kMoveCluster - 1) / kMoveCluster : 1;
+  for (int wave = 0; wave < waves; ++wave) {
+    const int tile = first_tile + wave * kMoveCluster;
+    const bool active = tile < n_tiles;
+    const int64_t dst = active ? record(tile, a.dst_bt, a.dst_max_pages, a.dst_n_pages, a.dst_cap) : -1;
+    if (threadIdx.x < kTile) {
+      const int t = tile * kTile + threadIdx.x;
+      int64_t f = -1;
+      int s = -1;
+      if (active && t < kept) {
+        s = keep[t];
+        if (s >= 0 && s < a.src_cap)
+          f = record(s / kTile, a.src_bt, a.src_max_pages, a.src_n_pages, a.src_cap);
+      }
+      from[threadIdx.x] = f;
+      from_row[threadIdx.x] = s & (kTile - 1);
+    }
+    __syncthreads();
+    uint4 v[kMoveUnits];
+    int live[kMoveUnits];          // bit 0: the (first) row has a source, bit 1: the pair's second
+#pragma unroll
+    for (int i = 0; i < kMoveUnits; ++i) {
+      const Unit u = unit_of<D>(threadIdx.x + i * kMoveThreads, bits, sect > 0);
+      live[i] = 0;
+      if (u.bytes == 0 || dst < 0) continue;
+      if (!u.v_codes) {
+        const int64_t f = from[u.row];
+        if (f < 0) continue;
+        live[i] = 1;
+        const uint8_t* p = a.src + f + u.off + from_row[u.row] * u.row_bytes + u.chunk * 16;
+        if (u.bytes == 16) {
+          v[i] = *reinterpret_cast<const uint4*>(p);
+        } else if (u.bytes == 8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          v[i].x = x.x;
+          v[i].y = x.y;
+        } else {
+          v[i].x = *reinterpret_cast<const uint16_t*>(p);
+        }
+      } else {
+        // units 4 chunk .. + 3 of each token sit in 4 adjacent words of its pair (the swizzle
+        // moves whole groups of 8 units)
+        const int units = u.row_bytes / 2;
+        uint4 w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[e] = make_uint4(0u, 0u, 0u, 0u);
+          const int64_t f = from[u.row + e];
+          if (f < 0) continue;
+          live[i] |= 1 << e;
+          const int r = from_row[u.row + e], pair = r >> 1;
+          w[e] = *reinterpret_cast<const uint4*>(a.src + f + u.off + pair * (2 * u.row_bytes) +
+                                                 ((4 * u.chunk) ^ v_unit_swizzle(pair, units)) * 4);
+          if (r & 1) {
+            w[e].x >>= 16;
+            w[e].y >>= 16;
+            w[e].z >>= 16;
+            w[e].w >>= 16;
+          }
+        }
+        v[i].x = __byte_perm(w[0].x, w[1].x, 0x5410);
+        v[i].y = __byte_perm(w[0].y, w[1].y, 0x5410);
+        v[i].z = __byte_perm(w[0].z, w[1].z, 0x5410);
+        v[i].w = __byte_perm(w[0].w, w[1].w, 0x5410);
+      }
+    }
+    float wt = 0.f;
+    if (a.weights && sect == 0 && threadIdx.x < kTile && active) {
+      const int t = tile * kTile + threadIdx.x;
+      const int s = t < kept ? keep[t] : -1;
+      if (s >= 0 && s < a.src_cap) wt = a.weights[bh * a.src_cap + s];
+    }
+    if (IN_PLACE) cg::this_cluster().sync();   // every row of the wave is read
+#pragma unroll
+    for (int i = 0; i < kMoveUnits; ++i) {
+      if (live[i] == 0) continue;
+      const Unit u = unit_of<D>(threadIdx.x + i * kMoveThreads, bits, sect > 0);
+      if (!u.v_codes) {
+        uint8_t* p = a.dst + dst + u.off + u.row * u.row_bytes + u.chunk * 16;
+        if (u.bytes == 16)
+          *reinterpret_cast<uint4*>(p) = v[i];
+        else if (u.bytes == 8)
+          *reinterpret_cast<uint2*>(p) = make_uint2(v[i].x, v[i].y);
+        else
+          *reinterpret_cast<uint16_t*>(p) = uint16_t(v[i].x);
+      } else {
+        const int units = u.row_bytes / 2, pair = u.row >> 1;
+        uint8_t* p = a.dst + dst + u.off + pair * (2 * u.row_bytes) +
+                     ((4 * u.chunk) ^ v_unit_swizzle(pair, units)) * 4;
+        if (live[i] == 3) {
+          *reinterpret_cast<uint4*>(p) = v[i];
+        } else {   // one token of the pair alone: its 16-bit halves
+          const int e = live[i] >> 1;
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint16_t*>(p + 4 * k + 2 * e) = uint16_t(w[k] >> (16 * e));
+        }
+      }
+    }
+    if (a.weights && sect == 0 && threadIdx.x < kTile && active) {
+      const int t = tile * kTile + threadIdx.x;
+      if (t < kept) a.to_weights[bh * a.dst_cap + t] = wt;
+    }
+    __syncthreads();   // (from is rewritten)
+  }
+  // new tokens start at weight 0 (in place: after the last wave's barrier every source is read)
+  if (a.weights && sect == 0) {
+    float* const w = a.to_weights + bh * a.dst_cap;
+    if (IN_PLACE) {
+      for (int t = kept + first_tile * kMoveThreads + threadIdx.x; t < a.dst_cap; t += kMoveCluster * kMoveThreads)
+        w[t] = 0.f;
+    } else if (threadIdx.x < kTile) {
+      const int t = first_tile * kTile + threadIdx.x;
+      if (t >= kept) w[t] = 0.f;
+    }
+  }
+}
+
+template <typename Kernel, typename Args>
+cudaError_t launch_clusters(Kernel kernel, dim3 grid, int threads, size_t smem, int cluster,
+                            cudaStream_t stream, const Args& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+}  // namespace
+
+cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads, int capacity,
+                                const int32_t* ctx_lens, int budget, int n_first, int n_last,
+                                int32_t* keep, int32_t* kept_lens, cudaStream_t stream) {
+  SelArgs a;
+  a.weights = weights;
+  a.ctx_lens = ctx_lens;
+  a.keep = keep;
+  a.kept_lens = kept_lens;
+  a.H = n_kv_heads;
+  a.cap = capacity;
+  a.budget = budget;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  const int64_t rows = int64_t(batch) * n_kv_heads;
+  // CTAs per row: enough that the keys fit shared memory, more while the rows leave SMs free
+  // and each CTA keeps a few thousand slots
+  int C = 1;
+  while (C < kSelMaxCluster && (int64_t(capacity) > int64_t(C) * kSelKeys ||
+                                (rows * C * 2 <= device_sm_count() && capacity / C >= 4096)))
+    C *= 2;
+  const int64_t per_cta = (int64_t(capacity) / C + 32 * kSelWarps + 31) / 32 * 32;
+  a.slice = per_cta <= kSelKeys ? int(per_cta) : 0;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSelKeys * 4);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(evict_select_kernel, dim3(unsigned(rows * C)), kSelThreads,
+                         size_t(a.slice) * 4, C, stream, a);
+}
+
+cudaError_t launch_evict_compact(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                                 const rq_shape& ts, const rq_cache& to, const rq_paging* to_paging,
+                                 bool in_place, const int32_t* keep, int budget,
+                                 const int32_t* kept_lens, const float* weights, float* to_weights,
+                                 cudaStream_t stream) {
+  MoveArgs a;
+  a.src = cache.data;
+  a.dst = to.data;
+  a.rec_bytes = record_bytes(s);
+  a.src_bt = paging ? paging->block_table : nullptr;
+  a.src_max_pages = paging ? paging->max_pages : 0;
+  a.src_n_pages = paging ? paging->n_pages : 0;
+  a.dst_bt = to_paging ? to_paging->block_table : nullptr;
+  a.dst_max_pages = to_paging ? to_paging->max_pages : 0;
+  a.dst_n_pages = to_paging ? to_paging->n_pages : 0;
+  a.keep = keep;
+  a.kept_lens = kept_lens;
+  a.weights = weights;
+  a.to_weights = to_weights;
+  a.H = s.n_kv_heads;
+  a.L = s.n_loops;
+  a.budget = budget;
+  a.src_cap = s.capacity;
+  a.dst_cap = ts.capacity;
+  // tiles that may hold kept rows (with weights: every tile, for the zeros)
+  const int kept_most = budget < ts.capacity ? budget : ts.capacity;
+  a.tiles = weights ? ts.capacity / kTile : (kept_most + kTile - 1) / kTile;
+  for (int l = 0; l < RQ_MAX_LOOPS; ++l) a.res_bits[l] = s.res_bits[l];
+  const int64_t bh = int64_t(s.batch) * s.n_kv_heads;
+  const int64_t x = bh * (in_place ? kMoveCluster : a.tiles);
+  if (x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid{unsigned(x), unsigned(s.n_loops), 1u};
+  if (in_place) {
+    if (s.head_dim == 128)
+      return launch_clusters(evict_compact_kernel<128, true>, grid, kMoveThreads, 0, kMoveCluster, stream, a);
+    return launch_clusters(evict_compact_kernel<64, true>, grid, kMoveThreads, 0, kMoveCluster, stream, a);
+  }
+  if (s.head_dim == 128)
+    evict_compact_kernel<128, false><<<grid, kMoveThreads, 0, stream>>>(a);
+  else
+    evict_compact_kernel<64, false><<<grid, kMoveThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace rq

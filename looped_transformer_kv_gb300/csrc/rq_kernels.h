@@ -154,6 +154,44 @@ cudaError_t launch_rq_ablation_decode(const rq_shape& s, const rq_cache& cache, 
                                       const int32_t* ctx_lens, int max_ctx, uint16_t* out,
                                       float* ws, cudaStream_t stream);
 
+// A chunk call (rq_chunk_attention), arguments as there.
+struct ChunkCall {
+  const uint16_t* q;
+  int64_t q_strides[3];
+  int loop;
+  const uint16_t* kv_new;
+  int64_t kv_strides[5];
+  const int32_t* n_lens;
+  int n_new;
+  const int32_t* ctx_lens;
+  int max_ctx;
+  uint16_t* out;
+  float* weights;
+  int window;
+};
+
+size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window);
+cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                         const ChunkCall& c, void* ws, cudaStream_t stream);
+
+// Few rows (rq_decode_mma.cu): split plan and launch of the decode kernel's chunk variants.
+// part: [B][Hkv][rows][n_splits] partial records; scores (or null): [B][Hkv][window rows]
+// [score_stride], log2 units.
+SplitPlan plan_splits_chunk(const rq_shape& s, int loop, int rows, int max_ctx);
+cudaError_t launch_chunk_mma(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                             const ChunkCall& c, const SplitPlan& plan, float* part, float* scores,
+                             int64_t score_stride, unsigned* err, cudaStream_t stream);
+
+// Eviction (rq_evict.cu), arguments as in include/rq.h.
+cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads, int capacity,
+                                const int32_t* ctx_lens, int budget, int n_first, int n_last,
+                                int32_t* keep, int32_t* kept_lens, cudaStream_t stream);
+cudaError_t launch_evict_compact(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                                 const rq_shape& ts, const rq_cache& to, const rq_paging* to_paging,
+                                 bool in_place, const int32_t* keep, int budget,
+                                 const int32_t* kept_lens, const float* weights, float* to_weights,
+                                 cudaStream_t stream);
+
 int device_sm_count();
 
 // The argument checks of rq_decode_attention other than its workspace (C ABI layer).

@@ -46,17 +46,22 @@ class PackedCache:
     """One layer's packed cache in device memory: the tile records of include/rq.h in one
     buffer (256-byte aligned), [B][Hkv][capacity/64] records, or [n_pages][Hkv] in paged
     form, plus the rotation signs.  record_bytes() is rq_record_bytes; section(...) gives the
-    byte range of one kind of row inside a record (for reading the cache back)."""
+    byte range of one kind of row inside a record (for reading the cache back).  data: an
+    existing uint8 buffer of exactly the cache's bytes to use instead of a new one (kept alive
+    here)."""
 
-    def __init__(self, shape, rot_signs, device="cuda", n_pages=None):
+    def __init__(self, shape, rot_signs, device="cuda", n_pages=None, data=None):
         B, H, cap, d = shape.batch, shape.n_kv_heads, shape.capacity, shape.head_dim
         self.n_pages = n_pages
         self.shape = shape
         self.rec = int(_lib.lib().rq_record_bytes(ctypes.byref(shape)))
         assert self.rec > 0
         n_rec = (n_pages * H) if n_pages is not None else (B * H * (cap // PAGE))
-        self.data = torch.empty(n_rec * self.rec, dtype=torch.uint8, device=device)
-        self.rot_signs = rot_signs.to(device=device, dtype=torch.int8).contiguous()  # [2][H][d]
+        if data is None:
+            data = torch.empty(n_rec * self.rec, dtype=torch.uint8, device=device)
+        assert data.dtype == torch.uint8 and data.is_contiguous() and data.numel() == n_rec * self.rec
+        self.data = data.view(-1)
+        self.rot_signs = rot_signs.to(device=data.device, dtype=torch.int8).contiguous()  # [2][H][d]
         assert tuple(self.rot_signs.shape) == (2, H, d)
         c = RqCache()
         c.data = self.data.data_ptr()
@@ -211,6 +216,96 @@ def bf16_decode_attention(shape, k, v, q, loop_begin, loop_count, pending_kv, ct
         ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(q), int(loop_begin), int(loop_count),
         _ptr(pending_kv), _ptr(ctx_lens), int(max_ctx), _ptr(out), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _f32(t):
+    assert t is None or (t.dtype == torch.float32 and t.is_contiguous())
+    return _ptr(t)
+
+
+def _i32(t):
+    assert t is None or (t.dtype == torch.int32 and t.is_contiguous())
+    return _ptr(t)
+
+
+def chunk_workspace_bytes(shape, loop, n_new, max_ctx, window=0):
+    """rq_chunk_workspace_bytes: workspace of chunk_attention / paged_chunk_attention."""
+    return int(_lib.lib().rq_chunk_workspace_bytes(ctypes.byref(shape), int(loop), int(n_new),
+                                                   int(max_ctx), int(window)))
+
+
+def _chunk_args(shape, q, loop, kv_new, ctx_lens, max_ctx, out, ws, n_lens, weights, window, stream):
+    B, n, d = shape.batch, q.shape[1], shape.head_dim
+    assert q.dtype == torch.bfloat16 and tuple(q.shape) == (B, n, shape.n_q_heads, d)
+    assert kv_new.dtype == torch.bfloat16
+    assert tuple(kv_new.shape) == (B, n, 2, shape.n_loops, shape.n_kv_heads, d)
+    assert n == 0 or (q.stride(3) == 1 and kv_new.stride(5) == 1)
+    assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape
+    assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
+    assert weights is None or tuple(weights.shape) == (B, shape.n_kv_heads, shape.capacity)
+    qs = (ctypes.c_int64 * 3)(*[q.stride(i) for i in range(3)])
+    ks = (ctypes.c_int64 * 5)(*[kv_new.stride(i) for i in range(5)])
+    return (_ptr(q), qs, int(loop), _ptr(kv_new), ks, _i32(n_lens), int(n), _i32(ctx_lens),
+            int(max_ctx), _ptr(out), _f32(weights), int(window), _ptr(ws),
+            ws.numel() * ws.element_size(), _stream(stream))
+
+
+def chunk_attention(shape, cache, q, loop, kv_new, ctx_lens, max_ctx, out, ws, n_lens=None,
+                    weights=None, window=0, stream=None):
+    """rq_chunk_attention: q, out bf16 [B][n][Hq][d] (q any strides, channel stride 1), kv_new as
+    in encode_append, n_lens int32 [B]; weights fp32 [B][Hkv][capacity] collects the softmax
+    weights of each sequence's last `window` tokens."""
+    check("rq_chunk_attention", _lib.lib().rq_chunk_attention(
+        ctypes.byref(shape), ctypes.byref(cache.struct),
+        *_chunk_args(shape, q, loop, kv_new, ctx_lens, max_ctx, out, ws, n_lens, weights, window,
+                     stream)))
+
+
+def paged_chunk_attention(shape, cache, paging, q, loop, kv_new, ctx_lens, max_ctx, out, ws,
+                          n_lens=None, weights=None, window=0, stream=None):
+    """rq_paged_chunk_attention; the other arguments as in chunk_attention."""
+    check("rq_paged_chunk_attention", _lib.lib().rq_paged_chunk_attention(
+        ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
+        *_chunk_args(shape, q, loop, kv_new, ctx_lens, max_ctx, out, ws, n_lens, weights, window,
+                     stream)))
+
+
+def evict_select(weights, ctx_lens, budget, keep, kept_lens, n_first=0, n_last=0, stream=None):
+    """rq_evict_select: weights fp32 [B][Hkv][capacity]; keep int32 [B][Hkv][budget] takes the kept
+    slots, ascending, kept_lens int32 [B] their number."""
+    B, H, cap = weights.shape
+    assert tuple(keep.shape) == (B, H, budget) and ctx_lens.numel() == B and kept_lens.numel() == B
+    check("rq_evict_select", _lib.lib().rq_evict_select(
+        _f32(weights), B, H, cap, _i32(ctx_lens), int(budget), int(n_first), int(n_last),
+        _i32(keep), _i32(kept_lens), _stream(stream)))
+
+
+def _compact_args(shape, to_shape, keep, kept_lens, weights, to_weights, stream):
+    B, H = shape.batch, shape.n_kv_heads
+    assert tuple(keep.shape[:2]) == (B, H) and keep.dim() == 3 and kept_lens.numel() == B
+    assert weights is None or tuple(weights.shape) == (B, H, shape.capacity)
+    assert to_weights is None or tuple(to_weights.shape) == (B, H, to_shape.capacity)
+    return (_i32(keep), int(keep.shape[2]), _i32(kept_lens), _f32(weights), _f32(to_weights),
+            _stream(stream))
+
+
+def evict_compact(shape, cache, to_shape, to_cache, keep, kept_lens, weights=None, to_weights=None,
+                  stream=None):
+    """rq_evict_compact: row keep[b][h][t] of cache becomes row t of to_cache (which may be the
+    same cache), its weights alike."""
+    check("rq_evict_compact", _lib.lib().rq_evict_compact(
+        ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(to_shape),
+        ctypes.byref(to_cache.struct),
+        *_compact_args(shape, to_shape, keep, kept_lens, weights, to_weights, stream)))
+
+
+def paged_evict_compact(shape, cache, paging, to_shape, to_cache, to_paging, keep, kept_lens,
+                        weights=None, to_weights=None, stream=None):
+    """rq_paged_evict_compact; the other arguments as in evict_compact."""
+    check("rq_paged_evict_compact", _lib.lib().rq_paged_evict_compact(
+        ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
+        ctypes.byref(to_shape), ctypes.byref(to_cache.struct), ctypes.byref(to_paging),
+        *_compact_args(shape, to_shape, keep, kept_lens, weights, to_weights, stream)))
 
 
 def synth_params(seed, layer, head_dim, n_kv_heads, dist, sigma, outlier_mult, outlier_table):
