@@ -1,6 +1,6 @@
-// Chunk attention (rq_chunk_attention): host side, combine and weights.
+// Chunk attention (rq_chunk_attention): host side, and the kernels of calls with few rows.
 //
-// A row is one (new token j, query head g) of a kv-head: row = j * heads + g.  The rows take the
+// A row is one (new token j, query head g) of a kv-head: row = j * heads + g.  Few rows take the
 // decode kernel's chunk variants (rq_decode_mma.cuh): the cache is streamed once per block of 8
 // rows, and the combine below merges the splits and adds the chunk's own tokens, causally.
 #include "rq_common.cuh"
@@ -157,7 +157,16 @@ RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int 
 
 }  // namespace
 
+// Rows of a kv-head up to which the cache is streamed once per 8 rows; above, it is rebuilt once
+// (2 d fp16 written and read per token-head) and attended in tiles of 128 rows.
+constexpr int kFewRows = 32;
+
+bool few_rows(const rq_shape& s, int n_new) {
+  return int64_t(s.n_q_heads / s.n_kv_heads) * n_new <= kFewRows;
+}
+
 size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
+  if (!few_rows(s, n_new)) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window);
   return rows_layout(s, loop, n_new, max_ctx, window).total;
 }
 
@@ -167,6 +176,7 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   unsigned* err = reinterpret_cast<unsigned*>(w);
   cudaError_t e = cudaMemsetAsync(w, 0, kWsHeaderBytes, stream);
   if (e != cudaSuccess) return e;
+  if (!few_rows(s, c.n_new)) return launch_chunk_tc(s, cache, paging, c, ws, stream);
   const RowsLayout l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window);
   float* const scores = c.weights ? reinterpret_cast<float*>(w + l.scores) : nullptr;
   e = launch_chunk_mma(s, cache, paging, c, l.plan, reinterpret_cast<float*>(w + l.part), scores,

@@ -182,6 +182,12 @@ cudaError_t launch_chunk_mma(const rq_shape& s, const rq_cache& cache, const rq_
                              const ChunkCall& c, const SplitPlan& plan, float* part, float* scores,
                              int64_t score_stride, unsigned* err, cudaStream_t stream);
 
+// Many rows (rq_chunk_tc.cu): workspace (from its start: the header) and launch.  The header is
+// cleared by the caller.
+size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window);
+cudaError_t launch_chunk_tc(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                            const ChunkCall& c, void* ws, cudaStream_t stream);
+
 // Eviction (rq_evict.cu), arguments as in include/rq.h.
 cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads, int capacity,
                                 const int32_t* ctx_lens, int budget, int n_first, int n_last,
