@@ -11,6 +11,8 @@
 // Operands are fp16: a rebuilt element and a softmax weight are each rounded once (2^-11
 // relative); the queries are exact (a row's bf16 values times a power of two, undone in the
 // score's fp32 scale).  Collected weights need more: their scores take K as two fp16 parts.
+#include <climits>
+
 #include "rq_common.cuh"
 #include "rq_kernels.h"
 #include "rq_tc.cuh"
@@ -23,10 +25,6 @@ constexpr int kRows = 128;                 // query rows per tile
 constexpr float kStateMax = 65504.f;
 constexpr float kSlack = 8.f;              // log2 units a maximum may grow before O is rescaled
 constexpr uint64_t kTcWaitLimitNs = 2000000000ull;
-
-__device__ __forceinline__ float code_float(uint32_t code) {   // exact integer below 2^23
-  return __uint_as_float(0x4B000000u | code) - 8388608.f;
-}
 
 __device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
   uint32_t r;
@@ -60,204 +58,489 @@ struct RebuildArgs {
   const int8_t* signs[2];
   const uint16_t* kv_new;
   int64_t ks0, ks1, kv_v, ks_h;
+  int vec;                       // kv_new rows allow 16-byte loads
   uint8_t *k, *klo, *val;        // images [unit][tile][...]; klo may be null
 };
 
-// Codes of one token's row -> x[ch] = fma(step, code, offset-term): ADD adds to x.
-template <int D, int BITS, bool V, bool ADD>
-__device__ __forceinline__ void add_level(const uint8_t* codes, const uint8_t* meta, int r, float a,
-                                          float (&x)[D]) {
-  constexpr int NG = D / 32, RB = D * BITS / 8;
-  float s[NG], z[NG];
+// The residual levels s c + z of one word, as fp16 pairs of neighbouring channels (rounded once;
+// LO: and the rest of the fp32 value as a second fp16).
+template <int BITS, bool LO>
+__device__ __forceinline__ void word_levels(uint32_t w, uint32_t meta, uint32_t* hi, uint32_t* lo) {
+  constexpr int HALF = 8 / BITS;                     // pairs per 16 code bits
+  constexpr uint32_t MASK = BITS == 2 ? 0x00030003u : 0x000F000Fu;
+  const __half2 m = *reinterpret_cast<const __half2*>(&meta);
+  const __half2 s = __half2half2(__low2half(m)), z = __half2half2(__high2half(m));
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const float2 m = __half22float2(*reinterpret_cast<const __half2*>(meta + (r * NG + g) * 4));
-    s[g] = m.x * a;
-    z[g] = m.y * a;
-  }
-  auto put = [&](int ch, uint32_t code) {
-    const int g = ch / 32;
-    x[ch] = fmaf(s[g], code_float(code), ADD ? x[ch] + z[g] : z[g]);
-  };
-  constexpr uint32_t MASK = (1u << BITS) - 1u;
-  if constexpr (!V) {   // words group-interleaved: word s holds channels of group s % NG
-    constexpr int PER = 32 / BITS;
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t x = e ? w >> 16 : w;
+    const uint32_t y = __byte_perm(x, x << (16 - BITS), 0x7610);   // halves: codes 0.., codes 1..
 #pragma unroll
-    for (int w = 0; w < RB / 4; ++w) {
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + r * RB + w * 4);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) put((w % NG) * 32 + (w / NG) * PER + i, (word >> (i * BITS)) & MASK);
-    }
-  } else {              // token pairs: unit u at word u ^ swizzle, this token's half
-    constexpr int PER = 16 / BITS, UNITS = RB / 2;
-    const int p = r >> 1;
-    const uint8_t* row = codes + p * 2 * RB + (r & 1) * 2;
-    const int sw = v_unit_swizzle(p, UNITS);
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const uint32_t unit = *reinterpret_cast<const uint16_t*>(row + (u ^ sw) * 4);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) put(u * PER + i, (unit >> (i * BITS)) & MASK);
-    }
-  }
-}
-
-template <int D, bool V>
-__device__ __forceinline__ void rebuild_row(const uint8_t* sec, int bits, const float* sign, int r,
-                                            float (&x)[D]) {
-  constexpr int NG = D / 32;
-  constexpr int REF = kTile * (D / 2 + 4 * NG);             // bytes of one side of the reference
-  const uint8_t* ref = sec + (V ? REF : 0);
-  if (bits == 0) {
-    add_level<D, 4, V, false>(ref, ref + kTile * D / 2, r, 1.f, x);
-    return;
-  }
-  const int rb = D * bits / 8, side = kTile * (rb + 4 * NG + 2);
-  const uint8_t* res = sec + 2 * REF + (V ? side : 0);
-  const float a = __half2float(*reinterpret_cast<const __half*>(res + kTile * (rb + 4 * NG) + r * 2));
-  if (bits == 2)
-    add_level<D, 2, V, false>(res, res + kTile * rb, r, 1.f, x);
-  else
-    add_level<D, 4, V, false>(res, res + kTile * rb, r, 1.f, x);
-#pragma unroll
-  for (int h = 1; h < D; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-      if ((i & h) == 0) {
-        const float u = x[i], w = x[i + h];
-        x[i] = u + w;
-        x[i + h] = u - w;
-      }
-#pragma unroll
-  for (int i = 0; i < D; i += 4) {
-    const float4 sg = *reinterpret_cast<const float4*>(sign + i);
-    x[i] *= sg.x;
-    x[i + 1] *= sg.y;
-    x[i + 2] *= sg.z;
-    x[i + 3] *= sg.w;
-  }
-  add_level<D, 4, V, true>(ref, ref + kTile * D / 2, r, a, x);
-}
-
-template <int D>
-constexpr int rebuild_smem() {   // sections, signs, images, barrier
-  return kTile * (D + 8 * (D / 32)) + kTile * (D + 8 * (D / 32) + 4) + 2 * D * 4 + 3 * 64 * D * 2 + 16;
-}
-
-// One CTA per 64 keys of a (sequence, kv-head): a thread per key and side (K, V) holds the row's
-// D channels in registers, so the Hadamard transform needs no exchange.  Bound by instruction
-// issue (about 2,200 per row) together with HBM (one loop's record read, 4 D bytes written).
-template <int D>
-__global__ void __launch_bounds__(128) rebuild_kernel(const __grid_constant__ RebuildArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int NG = D / 32;
-  constexpr int REF = kTile * (D + 8 * NG);
-  const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
-  int n, ctx;
-  if (!lens_of(a.v, b, n, ctx)) {
-    if (threadIdx.x == 0) atomicOr(a.v.err, 1u);
-    return;
-  }
-  const int t0 = blockIdx.x * kTile, total = n > 0 ? ctx + n : 0;
-  if (t0 >= (total + kKeys - 1) / kKeys * kKeys) return;
-  uint8_t* const img_k = smem;
-  uint8_t* const img_lo = smem + 64 * D * 2;
-  uint8_t* const img_v = smem + 2 * 64 * D * 2;
-  float* const sign = reinterpret_cast<float*>(smem + 3 * 64 * D * 2);      // [2][D]
-  uint8_t* const sec = smem + 3 * 64 * D * 2 + 2 * D * 4;
-  uint64_t* const bar = reinterpret_cast<uint64_t*>(sec + REF + kTile * (D + 8 * NG + 4));
-  const bool cached = t0 < ctx;
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(bar), 1);
-    fence_mbar_init();
-    if (cached) {
-      int64_t rec;
-      if (a.bt) {
-        int pg = a.bt[int64_t(b) * a.max_pages + blockIdx.x];
-        if (pg < 0 || pg >= a.n_pages) {
-          atomicOr(a.v.err, 1u);
-          pg = 0;
-        }
-        rec = int64_t(pg) * a.v.H + h;
+    for (int i = 0; i < HALF; ++i) {
+      const uint32_t c = code_pair_normal(y >> (2 * BITS * i), MASK);
+      const __half2 ch = *reinterpret_cast<const __half2*>(&c);
+      if constexpr (LO) {
+        const float2 cf = __half22float2(ch), mf = __half22float2(m);
+        const float v0 = fmaf(mf.x, cf.x, mf.y), v1 = fmaf(mf.x, cf.y, mf.y);
+        const uint32_t h = half2_sat(v0, v1);
+        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        hi[e * HALF + i] = h;
+        lo[e * HALF + i] = half2_sat(v0 - hf.x, v1 - hf.y);
       } else {
-        rec = (int64_t(b) * a.v.H + h) * (a.cap / kTile) + blockIdx.x;
+        const __half2 v = __hfma2(ch, s, z);
+        hi[e * HALF + i] = *reinterpret_cast<const uint32_t*>(&v);
       }
-      const uint8_t* src = a.data + rec * a.rec_bytes;
-      const uint32_t res = a.bits ? uint32_t(loop_section_bytes(D, a.bits)) : 0u;
-      mbar_arrive_expect_tx(smem_u32(bar), uint32_t(REF) + res);
-      bulk_g2s(smem_u32(sec), src, uint32_t(REF), smem_u32(bar));
-      if (res) bulk_g2s(smem_u32(sec + REF), src + a.sec_off, res, smem_u32(bar));
     }
   }
-  const float inv_sqrt_d = (D == 128) ? 0.08838834764831845f : 0.125f;
-  for (int i = threadIdx.x; i < 2 * D; i += 128)
-    sign[i] = float(a.signs[i / D][int64_t(h) * D + i % D]) * inv_sqrt_d;
+}
+
+// x (8 channels as 4 fp32 pairs) += a s c of 8 4-bit codes: a code at bit k of a 16-bit half is
+// the exact fp32 c 2^k after subtracting 2^23, its power of two folded into the steps.
+__device__ __forceinline__ void add_codes4(uint32_t w, uint64_t s01, uint64_t s23, uint64_t* x) {
+  const uint64_t base = pack2(-8388608.f, -8388608.f);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t y = e ? w >> 16 : w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t c = pack2(__uint_as_float((y & (0xFu << (8 * i))) | 0x4B000000u),
+                               __uint_as_float((y & (0xF0u << (8 * i))) | 0x4B000000u));
+      x[2 * e + i] = fma2(add2(c, base), i ? s23 : s01, x[2 * e + i]);
+    }
+  }
+}
+
+template <int D, int RES, bool KLO>
+struct RebuildSmem {
+  static constexpr int NG = D / 32;
+  static constexpr int kRef = kTile * (D + 8 * NG);                       // one record's sections
+  static constexpr int kRes = RES ? kTile * (2 * (D * RES / 8) + 8 * NG + 4) : 0;
+  static constexpr int kImg = kKeys * D * 2;
+  // H; E, then the image going out (V's in a region of its own where there is room); K's low parts
+  static constexpr int h = 0, e = RES ? 128 * D * 2 : 0, v = RES ? e : e + kImg, lo = v + kImg;
+  static constexpr int sec = lo + (KLO ? kImg : 0);
+  static constexpr int az = sec + 2 * (kRef + kRes), sign = az + kKeys * NG * 8;
+  static constexpr int bars = sign + 2 * D * 4, total = bars + 64 + 1024;
+  static_assert(total <= (KLO ? 227 * 1024 : 113 * 1024), "two CTAs per SM without K's low parts");
+};
+
+// Persistent CTAs over tiles of 128 keys.  The rotation is undone on the tensor cores:
+//   K: D[key][channel] = E H^T,   V: D[channel][key] = H E^T     (E: residual levels, fp16;
+// H: Hadamard +-1), and the epilogues add the reference, x = D sign / sqrt(d) + a (s c + z), in
+// fp32, round once and write the images through shared memory: a thread per key and half the
+// channels for K, per channel and half the keys for V (the V image has channels as rows).
+// Bound by HBM (one loop's rows read, 4 d bytes per token-head written) and by the instructions
+// of the conversions (about 1,500 per token-head).
+template <int D, int RES, bool KLO>
+__global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_constant__ RebuildArgs a, int n_items) {
+  using L = RebuildSmem<D, RES, KLO>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  constexpr int NG = D / 32;
+  constexpr int SIDE = kTile * (D / 2 + 4 * NG);         // K (or V) part of the reference section
+  constexpr int RROW = D * RES / 8;
+  constexpr int RSIDE = kTile * (RROW + 4 * NG + 2);
+  constexpr int SEC = L::kRef + L::kRes;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+  const uint32_t loaded = smem_u32(bars), kdone = loaded + 8, vdone = loaded + 16;
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 3);
+  float* const sign = reinterpret_cast<float*>(smem + L::sign);            // [2][D], / sqrt(d)
+  float2* const az = reinterpret_cast<float2*>(smem + L::az);              // [pair][group][parity]
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int r = tid & 127, hh = tid >> 7;
+  const uint32_t lanes = uint32_t(warp & 3) << 21;
+
+  if (RES && warp == 0) tc_alloc(smem_u32(tslot), 256);
+  if (tid == 0) {
+    mbar_init(loaded, 1);
+    mbar_init(kdone, 1);
+    mbar_init(vdone, 1);
+    fence_mbar_init();
+  }
+  if constexpr (RES != 0) {   // H as an image of 128 rows (D = 64: its rows twice)
+    for (int i = tid; i < 128 * (D / 8); i += 256) {
+      const int row = i / (D / 8), c = i % (D / 8);
+      uint32_t w[4];
+      const uint32_t flip = (__popc(row & (8 * c)) & 1) ? 0x80008000u : 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t s0 = uint32_t(__popc(row & (2 * k)) & 1) << 15;
+        const uint32_t s1 = uint32_t(__popc(row & (2 * k + 1)) & 1) << 31;
+        w[k] = (0x3C003C00u | s0 | s1) ^ flip;
+      }
+      *reinterpret_cast<uint4*>(smem + L::h + (c / 8) * (128 * 128) + panel_offset(row, c % 8)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
   __syncthreads();
-  const bool arrived = !cached || mbar_wait_bounded(smem_u32(bar), 0, kTcWaitLimitNs);
-  if (!arrived) atomicOr(a.v.err, 1u);
-  const bool is_v = threadIdx.x >= 64;
-  const int r = threadIdx.x & 63, t = t0 + r;
-  float x[D];
-  if (t < ctx && arrived) {
-    if (is_v)
-      rebuild_row<D, true>(sec, a.bits, sign + D, r, x);
-    else
-      rebuild_row<D, false>(sec, a.bits, sign, r, x);
-  } else if (t >= ctx && t < total) {
-    const uint16_t* p = a.kv_new + b * a.ks0 + (t - ctx) * a.ks1 + h * a.ks_h + (is_v ? a.kv_v : 0);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      x[i] = bf16_bits_to_float(p[i]);
-      bad |= !(fabsf(x[i]) <= kStateMax);
+  tc_fence_after();
+  const uint32_t tmem = RES ? *tslot : 0u;
+  const float inv_sqrt_d = (D == 128) ? 0.08838834764831845f : 0.125f;
+  int phase = 0;
+  bool failed = false, loading = false;
+
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    // heads first: the heads of a chunk token lie next to each other
+    const int h = item % a.v.H, tile = item / a.v.H % a.v.tiles, bl = item / a.v.H / a.v.tiles;
+    const int b = a.v.b0 + bl, unit = bl * a.v.H + h;
+    int n, ctx;
+    if (!lens_of(a.v, b, n, ctx)) {
+      if (tid == 0) atomicOr(a.v.err, 1u);
+      continue;
     }
-    if (bad) {   // its own and later rows become NaN; the image keeps a zero row
-      atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, t - ctx);
-#pragma unroll
-      for (int i = 0; i < D; ++i) x[i] = 0.f;
+    const int t0 = tile * kKeys, total = n > 0 ? ctx + n : 0;
+    if (t0 >= total) continue;
+    const int old = min(kKeys, max(0, ctx - t0));          // cached keys of the tile
+    const bool cached = old > 0;
+    uint8_t* const sec0 = smem + L::sec;
+    loading = cached;
+    if (tid == 0) {
+      if (cached) {
+        fence_async_smem();
+        const int n_rec = old > kTile ? 2 : 1;
+        mbar_arrive_expect_tx(loaded, uint32_t(n_rec) * SEC);
+        for (int i = 0; i < n_rec; ++i) {
+          int64_t rec;
+          if (a.bt) {
+            int pg = a.bt[int64_t(b) * a.max_pages + 2 * tile + i];
+            if (pg < 0 || pg >= a.n_pages) {
+              atomicOr(a.v.err, 1u);
+              pg = 0;
+            }
+            rec = int64_t(pg) * a.v.H + h;
+          } else {
+            rec = (int64_t(b) * a.v.H + h) * (a.cap / kTile) + 2 * tile + i;
+          }
+          const uint8_t* src = a.data + rec * a.rec_bytes;
+          const uint32_t dst = smem_u32(sec0) + i * SEC;
+          bulk_g2s(dst, src, L::kRef, loaded);
+          if (RES) bulk_g2s(dst + L::kRef, src + a.sec_off, L::kRes, loaded);
+        }
+      }
+      bulk_s2g_wait_read();       // the last tile's image has left
     }
-  } else {
+    if (tid < 2 * D) sign[tid] = float(a.signs[tid / D][int64_t(h) * D + tid % D]) * inv_sqrt_d;
+    __syncthreads();
+    if (cached) {
+      failed = !mbar_wait_bounded(loaded, phase, kTcWaitLimitNs);
+      if constexpr (RES != 0) {   // E of K: a thread per key and half its words
+        constexpr int PER = 32 / RES, CPW = PER / 8;      // codes and 16-byte chunks per word
+        const int key = tid >> 1;
+        const uint8_t* const res = sec0 + (key >> 6) * SEC + L::kRef;
+        const int row = key & 63;
+        uint32_t m[NG];
 #pragma unroll
-    for (int i = 0; i < D; ++i) x[i] = 0.f;
-  }
-  if (!is_v) {
+        for (int g = 0; g < NG; ++g) m[g] = *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + g) * 4);
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
+        for (int jj = 0; jj < RES / 2; ++jj) {
+          const int j = 2 * jj + (tid & 1);               // word j of every group
+          uint32_t w[NG];
+          if constexpr (NG == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(res + row * RROW + j * 16);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(res + row * RROW + j * 8);
+            w[0] = x.x, w[1] = x.y;
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            uint32_t hi[PER / 2], lo[PER / 2];
+            word_levels<RES, KLO>(w[g], m[g], hi, lo);
+#pragma unroll
+            for (int c = 0; c < CPW; ++c) {
+              const uint32_t o = (g / 2) * (kKeys * 128) + panel_offset(key, (g % 2) * 4 + j * CPW + c);
+              *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+              if constexpr (KLO)
+                *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+      }
+      // a s and a z of every (key, group) of V
+      for (int i = tid; i < kKeys * NG; i += 256) {
+        const int t = i / NG, g = i % NG;
+        const uint8_t* s = sec0 + (t >> 6) * SEC;
+        const float2 m = __half22float2(*reinterpret_cast<const __half2*>(s + SIDE + kTile * D / 2 + ((t & 63) * NG + g) * 4));
+        float al = 1.f;
+        if (RES)
+          al = __half2float(*reinterpret_cast<const __half*>(s + L::kRef + RSIDE + kTile * (RROW + 4 * NG) + (t & 63) * 2));
+        // (the odd key's code sits 16 bits higher in its word)
+        az[((t >> 1) * NG + g) * 2 + (t & 1)] = make_float2((t & 1) ? m.x * al * 0x1p-16f : m.x * al, m.y * al);
+      }
+    }
+    if (__syncthreads_or(failed)) {
+      failed = true;
+      break;
+    }
+    if constexpr (RES != 0) if (cached) {
+      constexpr uint32_t idk = f16_idesc(kKeys, D), idv = f16_idesc(128, kKeys);
+      const uint32_t hs = smem_u32(smem + L::h), es = smem_u32(smem + L::e);
+      if (tid == 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int part = 0; part < (KLO ? 2 : 1); ++part)
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            tc_mma(tmem, panel_desc((part ? smem_u32(smem + L::lo) : es) + (x / 4) * (kKeys * 128) + (x % 4) * 32),
+                   panel_desc(hs + (x / 4) * (128 * 128) + (x % 4) * 32), idk, part > 0 || x > 0);
+        tc_commit(kdone);
+      }
+      // E of V: a thread per pair of keys and 16 bytes of its words (4 units of both keys)
+      constexpr int CHUNKS = D * RES / 64;                // 16-byte chunks of a pair's words
+      constexpr int IT = (64 * CHUNKS + 255) / 256;
+      uint4 w[IT];
+      uint32_t m[IT][2];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int id = tid + 256 * i, p = id / CHUNKS, c = id % CHUNKS, row = (2 * p) & 63;
+        if (id >= 64 * CHUNKS) continue;
+        const uint8_t* const res = sec0 + (p >> 5) * SEC + L::kRef + RSIDE;
+        const int u0 = (4 * c) ^ v_unit_swizzle(p & 31, RROW / 2), g = u0 * (16 / RES) / 32;
+        w[i] = *reinterpret_cast<const uint4*>(res + (p & 31) * 2 * RROW + c * 16);
+        m[i][0] = *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + g) * 4);
+        m[i][1] = *reinterpret_cast<const uint32_t*>(res + kTile * RROW + ((row + 1) * NG + g) * 4);
+      }
+      failed = !mbar_wait_bounded(kdone, phase, kTcWaitLimitNs);
+      if (__syncthreads_or(failed)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int id = tid + 256 * i, p = id / CHUNKS, c = id % CHUNKS;
+        if (id >= 64 * CHUNKS) continue;
+        const int u0 = (4 * c) ^ v_unit_swizzle(p & 31, RROW / 2);
+        constexpr int PER = 32 / RES, CPW = PER / 8;
+        const int chunk0 = u0 * (16 / RES) / 8;           // its first channels, in 16-byte chunks
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t words[2] = {__byte_perm(w[i].x, w[i].y, e ? 0x7632 : 0x5410),
+                                     __byte_perm(w[i].z, w[i].w, e ? 0x7632 : 0x5410)};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t hi[PER / 2], lo[PER / 2];
+            word_levels<RES, false>(words[k], m[i][e], hi, lo);
+#pragma unroll
+            for (int q = 0; q < CPW; ++q) {
+              const int chunk = chunk0 + k * CPW + q;
+              *reinterpret_cast<uint4*>(smem + L::e + (chunk / 8) * (kKeys * 128) + panel_offset(2 * p + e, chunk % 8)) =
+                  make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            }
+          }
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          tc_mma(tmem + 128, panel_desc(hs + (x / 4) * (128 * 128) + (x % 4) * 32),
+                 panel_desc(es + (x / 4) * (kKeys * 128) + (x % 4) * 32), idv, x > 0);
+        tc_commit(vdone);
+      }
+    }
+    const int64_t at = (int64_t(unit) * a.v.tiles + tile) * L::kImg;
+    int first_out = INT_MAX;       // first chunk token out of range this thread saw
+    uint64_t x[D / 4];             // K epilogue: key r, of every group channels 16 hh ..
+    if (cached) {
+      const uint8_t* const sec = sec0 + (r >> 6) * SEC;
+      const int row = r & 63;
+      float al = 1.f;
+      if (RES) al = __half2float(*reinterpret_cast<const __half*>(sec + L::kRef + kTile * (RROW + 4 * NG) + row * 2));
+      // words 2 hh and 2 hh + 1 of every group
+      uint32_t w[2][NG];
+      if constexpr (NG == 4) {   // (odd row pairs read them in the other order: distinct banks)
+        const int swap = (r >> 1) & 1;
+        uint4 y[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          y[k] = *reinterpret_cast<const uint4*>(sec + row * (D / 2) + (2 * hh + (k ^ swap)) * 16);
+        const uint4 y0 = swap ? y[1] : y[0], y1 = swap ? y[0] : y[1];
+        w[0][0] = y0.x, w[0][1] = y0.y, w[0][2] = y0.z, w[0][3] = y0.w;
+        w[1][0] = y1.x, w[1][1] = y1.y, w[1][2] = y1.z, w[1][3] = y1.w;
+      } else {
+        const uint4 y = *reinterpret_cast<const uint4*>(sec + row * (D / 2) + hh * 16);
+        w[0][0] = y.x, w[0][1] = y.y, w[1][0] = y.z, w[1][1] = y.w;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float2 m = __half22float2(*reinterpret_cast<const __half2*>(sec + kTile * D / 2 + (row * NG + g) * 4));
+        const float as = m.x * al, z = m.y * al;
+        const uint64_t s01 = pack2(as, as * 0x1p-4f), s23 = pack2(as * 0x1p-8f, as * 0x1p-12f), zz = pack2(z, z);
+        if constexpr (RES != 0) {
+          uint32_t d[16];
+          tc_ld16(tmem + lanes + 32 * g + 16 * hh, d);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[8 * g + i] = fma2(pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])),
+                                *reinterpret_cast<const uint64_t*>(sign + g * 32 + 16 * hh + 2 * i), zz);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[8 * g + i] = zz;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) add_codes4(w[k][g], s01, s23, x + 8 * g + 4 * k);
+      }
+    }
+    if (RES && cached) {
+      failed = !mbar_wait_bounded(vdone, phase, kTcWaitLimitNs);       // E is free
+      tc_fence_after();
+    }
+    if (r < old) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x0, x1;
+          unpack2(x[4 * i + k], x0, x1);
+          hi[k] = half2_sat(x0, x1);
+          if constexpr (KLO) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+            lo[k] = half2_sat(x0 - f.x, x1 - f.y);
+          }
+        }
+        const int g = i / 2, chunk = (g % 2) * 4 + 2 * hh + i % 2;
+        const uint32_t o = (g / 2) * (kKeys * 128) + panel_offset(r, chunk);
+        *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (KLO) *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    // the chunk's own keys, 8 channels per thread; zeros behind them.  A token out of range makes
+    // its own and later rows NaN; the images stay finite.
+    for (int i = old * (D / 8) + tid; i < kKeys * (D / 8); i += 256) {
+      const int key = i / (D / 8), c = i % (D / 8), t = t0 + key;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (t < total) {
+        const uint16_t* const src = a.kv_new + b * a.ks0 + int64_t(t - ctx) * a.ks1 + h * a.ks_h + 8 * c;
+        if (a.vec) {
+          const uint4 q = *reinterpret_cast<const uint4*>(src);
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = uint32_t(src[2 * k]) | (uint32_t(src[2 * k + 1]) << 16);
+        }
+      }
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float x0 = x[8 * c + 2 * k], x1 = x[8 * c + 2 * k + 1];
-        hi[k] = half2_sat(x0, x1);
+        float v0 = __uint_as_float(w[k] << 16), v1 = __uint_as_float(w[k] & 0xffff0000u);
+        const bool b0 = !(fabsf(v0) <= kStateMax), b1 = !(fabsf(v1) <= kStateMax);
+        if (b0 | b1) first_out = min(first_out, t - ctx);
+        v0 = b0 ? 0.f : v0;
+        v1 = b1 ? 0.f : v1;
+        hi[k] = half2_sat(v0, v1);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-        lo[k] = half2_sat(x0 - f.x, x1 - f.y);
+        lo[k] = half2_sat(v0 - f.x, v1 - f.y);
       }
-      const uint32_t o = (c / 8) * (64 * 128) + panel_offset(r, c % 8);
-      *reinterpret_cast<uint4*>(img_k + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (a.klo) *reinterpret_cast<uint4*>(img_lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
+      *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (KLO) *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-  } else {   // transposed: panel row = channel, column = key
+    fence_async_smem();
+    if (__syncthreads_or(failed)) {
+      failed = true;
+      break;
+    }
+    if (tid == 0) {
+      bulk_s2g(a.k + at, smem_u32(smem + L::e), L::kImg);
+      if (KLO) bulk_s2g(a.klo + at, smem_u32(smem + L::lo), L::kImg);
+      bulk_s2g_commit();
+      if (L::v == L::e) bulk_s2g_wait_read();
+    }
+    // ---- V epilogue: channel ch, 32 keys at a time from k0 of record rec
+    constexpr int QS = D / 64;
+    const int ch = r & (D - 1), g = ch >> 5, u4 = (ch >> 2) * 4, nib = 4 * (ch & 3);
+    const int part = D == 128 ? 0 : r >> 6;               // (D = 64: lanes 64 .. hold the channels again)
+    const float sg = RES ? sign[D + ch] : 0.f;
+    const uint64_t sg2 = pack2(sg, sg), base = pack2(-8388608.f, -8388608.f);
+    uint32_t img[QS][16];
 #pragma unroll
-    for (int d = 0; d < D; d += 2) {
-      const uint32_t w = half2_sat(x[d], x[d + 1]);
-      *reinterpret_cast<uint16_t*>(img_v + panel_offset(d, r >> 3) + (r & 7) * 2) = uint16_t(w);
-      *reinterpret_cast<uint16_t*>(img_v + panel_offset(d + 1, r >> 3) + (r & 7) * 2) = uint16_t(w >> 16);
+    for (int q = 0; q < QS; ++q) {
+      const int k0 = hh * 64 + (D == 128 ? q : part) * 32;     // first key of these
+      uint32_t d[32];
+      if constexpr (RES != 0) {
+        if (cached) {
+          tc_ld32(tmem + 128 + lanes + k0, d);
+          tc_wait_ld();
+        }
+      }
+      float v[32];
+      if (cached) {
+        const uint8_t* const words = sec0 + hh * SEC + SIDE + (D == 128 ? q : part) * 16 * D;
+        const float2* const azk = az + ((k0 >> 1) * NG + g) * 2;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          constexpr int UNITS = D / 4;
+          const int swz = UNITS == 32 ? 8 * (k & 3) : 8 * ((k >> 1) & 1);    // (16 pairs: k decides)
+          const uint32_t word = *reinterpret_cast<const uint32_t*>(words + k * D + (u4 ^ (swz * 4))) >> nib;
+          const float4 f = *reinterpret_cast<const float4*>(azk + k * NG * 2);
+          uint64_t y = pack2(f.y, f.w);
+          if constexpr (RES != 0)
+            y = fma2(pack2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1])), sg2, y);
+          const uint64_t code = pack2(__uint_as_float((word & 0xFu) | 0x4B000000u),
+                                      __uint_as_float((word & 0xF0000u) | 0x4B000000u));
+          unpack2(fma2(add2(code, base), pack2(f.x, f.z), y), v[2 * k], v[2 * k + 1]);
+        }
+      }
+      if (k0 + 32 > old) {        // the chunk's own keys (all loads in flight, then the checks)
+        const uint16_t* const src = a.kv_new + a.kv_v + b * a.ks0 + h * a.ks_h + ch;
+        uint16_t y[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int t = t0 + k0 + k;
+          y[k] = t >= ctx && t < total ? src[int64_t(t - ctx) * a.ks1] : uint16_t(0);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int t = t0 + k0 + k;
+          const float f = bf16_bits_to_float(y[k]);
+          const bool out_of_range = !(fabsf(f) <= kStateMax);
+          if (t >= ctx) v[k] = out_of_range ? 0.f : f;
+          if (out_of_range) first_out = min(first_out, t - ctx);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) img[q][k] = half2_sat(v[2 * k], v[2 * k + 1]);
     }
+    if (L::v == L::e) __syncthreads();                    // K's image has left
+#pragma unroll
+    for (int q = 0; q < QS; ++q) {
+      const int c0 = (D == 128 ? q : part) * 4;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(smem + L::v + hh * (D * 128) + panel_offset(ch, c0 + c)) =
+            make_uint4(img[q][4 * c], img[q][4 * c + 1], img[q][4 * c + 2], img[q][4 * c + 3]);
+    }
+    if (first_out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, first_out);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();                                      // (sections, az and D are free)
+    tc_fence_after();
+    if (tid == 0) {
+      bulk_s2g(a.val + at, smem_u32(smem + L::v), L::kImg);
+      bulk_s2g_commit();
+    }
+    if (cached) phase ^= 1;
+    loading = false;
   }
-  fence_async_smem();
+  if (tid == 0) {
+    if (failed) {
+      atomicOr(a.v.err, 1u);
+      if (loading) mbar_wait_bounded(loaded, phase, kTcWaitLimitNs);     // (a copy that is still in flight)
+    }
+    bulk_s2g_wait();
+  }
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int64_t unit = int64_t(blockIdx.z) * a.v.H + h;
-    const int tile = blockIdx.x >> 1, half = blockIdx.x & 1;
-    const int64_t at = (unit * a.v.tiles + tile) * (kKeys * D * 2);
-#pragma unroll
-    for (int p = 0; p < D / 64; ++p) {
-      const int64_t o = at + p * (kKeys * 128) + half * (64 * 128);
-      bulk_s2g(a.k + o, smem_u32(img_k + p * 64 * 128), 64 * 128);
-      if (a.klo) bulk_s2g(a.klo + o, smem_u32(img_lo + p * 64 * 128), 64 * 128);
-    }
-    bulk_s2g(a.val + at + half * (D * 128), smem_u32(img_v), D * 128);
-    bulk_s2g_commit_wait();
-  }
+  if (RES && warp == 0) tc_free(tmem, 256);
 }
 
 // -------------------------------------------------------------------------------- attention
@@ -266,61 +549,96 @@ struct AttnArgs {
   ChunkView v;
   const uint16_t* q;
   int64_t qs0, qs1, qs2;
+  int qvec;                // q rows allow 16-byte loads
   const uint8_t *k, *klo, *val;
   uint16_t* out;
-  float* part;             // [unit][row][split][4 + D] (m, l, pad, O), or null: one split
-  float2* stats;           // (LSE) [unit][row][split] (m, l)
-  int n_splits, max_rows;  // max_rows: rows of a unit (n_new * heads, or the window's)
+  float* part;             // [unit][split][row tile] O images (below), or null: one split
+  float2* stats;           // [unit][split][padded row] (m, l): log2 units (LSE, or with part)
+  int n_splits, row_tiles; // row tiles (of 128) of a unit: stats' and part's
   float scale_log2;
 };
 
 template <int D>
 struct AttnSmem {
   static constexpr int kTileBytes = kKeys * D * 2;      // one K, V^T or Q tile
-  static constexpr int q = 0, k = 2 * kTileBytes, v = k + 2 * kTileBytes, bars = v + 2 * kTileBytes;
+  static constexpr int q = 0, k = 2 * kTileBytes, v = k + 2 * kTileBytes, exps = v + 2 * kTileBytes;
+  static constexpr int bars = exps + 2 * kRows * 4;
   static constexpr int total = bars + 256 + 1024;       // + alignment of the base
 };
 
-// Load a row of queries, scale it by a power of two so that its largest element lies in
-// [2^14, 2^15), store it as fp16 in a swizzled tile image.  Returns the exponent undone later.
-template <int D>
-__device__ __forceinline__ int store_query(const uint16_t* qp, bool valid, uint8_t* img, int r) {
-  float mx = 0.f;
-  uint32_t w[D / 2];
+// 32 rows of queries (this warp's rows of a tile) -> fp16 in the swizzled tile image, each row
+// scaled by a power of two so that its largest element lies in [2^14, 2^15); exps: the exponents,
+// undone in the scores' scale.  `row_ptr(r)`: row r's values, or null (zeros).
+template <int D, typename RowPtr>
+__device__ __forceinline__ void store_queries(RowPtr row_ptr, bool vec, uint8_t* img, int* exps, int r0, int lane) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;             // lanes per row, rows at a time
+  const int c = lane % LPR, sub = lane / LPR;
+  uint4 v[32 / RPI];
 #pragma unroll
-  for (int i = 0; i < D / 2; ++i) {
-    w[i] = valid ? uint32_t(qp[2 * i]) | (uint32_t(qp[2 * i + 1]) << 16) : 0u;
-    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-  }
-  int e = 0;
-  if (mx > 0.f && mx < INFINITY) {
-    frexpf(mx, &e);
-    e = 15 - e;
-    e = e > 100 ? 100 : e;        // (tiny rows: the scores vanish either way)
-  }
-  const float up = ldexpf(1.f, e > 60 ? 60 : e), up2 = ldexpf(1.f, e > 60 ? e - 60 : 0);
+  for (int i = 0; i < 32 / RPI; ++i) {
+    const uint16_t* p = row_ptr(r0 + i * RPI + sub);
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p == nullptr) continue;
+    if (vec) {
+      v[i] = *reinterpret_cast<const uint4*>(p + 8 * c);
+    } else {
+      uint32_t w[4];
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    uint32_t o[4];
+      for (int k = 0; k < 4; ++k) w[k] = uint32_t(p[8 * c + 2 * k]) | (uint32_t(p[8 * c + 2 * k + 1]) << 16);
+      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32 / RPI; ++i) {
+    const int r = r0 + i * RPI + sub;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float f[8], mx = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t x = w[4 * c + k];
-      o[k] = pack_half2(__uint_as_float(x << 16) * up * up2, __uint_as_float(x & 0xffff0000u) * up * up2);
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      mx = fmaxf(mx, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
     }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
+    // mx in [2^(x-127), 2^(x-126)), x its exponent field: scale by 2^(14 - (x - 127))
+    const int x = int(__float_as_uint(mx) >> 23);
+    const int e = x == 0 || x == 255 ? 0 : min(141 - x, 100);   // (0, subnormal, inf: as they are)
+    const float up = __uint_as_float(uint32_t(127 + (e >> 1)) << 23);
+    const float up2 = __uint_as_float(uint32_t(127 + e - (e >> 1)) << 23);
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = pack_half2(f[2 * k] * up * up2, f[2 * k + 1] * up * up2);
     *reinterpret_cast<uint4*>(img + (c / 8) * (kRows * 128) + panel_offset(r, c % 8)) =
         make_uint4(o[0], o[1], o[2], o[3]);
+    if (c == 0) exps[r] = e;
   }
-  return e;
+  __syncwarp();
+}
+
+// A row tile's O image in the workspace: 128 rows of D floats, the 16-byte chunk c of row r at
+// chunk position c ^ (r % (D / 4)).
+template <int D>
+__device__ __forceinline__ int o_image_offset(int r, int c) {
+  return r * (D * 4) + ((c ^ (r & (D / 4 - 1))) << 4);
+}
+
+__device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of warpgroup 0 or 1
+  if (i == 0)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 
 // Two tiles of 128 query rows per CTA share every K and V tile.  Warps 0-3 and 4-7: softmax of
 // tile 0 and 1, a thread per row; warp 8: copies; warp 9: products.  While one tile's softmax
 // runs, the other's products do:  S_0 S_1 | P_0 V, S_0' | P_1 V, S_1' | ...
 // The running maximum m is raised only when a tile exceeds it by 2^8 (O is rescaled in tensor
-// memory then; P stays below 2^8); P overwrites S's columns.
+// memory then; P stays below 2^8); P overwrites S's columns.  The softmax warps take registers
+// from the others, so that a row's 128 scores stay in registers.
 // LSE: scores with K in two parts, no P and V; (m, l) per row and split are stored.
 template <int D, bool LSE>
-__global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t raw[];
   using L = AttnSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -345,7 +663,7 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
   // (one thread reads the error word: another CTA may be setting it)
   const bool flagged = __syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile unsigned*>(a.v.err) != 0u);
   const bool ok = lens_of(a.v, b, n, ctx) && !flagged;
-  if (!ok) n = a.v.n_lens ? (n < 0 || n > a.v.n_new ? a.v.n_new : n) : a.v.n_new;
+  if (!ok) n = n < 0 || n > a.v.n_new ? a.v.n_new : n;
   const int first = LSE ? max(0, n - a.v.window) * a.v.heads : 0;   // first row of the unit's rows
   const int rows = n * a.v.heads - first;
   const int r0 = block * 2 * kRows;
@@ -372,109 +690,114 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
   bool failed = false;
-  float m = -INFINITY, l = 0.f, c = 0.f;
 
-  if (T > 0) {
-    if (warp == 8) {
-      if (lane == 0) {                                               // ---- copies
-        const uint8_t* k = a.k + (unit * a.v.tiles + kt0) * L::kTileBytes;
-        const uint8_t* v = (LSE ? a.klo : a.val) + (unit * a.v.tiles + kt0) * L::kTileBytes;
-        int issued = 0;
-        for (int j = 0; j < T; ++j, ++issued) {
-          const int s = j & 1;
-          if (j >= 2 && !(mbar_wait_bounded(kfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs))) break;
-          mbar_arrive_expect_tx(kfull(s), L::kTileBytes);
-          bulk_g2s(smem_u32(smem + L::k + s * L::kTileBytes), k + int64_t(j) * L::kTileBytes, L::kTileBytes, kfull(s));
-          if (j >= 2 && !(mbar_wait_bounded(vfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs))) {
-            mbar_wait_bounded(kfull(s), (j >> 1) & 1, kTcWaitLimitNs);
-            break;
-          }
-          mbar_arrive_expect_tx(vfull(s), L::kTileBytes);
-          bulk_g2s(smem_u32(smem + L::v + s * L::kTileBytes), v + int64_t(j) * L::kTileBytes, L::kTileBytes, vfull(s));
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8 && lane == 0 && T > 0) {                           // ---- copies
+      const uint8_t* k = a.k + (unit * a.v.tiles + kt0) * L::kTileBytes;
+      const uint8_t* v = (LSE ? a.klo : a.val) + (unit * a.v.tiles + kt0) * L::kTileBytes;
+      int issued = 0;
+      for (int j = 0; j < T; ++j, ++issued) {
+        const int s = j & 1;
+        if (j >= 2 && !mbar_wait_bounded(kfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs)) break;
+        mbar_arrive_expect_tx(kfull(s), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::k + s * L::kTileBytes), k + int64_t(j) * L::kTileBytes, L::kTileBytes, kfull(s));
+        if (j >= 2 && !mbar_wait_bounded(vfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs)) {
+          mbar_wait_bounded(kfull(s), (j >> 1) & 1, kTcWaitLimitNs);
+          break;
         }
-        failed = issued < T;
-        for (int j = max(0, issued - 2); j < issued; ++j) {          // no copy outlives the CTA
-          failed |= !mbar_wait_bounded(kfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
-          failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
-        }
+        mbar_arrive_expect_tx(vfull(s), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::v + s * L::kTileBytes), v + int64_t(j) * L::kTileBytes, L::kTileBytes, vfull(s));
       }
-      __syncwarp();
-    } else if (warp == 9) {
-      if (lane == 0) {                                               // ---- products
-        constexpr uint32_t ids = f16_idesc(kRows, kKeys), ido = f16_idesc(kRows, D);
-        auto scores = [&](int i, int s) {
-          const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + s * L::kTileBytes);
+      failed = issued < T;
+      for (int j = max(0, issued - 2); j < issued; ++j) {            // no copy outlives the CTA
+        failed |= !mbar_wait_bounded(kfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
+        failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
+      }
+    } else if (warp == 9 && lane == 0 && T > 0) {                    // ---- products
+      constexpr uint32_t ids = f16_idesc(kRows, kKeys), ido = f16_idesc(kRows, D);
+      auto scores = [&](int i, int s) {
+        const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + s * L::kTileBytes);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
+                 panel_desc(k + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, x > 0);
+        if (LSE) {
+          const uint32_t k2 = smem_u32(smem + L::v + s * L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
-            tc_mma(tS[i], panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
-                   panel_desc(k + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, x > 0);
-          if (LSE) {
-            const uint32_t k2 = smem_u32(smem + L::v + s * L::kTileBytes);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              tc_mma(tS[i], panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
-                     panel_desc(k2 + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, true);
-          }
-          tc_commit(sready(i));
-        };
-        auto values = [&](int i, int s, bool add) {
-          const uint32_t v = smem_u32(smem + L::v + s * L::kTileBytes);
-#pragma unroll
-          for (int x = 0; x < kKeys / 16; ++x)
-            tc_mma_ta(tO[i], tS[i] + 8 * x, panel_desc(v + (x / 4) * (D * 128) + (x % 4) * 32), ido, add || x > 0);
-        };
-        const int I = two ? 2 : 1;
-        bool good = mbar_wait_bounded(qready, 0, kTcWaitLimitNs) && mbar_wait_bounded(kfull(0), 0, kTcWaitLimitNs) &&
-                    (!LSE || mbar_wait_bounded(vfull(0), 0, kTcWaitLimitNs));
-        tc_fence_after();
-        if (good) {
-          for (int i = 0; i < I; ++i) scores(i, 0);
-          tc_commit(kfree(0));
-          if (LSE) tc_commit(vfree(0));
+            tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
+                   panel_desc(k2 + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, true);
         }
-        for (int j = 0; j < T && good; ++j) {
-          const int s = j & 1;
-          if (!LSE) good = mbar_wait_bounded(vfull(s), (j >> 1) & 1, kTcWaitLimitNs);
-          for (int i = 0; i < I && good; ++i) {
-            good = mbar_wait_bounded(pready(i), j & 1, kTcWaitLimitNs);
-            if (!good) break;
-            tc_fence_after();
-            if (!LSE) values(i, s, j > 0);
-            if (j + 1 < T) {
-              const int s1 = s ^ 1;
-              if (i == 0)
-                good = mbar_wait_bounded(kfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs) &&
-                       (!LSE || mbar_wait_bounded(vfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs));
-              if (good) scores(i, s1);
-            }
-          }
-          if (good && !LSE) tc_commit(vfree(s));
-          if (good && j + 1 < T) {
-            tc_commit(kfree(s ^ 1));
-            if (LSE) tc_commit(vfree(s ^ 1));
-          }
-        }
-        tc_commit(done);
-        failed = !good;
-        if (!good) mbar_wait_bounded(done, 0, kTcWaitLimitNs);       // nothing in flight
+        tc_commit(sready(i));
+      };
+      auto values = [&](int i, int s, bool add) {
+        const uint32_t v = smem_u32(smem + L::v + s * L::kTileBytes);
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x)
+          tc_mma_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * x, panel_desc(v + (x / 4) * (D * 128) + (x % 4) * 32),
+                    ido, add || x > 0);
+      };
+      const int I = two ? 2 : 1;
+      bool good = mbar_wait_bounded(qready, 0, kTcWaitLimitNs) && mbar_wait_bounded(kfull(0), 0, kTcWaitLimitNs) &&
+                  (!LSE || mbar_wait_bounded(vfull(0), 0, kTcWaitLimitNs));
+      tc_fence_after();
+      if (good) {
+        for (int i = 0; i < I; ++i) scores(i, 0);
+        tc_commit(kfree(0));
+        if (LSE) tc_commit(vfree(0));
       }
-      __syncwarp();
-    } else {                                                         // ---- softmax
-      const int i = warp >> 2, r = threadIdx.x & (kRows - 1);
-      const int row = r0 + i * kRows + r;
-      const bool valid = row < rows;
-      const int arow = row + first, j = min(arow / a.v.heads, n - 1), g = arow % a.v.heads;
-      const uint16_t* qp = a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.v.heads + g) * a.qs2;
-      const int e = store_query<D>(qp, valid, smem + L::q + i * L::kTileBytes, r);
-      c = ldexpf(a.scale_log2, -e);
+      for (int j = 0; j < T && good; ++j) {
+        const int s = j & 1;
+        if (!LSE) good = mbar_wait_bounded(vfull(s), (j >> 1) & 1, kTcWaitLimitNs);
+        for (int i = 0; i < I && good; ++i) {
+          good = mbar_wait_bounded(pready(i), j & 1, kTcWaitLimitNs);
+          if (!good) break;
+          tc_fence_after();
+          if (!LSE) values(i, s, j > 0);
+          if (j + 1 < T) {
+            const int s1 = s ^ 1;
+            if (i == 0)
+              good = mbar_wait_bounded(kfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs) &&
+                     (!LSE || mbar_wait_bounded(vfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs));
+            if (good) scores(i, s1);
+          }
+        }
+        if (good && !LSE) tc_commit(vfree(s));
+        if (good && j + 1 < T) {
+          tc_commit(kfree(s ^ 1));
+          if (LSE) tc_commit(vfree(s ^ 1));
+        }
+      }
+      tc_commit(done);
+      failed = !good;
+      if (!good) mbar_wait_bounded(done, 0, kTcWaitLimitNs);         // nothing in flight
+    }
+    __syncwarp();
+  } else {                                                           // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int i = warp >> 2, r = threadIdx.x & (kRows - 1);
+    const int row = r0 + i * kRows + r;
+    const bool valid = row < rows;
+    const uint32_t lanes = uint32_t(warp & 3) << 21;                 // this warp's tensor-memory lanes
+    const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
+    int* const exps = reinterpret_cast<int*>(smem + L::exps) + i * kRows;
+    float m = -INFINITY, l = 0.f;
+    if (T > 0) {
+      store_queries<D>(
+          [&](int rr) -> const uint16_t* {
+            const int x = r0 + i * kRows + rr;
+            if (x >= rows) return nullptr;
+            const int j = (x + first) / a.v.heads, g = (x + first) % a.v.heads;
+            return a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.v.heads + g) * a.qs2;
+          },
+          a.qvec, smem + L::q + i * L::kTileBytes, exps, (warp & 3) * 32, lane);
       fence_async_smem();
       mbar_arrive(qready);
-      const uint32_t lanes = uint32_t(warp & 3) << 21;               // this warp's tensor-memory lanes
-      const int lim = ctx + j;                                       // last key the row sees
-      const int j_first = min((r0 + i * kRows + first) / a.v.heads, n - 1);
-      const int clear = ctx + j_first;                               // every row of the tile sees these
+      const float c = ldexpf(a.scale_log2, -exps[r]);
+      const int lim = ctx + min((row + first) / a.v.heads, n - 1);   // last key the row sees
+      const int clear = ctx + min((r0 + i * kRows + first) / a.v.heads, n - 1);   // every row of the tile sees these
       if (i == 0 || two) {
         for (int jt = 0; jt < T; ++jt) {
           if (!mbar_wait_bounded(sready(i), jt & 1, kTcWaitLimitNs)) {
@@ -484,7 +807,7 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
           tc_fence_after();
           uint32_t s[kKeys];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) tc_ld32(tS[i] + lanes + 32 * x, s + 32 * x);
+          for (int x = 0; x < 4; ++x) tc_ld32(tS + 32 * x, s + 32 * x);
           tc_wait_ld();
           const int key0 = (kt0 + jt) * kKeys;
           if (key0 + kKeys - 1 > clear) {
@@ -497,7 +820,11 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
 #pragma unroll
           for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
 #pragma unroll
-          for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+          for (int x = 4; x < kKeys; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              mx[y] = x + 4 + y < kKeys ? fmaxf(mx[y], fmaxf(__uint_as_float(s[x + y]), __uint_as_float(s[min(x + 4 + y, kKeys - 1)])))
+                                        : fmaxf(mx[y], __uint_as_float(s[x + y]));
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           if (__any_sync(RQ_FULL_MASK, mt > m + kSlack)) {
             const float mn = mt > m + kSlack ? mt : m;
@@ -505,14 +832,14 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
             l *= f;
             m = mn;
             if (!LSE && jt > 0) {
-#pragma unroll
-              for (int x = 0; x < D / 32; ++x) {
-                uint32_t o[32];
-                tc_ld32(tO[i] + lanes + 32 * x, o);
+#pragma unroll 1
+              for (int x = 0; x < D / 16; ++x) {
+                uint32_t o[16];
+                tc_ld16(tO + 16 * x, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                tc_st32(tO[i] + lanes + 32 * x, o);
+                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tc_st16(tO + 16 * x, o);
               }
             }
           }
@@ -532,7 +859,7 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
               sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
               if (!LSE) p[x] = pack_half2(p0, p1);
             }
-            if (!LSE) tc_st32(tS[i] + lanes + 32 * half, p);
+            if (!LSE) tc_st32(tS + 32 * half, p);
           }
           float s0, s1;
           unpack2(add2(sum[0], sum[1]), s0, s1);
@@ -544,64 +871,91 @@ __global__ void __launch_bounds__(320, 1) attention_kernel(const __grid_constant
         if (!LSE && !failed) failed = !mbar_wait_bounded(done, 0, kTcWaitLimitNs);
       }
     }
-  }
-  const bool gave_up = __syncthreads_or(failed);
-  if (gave_up && threadIdx.x == 0) atomicOr(a.v.err, 1u);
-  if (warp < 8) {                                                    // ---- store
-    const int i = warp >> 2;
-    const int row = r0 + i * kRows + (threadIdx.x & (kRows - 1));
-    const bool valid = row < rows;
-    const uint32_t lanes = uint32_t(warp & 3) << 21;
+    // ---- store (a wait that gave up: NaN)
+    const bool gave_up = __any_sync(RQ_FULL_MASK, failed);
     const float nan = __int_as_float(0x7fc00000);
-    const int arow = row + first, j = arow / a.v.heads, g = arow % a.v.heads;
+    const int j = (row + first) / a.v.heads;
     const bool bad = !ok || gave_up || (valid && j >= a.v.first_bad[int64_t(b) * a.v.H + h]);
-    if (LSE) {
-      if (valid) a.stats[(unit * a.max_rows + row) * a.n_splits + split] = bad ? make_float2(nan, nan) : make_float2(m, l);
-    } else if (i == 0 || two) {
-      tc_fence_after();
-      float* const part = a.part + ((unit * a.max_rows + row) * a.n_splits + split) * (4 + D);
-      if (a.part && valid) *reinterpret_cast<float2*>(part) = bad ? make_float2(0.f, nan) : make_float2(m, l);
+    if ((i == 0 || two) && (LSE || a.part)) {
+      const int64_t tile = (unit * a.n_splits + split) * a.row_tiles + block * 2 + i;
+      if (valid) a.stats[tile * kRows + r] = bad ? make_float2(0.f, nan) : make_float2(m, l);
+      if (!LSE) {
+        uint8_t* const img = smem + (i == 0 ? L::q : L::k);          // (every product and copy is done)
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t w[32];
+          if (T > 0 && !gave_up) {
+            tc_ld32(tO + 32 * x, w);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) w[y] = 0u;
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            *reinterpret_cast<uint4*>(img + o_image_offset<D>(r, 8 * x + y)) =
+                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+        }
+        fence_async_smem();
+        warpgroup_barrier(i);
+        if (r == 0) {
+          bulk_s2g(a.part + tile * (kRows * D), smem_u32(img), kRows * D * 4);
+          bulk_s2g_commit();
+          bulk_s2g_wait();
+        }
+      }
+    } else if (!LSE && (i == 0 || two)) {
+      uint8_t* const img = smem + L::q + i * L::kTileBytes;          // 128 rows of D bf16
+      constexpr int CR = D / 8;                                      // 16-byte chunks of a row
       const float inv = bad ? nan : 1.f / l;
-      uint16_t* const o = a.out + ((int64_t(b) * a.v.n_new + j) * a.v.H * a.v.heads + h * a.v.heads + g) * D;
+      tc_fence_after();
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         uint32_t w[32];
         if (T > 0 && !gave_up) {
-          tc_ld32(tO[i] + lanes + 32 * x, w);
+          tc_ld32(tO + 32 * x, w);
           tc_wait_ld();
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) w[y] = 0u;
         }
-        if (!valid) continue;
-        if (a.part) {
 #pragma unroll
-          for (int y = 0; y < 32; y += 4)
-            *reinterpret_cast<uint4*>(part + 4 + 32 * x + y) = make_uint4(w[y], w[y + 1], w[y + 2], w[y + 3]);
+        for (int y = 0; y < 4; ++y) {
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(w[8 * y + 2 * k]) * inv,
+                                                          __uint_as_float(w[8 * y + 2 * k + 1]) * inv);
+            p[k] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(img + r * (D * 2) + (((4 * x + y) ^ (r & (CR - 1))) << 4)) =
+              make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      __syncwarp();
+      const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+#pragma unroll 4
+      for (int k = lane; k < 32 * CR; k += 32) {                     // this warp's rows, 16 bytes a lane
+        const int rr = (warp & 3) * 32 + k / CR, cc = k % CR, x = r0 + i * kRows + rr;
+        if (x >= rows) continue;
+        const uint4 w = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
+        uint16_t* const o = a.out + ((int64_t(b) * a.v.n_new + x / a.v.heads) * a.v.H * a.v.heads +
+                                     h * a.v.heads + x % a.v.heads) * D + 8 * cc;
+        if (vec) {
+          *reinterpret_cast<uint4*>(o) = w;
         } else {
+          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int y = 0; y < 32; y += 8) {
-            uint32_t p[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(w[y + 2 * k]) * inv,
-                                                            __uint_as_float(w[y + 2 * k + 1]) * inv);
-              p[k] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            if ((reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-              *reinterpret_cast<uint4*>(o + 32 * x + y) = make_uint4(p[0], p[1], p[2], p[3]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                o[32 * x + y + 2 * k] = uint16_t(p[k]);
-                o[32 * x + y + 2 * k + 1] = uint16_t(p[k] >> 16);
-              }
-            }
+          for (int e = 0; e < 4; ++e) {
+            o[2 * e] = uint16_t(q[e]);
+            o[2 * e + 1] = uint16_t(q[e] >> 16);
           }
         }
       }
     }
   }
+  if (__syncthreads_or(failed) && threadIdx.x == 0) atomicOr(a.v.err, 1u);
   tc_fence_before();
   __syncthreads();
   if (warp == 9) tc_free(tmem, 512);
@@ -612,27 +966,38 @@ template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int P = D / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t wid = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
-  if (wid >= a.max_rows) return;
-  const int row = int(wid), j = row / a.v.heads, g = row % a.v.heads;
+  const int j = row / a.v.heads, g = row % a.v.heads;
   int n = a.v.n_lens ? a.v.n_lens[b] : a.v.n_new;
   if (n < 0 || n > a.v.n_new) n = a.v.n_new;
   if (j >= n) return;
   const int64_t unit = int64_t(blockIdx.z) * a.v.H + h;
-  const float* part = a.part + (unit * a.max_rows + row) * a.n_splits * (4 + D);
+  const int64_t tile0 = unit * a.n_splits * a.row_tiles + row / kRows;
+  const int r = row % kRows;
   float M = -INFINITY, l = 0.f, o[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) o[i] = 0.f;
-  for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, part[int64_t(s) * (4 + D)]);
+  for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, a.stats[(tile0 + int64_t(s) * a.row_tiles) * kRows + r].x);
+#pragma unroll 4
   for (int s = 0; s < a.n_splits; ++s) {
-    const float* p = part + int64_t(s) * (4 + D);
-    const float ms = p[0], ls = p[1];
-    if (ms == -INFINITY) continue;
-    const float f = ex2(ms - M);
-    l = fmaf(f, ls, l);
-#pragma unroll
-    for (int i = 0; i < P; ++i) o[i] = fmaf(f, p[4 + lane * P + i], o[i]);
+    const int64_t tile = tile0 + int64_t(s) * a.row_tiles;
+    const float2 st = a.stats[tile * kRows + r];
+    if (st.x == -INFINITY) continue;
+    const float f = ex2(st.x - M);
+    l = fmaf(f, st.y, l);
+    const uint8_t* img = reinterpret_cast<const uint8_t*>(a.part + tile * (kRows * D));
+    if constexpr (D == 128) {
+      const float4 v = *reinterpret_cast<const float4*>(img + o_image_offset<D>(r, lane));
+      o[0] = fmaf(f, v.x, o[0]);
+      o[1] = fmaf(f, v.y, o[1]);
+      o[2] = fmaf(f, v.z, o[2]);
+      o[3] = fmaf(f, v.w, o[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(img + o_image_offset<D>(r, lane / 2) + (lane & 1) * 8);
+      o[0] = fmaf(f, v.x, o[0]);
+      o[1] = fmaf(f, v.y, o[1]);
+    }
   }
   uint16_t* out = a.out + ((int64_t(b) * a.v.n_new + j) * a.v.H * a.v.heads + h * a.v.heads + g) * D + lane * P;
   const float inv = *reinterpret_cast<volatile unsigned*>(a.v.err) ? __int_as_float(0x7fc00000) : 1.f / l;
@@ -646,12 +1011,13 @@ struct WeightArgs {
   ChunkView v;
   const uint16_t* q;
   int64_t qs0, qs1, qs2;
+  int qvec;
   const uint8_t *k, *klo;
   uint8_t* qimg;           // [unit][row tile][image of 128 rows]
   float2* scale;           // [unit][row]: (score scale, -log2-sum-exp); (0, -inf): no row
-  const float2* stats;     // [unit][row][split]
+  const float2* stats;     // [unit][split][padded row]
   float* weights;
-  int n_splits, max_rows, q_tiles, cap;
+  int n_splits, q_tiles, cap;
   float scale_log2;
 };
 
@@ -666,21 +1032,26 @@ __global__ void __launch_bounds__(128) window_rows_kernel(const __grid_constant_
   const int first = max(0, n - a.v.window) * a.v.heads, rows = n * a.v.heads - first;
   const int row = blockIdx.x * kRows + threadIdx.x;
   if (int(blockIdx.x) * kRows >= rows) return;
-  const bool valid = row < rows;
-  const int arow = valid ? row + first : first;
-  const int j = arow / a.v.heads, g = arow % a.v.heads;
-  const int e = store_query<D>(a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.v.heads + g) * a.qs2, valid, img,
-                               threadIdx.x);
+  __shared__ int exps[kRows];
+  store_queries<D>(
+      [&](int rr) -> const uint16_t* {
+        const int x = int(blockIdx.x) * kRows + rr;
+        if (x >= rows) return nullptr;
+        const int j = (x + first) / a.v.heads, g = (x + first) % a.v.heads;
+        return a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.v.heads + g) * a.qs2;
+      },
+      a.qvec, img, exps, (threadIdx.x >> 5) * 32, threadIdx.x & 31);
   float2 sc = make_float2(0.f, -INFINITY);
-  if (valid) {
-    const float2* st = a.stats + (unit * a.max_rows + row) * a.n_splits;
+  if (row < rows) {
+    const float2* st = a.stats + unit * a.n_splits * (int64_t(a.q_tiles) * kRows) + row;
+    const int64_t step = int64_t(a.q_tiles) * kRows;
     float M = -INFINITY, l = 0.f;
-    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, st[s].x);
+    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, st[s * step].x);
     for (int s = 0; s < a.n_splits; ++s) {
-      const float2 x = st[s];
+      const float2 x = st[s * step];
       if (x.x != -INFINITY) l = fmaf(ex2(x.x - M), x.y, l);
     }
-    sc = make_float2(ldexpf(a.scale_log2, -e), -(M + log2f(l)));
+    sc = make_float2(ldexpf(a.scale_log2, -exps[threadIdx.x]), -(M + log2f(l)));
   }
   a.scale[unit * (int64_t(a.q_tiles) * kRows) + row] = sc;
   __syncthreads();
@@ -849,7 +1220,7 @@ constexpr size_t kGroupBytes = size_t(4) << 30;   // images of the sequences han
 
 struct TcLayout {
   int group;               // sequences handled together
-  int tiles, rows, wrows, q_tiles, splits, wsplits;
+  int tiles, rows, r_tiles, wrows, q_tiles, splits, wsplits;
   size_t first_bad, k, klo, val, part, stats, qimg, scale, total;
 };
 
@@ -876,6 +1247,7 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   l.tiles = int((int64_t(max_ctx) + n_new + kKeys - 1) / kKeys);
   l.rows = n_new * heads;
   l.wrows = window * heads;
+  l.r_tiles = (l.rows + kRows - 1) / kRows;
   l.q_tiles = (l.wrows + kRows - 1) / kRows;
   const size_t tile = size_t(kKeys) * D * 2;
   const size_t seq = size_t(s.n_kv_heads) * l.tiles * tile * (window ? 3 : 2);
@@ -895,15 +1267,36 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   l.klo = o;
   if (window) o += units * l.tiles * tile;
   l.part = o;
-  if (l.splits > 1) o = round1k(o + units * l.rows * l.splits * (4 + size_t(D)) * 4);
-  l.stats = o;
-  o = round1k(o + units * l.wrows * l.wsplits * 8);
+  if (l.splits > 1) o += units * l.r_tiles * l.splits * (size_t(kRows) * D * 4);
+  l.stats = o;   // of the outputs' splits, then of the window's
+  const size_t st = l.splits > 1 ? size_t(l.r_tiles) * l.splits : 0, wst = size_t(l.q_tiles) * l.wsplits;
+  o += units * (st > wst ? st : wst) * kRows * 8;
   l.qimg = o;
   o += units * l.q_tiles * (size_t(kRows) * D * 2);
   l.scale = o;
   o = round1k(o + units * l.q_tiles * kRows * 8);
   l.total = o;
   return l;
+}
+
+template <int D, int RES, bool KLO>
+cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, cudaStream_t stream) {
+  using L = RebuildSmem<D, RES, KLO>;
+  const cudaError_t e = cudaFuncSetAttribute(rebuild_kernel<D, RES, KLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  if (e != cudaSuccess) return e;
+  if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int64_t ctas = int64_t(device_sm_count()) * (KLO ? 1 : 2);
+  rebuild_kernel<D, RES, KLO><<<unsigned(items < ctas ? items : ctas), 256, L::total, stream>>>(r, int(items));
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_rebuild_any(const RebuildArgs& r, int64_t items, cudaStream_t stream) {
+  if (r.bits == 0)
+    return r.klo ? launch_rebuild<D, 0, true>(r, items, stream) : launch_rebuild<D, 0, false>(r, items, stream);
+  if (r.bits == 2)
+    return r.klo ? launch_rebuild<D, 2, true>(r, items, stream) : launch_rebuild<D, 2, false>(r, items, stream);
+  return r.klo ? launch_rebuild<D, 4, true>(r, items, stream) : launch_rebuild<D, 4, false>(r, items, stream);
 }
 
 template <int D>
@@ -913,8 +1306,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
   cudaError_t e;
   using AS = AttnSmem<D>;
   using WS = WeightSmem<D>;
-  if ((e = cudaFuncSetAttribute(rebuild_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, rebuild_smem<D>())) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
+  if ((e = cudaFuncSetAttribute(attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(attention_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WS::total)) != cudaSuccess ||
       (e = cudaMemsetAsync(w + l.first_bad, 0x7f, size_t(s.batch) * s.n_kv_heads * 4, stream)) != cudaSuccess)
@@ -955,8 +1347,8 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.k = wb + l.k;
     r.klo = c.window ? wb + l.klo : nullptr;
     r.val = wb + l.val;
-    rebuild_kernel<D><<<dim3(unsigned(l.tiles) * 2, H, nb), 128, rebuild_smem<D>(), stream>>>(r);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    r.vec = reinterpret_cast<uintptr_t>(r.kv_new) % 16 == 0 && r.ks0 % 8 == 0 && r.ks1 % 8 == 0 && r.ks_h % 8 == 0;
+    if ((e = launch_rebuild_any<D>(r, int64_t(nb) * H * l.tiles, stream)) != cudaSuccess) return e;
     AttnArgs a;
     a.v = v;
     a.q = c.q;
@@ -970,10 +1362,11 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     a.part = l.splits > 1 ? reinterpret_cast<float*>(w + l.part) : nullptr;
     a.stats = reinterpret_cast<float2*>(w + l.stats);
     a.n_splits = l.splits;
-    a.max_rows = l.rows;
+    a.row_tiles = l.r_tiles;
+    a.qvec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.qs0 % 8 == 0 && a.qs1 % 8 == 0 && a.qs2 % 8 == 0;
     a.scale_log2 = scale;
     const unsigned blocks = unsigned((l.rows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, false><<<dim3(blocks * l.splits, H, nb), 320, AS::total, stream>>>(a);
+    attention_kernel<D, false><<<dim3(blocks * l.splits, H, nb), 384, AS::total, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.splits > 1) {
       merge_kernel<D><<<dim3(unsigned((l.rows + 3) / 4), H, nb), 128, 0, stream>>>(a);
@@ -981,9 +1374,9 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     }
     if (!c.window) continue;
     a.n_splits = l.wsplits;
-    a.max_rows = l.wrows;
+    a.row_tiles = l.q_tiles;
     const unsigned wblocks = unsigned((l.wrows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, true><<<dim3(wblocks * l.wsplits, H, nb), 320, AS::total, stream>>>(a);
+    attention_kernel<D, true><<<dim3(wblocks * l.wsplits, H, nb), 384, AS::total, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     WeightArgs x;
     x.v = v;
@@ -998,7 +1391,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     x.stats = a.stats;
     x.weights = c.weights;
     x.n_splits = l.wsplits;
-    x.max_rows = l.wrows;
+    x.qvec = a.qvec;
     x.q_tiles = l.q_tiles;
     x.cap = s.capacity;
     x.scale_log2 = scale;

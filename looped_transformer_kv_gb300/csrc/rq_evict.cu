@@ -12,22 +12,24 @@ namespace {
 
 // ------------------------------------------------------------------------------ select
 //
-// The k-th largest of a row's weights by radix selection: weights become 32-bit keys of the
-// same order, three passes over 11, 11 and 10 key bits count the digits of the keys that still
-// match, and fix the digit of the k-th one.  One more pass in slot order takes every key above
-// the k-th and, of its equals, the first ones.  A row is shared by a cluster of CTAs (each holds
-// its part of the keys in shared memory, the counts are added over the cluster).
+// Weights become 32-bit keys of the same order.  A short row (at most 1024 slots): a slot's rank is
+// counted directly, every key against every other.  A long one: the k-th largest key by radix
+// selection: three passes over 11, 11 and 10 key bits count the digits of the keys that still
+// match, and fix the digit of the k-th one.  One more pass in slot order takes every key above the
+// k-th and, of its equals, the first ones.  A long row may be shared by a cluster of CTAs (each
+// holds its part of the keys in shared memory, the counts are added over the cluster).
 // Bytes: 4 per slot read once, 4 per kept slot written; what bounds it is the latency of the
-// passes' barriers (short rows) and the shared-memory atomics of the first pass (long ones).
+// passes: loads and counts in the first, barriers in all.
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelKeys = 48 * 1024;     // keys a CTA holds in shared memory (192 KB)
+constexpr int kShortRow = 1024;
 constexpr uint32_t kHeld = 0xffffffffu; // key of a slot that is kept whatever its weight
 
-// Same order as the weights; NaN above every number, -0 as +0.
+// Same order as the weights; NaN above every number, -0 as +0; never 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(w + 0.f);
@@ -42,6 +44,8 @@ struct SelArgs {
   int H, cap, budget, n_first, n_last, slice;   // slice: keys of shared memory, 0: none
 };
 
+// Exclusive scan of one value per thread over the block (WARPS warps); total: the sum.
+template <int WARPS>
 __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -52,16 +56,60 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int& 
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int before = 0;
-  total = 0;
+  int s = lane < WARPS ? warp_sums[lane] : 0, before = lane < warp ? s : 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const int s = warp_sums[w];
-    if (w < warp) before += s;
-    total += s;
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(RQ_FULL_MASK, s, o);
+    before += __shfl_xor_sync(RQ_FULL_MASK, before, o);
   }
+  total = s;
   __syncthreads();
   return before + x - v;
+}
+
+// A row of at most kShortRow slots per CTA of kShortRow / 4 threads: 4 consecutive slots a thread.
+__global__ void __launch_bounds__(kShortRow / 4) evict_select_short_kernel(const __grid_constant__ SelArgs a) {
+  const int bh = blockIdx.x, b = bh / a.H;
+  const int n = a.ctx_lens[b];
+  __shared__ __align__(16) uint32_t keys[kShortRow];
+  __shared__ int warp_sums[32];
+  const bool bad = n < 0 || n > a.cap;
+  const int k = bad ? -1 : min(n, a.budget);
+  if (bh % a.H == 0 && threadIdx.x == 0) a.kept_lens[b] = k;
+  if (bad) return;
+  int32_t* const out = a.keep + int64_t(bh) * a.budget;
+  const float* const row = a.weights + int64_t(bh) * a.cap;
+  const int t0 = threadIdx.x * 4;
+  uint32_t mine[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + i;
+    mine[i] = t >= n ? 0u : (t < a.n_first || t >= n - a.n_last) ? kHeld : weight_key(row[t]);
+  }
+  *reinterpret_cast<uint4*>(keys + t0) = make_uint4(mine[0], mine[1], mine[2], mine[3]);
+  __syncthreads();
+  int rank[4] = {0, 0, 0, 0};           // keys above, and equal ones before
+  for (int u = 0; u < (n + 3) / 4; ++u) {   // (slots behind n have key 0, below every other)
+    const uint4 o = *reinterpret_cast<const uint4*>(keys + 4 * u);
+    const uint32_t ok[4] = {o.x, o.y, o.z, o.w};
+    const uint32_t eq = 4 * u < t0 ? 1u : 0u;   // earlier groups: an equal key counts as above
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rank[i] += ok[e] > mine[i] - eq ? 1 : 0;
+  }
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < i; ++e) rank[i] += mine[e] == mine[i] ? 1 : 0;
+  int c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c += t0 + i < n && rank[i] < k ? 1 : 0;
+  int total;
+  int at = block_exclusive_scan<kShortRow / 128>(c, warp_sums, total);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (t0 + i < n && rank[i] < k) out[at++] = t0 + i;
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ SelArgs a) {
@@ -72,7 +120,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   extern __shared__ uint32_t keys[];
   __shared__ int hist[2][kBins];          // alternating passes
-  __shared__ int warp_sums[kSelWarps];
+  __shared__ int warp_sums[32];
   __shared__ int found[2], counts[2];     // (digit, its rank from above); (above, equal) of this CTA
   const bool bad = n < 0 || n > a.cap;
   const int k = bad ? -1 : min(n, a.budget);
@@ -83,6 +131,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int t = rank * kSelThreads + threadIdx.x; t < n; t += C * kSelThreads) out[t] = t;
     return;
   }
+  auto sync_all = [&]() {
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   // this CTA's slots [t0, t1): a multiple of 32 per warp
   const int per_warp = ((n + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32;
   const int t0 = min(n, rank * kSelWarps * per_warp), t1 = min(n, t0 + kSelWarps * per_warp);
@@ -104,45 +158,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const int sh = shift[pass];
     const uint32_t digits = pass == 2 ? 1024u : 2048u;
     int* const h = hist[pass & 1];
-    for (int t = t0 + threadIdx.x; t - threadIdx.x < t1; t += kSelThreads) {
-      uint32_t key = 0;
-      bool mine = t < t1;
-      if (mine) {
+    constexpr int U = 8;                  // slots a thread has in flight
+    for (int base = t0; base < t1; base += U * kSelThreads) {
+      uint32_t key[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = base + u * kSelThreads + threadIdx.x;
+        key[u] = t < t1 ? (pass == 0 ? fresh_key(t) : key_at(t)) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = base + u * kSelThreads + threadIdx.x;
+        bool mine = t < t1;
         if (pass == 0) {
-          key = fresh_key(t);
-          if (stored) keys[t - t0] = key;
+          if (mine && stored) keys[t - t0] = key[u];
         } else {
-          key = key_at(t);
-          mine = (key >> (sh + (pass == 2 ? 10 : 11))) == prefix;
+          mine = mine && (key[u] >> (sh + (pass == 2 ? 10 : 11))) == prefix;
+        }
+        const uint32_t d = (key[u] >> sh) & (digits - 1u);
+        // a warp whose keys share a digit (equal weights) adds once
+        const unsigned active = __ballot_sync(RQ_FULL_MASK, mine);
+        if (active == 0u) continue;
+        const uint32_t d0 = __shfl_sync(RQ_FULL_MASK, d, __ffs(active) - 1);
+        if (__all_sync(RQ_FULL_MASK, !mine || d == d0)) {
+          if (lane == 0) atomicAdd(&h[d0], __popc(active));
+        } else if (mine) {
+          atomicAdd(&h[d], 1);
         }
       }
-      const uint32_t d = (key >> sh) & (digits - 1u);
-      // a warp whose keys share a digit (equal weights) adds once
-      const unsigned active = __ballot_sync(RQ_FULL_MASK, mine);
-      if (active == 0u) continue;
-      const uint32_t d0 = __shfl_sync(RQ_FULL_MASK, d, __ffs(active) - 1);
-      if (__all_sync(RQ_FULL_MASK, !mine || d == d0)) {
-        if (lane == 0) atomicAdd(&h[d0], __popc(active));
-      } else if (mine) {
-        atomicAdd(&h[d], 1);
-      }
     }
-    cluster.sync();
-    // counts of the cluster, four digits per thread, from the highest digit down
-    int c[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = kBins - 1 - (int(threadIdx.x) * 4 + i);
-      c[i] = 0;
-      for (int r = 0; r < C; ++r) c[i] += cluster.map_shared_rank(h, r)[d];
-      sum += c[i];
+    sync_all();
+    // counts of the cluster, two digits per thread, from the highest digit down
+    int c[2] = {0, 0};
+    const int top = kBins - 1 - 2 * int(threadIdx.x);
+    for (int r = 0; r < C; ++r) {
+      const int* const hr = C > 1 ? cluster.map_shared_rank(h, r) : h;
+      c[0] += hr[top];
+      c[1] += hr[top - 1];
     }
     int total;
-    int above = block_exclusive_scan(sum, warp_sums, total);
+    int above = block_exclusive_scan<kSelWarps>(c[0] + c[1], warp_sums, total);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (above < need && need <= above + c[i]) {
-        found[0] = kBins - 1 - (int(threadIdx.x) * 4 + i);
+        found[0] = top - i;
         found[1] = need - above;
       }
       above += c[i];
@@ -150,7 +209,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __syncthreads();
     prefix = (prefix << (pass == 2 ? 10 : 11)) | uint32_t(found[0]);
     need = found[1];
-    cluster.sync();   // the counts of this pass have been read by everyone
+    sync_all();       // the counts of this pass have been read by everyone
     if (pass == 0) {  // (the last pass counts in this array again)
       for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[0][i] = 0;
       __syncthreads();
@@ -159,17 +218,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   // prefix: the k-th key; `need` of its equals are kept, the lowest slots
   const int w0 = t0 + warp * per_warp, w1 = min(t1, w0 + per_warp);
   int above = 0, equal = 0;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t key = t < w1 ? key_at(t) : 0u;
-    above += __popc(__ballot_sync(RQ_FULL_MASK, t < w1 && key > prefix));
-    equal += __popc(__ballot_sync(RQ_FULL_MASK, t < w1 && key == prefix));
+  for (int t = w0 + lane; t < w1; t += 32) {
+    const uint32_t key = key_at(t);
+    above += key > prefix ? 1 : 0;
+    equal += key == prefix ? 1 : 0;
   }
-  int total;
-  const int above_before = block_exclusive_scan(lane == 0 ? above : 0, warp_sums, total);
-  if (threadIdx.x == 0) counts[0] = total;
-  const int equal_before = block_exclusive_scan(lane == 0 ? equal : 0, warp_sums, total);
-  if (threadIdx.x == 0) counts[1] = total;
-  cluster.sync();
+  int above_all, equal_all;
+  const int above_before = block_exclusive_scan<kSelWarps>(above, warp_sums, above_all);
+  const int equal_before = block_exclusive_scan<kSelWarps>(equal, warp_sums, equal_all);
+  if (threadIdx.x == 0) {
+    counts[0] = above_all;
+    counts[1] = equal_all;
+  }
+  sync_all();
   int A = __shfl_sync(RQ_FULL_MASK, above_before, 0), E = __shfl_sync(RQ_FULL_MASK, equal_before, 0);
   for (int r = 0; r < rank; ++r) {
     A += cluster.map_shared_rank(counts, r)[0];
@@ -186,7 +247,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     A += __popc(ma);
     E += __popc(me);
   }
-  cluster.sync();   // (no CTA leaves while its counts may be read)
+  if (C > 1) cluster.sync();   // (no CTA leaves while its counts may be read)
 }
 
 // ------------------------------------------------------------------------------ compact
@@ -229,12 +290,14 @@ struct Unit {
   bool v_codes;
 };
 
-template <int D>
-__device__ __forceinline__ Unit unit_of(int i, int bits, bool residual) {
+// KIND: 0 the reference section, else a residual section of that many bits.
+template <int D, int KIND>
+__device__ __forceinline__ Unit unit_of(int i) {
   constexpr int NG = D / 32;
-  const int rb = D * bits / 8, chunks = rb / 16;
-  const int nc = kTile * chunks, per = nc + kTile + (residual ? kTile : 0);
-  const int side = kTile * (rb + NG * 4 + (residual ? 2 : 0));
+  constexpr bool residual = KIND != 0;
+  constexpr int rb = D * (residual ? KIND : 4) / 8, chunks = rb / 16;
+  constexpr int nc = kTile * chunks, per = nc + kTile + (residual ? kTile : 0);
+  constexpr int side = kTile * (rb + NG * 4 + (residual ? 2 : 0));
   Unit u;
   u.v_codes = false;
   const bool v = i >= per;
@@ -268,16 +331,14 @@ __device__ __forceinline__ Unit unit_of(int i, int bits, bool residual) {
   return u;
 }
 
-template <int D, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __grid_constant__ MoveArgs a) {
-  const int sect = blockIdx.y;                       // 0: reference, 1 + l: loop l
+template <int D, bool IN_PLACE, int KIND>
+__device__ __forceinline__ void move_section(const MoveArgs& a, int sect) {
   const int per_bh = IN_PLACE ? kMoveCluster : a.tiles;
   const int64_t bh = blockIdx.x / per_bh;
   const int first_tile = blockIdx.x % per_bh;
   const int b = int(bh / a.H), h = int(bh % a.H);
   const int kept = max(0, min(a.kept_lens[b], min(a.budget, a.dst_cap)));
   const int n_tiles = (kept + kTile - 1) / kTile;
-  const int bits = sect == 0 ? 4 : a.res_bits[sect - 1];
   const int sec_off = sect == 0 ? 0 : loop_section_offset(D, a.res_bits, sect - 1);
   const int32_t* const keep = a.keep + bh * a.budget;
   __shared__ int64_t from[kTile];                    // record offset of each row's source, -1: none
@@ -318,7 +379,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __gri
     int live[kMoveUnits];          // bit 0: the (first) row has a source, bit 1: the pair's second
 #pragma unroll
     for (int i = 0; i < kMoveUnits; ++i) {
-      const Unit u = unit_of<D>(threadIdx.x + i * kMoveThreads, bits, sect > 0);
+      const Unit u = unit_of<D, KIND>(threadIdx.x + i * kMoveThreads);
       live[i] = 0;
       if (u.bytes == 0 || dst < 0) continue;
       if (!u.v_codes) {
@@ -372,7 +433,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < kMoveUnits; ++i) {
       if (live[i] == 0) continue;
-      const Unit u = unit_of<D>(threadIdx.x + i * kMoveThreads, bits, sect > 0);
+      const Unit u = unit_of<D, KIND>(threadIdx.x + i * kMoveThreads);
       if (!u.v_codes) {
         uint8_t* p = a.dst + dst + u.off + u.row * u.row_bytes + u.chunk * 16;
         if (u.bytes == 16)
@@ -415,6 +476,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __gri
   }
 }
 
+template <int D, bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __grid_constant__ MoveArgs a) {
+  const int sect = blockIdx.y;                       // 0: reference, 1 + l: loop l
+  if (sect == 0)
+    move_section<D, IN_PLACE, 0>(a, 0);
+  else if (a.res_bits[sect - 1] == 2)
+    move_section<D, IN_PLACE, 2>(a, sect);
+  else
+    move_section<D, IN_PLACE, 4>(a, sect);
+}
+
 template <typename Kernel, typename Args>
 cudaError_t launch_clusters(Kernel kernel, dim3 grid, int threads, size_t smem, int cluster,
                             cudaStream_t stream, const Args& args) {
@@ -449,6 +521,11 @@ cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads,
   a.n_first = n_first;
   a.n_last = n_last;
   const int64_t rows = int64_t(batch) * n_kv_heads;
+  if (capacity <= kShortRow) {
+    a.slice = 0;
+    evict_select_short_kernel<<<unsigned(rows), kShortRow / 4, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
   // CTAs per row: enough that the keys fit shared memory, more while the rows leave SMs free
   // and each CTA keeps a few thousand slots
   int C = 1;

@@ -86,6 +86,13 @@ def rebuild(records, n, d, bits, loop, kv, signs):
     return out
 
 
+def residual_norms(records, n, d, bits, loop, kv):
+    """Euclidean norm of each token's residual levels (0 for the final loop)."""
+    if loop == len(bits):
+        return np.zeros(n)
+    return np.array([np.linalg.norm(_level(records[t // TILE], t % TILE, d, bits, loop, kv)) for t in range(n)])
+
+
 def attend(q, k, v, ctx, scale):
     """q [m][G][d], k, v [ctx + m][d]: causal over the chunk.  Outputs [m][G][d], weights
     [m][G][ctx + m] and the largest sum |q k| * scale of each row."""
