@@ -54,6 +54,7 @@ struct RebuildArgs {
   int64_t rec_bytes;
   const int32_t* bt;
   int max_pages, n_pages, cap;
+  int old_tiles;                 // tiles of cached keys, at most
   int bits, sec_off;             // residual bits (0: final loop), offset of the loop's section
   const int8_t* signs[2];
   const uint16_t* kv_new;
@@ -123,7 +124,137 @@ struct RebuildSmem {
   static_assert(total <= (KLO ? 227 * 1024 : 113 * 1024), "two CTAs per SM without K's low parts");
 };
 
-// Persistent CTAs over tiles of 128 keys.  The rotation is undone on the tensor cores:
+// 8 channels of chunk token t (K or V side) as fp16 pairs; a value out of range becomes 0 and `out`
+// the token, so that the images stay finite while its own and later rows become NaN.
+__device__ __forceinline__ uint4 load_states(const uint16_t* src, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(src);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = uint32_t(src[2 * k]) | (uint32_t(src[2 * k + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t state_pair(uint32_t w, int t, int& out, uint32_t* lo = nullptr) {
+  float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+  const bool b0 = !(fabsf(v0) <= kStateMax), b1 = !(fabsf(v1) <= kStateMax);
+  if (b0 | b1) out = min(out, t);
+  v0 = b0 ? 0.f : v0;
+  v1 = b1 ? 0.f : v1;
+  const uint32_t hi = half2_sat(v0, v1);
+  if (lo) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    *lo = half2_sat(v0 - f.x, v1 - f.y);
+  }
+  return hi;
+}
+
+// The chunk's own keys in the tile that holds the context's end: rows old .. 127 of the image in
+// shared memory (zeros behind the last token).
+template <int D, bool KLO, bool V>
+__device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int n, int ctx, int t0, int old,
+                                        uint8_t* img, uint8_t* img_lo) {
+  int out = INT_MAX;
+#pragma unroll 1
+  for (int i = old * (D / 8) + threadIdx.x; i < kKeys * (D / 8); i += 256) {
+    const int key = i / (D / 8), c = i % (D / 8), t = t0 + key - ctx;
+    const uint16_t* src = a.kv_new + (V ? a.kv_v : 0) + b * a.ks0 + int64_t(min(t, n - 1)) * a.ks1 + h * a.ks_h + 8 * c;
+    uint4 y = load_states(src, a.vec);
+    if (t >= n) y = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t lo[4];
+    const uint32_t w[4] = {state_pair(y.x, t, out, lo), state_pair(y.y, t, out, lo + 1),
+                           state_pair(y.z, t, out, lo + 2), state_pair(y.w, t, out, lo + 3)};
+    if constexpr (!V) {
+      const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
+      *reinterpret_cast<uint4*>(img + o) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (KLO) *reinterpret_cast<uint4*>(img_lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint16_t*>(img + (key >> 6) * (D * 128) + panel_offset(8 * c + e, (key & 63) >> 3) +
+                                     (key & 7) * 2) = uint16_t(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+  if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
+}
+
+// Tiles of the chunk's own keys alone: one CTA each.  Rows are loaded 16 bytes a lane; V goes
+// through shared memory to have channels as rows.  Bound by HBM latency.
+template <int D, bool KLO>
+__global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant__ RebuildArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+  constexpr int IMG = kKeys * D * 2, C = D / 8, IT = kKeys * C / 256;
+  uint8_t* const img = smem;                    // K, then V
+  uint8_t* const rows = smem + IMG;             // V as it came
+  uint8_t* const img_lo = smem + 2 * IMG;
+  const int tid = threadIdx.x, h = blockIdx.x % a.v.H, b = a.v.b0 + blockIdx.z;
+  int n, ctx;
+  if (!lens_of(a.v, b, n, ctx)) {
+    if (tid == 0) atomicOr(a.v.err, 1u);
+    return;
+  }
+  const int tile = (ctx + kKeys - 1) / kKeys + blockIdx.x / a.v.H, t0 = tile * kKeys - ctx;   // first token
+  if (t0 >= n) return;
+  const int c = tid % C;
+  const uint16_t* const src = a.kv_new + b * a.ks0 + h * a.ks_h + 8 * c;
+  uint4 y[IT], v[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const uint16_t* p = src + int64_t(min(t0 + (tid + 256 * i) / C, n - 1)) * a.ks1;
+    y[i] = load_states(p, a.vec);
+    v[i] = load_states(p + a.kv_v, a.vec);
+  }
+  int out = INT_MAX;
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int key = (tid + 256 * i) / C, t = t0 + key;
+    if (t >= n) y[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t lo[4];
+    const uint4 hi = make_uint4(state_pair(y[i].x, t, out, lo), state_pair(y[i].y, t, out, lo + 1),
+                                state_pair(y[i].z, t, out, lo + 2), state_pair(y[i].w, t, out, lo + 3));
+    const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
+    *reinterpret_cast<uint4*>(img + o) = hi;
+    if (KLO) *reinterpret_cast<uint4*>(img_lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(rows + key * (D * 2) + c * 16) =
+        make_uint4(state_pair(v[i].x, t, out), state_pair(v[i].y, t, out), state_pair(v[i].z, t, out),
+                   state_pair(v[i].w, t, out));
+  }
+  if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
+  fence_async_smem();
+  __syncthreads();
+  const int64_t at = ((int64_t(blockIdx.z) * a.v.H + h) * a.v.tiles + tile) * IMG;
+  if (tid == 0) {
+    bulk_s2g(a.k + at, smem_u32(img), IMG);
+    if (KLO) bulk_s2g(a.klo + at, smem_u32(img_lo), IMG);
+    bulk_s2g_commit();
+  }
+  // V^T: a thread per channel and 8 keys at a time (lanes: channels)
+  uint4 w[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int id = tid + 256 * i, ch = id % D, k0 = id / D * 8;
+    uint32_t p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      p[k] = uint32_t(*reinterpret_cast<const uint16_t*>(rows + (k0 + 2 * k) * (D * 2) + ch * 2)) |
+             (uint32_t(*reinterpret_cast<const uint16_t*>(rows + (k0 + 2 * k + 1) * (D * 2) + ch * 2)) << 16);
+    w[i] = make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  __syncthreads();                              // `rows` becomes the image
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int id = tid + 256 * i, ch = id % D, k0 = id / D * 8;
+    *reinterpret_cast<uint4*>(rows + (k0 >> 6) * (D * 128) + panel_offset(ch, (k0 & 63) >> 3)) = w[i];
+  }
+  fence_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_s2g(a.val + at, smem_u32(rows), IMG);
+    bulk_s2g_commit();
+    bulk_s2g_wait();
+  }
+}
+
+// Persistent CTAs over tiles of 128 keys that hold cached ones.  The rotation is undone on the tensor cores:
 //   K: D[key][channel] = E H^T,   V: D[channel][key] = H E^T     (E: residual levels, fp16;
 // H: Hadamard +-1), and the epilogues add the reference, x = D sign / sqrt(d) + a (s c + z), in
 // fp32, round once and write the images through shared memory: a thread per key and half the
@@ -180,49 +311,63 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
   int phase = 0;
   bool failed = false, loading = false;
 
+  // record i (0, 1) of a tile; a bad page (flagged) reads as page 0
+  auto record = [&](int b, int h, int tile, int i) -> const uint8_t* {
+    int64_t rec;
+    if (a.bt) {
+      int pg = a.bt[int64_t(b) * a.max_pages + 2 * tile + i];
+      if (pg < 0 || pg >= a.n_pages) {
+        atomicOr(a.v.err, 1u);
+        pg = 0;
+      }
+      rec = int64_t(pg) * a.v.H + h;
+    } else {
+      rec = (int64_t(b) * a.v.H + h) * (a.cap / kTile) + 2 * tile + i;
+    }
+    return a.data + rec * a.rec_bytes;
+  };
+  int bl_known = -1, n = 0, ctx = 0;
+  bool lens_good = false;
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
     // heads first: the heads of a chunk token lie next to each other
-    const int h = item % a.v.H, tile = item / a.v.H % a.v.tiles, bl = item / a.v.H / a.v.tiles;
+    const int h = item % a.v.H, tile = item / a.v.H % a.old_tiles, bl = item / a.v.H / a.old_tiles;
     const int b = a.v.b0 + bl, unit = bl * a.v.H + h;
-    int n, ctx;
-    if (!lens_of(a.v, b, n, ctx)) {
-      if (tid == 0) atomicOr(a.v.err, 1u);
-      continue;
+    if (bl != bl_known) {
+      bl_known = bl;
+      lens_good = lens_of(a.v, b, n, ctx);
+      if (!lens_good && tid == 0) atomicOr(a.v.err, 1u);
     }
-    const int t0 = tile * kKeys, total = n > 0 ? ctx + n : 0;
-    if (t0 >= total) continue;
-    const int old = min(kKeys, max(0, ctx - t0));          // cached keys of the tile
-    const bool cached = old > 0;
+    if (!lens_good) continue;
+    const int t0 = tile * kKeys;
+    if (t0 >= ctx || n == 0) continue;
+    const int old = min(kKeys, ctx - t0);                  // cached keys of the tile
     uint8_t* const sec0 = smem + L::sec;
-    loading = cached;
+    loading = true;
     if (tid == 0) {
-      if (cached) {
-        fence_async_smem();
-        const int n_rec = old > kTile ? 2 : 1;
-        mbar_arrive_expect_tx(loaded, uint32_t(n_rec) * SEC);
-        for (int i = 0; i < n_rec; ++i) {
-          int64_t rec;
-          if (a.bt) {
-            int pg = a.bt[int64_t(b) * a.max_pages + 2 * tile + i];
-            if (pg < 0 || pg >= a.n_pages) {
-              atomicOr(a.v.err, 1u);
-              pg = 0;
-            }
-            rec = int64_t(pg) * a.v.H + h;
-          } else {
-            rec = (int64_t(b) * a.v.H + h) * (a.cap / kTile) + 2 * tile + i;
-          }
-          const uint8_t* src = a.data + rec * a.rec_bytes;
-          const uint32_t dst = smem_u32(sec0) + i * SEC;
-          bulk_g2s(dst, src, L::kRef, loaded);
-          if (RES) bulk_g2s(dst + L::kRef, src + a.sec_off, L::kRes, loaded);
+      fence_async_smem();
+      const int n_rec = old > kTile ? 2 : 1;
+      mbar_arrive_expect_tx(loaded, uint32_t(n_rec) * SEC);
+      for (int i = 0; i < n_rec; ++i) {
+        const uint8_t* src = record(b, h, tile, i);
+        const uint32_t dst = smem_u32(sec0) + i * SEC;
+        bulk_g2s(dst, src, L::kRef, loaded);
+        if (RES) bulk_g2s(dst + L::kRef, src + a.sec_off, L::kRes, loaded);
+      }
+      // the sections of the next tile of this sequence come to L2 meanwhile
+      const int next = item + gridDim.x;
+      if (next < n_items && next / a.v.H / a.old_tiles == bl) {
+        const int nh = next % a.v.H, nt = next / a.v.H % a.old_tiles;
+        for (int i = 0; i < 2 && nt * kKeys + i * kTile < ctx; ++i) {
+          const uint8_t* src = record(b, nh, nt, i);
+          bulk_prefetch(src, L::kRef);
+          if (RES) bulk_prefetch(src + a.sec_off, L::kRes);
         }
       }
       bulk_s2g_wait_read();       // the last tile's image has left
     }
     if (tid < 2 * D) sign[tid] = float(a.signs[tid / D][int64_t(h) * D + tid % D]) * inv_sqrt_d;
     __syncthreads();
-    if (cached) {
+    {
       failed = !mbar_wait_bounded(loaded, phase, kTcWaitLimitNs);
       if constexpr (RES != 0) {   // E of K: a thread per key and half its words
         constexpr int PER = 32 / RES, CPW = PER / 8;      // codes and 16-byte chunks per word
@@ -275,7 +420,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
       failed = true;
       break;
     }
-    if constexpr (RES != 0) if (cached) {
+    if constexpr (RES != 0) {
       constexpr uint32_t idk = f16_idesc(kKeys, D), idv = f16_idesc(128, kKeys);
       const uint32_t hs = smem_u32(smem + L::h), es = smem_u32(smem + L::e);
       if (tid == 0) {
@@ -346,9 +491,8 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
       }
     }
     const int64_t at = (int64_t(unit) * a.v.tiles + tile) * L::kImg;
-    int first_out = INT_MAX;       // first chunk token out of range this thread saw
     uint64_t x[D / 4];             // K epilogue: key r, of every group channels 16 hh ..
-    if (cached) {
+    {
       const uint8_t* const sec = sec0 + (r >> 6) * SEC;
       const int row = r & 63;
       float al = 1.f;
@@ -389,11 +533,11 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
         for (int k = 0; k < 2; ++k) add_codes4(w[k][g], s01, s23, x + 8 * g + 4 * k);
       }
     }
-    if (RES && cached) {
+    if (RES) {
       failed = !mbar_wait_bounded(vdone, phase, kTcWaitLimitNs);       // E is free
       tc_fence_after();
     }
-    if (r < old) {
+    {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t hi[4], lo[4];
@@ -413,36 +557,10 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
         if constexpr (KLO) *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    // the chunk's own keys, 8 channels per thread; zeros behind them.  A token out of range makes
-    // its own and later rows NaN; the images stay finite.
-    for (int i = old * (D / 8) + tid; i < kKeys * (D / 8); i += 256) {
-      const int key = i / (D / 8), c = i % (D / 8), t = t0 + key;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (t < total) {
-        const uint16_t* const src = a.kv_new + b * a.ks0 + int64_t(t - ctx) * a.ks1 + h * a.ks_h + 8 * c;
-        if (a.vec) {
-          const uint4 q = *reinterpret_cast<const uint4*>(src);
-          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = uint32_t(src[2 * k]) | (uint32_t(src[2 * k + 1]) << 16);
-        }
-      }
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v0 = __uint_as_float(w[k] << 16), v1 = __uint_as_float(w[k] & 0xffff0000u);
-        const bool b0 = !(fabsf(v0) <= kStateMax), b1 = !(fabsf(v1) <= kStateMax);
-        if (b0 | b1) first_out = min(first_out, t - ctx);
-        v0 = b0 ? 0.f : v0;
-        v1 = b1 ? 0.f : v1;
-        hi[k] = half2_sat(v0, v1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-        lo[k] = half2_sat(v0 - f.x, v1 - f.y);
-      }
-      const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
-      *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if constexpr (KLO) *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    // the chunk's own keys of the last cached tile over the rows behind the context
+    if (old < kKeys) {
+      __syncthreads();
+      mixed_rows<D, KLO, false>(a, b, h, n, ctx, t0, old, smem + L::e, smem + L::lo);
     }
     fence_async_smem();
     if (__syncthreads_or(failed)) {
@@ -461,65 +579,44 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     const int part = D == 128 ? 0 : r >> 6;               // (D = 64: lanes 64 .. hold the channels again)
     const float sg = RES ? sign[D + ch] : 0.f;
     const uint64_t sg2 = pack2(sg, sg), base = pack2(-8388608.f, -8388608.f);
-    uint32_t img[QS][16];
-#pragma unroll
+    if (L::v == L::e) __syncthreads();                    // K's image has left
+#pragma unroll 1
     for (int q = 0; q < QS; ++q) {
       const int k0 = hh * 64 + (D == 128 ? q : part) * 32;     // first key of these
       uint32_t d[32];
       if constexpr (RES != 0) {
-        if (cached) {
-          tc_ld32(tmem + 128 + lanes + k0, d);
-          tc_wait_ld();
-        }
+        tc_ld32(tmem + 128 + lanes + k0, d);
+        tc_wait_ld();
       }
       float v[32];
-      if (cached) {
-        const uint8_t* const words = sec0 + hh * SEC + SIDE + (D == 128 ? q : part) * 16 * D;
-        const float2* const azk = az + ((k0 >> 1) * NG + g) * 2;
+      const uint8_t* const words = sec0 + hh * SEC + SIDE + (D == 128 ? q : part) * 16 * D;
+      const float2* const azk = az + ((k0 >> 1) * NG + g) * 2;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          constexpr int UNITS = D / 4;
-          const int swz = UNITS == 32 ? 8 * (k & 3) : 8 * ((k >> 1) & 1);    // (16 pairs: k decides)
-          const uint32_t word = *reinterpret_cast<const uint32_t*>(words + k * D + (u4 ^ (swz * 4))) >> nib;
-          const float4 f = *reinterpret_cast<const float4*>(azk + k * NG * 2);
-          uint64_t y = pack2(f.y, f.w);
-          if constexpr (RES != 0)
-            y = fma2(pack2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1])), sg2, y);
-          const uint64_t code = pack2(__uint_as_float((word & 0xFu) | 0x4B000000u),
-                                      __uint_as_float((word & 0xF0000u) | 0x4B000000u));
-          unpack2(fma2(add2(code, base), pack2(f.x, f.z), y), v[2 * k], v[2 * k + 1]);
-        }
+      for (int k = 0; k < 16; ++k) {
+        constexpr int UNITS = D / 4;
+        const int swz = UNITS == 32 ? 8 * (k & 3) : 8 * ((k >> 1) & 1);    // (16 pairs: k decides)
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(words + k * D + (u4 ^ (swz * 4))) >> nib;
+        const float4 f = *reinterpret_cast<const float4*>(azk + k * NG * 2);
+        uint64_t y = pack2(f.y, f.w);
+        if constexpr (RES != 0)
+          y = fma2(pack2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1])), sg2, y);
+        const uint64_t code = pack2(__uint_as_float((word & 0xFu) | 0x4B000000u),
+                                    __uint_as_float((word & 0xF0000u) | 0x4B000000u));
+        unpack2(fma2(add2(code, base), pack2(f.x, f.z), y), v[2 * k], v[2 * k + 1]);
       }
-      if (k0 + 32 > old) {        // the chunk's own keys (all loads in flight, then the checks)
-        const uint16_t* const src = a.kv_new + a.kv_v + b * a.ks0 + h * a.ks_h + ch;
-        uint16_t y[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int t = t0 + k0 + k;
-          y[k] = t >= ctx && t < total ? src[int64_t(t - ctx) * a.ks1] : uint16_t(0);
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int t = t0 + k0 + k;
-          const float f = bf16_bits_to_float(y[k]);
-          const bool out_of_range = !(fabsf(f) <= kStateMax);
-          if (t >= ctx) v[k] = out_of_range ? 0.f : f;
-          if (out_of_range) first_out = min(first_out, t - ctx);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) img[q][k] = half2_sat(v[2 * k], v[2 * k + 1]);
-    }
-    if (L::v == L::e) __syncthreads();                    // K's image has left
-#pragma unroll
-    for (int q = 0; q < QS; ++q) {
       const int c0 = (D == 128 ? q : part) * 4;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(smem + L::v + hh * (D * 128) + panel_offset(ch, c0 + c)) =
-            make_uint4(img[q][4 * c], img[q][4 * c + 1], img[q][4 * c + 2], img[q][4 * c + 3]);
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = half2_sat(v[8 * c + 2 * k], v[8 * c + 2 * k + 1]);
+        *reinterpret_cast<uint4*>(smem + L::v + hh * (D * 128) + panel_offset(ch, c0 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    if (first_out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, first_out);
+    if (old < kKeys) {
+      __syncthreads();
+      mixed_rows<D, KLO, true>(a, b, h, n, ctx, t0, old, smem + L::v, nullptr);
+    }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();                                      // (sections, az and D are free)
@@ -528,7 +625,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
       bulk_s2g(a.val + at, smem_u32(smem + L::v), L::kImg);
       bulk_s2g_commit();
     }
-    if (cached) phase ^= 1;
+    phase ^= 1;
     loading = false;
   }
   if (tid == 0) {
@@ -1306,7 +1403,9 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
   cudaError_t e;
   using AS = AttnSmem<D>;
   using WS = WeightSmem<D>;
-  if ((e = cudaFuncSetAttribute(attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
+  if ((e = cudaFuncSetAttribute(chunk_image_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kKeys * D * 2 + 128)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(chunk_image_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kKeys * D * 2 + 128)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(attention_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WS::total)) != cudaSuccess ||
       (e = cudaMemsetAsync(w + l.first_bad, 0x7f, size_t(s.batch) * s.n_kv_heads * 4, stream)) != cudaSuccess)
@@ -1347,8 +1446,16 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.k = wb + l.k;
     r.klo = c.window ? wb + l.klo : nullptr;
     r.val = wb + l.val;
-    r.vec = reinterpret_cast<uintptr_t>(r.kv_new) % 16 == 0 && r.ks0 % 8 == 0 && r.ks1 % 8 == 0 && r.ks_h % 8 == 0;
-    if ((e = launch_rebuild_any<D>(r, int64_t(nb) * H * l.tiles, stream)) != cudaSuccess) return e;
+    r.vec = reinterpret_cast<uintptr_t>(r.kv_new) % 16 == 0 && r.ks0 % 8 == 0 && r.ks1 % 8 == 0 &&
+            r.kv_v % 8 == 0 && r.ks_h % 8 == 0;
+    r.old_tiles = (c.max_ctx + kKeys - 1) / kKeys;
+    if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, stream)) != cudaSuccess) return e;
+    const dim3 own(unsigned((c.n_new + kKeys - 1) / kKeys) * H, 1, nb);
+    if (c.window)
+      chunk_image_kernel<D, true><<<own, 256, 3 * kKeys * D * 2 + 128, stream>>>(r);
+    else
+      chunk_image_kernel<D, false><<<own, 256, 2 * kKeys * D * 2 + 128, stream>>>(r);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     AttnArgs a;
     a.v = v;
     a.q = c.q;

@@ -128,6 +128,9 @@ __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes
                "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {   // into L2
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void bulk_s2g_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_s2g_wait_read() {   // their sources may be written again
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
