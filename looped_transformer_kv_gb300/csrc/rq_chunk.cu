@@ -157,16 +157,23 @@ RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int 
 
 }  // namespace
 
-// Rows of a kv-head up to which the cache is streamed once per 8 rows; above, it is rebuilt once
-// (2 d fp16 written and read per token-head) and attended in tiles of 128 rows.
-constexpr int kFewRows = 32;
+// How a call runs.  Streaming the cache once per 8 rows wins up to 8 rows (and, because its scores
+// carry 21 bits, whenever up to 32 rows collect weights); up to 128 rows of up to 32 tokens are
+// attended in one pass with the codes converted in shared memory (the combine walks a row's chunk
+// tokens one by one); more share K and V rebuilt once.
+enum class ChunkPath { kStream, kFused, kTiles };
 
-bool few_rows(const rq_shape& s, int n_new) {
-  return int64_t(s.n_q_heads / s.n_kv_heads) * n_new <= kFewRows;
+ChunkPath chunk_path(const rq_shape& s, int n_new, int window) {
+  const int64_t rows = int64_t(s.n_q_heads / s.n_kv_heads) * n_new;
+  if (rows <= (window > 0 ? 32 : 8)) return ChunkPath::kStream;
+  if (window == 0 && rows <= 128 && n_new <= 32) return ChunkPath::kFused;
+  return ChunkPath::kTiles;
 }
 
 size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
-  if (!few_rows(s, n_new)) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window);
+  const ChunkPath path = chunk_path(s, n_new, window);
+  if (path == ChunkPath::kTiles) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window);
+  if (path == ChunkPath::kFused) return chunk_fused_workspace_bytes(s, loop, n_new, max_ctx);
   return rows_layout(s, loop, n_new, max_ctx, window).total;
 }
 
@@ -174,15 +181,22 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
                          const ChunkCall& c, void* ws, cudaStream_t stream) {
   char* const w = static_cast<char*>(ws);
   unsigned* err = reinterpret_cast<unsigned*>(w);
-  cudaError_t e = cudaMemsetAsync(w, 0, kWsHeaderBytes, stream);
-  if (e != cudaSuccess) return e;
-  if (!few_rows(s, c.n_new)) return launch_chunk_tc(s, cache, paging, c, ws, stream);
-  const RowsLayout l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window);
-  float* const scores = c.weights ? reinterpret_cast<float*>(w + l.scores) : nullptr;
-  e = launch_chunk_mma(s, cache, paging, c, l.plan, reinterpret_cast<float*>(w + l.part), scores,
-                       l.score_stride, err, stream);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   TailArgs a;
+  const ChunkPath path = chunk_path(s, c.n_new, c.window);
+  RowsLayout l = {};
+  if (path == ChunkPath::kFused) {
+    if ((e = launch_chunk_fused(s, cache, paging, c, ws, &a.part, &a.n_splits, stream)) != cudaSuccess) return e;
+  } else {
+    if ((e = cudaMemsetAsync(w, 0, kWsHeaderBytes, stream)) != cudaSuccess) return e;
+    if (path == ChunkPath::kTiles) return launch_chunk_tc(s, cache, paging, c, ws, stream);
+    l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window);
+    a.part = reinterpret_cast<const float*>(w + l.part);
+    a.n_splits = l.plan.n_splits;
+    e = launch_chunk_mma(s, cache, paging, c, l.plan, reinterpret_cast<float*>(w + l.part),
+                         c.weights ? reinterpret_cast<float*>(w + l.scores) : nullptr, l.score_stride, err, stream);
+    if (e != cudaSuccess) return e;
+  }
   a.q = c.q;
   a.kv_new = c.kv_new + c.loop * c.kv_strides[3];
   a.qs0 = c.q_strides[0];
@@ -195,10 +209,9 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   a.n_lens = c.n_lens;
   a.ctx_lens = c.ctx_lens;
   a.vsigns = c.loop < s.n_loops - 1 ? cache.rot_signs[1] : nullptr;
-  a.part = reinterpret_cast<const float*>(w + l.part);
   a.err = err;
   a.out = c.out;
-  a.scores = scores;
+  a.scores = c.weights ? reinterpret_cast<float*>(w + l.scores) : nullptr;
   a.lse = reinterpret_cast<float*>(w + l.lse);
   a.weights = c.weights;
   a.score_stride = l.score_stride;
@@ -206,7 +219,6 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   a.H = s.n_kv_heads;
   a.heads = s.n_q_heads / s.n_kv_heads;
   a.n_new = c.n_new;
-  a.n_splits = l.plan.n_splits;
   a.window = c.window;
   a.cap = s.capacity;
   a.max_ctx = c.max_ctx;

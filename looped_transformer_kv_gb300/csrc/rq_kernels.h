@@ -182,6 +182,13 @@ cudaError_t launch_chunk_mma(const rq_shape& s, const rq_cache& cache, const rq_
                              const ChunkCall& c, const SplitPlan& plan, float* part, float* scores,
                              int64_t score_stride, unsigned* err, cudaStream_t stream);
 
+// Up to 128 rows, no weights (rq_chunk_fused.cu): clears the header, then partial records as
+// launch_chunk_mma's; part and n_splits say where and how many.
+size_t chunk_fused_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx);
+cudaError_t launch_chunk_fused(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
+                               const ChunkCall& c, void* ws, const float** part, int* n_splits,
+                               cudaStream_t stream);
+
 // Many rows (rq_chunk_tc.cu): workspace (from its start: the header) and launch.  The header is
 // cleared by the caller.
 size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window);

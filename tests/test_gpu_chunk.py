@@ -14,7 +14,7 @@ if torch.cuda.is_available():
     from looped_transformer_kv_gb300 import rq
 
 # A score or output of the kernels differs from the 64-bit one by roundings only.  Calls with
-# many rows round each residual level, each rebuilt K and V element and each softmax weight once to
+# more than 8 rows round each residual level, each rebuilt K and V element and each softmax weight once to
 # fp16 (half a step: 2^-11); the sums are fp32.  The rotation keeps norms, so a token's residual
 # levels r add at most 2^-11 |q| |r| scale to a score's error and 2^-11 |r| to a V element's.  With
 # e = 2^-11 scale (sum|q k| + |q| |r|) (the largest error of a row's scores) every weight is within
@@ -214,7 +214,7 @@ def test_chunk_weight_beyond_the_capacity_is_dropped():
     c.check()
 
 
-@pytest.mark.parametrize("n_new", [4, 80])
+@pytest.mark.parametrize("n_new", [4, 20, 80])
 @pytest.mark.parametrize("kv", [0, 1])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e5])
 def test_token_out_of_range_reaches_its_own_and_later_rows_only(n_new, kv, value):
@@ -235,7 +235,7 @@ def test_token_out_of_range_reaches_its_own_and_later_rows_only(n_new, kv, value
     clean.check()
 
 
-@pytest.mark.parametrize("n_new", [2, 70])
+@pytest.mark.parametrize("n_new", [2, 20, 70])
 @pytest.mark.parametrize("fault", ["ctx", "negative", "n_len", "page"])
 def test_bad_device_values_set_the_error_word(n_new, fault):
     c = Case(2, 2, 2, 128, (2,), [70, 100], n_new, [n_new, 1], paged=fault == "page", max_ctx=100)
@@ -300,6 +300,30 @@ def test_nothing_new_enqueues_nothing():
     c = Case(1, 2, 2, 128, (2,), [70], 1)
     q = c.q[:, :0]
     rq.chunk_attention(c.shape, c.cache, q, 0, c.new[:, :0], c.ctx_lens, 70, c.out[:, :0], c.ws)
+
+
+MIDDLE = [
+    # B, Hq, H, d, bits, loop, ctx, n_new, n_lens
+    (1, 2, 2, 128, (2,), 0, [64], 9, None),
+    (2, 8, 2, 128, (2, 4), 0, [129, 1], 8, [8, 3]),
+    (2, 8, 2, 128, (4, 2), 0, [63, 0], 9, [9, 0]),
+    (1, 4, 1, 128, (2, 2), 2, [200], 32, None),
+    (2, 6, 2, 64, (2,), 0, [65, 640], 11, [1, 11]),
+    (1, 16, 1, 64, (4,), 0, [300], 3, None),
+    (1, 8, 2, 64, (), 0, [127], 7, None),
+    (1, 8, 1, 128, (2,), 0, [3000], 16, None),
+    (3, 128, 1, 128, (4,), 0, [100, 192, 7], 1, None),
+]
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("case", range(len(MIDDLE)))
+def test_middle_rows(case, paged):
+    B, Hq, H, d, bits, loop, ctx, n, lens = MIDDLE[case]
+    c = Case(B, Hq, H, d, bits, ctx, n, lens, seed=case, loop=loop, paged=paged, spread=case == 2)
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
 
 
 MANY = [
