@@ -8,13 +8,18 @@
 // so one product with K = 2 d gives the scores and one with N = 2 d both accumulators; the
 // combine kernel undoes the rotation once.  Tiles are the cache's 64-token records.
 //
-// Warps 0-3: softmax, a thread per row; 4-11: codes -> operand images; 12: products; 13: copies.
-// Tensor memory: queries (A operand) 128 columns, two score tiles of 64 (the softmax weights
-// overwrite them), accumulators 256.  Shared memory: 4 raw records, two K and two V images.
-// The queries are fp16 (q exactly, R q rounded once, both times the row's power of two), operands
-// and weights are rounded to fp16 once; sums are fp32.
-// Bound by the conversions (about 420 instructions per thread and 64-token tile of 8 warps), near
-// the tensor time of a 128-row tile (1,024 cycles) and the HBM time of a record (700 cycles).
+// Warps 0-3: softmax, a thread per row; 4-11: K codes -> operand images; 12-19: V's; 20: products;
+// 21: copies.  Tensor memory: queries (A operand) 128 columns, two score tiles of 64 (the softmax
+// weights overwrite them), accumulators 256.  Shared memory: 4 raw records, two K and two V images.
+//
+// A code pair sits 16 bits apart in its word, so an image's channels are permuted: inside 8
+// channels (4-bit codes) position 2 i + e holds channel i + 4 e, inside 16 (2-bit codes) channel
+// i + 8 e.  The queries are stored in the same order and the accumulators are put back in order
+// when they leave.
+// The queries are fp16 (q exactly, R q rounded once, both times the row's power of two); a level
+// s c + z is rounded once to fp16, a reference level once more by a; weights once; sums are fp32.
+// Bound by the conversions (about 3 instructions per code pair, 256 pairs per token), near the
+// tensor time of a 128-row tile (1,024 cycles) and the HBM time of a record (700 cycles).
 #include "rq_common.cuh"
 #include "rq_kernels.h"
 #include "rq_tc.cuh"
@@ -45,9 +50,16 @@ struct FusedArgs {
   float scale_log2;
 };
 
+// Position of channel c in an image of BITS-bit codes (the order above).
+template <int BITS>
+__host__ __device__ constexpr int image_position(int c) {
+  constexpr int N = 16 / BITS;            // codes of 16 bits
+  return c / (2 * N) * (2 * N) + 2 * (c % N) + c / N % 2;
+}
+
 // One warp per row: the row's fp16 queries and its scale.  Clears the call's error word first (it
 // runs before anything that sets it).
-template <int D, bool RES>
+template <int D, int RES>
 __global__ void __launch_bounds__(128) fused_rows_kernel(const __grid_constant__ FusedArgs a, int n_rows) {
   constexpr int P = D / 32;
   if (blockIdx.x == 0 && threadIdx.x < kWsHeaderBytes / 4) a.err[threadIdx.x] = 0u;
@@ -73,14 +85,14 @@ __global__ void __launch_bounds__(128) fused_rows_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     v[i] = v[i] * up * up2;
-    o[lane * P + i] = __float2half_rn(v[i]);
+    o[image_position<4>(lane * P + i)] = __float2half_rn(v[i]);
     if (RES) r[i] = v[i] * float(a.ksigns[int64_t(h) * D + lane * P + i]);
   }
   if (RES) {
     warp_fwht<P>(r, lane);
     const float inv_sqrt_d = (D == 128) ? 0.08838834764831845f : 0.125f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) o[D + lane * P + i] = __float2half_rn(r[i] * inv_sqrt_d);
+    for (int i = 0; i < P; ++i) o[D + image_position<RES ? RES : 4>(lane * P + i)] = __float2half_rn(r[i] * inv_sqrt_d);
   }
   if (lane == 0) a.qscale[wid] = ldexpf(a.scale_log2, -e);
 }
@@ -93,37 +105,37 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t panel) {
 }
 constexpr uint32_t kMnB = 1u << 16;   // instruction descriptor: B's N index is contiguous
 
-// 8 levels a (s c + z) of a word of eight 4-bit codes, as 16 bytes of fp16 (fp32 until the one
-// rounding): s01 = (s, s / 16), s23 = (s / 256, s / 4096), zz = (z, z), all times a.
-__device__ __forceinline__ uint4 levels4(uint32_t w, uint64_t s01, uint64_t s23, uint64_t zz) {
-  const uint64_t base = pack2(-8388608.f, -8388608.f);
-  uint32_t o[4];
+// The levels s c + z of a word's codes as 16-byte chunks of the image (4-bit codes: one, 2-bit: two).
+// A code at bit k < 8 of a 16-bit half is the exact fp16 c 2^k after subtracting 1024, its power of
+// two folded into the step (below 2^-14 a step loses bits: at most 2^-17 in a level).
+template <int BITS>
+struct Steps {
+  __half2 s[4 / (BITS / 2)], z;
+  __device__ __forceinline__ explicit Steps(uint32_t meta) {
+    const __half2 m = *reinterpret_cast<const __half2*>(&meta);
+    z = __high2half2(m);
+    s[0] = __low2half2(m);
+#pragma unroll
+    for (int i = 1; i < 8 / BITS; ++i) s[i] = __hmul2(s[i - 1], __float2half2_rn(BITS == 2 ? 0.25f : 0.0625f));
+  }
+};
+template <int BITS>
+__device__ __forceinline__ void levels(uint32_t w, const Steps<BITS>& st, uint32_t* o) {
+  constexpr uint32_t MASK = BITS == 2 ? 0x00030003u : 0x000F000Fu;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const uint32_t y = e ? w >> 16 : w;
+    const uint32_t x = e ? w >> 8 : w;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint64_t c = pack2(__uint_as_float((y & (0xFu << (8 * i))) | 0x4B000000u),
-                               __uint_as_float((y & (0xF0u << (8 * i))) | 0x4B000000u));
-      float x0, x1;
-      unpack2(fma2(add2(c, base), i ? s23 : s01, zz), x0, x1);
-      asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(o[2 * e + i]) : "f"(x1), "f"(x0));
+    for (int i = 0; i < 8 / BITS; ++i) {
+      const uint32_t c = code_pair_normal(x, MASK << (BITS * i));
+      const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&c), st.s[i], st.z);
+      o[e * (8 / BITS) + i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
-
-// Residual levels s c + z of 16 code bits' worth of a word half: pairs of neighbouring channels.
-template <int BITS>
-__device__ __forceinline__ void res_pairs(uint32_t x, __half2 s, __half2 z, uint32_t* o) {
-  constexpr uint32_t MASK = BITS == 2 ? 0x00030003u : 0x000F000Fu;
-  const uint32_t y = __byte_perm(x, x << (16 - BITS), 0x7610);   // halves: codes 0.., codes 1..
-#pragma unroll
-  for (int i = 0; i < 8 / BITS; ++i) {
-    const uint32_t c = code_pair_normal(y >> (2 * BITS * i), MASK);
-    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&c), s, z);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
+__device__ __forceinline__ uint32_t times(uint32_t x, __half2 a) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x), a);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <int D, int RES>
@@ -138,7 +150,7 @@ struct FusedSmem {
 };
 
 template <int D, int RES>
-__global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ FusedArgs a) {
+__global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ FusedArgs a) {
   using L = FusedSmem<D, RES>;
   constexpr int NG = L::NG, KD = 64 * L::NP;                 // scores' K, accumulators' N
   constexpr int SIDE = kTile * (D / 2 + 4 * NG);             // K (or V) part of the reference section
@@ -172,11 +184,11 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
   const int kt0 = int(int64_t(split) * n_tiles / a.n_splits), T = int(int64_t(split + 1) * n_tiles / a.n_splits) - kt0;
   const int active = (rows + 31) / 32;                       // softmax warps with rows
 
-  if (warp == 12) tc_alloc(smem_u32(tslot), 512);
+  if (warp == 20) tc_alloc(smem_u32(tslot), 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRawStages; ++i) {
       mbar_init(rawfull(i), 1);
-      mbar_init(rawfree(i), 8);
+      mbar_init(rawfree(i), 16);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull(i), 8);
@@ -197,8 +209,9 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
   const uint32_t tQ = tmem, tS = tmem + 128, tO = tmem + 256;
   bool failed = false;
 
-  if (warp == 13) {
-    if (lane == 0) {                                         // ---- copies
+  if (warp >= 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 21 && lane == 0) {                           // ---- copies
       int issued = 0;
       for (; issued < T; ++issued) {
         const int s = issued % kRawStages, use = issued / kRawStages;
@@ -224,9 +237,7 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
       for (int j = max(0, issued - kRawStages); j < issued; ++j)     // no copy outlives the CTA
         failed |= !mbar_wait_bounded(rawfull(j % kRawStages), (j / kRawStages) & 1, kFuWaitLimitNs);
     }
-    __syncwarp();
-  } else if (warp == 12) {
-    if (lane == 0 && T > 0) {                                // ---- products
+    if (warp == 20 && lane == 0 && T > 0) {                  // ---- products
       constexpr uint32_t ids = f16_idesc(kFuRows, kTile), ido = f16_idesc(kFuRows, KD) | kMnB;
       auto scores = [&](int s) {
         const uint32_t k = smem_u32(smem + L::k + s * L::kImg);
@@ -261,141 +272,157 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
       failed = !mbar_wait_bounded(done, 0, kFuWaitLimitNs) || !good;
     }
     __syncwarp();
-  } else if (warp >= 4) {                                    // ---- codes -> operand images
+  } else if (warp >= 12) {                                   // ---- V codes -> operand images
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // a thread per pair of tokens and 4 (2-bit residuals: 2) 16-bit units of both
+    const int tid = threadIdx.x - 384;
+    constexpr int CH = D / 16;                               // 16-byte chunks of a pair's reference words
+    const int p = tid / CH, u0 = (4 * (tid % CH)) ^ v_unit_swizzle(p, D / 4), g = u0 / 8;
+    const bool has_ref = D == 128 || tid < 32 * CH;
+    constexpr int W = RES == 2 ? 2 : 4, PR = RES ? D * RES / 16 / W : 1;   // residual words per thread, threads per pair
+    const int rp = tid / PR, rc = tid % PR, ru0 = (W * rc) ^ v_unit_swizzle(rp, RROW / 2), rg = RES ? ru0 * 16 / (RES ? RES : 1) / 32 : 0;
+    const bool has_res = RES && tid < 32 * PR;
+    for (int j = 0; j < T; ++j) {
+      const int st = j % kRawStages, s = j & 1;
+      const uint8_t* const rec = smem + L::raw + st * L::kRaw;
+      const uint8_t* const res = rec + L::kRef + RSIDE;      // V's part of the residual section
+      const uint8_t* const vr = rec + SIDE;
+      const int live = min(kTile, ctx - (kt0 + j) * kTile);  // cached tokens of the record
+      bool good = mbar_wait_bounded(rawfull(st), (j / kRawStages) & 1, kFuWaitLimitNs);
+      if (good && j >= 2) good = mbar_wait_bounded(vfree(s), ((j >> 1) - 1) & 1, kFuWaitLimitNs);
+      if (__any_sync(RQ_FULL_MASK, !good)) {
+        failed = true;
+        break;
+      }
+      uint8_t* const img = smem + L::v + s * L::kImg;
+      if (has_ref) {
+        const uint4 w = *reinterpret_cast<const uint4*>(vr + p * D + (tid % CH) * 16);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 2 * p + e;
+          const bool on = row < live;                        // (rows behind the context: zeros)
+          uint32_t al = 0x3C003C00u;
+          if (RES) al = *reinterpret_cast<const uint16_t*>(res + kTile * (RROW + 4 * NG) + row * 2) * 0x10001u;
+          al = on ? al : 0u;
+          const __half2 a2 = *reinterpret_cast<const __half2*>(&al);
+          const Steps<4> steps(on ? *reinterpret_cast<const uint32_t*>(vr + kTile * D / 2 + (row * NG + g) * 4) : 0u);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {                      // units u0 + 2 k, + 1: 8 channels
+            uint32_t o[4];
+            levels<4>(k ? __byte_perm(w.z, w.w, e ? 0x7632 : 0x5410) : __byte_perm(w.x, w.y, e ? 0x7632 : 0x5410), steps, o);
+            const int chunk = u0 / 2 + k;
+            *reinterpret_cast<uint4*>(img + (chunk / 8) * L::kPanel + panel_offset(row, chunk % 8)) =
+                RES ? make_uint4(times(o[0], a2), times(o[1], a2), times(o[2], a2), times(o[3], a2))
+                    : make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if constexpr (RES != 0) {
+        if (has_res) {
+          uint32_t w[W];
+          if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(res + rp * 2 * RROW + rc * 8);
+            w[0] = x.x, w[1] = x.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(res + rp * 2 * RROW + rc * 16);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 2 * rp + e;
+            const Steps<RES> steps(row < live ? *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + rg) * 4) : 0u);
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) {                // a token's word of two units
+              uint32_t o[16 / RES];
+              levels<RES>(__byte_perm(w[2 * k], w[2 * k + 1], e ? 0x7632 : 0x5410), steps, o);
+#pragma unroll
+              for (int q = 0; q < 4 / RES; ++q) {
+                const int chunk = (ru0 + 2 * k) * (16 / RES) / 8 + q;
+                *reinterpret_cast<uint4*>(img + (D / 64 + chunk / 8) * L::kPanel + panel_offset(row, chunk % 8)) =
+                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              }
+            }
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(vfull(s));
+        mbar_arrive(rawfree(st));
+      }
+    }
+  } else if (warp >= 4) {                                    // ---- K codes -> operand images
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // a thread per row and 32 codes of each section
     const int tid = threadIdx.x - 128;
+    const int row = D == 128 ? tid >> 2 : tid >> 1, part = D == 128 ? tid & 3 : tid & 1;
+    const bool has_ref = D == 128 || tid < 128;
+    constexpr int W = RES == 2 ? 2 : 4, PR = RES ? NG * RES / W : 1;       // residual words per thread, threads per row
+    const int rrow = tid / PR, rpart = tid % PR;
+    const bool has_res = RES && tid < kTile * PR;
     for (int j = 0; j < T; ++j) {
       const int st = j % kRawStages, s = j & 1;
       const uint8_t* const rec = smem + L::raw + st * L::kRaw;
       const uint8_t* const res = rec + L::kRef;
-      const int live = min(kTile, ctx - (kt0 + j) * kTile);  // cached tokens of the record
       bool good = mbar_wait_bounded(rawfull(st), (j / kRawStages) & 1, kFuWaitLimitNs);
       if (good && j >= 2) good = mbar_wait_bounded(kfree(s), ((j >> 1) - 1) & 1, kFuWaitLimitNs);
       if (__any_sync(RQ_FULL_MASK, !good)) {
         failed = true;
         break;
       }
-      {   // K: a thread per row and 32 codes of each section
-        uint8_t* const img = smem + L::k + s * L::kImg;
-        if (D == 128 || tid < 128) {
-          const int row = D == 128 ? tid >> 2 : tid >> 1, part = D == 128 ? tid & 3 : tid & 1;
-          float al = 1.f;
-          if (RES) al = __half2float(*reinterpret_cast<const __half*>(res + kTile * (RROW + 4 * NG) + row * 2));
-          // words `part` (d 64: 2 part, 2 part + 1) of every group
-          const uint4 w = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + part * 16);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      uint8_t* const img = smem + L::k + s * L::kImg;
+      if (has_ref) {
+        // words `part` (d 64: 2 part, 2 part + 1) of every group
+        const uint4 w = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + part * 16);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t al = 0x3C003C00u;
+        if (RES) al = *reinterpret_cast<const uint16_t*>(res + kTile * (RROW + 4 * NG) + row * 2) * 0x10001u;
+        const __half2 a2 = *reinterpret_cast<const __half2*>(&al);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int g = D == 128 ? i : i % 2, jj = D == 128 ? part : 2 * part + i / 2;
-            const float2 m = __half22float2(*reinterpret_cast<const __half2*>(rec + kTile * D / 2 + (row * NG + g) * 4));
-            const float sa = m.x * al, za = m.y * al;
-            *reinterpret_cast<uint4*>(img + (g / 2) * L::kPanel + panel_offset(row, (g % 2) * 4 + jj)) =
-                levels4(ws[i], pack2(sa, sa * 0x1p-4f), pack2(sa * 0x1p-8f, sa * 0x1p-12f), pack2(za, za));
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int g = D == 128 ? i : i % 2, jj = D == 128 ? part : 2 * part + i / 2;
+          const Steps<4> steps(*reinterpret_cast<const uint32_t*>(rec + kTile * D / 2 + (row * NG + g) * 4));
+          uint32_t o[4];
+          levels<4>(ws[i], steps, o);
+          *reinterpret_cast<uint4*>(img + (g / 2) * L::kPanel + panel_offset(row, (g % 2) * 4 + jj)) =
+              RES ? make_uint4(times(o[0], a2), times(o[1], a2), times(o[2], a2), times(o[3], a2))
+                  : make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if constexpr (RES != 0) {
-          constexpr int WPT = RES == 2 ? 2 : 4;              // words per thread: 32 codes
-          constexpr int ITEMS = kTile * NG * RES / WPT;      // threads with work
-          if (ITEMS >= 256 || tid < ITEMS) {
-            constexpr int PR = NG * RES / WPT;               // threads per row
-            const int row = tid / PR, part = tid % PR;
-            uint32_t ws[WPT];
-            if constexpr (WPT == 2) {
-              const uint2 w = *reinterpret_cast<const uint2*>(res + row * RROW + part * 8);
-              ws[0] = w.x, ws[1] = w.y;
-            } else {
-              const uint4 w = *reinterpret_cast<const uint4*>(res + row * RROW + part * 16);
-              ws[0] = w.x, ws[1] = w.y, ws[2] = w.z, ws[3] = w.w;
-            }
-#pragma unroll
-            for (int i = 0; i < WPT; ++i) {
-              const int word = part * WPT + i, g = word % NG, jj = word / NG;
-              const __half2 m = *reinterpret_cast<const __half2*>(res + kTile * RROW + (row * NG + g) * 4);
-              const __half2 sm = __low2half2(m), zm = __high2half2(m);
-              uint32_t o[16 / RES];
-              res_pairs<RES>(ws[i], sm, zm, o);
-              res_pairs<RES>(ws[i] >> 16, sm, zm, o + 8 / RES);
-#pragma unroll
-              for (int c = 0; c < 4 / RES; ++c)
-                *reinterpret_cast<uint4*>(img + (D / 64 + g / 2) * L::kPanel +
-                                          panel_offset(row, (g % 2) * 4 + jj * (4 / RES) + c)) =
-                    make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kfull(s));
       }
-      good = j < 2 || mbar_wait_bounded(vfree(s), ((j >> 1) - 1) & 1, kFuWaitLimitNs);
-      if (__any_sync(RQ_FULL_MASK, !good)) {
-        failed = true;
-        break;
+      if constexpr (RES != 0) {
+        if (has_res) {
+          uint32_t ws[W];
+          if constexpr (W == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(res + rrow * RROW + rpart * 8);
+            ws[0] = w.x, ws[1] = w.y;
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(res + rrow * RROW + rpart * 16);
+            ws[0] = w.x, ws[1] = w.y, ws[2] = w.z, ws[3] = w.w;
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const int word = rpart * W + i, g = word % NG, jj = word / NG;
+            const Steps<RES> steps(*reinterpret_cast<const uint32_t*>(res + kTile * RROW + (rrow * NG + g) * 4));
+            uint32_t o[16 / RES];
+            levels<RES>(ws[i], steps, o);
+#pragma unroll
+            for (int c = 0; c < 4 / RES; ++c)
+              *reinterpret_cast<uint4*>(img + (D / 64 + g / 2) * L::kPanel +
+                                        panel_offset(rrow, (g % 2) * 4 + jj * (4 / RES) + c)) =
+                  make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+        }
       }
-      {   // V: a thread per pair of tokens and 4 (2-bit residuals: 2) 16-bit units of both
-        uint8_t* const img = smem + L::v + s * L::kImg;
-        const uint8_t* const vr = rec + SIDE;
-        constexpr int CH = D / 16;                           // 16-byte chunks of a pair's words
-        if (D == 128 || tid < 32 * CH) {
-          const int p = tid / CH, c = tid % CH, u0 = (4 * c) ^ v_unit_swizzle(p, D / 4), g = u0 / 8;
-          const uint4 w = *reinterpret_cast<const uint4*>(vr + p * D + c * 16);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 2 * p + e;
-            const bool on = row < live;
-            float al = 1.f;
-            if (RES) al = __half2float(*reinterpret_cast<const __half*>(res + RSIDE + kTile * (RROW + 4 * NG) + row * 2));
-            const float2 m = __half22float2(*reinterpret_cast<const __half2*>(vr + kTile * D / 2 + (row * NG + g) * 4));
-            const float sa = on ? m.x * al : 0.f, za = on ? m.y * al : 0.f;
-            const uint64_t s01 = pack2(sa, sa * 0x1p-4f), s23 = pack2(sa * 0x1p-8f, sa * 0x1p-12f), zz = pack2(za, za);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {                    // units u0 + 2 k, + 1: 8 channels
-              const uint32_t word = k ? __byte_perm(w.z, w.w, e ? 0x7632 : 0x5410) : __byte_perm(w.x, w.y, e ? 0x7632 : 0x5410);
-              const int chunk = u0 / 2 + k;
-              *reinterpret_cast<uint4*>(img + (chunk / 8) * L::kPanel + panel_offset(row, chunk % 8)) = levels4(word, s01, s23, zz);
-            }
-          }
-        }
-        if constexpr (RES != 0) {
-          constexpr int W = RES == 2 ? 2 : 4;                // words per thread
-          constexpr int PR = D * RES / 16 / W;               // threads per pair
-          if (32 * PR >= 256 || tid < 32 * PR) {
-            const int p = tid / PR, c = tid % PR, u0 = (W * c) ^ v_unit_swizzle(p, RROW / 2), g = u0 * (16 / RES) / 32;
-            uint32_t w[W];
-            if constexpr (W == 2) {
-              const uint2 x = *reinterpret_cast<const uint2*>(res + RSIDE + p * 2 * RROW + c * 8);
-              w[0] = x.x, w[1] = x.y;
-            } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(res + RSIDE + p * 2 * RROW + c * 16);
-              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = 2 * p + e;
-              uint32_t mw = *reinterpret_cast<const uint32_t*>(res + RSIDE + kTile * RROW + (row * NG + g) * 4);
-              if (row >= live) mw = 0u;
-              const __half2 m = *reinterpret_cast<const __half2*>(&mw);
-              const __half2 sm = __low2half2(m), zm = __high2half2(m);
-              uint32_t o[W * 8 / RES];
-#pragma unroll
-              for (int i = 0; i < W; ++i) res_pairs<RES>(e ? w[i] >> 16 : w[i], sm, zm, o + i * (8 / RES));
-#pragma unroll
-              for (int k = 0; k < W * 2 / RES; ++k) {
-                const int chunk = u0 * (16 / RES) / 8 + k;
-                *reinterpret_cast<uint4*>(img + (D / 64 + chunk / 8) * L::kPanel + panel_offset(row, chunk % 8)) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-              }
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(vfull(s));
-          mbar_arrive(rawfree(st));
-        }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(kfull(s));
+        mbar_arrive(rawfree(st));
       }
     }
   } else {                                                   // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     const int row = threadIdx.x;
     const uint32_t lanes = uint32_t(warp) << 21;
     float m = -INFINITY, l = 0.f, c = 1.f;
@@ -494,8 +521,7 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
       tc_fence_after();
       float* const part = a.part + ((unit * a.rows + min(row, rows - 1)) * a.n_splits + split) * (4 + 2 * D);
       if (valid) *reinterpret_cast<float2*>(part) = make_float2(m, l);
-#pragma unroll 1
-      for (int x = 0; x < KD / 32; ++x) {
+      auto store = [&](int x, auto order) {                  // 32 columns, channels in order
         uint32_t w[32];
         if (T > 0) {
           tc_ld32(tO + lanes + 32 * x, w);
@@ -506,16 +532,23 @@ __global__ void __launch_bounds__(448, 1) fused_kernel(const __grid_constant__ F
         }
         if (valid) {
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            *reinterpret_cast<uint4*>(part + 4 + 32 * x + 4 * y) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+          for (int y = 0; y < 32; y += 4)
+            *reinterpret_cast<uint4*>(part + 4 + 32 * x + y) =
+                make_uint4(w[order.at(y)], w[order.at(y + 1)], w[order.at(y + 2)], w[order.at(y + 3)]);
         }
-      }
+      };
+      struct Four { __device__ static constexpr int at(int c) { return image_position<4>(c); } };
+      struct Residual { __device__ static constexpr int at(int c) { return image_position<RES ? RES : 4>(c); } };
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) store(x, Four());
+#pragma unroll 1
+      for (int x = D / 32; x < KD / 32; ++x) store(x, Residual());
       tc_fence_before();
     }
   }
   if (__syncthreads_or(failed) && threadIdx.x == 0) atomicOr(a.err, 1u);
   tc_fence_after();
-  if (warp == 12) tc_free(tmem, 512);
+  if (warp == 20) tc_free(tmem, 512);
 }
 
 size_t round1k(size_t n) { return (n + 1023) / 1024 * 1024; }
@@ -562,9 +595,9 @@ cudaError_t launch_fused(const FusedArgs& a, int batch, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(fused_kernel<D, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   if (e != cudaSuccess) return e;
   const int64_t n_rows = int64_t(batch) * a.H * a.rows;
-  fused_rows_kernel<D, RES != 0><<<unsigned((n_rows + 3) / 4), 128, 0, stream>>>(a, int(n_rows));
+  fused_rows_kernel<D, RES><<<unsigned((n_rows + 3) / 4), 128, 0, stream>>>(a, int(n_rows));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  fused_kernel<D, RES><<<dim3(unsigned(a.n_splits), unsigned(a.H), unsigned(batch)), 448, L::total, stream>>>(a);
+  fused_kernel<D, RES><<<dim3(unsigned(a.n_splits), unsigned(a.H), unsigned(batch)), 768, L::total, stream>>>(a);
   return cudaGetLastError();
 }
 

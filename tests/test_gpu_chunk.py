@@ -13,14 +13,15 @@ pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
     from looped_transformer_kv_gb300 import rq
 
-# A score or output of the kernels differs from the 64-bit one by roundings only.  Calls with
-# more than 8 rows round each residual level, each rebuilt K and V element and each softmax weight once to
-# fp16 (half a step: 2^-11); the sums are fp32.  The rotation keeps norms, so a token's residual
-# levels r add at most 2^-11 |q| |r| scale to a score's error and 2^-11 |r| to a V element's.  With
-# e = 2^-11 scale (sum|q k| + |q| |r|) (the largest error of a row's scores) every weight is within
-# a factor exp(2 e) of its own, so an output is off by at most sum p|v| (exp(2 e) - 1 + 2 * 2^-11)
-# + 2^-11 sum p |r_v|, and by half a bf16 step (2^-8 relative) of its result.  fp32 steps in sums of
-# up to a few thousand terms stay below 1e-5 of sum p|v|.
+# A score or output of the kernels differs from the 64-bit one by roundings only.  With more than 8
+# rows the operands are fp16, one rounding half a step, 2^-11: a residual level r once, a rebuilt
+# element or reference level at most twice, a rotated query once, a softmax weight once; the sums are
+# fp32.  The rotation keeps norms and a ref = K - R^T r, so a score is off by at most
+#   e = 2^-11 scale (2 sum|q k| + 4 |q| |r|)
+# and a V element by 2^-11 (2 |v| + 3 |r|).  A weight is then within a factor exp(2 e) of its own and
+# an output off by at most sum p|v| (exp(2 e) - 1 + 3 * 2^-11) + 3 * 2^-11 sum p |r_v|, and by half a
+# bf16 step (2^-8 relative) of its result.  fp32 steps in sums of up to a few thousand terms stay
+# below 1e-5 of sum p|v|.
 HALF16, HALFB = 2.0 ** -11, 2.0 ** -8
 # Collected weights come from scores in which each product carries at least 21 bits (two fp16
 # parts) and fp32 sums of d terms: e = (2^-21 + d 2^-24) sum|q k| scale; twice that in a weight,
@@ -132,8 +133,8 @@ class Case:
             rk, rv = (np.concatenate([R.residual_norms(rec, ctx, d, self.bits, self.loop, kv), np.zeros(m)])
                       for kv in (0, 1))
             qn = np.linalg.norm(self.q_host[b, :m, h * G:(h + 1) * G].double().numpy(), axis=-1)
-            e = HALF16 * (mag + qn * rk.max() * d ** -0.5)[..., None]
-            tol = pv * (np.expm1(2 * e) + 2 * HALF16 + 1e-5) + HALF16 * (p @ rv)[..., None]
+            e = HALF16 * (2 * mag + 4 * qn * rk.max() * d ** -0.5)[..., None]
+            tol = pv * (np.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[..., None]
             tol += HALFB * np.abs(ref) * 1.01 + 1e-30
             worst = (np.abs(got - ref) / tol).max()
             assert worst <= 1, (b, h, worst)
