@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
 
   if (warp >= 20) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 21 && lane == 0) {                           // ---- copies
+    const bool leader = elect_one();
+    if (warp == 21 && leader) {                             // ---- copies
       int issued = 0;
       for (; issued < T; ++issued) {
         const int s = issued % kRawStages, use = issued / kRawStages;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
       for (int j = max(0, issued - kRawStages); j < issued; ++j)     // no copy outlives the CTA
         failed |= !mbar_wait_bounded(rawfull(j % kRawStages), (j / kRawStages) & 1, kFuWaitLimitNs);
     }
-    if (warp == 20 && lane == 0 && T > 0) {                  // ---- products
+    if (warp == 20 && leader && T > 0) {                     // ---- products
       constexpr uint32_t ids = f16_idesc(kFuRows, kTile), ido = f16_idesc(kFuRows, KD) | kMnB;
       auto scores = [&](int s) {
         const uint32_t k = smem_u32(smem + L::k + s * L::kImg);

@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = RES ? *tslot : 0u;
+  const bool leader = warp == 0 && elect_one();            // issues the products
   const float inv_sqrt_d = (D == 128) ? 0.08838834764831845f : 0.125f;
   int phase = 0;
   bool failed = false, loading = false;
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     if constexpr (RES != 0) {
       constexpr uint32_t idk = f16_idesc(kKeys, D), idv = f16_idesc(128, kKeys);
       const uint32_t hs = smem_u32(smem + L::h), es = smem_u32(smem + L::e);
-      if (tid == 0) {
+      if (leader) {
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < (KLO ? 2 : 1); ++part)
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
       fence_async_smem();
       tc_fence_before();
       __syncthreads();
-      if (tid == 0) {
+      if (leader) {
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
@@ -791,7 +792,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8 && lane == 0 && T > 0) {                           // ---- copies
+    const bool leader = elect_one();
+    if (warp == 8 && leader && T > 0) {                             // ---- copies
       const uint8_t* k = a.k + (unit * a.v.tiles + kt0) * L::kTileBytes;
       const uint8_t* v = (LSE ? a.klo : a.val) + (unit * a.v.tiles + kt0) * L::kTileBytes;
       int issued = 0;
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         failed |= !mbar_wait_bounded(kfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
         failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
       }
-    } else if (warp == 9 && lane == 0 && T > 0) {                    // ---- products
+    } else if (warp == 9 && leader && T > 0) {                      // ---- products
       constexpr uint32_t ids = f16_idesc(kRows, kKeys), ido = f16_idesc(kRows, D);
       auto scores = [&](int i, int s) {
         const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + s * L::kTileBytes);
@@ -1235,7 +1237,7 @@ __global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t id = f16_idesc(kKeys, kRows);
       bool good = mbar_wait_bounded(kfull, 0, kTcWaitLimitNs);
       for (int j = 0; j < T && good; ++j) {
