@@ -659,9 +659,10 @@ struct AttnArgs {
 template <int D>
 struct AttnSmem {
   static constexpr int kTileBytes = kKeys * D * 2;      // one K, V^T or Q tile
-  static constexpr int q = 0, k = 2 * kTileBytes, v = k + 2 * kTileBytes, exps = v + 2 * kTileBytes;
+  static constexpr int q = 0, k = 2 * kTileBytes, v = k + 3 * kTileBytes, exps = v + 2 * kTileBytes;
   static constexpr int bars = exps + 2 * kRows * 4;
   static constexpr int total = bars + 256 + 1024;       // + alignment of the base
+  static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
 
 // 32 rows of queries (this warp's rows of a tile) -> fp16 in the swizzled tile image, each row
@@ -741,16 +742,16 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
   using L = AttnSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  // barriers: K full/free [2], V full/free [2], S ready [2], P ready [2], Q ready, done
+  // barriers: K full [3], V full [2], S ready [row tile][key tile % 2], P ready [2], Q ready, done.
+  // S of a key tile being ready also means that the values of the tile before are done, so the
+  // copies wait for it and need no barriers of their own (each commit stalls the products).
   const uint32_t bar0 = smem_u32(bars);
   auto kfull = [&](int s) { return bar0 + 8 * s; };
-  auto kfree = [&](int s) { return bar0 + 8 * (2 + s); };
-  auto vfull = [&](int s) { return bar0 + 8 * (4 + s); };
-  auto vfree = [&](int s) { return bar0 + 8 * (6 + s); };
-  auto sready = [&](int i) { return bar0 + 8 * (8 + i); };
-  auto pready = [&](int i) { return bar0 + 8 * (10 + i); };
-  const uint32_t qready = bar0 + 8 * 12, done = bar0 + 8 * 13;
-  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 14);
+  auto vfull = [&](int s) { return bar0 + 8 * (3 + s); };
+  auto sready = [&](int i, int j) { return bar0 + 8 * (5 + 2 * i + (j & 1)); };
+  auto pready = [&](int i) { return bar0 + 8 * (9 + i); };
+  const uint32_t qready = bar0 + 8 * 11, done = bar0 + 8 * 12;
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 13);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
@@ -775,11 +776,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 
   if (warp == 9) tc_alloc(smem_u32(tslot), 512);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(bar0 + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(sready(i), 1);
-      mbar_init(pready(i), kRows);
-    }
+    for (int i = 0; i < 9; ++i) mbar_init(bar0 + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(pready(i), kRows);
     mbar_init(qready, 2 * kRows);
     mbar_init(done, 1);
     fence_mbar_init();
@@ -796,40 +794,45 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
     if (warp == 8 && leader && T > 0) {                             // ---- copies
       const uint8_t* k = a.k + (unit * a.v.tiles + kt0) * L::kTileBytes;
       const uint8_t* v = (LSE ? a.klo : a.val) + (unit * a.v.tiles + kt0) * L::kTileBytes;
-      int issued = 0;
-      for (int j = 0; j < T; ++j, ++issued) {
-        const int s = j & 1;
-        if (j >= 2 && !mbar_wait_bounded(kfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs)) break;
-        mbar_arrive_expect_tx(kfull(s), L::kTileBytes);
-        bulk_g2s(smem_u32(smem + L::k + s * L::kTileBytes), k + int64_t(j) * L::kTileBytes, L::kTileBytes, kfull(s));
-        if (j >= 2 && !mbar_wait_bounded(vfree(s), ((j >> 1) - 1) & 1, kTcWaitLimitNs)) {
-          mbar_wait_bounded(kfull(s), (j >> 1) & 1, kTcWaitLimitNs);
-          break;
-        }
-        mbar_arrive_expect_tx(vfull(s), L::kTileBytes);
-        bulk_g2s(smem_u32(smem + L::v + s * L::kTileBytes), v + int64_t(j) * L::kTileBytes, L::kTileBytes, vfull(s));
+      auto load_k = [&](int j) {
+        mbar_arrive_expect_tx(kfull(j % 3), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::k + (j % 3) * L::kTileBytes), k + int64_t(j) * L::kTileBytes, L::kTileBytes, kfull(j % 3));
+      };
+      auto load_v = [&](int j) {
+        mbar_arrive_expect_tx(vfull(j & 1), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::v + (j & 1) * L::kTileBytes), v + int64_t(j) * L::kTileBytes, L::kTileBytes, vfull(j & 1));
+      };
+      const int last_tile = two ? 1 : 0;
+      int nk = 0, nv = 0;                                            // copies issued
+      for (; nk < min(T, 3); ++nk) {
+        load_k(nk);
+        if (nk < 2) load_v(nv++);
       }
-      failed = issued < T;
-      for (int j = max(0, issued - 2); j < issued; ++j) {            // no copy outlives the CTA
-        failed |= !mbar_wait_bounded(kfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
-        failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
+      for (int j = 2; j < T; ++j) {
+        // scores of tile j - 1 done (so of j - 2, and its values): K j + 1 and V j have room
+        if (!mbar_wait_bounded(sready(last_tile, j - 1), ((j - 1) >> 1) & 1, kTcWaitLimitNs)) break;
+        load_v(nv++);
+        if (j + 1 < T) load_k(nk++);
       }
+      failed = nv < T;
+      for (int j = max(0, nk - 3); j < nk; ++j) failed |= !mbar_wait_bounded(kfull(j % 3), (j / 3) & 1, kTcWaitLimitNs);
+      for (int j = max(0, nv - 2); j < nv; ++j) failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
     } else if (warp == 9 && leader && T > 0) {                      // ---- products
       constexpr uint32_t ids = f16_idesc(kRows, kKeys), ido = f16_idesc(kRows, D);
-      auto scores = [&](int i, int s) {
-        const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + s * L::kTileBytes);
+      auto scores = [&](int i, int j) {
+        const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + (j % 3) * L::kTileBytes);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
           tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
                  panel_desc(k + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, x > 0);
         if (LSE) {
-          const uint32_t k2 = smem_u32(smem + L::v + s * L::kTileBytes);
+          const uint32_t k2 = smem_u32(smem + L::v + (j & 1) * L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
             tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
                    panel_desc(k2 + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, true);
         }
-        tc_commit(sready(i));
+        tc_commit(sready(i, j));
       };
       auto values = [&](int i, int s, bool add) {
         const uint32_t v = smem_u32(smem + L::v + s * L::kTileBytes);
@@ -842,31 +845,20 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
       bool good = mbar_wait_bounded(qready, 0, kTcWaitLimitNs) && mbar_wait_bounded(kfull(0), 0, kTcWaitLimitNs) &&
                   (!LSE || mbar_wait_bounded(vfull(0), 0, kTcWaitLimitNs));
       tc_fence_after();
-      if (good) {
+      if (good)
         for (int i = 0; i < I; ++i) scores(i, 0);
-        tc_commit(kfree(0));
-        if (LSE) tc_commit(vfree(0));
-      }
       for (int j = 0; j < T && good; ++j) {
         const int s = j & 1;
         if (!LSE) good = mbar_wait_bounded(vfull(s), (j >> 1) & 1, kTcWaitLimitNs);
+        if (good && j + 1 < T)
+          good = mbar_wait_bounded(kfull((j + 1) % 3), ((j + 1) / 3) & 1, kTcWaitLimitNs) &&
+                 (!LSE || mbar_wait_bounded(vfull(s ^ 1), ((j + 1) >> 1) & 1, kTcWaitLimitNs));
         for (int i = 0; i < I && good; ++i) {
           good = mbar_wait_bounded(pready(i), j & 1, kTcWaitLimitNs);
           if (!good) break;
           tc_fence_after();
           if (!LSE) values(i, s, j > 0);
-          if (j + 1 < T) {
-            const int s1 = s ^ 1;
-            if (i == 0)
-              good = mbar_wait_bounded(kfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs) &&
-                     (!LSE || mbar_wait_bounded(vfull(s1), ((j + 1) >> 1) & 1, kTcWaitLimitNs));
-            if (good) scores(i, s1);
-          }
-        }
-        if (good && !LSE) tc_commit(vfree(s));
-        if (good && j + 1 < T) {
-          tc_commit(kfree(s ^ 1));
-          if (LSE) tc_commit(vfree(s ^ 1));
+          if (j + 1 < T) scores(i, j + 1);
         }
       }
       tc_commit(done);
@@ -899,7 +891,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
       const int clear = ctx + min((r0 + i * kRows + first) / a.v.heads, n - 1);   // every row of the tile sees these
       if (i == 0 || two) {
         for (int jt = 0; jt < T; ++jt) {
-          if (!mbar_wait_bounded(sready(i), jt & 1, kTcWaitLimitNs)) {
+          if (!mbar_wait_bounded(sready(i, jt), (jt >> 1) & 1, kTcWaitLimitNs)) {
             failed = true;
             break;
           }
