@@ -29,6 +29,17 @@ struct TailArgs {
   float scale_log2;
 };
 
+template <int P>
+__device__ __forceinline__ void load_floats(const float* p, float (&x)[P]) {
+  if constexpr (P == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  }
+}
+
 // One warp per row: merge the split partials, then the chunk's tokens 0..j one by one (online
 // softmax), undo the rotation, store bf16.  Rows whose weights are asked for also store the
 // chunk tokens' scores and their log2-sum-exp.  Latency-bound: j + 1 dependent dot products.
@@ -57,17 +68,33 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
 #pragma unroll
   for (int i = 0; i < P; ++i) ar[i] = ae[i] = 0.f;
   if (!bad) {
+    // splits in groups of 32: a lane loads one split's (m, l), the warp their accumulators
     const float* part = a.part + wid * a.n_splits * rec;
-    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, part[int64_t(s) * rec]);
-    for (int s = 0; s < a.n_splits; ++s) {
-      const float* ps = part + int64_t(s) * rec;
-      if (ps[0] == -INFINITY) continue;
-      const float f = exp2f(ps[0] - M);
-      ell = fmaf(f, ps[1], ell);
+    for (int s0 = 0; s0 < a.n_splits; s0 += 32) {
+      const int ns = min(32, a.n_splits - s0);
+      const float2 ml = lane < ns ? *reinterpret_cast<const float2*>(part + int64_t(s0 + lane) * rec)
+                                  : make_float2(-INFINITY, 0.f);
+      const float m = fmaxf(M, warp_max(ml.x)), f0 = M == -INFINITY ? 0.f : exp2f(M - m);
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      ell = fmaf(ell, f0, warp_sum(f == 0.f ? 0.f : f * ml.y));
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        ar[i] = fmaf(f, ps[4 + lane * P + i], ar[i]);
-        ae[i] = fmaf(f, ps[4 + D + lane * P + i], ae[i]);
+        ar[i] *= f0;
+        ae[i] *= f0;
+      }
+      M = m;
+#pragma unroll 4
+      for (int s = 0; s < ns; ++s) {
+        const float fs = __shfl_sync(RQ_FULL_MASK, f, s);
+        float x[P], y[P];
+        const float* ps = part + int64_t(s0 + s) * rec + 4 + lane * P;
+        load_floats<P>(ps, x);
+        load_floats<P>(ps + D, y);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {   // (an empty split's accumulators may hold anything)
+          ar[i] = fs == 0.f ? ar[i] : fmaf(fs, x[i], ar[i]);
+          ae[i] = fs == 0.f ? ae[i] : fmaf(fs, y[i], ae[i]);
+        }
       }
     }
     float qv[P];
@@ -112,20 +139,49 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
   if (voted && lane == 0) a.lse[wrow] = bad ? nan : M + log2f(ell);
 }
 
-// One thread per slot: the weights of the window's rows, in row order.
+// Four slots per thread: the weights of the window's rows, in row order.  Bound by HBM: a score per
+// slot and row read, a weight read and written.
 __global__ void __launch_bounds__(128) chunk_weights_kernel(const __grid_constant__ TailArgs a) {
-  const int t = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int t0 = (blockIdx.x * 128 + threadIdx.x) * 4, h = blockIdx.y, b = blockIdx.z;
   const int n_len = a.n_lens ? a.n_lens[b] : a.n_new, ctx = a.ctx_lens[b];
   if (n_len < 0 || n_len > a.n_new || ctx < 0 || ctx > a.max_ctx) return;   // (flagged)
-  if (t >= ctx + n_len || t >= a.cap) return;
+  const int end = min(ctx + n_len, a.cap);
+  if (t0 >= end) return;
   const int first = max(0, n_len - a.window);
   const int64_t base = (int64_t(b) * a.H + h) * a.window * a.heads;
   const int n = (n_len - first) * a.heads;
-  const int from = t < ctx ? 0 : max(0, t - ctx - first) * a.heads;   // chunk token t - ctx: rows j >= it
-  float w = 0.f;
-  for (int r = from; r < n; ++r)
-    w += exp2f(a.scores[(base + r) * a.score_stride + t] - a.lse[base + r]);
-  a.weights[(int64_t(b) * a.H + h) * a.cap + t] += w;
+  const float* const scores = a.scores + base * a.score_stride + t0;
+  const float* const lse = a.lse + base;
+  float* const out = a.weights + (int64_t(b) * a.H + h) * a.cap + t0;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  if (t0 + 4 <= ctx) {                // cached slots: every row
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) {
+      const float4 s = *reinterpret_cast<const float4*>(scores + r * a.score_stride);
+      const float z = lse[r];
+      w[0] += exp2f(s.x - z);
+      w[1] += exp2f(s.y - z);
+      w[2] += exp2f(s.z - z);
+      w[3] += exp2f(s.w - z);
+    }
+  } else {
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + i;
+      if (t >= end) break;
+      const int from = t < ctx ? 0 : max(0, t - ctx - first) * a.heads;   // chunk token t - ctx: rows j >= it
+      for (int r = from; r < n; ++r) w[i] += exp2f(scores[r * a.score_stride + i] - lse[r]);
+    }
+  }
+  if (t0 + 4 <= end && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+    float4 v = *reinterpret_cast<const float4*>(out);
+    v.x += w[0];
+    v.y += w[1];
+    v.z += w[2];
+    v.w += w[3];
+    *reinterpret_cast<float4*>(out) = v;
+  } else {
+    for (int i = 0; i < 4 && t0 + i < end; ++i) out[i] += w[i];
+  }
 }
 
 // Workspace of a call with few rows: header, partial records, then (with weights) the scores and
@@ -230,7 +286,7 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   else
     chunk_combine_kernel<64><<<unsigned((warps + 3) / 4), 128, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || !c.weights) return e;
-  const dim3 grid((c.max_ctx + c.n_new + 127) / 128, s.n_kv_heads, s.batch);
+  const dim3 grid((c.max_ctx + c.n_new + 511) / 512, s.n_kv_heads, s.batch);
   chunk_weights_kernel<<<grid, 128, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -1153,7 +1153,7 @@ __global__ void __launch_bounds__(128) window_rows_kernel(const __grid_constant_
 template <int D>
 struct WeightSmem {
   static constexpr int kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 1;                       // (two CTAs per SM)
   static constexpr int kStage = kTileBytes + kRows * 8;   // queries, scales
   static constexpr int k = 0, q = 2 * kTileBytes, bars = q + kStages * kStage;
   static constexpr int total = bars + 256 + 1024;
@@ -1163,7 +1163,7 @@ struct WeightSmem {
 // thread's registers, in row order.  Row tiles alternate between two tensor-memory buffers and the
 // two softmax warpgroups.  Bound by the exponentials.
 template <int D>
-__global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ uint8_t raw[];
   using L = WeightSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -1190,7 +1190,7 @@ __global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__
   const int T = to - from;
   if (warp == 9) tc_alloc(smem_u32(tslot), 256);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < L::kStages; ++i) {
       mbar_init(qfull(i), 1);
       mbar_init(qfree(i), kRows + 1);                    // the products, and the scales' readers
     }
@@ -1216,16 +1216,16 @@ __global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__
       bulk_g2s(smem_u32(smem + L::k + L::kTileBytes), a.klo + at, L::kTileBytes, kfull);
       int issued = 0;
       for (int j = 0; j < T; ++j, ++issued) {
-        const int s = j % 3;
-        if (j >= 3 && !mbar_wait_bounded(qfree(s), (j / 3 - 1) & 1, kTcWaitLimitNs)) break;
+        const int s = j % L::kStages;
+        if (j >= L::kStages && !mbar_wait_bounded(qfree(s), (j / L::kStages - 1) & 1, kTcWaitLimitNs)) break;
         const uint32_t dst = smem_u32(smem + L::q + s * L::kStage);
         mbar_arrive_expect_tx(qfull(s), L::kStage);
         bulk_g2s(dst, a.qimg + (unit * a.q_tiles + from + j) * L::kTileBytes, L::kTileBytes, qfull(s));
         bulk_g2s(dst + L::kTileBytes, a.scale + (unit * a.q_tiles + from + j) * kRows, kRows * 8, qfull(s));
       }
       failed = issued < T || !mbar_wait_bounded(kfull, 0, kTcWaitLimitNs);
-      for (int j = max(0, issued - 3); j < issued; ++j)
-        failed |= !mbar_wait_bounded(qfull(j % 3), (j / 3) & 1, kTcWaitLimitNs);
+      for (int j = max(0, issued - L::kStages); j < issued; ++j)
+        failed |= !mbar_wait_bounded(qfull(j % L::kStages), (j / L::kStages) & 1, kTcWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -1233,8 +1233,8 @@ __global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__
       constexpr uint32_t id = f16_idesc(kKeys, kRows);
       bool good = mbar_wait_bounded(kfull, 0, kTcWaitLimitNs);
       for (int j = 0; j < T && good; ++j) {
-        const int s = j % 3, i = j & 1;
-        good = mbar_wait_bounded(qfull(s), (j / 3) & 1, kTcWaitLimitNs) &&
+        const int s = j % L::kStages, i = j & 1;
+        good = mbar_wait_bounded(qfull(s), (j / L::kStages) & 1, kTcWaitLimitNs) &&
                (j < 2 || mbar_wait_bounded(sfree(i), ((j >> 1) - 1) & 1, kTcWaitLimitNs));
         if (!good) break;
         tc_fence_after();
@@ -1260,9 +1260,9 @@ __global__ void __launch_bounds__(320, 1) weights_kernel(const __grid_constant__
     // rows before this one do not see the key
     const int row_min = max(0, key - ctx - j0) * a.v.heads;
     for (int j = i; j < T; j += 2) {
-      const int s = j % 3;
+      const int s = j % L::kStages;
       if (!mbar_wait_bounded(sready(i), (j >> 1) & 1, kTcWaitLimitNs) ||
-          !mbar_wait_bounded(qfull(s), (j / 3) & 1, kTcWaitLimitNs)) {
+          !mbar_wait_bounded(qfull(s), (j / L::kStages) & 1, kTcWaitLimitNs)) {
         failed = true;
         break;
       }

@@ -21,11 +21,11 @@ namespace {
 // Bytes: 4 per slot read once, 4 per kept slot written; what bounds it is the latency of the
 // passes: loads and counts in the first, barriers in all.
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;      // two CTAs per SM
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelKeys = 48 * 1024;     // keys a CTA holds in shared memory (192 KB)
+constexpr int kSelKeys = 48 * 1024;     // keys a CTA holds in shared memory, at most (192 KB)
 constexpr int kShortRow = 1024;
 constexpr uint32_t kHeld = 0xffffffffu; // key of a slot that is kept whatever its weight
 
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kShortRow / 4) evict_select_short_kernel(const
     if (t0 + i < n && rank[i] < k) out[at++] = t0 + i;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ SelArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int bh = blockIdx.x / C, b = bh / a.H;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   extern __shared__ uint32_t keys[];
   __shared__ int hist[2][kBins];          // alternating passes
   __shared__ int warp_sums[32];
-  __shared__ int found[2], counts[2];     // (digit, its rank from above); (above, equal) of this CTA
+  __shared__ int found[3], counts[2];     // (digit, its rank from above, its keys); (above, equal) of this CTA
   const bool bad = n < 0 || n > a.cap;
   const int k = bad ? -1 : min(n, a.budget);
   if (rank == 0 && bh % a.H == 0 && threadIdx.x == 0) a.kept_lens[b] = k;
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 
   uint32_t prefix = 0;                    // the k-th key's digits so far
   int need = k;                           // its rank among the keys that match them
+  int low = 0;                            // key bits that need no look: every match is kept
   const int shift[3] = {21, 10, 0};
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
@@ -188,38 +189,49 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       }
     }
     sync_all();
-    // counts of the cluster, two digits per thread, from the highest digit down
-    int c[2] = {0, 0};
-    const int top = kBins - 1 - 2 * int(threadIdx.x);
+    // counts of the cluster, a few digits per thread, from the highest digit down
+    constexpr int PT = kBins / kSelThreads;
+    int c[PT], sum = 0;
+    const int top = kBins - 1 - PT * int(threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < PT; ++i) c[i] = 0;
     for (int r = 0; r < C; ++r) {
       const int* const hr = C > 1 ? cluster.map_shared_rank(h, r) : h;
-      c[0] += hr[top];
-      c[1] += hr[top - 1];
-    }
-    int total;
-    int above = block_exclusive_scan<kSelWarps>(c[0] + c[1], warp_sums, total);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < PT; ++i) c[i] += hr[top - i];
+    }
+#pragma unroll
+    for (int i = 0; i < PT; ++i) sum += c[i];
+    int total;
+    int above = block_exclusive_scan<kSelWarps>(sum, warp_sums, total);
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
       if (above < need && need <= above + c[i]) {
         found[0] = top - i;
         found[1] = need - above;
+        found[2] = c[i];
       }
       above += c[i];
     }
     __syncthreads();
     prefix = (prefix << (pass == 2 ? 10 : 11)) | uint32_t(found[0]);
     need = found[1];
+    const bool all = found[2] == need;
     sync_all();       // the counts of this pass have been read by everyone
+    if (all) {        // (the same for the whole cluster)
+      low = sh;
+      break;
+    }
     if (pass == 0) {  // (the last pass counts in this array again)
       for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[0][i] = 0;
       __syncthreads();
     }
   }
-  // prefix: the k-th key; `need` of its equals are kept, the lowest slots
+  // prefix: the k-th key above bit `low`; `need` of its equals there are kept, the lowest slots
   const int w0 = t0 + warp * per_warp, w1 = min(t1, w0 + per_warp);
   int above = 0, equal = 0;
   for (int t = w0 + lane; t < w1; t += 32) {
-    const uint32_t key = key_at(t);
+    const uint32_t key = key_at(t) >> low;
     above += key > prefix ? 1 : 0;
     equal += key == prefix ? 1 : 0;
   }
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     E += cluster.map_shared_rank(counts, r)[1];
   }
   for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t key = t < w1 ? key_at(t) : 0u;
+    const uint32_t key = t < w1 ? key_at(t) >> low : 0u;
     const bool is_above = t < w1 && key > prefix, is_equal = t < w1 && key == prefix;
     const unsigned ma = __ballot_sync(RQ_FULL_MASK, is_above);
     const unsigned me = __ballot_sync(RQ_FULL_MASK, is_equal);
