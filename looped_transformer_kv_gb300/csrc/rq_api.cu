@@ -150,6 +150,7 @@ rq_status check_chunk_sizes(const rq_shape* s, int32_t loop, int32_t n_new, int3
   if (max_ctx < 0 || max_ctx > s->capacity) return RQ_ERR_INVALID_ARG;
   if (window < 0 || window > n_new) return RQ_ERR_INVALID_ARG;
   if (int64_t(max_ctx) + n_new > (int64_t(1) << 30)) return RQ_ERR_UNSUPPORTED;
+  if (int64_t(s->n_q_heads / s->n_kv_heads) * n_new > (int64_t(1) << 24)) return RQ_ERR_UNSUPPORTED;
   if (int64_t(s->batch) * s->n_q_heads * (n_new > 0 ? n_new : 1) > (int64_t(1) << 31))
     return RQ_ERR_UNSUPPORTED;
   return RQ_OK;

@@ -116,12 +116,13 @@ struct RebuildSmem {
   static constexpr int kRef = kTile * (D + 8 * NG);                       // one record's sections
   static constexpr int kRes = RES ? kTile * (2 * (D * RES / 8) + 8 * NG + 4) : 0;
   static constexpr int kImg = kKeys * D * 2;
-  // H; E, then the image going out (V's in a region of its own where there is room); K's low parts
-  static constexpr int h = 0, e = RES ? 128 * D * 2 : 0, v = RES ? e : e + kImg, lo = v + kImg;
-  static constexpr int sec = lo + (KLO ? kImg : 0);
+  // H; E, then the images going out (V's and K's low parts in a region of their own where there is
+  // room)
+  static constexpr int h = 0, e = RES ? 128 * D * 2 : 0, v = RES ? e : e + kImg;
+  static constexpr int sec = v + kImg;
   static constexpr int az = sec + 2 * (kRef + kRes), sign = az + kKeys * NG * 8;
   static constexpr int bars = sign + 2 * D * 4, total = bars + 64 + 1024;
-  static_assert(total <= (KLO ? 227 * 1024 : 113 * 1024), "two CTAs per SM without K's low parts");
+  static_assert(total <= 113 * 1024, "two CTAs per SM");
 };
 
 // 8 channels of chunk token t (K or V side) as fp16 pairs; a value out of range becomes 0 and `out`
@@ -148,24 +149,23 @@ __device__ __forceinline__ uint32_t state_pair(uint32_t w, int t, int& out, uint
 }
 
 // The chunk's own keys in the tile that holds the context's end: rows old .. 127 of the image in
-// shared memory (zeros behind the last token).
-template <int D, bool KLO, bool V>
+// shared memory (zeros behind the last token).  PART 0: K, 1: K's low parts, 2: V.
+template <int D, int PART>
 __device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int n, int ctx, int t0, int old,
-                                        uint8_t* img, uint8_t* img_lo) {
+                                        uint8_t* img) {
   int out = INT_MAX;
 #pragma unroll 1
   for (int i = old * (D / 8) + threadIdx.x; i < kKeys * (D / 8); i += 256) {
     const int key = i / (D / 8), c = i % (D / 8), t = t0 + key - ctx;
-    const uint16_t* src = a.kv_new + (V ? a.kv_v : 0) + b * a.ks0 + int64_t(min(t, n - 1)) * a.ks1 + h * a.ks_h + 8 * c;
+    const uint16_t* src = a.kv_new + (PART == 2 ? a.kv_v : 0) + b * a.ks0 + int64_t(min(t, n - 1)) * a.ks1 + h * a.ks_h + 8 * c;
     uint4 y = load_states(src, a.vec);
     if (t >= n) y = make_uint4(0u, 0u, 0u, 0u);
     uint32_t lo[4];
-    const uint32_t w[4] = {state_pair(y.x, t, out, lo), state_pair(y.y, t, out, lo + 1),
-                           state_pair(y.z, t, out, lo + 2), state_pair(y.w, t, out, lo + 3)};
-    if constexpr (!V) {
-      const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
-      *reinterpret_cast<uint4*>(img + o) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (KLO) *reinterpret_cast<uint4*>(img_lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    uint32_t w[4] = {state_pair(y.x, t, out, lo), state_pair(y.y, t, out, lo + 1), state_pair(y.z, t, out, lo + 2),
+                     state_pair(y.w, t, out, lo + 3)};
+    if constexpr (PART < 2) {
+      *reinterpret_cast<uint4*>(img + (c / 8) * (kKeys * 128) + panel_offset(key, c % 8)) =
+          PART ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant_
 // Bound by HBM (one loop's rows read, 4 d bytes per token-head written) and by the instructions
 // of the conversions (about 1,500 per token-head).
 template <int D, int RES, bool KLO>
-__global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_constant__ RebuildArgs a, int n_items) {
+__global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__ RebuildArgs a, int n_items) {
   using L = RebuildSmem<D, RES, KLO>;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -368,6 +368,8 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     }
     if (tid < 2 * D) sign[tid] = float(a.signs[tid / D][int64_t(h) * D + tid % D]) * inv_sqrt_d;
     __syncthreads();
+    constexpr int LOW = KLO && RES ? 16 * NG / 2 : 1;   // fp16 pairs of low parts a thread keeps
+    uint32_t e_lo[LOW];
     {
       failed = !mbar_wait_bounded(loaded, phase, kTcWaitLimitNs);
       if constexpr (RES != 0) {   // E of K: a thread per key and half its words
@@ -391,15 +393,12 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
           }
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            uint32_t hi[PER / 2], lo[PER / 2];
-            word_levels<RES, KLO>(w[g], m[g], hi, lo);
+            uint32_t hi[PER / 2];
+            word_levels<RES, KLO>(w[g], m[g], hi, e_lo + (jj * NG + g) * (KLO ? PER / 2 : 0));
 #pragma unroll
-            for (int c = 0; c < CPW; ++c) {
-              const uint32_t o = (g / 2) * (kKeys * 128) + panel_offset(key, (g % 2) * 4 + j * CPW + c);
-              *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              if constexpr (KLO)
-                *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-            }
+            for (int c = 0; c < CPW; ++c)
+              *reinterpret_cast<uint4*>(smem + L::e + (g / 2) * (kKeys * 128) + panel_offset(key, (g % 2) * 4 + j * CPW + c)) =
+                  make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
           }
         }
         fence_async_smem();
@@ -424,15 +423,40 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     if constexpr (RES != 0) {
       constexpr uint32_t idk = f16_idesc(kKeys, D), idv = f16_idesc(128, kKeys);
       const uint32_t hs = smem_u32(smem + L::h), es = smem_u32(smem + L::e);
-      if (leader) {
-        tc_fence_after();
-#pragma unroll
-        for (int part = 0; part < (KLO ? 2 : 1); ++part)
+      auto k_products = [&](bool add) {
+        if (leader) {
+          tc_fence_after();
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
-            tc_mma(tmem, panel_desc((part ? smem_u32(smem + L::lo) : es) + (x / 4) * (kKeys * 128) + (x % 4) * 32),
-                   panel_desc(hs + (x / 4) * (128 * 128) + (x % 4) * 32), idk, part > 0 || x > 0);
-        tc_commit(kdone);
+            tc_mma(tmem, panel_desc(es + (x / 4) * (kKeys * 128) + (x % 4) * 32),
+                   panel_desc(hs + (x / 4) * (128 * 128) + (x % 4) * 32), idk, add || x > 0);
+          tc_commit(kdone);
+        }
+      };
+      k_products(false);
+      if constexpr (KLO) {     // the levels' low parts, in the same place
+        failed = !mbar_wait_bounded(kdone, 0, kTcWaitLimitNs);
+        if (__syncthreads_or(failed)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        constexpr int PER = 32 / RES, CPW = PER / 8;
+#pragma unroll
+        for (int jj = 0; jj < RES / 2; ++jj)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int c = 0; c < CPW; ++c) {
+              const uint32_t* lo = e_lo + (jj * NG + g) * (PER / 2) + 4 * c;
+              const int j = 2 * jj + (tid & 1);
+              *reinterpret_cast<uint4*>(smem + L::e + (g / 2) * (kKeys * 128) + panel_offset(tid >> 1, (g % 2) * 4 + j * CPW + c)) =
+                  make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        k_products(true);
       }
       // E of V: a thread per pair of keys and 16 bytes of its words (4 units of both keys)
       constexpr int CHUNKS = D * RES / 64;                // 16-byte chunks of a pair's words
@@ -449,7 +473,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
         m[i][0] = *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + g) * 4);
         m[i][1] = *reinterpret_cast<const uint32_t*>(res + kTile * RROW + ((row + 1) * NG + g) * 4);
       }
-      failed = !mbar_wait_bounded(kdone, phase, kTcWaitLimitNs);
+      failed = !mbar_wait_bounded(kdone, KLO ? 1 : phase, kTcWaitLimitNs);
       if (__syncthreads_or(failed)) {
         failed = true;
         break;
@@ -538,30 +562,29 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
       failed = !mbar_wait_bounded(vdone, phase, kTcWaitLimitNs);       // E is free
       tc_fence_after();
     }
-    {
+    auto k_image = [&](uint8_t* img, bool low) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        uint32_t hi[4], lo[4];
+        uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float x0, x1;
           unpack2(x[4 * i + k], x0, x1);
-          hi[k] = half2_sat(x0, x1);
-          if constexpr (KLO) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-            lo[k] = half2_sat(x0 - f.x, x1 - f.y);
+          w[k] = half2_sat(x0, x1);
+          if (low) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            w[k] = half2_sat(x0 - f.x, x1 - f.y);
           }
         }
         const int g = i / 2, chunk = (g % 2) * 4 + 2 * hh + i % 2;
-        const uint32_t o = (g / 2) * (kKeys * 128) + panel_offset(r, chunk);
-        *reinterpret_cast<uint4*>(smem + L::e + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (KLO) *reinterpret_cast<uint4*>(smem + L::lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(img + (g / 2) * (kKeys * 128) + panel_offset(r, chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
+    };
+    k_image(smem + L::e, false);
     // the chunk's own keys of the last cached tile over the rows behind the context
     if (old < kKeys) {
       __syncthreads();
-      mixed_rows<D, KLO, false>(a, b, h, n, ctx, t0, old, smem + L::e, smem + L::lo);
+      mixed_rows<D, 0>(a, b, h, n, ctx, t0, old, smem + L::e);
     }
     fence_async_smem();
     if (__syncthreads_or(failed)) {
@@ -570,9 +593,23 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     }
     if (tid == 0) {
       bulk_s2g(a.k + at, smem_u32(smem + L::e), L::kImg);
-      if (KLO) bulk_s2g(a.klo + at, smem_u32(smem + L::lo), L::kImg);
       bulk_s2g_commit();
       if (L::v == L::e) bulk_s2g_wait_read();
+    }
+    if constexpr (KLO) {
+      if (L::v == L::e) __syncthreads();                  // K's image has left
+      k_image(smem + L::v, true);
+      if (old < kKeys) {
+        __syncthreads();
+        mixed_rows<D, 1>(a, b, h, n, ctx, t0, old, smem + L::v);
+      }
+      fence_async_smem();
+      __syncthreads();
+      if (tid == 0) {
+        bulk_s2g(a.klo + at, smem_u32(smem + L::v), L::kImg);
+        bulk_s2g_commit();
+        bulk_s2g_wait_read();
+      }
     }
     // ---- V epilogue: channel ch, 32 keys at a time from k0 of record rec
     constexpr int QS = D / 64;
@@ -580,7 +617,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     const int part = D == 128 ? 0 : r >> 6;               // (D = 64: lanes 64 .. hold the channels again)
     const float sg = RES ? sign[D + ch] : 0.f;
     const uint64_t sg2 = pack2(sg, sg), base = pack2(-8388608.f, -8388608.f);
-    if (L::v == L::e) __syncthreads();                    // K's image has left
+    if (KLO || L::v == L::e) __syncthreads();             // the image before has left
 #pragma unroll 1
     for (int q = 0; q < QS; ++q) {
       const int k0 = hh * 64 + (D == 128 ? q : part) * 32;     // first key of these
@@ -616,7 +653,7 @@ __global__ void __launch_bounds__(256, KLO ? 1 : 2) rebuild_kernel(const __grid_
     }
     if (old < kKeys) {
       __syncthreads();
-      mixed_rows<D, KLO, true>(a, b, h, n, ctx, t0, old, smem + L::v, nullptr);
+      mixed_rows<D, 2>(a, b, h, n, ctx, t0, old, smem + L::v);
     }
     fence_async_smem();
     tc_fence_before();
@@ -754,10 +791,10 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 13);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
-  const int64_t unit = int64_t(blockIdx.z) * a.v.H + h;
   const int split = blockIdx.x % a.n_splits;
-  const int block = int(gridDim.x / a.n_splits) - 1 - int(blockIdx.x / a.n_splits);   // long rows first
+  const int64_t unit = blockIdx.x / a.n_splits;
+  const int h = int(unit % a.v.H), b = a.v.b0 + int(unit / a.v.H);
+  const int block = int(gridDim.y) - 1 - int(blockIdx.y);      // the longest row blocks of all units first
   int n, ctx;
   // (one thread reads the error word: another CTA may be setting it)
   const bool flagged = __syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile unsigned*>(a.v.err) != 0u);
@@ -808,11 +845,12 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         load_k(nk);
         if (nk < 2) load_v(nv++);
       }
-      for (int j = 2; j < T; ++j) {
-        // scores of tile j - 1 done (so of j - 2, and its values): K j + 1 and V j have room
-        if (!mbar_wait_bounded(sready(last_tile, j - 1), ((j - 1) >> 1) & 1, kTcWaitLimitNs)) break;
-        load_v(nv++);
-        if (j + 1 < T) load_k(nk++);
+      for (int j = 0; nv < T; ++j) {
+        // scores of tile j done, so the values of the tile before: room for K j + 3 and V j + 1
+        // (LSE: V holds K's low parts, done with the scores: j + 2)
+        if (!mbar_wait_bounded(sready(last_tile, j), (j >> 1) & 1, kTcWaitLimitNs)) break;
+        if (nk < T) load_k(nk++);
+        if (nv < min(T, j + (LSE ? 3 : 2))) load_v(nv++);
       }
       failed = nv < T;
       for (int j = max(0, nk - 3); j < nk; ++j) failed |= !mbar_wait_bounded(kfull(j % 3), (j / 3) & 1, kTcWaitLimitNs);
@@ -1376,7 +1414,7 @@ cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, cudaStream_t str
   const cudaError_t e = cudaFuncSetAttribute(rebuild_kernel<D, RES, KLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   if (e != cudaSuccess) return e;
   if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int64_t ctas = int64_t(device_sm_count()) * (KLO ? 1 : 2);
+  const int64_t ctas = int64_t(device_sm_count()) * 2;
   rebuild_kernel<D, RES, KLO><<<unsigned(items < ctas ? items : ctas), 256, L::total, stream>>>(r, int(items));
   return cudaGetLastError();
 }
@@ -1467,7 +1505,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     a.qvec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.qs0 % 8 == 0 && a.qs1 % 8 == 0 && a.qs2 % 8 == 0;
     a.scale_log2 = scale;
     const unsigned blocks = unsigned((l.rows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, false><<<dim3(blocks * l.splits, H, nb), 384, AS::total, stream>>>(a);
+    attention_kernel<D, false><<<dim3(nb * H * l.splits, blocks, 1), 384, AS::total, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.splits > 1) {
       merge_kernel<D><<<dim3(unsigned((l.rows + 3) / 4), H, nb), 128, 0, stream>>>(a);
@@ -1477,7 +1515,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     a.n_splits = l.wsplits;
     a.row_tiles = l.q_tiles;
     const unsigned wblocks = unsigned((l.wrows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, true><<<dim3(wblocks * l.wsplits, H, nb), 384, AS::total, stream>>>(a);
+    attention_kernel<D, true><<<dim3(nb * H * l.wsplits, wblocks, 1), 384, AS::total, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     WeightArgs x;
     x.v = v;
