@@ -593,7 +593,10 @@ FusedLayout fused_layout(const rq_shape& s, int loop, int n_new, int max_ctx) {
 template <int D, int RES>
 cudaError_t launch_fused(const FusedArgs& a, int batch, cudaStream_t stream) {
   using L = FusedSmem<D, RES>;
-  cudaError_t e = cudaFuncSetAttribute(fused_kernel<D, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(fused_kernel<D, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  });
   if (e != cudaSuccess) return e;
   const int64_t n_rows = int64_t(batch) * a.H * a.rows;
   fused_rows_kernel<D, RES><<<unsigned((n_rows + 3) / 4), 128, 0, stream>>>(a, int(n_rows));

@@ -1411,7 +1411,10 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
 template <int D, int RES, bool KLO>
 cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, cudaStream_t stream) {
   using L = RebuildSmem<D, RES, KLO>;
-  const cudaError_t e = cudaFuncSetAttribute(rebuild_kernel<D, RES, KLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  static OncePerDevice once;
+  const cudaError_t e = once([] {
+    return cudaFuncSetAttribute(rebuild_kernel<D, RES, KLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  });
   if (e != cudaSuccess) return e;
   if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int64_t ctas = int64_t(device_sm_count()) * 2;
@@ -1435,11 +1438,18 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
   cudaError_t e;
   using AS = AttnSmem<D>;
   using WS = WeightSmem<D>;
-  if ((e = cudaFuncSetAttribute(chunk_image_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kKeys * D * 2 + 128)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(chunk_image_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kKeys * D * 2 + 128)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(attention_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AS::total)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WS::total)) != cudaSuccess ||
+  static OncePerDevice once;
+  e = once([] {
+    cudaError_t x;
+    const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if ((x = cudaFuncSetAttribute(chunk_image_kernel<D, true>, smem, 3 * kKeys * D * 2 + 128)) != cudaSuccess ||
+        (x = cudaFuncSetAttribute(chunk_image_kernel<D, false>, smem, 2 * kKeys * D * 2 + 128)) != cudaSuccess ||
+        (x = cudaFuncSetAttribute(attention_kernel<D, false>, smem, AS::total)) != cudaSuccess ||
+        (x = cudaFuncSetAttribute(attention_kernel<D, true>, smem, AS::total)) != cudaSuccess)
+      return x;
+    return cudaFuncSetAttribute(weights_kernel<D>, smem, WS::total);
+  });
+  if (e != cudaSuccess ||
       (e = cudaMemsetAsync(w + l.first_bad, 0x7f, size_t(s.batch) * s.n_kv_heads * 4, stream)) != cudaSuccess)
     return e;
   ChunkView v;

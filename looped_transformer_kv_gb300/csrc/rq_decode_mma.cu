@@ -1,6 +1,7 @@
 // ResidualQuant split-KV decode attention on the tensor cores (sm_103a): host side (query
 // blocks, split plan, launches) and the contiguous-cache kernel variants.  The kernel itself
 // is in rq_decode_mma.cuh.
+#include <atomic>
 #include <mutex>
 
 #include "rq_decode_mma.cuh"
@@ -243,12 +244,20 @@ QueryBlock chunk_block(const rq_shape& s, int loop, int rows) {
 
 SplitPlan plan_splits_chunk(const rq_shape& s, int loop, int rows, int max_ctx) {
   const QueryBlock bq = chunk_block(s, loop, rows);
-  rq_cache dummy;
-  memset(&dummy, 0, sizeof(dummy));
-  BlockLaunch bl;
-  int ctas = 1;
-  if (build_block(s, dummy, bq, 0, bl))
-    ctas = resident_ctas(s.head_dim, bl.res4, bq.nr, block_packing(bq), bl.smem);
+  // CTAs per SM of the block's variant: asked of the runtime once per device
+  static std::atomic<int> known[64][2][3][3];
+  const int kind = bq.nr == 0 ? 0 : s.res_bits[loop] / 2, pk = block_packing(bq);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = -1;
+  std::atomic<int>* const slot = dev < 0 ? nullptr : &known[dev][s.head_dim / 128][kind][pk];
+  int ctas = slot ? slot->load() : 0;
+  if (ctas == 0) {
+    rq_cache dummy;
+    memset(&dummy, 0, sizeof(dummy));
+    BlockLaunch bl;
+    ctas = build_block(s, dummy, bq, 0, bl) ? resident_ctas(s.head_dim, bl.res4, bq.nr, pk, bl.smem) : 1;
+    if (slot) slot->store(ctas);
+  }
   rq_shape units = s;   // every block of rows is a unit of its own
   units.n_kv_heads *= (rows + bq.gw - 1) / bq.gw;
   return plan_splits_for(units, max_ctx, ctas, kT);

@@ -14,12 +14,13 @@ namespace {
 //
 // Weights become 32-bit keys of the same order.  A short row (at most 1024 slots): a slot's rank is
 // counted directly, every key against every other.  A long one: the k-th largest key by radix
-// selection: three passes over 11, 11 and 10 key bits count the digits of the keys that still
-// match, and fix the digit of the k-th one.  One more pass in slot order takes every key above the
-// k-th and, of its equals, the first ones.  A long row may be shared by a cluster of CTAs (each
+// selection.  Passes over the row count the keys' first 11 bits, the next 11 of those that share the
+// k-th one's, and the last 10, as far as needed (a digit all of whose keys are kept ends it).  Then
+// a pass counts and one writes, in slot order, every key above the k-th and, of its equals, the
+// first ones.  A long row may be shared by a cluster of CTAs (each
 // holds its part of the keys in shared memory, the counts are added over the cluster).
-// Bytes: 4 per slot read once, 4 per kept slot written; what bounds it is the latency of the
-// passes: loads and counts in the first, barriers in all.
+// Bytes: 4 per slot read once, 4 per kept slot written; what bounds it is the instructions of the
+// passes (a row of 16,384 slots and 512 threads: about 50 per slot and lane), then their barriers.
 
 constexpr int kSelThreads = 512;      // two CTAs per SM
 constexpr int kSelWarps = kSelThreads / 32;
@@ -29,7 +30,7 @@ constexpr int kSelKeys = 48 * 1024;     // keys a CTA holds in shared memory, at
 constexpr int kShortRow = 1024;
 constexpr uint32_t kHeld = 0xffffffffu; // key of a slot that is kept whatever its weight
 
-// Same order as the weights; NaN above every number, -0 as +0; never 0.
+// Same order as the weights; NaN above every number, -0 as +0; at least 2^21 (the key of -inf).
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(w + 0.f);
@@ -119,9 +120,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   const int n = a.ctx_lens[b];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[2][kBins];          // alternating passes
+  __shared__ int hist[kBins];
   __shared__ int warp_sums[32];
-  __shared__ int found[3], counts[2];     // (digit, its rank from above, its keys); (above, equal) of this CTA
+  __shared__ int found[3], counts[2];     // (digit, rank among its keys, its keys); (kept, equal) of this CTA
   const bool bad = n < 0 || n > a.cap;
   const int k = bad ? -1 : min(n, a.budget);
   if (rank == 0 && bh % a.H == 0 && threadIdx.x == 0) a.kept_lens[b] = k;
@@ -137,66 +138,67 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     else
       __syncthreads();
   };
-  // this CTA's slots [t0, t1): a multiple of 32 per warp
+  // this CTA's slots [t0, t1), a warp's [w0, w1): a multiple of 32 each
   const int per_warp = ((n + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32;
   const int t0 = min(n, rank * kSelWarps * per_warp), t1 = min(n, t0 + kSelWarps * per_warp);
+  const int w0 = min(n, t0 + warp * per_warp), w1 = min(t1, w0 + per_warp);
   const float* const row = a.weights + int64_t(bh) * a.cap;
   const int held_from = n - a.n_last;
-  auto fresh_key = [&](int t) {
-    return (t < a.n_first || t >= held_from) ? kHeld : weight_key(row[t]);
-  };
   const bool stored = t1 - t0 <= a.slice;
-  for (int i = threadIdx.x; i < 2 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-  __syncthreads();
-  auto key_at = [&](int t) { return stored ? keys[t - t0] : fresh_key(t); };
-
-  uint32_t prefix = 0;                    // the k-th key's digits so far
-  int need = k;                           // its rank among the keys that match them
-  int low = 0;                            // key bits that need no look: every match is kept
-  const int shift[3] = {21, 10, 0};
+  // keys of slots base + 32 u + lane, U of them in flight; 0 behind the warp's slots
+  constexpr int U = 8;
+  auto fresh_keys = [&](int base, uint32_t (&key)[U]) {
+    float w[U];
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int sh = shift[pass];
-    const uint32_t digits = pass == 2 ? 1024u : 2048u;
-    int* const h = hist[pass & 1];
-    constexpr int U = 8;                  // slots a thread has in flight
-    for (int base = t0; base < t1; base += U * kSelThreads) {
-      uint32_t key[U];
+    for (int u = 0; u < U; ++u) w[u] = row[min(base + 32 * u + lane, w1 - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) key[u] = base + 32 * u + lane < w1 ? weight_key(w[u]) : 0u;
+    if (base < a.n_first || base + 32 * U > held_from) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = base + u * kSelThreads + threadIdx.x;
-        key[u] = t < t1 ? (pass == 0 ? fresh_key(t) : key_at(t)) : 0u;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = base + u * kSelThreads + threadIdx.x;
-        bool mine = t < t1;
-        if (pass == 0) {
-          if (mine && stored) keys[t - t0] = key[u];
-        } else {
-          mine = mine && (key[u] >> (sh + (pass == 2 ? 10 : 11))) == prefix;
-        }
-        const uint32_t d = (key[u] >> sh) & (digits - 1u);
-        // a warp whose keys share a digit (equal weights) adds once
-        const unsigned active = __ballot_sync(RQ_FULL_MASK, mine);
-        if (active == 0u) continue;
-        const uint32_t d0 = __shfl_sync(RQ_FULL_MASK, d, __ffs(active) - 1);
-        if (__all_sync(RQ_FULL_MASK, !mine || d == d0)) {
-          if (lane == 0) atomicAdd(&h[d0], __popc(active));
-        } else if (mine) {
-          atomicAdd(&h[d], 1);
-        }
+        const int t = base + 32 * u + lane;
+        if (t < w1 && (t < a.n_first || t >= held_from)) key[u] = kHeld;
       }
     }
+  };
+  auto load_keys = [&](int base, uint32_t (&key)[U]) {
+    if (stored) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = base + 32 * u + lane;
+        key[u] = t < w1 ? keys[t - t0] : 0u;
+      }
+    } else {
+      fresh_keys(base, key);
+    }
+  };
+  for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
+  // the first digits of every key (held keys are above every other: they count too)
+  for (int base = w0; base < w1; base += 32 * U) {
+    uint32_t key[U];
+    fresh_keys(base, key);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = base + 32 * u + lane;
+      if (t < w1) {
+        if (stored) keys[t - t0] = key[u];
+        atomicAdd(&hist[key[u] >> 21], 1);
+      }
+    }
+  }
+  uint32_t prefix = 0;                    // the k-th key's digits so far
+  int need = k, bits = 0;                 // its rank among the keys that match them; their number
+  for (int pass = 0;; ++pass) {
     sync_all();
-    // counts of the cluster, a few digits per thread, from the highest digit down
+    // counts of the cluster, a few digits per thread, from the highest down
     constexpr int PT = kBins / kSelThreads;
     int c[PT], sum = 0;
     const int top = kBins - 1 - PT * int(threadIdx.x);
 #pragma unroll
     for (int i = 0; i < PT; ++i) c[i] = 0;
     for (int r = 0; r < C; ++r) {
-      const int* const hr = C > 1 ? cluster.map_shared_rank(h, r) : h;
+      const int* const hr = C > 1 ? cluster.map_shared_rank(hist, r) : hist;
 #pragma unroll
       for (int i = 0; i < PT; ++i) c[i] += hr[top - i];
     }
@@ -214,50 +216,65 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
       above += c[i];
     }
     __syncthreads();
-    prefix = (prefix << (pass == 2 ? 10 : 11)) | uint32_t(found[0]);
+    const int width = pass == 2 ? 10 : 11;
+    prefix = (prefix << width) | uint32_t(found[0]);
+    bits += width;
     need = found[1];
-    const bool all = found[2] == need;
-    sync_all();       // the counts of this pass have been read by everyone
-    if (all) {        // (the same for the whole cluster)
-      low = sh;
-      break;
-    }
-    if (pass == 0) {  // (the last pass counts in this array again)
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[0][i] = 0;
-      __syncthreads();
+    const int match = found[2];
+    if (C > 1) cluster.sync();            // the counts have been read by everyone
+    if (match == need || bits == 32) break;   // every match is kept, or they are equal
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    const int next = bits == 11 ? 10 : 0;     // the next digit's lowest bit
+    const uint32_t mask = bits == 11 ? 2047u : 1023u;
+    for (int base = w0; base < w1; base += 32 * U) {
+      uint32_t key[U];
+      load_keys(base, key);
+#pragma unroll
+      for (int u = 0; u < U; ++u)         // (a slot behind the row has key 0, no key's digits)
+        if (key[u] >> (32 - bits) == prefix) atomicAdd(&hist[(key[u] >> next) & mask], 1);
     }
   }
-  // prefix: the k-th key above bit `low`; `need` of its equals there are kept, the lowest slots
-  const int w0 = t0 + warp * per_warp, w1 = min(t1, w0 + per_warp);
-  int above = 0, equal = 0;
-  for (int t = w0 + lane; t < w1; t += 32) {
-    const uint32_t key = key_at(t) >> low;
-    above += key > prefix ? 1 : 0;
-    equal += key == prefix ? 1 : 0;
+  // keys above `high` are kept, and the first `need` slots of low .. high
+  const uint32_t low = bits == 32 ? prefix : prefix << (32 - bits);
+  const uint32_t high = bits == 32 ? prefix : low | ((1u << (32 - bits)) - 1u);
+  int kept = 0, equal = 0;
+  for (int base = w0; base < w1; base += 32 * U) {
+    uint32_t key[U];
+    load_keys(base, key);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      kept += key[u] > high ? 1 : 0;
+      equal += key[u] >= low ? 1 : 0;
+    }
   }
-  int above_all, equal_all;
-  const int above_before = block_exclusive_scan<kSelWarps>(above, warp_sums, above_all);
+  equal -= kept;
+  int kept_all, equal_all;
+  const int kept_before = block_exclusive_scan<kSelWarps>(kept, warp_sums, kept_all);
   const int equal_before = block_exclusive_scan<kSelWarps>(equal, warp_sums, equal_all);
   if (threadIdx.x == 0) {
-    counts[0] = above_all;
+    counts[0] = kept_all;
     counts[1] = equal_all;
   }
   sync_all();
-  int A = __shfl_sync(RQ_FULL_MASK, above_before, 0), E = __shfl_sync(RQ_FULL_MASK, equal_before, 0);
+  int A = __shfl_sync(RQ_FULL_MASK, kept_before, 0), E = __shfl_sync(RQ_FULL_MASK, equal_before, 0);
   for (int r = 0; r < rank; ++r) {
     A += cluster.map_shared_rank(counts, r)[0];
     E += cluster.map_shared_rank(counts, r)[1];
   }
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t key = t < w1 ? key_at(t) >> low : 0u;
-    const bool is_above = t < w1 && key > prefix, is_equal = t < w1 && key == prefix;
-    const unsigned ma = __ballot_sync(RQ_FULL_MASK, is_above);
-    const unsigned me = __ballot_sync(RQ_FULL_MASK, is_equal);
-    const unsigned lower = (1u << lane) - 1u;
-    const int a_here = A + __popc(ma & lower), e_here = E + __popc(me & lower);
-    if (is_above || (is_equal && e_here < need)) out[a_here + min(e_here, need)] = t;
-    A += __popc(ma);
-    E += __popc(me);
+  const unsigned lower = (1u << lane) - 1u;
+  for (int base = w0; base < w1; base += 32 * U) {
+    uint32_t key[U];
+    load_keys(base, key);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool above = key[u] > high, among = key[u] >= low && !above;
+      const unsigned ma = __ballot_sync(RQ_FULL_MASK, above), me = __ballot_sync(RQ_FULL_MASK, among);
+      const int e_here = E + __popc(me & lower);
+      if (above || (among && e_here < need)) out[A + __popc(ma & lower) + min(e_here, need)] = base + 32 * u + lane;
+      A += __popc(ma);
+      E += __popc(me);
+    }
   }
   if (C > 1) cluster.sync();   // (no CTA leaves while its counts may be read)
 }
@@ -288,7 +305,7 @@ struct MoveArgs {
   const int32_t* kept_lens;
   const float* weights;
   float* to_weights;
-  int H, L, budget, src_cap, dst_cap, tiles;
+  int H, L, budget, src_cap, dst_cap, ctas;   // ctas: per (sequence, kv-head), out of place
   int8_t res_bits[RQ_MAX_LOOPS];
 };
 
@@ -345,16 +362,17 @@ __device__ __forceinline__ Unit unit_of(int i) {
 
 template <int D, bool IN_PLACE, int KIND>
 __device__ __forceinline__ void move_section(const MoveArgs& a, int sect) {
-  const int per_bh = IN_PLACE ? kMoveCluster : a.tiles;
-  const int64_t bh = blockIdx.x / per_bh;
-  const int first_tile = blockIdx.x % per_bh;
+  const int step = IN_PLACE ? kMoveCluster : a.ctas;        // CTAs of a (sequence, kv-head): tile step
+  const int64_t bh = blockIdx.x / step;
+  const int first_tile = blockIdx.x % step;
   const int b = int(bh / a.H), h = int(bh % a.H);
   const int kept = max(0, min(a.kept_lens[b], min(a.budget, a.dst_cap)));
   const int n_tiles = (kept + kTile - 1) / kTile;
   const int sec_off = sect == 0 ? 0 : loop_section_offset(D, a.res_bits, sect - 1);
   const int32_t* const keep = a.keep + bh * a.budget;
-  __shared__ int64_t from[kTile];                    // record offset of each row's source, -1: none
-  __shared__ int from_row[kTile];
+  const bool moves_weights = a.weights && sect == 0;
+  __shared__ int64_t from[2][kTile];                 // record offset of each row's source, -1: none
+  __shared__ int from_row[2][kTile];
 
   // offset of the record of a tile, -1 where the block table has no page for it
   auto record = [&](int tile, const int32_t* bt, int max_pages, int n_pages, int cap) -> int64_t {
@@ -368,78 +386,66 @@ __device__ __forceinline__ void move_section(const MoveArgs& a, int sect) {
     }
     return rec * a.rec_bytes + sec_off;
   };
+  auto slot_of = [&](int tile) {                     // this thread's row of the tile: its source, or -1
+    const int t = tile * kTile + threadIdx.x;
+    if (threadIdx.x >= kTile || tile >= n_tiles || t >= kept) return -1;
+    const int s = keep[t];
+    return s >= 0 && s < a.src_cap ? s : -1;
+  };
 
-  const int waves = IN_PLACE ? (n_tiles + kMoveCluster - 1) / kMoveCluster : 1;
+  // (in place every CTA of the cluster takes every wave's barrier)
+  const int waves = IN_PLACE ? (n_tiles + step - 1) / step : max(0, (n_tiles - first_tile + step - 1) / step);
+  int slot = slot_of(first_tile);
   for (int wave = 0; wave < waves; ++wave) {
-    const int tile = first_tile + wave * kMoveCluster;
-    const bool active = tile < n_tiles;
-    const int64_t dst = active ? record(tile, a.dst_bt, a.dst_max_pages, a.dst_n_pages, a.dst_cap) : -1;
+    const int tile = first_tile + wave * step, buf = wave & 1;
+    const int64_t dst =
+        tile < n_tiles ? record(tile, a.dst_bt, a.dst_max_pages, a.dst_n_pages, a.dst_cap) : -1;
     if (threadIdx.x < kTile) {
-      const int t = tile * kTile + threadIdx.x;
-      int64_t f = -1;
-      int s = -1;
-      if (active && t < kept) {
-        s = keep[t];
-        if (s >= 0 && s < a.src_cap)
-          f = record(s / kTile, a.src_bt, a.src_max_pages, a.src_n_pages, a.src_cap);
-      }
-      from[threadIdx.x] = f;
-      from_row[threadIdx.x] = s & (kTile - 1);
+      from[buf][threadIdx.x] =
+          slot < 0 ? -1 : record(slot / kTile, a.src_bt, a.src_max_pages, a.src_n_pages, a.src_cap);
+      from_row[buf][threadIdx.x] = slot & (kTile - 1);
     }
     __syncthreads();
-    uint4 v[kMoveUnits];
-    int live[kMoveUnits];          // bit 0: the (first) row has a source, bit 1: the pair's second
+    float wt = 0.f;
+    if (moves_weights && slot >= 0) wt = a.weights[bh * a.src_cap + slot];
+    slot = slot_of(tile + step);                     // the next wave's, while this one moves
+    uint4 v[kMoveUnits][2];
+    int live[kMoveUnits];          // bit 0: the (first) row has a source, bit 1: the pair's second;
+                                   // V codes: bits 2, 3: it is the odd token of its source pair
 #pragma unroll
     for (int i = 0; i < kMoveUnits; ++i) {
       const Unit u = unit_of<D, KIND>(threadIdx.x + i * kMoveThreads);
       live[i] = 0;
       if (u.bytes == 0 || dst < 0) continue;
       if (!u.v_codes) {
-        const int64_t f = from[u.row];
+        const int64_t f = from[buf][u.row];
         if (f < 0) continue;
         live[i] = 1;
-        const uint8_t* p = a.src + f + u.off + from_row[u.row] * u.row_bytes + u.chunk * 16;
+        const uint8_t* p = a.src + f + u.off + from_row[buf][u.row] * u.row_bytes + u.chunk * 16;
         if (u.bytes == 16) {
-          v[i] = *reinterpret_cast<const uint4*>(p);
+          v[i][0] = *reinterpret_cast<const uint4*>(p);
         } else if (u.bytes == 8) {
           const uint2 x = *reinterpret_cast<const uint2*>(p);
-          v[i].x = x.x;
-          v[i].y = x.y;
+          v[i][0].x = x.x;
+          v[i][0].y = x.y;
         } else {
-          v[i].x = *reinterpret_cast<const uint16_t*>(p);
+          v[i][0].x = *reinterpret_cast<const uint16_t*>(p);
         }
       } else {
         // units 4 chunk .. + 3 of each token sit in 4 adjacent words of its pair (the swizzle
         // moves whole groups of 8 units)
         const int units = u.row_bytes / 2;
-        uint4 w[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          w[e] = make_uint4(0u, 0u, 0u, 0u);
-          const int64_t f = from[u.row + e];
+          v[i][e] = make_uint4(0u, 0u, 0u, 0u);
+          const int64_t f = from[buf][u.row + e];
           if (f < 0) continue;
-          live[i] |= 1 << e;
-          const int r = from_row[u.row + e], pair = r >> 1;
-          w[e] = *reinterpret_cast<const uint4*>(a.src + f + u.off + pair * (2 * u.row_bytes) +
-                                                 ((4 * u.chunk) ^ v_unit_swizzle(pair, units)) * 4);
-          if (r & 1) {
-            w[e].x >>= 16;
-            w[e].y >>= 16;
-            w[e].z >>= 16;
-            w[e].w >>= 16;
-          }
+          const int r = from_row[buf][u.row + e], pair = r >> 1;
+          live[i] |= (1 | ((r & 1) << 2)) << e;
+          v[i][e] = *reinterpret_cast<const uint4*>(a.src + f + u.off + pair * (2 * u.row_bytes) +
+                                                    ((4 * u.chunk) ^ v_unit_swizzle(pair, units)) * 4);
         }
-        v[i].x = __byte_perm(w[0].x, w[1].x, 0x5410);
-        v[i].y = __byte_perm(w[0].y, w[1].y, 0x5410);
-        v[i].z = __byte_perm(w[0].z, w[1].z, 0x5410);
-        v[i].w = __byte_perm(w[0].w, w[1].w, 0x5410);
       }
-    }
-    float wt = 0.f;
-    if (a.weights && sect == 0 && threadIdx.x < kTile && active) {
-      const int t = tile * kTile + threadIdx.x;
-      const int s = t < kept ? keep[t] : -1;
-      if (s >= 0 && s < a.src_cap) wt = a.weights[bh * a.src_cap + s];
     }
     if (IN_PLACE) cg::this_cluster().sync();   // every row of the wave is read
 #pragma unroll
@@ -449,47 +455,41 @@ __device__ __forceinline__ void move_section(const MoveArgs& a, int sect) {
       if (!u.v_codes) {
         uint8_t* p = a.dst + dst + u.off + u.row * u.row_bytes + u.chunk * 16;
         if (u.bytes == 16)
-          *reinterpret_cast<uint4*>(p) = v[i];
+          *reinterpret_cast<uint4*>(p) = v[i][0];
         else if (u.bytes == 8)
-          *reinterpret_cast<uint2*>(p) = make_uint2(v[i].x, v[i].y);
+          *reinterpret_cast<uint2*>(p) = make_uint2(v[i][0].x, v[i][0].y);
         else
-          *reinterpret_cast<uint16_t*>(p) = uint16_t(v[i].x);
+          *reinterpret_cast<uint16_t*>(p) = uint16_t(v[i][0].x);
       } else {
         const int units = u.row_bytes / 2, pair = u.row >> 1;
         uint8_t* p = a.dst + dst + u.off + pair * (2 * u.row_bytes) +
                      ((4 * u.chunk) ^ v_unit_swizzle(pair, units)) * 4;
-        if (live[i] == 3) {
-          *reinterpret_cast<uint4*>(p) = v[i];
+        // bytes of the first token from the first word's half, of the second from the second's
+        const uint32_t pick = ((live[i] & 4) ? 0x32u : 0x10u) | ((live[i] & 8) ? 0x7600u : 0x5400u);
+        const uint32_t w[4] = {__byte_perm(v[i][0].x, v[i][1].x, pick), __byte_perm(v[i][0].y, v[i][1].y, pick),
+                               __byte_perm(v[i][0].z, v[i][1].z, pick), __byte_perm(v[i][0].w, v[i][1].w, pick)};
+        if ((live[i] & 3) == 3) {
+          *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {   // one token of the pair alone: its 16-bit halves
-          const int e = live[i] >> 1;
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          const int e = (live[i] & 3) >> 1;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint16_t*>(p + 4 * k + 2 * e) = uint16_t(w[k] >> (16 * e));
         }
       }
     }
-    if (a.weights && sect == 0 && threadIdx.x < kTile && active) {
-      const int t = tile * kTile + threadIdx.x;
-      if (t < kept) a.to_weights[bh * a.dst_cap + t] = wt;
-    }
-    __syncthreads();   // (from is rewritten)
+    if (moves_weights && threadIdx.x < kTile && tile * kTile + threadIdx.x < kept)
+      a.to_weights[bh * a.dst_cap + tile * kTile + threadIdx.x] = wt;
   }
   // new tokens start at weight 0 (in place: after the last wave's barrier every source is read)
-  if (a.weights && sect == 0) {
+  if (moves_weights) {
     float* const w = a.to_weights + bh * a.dst_cap;
-    if (IN_PLACE) {
-      for (int t = kept + first_tile * kMoveThreads + threadIdx.x; t < a.dst_cap; t += kMoveCluster * kMoveThreads)
-        w[t] = 0.f;
-    } else if (threadIdx.x < kTile) {
-      const int t = first_tile * kTile + threadIdx.x;
-      if (t >= kept) w[t] = 0.f;
-    }
+    for (int t = kept + first_tile * kMoveThreads + threadIdx.x; t < a.dst_cap; t += step * kMoveThreads) w[t] = 0.f;
   }
 }
 
 template <int D, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const __grid_constant__ MoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_compact_kernel(const __grid_constant__ MoveArgs a) {
   const int sect = blockIdx.y;                       // 0: reference, 1 + l: loop l
   if (sect == 0)
     move_section<D, IN_PLACE, 0>(a, 0);
@@ -546,8 +546,10 @@ cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads,
     C *= 2;
   const int64_t per_cta = (int64_t(capacity) / C + 32 * kSelWarps + 31) / 32 * 32;
   a.slice = per_cta <= kSelKeys ? int(per_cta) : 0;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSelKeys * 4);
+  static OncePerDevice once;
+  const cudaError_t e = once([] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+  });
   if (e != cudaSuccess) return e;
   return launch_clusters(evict_select_kernel, dim3(unsigned(rows * C)), kSelThreads,
                          size_t(a.slice) * 4, C, stream, a);
@@ -577,12 +579,16 @@ cudaError_t launch_evict_compact(const rq_shape& s, const rq_cache& cache, const
   a.budget = budget;
   a.src_cap = s.capacity;
   a.dst_cap = ts.capacity;
-  // tiles that may hold kept rows (with weights: every tile, for the zeros)
   const int kept_most = budget < ts.capacity ? budget : ts.capacity;
-  a.tiles = weights ? ts.capacity / kTile : (kept_most + kTile - 1) / kTile;
+  const int tiles = (kept_most + kTile - 1) / kTile;
+  // four tiles per CTA hide the look-up of the sources behind the moves; fewer where that would
+  // leave SMs idle
+  const int64_t units = int64_t(s.batch) * s.n_kv_heads * s.n_loops;
+  const int per = units * ((tiles + 3) / 4) >= 8 * int64_t(device_sm_count()) ? 4 : 1;
+  a.ctas = (tiles + per - 1) / per;
   for (int l = 0; l < RQ_MAX_LOOPS; ++l) a.res_bits[l] = s.res_bits[l];
   const int64_t bh = int64_t(s.batch) * s.n_kv_heads;
-  const int64_t x = bh * (in_place ? kMoveCluster : a.tiles);
+  const int64_t x = bh * (in_place ? kMoveCluster : a.ctas);
   if (x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid{unsigned(x), unsigned(s.n_loops), 1u};
   if (in_place) {

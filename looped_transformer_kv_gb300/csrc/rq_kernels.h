@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/rq.h"
 
 namespace rq {
@@ -206,6 +208,21 @@ cudaError_t launch_evict_compact(const rq_shape& s, const rq_cache& cache, const
                                  cudaStream_t stream);
 
 int device_sm_count();
+
+// Runs `set` (kernel attributes) once per device; `done` is the caller's own static flags.
+struct OncePerDevice {
+  std::atomic<bool> done[64];
+  template <typename F>
+  cudaError_t operator()(F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if ((e = set()) == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // The argument checks of rq_decode_attention other than its workspace (C ABI layer).
 rq_status validate_decode(const rq_shape* shape, const rq_cache* cache, const uint16_t* q,

@@ -234,19 +234,22 @@ def chunk_workspace_bytes(shape, loop, n_new, max_ctx, window=0):
                                                    int(max_ctx), int(window)))
 
 
+_I3, _I5 = ctypes.c_int64 * 3, ctypes.c_int64 * 5
+
+
 def _chunk_args(shape, q, loop, kv_new, ctx_lens, max_ctx, out, ws, n_lens, weights, window, stream):
-    B, n, d = shape.batch, q.shape[1], shape.head_dim
-    assert q.dtype == torch.bfloat16 and tuple(q.shape) == (B, n, shape.n_q_heads, d)
-    assert kv_new.dtype == torch.bfloat16
-    assert tuple(kv_new.shape) == (B, n, 2, shape.n_loops, shape.n_kv_heads, d)
-    assert n == 0 or (q.stride(3) == 1 and kv_new.stride(5) == 1)
-    assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape
+    B, n, Hq, d = q.shape
+    H = shape.n_kv_heads
+    assert q.dtype == kv_new.dtype == out.dtype == torch.bfloat16
+    assert B == shape.batch and Hq == shape.n_q_heads and d == shape.head_dim
+    assert kv_new.shape == (B, n, 2, shape.n_loops, H, d)
+    qs, ks = q.stride(), kv_new.stride()
+    assert n == 0 or qs[3] == ks[5] == 1
+    assert out.is_contiguous() and out.shape == q.shape
     assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
-    assert weights is None or tuple(weights.shape) == (B, shape.n_kv_heads, shape.capacity)
-    qs = (ctypes.c_int64 * 3)(*[q.stride(i) for i in range(3)])
-    ks = (ctypes.c_int64 * 5)(*[kv_new.stride(i) for i in range(5)])
-    return (_ptr(q), qs, int(loop), _ptr(kv_new), ks, _i32(n_lens), int(n), _i32(ctx_lens),
-            int(max_ctx), _ptr(out), _f32(weights), int(window), _ptr(ws),
+    assert weights is None or weights.shape == (B, H, shape.capacity)
+    return (q.data_ptr(), _I3(*qs[:3]), loop, kv_new.data_ptr(), _I5(*ks[:5]), _i32(n_lens), n,
+            _i32(ctx_lens), max_ctx, out.data_ptr(), _f32(weights), window, ws.data_ptr(),
             ws.numel() * ws.element_size(), _stream(stream))
 
 
