@@ -46,6 +46,90 @@ __device__ __forceinline__ bool lens_of(const ChunkView& v, int b, int& n, int& 
   return n >= 0 && n <= v.n_new && ctx >= 0 && ctx <= v.max_ctx;
 }
 
+// --------------------------------------------------------------------------------- schedule
+
+// Rows and key tiles of row block `block` of a (sequence, kv-head): key tiles up to the block's last
+// row's own token.  A sequence with bad lengths has one tile (its outputs become NaN).
+struct BlockInfo {
+  int b, h, n, ctx, first, rows, tiles;   // first: the unit's first row (a window's), rows: behind it
+  bool ok;
+};
+__device__ __forceinline__ BlockInfo block_info(const ChunkView& v, int unit, int block, bool window) {
+  BlockInfo x;
+  x.h = unit % v.H;
+  x.b = v.b0 + unit / v.H;
+  x.ok = lens_of(v, x.b, x.n, x.ctx);
+  if (!x.ok) x.n = x.n < 0 || x.n > v.n_new ? v.n_new : x.n;
+  x.first = window ? max(0, x.n - v.window) * v.heads : 0;
+  x.rows = x.n * v.heads - x.first;
+  const int r0 = block * 2 * kRows;
+  const int j_last = (min(r0 + 2 * kRows, x.rows) - 1 + x.first) / v.heads;
+  x.tiles = r0 >= x.rows ? 0 : x.ok ? (x.ctx + j_last + kKeys) / kKeys : 1;
+  return x;
+}
+
+// The attention's work in one line: row blocks, the longest of every unit first, each block's set-up
+// (as long as about five key tiles) and its key tiles in order.  The line is cut evenly for one CTA
+// per SM; a cut close to a block's edge moves there, because a block that two CTAs share costs a
+// merge of their results.  A shorter line is cut for fewer CTAs, yet one for each block.
+constexpr int kSetup = 5, kSnap = 7;
+
+struct Schedule {
+  int pairs, grid;         // row blocks of all units, CTAs at most
+  int* at;                 // [pairs + 1] places of the pairs on the line: pair p is row block
+                           // blocks - 1 - p / units of unit p % units
+  int2* cut;               // [grid + 1] (place, pair) where each CTA starts
+};
+
+// key tile of a place on a pair's stretch
+__device__ __forceinline__ int tile_at(int place, int from) { return max(0, place - from - kSetup); }
+
+// One CTA of 256 threads.
+__device__ __forceinline__ void write_schedule(const ChunkView& v, const Schedule& s, int units, int blocks) {
+  __shared__ int sums[256];
+  const int per = (s.pairs + 255) / 256;
+  const int p0 = min(s.pairs, int(threadIdx.x) * per), p1 = min(s.pairs, p0 + per);
+  auto stretch = [&](int p) {
+    const int tiles = block_info(v, p % units, blocks - 1 - p / units, false).tiles;
+    return tiles ? tiles + kSetup : 0;
+  };
+  int sum = 0;
+  for (int p = p0; p < p1; ++p) sum += stretch(p);
+  sums[threadIdx.x] = sum;
+  __syncthreads();
+  int at = 0, total = 0;
+  for (int i = 0; i < 256; ++i) {
+    at += i < int(threadIdx.x) ? sums[i] : 0;
+    total += sums[i];
+  }
+  for (int p = p0; p < p1; ++p) {
+    s.at[p] = at;
+    at += stretch(p);
+  }
+  if (threadIdx.x == 0) s.at[s.pairs] = total;
+  __syncthreads();
+  const int ctas = max(1, min(s.grid, max(s.pairs, total / 8)));
+  for (int c = threadIdx.x; c <= s.grid; c += 256) {
+    int x = c >= ctas ? total : int(int64_t(c) * total / ctas);
+    int lo = 0, hi = s.pairs;              // the last pair at or before x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s.at[mid] <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int from = s.at[lo], to = s.at[lo + 1];
+    if (x < to && x > from) {
+      if (x - from <= kSnap && x - from <= to - x)
+        x = from;
+      else if (to - x <= kSnap)
+        x = to;
+    }
+    s.cut[c] = make_int2(x, lo);
+  }
+}
+
 // ---------------------------------------------------------------------------------- rebuild
 
 struct RebuildArgs {
@@ -61,6 +145,8 @@ struct RebuildArgs {
   int64_t ks0, ks1, kv_v, ks_h;
   int vec;                       // kv_new rows allow 16-byte loads
   uint8_t *k, *klo, *val;        // images [unit][tile][...]; klo may be null
+  Schedule schedule;             // the attention's; at may be null
+  int units, blocks;
 };
 
 // The residual levels s c + z of one word, as fp16 pairs of neighbouring channels (rounded once;
@@ -176,10 +262,14 @@ __device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int 
   if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
 }
 
-// Tiles of the chunk's own keys alone: one CTA each.  Rows are loaded 16 bytes a lane; V goes
+// Tiles of the chunk's own keys alone: one CTA each (and one for the attention's schedule).  Rows are loaded 16 bytes a lane; V goes
 // through shared memory to have channels as rows.  Bound by HBM latency.
 template <int D, bool KLO>
 __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant__ RebuildArgs a) {
+  if (blockIdx.x == gridDim.x - 1) {            // the attention's schedule
+    if (blockIdx.z == 0 && a.schedule.at) write_schedule(a.v, a.schedule, a.units, a.blocks);
+    return;
+  }
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
   constexpr int IMG = kKeys * D * 2, C = D / 8, IT = kKeys * C / 256;
@@ -687,9 +777,12 @@ struct AttnArgs {
   int qvec;                // q rows allow 16-byte loads
   const uint8_t *k, *klo, *val;
   uint16_t* out;
-  float* part;             // [unit][split][row tile] O images (below), or null: one split
-  float2* stats;           // [unit][split][padded row] (m, l): log2 units (LSE, or with part)
-  int n_splits, row_tiles; // row tiles (of 128) of a unit: stats' and part's
+  Schedule schedule;       // (SCHED)
+  float* part;             // O images (below) of shared blocks, by row tile: SCHED [2 CTA + (0 first,
+                           // 1 last)][2], else [unit][split][row_tiles]
+  float2* stats;           // (m, l) of their rows, and LSE's
+  int n_splits, row_tiles; // (not SCHED) row_tiles: of 128 rows, of a unit
+  int units, blocks;       // row blocks (of 256) of a unit
   float scale_log2;
 };
 
@@ -766,50 +859,96 @@ __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of w
     asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 
-// Two tiles of 128 query rows per CTA share every K and V tile.  Warps 0-3 and 4-7: softmax of
-// tile 0 and 1, a thread per row; warp 8: copies; warp 9: products.  While one tile's softmax
-// runs, the other's products do:  S_0 S_1 | P_0 V, S_0' | P_1 V, S_1' | ...
+// A CTA's work is one or more segments: a row block of 256 query rows (two tiles of 128) and a range
+// of its key tiles, every K and V tile shared by the two.  Warps 0-3 and 4-7: softmax of row tile 0
+// and 1, a thread per row; warp 8: copies; warp 9: products.  While one row tile's softmax runs, the
+// other's products do:  S_0 S_1 | P_0 V, S_0' | P_1 V, S_1' | ...
 // The running maximum m is raised only when a tile exceeds it by 2^8 (O is rescaled in tensor
 // memory then; P stays below 2^8); P overwrites S's columns.  The softmax warps take registers
 // from the others, so that a row's 128 scores stay in registers.
+// SCHED: the CTAs share the key tiles evenly (one CTA per SM): a block that lies in one CTA's range
+// is stored, the others leave their (m, l, O) for merge_kernel, at most two per CTA.  Else one CTA
+// takes one split of one row block.  Sharing evenly wins where a CTA gets many tiles (2048 tokens x
+// 4 heads after 14336: 321 + 21 us against 377 + 34 us and 134 MB left to merge), splits where it
+// gets few (a ragged first chunk of 1023: 44 us against 54, each segment's set-up counts).
 // LSE: scores with K in two parts, no P and V; (m, l) per row and split are stored.
-template <int D, bool LSE>
+template <int D, bool LSE, bool SCHED>
 __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t raw[];
   using L = AttnSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  // barriers: K full [3], V full [2], S ready [row tile][key tile % 2], P ready [2], Q ready, done.
-  // S of a key tile being ready also means that the values of the tile before are done, so the
-  // copies wait for it and need no barriers of their own (each commit stalls the products).
+  // barriers: K full [3], V full [2], S ready [row tile][2], P ready [2], Q ready, done.  S of a key
+  // tile being ready also means that the values of the tile before are done, so the copies wait
+  // for it and need no barriers of their own (each commit stalls the products).
   const uint32_t bar0 = smem_u32(bars);
-  auto kfull = [&](int s) { return bar0 + 8 * s; };
-  auto vfull = [&](int s) { return bar0 + 8 * (3 + s); };
-  auto sready = [&](int i, int j) { return bar0 + 8 * (5 + 2 * i + (j & 1)); };
+  auto kfull = [&](int g) { return bar0 + 8 * (g % 3); };
+  auto vfull = [&](int g) { return bar0 + 8 * (3 + (g & 1)); };
+  auto sready = [&](int i, int c) { return bar0 + 8 * (5 + 2 * i + (c & 1)); };
   auto pready = [&](int i) { return bar0 + 8 * (9 + i); };
   const uint32_t qready = bar0 + 8 * 11, done = bar0 + 8 * 12;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 13);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % a.n_splits;
-  const int64_t unit = blockIdx.x / a.n_splits;
-  const int h = int(unit % a.v.H), b = a.v.b0 + int(unit / a.v.H);
-  const int block = int(gridDim.y) - 1 - int(blockIdx.y);      // the longest row blocks of all units first
-  int n, ctx;
+  // the CTA's stretch [begin, end) of the line, and a pair at or before its start
+  int begin = 0, end = 0, pair = 0, split_kt = 0;
+  BlockInfo only{};                                          // (not SCHED) the CTA's row block
+  if constexpr (SCHED) {
+    const int2 cut = a.schedule.cut[blockIdx.x];
+    begin = cut.x;
+    pair = cut.y;
+    end = a.schedule.cut[blockIdx.x + 1].x;
+    if (begin == end) return;
+  } else {
+    pair = int(blockIdx.y) * a.units + int(blockIdx.x) / a.n_splits;
+    only = block_info(a.v, pair % a.units, a.blocks - 1 - pair / a.units, LSE);
+    const int split = int(blockIdx.x) % a.n_splits;
+    if (only.tiles == 0) return;
+    split_kt = int(int64_t(split) * only.tiles / a.n_splits);
+    end = int(int64_t(split + 1) * only.tiles / a.n_splits) - split_kt;
+  }
   // (one thread reads the error word: another CTA may be setting it)
   const bool flagged = __syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile unsigned*>(a.v.err) != 0u);
-  const bool ok = lens_of(a.v, b, n, ctx) && !flagged;
-  if (!ok) n = n < 0 || n > a.v.n_new ? a.v.n_new : n;
-  const int first = LSE ? max(0, n - a.v.window) * a.v.heads : 0;   // first row of the unit's rows
-  const int rows = n * a.v.heads - first;
-  const int r0 = block * 2 * kRows;
-  if (r0 >= rows) return;
-  const bool two = r0 + kRows < rows;                               // the second tile has rows
-  // key tiles of this split: of those up to the block's last row's own token
-  const int j_last = (min(r0 + 2 * kRows, rows) - 1 + first) / a.v.heads;
-  const int n_tiles = ok ? (ctx + j_last + kKeys) / kKeys : 0;
-  const int kt0 = int(int64_t(split) * n_tiles / a.n_splits), kt1 = int(int64_t(split + 1) * n_tiles / a.n_splits);
-  const int T = kt1 - kt0;
+
+  // Walks the CTA's segments in order: next() is false behind the last one.
+  struct Walk {
+    const AttnArgs& a;
+    int begin, x, end, p, split_kt, segments;
+    BlockInfo block;
+    int unit, r0, kt0, T;      // key tiles kt0 .. kt0 + T of the block
+    bool whole, at_begin, two;
+    __device__ __forceinline__ Walk(const AttnArgs& args, int begin_, int end_, int pair_, int split_kt_, const BlockInfo& only)
+        : a(args), begin(begin_), x(begin_), end(end_), p(pair_), split_kt(split_kt_), segments(0), block(only) {}
+    __device__ __forceinline__ void take(int pair) {
+      unit = pair % a.units;
+      r0 = (a.blocks - 1 - pair / a.units) * 2 * kRows;
+      if constexpr (SCHED) block = block_info(a.v, unit, a.blocks - 1 - pair / a.units, LSE);
+      two = r0 + kRows < block.rows;
+    }
+    __device__ __forceinline__ bool next() {
+      if constexpr (!SCHED) {  // one segment (an empty split's has no tiles)
+        if (segments++ > 0) return false;
+        take(p);
+        kt0 = split_kt;
+        T = end;
+        whole = !LSE && a.n_splits == 1;
+        return true;
+      }
+      while (x < end) {
+        while (a.schedule.at[p + 1] <= x) ++p;
+        const int from = a.schedule.at[p], to = a.schedule.at[p + 1], stop = min(end, to);
+        kt0 = tile_at(x, from);
+        T = tile_at(stop, from) - kt0;
+        whole = kt0 == 0 && stop == to;
+        at_begin = begin >= from;
+        x = stop;
+        if (T == 0) continue;  // (a stretch inside the block's set-up)
+        take(p);
+        return true;
+      }
+      return false;
+    }
+  };
 
   if (warp == 9) tc_alloc(smem_u32(tslot), 512);
   if (threadIdx.x == 0) {
@@ -828,132 +967,171 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const bool leader = elect_one();
-    if (warp == 8 && leader && T > 0) {                             // ---- copies
-      const uint8_t* k = a.k + (unit * a.v.tiles + kt0) * L::kTileBytes;
-      const uint8_t* v = (LSE ? a.klo : a.val) + (unit * a.v.tiles + kt0) * L::kTileBytes;
-      auto load_k = [&](int j) {
-        mbar_arrive_expect_tx(kfull(j % 3), L::kTileBytes);
-        bulk_g2s(smem_u32(smem + L::k + (j % 3) * L::kTileBytes), k + int64_t(j) * L::kTileBytes, L::kTileBytes, kfull(j % 3));
+    if (warp == 8 && leader && end > begin) {                       // ---- copies
+      // K and V run ahead of the scores: a walk each, in tiles from the CTA's first
+      Walk wk(a, begin, end, pair, split_kt, only), wv(wk), ws(wk);
+      wk.T = wv.T = ws.T = 0;
+      int nk = 0, nv = 0, jk = 0, jv = 0;                            // copies issued; tiles of the walk's segment
+      bool more_k = true, more_v = true;
+      auto load_k = [&]() {
+        if (jk == wk.T) {
+          jk = 0;
+          if (!(more_k = wk.next())) return;
+        }
+        const int64_t at = (int64_t(wk.unit) * a.v.tiles + wk.kt0 + jk++) * L::kTileBytes;
+        mbar_arrive_expect_tx(kfull(nk), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::k + (nk % 3) * L::kTileBytes), a.k + at, L::kTileBytes, kfull(nk));
+        ++nk;
       };
-      auto load_v = [&](int j) {
-        mbar_arrive_expect_tx(vfull(j & 1), L::kTileBytes);
-        bulk_g2s(smem_u32(smem + L::v + (j & 1) * L::kTileBytes), v + int64_t(j) * L::kTileBytes, L::kTileBytes, vfull(j & 1));
+      auto load_v = [&]() {
+        if (jv == wv.T) {
+          jv = 0;
+          if (!(more_v = wv.next())) return;
+        }
+        const int64_t at = (int64_t(wv.unit) * a.v.tiles + wv.kt0 + jv++) * L::kTileBytes;
+        mbar_arrive_expect_tx(vfull(nv), L::kTileBytes);
+        bulk_g2s(smem_u32(smem + L::v + (nv & 1) * L::kTileBytes), (LSE ? a.klo : a.val) + at, L::kTileBytes, vfull(nv));
+        ++nv;
       };
-      const int last_tile = two ? 1 : 0;
-      int nk = 0, nv = 0;                                            // copies issued
-      for (; nk < min(T, 3); ++nk) {
-        load_k(nk);
-        if (nk < 2) load_v(nv++);
+      for (int i = 0; i < 3 && more_k; ++i) {
+        load_k();
+        if (i < 2 && more_v) load_v();
       }
-      for (int j = 0; nv < T; ++j) {
-        // scores of tile j done, so the values of the tile before: room for K j + 3 and V j + 1
-        // (LSE: V holds K's low parts, done with the scores: j + 2)
-        if (!mbar_wait_bounded(sready(last_tile, j), (j >> 1) & 1, kTcWaitLimitNs)) break;
-        if (nk < T) load_k(nk++);
-        if (nv < min(T, j + (LSE ? 3 : 2))) load_v(nv++);
+      int c1 = 0, js = 0;                                            // tiles of row tile 1 so far (tile 0: g)
+      for (int g = 0; more_v; ++g) {
+        if (js == ws.T) {
+          js = 0;
+          if (!ws.next()) break;
+        }
+        ++js;
+        // scores of tile g done, so the values of the tile before: room for K g + 3 and V g + 1
+        // (LSE: V holds K's low parts, done with the scores: g + 2)
+        const int i = ws.two ? 1 : 0, ci = i ? c1 : g;
+        if (!mbar_wait_bounded(sready(i, ci), (ci >> 1) & 1, kTcWaitLimitNs)) {
+          failed = true;
+          break;
+        }
+        c1 += i;
+        if (more_k) load_k();
+        if (nv < g + (LSE ? 3 : 2)) load_v();
       }
-      failed = nv < T;
-      for (int j = max(0, nk - 3); j < nk; ++j) failed |= !mbar_wait_bounded(kfull(j % 3), (j / 3) & 1, kTcWaitLimitNs);
-      for (int j = max(0, nv - 2); j < nv; ++j) failed |= !mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1, kTcWaitLimitNs);
-    } else if (warp == 9 && leader && T > 0) {                      // ---- products
+      for (int j = max(0, nk - 3); j < nk; ++j) failed |= !mbar_wait_bounded(kfull(j), (j / 3) & 1, kTcWaitLimitNs);
+      for (int j = max(0, nv - 2); j < nv; ++j) failed |= !mbar_wait_bounded(vfull(j), (j >> 1) & 1, kTcWaitLimitNs);
+    } else if (warp == 9 && leader && end > begin) {                // ---- products
       constexpr uint32_t ids = f16_idesc(kRows, kKeys), ido = f16_idesc(kRows, D);
-      auto scores = [&](int i, int j) {
-        const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + (j % 3) * L::kTileBytes);
+      int c1 = 0, g = 0, seg = 0;                                    // tiles of row tile 1, of the CTA (and row tile 0); segments
+      bool good = true;
+      auto scores = [&](int i, int gk, int ci) {
+        const uint32_t q = smem_u32(smem + L::q + i * L::kTileBytes), k = smem_u32(smem + L::k + (gk % 3) * L::kTileBytes);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
           tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
                  panel_desc(k + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, x > 0);
         if (LSE) {
-          const uint32_t k2 = smem_u32(smem + L::v + (j & 1) * L::kTileBytes);
+          const uint32_t k2 = smem_u32(smem + L::v + (gk & 1) * L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
             tc_mma(tmem + 128 * i, panel_desc(q + (x / 4) * (kRows * 128) + (x % 4) * 32),
                    panel_desc(k2 + (x / 4) * (kKeys * 128) + (x % 4) * 32), ids, true);
         }
-        tc_commit(sready(i, j));
+        tc_commit(sready(i, ci));
       };
-      auto values = [&](int i, int s, bool add) {
-        const uint32_t v = smem_u32(smem + L::v + s * L::kTileBytes);
+      auto values = [&](int i, int gv, bool add) {
+        const uint32_t v = smem_u32(smem + L::v + (gv & 1) * L::kTileBytes);
 #pragma unroll
         for (int x = 0; x < kKeys / 16; ++x)
           tc_mma_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * x, panel_desc(v + (x / 4) * (D * 128) + (x % 4) * 32),
                     ido, add || x > 0);
       };
-      const int I = two ? 2 : 1;
-      bool good = mbar_wait_bounded(qready, 0, kTcWaitLimitNs) && mbar_wait_bounded(kfull(0), 0, kTcWaitLimitNs) &&
-                  (!LSE || mbar_wait_bounded(vfull(0), 0, kTcWaitLimitNs));
-      tc_fence_after();
-      if (good)
-        for (int i = 0; i < I; ++i) scores(i, 0);
-      for (int j = 0; j < T && good; ++j) {
-        const int s = j & 1;
-        if (!LSE) good = mbar_wait_bounded(vfull(s), (j >> 1) & 1, kTcWaitLimitNs);
-        if (good && j + 1 < T)
-          good = mbar_wait_bounded(kfull((j + 1) % 3), ((j + 1) / 3) & 1, kTcWaitLimitNs) &&
-                 (!LSE || mbar_wait_bounded(vfull(s ^ 1), ((j + 1) >> 1) & 1, kTcWaitLimitNs));
-        for (int i = 0; i < I && good; ++i) {
-          good = mbar_wait_bounded(pready(i), j & 1, kTcWaitLimitNs);
-          if (!good) break;
-          tc_fence_after();
-          if (!LSE) values(i, s, j > 0);
-          if (j + 1 < T) scores(i, j + 1);
+      auto k_there = [&](int gk) {
+        return mbar_wait_bounded(kfull(gk), (gk / 3) & 1, kTcWaitLimitNs) &&
+               (!LSE || mbar_wait_bounded(vfull(gk), (gk >> 1) & 1, kTcWaitLimitNs));
+      };
+      for (Walk w(a, begin, end, pair, split_kt, only); good && w.next(); ++seg) {
+        const int I = w.two ? 2 : 1;
+        good = k_there(g) && mbar_wait_bounded(qready, seg & 1, kTcWaitLimitNs);
+        tc_fence_after();
+        if (good)
+          for (int i = 0; i < I; ++i) scores(i, g, i ? c1 : g);
+        for (int j = 0; j < w.T && good; ++j, ++g) {
+          if (!LSE) good = mbar_wait_bounded(vfull(g), (g >> 1) & 1, kTcWaitLimitNs);
+          if (good && j + 1 < w.T) good = k_there(g + 1);
+          for (int i = 0; i < I && good; ++i) {
+            const int ci = i ? c1++ : g;
+            good = mbar_wait_bounded(pready(i), ci & 1, kTcWaitLimitNs);
+            if (!good) break;
+            tc_fence_after();
+            if (!LSE) values(i, g, j > 0);
+            if (j + 1 < w.T) scores(i, g + 1, ci + 1);
+          }
         }
+        tc_commit(done);
+        if (!good) mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs);   // nothing in flight
       }
-      tc_commit(done);
       failed = !good;
-      if (!good) mbar_wait_bounded(done, 0, kTcWaitLimitNs);         // nothing in flight
     }
     __syncwarp();
   } else {                                                           // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int i = warp >> 2, r = threadIdx.x & (kRows - 1);
-    const int row = r0 + i * kRows + r;
-    const bool valid = row < rows;
     const uint32_t lanes = uint32_t(warp & 3) << 21;                 // this warp's tensor-memory lanes
     const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
     int* const exps = reinterpret_cast<int*>(smem + L::exps) + i * kRows;
-    float m = -INFINITY, l = 0.f;
-    if (T > 0) {
-      store_queries<D>(
-          [&](int rr) -> const uint16_t* {
-            const int x = r0 + i * kRows + rr;
-            if (x >= rows) return nullptr;
-            const int j = (x + first) / a.v.heads, g = (x + first) % a.v.heads;
-            return a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.v.heads + g) * a.qs2;
-          },
-          a.qvec, smem + L::q + i * L::kTileBytes, exps, (warp & 3) * 32, lane);
-      fence_async_smem();
-      mbar_arrive(qready);
-      const float c = ldexpf(a.scale_log2, -exps[r]);
-      const int lim = ctx + min((row + first) / a.v.heads, n - 1);   // last key the row sees
-      const int clear = ctx + min((r0 + i * kRows + first) / a.v.heads, n - 1);   // every row of the tile sees these
-      if (i == 0 || two) {
-        for (int jt = 0; jt < T; ++jt) {
-          if (!mbar_wait_bounded(sready(i, jt), (jt >> 1) & 1, kTcWaitLimitNs)) {
+    uint8_t* const img = smem + L::q + i * L::kTileBytes;            // queries, then results going out
+    int ci = 0, seg = 0;
+    for (Walk w(a, begin, end, pair, split_kt, only); !failed && w.next(); ++seg) {
+      const BlockInfo& x = w.block;
+      const int row = w.r0 + i * kRows + r;
+      const bool valid = row < x.rows;
+      float m = -INFINITY, l = 0.f;
+      if (w.T > 0) {
+        if (i == 0 || w.two)
+          store_queries<D>(
+              [&](int rr) -> const uint16_t* {
+                const int y = w.r0 + i * kRows + rr;
+                if (y >= x.rows) return nullptr;
+                const int j = (y + x.first) / a.v.heads, g = (y + x.first) % a.v.heads;
+                return a.q + x.b * a.qs0 + j * a.qs1 + (int64_t(x.h) * a.v.heads + g) * a.qs2;
+              },
+              a.qvec, img, exps, (warp & 3) * 32, lane);
+        fence_async_smem();
+        mbar_arrive(qready);
+      }
+      if (i == 1 && !w.two) {    // no rows: only keeps step with the segments
+        if (SCHED) failed = __any_sync(RQ_FULL_MASK, !mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs));
+        continue;
+      }
+      if (w.T > 0) {
+        const float c = ldexpf(a.scale_log2, -exps[r]);
+        const int lim = x.ctx + min((row + x.first) / a.v.heads, x.n - 1);   // last key the row sees
+        const int clear = x.ctx + min((w.r0 + i * kRows + x.first) / a.v.heads, x.n - 1);   // every row of the tile sees these
+        for (int jt = 0; jt < w.T; ++jt, ++ci) {
+          if (!mbar_wait_bounded(sready(i, ci), (ci >> 1) & 1, kTcWaitLimitNs)) {
             failed = true;
             break;
           }
           tc_fence_after();
           uint32_t s[kKeys];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) tc_ld32(tS + 32 * x, s + 32 * x);
+          for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
           tc_wait_ld();
-          const int key0 = (kt0 + jt) * kKeys;
+          const int key0 = (w.kt0 + jt) * kKeys;
           if (key0 + kKeys - 1 > clear) {
             const int rel = lim - key0;
 #pragma unroll
-            for (int x = 0; x < kKeys; ++x)
-              if (x > rel) s[x] = 0xff800000u;
+            for (int y = 0; y < kKeys; ++y)
+              if (y > rel) s[y] = 0xff800000u;
           }
           float mx[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
+          for (int y = 0; y < 4; ++y) mx[y] = __uint_as_float(s[y]);
 #pragma unroll
-          for (int x = 4; x < kKeys; x += 8)
+          for (int y = 4; y + 4 < kKeys; y += 8)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              mx[y] = x + 4 + y < kKeys ? fmaxf(mx[y], fmaxf(__uint_as_float(s[x + y]), __uint_as_float(s[min(x + 4 + y, kKeys - 1)])))
-                                        : fmaxf(mx[y], __uint_as_float(s[x + y]));
+            for (int z = 0; z < 4; ++z)
+              mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
+#pragma unroll
+          for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           if (__any_sync(RQ_FULL_MASK, mt > m + kSlack)) {
             const float mn = mt > m + kSlack ? mt : m;
@@ -962,13 +1140,13 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
             m = mn;
             if (!LSE && jt > 0) {
 #pragma unroll 1
-              for (int x = 0; x < D / 16; ++x) {
+              for (int y = 0; y < D / 16; ++y) {
                 uint32_t o[16];
-                tc_ld16(tO + 16 * x, o);
+                tc_ld16(tO + 16 * y, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                tc_st16(tO + 16 * x, o);
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                tc_st16(tO + 16 * y, o);
               }
             }
           }
@@ -979,14 +1157,14 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
           for (int half = 0; half < 2; ++half) {
             uint32_t p[32];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int k = half * 64 + 2 * x;
+            for (int y = 0; y < 32; ++y) {
+              const int k = half * 64 + 2 * y;
               float p0, p1;
               unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, m2), p0, p1);
               p0 = ex2(p0);
               p1 = ex2(p1);
-              sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
-              if (!LSE) p[x] = pack_half2(p0, p1);
+              sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+              if (!LSE) p[y] = pack_half2(p0, p1);
             }
             if (!LSE) tc_st32(tS + 32 * half, p);
           }
@@ -997,92 +1175,98 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
           tc_fence_before();
           mbar_arrive(pready(i));
         }
-        if (!LSE && !failed) failed = !mbar_wait_bounded(done, 0, kTcWaitLimitNs);
-      }
-    }
-    // ---- store (a wait that gave up: NaN)
-    const bool gave_up = __any_sync(RQ_FULL_MASK, failed);
-    const float nan = __int_as_float(0x7fc00000);
-    const int j = (row + first) / a.v.heads;
-    const bool bad = !ok || gave_up || (valid && j >= a.v.first_bad[int64_t(b) * a.v.H + h]);
-    if ((i == 0 || two) && (LSE || a.part)) {
-      const int64_t tile = (unit * a.n_splits + split) * a.row_tiles + block * 2 + i;
-      if (valid) a.stats[tile * kRows + r] = bad ? make_float2(0.f, nan) : make_float2(m, l);
-      if (!LSE) {
-        uint8_t* const img = smem + (i == 0 ? L::q : L::k);          // (every product and copy is done)
+        if (!failed && (!LSE || SCHED)) failed = !mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs);
+        failed = __any_sync(RQ_FULL_MASK, failed);
         tc_fence_after();
+      }
+      // ---- store (a wait that gave up: NaN)
+      const float nan = __int_as_float(0x7fc00000);
+      const bool there = w.T > 0 && !failed;                         // O holds the segment's sums
+      const int j = (row + x.first) / a.v.heads;
+      const bool bad = !x.ok || flagged || failed || (valid && j >= a.v.first_bad[int64_t(x.b) * a.v.H + x.h]);
+      if (LSE) {
+        const int64_t tile = (int64_t(w.unit) * a.n_splits + blockIdx.x % a.n_splits) * a.row_tiles + w.r0 / kRows + i;
+        if (valid) a.stats[tile * kRows + r] = bad ? make_float2(0.f, nan) : make_float2(m, l);
+      } else if (!w.whole) {
+        const int64_t tile = SCHED ? (2 * int64_t(blockIdx.x) + (w.at_begin ? 0 : 1)) * 2 + i
+                                   : (int64_t(w.unit) * a.n_splits + blockIdx.x % a.n_splits) * a.row_tiles + w.r0 / kRows + i;
+        a.stats[tile * kRows + r] = bad ? make_float2(0.f, nan) : make_float2(m, l);
+        constexpr int HALF = D / 2;                                  // channels that fit the image at a time
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t w[32];
-          if (T > 0 && !gave_up) {
-            tc_ld32(tO + 32 * x, w);
+          for (int y = 0; y < HALF / 32; ++y) {
+            uint32_t o[32];
+#pragma unroll
+            for (int z = 0; z < 32; ++z) o[z] = 0u;
+            if (there) {
+              tc_ld32(tO + half * HALF + 32 * y, o);
+              tc_wait_ld();
+            }
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              *reinterpret_cast<uint4*>(img + o_image_offset<HALF>(r, 8 * y + z)) =
+                  make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+          }
+          fence_async_smem();
+          warpgroup_barrier(i);
+          if (r == 0) {
+            bulk_s2g(a.part + (tile * 2 + half) * (kRows * HALF), smem_u32(img), kRows * HALF * 4);
+            bulk_s2g_commit();
+            bulk_s2g_wait_read();                                    // (the image may be written again)
+          }
+          warpgroup_barrier(i);
+        }
+      } else {
+        constexpr int CR = D / 8;                                    // 16-byte chunks of a row of bf16
+        const float inv = bad ? nan : 1.f / l;
+#pragma unroll 1
+        for (int y = 0; y < D / 32; ++y) {
+          uint32_t o[32];
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] = 0u;
+          if (there) {
+            tc_ld32(tO + 32 * y, o);
             tc_wait_ld();
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) w[y] = 0u;
           }
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            *reinterpret_cast<uint4*>(img + o_image_offset<D>(r, 8 * x + y)) =
-                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
-        }
-        fence_async_smem();
-        warpgroup_barrier(i);
-        if (r == 0) {
-          bulk_s2g(a.part + tile * (kRows * D), smem_u32(img), kRows * D * 4);
-          bulk_s2g_commit();
-          bulk_s2g_wait();
-        }
-      }
-    } else if (!LSE && (i == 0 || two)) {
-      uint8_t* const img = smem + L::q + i * L::kTileBytes;          // 128 rows of D bf16
-      constexpr int CR = D / 8;                                      // 16-byte chunks of a row
-      const float inv = bad ? nan : 1.f / l;
-      tc_fence_after();
+          for (int z = 0; z < 4; ++z) {
+            uint32_t p[4];
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t w[32];
-        if (T > 0 && !gave_up) {
-          tc_ld32(tO + 32 * x, w);
-          tc_wait_ld();
-        } else {
-#pragma unroll
-          for (int y = 0; y < 32; ++y) w[y] = 0u;
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t p[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(w[8 * y + 2 * k]) * inv,
-                                                          __uint_as_float(w[8 * y + 2 * k + 1]) * inv);
-            p[k] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * z + 2 * k]) * inv,
+                                                            __uint_as_float(o[8 * z + 2 * k + 1]) * inv);
+              p[k] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(img + r * (D * 2) + (((4 * y + z) ^ (r & (CR - 1))) << 4)) =
+                make_uint4(p[0], p[1], p[2], p[3]);
           }
-          *reinterpret_cast<uint4*>(img + r * (D * 2) + (((4 * x + y) ^ (r & (CR - 1))) << 4)) =
-              make_uint4(p[0], p[1], p[2], p[3]);
         }
-      }
-      __syncwarp();
-      const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+        __syncwarp();
+        const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll 4
-      for (int k = lane; k < 32 * CR; k += 32) {                     // this warp's rows, 16 bytes a lane
-        const int rr = (warp & 3) * 32 + k / CR, cc = k % CR, x = r0 + i * kRows + rr;
-        if (x >= rows) continue;
-        const uint4 w = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
-        uint16_t* const o = a.out + ((int64_t(b) * a.v.n_new + x / a.v.heads) * a.v.H * a.v.heads +
-                                     h * a.v.heads + x % a.v.heads) * D + 8 * cc;
-        if (vec) {
-          *reinterpret_cast<uint4*>(o) = w;
-        } else {
-          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+        for (int k = lane; k < 32 * CR; k += 32) {                   // this warp's rows, 16 bytes a lane
+          const int rr = (warp & 3) * 32 + k / CR, cc = k % CR, y = w.r0 + i * kRows + rr;
+          if (y >= x.rows) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
+          uint16_t* const o = a.out + ((int64_t(x.b) * a.v.n_new + y / a.v.heads) * a.v.H * a.v.heads +
+                                       x.h * a.v.heads + y % a.v.heads) * D + 8 * cc;
+          if (vec) {
+            *reinterpret_cast<uint4*>(o) = v;
+          } else {
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[2 * e] = uint16_t(q[e]);
-            o[2 * e + 1] = uint16_t(q[e] >> 16);
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = uint16_t(q[e]);
+              o[2 * e + 1] = uint16_t(q[e] >> 16);
+            }
           }
         }
+        __syncwarp();                                                // (the next queries overwrite the rows)
       }
+      tc_fence_before();
     }
+    if (r == 0) bulk_s2g_wait();
   }
   if (__syncthreads_or(failed) && threadIdx.x == 0) atomicOr(a.v.err, 1u);
   tc_fence_before();
@@ -1090,48 +1274,79 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
   if (warp == 9) tc_free(tmem, 512);
 }
 
-// One warp per row: merge the splits' (m, l, O).
-template <int D>
-__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int P = D / 32;
+// The row blocks that several CTAs share: 8 CTAs of 32 rows for each row block and unit (SCHED: for
+// each cut, the first one inside a row block acts), a warp for four rows at a time.
+template <int D, bool SCHED>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int P = D / 32, HALF = D / 2;
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
-  const int j = row / a.v.heads, g = row % a.v.heads;
-  int n = a.v.n_lens ? a.v.n_lens[b] : a.v.n_new;
-  if (n < 0 || n > a.v.n_new) n = a.v.n_new;
-  if (j >= n) return;
-  const int64_t unit = int64_t(blockIdx.z) * a.v.H + h;
-  const int64_t tile0 = unit * a.n_splits * a.row_tiles + row / kRows;
-  const int r = row % kRows;
-  float M = -INFINITY, l = 0.f, o[P];
+  int p = blockIdx.x, from = 0, to = a.n_splits, start = 0, stop = 1;
+  const int c = SCHED ? int(blockIdx.x) + 1 : 1;             // CTAs (splits) c - 1 .. have parts
+  if constexpr (SCHED) {
+    const int2 cut = a.schedule.cut[c];
+    p = cut.y;
+    start = a.schedule.cut[c - 1].x;
+    stop = cut.x;
+    from = a.schedule.at[p];
+    to = a.schedule.at[p + 1];
+    if (stop <= from || stop >= to || start > from) return;
+  }
+  const int unit = p % a.units, block = a.blocks - 1 - p / a.units;
+  const BlockInfo info = block_info(a.v, unit, block, false);
+  const bool flagged = *reinterpret_cast<volatile unsigned*>(a.v.err) != 0u;
+  const int local = blockIdx.y * 32 + (threadIdx.x >> 5) * 4;        // four rows
+  const int i = local / kRows;
+  if (block * 2 * kRows + local >= info.rows) return;
+  float M[4], l[4], o[4][P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) o[i] = 0.f;
-  for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, a.stats[(tile0 + int64_t(s) * a.row_tiles) * kRows + r].x);
-#pragma unroll 4
-  for (int s = 0; s < a.n_splits; ++s) {
-    const int64_t tile = tile0 + int64_t(s) * a.row_tiles;
-    const float2 st = a.stats[tile * kRows + r];
-    if (st.x == -INFINITY) continue;
-    const float f = ex2(st.x - M);
-    l = fmaf(f, st.y, l);
-    const uint8_t* img = reinterpret_cast<const uint8_t*>(a.part + tile * (kRows * D));
-    if constexpr (D == 128) {
-      const float4 v = *reinterpret_cast<const float4*>(img + o_image_offset<D>(r, lane));
-      o[0] = fmaf(f, v.x, o[0]);
-      o[1] = fmaf(f, v.y, o[1]);
-      o[2] = fmaf(f, v.z, o[2]);
-      o[3] = fmaf(f, v.w, o[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(img + o_image_offset<D>(r, lane / 2) + (lane & 1) * 8);
-      o[0] = fmaf(f, v.x, o[0]);
-      o[1] = fmaf(f, v.y, o[1]);
+  for (int k = 0; k < 4; ++k) {
+    M[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < P; ++e) o[k][e] = 0.f;
+  }
+  // CTA s has [start, stop) of the line
+  for (int s = c - 1; start < to; ++s, start = stop, stop = !SCHED ? s + 1 : start < to ? a.schedule.cut[s + 1].x : start) {
+    const int64_t tile = SCHED ? (2 * int64_t(s) + (start >= from ? 0 : 1)) * 2 + i
+                               : (int64_t(unit) * a.n_splits + s) * a.row_tiles + block * 2 + i;
+    // lane's channels P lane ..: in the half-row image lane / 16
+    const uint8_t* img = reinterpret_cast<const uint8_t*>(a.part + (tile * 2 + lane / 16) * (kRows * HALF));
+    const int byte = (lane % 16) * P * 4;
+    float2 st[4];
+    float v[4][P];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = (local + k) % kRows;
+      st[k] = a.stats[tile * kRows + r];
+      const uint8_t* src = img + o_image_offset<HALF>(r, byte / 16) + byte % 16;
+      if constexpr (P == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        v[k][0] = y.x, v[k][1] = y.y, v[k][2] = y.z, v[k][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        v[k][0] = y.x, v[k][1] = y.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (st[k].x == -INFINITY) continue;
+      const float m = fmaxf(M[k], st[k].x), f0 = ex2(M[k] - m), f = ex2(st[k].x - m);
+      M[k] = m;
+      l[k] = fmaf(l[k], f0, f * st[k].y);
+#pragma unroll
+      for (int e = 0; e < P; ++e) o[k][e] = fmaf(o[k][e], f0, f * v[k][e]);
     }
   }
-  uint16_t* out = a.out + ((int64_t(b) * a.v.n_new + j) * a.v.H * a.v.heads + h * a.v.heads + g) * D + lane * P;
-  const float inv = *reinterpret_cast<volatile unsigned*>(a.v.err) ? __int_as_float(0x7fc00000) : 1.f / l;
 #pragma unroll
-  for (int i = 0; i < P; ++i) out[i] = float_to_bf16_bits(o[i] * inv);
+  for (int k = 0; k < 4; ++k) {
+    const int row = block * 2 * kRows + local + k;
+    if (row >= info.rows) break;
+    const int j = row / a.v.heads, g = row % a.v.heads;
+    uint16_t* out = a.out + ((int64_t(info.b) * a.v.n_new + j) * a.v.H * a.v.heads + info.h * a.v.heads + g) * D + lane * P;
+    const float inv = flagged ? __int_as_float(0x7fc00000) : 1.f / l[k];
+#pragma unroll
+    for (int e = 0; e < P; ++e) out[e] = float_to_bf16_bits(o[k][e] * inv);
+  }
 }
 
 // ---------------------------------------------------------------------------------- weights
@@ -1349,9 +1564,12 @@ constexpr size_t kGroupBytes = size_t(4) << 30;   // images of the sequences han
 
 struct TcLayout {
   int group;               // sequences handled together
-  int tiles, rows, r_tiles, wrows, q_tiles, splits, wsplits;
-  size_t first_bad, k, klo, val, part, stats, qimg, scale, total;
+  int tiles, blocks, r_tiles, wblocks, q_tiles, splits, wsplits, ctas;   // ctas: of the scheduled attention, or 0
+  size_t first_bad, schedule, k, klo, val, part, stats, qimg, scale, total;
 };
+
+constexpr int kMaxPairs = 8192;   // scheduled row blocks, at most: more keep every SM busy as they are
+constexpr int kMinShare = 64;     // key tiles per CTA from which they are shared evenly
 
 // Splits of the keys so that the CTAs (one per SM) come in few, even waves: least
 // waves x (tiles per split + set-up), the set-up worth about two tiles.
@@ -1374,32 +1592,40 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   TcLayout l;
   const int heads = s.n_q_heads / s.n_kv_heads, D = s.head_dim;
   l.tiles = int((int64_t(max_ctx) + n_new + kKeys - 1) / kKeys);
-  l.rows = n_new * heads;
-  l.wrows = window * heads;
-  l.r_tiles = (l.rows + kRows - 1) / kRows;
-  l.q_tiles = (l.wrows + kRows - 1) / kRows;
+  const int rows = n_new * heads, wrows = window * heads;
+  l.blocks = (rows + 2 * kRows - 1) / (2 * kRows);
+  l.wblocks = (wrows + 2 * kRows - 1) / (2 * kRows);
+  l.q_tiles = (wrows + kRows - 1) / kRows;
   const size_t tile = size_t(kKeys) * D * 2;
   const size_t seq = size_t(s.n_kv_heads) * l.tiles * tile * (window ? 3 : 2);
   const size_t fit = kGroupBytes / (seq ? seq : 1);
   l.group = int(fit < 1 ? 1 : (fit > size_t(s.batch) ? size_t(s.batch) : fit));
   const size_t units = size_t(l.group) * s.n_kv_heads;
-  const int64_t ctas = int64_t(units) * ((l.rows + 2 * kRows - 1) / (2 * kRows));
-  l.splits = plan_tc_splits(ctas, l.tiles);
-  l.wsplits = window ? plan_tc_splits(int64_t(units) * ((l.wrows + 2 * kRows - 1) / (2 * kRows)), l.tiles) : 1;
+  const int64_t pairs = int64_t(units) * l.blocks;
+  const int64_t work = pairs * l.tiles;
+  l.ctas = pairs <= kMaxPairs && work >= int64_t(kMinShare) * device_sm_count() && work < (int64_t(1) << 29)
+               ? device_sm_count() : 0;
+  l.splits = l.ctas ? 1 : plan_tc_splits(pairs, l.tiles);
+  l.r_tiles = (rows + kRows - 1) / kRows;
+  l.wsplits = window ? plan_tc_splits(int64_t(units) * l.wblocks, l.tiles) : 1;
   size_t o = kWsHeaderBytes;
   l.first_bad = o;
   o = round1k(o + size_t(s.batch) * s.n_kv_heads * 4);
+  l.schedule = o;
+  if (l.ctas) o = round1k(o + (size_t(l.ctas) + 1) * 8 + (size_t(pairs) + 1) * 4);
   l.k = o;
   o += units * l.tiles * tile;
   l.val = o;
   o += units * l.tiles * tile;
   l.klo = o;
   if (window) o += units * l.tiles * tile;
+  // row tiles of shared blocks
+  const size_t shared = l.ctas ? size_t(l.ctas) * 4 : l.splits > 1 ? units * l.splits * l.r_tiles : 0;
   l.part = o;
-  if (l.splits > 1) o += units * l.r_tiles * l.splits * (size_t(kRows) * D * 4);
-  l.stats = o;   // of the outputs' splits, then of the window's
-  const size_t st = l.splits > 1 ? size_t(l.r_tiles) * l.splits : 0, wst = size_t(l.q_tiles) * l.wsplits;
-  o += units * (st > wst ? st : wst) * kRows * 8;
+  o += shared * (size_t(kRows) * D * 4);
+  l.stats = o;   // of the shared blocks, then of the window's rows
+  const size_t wst = units * l.q_tiles * l.wsplits;
+  o += (shared > wst ? shared : wst) * kRows * 8;
   l.qimg = o;
   o += units * l.q_tiles * (size_t(kRows) * D * 2);
   l.scale = o;
@@ -1444,8 +1670,9 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
     if ((x = cudaFuncSetAttribute(chunk_image_kernel<D, true>, smem, 3 * kKeys * D * 2 + 128)) != cudaSuccess ||
         (x = cudaFuncSetAttribute(chunk_image_kernel<D, false>, smem, 2 * kKeys * D * 2 + 128)) != cudaSuccess ||
-        (x = cudaFuncSetAttribute(attention_kernel<D, false>, smem, AS::total)) != cudaSuccess ||
-        (x = cudaFuncSetAttribute(attention_kernel<D, true>, smem, AS::total)) != cudaSuccess)
+        (x = cudaFuncSetAttribute(attention_kernel<D, false, false>, smem, AS::total)) != cudaSuccess ||
+        (x = cudaFuncSetAttribute(attention_kernel<D, false, true>, smem, AS::total)) != cudaSuccess ||
+        (x = cudaFuncSetAttribute(attention_kernel<D, true, false>, smem, AS::total)) != cudaSuccess)
       return x;
     return cudaFuncSetAttribute(weights_kernel<D>, smem, WS::total);
   });
@@ -1492,7 +1719,13 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
             r.kv_v % 8 == 0 && r.ks_h % 8 == 0;
     r.old_tiles = (c.max_ctx + kKeys - 1) / kKeys;
     if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, stream)) != cudaSuccess) return e;
-    const dim3 own(unsigned((c.n_new + kKeys - 1) / kKeys) * H, 1, nb);
+    r.units = int(nb * H);
+    r.blocks = l.blocks;
+    r.schedule.pairs = r.units * r.blocks;
+    r.schedule.grid = l.ctas;
+    r.schedule.cut = reinterpret_cast<int2*>(w + l.schedule);
+    r.schedule.at = l.ctas ? reinterpret_cast<int*>(w + l.schedule + (size_t(l.ctas) + 1) * 8) : nullptr;
+    const dim3 own(unsigned((c.n_new + kKeys - 1) / kKeys) * H + 1, 1, nb);
     if (c.window)
       chunk_image_kernel<D, true><<<own, 256, 3 * kKeys * D * 2 + 128, stream>>>(r);
     else
@@ -1508,24 +1741,30 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     a.klo = r.klo;
     a.val = r.val;
     a.out = c.out;
-    a.part = l.splits > 1 ? reinterpret_cast<float*>(w + l.part) : nullptr;
+    a.schedule = r.schedule;
+    a.part = reinterpret_cast<float*>(w + l.part);
     a.stats = reinterpret_cast<float2*>(w + l.stats);
     a.n_splits = l.splits;
     a.row_tiles = l.r_tiles;
+    a.units = r.units;
+    a.blocks = l.blocks;
     a.qvec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.qs0 % 8 == 0 && a.qs1 % 8 == 0 && a.qs2 % 8 == 0;
     a.scale_log2 = scale;
-    const unsigned blocks = unsigned((l.rows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, false><<<dim3(nb * H * l.splits, blocks, 1), 384, AS::total, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (l.splits > 1) {
-      merge_kernel<D><<<dim3(unsigned((l.rows + 3) / 4), H, nb), 128, 0, stream>>>(a);
+    if (l.ctas) {
+      attention_kernel<D, false, true><<<unsigned(l.ctas), 384, AS::total, stream>>>(a);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if (l.ctas > 1) merge_kernel<D, true><<<dim3(unsigned(l.ctas - 1), 2 * kRows / 32), 256, 0, stream>>>(a);
+    } else {
+      attention_kernel<D, false, false><<<dim3(nb * H * l.splits, unsigned(l.blocks)), 384, AS::total, stream>>>(a);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if (l.splits > 1) merge_kernel<D, false><<<dim3(nb * H * l.blocks, 2 * kRows / 32), 256, 0, stream>>>(a);
     }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!c.window) continue;
     a.n_splits = l.wsplits;
     a.row_tiles = l.q_tiles;
-    const unsigned wblocks = unsigned((l.wrows + 2 * kRows - 1) / (2 * kRows));
-    attention_kernel<D, true><<<dim3(nb * H * l.wsplits, wblocks, 1), 384, AS::total, stream>>>(a);
+    a.blocks = l.wblocks;
+    attention_kernel<D, true, false><<<dim3(nb * H * l.wsplits, unsigned(l.wblocks)), 384, AS::total, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     WeightArgs x;
     x.v = v;

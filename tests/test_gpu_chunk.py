@@ -350,3 +350,41 @@ def test_many_rows(case, window):
     c.call()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("d,Hq,ctx,lens", [(128, 16, [0, 130], [4096, 3001]), (64, 12, [257, 1], [4000, 4096])])
+def test_long_chunks_shared_evenly(d, Hq, ctx, lens):
+    """Enough key tiles that the CTAs share them evenly, across row blocks; the reference on the GPU."""
+    B, H = 2, 2
+    c = Case(B, Hq, H, d, (2,), ctx, 4096, lens, seed=d, window=3)
+    c.call()
+    torch.cuda.synchronize()
+    assert c.error_word() == 0
+    G = Hq // H
+    for b, h in itertools.product(range(B), range(H)):
+        m, n0 = lens[b], ctx[b]
+        assert (c.out[b, m:, h * G:(h + 1) * G] == 776.0).all()
+        rec = c.records(b, h)
+        k, v = (torch.cat([
+            torch.from_numpy(R.rebuild(rec, n0, d, c.bits, 0, kv, c.signs[kv, h].numpy())),
+            c.new_host[b, :m, kv, 0, h].double()]).cuda() for kv in (0, 1))
+        rk, rv = (torch.cat([torch.from_numpy(R.residual_norms(rec, n0, d, c.bits, 0, kv)),
+                             torch.zeros(m).double()]).cuda() for kv in (0, 1))
+        late = torch.arange(n0 + m, device="cuda").view(1, -1) > n0 + torch.arange(m, device="cuda").view(-1, 1)
+        added = torch.zeros(n0 + m, dtype=torch.float64, device="cuda")
+        for g in range(G):
+            q = c.q[b, :m, h * G + g].double()
+            s = (q @ k.T * d ** -0.5).masked_fill(late, -float("inf"))
+            p = torch.softmax(s, -1)
+            added += p[-3:].sum(0)
+            ref, got = p @ v, c.out[b, :m, h * G + g].double()
+            # the bound of Case.check, its largest score error over all keys
+            mag = (q.abs() @ k.abs().T * d ** -0.5).amax(-1, keepdim=True)
+            e = HALF16 * (2 * mag + 4 * q.norm(dim=-1, keepdim=True) * rk.max() * d ** -0.5)
+            tol = (p @ v.abs()) * (torch.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[:, None]
+            tol += HALFB * ref.abs() * 1.01 + 1e-30
+            assert ((got - ref).abs() <= tol).all(), (b, h, g, ((got - ref).abs() / tol).max().item())
+        got = c.weights[b, h].double() - c.w0[b, h].double().cuda()
+        # (weights: fp32 additions to values below 1, 2^-24 each, and the scores' 21 bits)
+        assert (got[:n0 + m] - added).abs().max().item() <= 2.0 ** -23 + 3 * G * 2e-4 * added.max().item()
+        assert (got[n0 + m:] == 0).all()
