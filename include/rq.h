@@ -248,7 +248,8 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  *              lies behind a sequence's last token is never used), or NULL: n_new each
  *   n_new      >= 0 (0: nothing enqueued)
  *   ctx_lens, max_ctx  as in rq_decode_attention (max_ctx may be 0)
- *   out        bf16 [B][n_new][Hq][d]; rows behind a sequence's last token are left as they were
+ *   out        bf16 [B][n_new][Hq][d]; rows behind a sequence's last token are left as they were;
+ *              it must not overlap q's or kv_new's span (RQ_ERR_INVALID_ARG)
  *   weights    fp32 [B][Hkv][capacity], or NULL: the softmax weights of the last `window` new
  *              tokens of each sequence (all of them if it has fewer), summed over their query
  *              heads of the kv-head, are added: weights[b][h][t] += sum P for cached slots
@@ -259,8 +260,10 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  *              is the call's error word, as in rq_decode_attention: nonzero after a device-side
  *              ctx_len outside [0, max_ctx], an n_len outside [0, n_new] (taken as n_new), a bad
  *              block-table entry, or a pipeline wait that gave up.  The call's outputs are then
- *              NaN, and its weights not to be used.  Calls that share a workspace must not
- *              overlap on the GPU.
+ *              NaN (after a wait that gave up, at least those of the rows it served), and its
+ *              weights not to be used.  Calls that share a workspace must not overlap on the GPU.
+ * Sizes: n_new * (Hq / Hkv) <= 65535 * 256, max_ctx + n_new <= 2^30, B * Hq * n_new <= 2^31
+ * (RQ_ERR_UNSUPPORTED).
  * A chunk token whose K or V row of the loop is not finite, or beyond fp16's largest number
  * (the states' range everywhere in this library), makes the outputs of its own and of the
  * sequence's later tokens NaN for the query heads of its kv-head; earlier tokens never see it.
@@ -294,8 +297,9 @@ rq_status rq_paged_chunk_attention(const rq_shape* shape, const rq_cache* cache,
  *   budget     >= 1; n_first, n_last >= 0, n_first + n_last <= budget
  *   keep       int32 [batch][n_kv_heads][budget]: the kept slots, ascending; entries at and
  *              behind kept_lens[b] are left as they were
- *   kept_lens  int32 [batch]: also the new ctx_lens after rq_evict_compact.  A ctx_len outside
- *              [0, capacity] gives -1 and no entries (a decode call refuses that length). */
+ *   kept_lens  int32 [batch], another array than ctx_lens (RQ_ERR_INVALID_ARG): also the new
+ *              ctx_lens after rq_evict_compact.  A ctx_len outside [0, capacity] gives -1 and no
+ *              entries (a decode call refuses that length). */
 rq_status rq_evict_select(const float* weights, int32_t batch, int32_t n_kv_heads,
                           int32_t capacity, const int32_t* ctx_lens, int32_t budget,
                           int32_t n_first, int32_t n_last, int32_t* keep, int32_t* kept_lens,
@@ -320,7 +324,8 @@ rq_status rq_evict_compact(const rq_shape* shape, const rq_cache* cache, const r
 
 /* The same on paged caches.  In place: the same data, block table and page count (the pages
  * behind the kept rows are then free); pages that several sequences share must not be
- * compacted in place.  A block-table entry outside [0, n_pages) is never dereferenced: its rows
+ * compacted in place.  Within one pool rows may also move to other pages: two block tables
+ * with no page in common (so shared pages can be read, and each sequence gets its own).  A block-table entry outside [0, n_pages) is never dereferenced: its rows
  * are left as they were. */
 rq_status rq_paged_evict_compact(const rq_shape* shape, const rq_cache* cache,
                                  const rq_paging* paging, const rq_shape* to_shape,

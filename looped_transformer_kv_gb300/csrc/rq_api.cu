@@ -143,6 +143,15 @@ bool strides_ok(const int64_t* strides, const int64_t* extents, int n) {
   return true;
 }
 
+// Does the span of bf16 rows of `d` elements at these (checked) strides meet [begin, end)?
+bool overlaps(const uint16_t* p, const int64_t* strides, const int64_t* extents, int n, int d,
+              uintptr_t begin, uintptr_t end) {
+  int64_t last = d;
+  for (int i = 0; i < n; ++i) last += (extents[i] - 1) * strides[i];
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(p), a1 = a0 + uintptr_t(last) * 2;
+  return a0 < end && begin < a1;
+}
+
 // Sizes a chunk call may have, without its pointers.
 rq_status check_chunk_sizes(const rq_shape* s, int32_t loop, int32_t n_new, int32_t max_ctx,
                             int32_t window) {
@@ -150,7 +159,7 @@ rq_status check_chunk_sizes(const rq_shape* s, int32_t loop, int32_t n_new, int3
   if (max_ctx < 0 || max_ctx > s->capacity) return RQ_ERR_INVALID_ARG;
   if (window < 0 || window > n_new) return RQ_ERR_INVALID_ARG;
   if (int64_t(max_ctx) + n_new > (int64_t(1) << 30)) return RQ_ERR_UNSUPPORTED;
-  if (int64_t(s->n_q_heads / s->n_kv_heads) * n_new > (int64_t(1) << 24)) return RQ_ERR_UNSUPPORTED;
+  if (int64_t(s->n_q_heads / s->n_kv_heads) * n_new > 65535 * 256) return RQ_ERR_UNSUPPORTED;   // (grid.y)
   if (int64_t(s->batch) * s->n_q_heads * (n_new > 0 ? n_new : 1) > (int64_t(1) << 31))
     return RQ_ERR_UNSUPPORTED;
   return RQ_OK;
@@ -172,6 +181,12 @@ rq_status chunk_common(const rq_shape* shape, const rq_cache* cache, const rq_pa
   if (!ws || ws_bytes < rq_chunk_workspace_bytes(shape, c.loop, c.n_new, c.max_ctx, c.window))
     return RQ_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RQ_ERR_WORKSPACE;
+  // rows are read while others are written
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(c.out);
+  const uintptr_t o1 = o0 + size_t(shape->batch) * c.n_new * shape->n_q_heads * shape->head_dim * 2;
+  if (overlaps(c.q, c.q_strides, qe, 3, shape->head_dim, o0, o1) ||
+      overlaps(c.kv_new, c.kv_strides, ke, 5, shape->head_dim, o0, o1))
+    return RQ_ERR_INVALID_ARG;
   try {
     return from_cuda(rq::launch_chunk(*shape, *cache, paging, c, ws, static_cast<cudaStream_t>(stream)));
   } catch (...) {
@@ -423,6 +438,9 @@ rq_status rq_evict_select(const float* weights, int32_t batch, int32_t n_kv_head
       int64_t(n_first) + n_last > budget)
     return RQ_ERR_INVALID_ARG;
   if (capacity > (1 << 30) || int64_t(batch) * n_kv_heads > (1 << 27)) return RQ_ERR_UNSUPPORTED;
+  // a sequence's heads read its length while another writes what is kept
+  const uintptr_t c0 = reinterpret_cast<uintptr_t>(ctx_lens), k0 = reinterpret_cast<uintptr_t>(kept_lens);
+  if (c0 < k0 + size_t(batch) * 4 && k0 < c0 + size_t(batch) * 4) return RQ_ERR_INVALID_ARG;
   try {
     return from_cuda(rq::launch_evict_select(weights, batch, n_kv_heads, capacity, ctx_lens, budget,
                                              n_first, n_last, keep, kept_lens,

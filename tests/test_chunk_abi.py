@@ -74,6 +74,27 @@ def test_chunk_refuses_bad_shapes(lib, bad, status):
     assert lib.lib().rq_chunk_workspace_bytes(ctypes.byref(_shape(**bad)), 0, 1, 0, 0) == 0
 
 
+@pytest.mark.parametrize("heads,n,status", [(1, 65535 * 256, OK), (1, 65535 * 256 + 1, UNSUPPORTED),
+                                            (256, 65535, OK), (256, 65536, UNSUPPORTED)])
+def test_most_rows_of_a_chunk(lib, heads, n, status):
+    s = _shape(batch=1, n_kv_heads=1, n_q_heads=heads)
+    size = lib.lib().rq_chunk_workspace_bytes(ctypes.byref(s), 0, n, 0, 0)
+    assert (size > 0) == (status == OK)
+    # (the call is refused either way: its workspace is too small)
+    assert _chunk(lib, shape=s, n=n, max_ctx=0, ws_bytes=16) == (WORKSPACE if status == OK else status)
+
+
+@pytest.mark.parametrize("apart", [0, 2, 2 * 2 * 4 * 128 * 2 - 2])
+def test_chunk_output_over_its_inputs_is_refused(lib, apart):
+    """Rows [2][2][4][128] each: out overlaps q, or kv_new, by at least one element."""
+    at, far = (1 << 32), ctypes.c_void_p(1 << 40)
+    strides = dict(qs=(2 * 4 * 128, 4 * 128, 128), ks=(0, 0, 0, 0, 0))
+    for off in (apart, -apart):
+        assert _chunk(lib, q=ctypes.c_void_p(at), kv=far, out=ctypes.c_void_p(at + off), **strides) == INVALID
+    strides = dict(qs=(0, 0, 0), ks=(2 * 4 * 128, 4 * 128, 256, 0, 128))
+    assert _chunk(lib, q=far, kv=ctypes.c_void_p(at), out=ctypes.c_void_p(at + apart), **strides) == INVALID
+
+
 def test_chunk_paging_is_validated(lib):
     assert _chunk(lib, paged=True) == INVALID
     g = lib.RqPaging()
@@ -105,6 +126,7 @@ def _select(lib, **kw):
     (dict(budget=0), INVALID), (dict(first=-1), INVALID), (dict(last=-1), INVALID),
     (dict(first=8), INVALID), (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), INVALID),
     (dict(B=1 << 20, H=1 << 10), UNSUPPORTED), (dict(cap=2 ** 31 - 1), UNSUPPORTED),
+    (dict(kept=P), INVALID), (dict(kept=ctypes.c_void_p(256 + 4)), INVALID),
 ])
 def test_select_refusals(lib, kw, status):
     assert _select(lib, **kw) == status

@@ -352,9 +352,41 @@ def test_many_rows(case, window):
     c.check()
 
 
-@pytest.mark.parametrize("d,Hq,ctx,lens", [(128, 16, [0, 130], [4096, 3001]), (64, 12, [257, 1], [4000, 4096])])
+def check_on_gpu(c, b, h, cached):
+    """Case.check with the 64-bit attention on the GPU; returns the weights its window should add.
+    cached: (k, v, norms of k's and v's residuals) of the cached tokens."""
+    G, d, m, n0 = c.Hq // c.H, c.d, c.lens[b], c.ctx[b]
+    assert (c.out[b, m:, h * G:(h + 1) * G] == 776.0).all()
+    k, v = (torch.cat([cached[kv].cuda(), c.new_host[b, :m, kv, c.loop, h].double().cuda()]) for kv in (0, 1))
+    rk, rv = (torch.cat([cached[2 + kv], torch.zeros(m).double()]).cuda() for kv in (0, 1))
+    late = torch.arange(n0 + m, device="cuda").view(1, -1) > n0 + torch.arange(m, device="cuda").view(-1, 1)
+    added = torch.zeros(n0 + m, dtype=torch.float64, device="cuda")
+    for g in range(G):
+        q = c.q[b, :m, h * G + g].double()
+        s = (q @ k.T * d ** -0.5).masked_fill(late, -float("inf"))
+        p = torch.softmax(s, -1)
+        added += p[max(0, m - c.window):].sum(0)
+        ref, got = p @ v, c.out[b, :m, h * G + g].double()
+        # the bound of Case.check, its largest score error over all keys
+        mag = (q.abs() @ k.abs().T * d ** -0.5).amax(-1, keepdim=True)
+        e = HALF16 * (2 * mag + 4 * q.norm(dim=-1, keepdim=True) * rk.max() * d ** -0.5)
+        tol = (p @ v.abs()) * (torch.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[:, None]
+        tol += HALFB * ref.abs() * 1.01 + 1e-30
+        assert ((got - ref).abs() <= tol).all(), (b, h, g, ((got - ref).abs() / tol).max().item())
+    return added
+
+
+def cached_rows(rec, n, d, bits, h, signs):
+    return ([torch.from_numpy(R.rebuild(rec, n, d, bits, 0, kv, signs[kv, h].numpy())) for kv in (0, 1)] +
+            [torch.from_numpy(R.residual_norms(rec, n, d, bits, 0, kv)) for kv in (0, 1)])
+
+
+LONG = [(128, 16, [0, 130], [4096, 3001]), (64, 12, [257, 1], [4000, 4096])]
+
+
+@pytest.mark.parametrize("d,Hq,ctx,lens", LONG)
 def test_long_chunks_shared_evenly(d, Hq, ctx, lens):
-    """Enough key tiles that the CTAs share them evenly, across row blocks; the reference on the GPU."""
+    """Enough key tiles that the CTAs share them evenly, across row blocks."""
     B, H = 2, 2
     c = Case(B, Hq, H, d, (2,), ctx, 4096, lens, seed=d, window=3)
     c.call()
@@ -362,29 +394,75 @@ def test_long_chunks_shared_evenly(d, Hq, ctx, lens):
     assert c.error_word() == 0
     G = Hq // H
     for b, h in itertools.product(range(B), range(H)):
-        m, n0 = lens[b], ctx[b]
-        assert (c.out[b, m:, h * G:(h + 1) * G] == 776.0).all()
-        rec = c.records(b, h)
-        k, v = (torch.cat([
-            torch.from_numpy(R.rebuild(rec, n0, d, c.bits, 0, kv, c.signs[kv, h].numpy())),
-            c.new_host[b, :m, kv, 0, h].double()]).cuda() for kv in (0, 1))
-        rk, rv = (torch.cat([torch.from_numpy(R.residual_norms(rec, n0, d, c.bits, 0, kv)),
-                             torch.zeros(m).double()]).cuda() for kv in (0, 1))
-        late = torch.arange(n0 + m, device="cuda").view(1, -1) > n0 + torch.arange(m, device="cuda").view(-1, 1)
-        added = torch.zeros(n0 + m, dtype=torch.float64, device="cuda")
-        for g in range(G):
-            q = c.q[b, :m, h * G + g].double()
-            s = (q @ k.T * d ** -0.5).masked_fill(late, -float("inf"))
-            p = torch.softmax(s, -1)
-            added += p[-3:].sum(0)
-            ref, got = p @ v, c.out[b, :m, h * G + g].double()
-            # the bound of Case.check, its largest score error over all keys
-            mag = (q.abs() @ k.abs().T * d ** -0.5).amax(-1, keepdim=True)
-            e = HALF16 * (2 * mag + 4 * q.norm(dim=-1, keepdim=True) * rk.max() * d ** -0.5)
-            tol = (p @ v.abs()) * (torch.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[:, None]
-            tol += HALFB * ref.abs() * 1.01 + 1e-30
-            assert ((got - ref).abs() <= tol).all(), (b, h, g, ((got - ref).abs() / tol).max().item())
+        end = ctx[b] + lens[b]
+        added = check_on_gpu(c, b, h, cached_rows(c.records(b, h), ctx[b], d, c.bits, h, c.signs))
         got = c.weights[b, h].double() - c.w0[b, h].double().cuda()
         # (weights: fp32 additions to values below 1, 2^-24 each, and the scores' 21 bits)
-        assert (got[:n0 + m] - added).abs().max().item() <= 2.0 ** -23 + 3 * G * 2e-4 * added.max().item()
-        assert (got[n0 + m:] == 0).all()
+        assert (got[:end] - added).abs().max().item() <= 2.0 ** -23 + 3 * G * 2e-4 * added.max().item()
+        assert (got[end:] == 0).all()
+    o, w = c.out.clone(), c.weights.clone()
+    c.weights.copy_(c.w0)
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(o.view(torch.int16), c.out.view(torch.int16)) and torch.equal(w, c.weights)
+
+
+def test_long_chunk_with_bad_lengths_is_nan():
+    c = Case(2, 16, 2, 128, (2,), [0, 130], 4096, [4096, 3001])
+    c.ctx_lens[1] = 131                        # max_ctx + 1
+    c.call()
+    torch.cuda.synchronize()
+    assert c.error_word() != 0
+    assert torch.isnan(c.out[0]).all() and torch.isnan(c.out[1, :3001]).all()
+    assert (c.out[1, 3001:] == 776.0).all()
+
+
+def test_more_sequences_than_are_rebuilt_together():
+    """Images of 130 sequences: more than 4 GB, so they go in two groups.  All have the same cache."""
+    B, Hq, H, d, n_new, cap = 130, 16, 4, 128, 40, 16384
+    g = torch.Generator().manual_seed(0)
+    ctx = torch.randint(0, 700, (B,), generator=g).tolist()
+    lens = torch.randint(0, n_new + 1, (B,), generator=g).tolist()
+    sampled = (0, 125, 126, 127, 128, 129)     # (the groups meet at 127)
+    for b, x in zip(sampled, (cap, 100, cap - 1, 700, 0, cap - 130)):
+        ctx[b], lens[b] = x, n_new - b % 3
+    one = Case(1, Hq, H, d, (2,), [cap - n_new], n_new, seed=1)      # its records go to every sequence
+    c = Case.__new__(Case)
+    c.Hq, c.H, c.d, c.ctx, c.lens, c.loop, c.window = Hq, H, d, ctx, lens, 0, 0
+    shape = rq.make_shape(B, Hq, H, d, 2, cap, (2,))
+    cache = rq.PackedCache(shape, one.signs, data=one.cache.data.repeat(B))
+    q = torch.randn(B, n_new, Hq, d, generator=g).bfloat16()
+    c.new_host = torch.randn(B, n_new, 2, 2, H, d, generator=g).bfloat16()
+    for b in range(B):
+        q[b, lens[b]:] = float("nan")
+        c.new_host[b, lens[b]:] = float("nan")
+        ctx[b] = min(ctx[b], cap - n_new)
+    c.q, c.out = q.cuda(), torch.full(q.shape, 776.0, dtype=torch.bfloat16).cuda()
+    c.ws = torch.full((rq.chunk_workspace_bytes(shape, 0, n_new, cap - n_new),), 255, dtype=torch.uint8).cuda()
+    assert c.ws.numel() > 4e9
+    rq.chunk_attention(shape, cache, c.q, 0, c.new_host.cuda(), torch.tensor(ctx, dtype=torch.int32).cuda(),
+                       cap - n_new, c.out, c.ws, n_lens=torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert c.error_word() == 0
+    for h in range(H):
+        k, v, rk, rv = cached_rows(one.records(0, h), cap - n_new, d, (2,), h, one.signs)
+        for b in sampled:
+            check_on_gpu(c, b, h, (k[:ctx[b]], v[:ctx[b]], rk[:ctx[b]], rv[:ctx[b]]))
+    out = c.out.float()
+    for b in range(B):
+        assert torch.isfinite(out[b, :lens[b]]).all() and (out[b, lens[b]:] == 776.0).all()
+
+
+@pytest.mark.parametrize("n_new", [2, 20, 90, 600])
+def test_two_calls_at_once(n_new):
+    """The same cache, two streams, a workspace each; one of the calls on another sequence length."""
+    a = Case(1, 8, 2, 128, (2,), [900], n_new)
+    b = Case(1, 8, 2, 128, (2,), [900], n_new, [n_new - 1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for c, s in zip((a, b), streams):
+            c.call(stream=s)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()

@@ -161,6 +161,28 @@ def test_compact(case, in_place, paged):
         assert torch.equal(to.data.view(to_paging.n_pages, -1).cpu()[free], old[free])
 
 
+def test_compact_to_other_pages_of_one_pool():
+    """Two sequences share their pages; each gets its own, in the same pool."""
+    d, bits, H, cap, budget = 128, (2, 4), 2, 256, 100
+    shape, pool, _, _ = _cache(2, H, d, bits, cap, 9, paged=True, spare=4)      # 12 pages
+    table = torch.tensor([[3, 0, 7, 5]] * 2, dtype=torch.int32).cuda()
+    to_table = torch.tensor([[1, 11], [8, 2]], dtype=torch.int32).cuda()
+    to_shape = rq.make_shape(2, H, H, d, 3, 128, bits)
+    rng = np.random.default_rng(9)
+    keep = np.stack([[np.sort(rng.choice(cap, budget, replace=False)) for _ in range(H)] for _ in range(2)])
+    want = {(b, h): _tokens(pool, table, b, h, d, bits, keep[b, h]) for b in range(2) for h in range(H)}
+    old = pool.data.clone().view(12, -1)
+    rq.paged_evict_compact(shape, pool, rq.make_paging(table, 12), to_shape, pool, rq.make_paging(to_table, 12),
+                           torch.from_numpy(keep.astype(np.int32)).cuda(),
+                           torch.tensor([budget, 65], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    for b, n in ((0, budget), (1, 65)):
+        for h in range(H):
+            assert _tokens(pool, to_table, b, h, d, bits, range(n)) == want[b, h][:n], (b, h)
+    rest = [p for p in range(12) if p not in (1, 11, 8, 2)]
+    assert torch.equal(pool.data.view(12, -1)[rest], old[rest])
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_entries_out_of_range_move_nothing(in_place):
     d, bits = 128, (2,)
