@@ -26,6 +26,7 @@ struct TailArgs {
   float* weights;
   int64_t score_stride;
   int B, H, heads, n_new, n_splits, window, cap, max_ctx;
+  int vec;                   // states, queries and outputs may be read and written 8 bytes at a time
   float scale_log2;
 };
 
@@ -40,9 +41,25 @@ __device__ __forceinline__ void load_floats(const float* p, float (&x)[P]) {
   }
 }
 
-// One warp per row: merge the split partials, then the chunk's tokens 0..j one by one (online
-// softmax), undo the rotation, store bf16.  Rows whose weights are asked for also store the
-// chunk tokens' scores and their log2-sum-exp.  Latency-bound: j + 1 dependent dot products.
+// P consecutive bf16 values, two per word.
+template <int P>
+__device__ __forceinline__ void load_words(const uint16_t* p, bool vec, uint32_t (&w)[P / 2]) {
+  if (vec) {
+    if constexpr (P == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) w[i] = uint32_t(p[2 * i]) | uint32_t(p[2 * i + 1]) << 16;
+  }
+}
+
+// One warp per row: merge the split partials, then the chunk's tokens 0..j, eight at a time (their
+// loads and sums in flight together; online softmax), undo the rotation, store bf16.  Rows whose
+// weights are asked for also store the chunk tokens' scores and their log2-sum-exp.  Latency-bound.
 template <int D>
 __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constant__ TailArgs a) {
   constexpr int P = D / 32;
@@ -98,28 +115,62 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
       }
     }
     float qv[P];
-    const uint16_t* qp = a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.heads + g) * a.qs2 + lane * P;
+    uint32_t qw[P / 2];
+    load_words<P>(a.q + b * a.qs0 + j * a.qs1 + (int64_t(h) * a.heads + g) * a.qs2 + lane * P, a.vec, qw);
 #pragma unroll
-    for (int i = 0; i < P; ++i) qv[i] = bf16_bits_to_float(qp[i]) * a.scale_log2;
-    for (int t = 0; t <= j; ++t) {
-      const uint16_t* kp = a.kv_new + b * a.ks0 + t * a.ks1 + h * a.ks_h + lane * P;
-      const uint16_t* vp = kp + a.kv_v;
-      float s = 0.f, v[P];
+    for (int i = 0; i < P; ++i) qv[i] = __uint_as_float(i & 1 ? qw[i / 2] & 0xffff0000u : qw[i / 2] << 16) * a.scale_log2;
+    const uint16_t* const own = a.kv_new + b * a.ks0 + h * a.ks_h + lane * P;
+    constexpr int U = 8;
+    for (int t0 = 0; t0 <= j; t0 += U) {
+      uint32_t k[U][P / 2], v[U][P / 2];
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float k = bf16_bits_to_float(kp[i]);
-        v[i] = bf16_bits_to_float(vp[i]);
-        bad |= !(fabsf(k) <= kStateMax) || !(fabsf(v[i]) <= kStateMax);
-        s = fmaf(qv[i], k, s);
+      for (int u = 0; u < U; ++u) {   // (behind the row's own token: that one again, weight 0)
+        const uint16_t* const kp = own + int64_t(min(t0 + u, j)) * a.ks1;
+        load_words<P>(kp, a.vec, k[u]);
+        load_words<P>(kp + a.kv_v, a.vec, v[u]);
       }
-      s = warp_sum(s);
-      if (voted && lane == 0) a.scores[wrow * a.score_stride + a.ctx_lens[b] + t] = s;
-      const float m = fmaxf(M, s), f0 = exp2f(M - m), f1 = exp2f(s - m);   // (s is finite)
-      ell = fmaf(ell, f0, f1);
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float x = __uint_as_float(i & 1 ? k[u][i / 2] & 0xffff0000u : k[u][i / 2] << 16);
+          const float y = __uint_as_float(i & 1 ? v[u][i / 2] & 0xffff0000u : v[u][i / 2] << 16);
+          bad |= !(fabsf(x) <= kStateMax) || !(fabsf(y) <= kStateMax);
+          s[u] = fmaf(qv[i], x, s[u]);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(RQ_FULL_MASK, s[u], o);
+      if (voted && lane == 0) {
+        float* const to = a.scores + wrow * a.score_stride + a.ctx_lens[b] + t0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (t0 + u <= j) to[u] = s[u];
+      }
+      float m = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = t0 + u <= j ? s[u] : -INFINITY;
+        m = fmaxf(m, s[u]);
+      }
+      const float f0 = exp2f(M - m);   // (m is finite: the row's own token has a finite score)
+      ell *= f0;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        ar[i] = fmaf(ar[i], f0, f1 * v[i]);
+        ar[i] *= f0;
         ae[i] *= f0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = exp2f(s[u] - m);
+        ell += f;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          ar[i] = fmaf(f, __uint_as_float(i & 1 ? v[u][i / 2] & 0xffff0000u : v[u][i / 2] << 16), ar[i]);
       }
       M = m;
     }
@@ -134,8 +185,19 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
   }
   const float nan = __int_as_float(0x7fc00000);
   const float inv = bad ? nan : 1.f / ell;
+  uint32_t w[P / 2];
 #pragma unroll
-  for (int i = 0; i < P; ++i) o[i] = float_to_bf16_bits(ar[i] * inv);
+  for (int i = 0; i < P / 2; ++i)
+    w[i] = uint32_t(float_to_bf16_bits(ar[2 * i] * inv)) | uint32_t(float_to_bf16_bits(ar[2 * i + 1] * inv)) << 16;
+  if (a.vec) {
+    if constexpr (P == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(o) = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
+  }
   if (voted && lane == 0) a.lse[wrow] = bad ? nan : M + log2f(ell);
 }
 
@@ -213,21 +275,26 @@ RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int 
 
 }  // namespace
 
-// How a call runs.  Streaming the cache once per 8 rows wins up to 8 rows (and, because its scores
-// carry 21 bits, whenever up to 32 rows collect weights); up to 128 rows of up to 32 tokens are
-// attended in one pass with the codes converted in shared memory (the combine walks a row's chunk
-// tokens one by one); more share K and V rebuilt once.
+// How a call runs (times in us, 2-bit loop, 128 channels, L2 flushed; B x Hkv after ctx):
+// - kStream: the cache once per 8 rows.  Up to 8 rows (8 x 8 after 16384: 112 us against 130 fused;
+//   16 rows 206 against 132).  With weights up to 32 rows, because its scores carry 21 bits and tiles
+//   need a second pass for that (32 rows 448 us against 728; 64 rows 857 against 729).
+// - kFused: up to 128 rows without weights, the codes converted in shared memory once for all rows
+//   (32 rows 136 us, 128 rows 185 us against 390 with tiles).  Its combine walks a row's chunk tokens
+//   (about 0.35 us each), so beyond 32 of them the context must be worth it: 64 tokens after 2048
+//   46 us against 52 (1 x 16), after 512 118 against 95 (16 x 16); 128 after 8192 263 against 369.
+// - kTiles: K and V rebuilt once, for everything else.
 enum class ChunkPath { kStream, kFused, kTiles };
 
-ChunkPath chunk_path(const rq_shape& s, int n_new, int window) {
+ChunkPath chunk_path(const rq_shape& s, int n_new, int max_ctx, int window) {
   const int64_t rows = int64_t(s.n_q_heads / s.n_kv_heads) * n_new;
   if (rows <= (window > 0 ? 32 : 8)) return ChunkPath::kStream;
-  if (window == 0 && rows <= 128 && n_new <= 32) return ChunkPath::kFused;
+  if (window == 0 && rows <= 128 && (n_new <= 32 || n_new * 32 <= max_ctx)) return ChunkPath::kFused;
   return ChunkPath::kTiles;
 }
 
 size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
-  const ChunkPath path = chunk_path(s, n_new, window);
+  const ChunkPath path = chunk_path(s, n_new, max_ctx, window);
   if (path == ChunkPath::kTiles) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window);
   if (path == ChunkPath::kFused) return chunk_fused_workspace_bytes(s, loop, n_new, max_ctx);
   return rows_layout(s, loop, n_new, max_ctx, window).total;
@@ -239,7 +306,7 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   unsigned* err = reinterpret_cast<unsigned*>(w);
   cudaError_t e;
   TailArgs a;
-  const ChunkPath path = chunk_path(s, c.n_new, c.window);
+  const ChunkPath path = chunk_path(s, c.n_new, c.max_ctx, c.window);
   RowsLayout l = {};
   if (path == ChunkPath::kFused) {
     if ((e = launch_chunk_fused(s, cache, paging, c, ws, &a.part, &a.n_splits, stream)) != cudaSuccess) return e;
@@ -278,6 +345,8 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   a.window = c.window;
   a.cap = s.capacity;
   a.max_ctx = c.max_ctx;
+  a.vec = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.kv_new) | reinterpret_cast<uintptr_t>(a.out)) & 7) == 0 &&
+          ((a.qs0 | a.qs1 | a.qs2 | a.ks0 | a.ks1 | a.kv_v | a.ks_h) & 3) == 0;
   const float scale = s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim));
   a.scale_log2 = scale * kLog2e;
   const int64_t warps = int64_t(s.batch) * s.n_q_heads * c.n_new;

@@ -314,6 +314,8 @@ MIDDLE = [
     (1, 8, 2, 64, (), 0, [127], 7, None),
     (1, 8, 1, 128, (2,), 0, [3000], 16, None),
     (3, 128, 1, 128, (4,), 0, [100, 192, 7], 1, None),
+    (1, 1, 1, 128, (2,), 0, [4096], 128, None),
+    (2, 4, 2, 64, (4,), 0, [2080, 70], 64, [63, 64]),
 ]
 
 
