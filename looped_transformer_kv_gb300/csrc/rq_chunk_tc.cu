@@ -262,8 +262,9 @@ __device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int 
   if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
 }
 
-// Tiles of the chunk's own keys alone: one CTA each (and one for the attention's schedule).  Rows are loaded 16 bytes a lane; V goes
-// through shared memory to have channels as rows.  Bound by HBM latency.
+// Tiles of the chunk's own keys alone: one CTA each (and one for the attention's schedule).  Rows
+// are loaded 16 bytes a lane; V goes through shared memory to have channels as rows.  Bound by the
+// latency of HBM (2,048 tokens of 8 heads: 7.5 us).
 template <int D, bool KLO>
 __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant__ RebuildArgs a) {
   if (blockIdx.x == gridDim.x - 1) {            // the attention's schedule
@@ -349,8 +350,9 @@ __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant_
 // H: Hadamard +-1), and the epilogues add the reference, x = D sign / sqrt(d) + a (s c + z), in
 // fp32, round once and write the images through shared memory: a thread per key and half the
 // channels for K, per channel and half the keys for V (the V image has channels as rows).
-// Bound by HBM (one loop's rows read, 4 d bytes per token-head written) and by the instructions
-// of the conversions (about 1,500 per token-head).
+// Bound by instructions and the barriers between its phases (140 warp instructions per token-head
+// with 2-bit residuals; two CTAs per SM overlap): 14,336 tokens of 8 heads in 33 us, 2.7 TB/s of
+// rows read and images written; with 4-bit residuals and low parts 12,000 of 16 heads in 69 us.
 template <int D, int RES, bool KLO>
 __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__ RebuildArgs a, int n_items) {
   using L = RebuildSmem<D, RES, KLO>;
@@ -869,9 +871,12 @@ __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of w
 // SCHED: the CTAs share the key tiles evenly (one CTA per SM): a block that lies in one CTA's range
 // is stored, the others leave their (m, l, O) for merge_kernel, at most two per CTA.  Else one CTA
 // takes one split of one row block.  Sharing evenly wins where a CTA gets many tiles (2048 tokens x
-// 4 heads after 14336: 321 + 21 us against 377 + 34 us and 134 MB left to merge), splits where it
-// gets few (a ragged first chunk of 1023: 44 us against 54, each segment's set-up counts).
+// 4 heads after 14336: 325 + 15 us against 376 + 34 us and 134 MB left to merge), splits where it
+// gets few (a ragged first chunk of 1023: 45 us against 54, each segment's set-up counts).
 // LSE: scores with K in two parts, no P and V; (m, l) per row and split are stored.
+// Bound by the products: 515 GFLOP in 325 us, 1,585 TFLOP/s (the tensor pipe active 70 % of the time,
+// at the clock that the power limit leaves); a chunk with few key tiles per CTA by each CTA's
+// set-up and the latency of its first and last tiles.
 template <int D, bool LSE, bool SCHED>
 __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t raw[];
@@ -1275,7 +1280,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 }
 
 // The row blocks that several CTAs share: 8 CTAs of 32 rows for each row block and unit (SCHED: for
-// each cut, the first one inside a row block acts), a warp for four rows at a time.
+// each cut, the first one inside a row block acts), a warp for four rows at a time.  Bound by HBM
+// latency: a few dependent loads per warp (15 us after the 325 us above).
 template <int D, bool SCHED>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int P = D / 32, HALF = D / 2;
@@ -1365,7 +1371,7 @@ struct WeightArgs {
   float scale_log2;
 };
 
-// Operand images of the window's queries, each row's score scale and log2-sum-exp.
+// Operand images of the window's queries, each row's score scale and log2-sum-exp.  Bound by latency.
 template <int D>
 __global__ void __launch_bounds__(128) window_rows_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ __align__(1024) uint8_t img[];
@@ -1414,7 +1420,9 @@ struct WeightSmem {
 
 // One CTA per 128 keys: S^T = K Q^T with the keys as rows, so a key's weights add up in its
 // thread's registers, in row order.  Row tiles alternate between two tensor-memory buffers and the
-// two softmax warpgroups.  Bound by the exponentials.
+// two softmax warpgroups.  With few rows (one row tile per CTA) bound by the latency of its steps,
+// copies, products, exponentials, which two CTAs per SM overlap (32 rows, 6,509 keys, 32 heads: 34 us);
+// with many by the exponentials.
 template <int D>
 __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ uint8_t raw[];
