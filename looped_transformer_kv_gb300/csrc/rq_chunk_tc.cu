@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
       };
       for (int i = 0; i < 3 && more_k; ++i) {
         load_k();
-        if (i < 2 && more_v) load_v();
+        if (i < (LSE ? 2 : 1) && more_v) load_v();   // (with more of V the products could lap the waits below)
       }
       int c1 = 0, js = 0;                                            // tiles of row tile 1 so far (tile 0: g)
       for (int g = 0; more_v; ++g) {
