@@ -419,29 +419,38 @@ def test_long_chunk_with_bad_lengths_is_nan():
     assert (c.out[1, 3001:] == 776.0).all()
 
 
-def test_more_sequences_than_are_rebuilt_together():
-    """Images of 130 sequences: more than 4 GB, so they go in two groups.  All have the same cache."""
-    B, Hq, H, d, n_new, cap = 130, 16, 4, 128, 40, 16384
-    g = torch.Generator().manual_seed(0)
+@pytest.mark.parametrize("n_new", [4096, 20, 2])
+def test_batch_without_new_tokens(n_new):
+    c = Case(2, 16, 2, 128, (2,), [70, 130], n_new, [0, 0], window=2)
+    c.call()
+    torch.cuda.synchronize()
+    assert c.error_word() == 0 and (c.out == 776.0).all() and torch.equal(c.weights.cpu(), c.w0)
+
+
+@pytest.mark.parametrize("n_new", [2, 8, 40])
+def test_cache_of_more_than_4_gigabytes(n_new):
+    """330 sequences with the same cached rows.  40 tokens: their images, more than 4 GB too, are made
+    in three groups, which meet at sequences 127 and 254."""
+    B, Hq, H, d, cap = 330, 16, 4, 128, 16384
+    g = torch.Generator().manual_seed(n_new)
     ctx = torch.randint(0, 700, (B,), generator=g).tolist()
     lens = torch.randint(0, n_new + 1, (B,), generator=g).tolist()
-    sampled = (0, 125, 126, 127, 128, 129)     # (the groups meet at 127)
+    sampled = (0, 126, 127, 253, 254, 329)
     for b, x in zip(sampled, (cap, 100, cap - 1, 700, 0, cap - 130)):
-        ctx[b], lens[b] = x, n_new - b % 3
+        ctx[b], lens[b] = min(x, cap - n_new), n_new - b % 2
     one = Case(1, Hq, H, d, (2,), [cap - n_new], n_new, seed=1)      # its records go to every sequence
     c = Case.__new__(Case)
     c.Hq, c.H, c.d, c.ctx, c.lens, c.loop, c.window = Hq, H, d, ctx, lens, 0, 0
     shape = rq.make_shape(B, Hq, H, d, 2, cap, (2,))
     cache = rq.PackedCache(shape, one.signs, data=one.cache.data.repeat(B))
+    assert cache.data.numel() > 2 ** 32
     q = torch.randn(B, n_new, Hq, d, generator=g).bfloat16()
     c.new_host = torch.randn(B, n_new, 2, 2, H, d, generator=g).bfloat16()
     for b in range(B):
         q[b, lens[b]:] = float("nan")
         c.new_host[b, lens[b]:] = float("nan")
-        ctx[b] = min(ctx[b], cap - n_new)
     c.q, c.out = q.cuda(), torch.full(q.shape, 776.0, dtype=torch.bfloat16).cuda()
     c.ws = torch.full((rq.chunk_workspace_bytes(shape, 0, n_new, cap - n_new),), 255, dtype=torch.uint8).cuda()
-    assert c.ws.numel() > 4e9
     rq.chunk_attention(shape, cache, c.q, 0, c.new_host.cuda(), torch.tensor(ctx, dtype=torch.int32).cuda(),
                        cap - n_new, c.out, c.ws, n_lens=torch.tensor(lens, dtype=torch.int32).cuda())
     torch.cuda.synchronize()
@@ -453,6 +462,18 @@ def test_more_sequences_than_are_rebuilt_together():
     out = c.out.float()
     for b in range(B):
         assert torch.isfinite(out[b, :lens[b]]).all() and (out[b, lens[b]:] == 776.0).all()
+
+
+@pytest.mark.parametrize("n_new", [2, 20, 90])
+def test_broadcast_inputs(n_new):
+    """Strides of 0: one query for all heads, the same new states for all kv-heads and sequences."""
+    c = Case(2, 4, 2, 128, (2,), [100, 300], n_new, window=1 if n_new == 90 else 0)
+    c.q = c.q[:, :, :1].expand(-1, -1, 4, -1)
+    c.new = c.new[:1, :, :, :, :1].expand(2, -1, -1, -1, 2, -1)
+    c.q_host, c.new_host = c.q.cpu(), c.new.cpu()
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
 
 
 @pytest.mark.parametrize("n_new", [2, 20, 90, 600])
