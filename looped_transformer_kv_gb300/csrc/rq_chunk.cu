@@ -5,6 +5,7 @@
 // rows, and the combine below merges the splits and adds the chunk's own tokens, causally.
 #include "rq_common.cuh"
 #include "rq_kernels.h"
+#include "rq_launch.cuh"
 
 namespace rq {
 namespace {
@@ -63,6 +64,8 @@ __device__ __forceinline__ void load_words(const uint16_t* p, bool vec, uint32_t
 // latency (2,048 rows of 7 splits and up to 8 tokens: 10 us; one token at a time 14).
 template <int D>
 __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constant__ TailArgs a) {
+  grid_wait();
+  grid_next();
   constexpr int P = D / 32;
   constexpr int rec = 4 + 2 * D;
   const int lane = threadIdx.x & 31;
@@ -205,6 +208,7 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
 // Four slots per thread: the weights of the window's rows, in row order.  Bound by HBM: a score per
 // slot and row read, a weight read and written (one row, 256 x 4,097 slots: 6 us, launch included).
 __global__ void __launch_bounds__(128) chunk_weights_kernel(const __grid_constant__ TailArgs a) {
+  grid_wait();
   const int t0 = (blockIdx.x * 128 + threadIdx.x) * 4, h = blockIdx.y, b = blockIdx.z;
   const int n_len = a.n_lens ? a.n_lens[b] : a.n_new, ctx = a.ctx_lens[b];
   if (n_len < 0 || n_len > a.n_new || ctx < 0 || ctx > a.max_ctx) return;   // (flagged)
@@ -351,14 +355,11 @@ cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_pagi
   const float scale = s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim));
   a.scale_log2 = scale * kLog2e;
   const int64_t warps = int64_t(s.batch) * s.n_q_heads * c.n_new;
-  if (s.head_dim == 128)
-    chunk_combine_kernel<128><<<unsigned((warps + 3) / 4), 128, 0, stream>>>(a);
-  else
-    chunk_combine_kernel<64><<<unsigned((warps + 3) / 4), 128, 0, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !c.weights) return e;
+  e = launch_after(true, s.head_dim == 128 ? chunk_combine_kernel<128> : chunk_combine_kernel<64>,
+                   unsigned((warps + 3) / 4), 128, 0, stream, a);
+  if (e != cudaSuccess || !c.weights) return e;
   const dim3 grid((c.max_ctx + c.n_new + 511) / 512, s.n_kv_heads, s.batch);
-  chunk_weights_kernel<<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(true, chunk_weights_kernel, grid, 128, 0, stream, a);
 }
 
 }  // namespace rq

@@ -27,6 +27,7 @@
 // stores of the images and weights through shared memory did not shorten it.
 #include "rq_common.cuh"
 #include "rq_kernels.h"
+#include "rq_launch.cuh"
 #include "rq_tc.cuh"
 
 namespace rq {
@@ -66,6 +67,7 @@ __host__ __device__ constexpr int image_position(int c) {
 // runs before anything that sets it).
 template <int D, int RES>
 __global__ void __launch_bounds__(128) fused_rows_kernel(const __grid_constant__ FusedArgs a, int n_rows) {
+  grid_next();
   constexpr int P = D / 32;
   if (blockIdx.x == 0 && threadIdx.x < kWsHeaderBytes / 4) a.err[threadIdx.x] = 0u;
   const int lane = threadIdx.x & 31;
@@ -156,6 +158,8 @@ struct FusedSmem {
 
 template <int D, int RES>
 __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ FusedArgs a) {
+  grid_wait();
+  grid_next();
   using L = FusedSmem<D, RES>;
   constexpr int NG = L::NG, KD = 64 * L::NP;                 // scores' K, accumulators' N
   constexpr int SIDE = kTile * (D / 2 + 4 * NG);             // K (or V) part of the reference section
@@ -606,8 +610,8 @@ cudaError_t launch_fused(const FusedArgs& a, int batch, cudaStream_t stream) {
   const int64_t n_rows = int64_t(batch) * a.H * a.rows;
   fused_rows_kernel<D, RES><<<unsigned((n_rows + 3) / 4), 128, 0, stream>>>(a, int(n_rows));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  fused_kernel<D, RES><<<dim3(unsigned(a.n_splits), unsigned(a.H), unsigned(batch)), 768, L::total, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(true, fused_kernel<D, RES>, dim3(unsigned(a.n_splits), unsigned(a.H), unsigned(batch)), 768,
+                      L::total, stream, a);
 }
 
 }  // namespace

@@ -15,6 +15,7 @@
 
 #include "rq_common.cuh"
 #include "rq_kernels.h"
+#include "rq_launch.cuh"
 #include "rq_tc.cuh"
 
 namespace rq {
@@ -267,6 +268,8 @@ __device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int 
 // latency of HBM (2,048 tokens of 8 heads: 7.5 us).
 template <int D, bool KLO>
 __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant__ RebuildArgs a) {
+  grid_wait();
+  grid_next();
   if (blockIdx.x == gridDim.x - 1) {            // the attention's schedule
     if (blockIdx.z == 0 && a.schedule.at) write_schedule(a.v, a.schedule, a.units, a.blocks);
     return;
@@ -355,6 +358,8 @@ __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant_
 // rows read and images written; with 4-bit residuals and low parts 12,000 of 16 heads in 69 us.
 template <int D, int RES, bool KLO>
 __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__ RebuildArgs a, int n_items) {
+  grid_wait();
+  grid_next();
   using L = RebuildSmem<D, RES, KLO>;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -879,6 +884,8 @@ __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of w
 // set-up and the latency of its first and last tiles.
 template <int D, bool LSE, bool SCHED>
 __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+  grid_wait();
+  grid_next();
   extern __shared__ uint8_t raw[];
   using L = AttnSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -1284,6 +1291,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 // latency: a few dependent loads per warp (15 us after the 325 us above).
 template <int D, bool SCHED>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ AttnArgs a) {
+  grid_wait();
+  grid_next();
   constexpr int P = D / 32, HALF = D / 2;
   const int lane = threadIdx.x & 31;
   int p = blockIdx.x, from = 0, to = a.n_splits, start = 0, stop = 1;
@@ -1374,6 +1383,8 @@ struct WeightArgs {
 // Operand images of the window's queries, each row's score scale and log2-sum-exp.  Bound by latency.
 template <int D>
 __global__ void __launch_bounds__(128) window_rows_kernel(const __grid_constant__ WeightArgs a) {
+  grid_wait();
+  grid_next();
   extern __shared__ __align__(1024) uint8_t img[];
   const int h = blockIdx.y, b = a.v.b0 + blockIdx.z;
   const int64_t unit = int64_t(blockIdx.z) * a.v.H + h;
@@ -1425,6 +1436,8 @@ struct WeightSmem {
 // with many by the exponentials.
 template <int D>
 __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__ WeightArgs a) {
+  grid_wait();
+  grid_next();
   extern __shared__ uint8_t raw[];
   using L = WeightSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -1643,7 +1656,7 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
 }
 
 template <int D, int RES, bool KLO>
-cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, cudaStream_t stream) {
+cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, bool after, cudaStream_t stream) {
   using L = RebuildSmem<D, RES, KLO>;
   static OncePerDevice once;
   const cudaError_t e = once([] {
@@ -1652,17 +1665,17 @@ cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, cudaStream_t str
   if (e != cudaSuccess) return e;
   if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int64_t ctas = int64_t(device_sm_count()) * 2;
-  rebuild_kernel<D, RES, KLO><<<unsigned(items < ctas ? items : ctas), 256, L::total, stream>>>(r, int(items));
-  return cudaGetLastError();
+  return launch_after(after, rebuild_kernel<D, RES, KLO>, unsigned(items < ctas ? items : ctas), 256, L::total, stream, r,
+                      int(items));
 }
 
 template <int D>
-cudaError_t launch_rebuild_any(const RebuildArgs& r, int64_t items, cudaStream_t stream) {
+cudaError_t launch_rebuild_any(const RebuildArgs& r, int64_t items, bool after, cudaStream_t stream) {
   if (r.bits == 0)
-    return r.klo ? launch_rebuild<D, 0, true>(r, items, stream) : launch_rebuild<D, 0, false>(r, items, stream);
+    return r.klo ? launch_rebuild<D, 0, true>(r, items, after, stream) : launch_rebuild<D, 0, false>(r, items, after, stream);
   if (r.bits == 2)
-    return r.klo ? launch_rebuild<D, 2, true>(r, items, stream) : launch_rebuild<D, 2, false>(r, items, stream);
-  return r.klo ? launch_rebuild<D, 4, true>(r, items, stream) : launch_rebuild<D, 4, false>(r, items, stream);
+    return r.klo ? launch_rebuild<D, 2, true>(r, items, after, stream) : launch_rebuild<D, 2, false>(r, items, after, stream);
+  return r.klo ? launch_rebuild<D, 4, true>(r, items, after, stream) : launch_rebuild<D, 4, false>(r, items, after, stream);
 }
 
 template <int D>
@@ -1726,7 +1739,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.vec = reinterpret_cast<uintptr_t>(r.kv_new) % 16 == 0 && r.ks0 % 8 == 0 && r.ks1 % 8 == 0 &&
             r.kv_v % 8 == 0 && r.ks_h % 8 == 0;
     r.old_tiles = (c.max_ctx + kKeys - 1) / kKeys;
-    if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, stream)) != cudaSuccess) return e;
+    if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, b0 > 0, stream)) != cudaSuccess) return e;
     r.units = int(nb * H);
     r.blocks = l.blocks;
     r.schedule.pairs = r.units * r.blocks;
@@ -1734,11 +1747,9 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.schedule.cut = reinterpret_cast<int2*>(w + l.schedule);
     r.schedule.at = l.ctas ? reinterpret_cast<int*>(w + l.schedule + (size_t(l.ctas) + 1) * 8) : nullptr;
     const dim3 own(unsigned((c.n_new + kKeys - 1) / kKeys) * H + 1, 1, nb);
-    if (c.window)
-      chunk_image_kernel<D, true><<<own, 256, 3 * kKeys * D * 2 + 128, stream>>>(r);
-    else
-      chunk_image_kernel<D, false><<<own, 256, 2 * kKeys * D * 2 + 128, stream>>>(r);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(b0 > 0 || c.max_ctx > 0, c.window ? chunk_image_kernel<D, true> : chunk_image_kernel<D, false>, own, 256,
+                     (c.window ? 3 : 2) * kKeys * D * 2 + 128, stream, r);
+    if (e != cudaSuccess) return e;
     AttnArgs a;
     a.v = v;
     a.q = c.q;
@@ -1759,21 +1770,23 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     a.qvec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.qs0 % 8 == 0 && a.qs1 % 8 == 0 && a.qs2 % 8 == 0;
     a.scale_log2 = scale;
     if (l.ctas) {
-      attention_kernel<D, false, true><<<unsigned(l.ctas), 384, AS::total, stream>>>(a);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      if (l.ctas > 1) merge_kernel<D, true><<<dim3(unsigned(l.ctas - 1), 2 * kRows / 32), 256, 0, stream>>>(a);
+      e = launch_after(true, attention_kernel<D, false, true>, unsigned(l.ctas), 384, AS::total, stream, a);
+      if (e == cudaSuccess && l.ctas > 1)
+        e = launch_after(true, merge_kernel<D, true>, dim3(unsigned(l.ctas - 1), 2 * kRows / 32), 256, 0, stream, a);
     } else {
-      attention_kernel<D, false, false><<<dim3(nb * H * l.splits, unsigned(l.blocks)), 384, AS::total, stream>>>(a);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      if (l.splits > 1) merge_kernel<D, false><<<dim3(nb * H * l.blocks, 2 * kRows / 32), 256, 0, stream>>>(a);
+      e = launch_after(true, attention_kernel<D, false, false>, dim3(nb * H * l.splits, unsigned(l.blocks)), 384, AS::total,
+                       stream, a);
+      if (e == cudaSuccess && l.splits > 1)
+        e = launch_after(true, merge_kernel<D, false>, dim3(nb * H * l.blocks, 2 * kRows / 32), 256, 0, stream, a);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     if (!c.window) continue;
     a.n_splits = l.wsplits;
     a.row_tiles = l.q_tiles;
     a.blocks = l.wblocks;
-    attention_kernel<D, true, false><<<dim3(nb * H * l.wsplits, unsigned(l.wblocks)), 384, AS::total, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(true, attention_kernel<D, true, false>, dim3(nb * H * l.wsplits, unsigned(l.wblocks)), 384, AS::total,
+                     stream, a);
+    if (e != cudaSuccess) return e;
     WeightArgs x;
     x.v = v;
     x.q = c.q;
@@ -1791,10 +1804,10 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     x.q_tiles = l.q_tiles;
     x.cap = s.capacity;
     x.scale_log2 = scale;
-    window_rows_kernel<D><<<dim3(unsigned(l.q_tiles), H, nb), kRows, kRows * D * 2, stream>>>(x);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    weights_kernel<D><<<dim3(unsigned(l.tiles), H, nb), 320, WS::total, stream>>>(x);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(true, window_rows_kernel<D>, dim3(unsigned(l.q_tiles), H, nb), kRows, kRows * D * 2, stream, x);
+    if (e != cudaSuccess) return e;
+    e = launch_after(true, weights_kernel<D>, dim3(unsigned(l.tiles), H, nb), 320, WS::total, stream, x);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
