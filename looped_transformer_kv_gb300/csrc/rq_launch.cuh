@@ -1,6 +1,7 @@
 // Kernels of one call in a row: each one's CTAs are launched while the kernel before still runs, as
 // its own finish, and wait in grid_wait() (their first statement, so that "complete" carries
-// through the row) until it is complete.  Saves about a microsecond of launch latency per kernel.
+// through the row) until it is complete.  Two or three kernels in a row: 2 to 5 us less (3 tokens after
+// 256: 21 -> 18.6 us; one step with weights 96 -> 91).
 #pragma once
 #include <cuda_runtime.h>
 
