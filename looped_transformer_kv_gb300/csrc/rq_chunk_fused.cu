@@ -280,6 +280,9 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
       }
       tc_commit(done);
       failed = !mbar_wait_bounded(done, 0, kFuWaitLimitNs) || !good;
+      for (int j = max(0, T - 2); j < T && !failed; ++j)     // no arrival outstanding when the CTA leaves
+        failed = !mbar_wait_bounded(kfree(j & 1), (j >> 1) & 1, kFuWaitLimitNs) ||
+                 !mbar_wait_bounded(vfree(j & 1), (j >> 1) & 1, kFuWaitLimitNs);
     }
     __syncwarp();
   } else if (warp >= 12) {                                   // ---- V codes -> operand images

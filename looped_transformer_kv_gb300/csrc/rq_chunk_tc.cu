@@ -1078,7 +1078,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
           }
         }
         tc_commit(done);
-        if (!good) mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs);   // nothing in flight
+        // nothing in flight, no arrival outstanding when the CTA leaves (else the softmax waits for it)
+        if (LSE || !good) good &= mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs);
       }
       failed = !good;
     }
@@ -1498,8 +1499,11 @@ __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__
         bulk_g2s(dst + L::kTileBytes, a.scale + (unit * a.q_tiles + from + j) * kRows, kRows * 8, qfull(s));
       }
       failed = issued < T || !mbar_wait_bounded(kfull, 0, kTcWaitLimitNs);
-      for (int j = max(0, issued - L::kStages); j < issued; ++j)
+      for (int j = max(0, issued - L::kStages); j < issued; ++j) {
         failed |= !mbar_wait_bounded(qfull(j % L::kStages), (j / L::kStages) & 1, kTcWaitLimitNs);
+        // (and no arrival outstanding when the CTA leaves)
+        failed = failed || !mbar_wait_bounded(qfree(j % L::kStages), (j / L::kStages) & 1, kTcWaitLimitNs);
+      }
     }
     __syncwarp();
   } else if (warp == 9) {
