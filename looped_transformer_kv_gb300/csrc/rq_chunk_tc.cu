@@ -72,7 +72,9 @@ __device__ __forceinline__ BlockInfo block_info(const ChunkView& v, int unit, in
 // The attention's work in one line: row blocks, the longest of every unit first, each block's set-up
 // (as long as about five key tiles) and its key tiles in order.  The line is cut evenly for one CTA
 // per SM; a cut close to a block's edge moves there, because a block that two CTAs share costs a
-// merge of their results.  A shorter line is cut for fewer CTAs, yet one for each block.
+// merge of their results.  A shorter line is cut for fewer CTAs, yet one for each block that has rows:
+// no stretch between two cuts is then shorter than a block of one tile, and every CTA that a merge
+// reads from has written.
 constexpr int kSetup = 5, kSnap = 7;
 
 struct Schedule {
@@ -87,21 +89,27 @@ __device__ __forceinline__ int tile_at(int place, int from) { return max(0, plac
 
 // One CTA of 256 threads.
 __device__ __forceinline__ void write_schedule(const ChunkView& v, const Schedule& s, int units, int blocks) {
-  __shared__ int sums[256];
+  __shared__ int sums[256], counts[256];
   const int per = (s.pairs + 255) / 256;
   const int p0 = min(s.pairs, int(threadIdx.x) * per), p1 = min(s.pairs, p0 + per);
   auto stretch = [&](int p) {
     const int tiles = block_info(v, p % units, blocks - 1 - p / units, false).tiles;
     return tiles ? tiles + kSetup : 0;
   };
-  int sum = 0;
-  for (int p = p0; p < p1; ++p) sum += stretch(p);
+  int sum = 0, count = 0;
+  for (int p = p0; p < p1; ++p) {
+    const int x = stretch(p);
+    sum += x;
+    count += x > 0 ? 1 : 0;
+  }
   sums[threadIdx.x] = sum;
+  counts[threadIdx.x] = count;
   __syncthreads();
-  int at = 0, total = 0;
+  int at = 0, total = 0, live = 0;       // live: blocks that have rows
   for (int i = 0; i < 256; ++i) {
     at += i < int(threadIdx.x) ? sums[i] : 0;
     total += sums[i];
+    live += counts[i];
   }
   for (int p = p0; p < p1; ++p) {
     s.at[p] = at;
@@ -109,7 +117,7 @@ __device__ __forceinline__ void write_schedule(const ChunkView& v, const Schedul
   }
   if (threadIdx.x == 0) s.at[s.pairs] = total;
   __syncthreads();
-  const int ctas = max(1, min(s.grid, max(s.pairs, total / 8)));
+  const int ctas = max(1, min(s.grid, max(live, total / 8)));
   for (int c = threadIdx.x; c <= s.grid; c += 256) {
     int x = c >= ctas ? total : int(int64_t(c) * total / ctas);
     int lo = 0, hi = s.pairs;              // the last pair at or before x

@@ -35,3 +35,26 @@ def test_window_calls_back_to_back():
             assert c.error_word() == 0
             assert torch.equal(c.out.view(torch.int16), out.view(torch.int16))
             assert weights is None or torch.equal(c.weights, weights)
+
+
+@pytest.mark.parametrize("B,Hq,H,d,n_new,max_ctx,ctx,lens", [
+    (1, 32, 8, 128, 2048, 4096, [1450], [5]),
+    (1, 16, 2, 128, 2048, 16384, [4000], [1]),
+    (2, 32, 4, 64, 2048, 4096, [1400, 900], [3, 0]),
+    (3, 16, 4, 128, 2048, 4096, [0, 2222, 129], [0, 40, 17]),
+    (4, 32, 2, 128, 1024, 4096, [3000, 1, 0, 700], [1, 0, 700, 0]),
+])
+def test_short_tail_in_a_call_planned_for_long_chunks(B, Hq, H, d, n_new, max_ctx, ctx, lens):
+    """Most row blocks of the plan have no rows: fewer key tiles than the CTAs that share them.  What
+    the workspace held before does not matter."""
+    c = Case(B, Hq, H, d, (2,), ctx, n_new, lens, max_ctx=max_ctx, seed=7)
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
+    out = c.out.clone()
+    for fill in (0x3F, 0x00, 0x48):                 # finite as fp32, fp16 and counts
+        c.ws.fill_(fill)
+        c.out.fill_(776.0)
+        c.call()
+        torch.cuda.synchronize()
+        assert c.error_word() == 0 and torch.equal(c.out.view(torch.int16), out.view(torch.int16))
