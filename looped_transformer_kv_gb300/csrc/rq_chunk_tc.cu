@@ -47,6 +47,22 @@ __device__ __forceinline__ bool lens_of(const ChunkView& v, int b, int& n, int& 
   return n >= 0 && n <= v.n_new && ctx >= 0 && ctx <= v.max_ctx;
 }
 
+// Lengths and block-table entries of the whole batch, where its sequences are handled in several
+// groups: what is wrong with a later one has to be known when the first group's outputs are stored.
+// A thread per sequence and record.
+__global__ void __launch_bounds__(256) check_kernel(const __grid_constant__ ChunkView v, const int32_t* bt, int max_pages,
+                                                    int n_pages) {
+  grid_next();
+  const int b = blockIdx.y, rec = blockIdx.x * 256 + threadIdx.x;
+  int n, ctx;
+  bool bad = !lens_of(v, b, n, ctx);
+  if (!bad && bt && n > 0 && rec < (ctx + kTile - 1) / kTile) {
+    const int pg = bt[int64_t(b) * max_pages + rec];
+    bad = pg < 0 || pg >= n_pages;
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(v.err, 1u);
+}
+
 // --------------------------------------------------------------------------------- schedule
 
 // Rows and key tiles of row block `block` of a (sequence, kv-head): key tiles up to the block's last
@@ -1725,6 +1741,15 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
   v.tiles = l.tiles;
   const float scale = (s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim))) * kLog2e;
   uint8_t* const wb = reinterpret_cast<uint8_t*>(w);
+  const bool checked = l.group < s.batch;
+  if (checked) {
+    v.b0 = 0;
+    const unsigned recs = paging ? unsigned((c.max_ctx + kTile - 1) / kTile) : 0u;
+    check_kernel<<<dim3(recs / 256 + 1, unsigned(s.batch)), 256, 0, stream>>>(v, paging ? paging->block_table : nullptr,
+                                                                              paging ? paging->max_pages : 0,
+                                                                              paging ? paging->n_pages : 0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   for (int b0 = 0; b0 < s.batch; b0 += l.group) {
     v.b0 = b0;
     const unsigned nb = unsigned(s.batch - b0 < l.group ? s.batch - b0 : l.group), H = unsigned(s.n_kv_heads);
@@ -1751,7 +1776,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.vec = reinterpret_cast<uintptr_t>(r.kv_new) % 16 == 0 && r.ks0 % 8 == 0 && r.ks1 % 8 == 0 &&
             r.kv_v % 8 == 0 && r.ks_h % 8 == 0;
     r.old_tiles = (c.max_ctx + kKeys - 1) / kKeys;
-    if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, b0 > 0, stream)) != cudaSuccess) return e;
+    if (c.max_ctx > 0 && (e = launch_rebuild_any<D>(r, int64_t(nb) * H * r.old_tiles, checked || b0 > 0, stream)) != cudaSuccess) return e;
     r.units = int(nb * H);
     r.blocks = l.blocks;
     r.schedule.pairs = r.units * r.blocks;
@@ -1759,7 +1784,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
     r.schedule.cut = reinterpret_cast<int2*>(w + l.schedule);
     r.schedule.at = l.ctas ? reinterpret_cast<int*>(w + l.schedule + (size_t(l.ctas) + 1) * 8) : nullptr;
     const dim3 own(unsigned((c.n_new + kKeys - 1) / kKeys) * H + 1, 1, nb);
-    e = launch_after(b0 > 0 || c.max_ctx > 0, c.window ? chunk_image_kernel<D, true> : chunk_image_kernel<D, false>, own, 256,
+    e = launch_after(checked || b0 > 0 || c.max_ctx > 0, c.window ? chunk_image_kernel<D, true> : chunk_image_kernel<D, false>, own, 256,
                      (c.window ? 3 : 2) * kKeys * D * 2 + 128, stream, r);
     if (e != cudaSuccess) return e;
     AttnArgs a;

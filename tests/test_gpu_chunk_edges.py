@@ -58,3 +58,46 @@ def test_short_tail_in_a_call_planned_for_long_chunks(B, Hq, H, d, n_new, max_ct
         c.call()
         torch.cuda.synchronize()
         assert c.error_word() == 0 and torch.equal(c.out.view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("fault", [None, "ctx", "negative", "n_len", "page"])
+def test_fault_of_a_later_group_makes_every_output_nan(fault):
+    """Operand images of one sequence take more than 2 GB (max_ctx 640,000, of which little is used),
+    so each sequence is a group of its own; the last one's lengths or pages are wrong."""
+    B, Hq, H, d, n, pages = 3, 32, 8, 128, 40, 10000
+    g = torch.Generator().manual_seed(3)
+    shape = rq.make_shape(B, Hq, H, d, 2, 64 * pages, (2,))
+    table = torch.full((B, pages), -1, dtype=torch.int32)
+    table[:, :3] = torch.arange(9).view(3, 3)
+    ctx = torch.tensor([100, 0, 129], dtype=torch.int32)
+    lens = torch.tensor([n, 7, n], dtype=torch.int32)
+    if fault == "ctx":
+        ctx[2] = 64 * pages - n + 1
+    elif fault == "negative":
+        ctx[2] = -1
+    elif fault == "n_len":
+        lens[2] = n + 1
+    elif fault == "page":
+        table[2, 2] = 9
+    table = table.cuda()
+    signs = torch.ones(2, H, d)
+    cache = rq.PackedCache(shape, signs, n_pages=9)
+    new = torch.randn(B, n, 2, 2, H, d, generator=g).bfloat16().cuda()
+    paging = rq.make_paging(table, 9)
+    good = table.clone()
+    good[2, 2] = 8
+    states = torch.randn(B, 192, 2, 2, H, d, generator=g).bfloat16().cuda()
+    rq.paged_encode_append(shape, cache, rq.make_paging(good, 9), states)
+    q = torch.randn(B, n, Hq, d, generator=g).bfloat16().cuda()
+    out = torch.full_like(q, 776.0)
+    need = rq.chunk_workspace_bytes(shape, 0, n, 64 * pages - n)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    rq.paged_chunk_attention(shape, cache, paging, q, 0, new, ctx.cuda(), 64 * pages - n, out, ws, n_lens=lens.cuda())
+    torch.cuda.synchronize()
+    word = int(ws[:4].view(torch.int32).item())
+    if fault is None:
+        assert word == 0 and torch.isfinite(out.float()).all()
+    else:
+        assert word != 0
+        assert out[0].isnan().all() and out[1, :7].isnan().all() and out[2].isnan().all()
+    assert (out[1, 7:] == 776.0).all()
