@@ -112,30 +112,28 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t panel) {
 }
 constexpr uint32_t kMnB = 1u << 16;   // instruction descriptor: B's N index is contiguous
 
-// The levels s c + z of a word's codes as 16-byte chunks of the image (4-bit codes: one, 2-bit: two).
-// A code at bit k < 8 of a 16-bit half is the exact fp16 c 2^k after subtracting 1024, its power of
-// two folded into the step (below 2^-14 a step loses bits: at most 2^-17 in a level).
-template <int BITS>
+// The levels s c + z of a word's codes as 16-byte chunks of the image (4-bit codes: one, 2-bit: two),
+// each rounded once, whatever the step's size: code_pair_at gives the code itself, not its multiple by
+// the power of two of its bit position, which would leave its inverse to a step that fp16 holds exactly
+// only above 2^-8 (2-bit codes; states of 0.001 then had errors of 0.2 %).
 struct Steps {
-  __half2 s[4 / (BITS / 2)], z;
+  __half2 s, z;
   __device__ __forceinline__ explicit Steps(uint32_t meta) {
     const __half2 m = *reinterpret_cast<const __half2*>(&meta);
+    s = __low2half2(m);
     z = __high2half2(m);
-    s[0] = __low2half2(m);
-#pragma unroll
-    for (int i = 1; i < 8 / BITS; ++i) s[i] = __hmul2(s[i - 1], __float2half2_rn(BITS == 2 ? 0.25f : 0.0625f));
   }
 };
 template <int BITS>
-__device__ __forceinline__ void levels(uint32_t w, const Steps<BITS>& st, uint32_t* o) {
+__device__ __forceinline__ void levels(uint32_t w, const Steps& st, uint32_t* o) {
   constexpr uint32_t MASK = BITS == 2 ? 0x00030003u : 0x000F000Fu;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const uint32_t x = e ? w >> 8 : w;
 #pragma unroll
     for (int i = 0; i < 8 / BITS; ++i) {
-      const uint32_t c = code_pair_normal(x, MASK << (BITS * i));
-      const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&c), st.s[i], st.z);
+      const uint32_t c = code_pair_at(x, MASK, BITS * i);
+      const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&c), st.s, st.z);
       o[e * (8 / BITS) + i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
           if (RES) al = *reinterpret_cast<const uint16_t*>(res + kTile * (RROW + 4 * NG) + row * 2) * 0x10001u;
           al = on ? al : 0u;
           const __half2 a2 = *reinterpret_cast<const __half2*>(&al);
-          const Steps<4> steps(on ? *reinterpret_cast<const uint32_t*>(vr + kTile * D / 2 + (row * NG + g) * 4) : 0u);
+          const Steps steps(on ? *reinterpret_cast<const uint32_t*>(vr + kTile * D / 2 + (row * NG + g) * 4) : 0u);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {                      // units u0 + 2 k, + 1: 8 channels
             uint32_t o[4];
@@ -343,7 +341,7 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = 2 * rp + e;
-            const Steps<RES> steps(row < live ? *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + rg) * 4) : 0u);
+            const Steps steps(row < live ? *reinterpret_cast<const uint32_t*>(res + kTile * RROW + (row * NG + rg) * 4) : 0u);
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {                // a token's word of two units
               uint32_t o[16 / RES];
@@ -395,7 +393,7 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int g = D == 128 ? i : i % 2, jj = D == 128 ? part : 2 * part + i / 2;
-          const Steps<4> steps(*reinterpret_cast<const uint32_t*>(rec + kTile * D / 2 + (row * NG + g) * 4));
+          const Steps steps(*reinterpret_cast<const uint32_t*>(rec + kTile * D / 2 + (row * NG + g) * 4));
           uint32_t o[4];
           levels<4>(ws[i], steps, o);
           *reinterpret_cast<uint4*>(img + (g / 2) * L::kPanel + panel_offset(row, (g % 2) * 4 + jj)) =
@@ -416,7 +414,7 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             const int word = rpart * W + i, g = word % NG, jj = word / NG;
-            const Steps<RES> steps(*reinterpret_cast<const uint32_t*>(res + kTile * RROW + (rrow * NG + g) * 4));
+            const Steps steps(*reinterpret_cast<const uint32_t*>(res + kTile * RROW + (rrow * NG + g) * 4));
             uint32_t o[16 / RES];
             levels<RES>(ws[i], steps, o);
 #pragma unroll

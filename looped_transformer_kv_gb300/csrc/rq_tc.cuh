@@ -150,6 +150,17 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Two codes, at bit `k` of the halves of w (mask: at bit 0), as exact fp16 values: under 2^(10 - k)
+// a unit in bit k of the mantissa is worth 1.
+__device__ __forceinline__ uint32_t code_pair_at(uint32_t w, uint32_t mask, int k) {
+  const uint32_t base = 0x64006400u - 0x04000400u * uint32_t(k);
+  uint32_t t;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t) : "r"(w), "r"(mask << k), "r"(base));
+  uint32_t out;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(out) : "r"(t), "r"(base));
+  return out;
+}
+
 __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error below 2^-22; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -1,14 +1,19 @@
 """Chunk attention where its kernels meet: calls in a row, schedules of ragged batches, groups of
 sequences, the ends of the states' range, on the GPU."""
 
+import itertools
+
+import numpy as np
 import pytest
+
+import chunk_reference as R
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     from looped_transformer_kv_gb300 import rq  # noqa: F401
-    from test_gpu_chunk import Case
+    from test_gpu_chunk import Case, HALF16, HALFB
 
 
 def test_window_calls_back_to_back():
@@ -101,3 +106,78 @@ def test_fault_of_a_later_group_makes_every_output_nan(fault):
         assert word != 0
         assert out[0].isnan().all() and out[1, :7].isnan().all() and out[2].isnan().all()
     assert (out[1, 7:] == 776.0).all()
+
+
+# fp16 resolves 2^-24 below 2^-14: half a step, 2^-25, is what a rounding of a cached element costs at
+# least.  The cache's own steps and offsets are stored with that resolution.
+FLOOR16 = 2.0 ** -25
+
+
+def scaled_case(cached, own, B, Hq, H, d, bits, ctx, n_new, lens=None, **kw):
+    """Case with the cached states times `cached` and the chunk's times `own`."""
+    c = Case(B, Hq, H, d, bits, ctx, n_new, lens, **kw)
+    g = torch.Generator().manual_seed(11)
+    L = len(bits) + 1
+    x = torch.randn(B, max(ctx + [1]), 2, 1, H, d, generator=g)
+    x = (x + 0.1 * torch.randn(*x.shape[:3], L, H, d, generator=g)) * cached
+    for b in range(B):
+        if ctx[b]:
+            pos = torch.full((B, ctx[b]), -1, dtype=torch.int32)
+            pos[b] = torch.arange(ctx[b])
+            src = x[:, :ctx[b]].bfloat16().cuda()
+            if c.paging is not None:
+                rq.paged_encode_append(c.shape, c.cache, c.paging, src, positions=pos.cuda())
+            else:
+                rq.encode_append(c.shape, c.cache, src, positions=pos.cuda())
+    c.new_host = (c.new_host.float() * own).bfloat16()
+    c.new.copy_(c.new_host)
+    return c
+
+
+def check_small(c):
+    """Case.check, in which the roundings of cached elements cost at least FLOOR16: two of a reference
+    element (times a, below 2), one of a residual level and thus sqrt(d) of a channel, one of a rebuilt
+    element."""
+    assert c.error_word() == 0
+    G, d = c.Hq // c.H, c.d
+    out = c.out.double().cpu().numpy()
+    least = FLOOR16 * (5 + d ** 0.5)
+    for b, h in itertools.product(range(c.B), range(c.H)):
+        m, ctx = c.lens[b], c.ctx[b]
+        if m == 0:
+            continue
+        ref, p, mag, v = c.reference(b, h)
+        got = out[b, :m, h * G:(h + 1) * G]
+        rec = c.records(b, h)
+        rk, rv = (np.concatenate([R.residual_norms(rec, ctx, d, c.bits, c.loop, kv), np.zeros(m)]) for kv in (0, 1))
+        q = c.q_host[b, :m, h * G:(h + 1) * G].double().numpy()
+        e = HALF16 * (2 * mag + 4 * np.linalg.norm(q, axis=-1) * rk.max() * d ** -0.5)[..., None]
+        e += (np.abs(q).sum(-1) * least * d ** -0.5)[..., None] * (ctx > 0)
+        pv = np.einsum("jgt,td->jgd", p, np.abs(v))
+        tol = pv * (np.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[..., None]
+        tol += p[..., :ctx].sum(-1)[..., None] * least + HALFB * np.abs(ref) * 1.01 + 1e-38
+        worst = (np.abs(got - ref) / tol).max()
+        assert worst <= 1, (b, h, worst)
+
+
+SMALL_STATES = [
+    # B, Hq, H, d, bits, loop, ctx, n_new, lens: 8 rows and fewer; 9 to 128
+    (2, 4, 2, 128, (2,), 0, [3, 200], 2, [2, 1]),
+    (1, 8, 1, 64, (4, 2), 0, [70], 1, None),
+    (2, 4, 1, 128, (2, 4), 0, [1, 130], 9, None),
+    (1, 8, 1, 128, (4,), 0, [2], 8, None),
+    (1, 16, 1, 64, (2,), 0, [5], 4, None),
+    (2, 10, 2, 128, (2,), 1, [4, 65], 3, [3, 1]),
+]
+
+
+@pytest.mark.parametrize("scale", [1e-2, 1e-3, 1e-4, 1e-5])
+@pytest.mark.parametrize("case", range(len(SMALL_STATES)))
+def test_small_states(case, scale):
+    B, Hq, H, d, bits, loop, ctx, n, lens = SMALL_STATES[case]
+    c = scaled_case(scale, scale, B, Hq, H, d, bits, ctx, n, lens, loop=loop, paged=case % 2 == 0)
+    c.call()
+    torch.cuda.synchronize()
+    check_small(c)
+    if scale >= 1e-3:
+        c.check()                                    # (one rounding relative to the states)
