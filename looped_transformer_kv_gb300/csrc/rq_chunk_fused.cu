@@ -36,7 +36,6 @@ namespace {
 constexpr uint64_t kFuWaitLimitNs = 2000000000ull;
 constexpr int kFuRows = 128;
 constexpr int kRawStages = 4;
-constexpr float kFuSlack = 8.f;
 
 struct FusedArgs {
   const uint8_t* data;
@@ -481,8 +480,8 @@ __global__ void __launch_bounds__(768, 1) fused_kernel(const __grid_constant__ F
 #pragma unroll
         for (int x = 4; x < kTile; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(v[x]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (__any_sync(RQ_FULL_MASK, mt > m + kFuSlack)) {
-          const float mn = mt > m + kFuSlack ? mt : m;
+        if (__any_sync(RQ_FULL_MASK, mt > m + kWeightTop)) {
+          const float mn = mt > m + kWeightTop ? mt - kWeightHead : m;
           const float f = m == -INFINITY ? 0.f : ex2(m - mn);
           l *= f;
           m = mn;

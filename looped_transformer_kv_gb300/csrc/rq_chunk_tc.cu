@@ -24,7 +24,6 @@ namespace {
 constexpr int kKeys = 128;                 // keys per tile (two cache records)
 constexpr int kRows = 128;                 // query rows per tile
 constexpr float kStateMax = 65504.f;
-constexpr float kSlack = 8.f;              // log2 units a maximum may grow before O is rescaled
 constexpr uint64_t kTcWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
@@ -894,8 +893,8 @@ __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of w
 // of its key tiles, every K and V tile shared by the two.  Warps 0-3 and 4-7: softmax of row tile 0
 // and 1, a thread per row; warp 8: copies; warp 9: products.  While one row tile's softmax runs, the
 // other's products do:  S_0 S_1 | P_0 V, S_0' | P_1 V, S_1' | ...
-// The running maximum m is raised only when a tile exceeds it by 2^8 (O is rescaled in tensor
-// memory then; P stays below 2^8); P overwrites S's columns.  The softmax warps take registers
+// Weights are 2^(S - m); m is raised only when one would exceed 2^15, to make the tile's largest 2^7
+// (O is rescaled in tensor memory then); P overwrites S's columns.  The softmax warps take registers
 // from the others, so that a row's 128 scores stay in registers.
 // SCHED: the CTAs share the key tiles evenly (one CTA per SM): a block that lies in one CTA's range
 // is stored, the others leave their (m, l, O) for merge_kernel, at most two per CTA.  Else one CTA
@@ -1170,8 +1169,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 #pragma unroll
           for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          if (__any_sync(RQ_FULL_MASK, mt > m + kSlack)) {
-            const float mn = mt > m + kSlack ? mt : m;
+          if (__any_sync(RQ_FULL_MASK, mt > m + kWeightTop)) {
+            const float mn = mt > m + kWeightTop ? mt - kWeightHead : m;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
             l *= f;
             m = mn;

@@ -150,6 +150,11 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Softmax weights are fp16 operands 2^(S - m).  When a score exceeds m + kWeightTop, m becomes the
+// largest one less kWeightHead: the largest weight of a row lies between 2^7 and 2^15 (fp16 ends at
+// 2^16), a weight keeps 11 bits down to 2^-21 of it and is resolved to 2^-32 of it.
+constexpr float kWeightTop = 15.f, kWeightHead = 7.f;
+
 // Two codes, at bit `k` of the halves of w (mask: at bit 0), as exact fp16 values: under 2^(10 - k)
 // a unit in bit k of the mantissa is worth 1.
 __device__ __forceinline__ uint32_t code_pair_at(uint32_t w, uint32_t mask, int k) {

@@ -134,10 +134,10 @@ def scaled_case(cached, own, B, Hq, H, d, bits, ctx, n_new, lens=None, **kw):
     return c
 
 
-def check_small(c):
+def check_small(c, least_weight=0.0):
     """Case.check, in which the roundings of cached elements cost at least FLOOR16: two of a reference
     element (times a, below 2), one of a residual level and thus sqrt(d) of a channel, one of a rebuilt
-    element."""
+    element; and that of a softmax weight least_weight of the row's largest."""
     assert c.error_word() == 0
     G, d = c.Hq // c.H, c.d
     out = c.out.double().cpu().numpy()
@@ -155,6 +155,7 @@ def check_small(c):
         e += (np.abs(q).sum(-1) * least * d ** -0.5)[..., None] * (ctx > 0)
         pv = np.einsum("jgt,td->jgd", p, np.abs(v))
         tol = pv * (np.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[..., None]
+        tol += (least_weight * p.max(-1))[..., None] * np.maximum(np.abs(v), 1).sum(0)
         tol += p[..., :ctx].sum(-1)[..., None] * least + HALFB * np.abs(ref) * 1.01 + 1e-38
         worst = (np.abs(got - ref) / tol).max()
         assert worst <= 1, (b, h, worst)
@@ -181,3 +182,39 @@ def test_small_states(case, scale):
     check_small(c)
     if scale >= 1e-3:
         c.check()                                    # (one rounding relative to the states)
+
+
+# A weight below 2^-14 has steps of 2^-24, and a row's largest lies at 2^7 at least (the maximum that
+# weights refer to lags by up to 2^8 above that): half a step is 2^-32 of it.  With 8 rows and fewer the
+# decode kernel multiplies codes (to 15 of the reference, to 15 of a residual, its rotation sqrt(d) of
+# them) by fp16 pairs of weight x a x step, the largest weight at 2^0 at least: half a step is 2^-25 of a
+# unit of the code.
+LEAST_WEIGHT = 2.0 ** -32
+
+
+@pytest.mark.parametrize("Hq,H,d,bits,n_new", [
+    (4, 1, 128, (2,), 1), (2, 2, 64, (4,), 3),                     # 8 rows and fewer
+    (8, 2, 128, (2,), 3), (4, 1, 64, (4, 2), 4), (8, 2, 128, (), 8),   # to 128
+    (8, 2, 128, (2,), 40), (20, 4, 64, (4, 2), 40), (4, 1, 128, (), 70),   # more
+])
+def test_weights_far_below_the_largest(Hq, H, d, bits, n_new):
+    """A first token that takes nearly all of the weight (the others: about 2^-29 of its own each) and
+    whose value is zero: the output is what the small weights add up to."""
+    B, ctx = 2, 64
+    c = Case(B, Hq, H, d, bits, [ctx] * B, n_new, seed=d + n_new)
+    g = torch.Generator().manual_seed(n_new)
+    L = len(bits) + 1
+    x = torch.randn(B, ctx, 2, 1, H, d, generator=g).expand(-1, -1, -1, L, -1, -1).clone()
+    x += 0.1 * torch.randn(x.shape, generator=g)
+    u = torch.randint(0, 2, (d,), generator=g) * 2.0 - 1
+    x[:, :, 1] += 1
+    x[:, 0, 0] = 40 / d ** 0.5 * u
+    x[:, 0, 1] = 0
+    rq.encode_append(c.shape, c.cache, x.bfloat16().cuda())
+    c.q_host = (0.5 * u + 0.5 * torch.randn(c.q_host.shape, generator=g)).bfloat16()
+    c.q.copy_(c.q_host)
+    c.call()
+    torch.cuda.synchronize()
+    _, p, _, _ = c.reference(0, 0)
+    assert np.median(p[..., 1:ctx]) < 2.0 ** -26 and np.median(p[..., 0]) > 0.999
+    check_small(c, LEAST_WEIGHT if n_new * Hq // H > 8 else FLOOR16 * 15 * (1 + d ** 0.5))
