@@ -10,7 +10,8 @@
 //
 // Operands are fp16: a rebuilt element and a softmax weight are each rounded once (2^-11
 // relative); the queries are exact (a row's bf16 values times a power of two, undone in the
-// score's fp32 scale).  Collected weights need more: their scores take K as two fp16 parts.
+// score's fp32 scale), and a tile with new keys carries a power of two, so that small states keep their
+// bits.  Collected weights need more: their scores take K as two fp16 parts.
 #include <climits>
 
 #include "rq_common.cuh"
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kKeys = 128;                 // keys per tile (two cache records)
 constexpr int kRows = 128;                 // query rows per tile
-constexpr float kStateMax = 65504.f;
+constexpr unsigned kStateMaxBits = 0x477f0000u;   // the largest bf16 up to 65504, as fp32
 constexpr uint64_t kTcWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
@@ -37,6 +38,7 @@ struct ChunkView {     // what every kernel knows of the call
   const int32_t* ctx_lens;
   unsigned* err;
   int* first_bad;      // [B][H]: first chunk token out of range (0x7f7f7f7f: none)
+  uint16_t* exps;      // [unit][tile]: exponents of K's image, and of V's << 8
   int b0, H, heads, n_new, max_ctx, window, tiles;   // tiles: key tiles per (sequence, head)
 };
 
@@ -45,6 +47,17 @@ __device__ __forceinline__ bool lens_of(const ChunkView& v, int b, int& n, int& 
   ctx = v.ctx_lens[b];
   return n >= 0 && n <= v.n_new && ctx >= 0 && ctx <= v.max_ctx;
 }
+
+// Images carry a power of two per tile, undone in its scores' scale and between tiles of different ones
+// in O: new states may lie below fp16's normal range (2^-14), so a tile that holds any takes the largest
+// multiple of 16 that leaves its bound below 2^15.  A tile of which 1/2 or more is the largest has 0, as
+// cached ones always have (their steps and offsets are no finer than fp16's 2^-24 themselves).
+// bound: its fp32 bits.
+__device__ __forceinline__ int image_exponent(unsigned bound) {
+  const int x = int(bound >> 23);                        // in [2^(x - 127), 2^(x - 126))
+  return min(max(141 - x, 0) & ~15, 64);                 // (O, below 2^61, times 2^64 is still an fp32)
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
 // Lengths and block-table entries of the whole batch, where its sequences are handled in several
 // groups: what is wrong with a later one has to be known when the first group's outputs are stored.
@@ -235,8 +248,7 @@ struct RebuildSmem {
   static_assert(total <= 113 * 1024, "two CTAs per SM");
 };
 
-// 8 channels of chunk token t (K or V side) as fp16 pairs; a value out of range becomes 0 and `out`
-// the token, so that the images stay finite while its own and later rows become NaN.
+// 8 channels of a chunk token's K or V.
 __device__ __forceinline__ uint4 load_states(const uint16_t* src, bool vec) {
   if (vec) return *reinterpret_cast<const uint4*>(src);
   uint32_t w[4];
@@ -244,12 +256,32 @@ __device__ __forceinline__ uint4 load_states(const uint16_t* src, bool vec) {
   for (int k = 0; k < 4; ++k) w[k] = uint32_t(src[2 * k]) | (uint32_t(src[2 * k + 1]) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint32_t state_pair(uint32_t w, int t, int& out, uint32_t* lo = nullptr) {
-  float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
-  const bool b0 = !(fabsf(v0) <= kStateMax), b1 = !(fabsf(v1) <= kStateMax);
+// The values of chunk token t (those at or behind token n: zeros); one out of range (beyond 65504, or not
+// a number) becomes 0 and `out` the token, so that the images stay finite while its own and later rows
+// become NaN.
+__device__ __forceinline__ uint32_t state_in_range(uint32_t w, int t, int& out) {
+  const bool b0 = (w << 16 & 0x7fffffffu) > kStateMaxBits, b1 = (w & 0x7fff0000u) > kStateMaxBits;
   if (b0 | b1) out = min(out, t);
-  v0 = b0 ? 0.f : v0;
-  v1 = b1 ? 0.f : v1;
+  return w & (b0 ? 0xffff0000u : 0xffffffffu) & (b1 ? 0x0000ffffu : 0xffffffffu);
+}
+__device__ __forceinline__ uint4 states_in_range(uint4 w, int t, int n, int& out) {
+  if (t >= n) return make_uint4(0u, 0u, 0u, 0u);
+  return make_uint4(state_in_range(w.x, t, out), state_in_range(w.y, t, out), state_in_range(w.z, t, out),
+                    state_in_range(w.w, t, out));
+}
+// most: largest magnitudes so far, as bf16 pairs (not-a-number above infinity)
+__device__ __forceinline__ void most_states(uint4 w, uint32_t& most) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x[k] & 0x7fff7fffu));
+}
+// fp32 bits of the warp's largest magnitude.
+__device__ __forceinline__ unsigned warp_bound(uint32_t most) {
+  return __reduce_max_sync(RQ_FULL_MASK, max(most << 16, most & 0xffff0000u));
+}
+// A pair of them times `up` as fp16 (lo: and the rest of the value).
+__device__ __forceinline__ uint32_t state_pair(uint32_t w, float up, uint32_t* lo = nullptr) {
+  const float v0 = __uint_as_float(w << 16) * up, v1 = __uint_as_float(w & 0xffff0000u) * up;
   const uint32_t hi = half2_sat(v0, v1);
   if (lo) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
@@ -258,21 +290,83 @@ __device__ __forceinline__ uint32_t state_pair(uint32_t w, int t, int& out, uint
   return hi;
 }
 
+// Largest magnitudes of a cached key's levels z .. z + top s over its groups, and (SUM) their norm.
+template <int NG, bool SUM>
+__device__ __forceinline__ float level_bound(const uint8_t* meta, float top) {
+  float most = 0.f, sq = 0.f;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const float2 m = __half22float2(*reinterpret_cast<const __half2*>(meta + 4 * g));
+    const float x = fmaxf(fabsf(m.y), fabsf(fmaf(top, m.x, m.y)));
+    most = fmaxf(most, x);
+    sq = fmaf(x, x, sq);
+  }
+  return SUM ? sqrtf(float(kGroup) * sq) : most;
+}
+
+// A tile that holds cached and new keys: bounds of its K and V, into `bounds` (fp32 bits, 0 before).
+template <int D, int RES>
+__device__ __noinline__ void mixed_bounds(const RebuildArgs& a, int b, int h, int n, int ctx, int t0, int old,
+                                          const uint8_t* sec0, unsigned* bounds) {
+  constexpr int NG = D / 32, RROW = D * RES / 8;
+  constexpr int SIDE = kTile * (D / 2 + 4 * NG), RSIDE = kTile * (RROW + 4 * NG + 2);
+  constexpr int REF = kTile * (D + 8 * NG), SEC = REF + (RES ? 2 * RSIDE : 0);
+  unsigned found[2] = {0u, 0u};
+  if (int(threadIdx.x) < old) {
+    const uint8_t* const s = sec0 + (threadIdx.x >> 6) * SEC;
+    const int row = threadIdx.x & 63;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      float x = level_bound<NG, false>(s + kv * SIDE + kTile * D / 2 + row * NG * 4, 15.f);
+      if constexpr (RES != 0) {   // |x| <= |a| largest reference level + norm of the residual levels
+        const uint8_t* const r = s + REF + kv * RSIDE + kTile * RROW;
+        const float al = __half2float(*reinterpret_cast<const __half*>(r + kTile * 4 * NG + row * 2));
+        x = fmaf(fabsf(al), x, level_bound<NG, true>(r + row * NG * 4, RES == 2 ? 3.f : 15.f));
+      }
+      found[kv] = __float_as_uint(x);
+    }
+  }
+  uint32_t most[2] = {0u, 0u};
+  int out = INT_MAX;
+  constexpr int C = D / 8, U = 4;            // 16-byte chunks of a row; loads of each side in flight
+  const int end = min(n, t0 + kKeys - ctx);  // the tile's new tokens: 0 .. end
+  const uint16_t* const src = a.kv_new + b * a.ks0 + h * a.ks_h + 8 * (threadIdx.x % C);
+#pragma unroll 1
+  for (int t = threadIdx.x / C; t < end; t += U * 256 / C) {
+    uint4 y[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)         // (behind the last row: that one again)
+        y[u][kv] = load_states(src + int64_t(min(t + u * (256 / C), end - 1)) * a.ks1 + kv * a.kv_v, a.vec);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+        most_states(states_in_range(y[u][kv], 0, 1, out), most[kv]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const unsigned x = max(warp_bound(most[kv]), __reduce_max_sync(RQ_FULL_MASK, found[kv]));
+    if ((threadIdx.x & 31) == 0) atomicMax(bounds + kv, x);
+  }
+}
+
 // The chunk's own keys in the tile that holds the context's end: rows old .. 127 of the image in
 // shared memory (zeros behind the last token).  PART 0: K, 1: K's low parts, 2: V.
 template <int D, int PART>
 __device__ __noinline__ void mixed_rows(const RebuildArgs& a, int b, int h, int n, int ctx, int t0, int old,
-                                        uint8_t* img) {
+                                        float up, uint8_t* img) {
   int out = INT_MAX;
 #pragma unroll 1
   for (int i = old * (D / 8) + threadIdx.x; i < kKeys * (D / 8); i += 256) {
     const int key = i / (D / 8), c = i % (D / 8), t = t0 + key - ctx;
     const uint16_t* src = a.kv_new + (PART == 2 ? a.kv_v : 0) + b * a.ks0 + int64_t(min(t, n - 1)) * a.ks1 + h * a.ks_h + 8 * c;
-    uint4 y = load_states(src, a.vec);
-    if (t >= n) y = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 y = states_in_range(load_states(src, a.vec), t, n, out);
     uint32_t lo[4];
-    uint32_t w[4] = {state_pair(y.x, t, out, lo), state_pair(y.y, t, out, lo + 1), state_pair(y.z, t, out, lo + 2),
-                     state_pair(y.w, t, out, lo + 3)};
+    uint32_t w[4] = {state_pair(y.x, up, lo), state_pair(y.y, up, lo + 1), state_pair(y.z, up, lo + 2),
+                     state_pair(y.w, up, lo + 3)};
     if constexpr (PART < 2) {
       *reinterpret_cast<uint4*>(img + (c / 8) * (kKeys * 128) + panel_offset(key, c % 8)) =
           PART ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(w[0], w[1], w[2], w[3]);
@@ -314,31 +408,76 @@ __global__ void __launch_bounds__(256) chunk_image_kernel(const __grid_constant_
   const int c = tid % C;
   const uint16_t* const src = a.kv_new + b * a.ks0 + h * a.ks_h + 8 * c;
   uint4 y[IT], v[IT];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
+  auto load = [&](int i, uint4& yk, uint4& yv) {
     const uint16_t* p = src + int64_t(min(t0 + (tid + 256 * i) / C, n - 1)) * a.ks1;
-    y[i] = load_states(p, a.vec);
-    v[i] = load_states(p + a.kv_v, a.vec);
-  }
-  int out = INT_MAX;
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int key = (tid + 256 * i) / C, t = t0 + key;
-    if (t >= n) y[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    yk = load_states(p, a.vec);
+    yv = load_states(p + a.kv_v, a.vec);
+  };
+  auto convert = [&](int i, const uint4& yk, const uint4& yv, float up_k, float up_v) {
+    const int key = (tid + 256 * i) / C;
     uint32_t lo[4];
-    const uint4 hi = make_uint4(state_pair(y[i].x, t, out, lo), state_pair(y[i].y, t, out, lo + 1),
-                                state_pair(y[i].z, t, out, lo + 2), state_pair(y[i].w, t, out, lo + 3));
+    const uint4 hi = make_uint4(state_pair(yk.x, up_k, lo), state_pair(yk.y, up_k, lo + 1),
+                                state_pair(yk.z, up_k, lo + 2), state_pair(yk.w, up_k, lo + 3));
     const uint32_t o = (c / 8) * (kKeys * 128) + panel_offset(key, c % 8);
     *reinterpret_cast<uint4*>(img + o) = hi;
     if (KLO) *reinterpret_cast<uint4*>(img_lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     *reinterpret_cast<uint4*>(rows + key * (D * 2) + c * 16) =
-        make_uint4(state_pair(v[i].x, t, out), state_pair(v[i].y, t, out), state_pair(v[i].z, t, out),
-                   state_pair(v[i].w, t, out));
+        make_uint4(state_pair(yv.x, up_v), state_pair(yv.y, up_v), state_pair(yv.z, up_v), state_pair(yv.w, up_v));
+  };
+  __shared__ unsigned bounds[2][8];
+  auto block_bound = [&](uint32_t most_k, uint32_t most_v, unsigned& k, unsigned& v) {
+    most_k = warp_bound(most_k);
+    most_v = warp_bound(most_v);
+    if (tid % 32 == 0) {
+      bounds[0][tid / 32] = most_k;
+      bounds[1][tid / 32] = most_v;
+    }
+    fence_async_smem();
+    __syncthreads();
+    k = __reduce_max_sync(RQ_FULL_MASK, bounds[0][tid % 8]);
+    v = __reduce_max_sync(RQ_FULL_MASK, bounds[1][tid % 8]);
+  };
+#pragma unroll
+  for (int i = 0; i < IT; ++i) load(i, y[i], v[i]);
+  uint32_t most_k = 0u, most_v = 0u;
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    if (t0 + (tid + 256 * i) / C >= n) y[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    most_states(y[i], most_k);
+    most_states(v[i], most_v);
+    convert(i, y[i], v[i], 1.f, 1.f);
   }
-  if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
-  fence_async_smem();
-  __syncthreads();
-  const int64_t at = ((int64_t(blockIdx.z) * a.v.H + h) * a.v.tiles + tile) * IMG;
+  unsigned bound_k, bound_v;
+  block_bound(most_k, most_v, bound_k, bound_v);
+  int ek = 0, ev = 0;
+  if (image_exponent(bound_k) | image_exponent(bound_v) || max(bound_k, bound_v) > kStateMaxBits) {
+    // a few tiles: once more, without what is out of range and with their powers of two
+    int out = INT_MAX;
+    uint4 yk, yv;
+    most_k = most_v = 0u;
+#pragma unroll 1
+    for (int i = 0; i < IT; ++i) {
+      load(i, yk, yv);
+      most_states(states_in_range(yk, t0 + (tid + 256 * i) / C, n, out), most_k);
+      most_states(states_in_range(yv, t0 + (tid + 256 * i) / C, n, out), most_v);
+    }
+    if (out != INT_MAX) atomicMin(a.v.first_bad + int64_t(b) * a.v.H + h, out);
+    __syncthreads();                            // (the bounds have been read)
+    block_bound(most_k, most_v, bound_k, bound_v);
+    ek = image_exponent(bound_k);
+    ev = image_exponent(bound_v);
+#pragma unroll 1
+    for (int i = 0; i < IT; ++i) {
+      const int t = t0 + (tid + 256 * i) / C;
+      load(i, yk, yv);
+      convert(i, states_in_range(yk, t, n, out), states_in_range(yv, t, n, out), power_of_two(ek), power_of_two(ev));
+    }
+    fence_async_smem();
+    __syncthreads();
+  }
+  const int64_t key_tile = (int64_t(blockIdx.z) * a.v.H + h) * a.v.tiles + tile;
+  if (tid == 0) a.v.exps[key_tile] = uint16_t(ek | ev << 8);
+  const int64_t at = key_tile * IMG;
   if (tid == 0) {
     bulk_s2g(a.k + at, smem_u32(img), IMG);
     if (KLO) bulk_s2g(a.klo + at, smem_u32(img_lo), IMG);
@@ -394,7 +533,9 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
   const uint32_t loaded = smem_u32(bars), kdone = loaded + 8, vdone = loaded + 16;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 3);
-  float* const sign = reinterpret_cast<float*>(smem + L::sign);            // [2][D], / sqrt(d)
+  float* const sign = reinterpret_cast<float*>(smem + L::sign);            // [2][D], / sqrt(d), times `up`
+  unsigned* const bounds = reinterpret_cast<unsigned*>(bars + 4);          // of a tile with new keys
+  float* const up = reinterpret_cast<float*>(bars + 5);                    // [2]: powers of two of the images
   float2* const az = reinterpret_cast<float2*>(smem + L::az);              // [pair][group][parity]
   const int tid = threadIdx.x, warp = tid >> 5;
   const int r = tid & 127, hh = tid >> 7;
@@ -450,8 +591,9 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
   int bl_known = -1, n = 0, ctx = 0;
   bool lens_good = false;
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    // heads first: the heads of a chunk token lie next to each other
-    const int h = item % a.v.H, tile = item / a.v.H % a.old_tiles, bl = item / a.v.H / a.old_tiles;
+    // heads first: the heads of a chunk token lie next to each other; the last tile, which may hold new
+    // keys and then takes longer, before the others
+    const int h = item % a.v.H, tile = a.old_tiles - 1 - item / a.v.H % a.old_tiles, bl = item / a.v.H / a.old_tiles;
     const int b = a.v.b0 + bl, unit = bl * a.v.H + h;
     if (bl != bl_known) {
       bl_known = bl;
@@ -477,7 +619,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
       // the sections of the next tile of this sequence come to L2 meanwhile
       const int next = item + gridDim.x;
       if (next < n_items && next / a.v.H / a.old_tiles == bl) {
-        const int nh = next % a.v.H, nt = next / a.v.H % a.old_tiles;
+        const int nh = next % a.v.H, nt = a.old_tiles - 1 - next / a.v.H % a.old_tiles;
         for (int i = 0; i < 2 && nt * kKeys + i * kTile < ctx; ++i) {
           const uint8_t* src = record(b, nh, nt, i);
           bulk_prefetch(src, L::kRef);
@@ -487,11 +629,25 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
       bulk_s2g_wait_read();       // the last tile's image has left
     }
     if (tid < 2 * D) sign[tid] = float(a.signs[tid / D][int64_t(h) * D + tid % D]) * inv_sqrt_d;
+    if (tid < 2) {
+      bounds[tid] = 0u;
+      up[tid] = 1.f;
+    }
     __syncthreads();
     constexpr int LOW = KLO && RES ? 16 * NG / 2 : 1;   // fp16 pairs of low parts a thread keeps
     uint32_t e_lo[LOW];
     {
       failed = !mbar_wait_bounded(loaded, phase, kTcWaitLimitNs);
+      if (old < kKeys) {
+        mixed_bounds<D, RES>(a, b, h, n, ctx, t0, old, sec0, bounds);
+        __syncthreads();
+        if (tid < 2 * D) sign[tid] *= power_of_two(image_exponent(bounds[tid / D]));
+        if (tid < 2) up[tid] = power_of_two(image_exponent(bounds[tid]));
+        __syncthreads();
+      }
+      if (tid == 0)
+        a.v.exps[int64_t(unit) * a.v.tiles + tile] =
+            old < kKeys ? uint16_t(image_exponent(bounds[0]) | image_exponent(bounds[1]) << 8) : uint16_t(0);
       if constexpr (RES != 0) {   // E of K: a thread per key and half its words
         constexpr int PER = 32 / RES, CPW = PER / 8;      // codes and 16-byte chunks per word
         const int key = tid >> 1;
@@ -532,6 +688,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
         float al = 1.f;
         if (RES)
           al = __half2float(*reinterpret_cast<const __half*>(s + L::kRef + RSIDE + kTile * (RROW + 4 * NG) + (t & 63) * 2));
+        al *= up[1];
         // (the odd key's code sits 16 bits higher in its word)
         az[((t >> 1) * NG + g) * 2 + (t & 1)] = make_float2((t & 1) ? m.x * al * 0x1p-16f : m.x * al, m.y * al);
       }
@@ -642,6 +799,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
       const int row = r & 63;
       float al = 1.f;
       if (RES) al = __half2float(*reinterpret_cast<const __half*>(sec + L::kRef + kTile * (RROW + 4 * NG) + row * 2));
+      al *= up[0];
       // words 2 hh and 2 hh + 1 of every group
       uint32_t w[2][NG];
       if constexpr (NG == 4) {   // (odd row pairs read them in the other order: distinct banks)
@@ -704,7 +862,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
     // the chunk's own keys of the last cached tile over the rows behind the context
     if (old < kKeys) {
       __syncthreads();
-      mixed_rows<D, 0>(a, b, h, n, ctx, t0, old, smem + L::e);
+      mixed_rows<D, 0>(a, b, h, n, ctx, t0, old, up[0], smem + L::e);
     }
     fence_async_smem();
     if (__syncthreads_or(failed)) {
@@ -721,7 +879,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
       k_image(smem + L::v, true);
       if (old < kKeys) {
         __syncthreads();
-        mixed_rows<D, 1>(a, b, h, n, ctx, t0, old, smem + L::v);
+        mixed_rows<D, 1>(a, b, h, n, ctx, t0, old, up[0], smem + L::v);
       }
       fence_async_smem();
       __syncthreads();
@@ -773,7 +931,7 @@ __global__ void __launch_bounds__(256, 2) rebuild_kernel(const __grid_constant__
     }
     if (old < kKeys) {
       __syncthreads();
-      mixed_rows<D, 2>(a, b, h, n, ctx, t0, old, smem + L::v);
+      mixed_rows<D, 2>(a, b, h, n, ctx, t0, old, up[1], smem + L::v);
     }
     fence_async_smem();
     tc_fence_before();
@@ -881,6 +1039,8 @@ template <int D>
 __device__ __forceinline__ int o_image_offset(int r, int c) {
   return r * (D * 4) + ((c ^ (r & (D / 4 - 1))) << 4);
 }
+
+__device__ __forceinline__ uint32_t times(uint32_t x, float f) { return __float_as_uint(__uint_as_float(x) * f); }
 
 __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of warpgroup 0 or 1
   if (i == 0)
@@ -1120,6 +1280,9 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
       const int row = w.r0 + i * kRows + r;
       const bool valid = row < x.rows;
       float m = -INFINITY, l = 0.f;
+      int ev = 0;                                                    // O's exponent
+      const uint16_t* const exps_of = a.v.exps + int64_t(w.unit) * a.v.tiles + w.kt0;
+      int exps32 = lane < w.T ? exps_of[lane] : 0;                    // a lane's of the next 32 tiles
       if (w.T > 0) {
         if (i == 0 || w.two)
           store_queries<D>(
@@ -1142,6 +1305,9 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         const int lim = x.ctx + min((row + x.first) / a.v.heads, x.n - 1);   // last key the row sees
         const int clear = x.ctx + min((w.r0 + i * kRows + x.first) / a.v.heads, x.n - 1);   // every row of the tile sees these
         for (int jt = 0; jt < w.T; ++jt, ++ci) {
+          if ((jt & 31) == 0 && jt > 0) exps32 = jt + lane < w.T ? exps_of[jt + lane] : 0;
+          const int tile_exps = __shfl_sync(RQ_FULL_MASK, exps32, jt & 31), tile_ev = tile_exps >> 8;
+          const float ct = c * power_of_two(-(tile_exps & 255));
           if (!mbar_wait_bounded(sready(i, ci), (ci >> 1) & 1, kTcWaitLimitNs)) {
             failed = true;
             break;
@@ -1168,12 +1334,14 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
               mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
 #pragma unroll
           for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          if (__any_sync(RQ_FULL_MASK, mt > m + kWeightTop)) {
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
+          if (__any_sync(RQ_FULL_MASK, mt > m + kWeightTop) || (!LSE && tile_ev != ev)) {
             const float mn = mt > m + kWeightTop ? mt - kWeightHead : m;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
             l *= f;
             m = mn;
+            const float fo = f * power_of_two(tile_ev - ev);
+            ev = tile_ev;
             if (!LSE && jt > 0) {
 #pragma unroll 1
               for (int y = 0; y < D / 16; ++y) {
@@ -1181,13 +1349,13 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
                 tc_ld16(tO + 16 * y, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * fo);
                 tc_st16(tO + 16 * y, o);
               }
             }
           }
           const float ms = m == -INFINITY ? 0.f : -m;
-          const uint64_t c2 = pack2(c, c), m2 = pack2(ms, ms);
+          const uint64_t c2 = pack2(ct, ct), m2 = pack2(ms, ms);
           uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -1216,7 +1384,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         tc_fence_after();
       }
       // ---- store (a wait that gave up: NaN)
-      const float nan = __int_as_float(0x7fc00000);
+      const float nan = __int_as_float(0x7fc00000), down = power_of_two(-ev);
       const bool there = w.T > 0 && !failed;                         // O holds the segment's sums
       const int j = (row + x.first) / a.v.heads;
       const bool bad = !x.ok || flagged || failed || (valid && j >= a.v.first_bad[int64_t(x.b) * a.v.H + x.h]);
@@ -1242,7 +1410,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
 #pragma unroll
             for (int z = 0; z < 8; ++z)
               *reinterpret_cast<uint4*>(img + o_image_offset<HALF>(r, 8 * y + z)) =
-                  make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+                  make_uint4(times(o[4 * z], down), times(o[4 * z + 1], down), times(o[4 * z + 2], down),
+                             times(o[4 * z + 3], down));
           }
           fence_async_smem();
           warpgroup_barrier(i);
@@ -1255,7 +1424,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         }
       } else {
         constexpr int CR = D / 8;                                    // 16-byte chunks of a row of bf16
-        const float inv = bad ? nan : 1.f / l;
+        const float inv = bad ? nan : down / l;
 #pragma unroll 1
         for (int y = 0; y < D / 32; ++y) {
           uint32_t o[32];
@@ -1560,6 +1729,7 @@ __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__
     const uint32_t lanes = uint32_t(warp & 3) << 21;
     // rows before this one do not see the key
     const int row_min = max(0, key - ctx - j0) * a.v.heads;
+    const float down = power_of_two(-(a.v.exps[unit * a.v.tiles + blockIdx.x] & 255));
     for (int j = i; j < T; j += 2) {
       const int s = j % L::kStages;
       if (!mbar_wait_bounded(sready(i), (j >> 1) & 1, kTcWaitLimitNs) ||
@@ -1579,8 +1749,8 @@ __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__
 #pragma unroll
         for (int y = 0; y < 32; y += 2) {
           const float4 f = sc[(32 * x + y) / 2];
-          const float p0 = ex2(fmaf(__uint_as_float(v[y]), f.x, f.y));
-          const float p1 = ex2(fmaf(__uint_as_float(v[y + 1]), f.z, f.w));
+          const float p0 = ex2(fmaf(__uint_as_float(v[y]) * down, f.x, f.y));
+          const float p1 = ex2(fmaf(__uint_as_float(v[y + 1]) * down, f.z, f.w));
           sum[0] += 32 * x + y >= rel ? p0 : 0.f;
           sum[1] += 32 * x + y + 1 >= rel ? p1 : 0.f;
         }
@@ -1613,7 +1783,7 @@ constexpr size_t kGroupBytes = size_t(4) << 30;   // images of the sequences han
 struct TcLayout {
   int group;               // sequences handled together
   int tiles, blocks, r_tiles, wblocks, q_tiles, splits, wsplits, ctas;   // ctas: of the scheduled attention, or 0
-  size_t first_bad, schedule, k, klo, val, part, stats, qimg, scale, total;
+  size_t first_bad, exps, schedule, k, klo, val, part, stats, qimg, scale, total;
 };
 
 constexpr int kMaxPairs = 8192;   // scheduled row blocks, at most: more keep every SM busy as they are
@@ -1659,6 +1829,8 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   size_t o = kWsHeaderBytes;
   l.first_bad = o;
   o = round1k(o + size_t(s.batch) * s.n_kv_heads * 4);
+  l.exps = o;
+  o = round1k(o + units * l.tiles * 2);
   l.schedule = o;
   if (l.ctas) o = round1k(o + (size_t(l.ctas) + 1) * 8 + (size_t(pairs) + 1) * 4);
   l.k = o;
@@ -1732,6 +1904,7 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
   v.ctx_lens = c.ctx_lens;
   v.err = reinterpret_cast<unsigned*>(w);
   v.first_bad = reinterpret_cast<int*>(w + l.first_bad);
+  v.exps = reinterpret_cast<uint16_t*>(w + l.exps);
   v.H = s.n_kv_heads;
   v.heads = s.n_q_heads / s.n_kv_heads;
   v.n_new = c.n_new;

@@ -134,10 +134,11 @@ def scaled_case(cached, own, B, Hq, H, d, bits, ctx, n_new, lens=None, **kw):
     return c
 
 
-def check_small(c, least_weight=0.0):
+def check_small(c, least_weight=0.0, least_new=0.0):
     """Case.check, in which the roundings of cached elements cost at least FLOOR16: two of a reference
     element (times a, below 2), one of a residual level and thus sqrt(d) of a channel, one of a rebuilt
-    element; and that of a softmax weight least_weight of the row's largest."""
+    element; that of a softmax weight least_weight of the row's largest, of an element beside larger ones
+    least_new of the largest."""
     assert c.error_word() == 0
     G, d = c.Hq // c.H, c.d
     out = c.out.double().cpu().numpy()
@@ -153,7 +154,10 @@ def check_small(c, least_weight=0.0):
         q = c.q_host[b, :m, h * G:(h + 1) * G].double().numpy()
         e = HALF16 * (2 * mag + 4 * np.linalg.norm(q, axis=-1) * rk.max() * d ** -0.5)[..., None]
         e += (np.abs(q).sum(-1) * least * d ** -0.5)[..., None] * (ctx > 0)
-        pv = np.einsum("jgt,td->jgd", p, np.abs(v))
+        k = np.concatenate([R.rebuild(rec, ctx, d, c.bits, c.loop, 0, c.signs[0, h].numpy()),
+                            c.new_host[b, :m, 0, c.loop, h].double().numpy()])
+        e += (np.abs(q).sum(-1) * least_new * np.abs(k).max() * d ** -0.5)[..., None]
+        pv = np.einsum("jgt,td->jgd", p, np.abs(v)) + least_new / HALF16 * np.abs(v).max()
         tol = pv * (np.expm1(2 * e) + 3 * HALF16 + 1e-5) + 3 * HALF16 * (p @ rv)[..., None]
         tol += (least_weight * p.max(-1))[..., None] * np.maximum(np.abs(v), 1).sum(0)
         tol += p[..., :ctx].sum(-1)[..., None] * least + HALFB * np.abs(ref) * 1.01 + 1e-38
@@ -218,3 +222,54 @@ def test_weights_far_below_the_largest(Hq, H, d, bits, n_new):
     _, p, _, _ = c.reference(0, 0)
     assert np.median(p[..., 1:ctx]) < 2.0 ** -26 and np.median(p[..., 0]) > 0.999
     check_small(c, LEAST_WEIGHT if n_new * Hq // H > 8 else FLOOR16 * 15 * (1 + d ** 0.5))
+
+
+SMALL_MANY = [
+    # B, Hq, H, d, bits, loop, ctx, n_new, lens
+    (1, 2, 2, 128, (2,), 0, [0], 200, None),
+    (2, 8, 2, 128, (4, 2), 0, [0, 70], 40, [40, 33]),
+    (1, 10, 2, 64, (2,), 1, [3], 65, None),
+    (2, 4, 2, 64, (4,), 0, [0, 129], 129, [7, 129]),
+]
+
+
+# A tile's operands carry a power of two that takes its largest element to 2^-1 or more: half a step,
+# 2^-25, is 2^-24 of it.
+LEAST_NEW = 2.0 ** -24
+
+
+@pytest.mark.parametrize("window", [0, 3])
+@pytest.mark.parametrize("cached,own", [(1e-3, 1e-3), (1e-5, 1e-5), (1, 1e-5), (1e-3, 2e-8), (1e-4, 1e-20),
+                                        (1e-20, 1e-12), (1, 6000)])
+@pytest.mark.parametrize("case", range(len(SMALL_MANY)))
+def test_many_rows_of_states_of_any_size(case, cached, own, window):
+    """New states of any size that their bf16 has (6000: the largest near 25,000) keep one rounding of
+    2^-11, or LEAST_NEW of the largest."""
+    B, Hq, H, d, bits, loop, ctx, n, lens = SMALL_MANY[case]
+    c = scaled_case(cached, own, B, Hq, H, d, bits, ctx, n, lens, loop=loop, window=window, paged=case % 2 == 1)
+    if own > 1:
+        c.q_host = (c.q_host.float() / 4000).bfloat16()       # (scores of a softmax still)
+        c.q.copy_(c.q_host)
+    c.call()
+    torch.cuda.synchronize()
+    check_small(c, least_new=LEAST_NEW)
+    if window:
+        c.check_weights()
+
+
+@pytest.mark.parametrize("ctx", [0, 70])
+@pytest.mark.parametrize("value", [float("nan"), float("-inf"), 7e4])
+def test_token_out_of_range_among_small_states(ctx, value):
+    """Its magnitude does not count for the tile's power of two: the rows before it keep their bits."""
+    args = (1e-3, 1e-5, 1, 4, 2, 128, (2,), [ctx], 200)
+    c, clean, at = scaled_case(*args), scaled_case(*args), 37
+    for kv in (0, 1):
+        c.new[0, at + 90 * kv, kv, 0, kv, 5 + kv] = value
+    c.call()
+    clean.call()
+    torch.cuda.synchronize()
+    assert c.error_word() == 0
+    assert c.out[0, at:, :2].isnan().all() and c.out[0, at + 90:, 2:].isnan().all()
+    c.out[0, at:, :2] = clean.out[0, at:, :2]
+    c.out[0, at + 90:, 2:] = clean.out[0, at + 90:, 2:]
+    check_small(c, least_new=LEAST_NEW)
