@@ -327,8 +327,9 @@ rq_status rq_evict_compact(const rq_shape* shape, const rq_cache* cache, const r
 /* The same on paged caches.  In place: the same data, block table and page count (the pages
  * behind the kept rows are then free); pages that several sequences share must not be
  * compacted in place.  Within one pool rows may also move to other pages: two block tables
- * with no page in common (so shared pages can be read, and each sequence gets its own).  A block-table entry outside [0, n_pages) is never dereferenced: its rows
- * are left as they were. */
+ * with no page in common (so shared pages can be read, and each sequence gets its own).  The same
+ * data and block table with another capacity or page count are refused (RQ_ERR_INVALID_ARG).  A
+ * block-table entry outside [0, n_pages) is never dereferenced: its rows are left as they were. */
 rq_status rq_paged_evict_compact(const rq_shape* shape, const rq_cache* cache,
                                  const rq_paging* paging, const rq_shape* to_shape,
                                  const rq_cache* to, const rq_paging* to_paging,

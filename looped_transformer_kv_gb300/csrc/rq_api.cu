@@ -225,8 +225,9 @@ rq_status compact_common(const rq_shape* shape, const rq_cache* cache, const rq_
     if (shape->res_bits[l] != to_shape->res_bits[l]) return RQ_ERR_INVALID_ARG;
   bool in_place = cache->data == to->data && shape->capacity == to_shape->capacity;
   if (paging) {
-    in_place = in_place && paging->block_table == to_paging->block_table &&
-               paging->n_pages == to_paging->n_pages;
+    const bool one = cache->data == to->data && paging->block_table == to_paging->block_table;
+    in_place = in_place && one && paging->n_pages == to_paging->n_pages;
+    if (one && !in_place) return RQ_ERR_INVALID_ARG;   // (the same pages, with nothing to order the moves)
   } else if (!in_place) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(cache->data), a1 = a0 + rq_cache_bytes(shape);
     const uintptr_t b0 = reinterpret_cast<uintptr_t>(to->data), b1 = b0 + rq_cache_bytes(to_shape);

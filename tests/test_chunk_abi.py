@@ -168,3 +168,20 @@ def test_compact_paging_is_validated(lib):
     h = lib.RqPaging()
     h.block_table, h.max_pages, h.n_pages = 16, 2, 8            # to's capacity is one page
     assert _compact(lib, paged=True, g=g, tg=h) == INVALID
+
+
+def test_compact_within_the_same_pages_under_another_plan_is_refused(lib):
+    """One pool and one block table, but another capacity or page count: not in place, and the rows would
+    move among the same pages unordered."""
+    g = lib.RqPaging()
+    g.block_table, g.max_pages, g.n_pages = 16, 2, 8
+    h = lib.RqPaging()
+    h.block_table, h.max_pages, h.n_pages = 16, 1, 8
+    one = _cache(lib)
+    for batch in (1, 2):
+        s, ts = _shape(batch=batch), _shape(batch=batch, capacity=64)
+        assert _compact(lib, paged=True, s=s, c=one, g=g, ts=ts, t=_cache(lib), tg=h) == INVALID
+        assert _compact(lib, paged=True, s=ts, c=one, g=h, ts=s, t=_cache(lib), tg=g) == INVALID
+        h2 = lib.RqPaging()
+        h2.block_table, h2.max_pages, h2.n_pages = 16, 2, 9
+        assert _compact(lib, paged=True, s=s, c=one, g=g, ts=s, t=_cache(lib), tg=h2) == INVALID
