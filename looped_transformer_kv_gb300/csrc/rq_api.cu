@@ -178,8 +178,8 @@ rq_status chunk_common(const rq_shape* shape, const rq_cache* cache, const rq_pa
   const int64_t ke[5] = {shape->batch, c.n_new, 2, shape->n_loops, shape->n_kv_heads};
   if (!strides_ok(c.q_strides, qe, 3) || !strides_ok(c.kv_strides, ke, 5)) return RQ_ERR_INVALID_ARG;
   if (c.n_new == 0) return RQ_OK;
-  if (!ws || ws_bytes < rq_chunk_workspace_bytes(shape, c.loop, c.n_new, c.max_ctx, c.window))
-    return RQ_ERR_WORKSPACE;
+  const rq::ChunkPath path = rq::chunk_path_within(*shape, c.loop, c.n_new, c.max_ctx, c.window, ws_bytes);
+  if (!ws || path == rq::ChunkPath::kNone) return RQ_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RQ_ERR_WORKSPACE;
   // rows are read while others are written
   const uintptr_t o0 = reinterpret_cast<uintptr_t>(c.out);
@@ -188,7 +188,8 @@ rq_status chunk_common(const rq_shape* shape, const rq_cache* cache, const rq_pa
       overlaps(c.kv_new, c.kv_strides, ke, 5, shape->head_dim, o0, o1))
     return RQ_ERR_INVALID_ARG;
   try {
-    return from_cuda(rq::launch_chunk(*shape, *cache, paging, c, ws, static_cast<cudaStream_t>(stream)));
+    return from_cuda(rq::launch_chunk(*shape, *cache, paging, c, path, ws, ws_bytes,
+                                      static_cast<cudaStream_t>(stream)));
   } catch (...) {
     return RQ_ERR_INTERNAL;
   }

@@ -261,21 +261,28 @@ struct RowsLayout {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
+// The best plan within `budget`, else one split.
+RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int window, size_t budget) {
   RowsLayout l;
   const int heads = s.n_q_heads / s.n_kv_heads;
   l.plan = plan_splits_chunk(s, loop, heads * n_new, max_ctx);
-  const size_t units = size_t(s.batch) * s.n_kv_heads;
-  size_t o = kWsHeaderBytes;
-  l.part = o;
-  o = round256(o + units * heads * n_new * l.plan.n_splits * partial_floats(s) * sizeof(float));
   l.score_stride = (int64_t(max_ctx) + n_new + 31) / 32 * 32;
-  l.scores = o;
-  o = round256(o + units * heads * window * size_t(l.score_stride) * sizeof(float));
-  l.lse = o;
-  o = round256(o + units * heads * window * sizeof(float));
-  l.total = o;
-  return l;
+  const size_t units = size_t(s.batch) * s.n_kv_heads;
+  const int tiles = max_ctx > 0 ? (max_ctx + kTile - 1) / kTile : 1;
+  for (;;) {
+    size_t o = kWsHeaderBytes;
+    l.part = o;
+    o = round256(o + units * heads * n_new * l.plan.n_splits * partial_floats(s) * sizeof(float));
+    l.scores = o;
+    o = round256(o + units * heads * window * size_t(l.score_stride) * sizeof(float));
+    l.lse = o;
+    o = round256(o + units * heads * window * sizeof(float));
+    l.total = o;
+    if (o <= budget || l.plan.n_splits == 1) return l;
+    const int per = (tiles + l.plan.n_splits - 2) / (l.plan.n_splits - 1);
+    l.plan.tokens_per_split = per * kTile;
+    l.plan.n_splits = (tiles + per - 1) / per;
+  }
 }
 
 }  // namespace
@@ -289,8 +296,6 @@ RowsLayout rows_layout(const rq_shape& s, int loop, int n_new, int max_ctx, int 
 //   (about 0.35 us each), so beyond 32 of them the context must be worth it: 64 tokens after 2048
 //   46 us against 52 (1 x 16), after 512 118 against 95 (16 x 16); 128 after 8192 263 against 369.
 // - kTiles: K and V rebuilt once, for everything else.
-enum class ChunkPath { kStream, kFused, kTiles };
-
 ChunkPath chunk_path(const rq_shape& s, int n_new, int max_ctx, int window) {
   const int64_t rows = int64_t(s.n_q_heads / s.n_kv_heads) * n_new;
   if (rows <= (window > 0 ? 32 : 8)) return ChunkPath::kStream;
@@ -298,27 +303,64 @@ ChunkPath chunk_path(const rq_shape& s, int n_new, int max_ctx, int window) {
   return ChunkPath::kTiles;
 }
 
+namespace {
+
+size_t path_bytes(ChunkPath path, const rq_shape& s, int loop, int n_new, int max_ctx, int window, size_t budget) {
+  if (path == ChunkPath::kTiles) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window, budget);
+  if (path == ChunkPath::kFused) return chunk_fused_workspace_bytes(s, loop, n_new, max_ctx, budget);
+  return rows_layout(s, loop, n_new, max_ctx, window, budget).total;
+}
+
+}  // namespace
+
+// The way a call with this much workspace runs.  Less than its best plan takes means fewer splits or
+// smaller groups, then another way that fits.  A call never needs more than chunk_workspace_bytes gives
+// one with more new tokens, more context or a longer window: each way's least need grows with the sizes,
+// each way that the larger call may take is open to the smaller one too (kTiles and kStream take any
+// rows), and where a smaller one can only stream, the larger one's size counts that.
+ChunkPath chunk_path_within(const rq_shape& s, int loop, int n_new, int max_ctx, int window, size_t budget) {
+  const int64_t rows = int64_t(s.n_q_heads / s.n_kv_heads) * n_new;
+  const ChunkPath best = chunk_path(s, n_new, max_ctx, window);
+  if (path_bytes(best, s, loop, n_new, max_ctx, window, budget) <= budget) return best;
+  if (window > 0 || rows <= 8 || rows > 128) return ChunkPath::kNone;
+  for (ChunkPath other : {ChunkPath::kFused, ChunkPath::kTiles, ChunkPath::kStream}) {
+    if (other == ChunkPath::kStream && rows > 32) break;
+    if (path_bytes(other, s, loop, n_new, max_ctx, window, budget) <= budget) return other;
+  }
+  return ChunkPath::kNone;
+}
+
 size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window) {
   const ChunkPath path = chunk_path(s, n_new, max_ctx, window);
-  if (path == ChunkPath::kTiles) return chunk_tc_workspace_bytes(s, n_new, max_ctx, window);
-  if (path == ChunkPath::kFused) return chunk_fused_workspace_bytes(s, loop, n_new, max_ctx);
-  return rows_layout(s, loop, n_new, max_ctx, window).total;
+  size_t most = path_bytes(path, s, loop, n_new, max_ctx, window, SIZE_MAX);
+  // shorter contexts that take the other way of up to 128 rows
+  if (path == ChunkPath::kFused && n_new > 32) {
+    const size_t x = path_bytes(ChunkPath::kTiles, s, loop, n_new, n_new * 32 - 1, window, SIZE_MAX);
+    most = x > most ? x : most;
+  }
+  // fewer tokens, which stream the cache
+  const int heads = s.n_q_heads / s.n_kv_heads, few = (window > 0 ? 32 : 8) / heads;
+  if (path != ChunkPath::kStream && few > 0) {
+    const int n = n_new < few ? n_new : few;
+    const size_t x = path_bytes(ChunkPath::kStream, s, loop, n, max_ctx, window < n ? window : n, 0);
+    most = x > most ? x : most;
+  }
+  return most;
 }
 
 cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                         const ChunkCall& c, void* ws, cudaStream_t stream) {
+                         const ChunkCall& c, ChunkPath path, void* ws, size_t ws_bytes, cudaStream_t stream) {
   char* const w = static_cast<char*>(ws);
   unsigned* err = reinterpret_cast<unsigned*>(w);
   cudaError_t e;
   TailArgs a;
-  const ChunkPath path = chunk_path(s, c.n_new, c.max_ctx, c.window);
   RowsLayout l = {};
   if (path == ChunkPath::kFused) {
-    if ((e = launch_chunk_fused(s, cache, paging, c, ws, &a.part, &a.n_splits, stream)) != cudaSuccess) return e;
+    if ((e = launch_chunk_fused(s, cache, paging, c, ws, ws_bytes, &a.part, &a.n_splits, stream)) != cudaSuccess) return e;
   } else {
     if ((e = cudaMemsetAsync(w, 0, kWsHeaderBytes, stream)) != cudaSuccess) return e;
-    if (path == ChunkPath::kTiles) return launch_chunk_tc(s, cache, paging, c, ws, stream);
-    l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window);
+    if (path == ChunkPath::kTiles) return launch_chunk_tc(s, cache, paging, c, ws, ws_bytes, stream);
+    l = rows_layout(s, c.loop, c.n_new, c.max_ctx, c.window, ws_bytes);
     a.part = reinterpret_cast<const float*>(w + l.part);
     a.n_splits = l.plan.n_splits;
     e = launch_chunk_mma(s, cache, paging, c, l.plan, reinterpret_cast<float*>(w + l.part),

@@ -583,20 +583,21 @@ struct FusedLayout {
   size_t part, qimg, qscale, total;
 };
 
-FusedLayout fused_layout(const rq_shape& s, int loop, int n_new, int max_ctx) {
+FusedLayout fused_layout(const rq_shape& s, int loop, int n_new, int max_ctx, size_t budget) {
   FusedLayout l;
   const size_t rows = size_t(s.batch) * s.n_q_heads * n_new;
   const int kd = s.head_dim * (loop < s.n_loops - 1 ? 2 : 1);
-  l.splits = plan_fused_splits(s, max_ctx);
-  size_t o = kWsHeaderBytes;
-  l.part = o;
-  o = round1k(o + rows * l.splits * partial_floats(s) * 4);
-  l.qimg = o;
-  o = round1k(o + rows * kd * 2);
-  l.qscale = o;
-  o = round1k(o + rows * 4);
-  l.total = o;
-  return l;
+  for (l.splits = plan_fused_splits(s, max_ctx);; --l.splits) {
+    size_t o = kWsHeaderBytes;
+    l.part = o;
+    o = round1k(o + rows * l.splits * partial_floats(s) * 4);
+    l.qimg = o;
+    o = round1k(o + rows * kd * 2);
+    l.qscale = o;
+    o = round1k(o + rows * 4);
+    l.total = o;
+    if (o <= budget || l.splits == 1) return l;
+  }
 }
 
 template <int D, int RES>
@@ -616,14 +617,14 @@ cudaError_t launch_fused(const FusedArgs& a, int batch, cudaStream_t stream) {
 
 }  // namespace
 
-size_t chunk_fused_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx) {
-  return fused_layout(s, loop, n_new, max_ctx).total;
+size_t chunk_fused_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, size_t budget) {
+  return fused_layout(s, loop, n_new, max_ctx, budget).total;
 }
 
 cudaError_t launch_chunk_fused(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                               const ChunkCall& c, void* ws, const float** part, int* n_splits,
-                               cudaStream_t stream) {
-  const FusedLayout l = fused_layout(s, c.loop, c.n_new, c.max_ctx);
+                               const ChunkCall& c, void* ws, size_t ws_bytes, const float** part,
+                               int* n_splits, cudaStream_t stream) {
+  const FusedLayout l = fused_layout(s, c.loop, c.n_new, c.max_ctx, ws_bytes);
   char* const w = static_cast<char*>(ws);
   FusedArgs a;
   a.data = cache.data;

@@ -1806,7 +1806,8 @@ int plan_tc_splits(int64_t ctas, int tiles) {
   return found;
 }
 
-TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
+// most: sequences handled together, at most; lean: no key tiles shared between CTAs.
+TcLayout tc_layout_of(const rq_shape& s, int n_new, int max_ctx, int window, int most, bool lean) {
   TcLayout l;
   const int heads = s.n_q_heads / s.n_kv_heads, D = s.head_dim;
   l.tiles = int((int64_t(max_ctx) + n_new + kKeys - 1) / kKeys);
@@ -1817,15 +1818,15 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   const size_t tile = size_t(kKeys) * D * 2;
   const size_t seq = size_t(s.n_kv_heads) * l.tiles * tile * (window ? 3 : 2);
   const size_t fit = kGroupBytes / (seq ? seq : 1);
-  l.group = int(fit < 1 ? 1 : (fit > size_t(s.batch) ? size_t(s.batch) : fit));
+  l.group = int(fit < 1 ? 1 : (fit > size_t(most) ? size_t(most) : fit));
   const size_t units = size_t(l.group) * s.n_kv_heads;
   const int64_t pairs = int64_t(units) * l.blocks;
   const int64_t work = pairs * l.tiles;
-  l.ctas = pairs <= kMaxPairs && work >= int64_t(kMinShare) * device_sm_count() && work < (int64_t(1) << 29)
+  l.ctas = !lean && pairs <= kMaxPairs && work >= int64_t(kMinShare) * device_sm_count() && work < (int64_t(1) << 29)
                ? device_sm_count() : 0;
-  l.splits = l.ctas ? 1 : plan_tc_splits(pairs, l.tiles);
+  l.splits = l.ctas || lean ? 1 : plan_tc_splits(pairs, l.tiles);
   l.r_tiles = (rows + kRows - 1) / kRows;
-  l.wsplits = window ? plan_tc_splits(int64_t(units) * l.wblocks, l.tiles) : 1;
+  l.wsplits = window && !lean ? plan_tc_splits(int64_t(units) * l.wblocks, l.tiles) : 1;
   size_t o = kWsHeaderBytes;
   l.first_bad = o;
   o = round1k(o + size_t(s.batch) * s.n_kv_heads * 4);
@@ -1854,6 +1855,17 @@ TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window) {
   return l;
 }
 
+// The best plan within `budget`, else the smallest.
+TcLayout tc_layout(const rq_shape& s, int n_new, int max_ctx, int window, size_t budget) {
+  for (int most = s.batch;;) {
+    for (bool lean : {false, true}) {
+      const TcLayout l = tc_layout_of(s, n_new, max_ctx, window, most, lean);
+      if (l.total <= budget || (lean && l.group == 1)) return l;
+      if (lean) most = l.group / 2;
+    }
+  }
+}
+
 template <int D, int RES, bool KLO>
 cudaError_t launch_rebuild(const RebuildArgs& r, int64_t items, bool after, cudaStream_t stream) {
   using L = RebuildSmem<D, RES, KLO>;
@@ -1879,8 +1891,8 @@ cudaError_t launch_rebuild_any(const RebuildArgs& r, int64_t items, bool after, 
 
 template <int D>
 cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging* paging, const ChunkCall& c,
-                      char* w, cudaStream_t stream) {
-  const TcLayout l = tc_layout(s, c.n_new, c.max_ctx, c.window);
+                      char* w, size_t ws_bytes, cudaStream_t stream) {
+  const TcLayout l = tc_layout(s, c.n_new, c.max_ctx, c.window, ws_bytes);
   cudaError_t e;
   using AS = AttnSmem<D>;
   using WS = WeightSmem<D>;
@@ -2023,15 +2035,15 @@ cudaError_t launch_tc(const rq_shape& s, const rq_cache& cache, const rq_paging*
 
 }  // namespace
 
-size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window) {
-  return tc_layout(s, n_new, max_ctx, window).total;
+size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window, size_t budget) {
+  return tc_layout(s, n_new, max_ctx, window, budget).total;
 }
 
 cudaError_t launch_chunk_tc(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                            const ChunkCall& c, void* ws, cudaStream_t stream) {
+                            const ChunkCall& c, void* ws, size_t ws_bytes, cudaStream_t stream) {
   char* const w = static_cast<char*>(ws);
-  return s.head_dim == 128 ? launch_tc<128>(s, cache, paging, c, w, stream)
-                           : launch_tc<64>(s, cache, paging, c, w, stream);
+  return s.head_dim == 128 ? launch_tc<128>(s, cache, paging, c, w, ws_bytes, stream)
+                           : launch_tc<64>(s, cache, paging, c, w, ws_bytes, stream);
 }
 
 }  // namespace rq

@@ -172,9 +172,14 @@ struct ChunkCall {
   int window;
 };
 
+// How a chunk call runs (rq_chunk.cu); kNone: its workspace is too small for any.
+enum class ChunkPath { kNone, kStream, kFused, kTiles };
+
+// Workspace for the best plan of a call; and the way it runs within `ws_bytes`.
 size_t chunk_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, int window);
+ChunkPath chunk_path_within(const rq_shape& s, int loop, int n_new, int max_ctx, int window, size_t ws_bytes);
 cudaError_t launch_chunk(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                         const ChunkCall& c, void* ws, cudaStream_t stream);
+                         const ChunkCall& c, ChunkPath path, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 // Few rows (rq_decode_mma.cu): split plan and launch of the decode kernel's chunk variants.
 // part: [B][Hkv][rows][n_splits] partial records; scores (or null): [B][Hkv][window rows]
@@ -186,16 +191,17 @@ cudaError_t launch_chunk_mma(const rq_shape& s, const rq_cache& cache, const rq_
 
 // Up to 128 rows, no weights (rq_chunk_fused.cu): clears the header, then partial records as
 // launch_chunk_mma's; part and n_splits say where and how many.
-size_t chunk_fused_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx);
+// Workspace bytes of the best plan within `budget`, else of the smallest one (this and the next).
+size_t chunk_fused_workspace_bytes(const rq_shape& s, int loop, int n_new, int max_ctx, size_t budget);
 cudaError_t launch_chunk_fused(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                               const ChunkCall& c, void* ws, const float** part, int* n_splits,
-                               cudaStream_t stream);
+                               const ChunkCall& c, void* ws, size_t ws_bytes, const float** part,
+                               int* n_splits, cudaStream_t stream);
 
 // Many rows (rq_chunk_tc.cu): workspace (from its start: the header) and launch.  The header is
 // cleared by the caller.
-size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window);
+size_t chunk_tc_workspace_bytes(const rq_shape& s, int n_new, int max_ctx, int window, size_t budget);
 cudaError_t launch_chunk_tc(const rq_shape& s, const rq_cache& cache, const rq_paging* paging,
-                            const ChunkCall& c, void* ws, cudaStream_t stream);
+                            const ChunkCall& c, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 // Eviction (rq_evict.cu), arguments as in include/rq.h.
 cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads, int capacity,

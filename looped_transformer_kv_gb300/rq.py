@@ -229,8 +229,8 @@ def _i32(t):
 
 
 def chunk_workspace_bytes(shape, loop, n_new, max_ctx, window=0):
-    """rq_chunk_workspace_bytes: workspace of chunk_attention / paged_chunk_attention, for exactly
-    these sizes (for several calls take the largest: it need not grow with n_new or max_ctx)."""
+    """rq_chunk_workspace_bytes: workspace of chunk_attention / paged_chunk_attention calls of this
+    shape and loop with at most these n_new, max_ctx and window."""
     return int(_lib.lib().rq_chunk_workspace_bytes(ctypes.byref(shape), int(loop), int(n_new),
                                                    int(max_ctx), int(window)))
 

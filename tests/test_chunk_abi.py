@@ -185,3 +185,45 @@ def test_compact_within_the_same_pages_under_another_plan_is_refused(lib):
         h2 = lib.RqPaging()
         h2.block_table, h2.max_pages, h2.n_pages = 16, 2, 9
         assert _compact(lib, paged=True, s=s, c=one, g=g, ts=s, t=_cache(lib), tg=h2) == INVALID
+
+
+def _fits(lib, shape, loop, n, max_ctx, window, ws_bytes):
+    """Would a call take this workspace?  (Its output lies over its queries, which is refused after the
+    workspace was looked at: nothing is ever enqueued.)"""
+    d, g = shape.head_dim, shape.n_q_heads
+    status = _chunk(lib, shape=shape, loop=loop, n=n, max_ctx=max_ctx, window=window,
+                    weights=P if window else None, qs=(n * g * d, g * d, d), ks=(0, 0, 0, 0, 0),
+                    kv=ctypes.c_void_p(1 << 44), ws_bytes=ws_bytes)
+    assert status in (INVALID, WORKSPACE)
+    return status == INVALID
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_chunk_workspace_serves_every_smaller_call(lib, seed):
+    """One workspace, made for the longest chunk, context and window, is enough for any shorter."""
+    import random
+    rng = random.Random(seed)
+    for _ in range(40):
+        H, heads, d = rng.choice([1, 2, 8, 16]), rng.choice([1, 1, 2, 4, 8, 16, 33, 128]), rng.choice([64, 128])
+        bits = [rng.choice([2, 4]) for _ in range(rng.randint(0, 3))]
+        s = _shape(batch=rng.choice([1, 2, 16, 300]), n_q_heads=H * heads, n_kv_heads=H, head_dim=d,
+                   n_loops=len(bits) + 1, res_bits=bits, capacity=64 * rng.choice([2, 40, 512, 4096]))
+        n = int(2 ** rng.uniform(0, 12))
+        ctx = rng.choice([0, s.capacity, rng.randint(0, s.capacity)])
+        w = rng.choice([0, 1, n, rng.randint(0, n)])
+        loop = rng.randint(0, len(bits))
+        size = lib.lib().rq_chunk_workspace_bytes(ctypes.byref(s), loop, n, ctx, w)
+        assert size > 0 and _fits(lib, s, loop, n, ctx, w, size)
+        for _ in range(40):
+            n1 = rng.choice([1, n, rng.randint(1, n), min(n, max(1, 8 // heads)), min(n, max(1, 128 // heads))])
+            ctx1 = rng.choice([0, ctx, rng.randint(0, ctx), min(ctx, n1 * 32), max(0, min(ctx, n1 * 32) - 1)])
+            w1 = rng.choice([0, min(w, n1), rng.randint(0, min(w, n1))])
+            assert _fits(lib, s, loop, n1, ctx1, w1, size), (n, ctx, w, n1, ctx1, w1, H, heads, d, s.batch)
+
+
+def test_chunk_workspace_for_the_capacity_serves_every_context(lib):
+    s = _shape(batch=1, n_q_heads=16, n_kv_heads=16, capacity=32768)
+    for n in (1, 8, 64):
+        size = lib.lib().rq_chunk_workspace_bytes(ctypes.byref(s), 0, n, 32768, 0)
+        for ctx in range(0, 32769, 64):
+            assert _fits(lib, s, 0, n, ctx, 0, size)

@@ -273,3 +273,62 @@ def test_token_out_of_range_among_small_states(ctx, value):
     c.out[0, at:, :2] = clean.out[0, at:, :2]
     c.out[0, at + 90:, 2:] = clean.out[0, at + 90:, 2:]
     check_small(c, least_new=LEAST_NEW)
+
+
+def takes(c, size):
+    """Would the call take a workspace of this size?  (Asked with the output over the queries, which is
+    refused after the workspace: nothing runs.)"""
+    with pytest.raises(rq._lib.RqError) as e:
+        args = (c.q, c.loop, c.new, c.ctx_lens, c.max_ctx, c.q, c.ws[:size])
+        kw = dict(n_lens=c.n_lens, weights=c.weights, window=c.window)
+        if c.paging is not None:
+            rq.paged_chunk_attention(c.shape, c.cache, c.paging, *args, **kw)
+        else:
+            rq.chunk_attention(c.shape, c.cache, *args, **kw)
+    assert e.value.status in (1, 3)
+    return e.value.status == 1
+
+
+@pytest.mark.parametrize("B,Hq,H,d,bits,ctx,n_new,lens,window", [
+    (1, 4, 2, 128, (2,), [5000], 2, None, 0),                 # the cache streamed, one split
+    (2, 4, 2, 64, (4,), [3000, 70], 2, [1, 2], 2),
+    (2, 8, 1, 128, (2,), [4000, 129], 4, [4, 3], 0),          # fused; streamed with a short workspace
+    (1, 2, 1, 128, (2, 4), [5000], 64, None, 0),              # fused; tiles with a short workspace
+    (3, 4, 2, 128, (2,), [300, 70, 0], 100, [100, 7, 64], 0),   # tiles, groups of fewer sequences
+    (3, 12, 2, 64, (2,), [1000, 0, 129], 40, [40, 1, 33], 7),
+    (1, 32, 2, 128, (2,), [4096], 2048, [300], 0),            # key tiles shared evenly; one CTA a block
+])
+def test_any_workspace_that_is_taken_does(B, Hq, H, d, bits, ctx, n_new, lens, window):
+    c = Case(B, Hq, H, d, bits, ctx, n_new, lens, window=window, seed=5, paged=B == 2)
+    most = c.ws.numel()
+    low, high = 0, most                                       # refused, taken
+    assert takes(c, high)
+    while high - low > 1:
+        mid = (low + high) // 2
+        low, high = (low, mid) if takes(c, mid) else (mid, high)
+    whole = c.ws
+    for size in sorted({high, (high + most) // 2, max(high, most - 1), most}):
+        whole.fill_(255)
+        c.ws = whole[:size]
+        c.out.fill_(776.0)
+        if c.weights is not None:
+            c.weights.copy_(c.w0)
+        c.call()
+        torch.cuda.synchronize()
+        c.check()
+        assert (whole[size:] == 255).all()
+
+
+@pytest.mark.parametrize("n_new,ctxs", [(1, [[8000], [3000], [1]]), (64, [[1984], [4000], [2048], [0]])])
+def test_workspace_for_the_capacity(n_new, ctxs):
+    """One workspace for calls of every context, and of fewer tokens."""
+    big = None
+    for ctx in ctxs:
+        for n in sorted({1, n_new}):
+            c = Case(1, 2, 1, 128, (2,), ctx, n, cap=32768 + 64)
+            if big is None:
+                big = torch.empty(rq.chunk_workspace_bytes(c.shape, 0, n_new, 32768), dtype=torch.uint8, device="cuda")
+            c.ws = big.fill_(255)
+            c.call()
+            torch.cuda.synchronize()
+            c.check()
