@@ -545,11 +545,10 @@ cudaError_t launch_evict_select(const float* weights, int batch, int n_kv_heads,
   // CTAs per row: enough that the keys fit shared memory, more while the rows leave SMs free
   // and each CTA keeps a few thousand slots
   int C = 1;
-  while (C < kSelMaxCluster && (int64_t(capacity) > int64_t(C) * kSelKeys ||
-                                (rows * C * 2 <= device_sm_count() && capacity / C >= 4096)))
+  auto per_cta = [&](int c) { return (int64_t(capacity) / c + 32 * kSelWarps + 31) / 32 * 32; };   // (warps take 32s)
+  while (C < kSelMaxCluster && (per_cta(C) > kSelKeys || (rows * C * 2 <= device_sm_count() && capacity / C >= 4096)))
     C *= 2;
-  const int64_t per_cta = (int64_t(capacity) / C + 32 * kSelWarps + 31) / 32 * 32;
-  a.slice = per_cta <= kSelKeys ? int(per_cta) : 0;
+  a.slice = per_cta(C) <= kSelKeys ? int(per_cta(C)) : 0;
   static OncePerDevice once;
   const cudaError_t e = once([] {
     return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);

@@ -272,3 +272,17 @@ def test_prompt_eviction_and_decode(Hq, H, bits):
             got = out[b, h * G:(h + 1) * G, 0].float().cpu().numpy()
             # (rq_decode_attention's bound: 2e-3 beyond half a bf16 step)
             assert (np.abs(got - ref[0]) <= 2e-3 + 2.0 ** -8 * np.abs(ref[0])).all()
+
+
+@pytest.mark.parametrize("cap", [48640, 48641, 49152, 97792, 98304])
+def test_select_at_the_ends_of_what_shared_memory_holds(cap):
+    """Rows about as long as the keys of one or two CTAs."""
+    g = torch.Generator().manual_seed(cap)
+    w = torch.randint(0, 5000, (1, 160, cap), generator=g).float()
+    budget = cap // 2
+    keep, kept = _select(w, [cap], budget, 2, 5)
+    assert kept[0] == budget
+    x = w[0].numpy().astype(np.float64)
+    x[:, :2] = x[:, cap - 5:] = np.inf
+    for h in (0, 77, 159):
+        assert (keep[0, h] == np.sort(np.argsort(-x[h], kind="stable")[:budget])).all()
