@@ -1049,6 +1049,18 @@ __device__ __forceinline__ void warpgroup_barrier(int i) {   // 128 threads of w
     asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 
+// The same, and whether `x` holds for any of them.
+__device__ __forceinline__ bool warpgroup_any(int i, bool x) {
+  uint32_t y;
+  if (i == 0)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(uint32_t(x)) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(uint32_t(x)) : "memory");
+  return y != 0u;
+}
+
 // A CTA's work is one or more segments: a row block of 256 query rows (two tiles of 128) and a range
 // of its key tiles, every K and V tile shared by the two.  Warps 0-3 and 4-7: softmax of row tile 0
 // and 1, a thread per row; warp 8: copies; warp 9: products.  While one row tile's softmax runs, the
@@ -1297,7 +1309,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
         mbar_arrive(qready);
       }
       if (i == 1 && !w.two) {    // no rows: only keeps step with the segments
-        if (SCHED) failed = __any_sync(RQ_FULL_MASK, !mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs));
+        if (SCHED) failed = warpgroup_any(i, !mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs));
         continue;
       }
       if (w.T > 0) {
@@ -1308,7 +1320,8 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
           if ((jt & 31) == 0 && jt > 0) exps32 = jt + lane < w.T ? exps_of[jt + lane] : 0;
           const int tile_exps = __shfl_sync(RQ_FULL_MASK, exps32, jt & 31), tile_ev = tile_exps >> 8;
           const float ct = c * power_of_two(-(tile_exps & 255));
-          if (!mbar_wait_bounded(sready(i, ci), (ci >> 1) & 1, kTcWaitLimitNs)) {
+          const bool good = mbar_wait_bounded(sready(i, ci), (ci >> 1) & 1, kTcWaitLimitNs);
+          if (__any_sync(RQ_FULL_MASK, !good)) {                      // (the warp leaves as one)
             failed = true;
             break;
           }
@@ -1380,7 +1393,7 @@ __global__ void __launch_bounds__(384, 1) attention_kernel(const __grid_constant
           mbar_arrive(pready(i));
         }
         if (!failed && (!LSE || SCHED)) failed = !mbar_wait_bounded(done, seg & 1, kTcWaitLimitNs);
-        failed = __any_sync(RQ_FULL_MASK, failed);
+        failed = warpgroup_any(i, failed);                           // (the warps leave together: they share barriers)
         tc_fence_after();
       }
       // ---- store (a wait that gave up: NaN)
@@ -1732,8 +1745,9 @@ __global__ void __launch_bounds__(320, 2) weights_kernel(const __grid_constant__
     const float down = power_of_two(-(a.v.exps[unit * a.v.tiles + blockIdx.x] & 255));
     for (int j = i; j < T; j += 2) {
       const int s = j % L::kStages;
-      if (!mbar_wait_bounded(sready(i), (j >> 1) & 1, kTcWaitLimitNs) ||
-          !mbar_wait_bounded(qfull(s), (j / L::kStages) & 1, kTcWaitLimitNs)) {
+      const bool good = mbar_wait_bounded(sready(i), (j >> 1) & 1, kTcWaitLimitNs) &&
+                        mbar_wait_bounded(qfull(s), (j / L::kStages) & 1, kTcWaitLimitNs);
+      if (__any_sync(RQ_FULL_MASK, !good)) {                          // (the warp leaves as one)
         failed = true;
         break;
       }
