@@ -249,15 +249,16 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  *   n_new      >= 0 (0: nothing enqueued)
  *   ctx_lens, max_ctx  as in rq_decode_attention (max_ctx may be 0)
  *   out        bf16 [B][n_new][Hq][d]; rows behind a sequence's last token are left as they were;
- *              it must not overlap q's or kv_new's span (RQ_ERR_INVALID_ARG)
+ *              it must not overlap q's or kv_new's span, first to last element, gaps between rows
+ *              included: strides may interleave rows in any way (RQ_ERR_INVALID_ARG)
  *   weights    fp32 [B][Hkv][capacity], or NULL: the softmax weights of the last `window` new
  *              tokens of each sequence (all of them if it has fewer), summed over their query
  *              heads of the kv-head, are added: weights[b][h][t] += sum P for cached slots
  *              t < ctx, and at t = ctx + j' for chunk token j' (the slot rq_encode_append gives
  *              it; slots at or above capacity are dropped).  Sums are fp32 in a fixed order.
  *   window     1..n_new with weights; 0 if and only if weights is NULL
- *   ws         256-byte aligned, at least rq_chunk_workspace_bytes(...) bytes for the call's n_new,
- *              max_ctx and window, or for larger ones: one workspace, made for the longest chunk,
+ *   ws         256-byte aligned, at least rq_chunk_workspace_bytes(...) bytes (on the same device)
+ *              for the call's n_new, max_ctx and window, or for larger ones: one workspace, made for the longest chunk,
  *              context and window (with one, if any call has one), serves every call of the shape and
  *              loop.  A call whose own best plan would take more makes do with fewer splits; the same
  *              call with the same ws_bytes gives the same bits.  Its first uint32
@@ -270,8 +271,20 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  * (RQ_ERR_UNSUPPORTED).
  * A chunk token whose K or V row of the loop is not finite, or beyond fp16's largest number
  * (the states' range everywhere in this library), makes the outputs of its own and of the
- * sequence's later tokens NaN for the query heads of its kv-head; earlier tokens never see it.
- * Scores, softmax statistics and accumulators are fp32. */
+ * sequence's later tokens NaN for the query heads of its kv-head, and so the weights that these
+ * add; earlier tokens never see it.
+ * Precision: scores, softmax statistics and accumulators are fp32, and the scores of collected
+ * weights carry 21 bits.  Operands follow the rows, n_new * (Hq / Hkv), of the call:
+ *   - up to 8 (with weights 32): as rq_decode_attention's, about 21 bits; new states exact.
+ *   - up to 128 without weights (of more than 32 tokens: after 32 * n_new cached ones): fp16, 11
+ *     bits, for rotated queries, levels and softmax weights, each rounded once, a level that a_l
+ *     scales twice; new states exact.
+ *   - others: fp16 for residual levels, rebuilt elements, new states and softmax weights.
+ * A rounding to fp16 is off by at most 2^-11 of the number, or by 2^-25 (a cached element: the
+ * resolution of the cache's own steps and offsets), 2^-24 of the largest element of the same tile
+ * of 128 keys (a new state; so states of 1e-5 keep their bits among their like) or 2^-32 of the
+ * row's largest weight (a weight), whichever is more.  Outputs on random states are 0.0010 to
+ * 0.0012 (rms, relative) beside their rounding to bf16, 0.0016, with fp16 operands. */
 size_t rq_chunk_workspace_bytes(const rq_shape* shape, int32_t loop, int32_t n_new,
                                 int32_t max_ctx, int32_t window);
 rq_status rq_chunk_attention(const rq_shape* shape, const rq_cache* cache, const uint16_t* q,

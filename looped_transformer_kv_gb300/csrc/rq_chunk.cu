@@ -205,8 +205,9 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const __grid_constan
   if (voted && lane == 0) a.lse[wrow] = bad ? nan : M + log2f(ell);
 }
 
-// Four slots per thread: the weights of the window's rows, in row order.  Bound by HBM: a score per
-// slot and row read, a weight read and written (one row, 256 x 4,097 slots: 6 us, launch included).
+// Four slots per thread: the weights of the window's rows, in row order.  A score per slot and row is
+// read, a weight read and written; with one row bound by latency (256 x 4,097 slots: 12.6 MB in 6 us,
+// launch included).
 __global__ void __launch_bounds__(128) chunk_weights_kernel(const __grid_constant__ TailArgs a) {
   grid_wait();
   const int t0 = (blockIdx.x * 128 + threadIdx.x) * 4, h = blockIdx.y, b = blockIdx.z;

@@ -19,9 +19,9 @@
 // The queries are fp16 (q exactly, R q rounded once, both times the row's power of two); a level
 // s c + z is rounded once to fp16, a reference level once more by a; weights once; sums are fp32.
 // 8 tokens x 4 heads after 16,384 (8 sequences, 8 kv-heads, 2-bit residuals): 118 us, 2.3 TB/s, 1,600
-// cycles per record and about 7 us per CTA to begin and end.  No one part bounds it: issue slots are 54 %
-// used, the tensor pipe 50 % (1,250 cycles of a 128-row tile whatever the rows), and each record's
-// operands cross shared memory twice (64 KB written, 64 KB read: about 1,050 cycles).  The copies
+// cycles per record and about 7 us per CTA to begin and end.  No one part bounds it: issue slots are 53 %
+// used, the tensor pipe 50 % (1,250 cycles of a 128-row tile whatever the rows), shared memory's data
+// banks 15 % each way; what does is the chain of a record through its parts, two deep.  The copies
 // alone take 69 us, conversions with the copies 92, products and softmax with them 110.  More raw
 // records, records prefetched to L2, a warp each for scores' and values' products, conflict-free
 // stores of the images and weights through shared memory did not shorten it.

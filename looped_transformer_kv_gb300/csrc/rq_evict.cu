@@ -285,11 +285,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
 // A 64-row tile of one section of `to` is made of units of at most 16 bytes; a thread loads the
 // sources of its units into registers and stores them.  K rows, steps and offsets are contiguous
 // per row; V code words hold two tokens, so a unit (4 words of a pair) takes the matching
-// 16-bit halves of two source pairs.  Bound by HBM: every kept byte is read and written once, and V
-// codes of a kept token whose pair neighbour is not kept cost twice their bytes, steps and offsets
-// a whole 32-byte sector (2,048 of up to 4,096 rows, 256 heads,
-// 3 residual loops: 488 MB wanted, 575 MB moved, 119 us, 4.8 TB/s),
-// then by the instructions of the gathers (issue slots 67 % used).
+// 16-bit halves of two source pairs.  V codes of a kept token whose pair neighbour is not kept cost
+// twice their bytes, steps and offsets a whole 32-byte sector: 2,048 of up to 4,096 rows, 256 heads, 3
+// residual loops: 488 MB wanted, 575 MB moved, in 119 us.  Neither wall is reached: 4.8 TB/s is 71 % of a
+// plain copy's rate, and the address arithmetic of the 16-byte gathers uses 67 % of the issue slots.
+// In place, 150 us for the same rows (128 out of place, timed alike); paged 160 and 132.
 // In place, a row only moves to a lower slot.  A cluster of CTAs takes the tiles of one (sequence,
 // kv-head, section) in ascending waves: all rows of a wave are read before any is written
 // (cluster barrier), and later waves read only rows at or above their own tiles.
