@@ -258,11 +258,11 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  *              it; slots at or above capacity are dropped).  Sums are fp32 in a fixed order.
  *   window     1..n_new with weights; 0 if and only if weights is NULL
  *   ws         256-byte aligned, at least rq_chunk_workspace_bytes(...) bytes (on the same device)
- *              for the call's n_new, max_ctx and window, or for larger ones: one workspace, made for the longest chunk,
- *              context and window (with one, if any call has one), serves every call of the shape and
- *              loop.  A call whose own best plan would take more makes do with fewer splits; the same
- *              call with the same ws_bytes gives the same bits.  Its first uint32
- *              is the call's error word, as in rq_decode_attention: nonzero after a device-side
+ *              for the call's n_new, max_ctx and window, or for larger ones: one workspace, made for
+ *              the longest chunk, context and window (with one, if any call has one), serves every
+ *              call of the shape and loop.  A call whose own best plan would take more makes do with
+ *              fewer splits; the same call with the same ws_bytes gives the same bits.  Its first
+ *              uint32 is the call's error word, as in rq_decode_attention: nonzero after a device-side
  *              ctx_len outside [0, max_ctx], an n_len outside [0, n_new] (taken as n_new), a bad
  *              block-table entry, or a pipeline wait that gave up.  The call's outputs are then
  *              NaN (after a wait that gave up, at least those of the rows it served), and its
