@@ -283,8 +283,8 @@ rq_status rq_advance_ctx(int32_t* ctx_lens, int32_t batch, int32_t n, int32_t ca
  * A rounding to fp16 is off by at most 2^-11 of the number, or by 2^-25 (a cached element: the
  * resolution of the cache's own steps and offsets), 2^-24 of the largest element of the same tile
  * of 128 keys (a new state; so states of 1e-5 keep their bits among their like) or 2^-32 of the
- * row's largest weight (a weight), whichever is more.  Outputs on random states are 0.0010 to
- * 0.0012 (rms, relative) beside their rounding to bf16, 0.0016, with fp16 operands. */
+ * row's largest weight (a weight), whichever is more.  With fp16 operands, outputs on random
+ * states are off by 0.0010 to 0.0015 (rms, relative) beside their rounding to bf16, 0.0016. */
 size_t rq_chunk_workspace_bytes(const rq_shape* shape, int32_t loop, int32_t n_new,
                                 int32_t max_ctx, int32_t window);
 rq_status rq_chunk_attention(const rq_shape* shape, const rq_cache* cache, const uint16_t* q,
