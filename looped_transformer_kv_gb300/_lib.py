@@ -1,5 +1,5 @@
 """ctypes declarations of librq's C ABI (include/rq.h, include/rq_synth.h, include/rq_test.h,
-include/rq_ablation.h).
+include/rq_ablation.h, include/rq_q8.h).
 
 Loading fails loudly: there is no fallback implementation of any entry point.
 """
@@ -21,7 +21,8 @@ EXPORTS = ("rq_cache_bytes", "rq_record_bytes", "rq_encode_append", "rq_decode_w
            "rq_test_decode_attention_wait_runs_out", "rq_ablation_encode_append",
            "rq_ablation_decode_attention", "rq_chunk_workspace_bytes", "rq_chunk_attention",
            "rq_paged_chunk_attention", "rq_evict_select", "rq_evict_compact",
-           "rq_paged_evict_compact")
+           "rq_paged_evict_compact", "rq_q8_cache_bytes", "rq_q8_paged_cache_bytes", "rq_q8_append",
+           "rq_paged_q8_append", "rq_q8_workspace_bytes", "rq_q8_attention", "rq_paged_q8_attention")
 
 
 class RqShape(ctypes.Structure):
@@ -41,6 +42,22 @@ class RqCache(ctypes.Structure):
 
 class RqPaging(ctypes.Structure):
     _fields_ = [("block_table", _P), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+class RqQ8Shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_loops", ctypes.c_int32), ("capacity", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
+class RqQ8Cache(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P)]
+
+
+class RqRope(ctypes.Structure):
+    _fields_ = [("table", _P), ("positions", _P), ("n_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class RqSynthParams(ctypes.Structure):
@@ -117,6 +134,23 @@ def lib():
     L.rq_evict_compact.restype = i32
     L.rq_paged_evict_compact.argtypes = [S, C, G, S, C, G, _P, i32, _P, _P, _P, _P]
     L.rq_paged_evict_compact.restype = i32
+    S8, C8, R = ctypes.POINTER(RqQ8Shape), ctypes.POINTER(RqQ8Cache), ctypes.POINTER(RqRope)
+    L.rq_q8_cache_bytes.argtypes = [S8]
+    L.rq_q8_cache_bytes.restype = sz
+    L.rq_q8_paged_cache_bytes.argtypes = [S8, i32]
+    L.rq_q8_paged_cache_bytes.restype = sz
+    append = [_P, I, i32, i32, _P, i32, _P, R, _P]
+    L.rq_q8_append.argtypes = [S8, C8] + append
+    L.rq_q8_append.restype = i32
+    L.rq_paged_q8_append.argtypes = [S8, C8, G] + append
+    L.rq_paged_q8_append.restype = i32
+    L.rq_q8_workspace_bytes.argtypes = [S8, i32, i32, i32, i32]
+    L.rq_q8_workspace_bytes.restype = sz
+    attend = [_P, I, i32, _P, i32, _P, i32, i32, i32, R, _P, _P, sz, _P]
+    L.rq_q8_attention.argtypes = [S8, C8] + attend
+    L.rq_q8_attention.restype = i32
+    L.rq_paged_q8_attention.argtypes = [S8, C8, G] + attend
+    L.rq_paged_q8_attention.restype = i32
     L.rq_status_str.argtypes = [i32]
     L.rq_status_str.restype = ctypes.c_char_p
     P = ctypes.POINTER(RqSynthParams)

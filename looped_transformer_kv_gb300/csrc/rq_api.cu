@@ -5,8 +5,13 @@
 
 #include "../../include/rq_ablation.h"
 #include "../../include/rq_test.h"
+#include "rq_checks.h"
 #include "rq_common.cuh"
 #include "rq_kernels.h"
+
+using rq::from_cuda;
+using rq::overlaps;
+using rq::strides_ok;
 
 namespace {
 
@@ -68,8 +73,6 @@ rq_status check_decode(const rq_shape* s, const uint16_t* q, int32_t loop_begin,
   return RQ_OK;
 }
 
-rq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA; }
-
 rq_status check_paging(const rq_shape* s, const rq_paging* pg) {
   if (!pg || !pg->block_table || pg->max_pages <= 0 || pg->n_pages <= 0)
     return RQ_ERR_INVALID_ARG;
@@ -129,27 +132,6 @@ rq_status decode_common(const rq_shape* shape, const rq_cache* cache, const rq_p
   } catch (...) {
     return RQ_ERR_INTERNAL;
   }
-}
-
-// Strides of a chunk call's q or kv_new: non-negative, and every element's offset in 63 bits.
-bool strides_ok(const int64_t* strides, const int64_t* extents, int n) {
-  int64_t last = 0;
-  for (int i = 0; i < n; ++i) {
-    if (strides[i] < 0) return false;
-    const int64_t steps = extents[i] > 0 ? extents[i] - 1 : 0;
-    if (steps > 0 && strides[i] > (INT64_MAX / 4 - last) / steps) return false;
-    last += steps * strides[i];
-  }
-  return true;
-}
-
-// Does the span of bf16 rows of `d` elements at these (checked) strides meet [begin, end)?
-bool overlaps(const uint16_t* p, const int64_t* strides, const int64_t* extents, int n, int d,
-              uintptr_t begin, uintptr_t end) {
-  int64_t last = d;
-  for (int i = 0; i < n; ++i) last += (extents[i] - 1) * strides[i];
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(p), a1 = a0 + uintptr_t(last) * 2;
-  return a0 < end && begin < a1;
 }
 
 // Sizes a chunk call may have, without its pointers.

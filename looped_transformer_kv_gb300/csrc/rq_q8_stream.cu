@@ -1,0 +1,702 @@
+// Attention over the 8-bit cache for few query rows (include/rq_q8.h): every tile that some row sees
+// is read once per 32 rows, with the codes turned into exact fp16 operands in registers.
+//
+//   S[t, r] = q_r . K_t on mma.sync, M = a warp's 16 slots, N = 8 rows; one scale per warp and tile
+//   (a block of 16 slots is a warp's share), so scores are S * scale_K * (softmax scale of the row).
+//   w = 2^(S - m) scale_V 2^-E, fp16; O[ch, r] += V^T w on mma.sync, M = 16 channels, K = the slots.
+// A warp keeps its own m and l (rows), E (all) and accumulators over its slots; the four warps are
+// merged once per segment.  m is raised when a score exceeds it by more than 8, E when a V scale
+// exceeds 2^(E + 7): weights stay below 2^15.
+//
+// The work is one line: for each sequence, for each block of rows and kv-head, its tiles.  It is cut
+// evenly for the CTAs that fit the GPU at once; a unit that a cut divides leaves partial results, and
+// the last of its CTAs to finish joins them in order.
+#include <algorithm>
+#include <cmath>
+
+#include "rq_kernels.h"
+#include "rq_launch.cuh"
+#include "rq_q8.cuh"
+#include "rq_tc.cuh"
+
+namespace rq {
+namespace {
+
+constexpr float kNoMax = -1e30f;      // m of a row that has seen nothing
+constexpr float kTop = 8.f;
+constexpr int kScaleTop = 7, kScaleHead = 6;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMostCtas = 1024;
+
+struct Cut {
+  int64_t pos, base;    // where a CTA's stretch begins; where sequence b's units begin
+  int32_t b, pad;
+};
+
+struct StreamArgs {
+  Q8View v;
+  Q8Call c;
+  int32_t B, Hq, G, cap, qvec;
+  int32_t blocks;        // blocks of 8 NT rows, of n_new tokens
+  float scale_log2;
+  unsigned* err;         // workspace: error word, ...
+  int32_t* used;         // CTAs with work
+  unsigned* tickets;     // [CTA] of the unit that is cut at its end
+  int64_t* prefix;       // [B + 1] places of the sequences
+  Cut* cut;              // [CTA + 1]
+  float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l)
+  float* part;           // ... [rows][D]
+  int32_t n_ctas;
+};
+
+// What a block of rows sees: tiles 0 .. sink and from `first` on, V in all.
+struct Rows {
+  int ctx, n, j0, j1;    // tokens of the block's rows
+  int rows;              // of the block
+  int sink, first, V, hi;
+  bool ok;
+};
+
+template <int NT>
+__device__ __forceinline__ Rows rows_of(const StreamArgs& a, int b, int block) {
+  Rows x;
+  x.ctx = a.c.ctx_lens[b];
+  x.n = a.c.n_lens ? a.c.n_lens[b] : a.c.n_new;
+  x.ok = x.ctx >= 0 && x.ctx <= a.c.max_ctx && x.n >= 0 && x.n <= a.c.n_new && x.ctx <= a.cap - x.n;
+  if (x.n < 0 || x.n > a.c.n_new) x.n = a.c.n_new;
+  const int r0 = block * 8 * NT;
+  x.rows = min(8 * NT, x.n * a.G - r0);
+  x.sink = x.first = x.hi = 0;
+  x.V = 0;
+  if (x.rows <= 0) return x;
+  x.j0 = r0 / a.G;
+  x.j1 = (r0 + x.rows - 1) / a.G;
+  x.V = 1;                                                  // (bad lengths: one tile, not read)
+  if (!x.ok) return x;
+  const int lo = a.c.window > 0 ? max(0, x.ctx + x.j0 + 1 - a.c.window) : 0;
+  x.hi = x.ctx + x.j1 + 1;
+  x.first = lo / kQ8Tile;
+  x.sink = min((min(a.c.n_sink, lo) + kQ8Tile - 1) / kQ8Tile, x.first);
+  x.V = x.sink + (x.hi + kQ8Tile - 1) / kQ8Tile - x.first;
+  return x;
+}
+
+// One CTA: clears the error word and tickets, cuts the line.
+template <int NT>
+__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ StreamArgs a) {
+  grid_next();
+  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) *a.err = 0u;
+  for (int i = tid; i < a.n_ctas; i += 1024) a.tickets[i] = 0u;
+  int64_t run = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+    int64_t units = 0;
+    if (b0 + tid < a.B) {
+      for (int k = 0; k < a.blocks; ++k) {
+        const Rows x = rows_of<NT>(a, b0 + tid, k);
+        bad |= !x.ok;
+        if (x.V == 0) break;
+        units += x.V;
+      }
+      units *= a.v.H;
+    }
+    int64_t sum = units;                                    // inclusive scan over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(RQ_FULL_MASK, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t before = run;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      run += warp_sum[w];
+    }
+    if (b0 + tid < a.B) a.prefix[b0 + tid] = before + sum - units;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.prefix[a.B] = run;
+    total = run;
+  }
+  bad = __syncthreads_or(bad);                              // (and the prefix is written)
+  if (bad && tid == 0) *a.err = 1u;
+  const int64_t N = total;
+  const int used = int(min(N, int64_t(a.n_ctas)));
+  if (tid == 0) *a.used = used;
+  for (int i = tid; i <= used; i += 1024) {
+    const int64_t pos = used ? N * i / used : 0;
+    int lo = 0, hi = a.B;                                   // the last sequence that begins at or before pos
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.prefix[mid] <= pos) lo = mid; else hi = mid;
+    }
+    a.cut[i] = {pos, a.prefix[lo], lo, 0};
+  }
+}
+
+// A CTA's segments in order.
+template <int NT>
+struct Walk {
+  const StreamArgs& a;
+  int64_t pos, end, base;   // base: where the units of (b, block) begin
+  int b, block;
+  Rows x;
+  int h, kt0, T;
+  int64_t unit;             // the unit's place on the line
+  bool loaded;
+  __device__ __forceinline__ Walk(const StreamArgs& args, const Cut& from, int64_t to)
+      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(0), loaded(false) {}
+  __device__ __forceinline__ bool next() {
+    if (pos >= end) return false;
+    for (;;) {
+      if (!loaded) {
+        x = rows_of<NT>(a, b, block);
+        loaded = true;
+      }
+      const int64_t stop = base + int64_t(x.V) * a.v.H;
+      if (pos < stop) break;
+      base = stop;
+      loaded = false;
+      if (x.V == 0 || ++block == a.blocks) {
+        block = 0;
+        if (++b == a.B) return false;                       // (not with a sound schedule)
+      }
+    }
+    h = int((pos - base) / x.V);
+    unit = base + int64_t(h) * x.V;
+    kt0 = int(pos - unit);
+    T = int(min(int64_t(x.V - kt0), end - pos));
+    pos += T;
+    return true;
+  }
+  __device__ __forceinline__ int tile(int v) const { return v < x.sink ? v : x.first + v - x.sink; }
+};
+
+template <int D, int NT>
+struct StreamSmem {
+  static constexpr int kCtas = NT == 1 ? 3 : 2;
+  static constexpr int kCodes = 2 * kQ8Tile * D, kStage = kCodes + 128;   // (scales: 32 bytes)
+  static constexpr int kRows = 8 * NT, kMergeRow = D + 4;
+  static constexpr int kMerge = 4 * 8 * kMergeRow * 4;
+  static constexpr int kQuery = NT * (D / 16) * 32 * 8;
+  static constexpr int kFixed = kMerge + kQuery + 4 * kRows * 8 + kRows * 8 + 512;
+  static constexpr int kStages0 = (227 * 1024 / kCtas - 1024 - kFixed) / kStage;
+  static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
+  static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kQuery;
+  static constexpr int row_scale = stats + 4 * kRows * 8, row_limit = row_scale + kRows * 4;
+  static constexpr int bars = row_limit + kRows * 4, misc = bars + 16 * kStages;
+  static constexpr int total = misc + 16 * 4 + 4 * kStages + 128;   // + alignment of the base
+  static_assert(kStages >= 2 && misc % 8 == 0, "stages");
+};
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ StreamArgs a) {
+  using L = StreamSmem<D, NT>;
+  constexpr int KS = D / 16;                                // k-steps of a score, 16-channel tiles of O
+  grid_wait();
+  const int me = int(blockIdx.x);
+  if (me >= *a.used) return;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = smem_u32(smem + L::bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (L::kStages + s); };
+  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [1]: last of a unit, [4 ..]: a warp's E
+  int* const bad_page = misc + 16;                          // [stage]
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 4);
+    }
+    misc[0] = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Cut from = a.cut[me];
+  Walk<NT> w(a, from, a.cut[me + 1].pos);
+
+  if (warp == 4) {                                          // ---- copies
+    int g = 0;
+    bool good = true;
+    while (good && w.next()) {
+      if (!w.x.ok) continue;
+      for (int t0 = 0; t0 < w.T && good; t0 += 32) {
+        int64_t rec = -1;
+        if (t0 + lane < w.T) rec = a.v.record(w.b, w.h, w.tile(w.kt0 + t0 + lane));
+        const int m = min(32, w.T - t0);
+        for (int t = 0; t < m && good; ++t, ++g) {
+          const int64_t r = __shfl_sync(RQ_FULL_MASK, rec, t);
+          const int s = g % L::kStages, n = g / L::kStages;
+          if (n > 0) good = mbar_wait_bounded(empty(s), (n - 1) & 1, kWaitNs);
+          good = __all_sync(RQ_FULL_MASK, good);
+          if (!good) break;
+          if (lane == 0) {
+            const int64_t at = r < 0 ? w.h : r;             // (no page: page 0, and flagged)
+            bad_page[s] = r < 0;
+            if (r < 0) atomicOr(a.err, 1u);
+            uint8_t* const stage = smem + s * L::kStage;
+            mbar_arrive_expect_tx(full(s), L::kCodes + 32);
+            bulk_g2s(smem_u32(stage), a.v.codes + at * a.v.rec_codes, L::kCodes, full(s));
+            bulk_g2s(smem_u32(stage + L::kCodes), a.v.scales + at * a.v.rec_scales, 32, full(s));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!good) {                                            // copies in flight land before the CTA leaves
+      for (int k = max(0, g - L::kStages); k < g; ++k) mbar_wait_bounded(full(k % L::kStages), (k / L::kStages) & 1, kWaitNs);
+      if (lane == 0) {
+        atomicExch(&misc[0], 1);
+        atomicOr(a.err, 1u);
+      }
+    }
+  } else {                                                  // ---- products
+    const int r = lane >> 2, c = lane & 3;
+    float* const merge = reinterpret_cast<float*>(smem + L::merge);
+    uint2* const query = reinterpret_cast<uint2*>(smem + L::query);
+    float2* const stats = reinterpret_cast<float2*>(smem + L::stats);          // [warp][row]
+    float* const row_scale = reinterpret_cast<float*>(smem + L::row_scale);
+    int* const row_limit = reinterpret_cast<int*>(smem + L::row_limit);        // a row's own slot
+    int g = 0;
+    bool dead = false;
+    while (w.next()) {
+      const Rows& x = w.x;
+      const int r0 = w.block * L::kRows;
+      // ---- the rows' queries as B fragments: (k-step, row) word pairs of the lanes that use them
+      if (x.ok) {
+        constexpr int LPR = D / 8, AT = 128 / LPR;          // lanes per row, rows at a time
+        const int qc = threadIdx.x % LPR;
+#pragma unroll 1
+        for (int y = threadIdx.x / LPR; y < L::kRows; y += AT) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = 0.f;
+          const int j = (r0 + y) / a.G, hq = w.h * a.G + (r0 + y) % a.G;
+          const bool live = y < x.rows;
+          if (live) q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec, f);
+          bool lost = false;
+          if (a.c.rope.table != nullptr) {
+            int pos = -1;
+            if (live) {
+              pos = a.c.rope.positions ? a.c.rope.positions[int64_t(w.b) * a.c.n_new + j] : x.ctx + j;
+              lost = pos < 0 || pos >= a.c.rope.n_pos;
+              if (lost) pos = -1;
+            }
+            q8_rotate<D>(f, a.c.rope, pos, lane);
+          }
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
+          // a power of two brings the row's largest element into [2^14, 2^15): bf16 values are exact
+          const int ex = int(__float_as_uint(mx) >> 23);
+          const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
+          const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
+          const int nt = y >> 3, n = y & 7;
+          const int cc = D == 128 ? qc >> 2 : qc >> 1, s = D == 128 ? 2 * (qc & 3) : 2 * (qc & 1);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            query[(nt * KS + s + k) * 32 + 4 * n + cc] =
+                make_uint2(pack_half2(f[4 * k] * up * up2, f[4 * k + 1] * up * up2),
+                           pack_half2(f[4 * k + 2] * up * up2, f[4 * k + 3] * up * up2));
+          if (qc == 0) {
+            row_scale[y] = lost ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+            row_limit[y] = x.ctx + min(j, x.n - 1);
+          }
+        }
+      }
+      consumers_sync();
+
+      float acc[NT][KS][4], m[NT][2], l[NT][2], cs[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          m[t][k] = kNoMax;
+          l[t][k] = 0.f;
+          cs[t][k] = row_scale[8 * t + 2 * c + k];
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
+      }
+      int E = -120;
+      uint2 qf[NT <= 2 ? NT * KS : 1];                      // (more rows: read again for every tile)
+      if (NT <= 2)
+#pragma unroll
+        for (int k = 0; k < NT * KS; ++k) qf[k] = query[k * 32 + lane];
+
+      for (int t = 0; x.ok && t < w.T; ++t, ++g) {
+        const int s = g % L::kStages;
+        if (!dead) dead = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(full(s), (g / L::kStages) & 1, kWaitNs));
+        if (dead) continue;                                 // (the copies' warp gives up in its turn)
+        const uint8_t* const stage = smem + s * L::kStage;
+        const int slot0 = w.tile(w.kt0 + t) * kQ8Tile + 16 * warp;
+        const int oldest = a.c.window > 0 ? x.ctx + x.j0 + 1 - a.c.window : 0;   // the first row's window
+        if (slot0 < x.hi && (slot0 + 15 >= oldest || slot0 < a.c.n_sink)) {
+          const float* const scales = reinterpret_cast<const float*>(stage + L::kCodes);
+          const bool no_page = bad_page[s] != 0;
+          const float ks = no_page ? __int_as_float(0x7fc00000) : scales[warp];
+          const float vs = no_page ? __int_as_float(0x7fc00000) : scales[4 + warp];
+          // ---- scores
+          float sc[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
+          {
+            const uint8_t* const k0 = stage + (16 * warp + r) * D;     // rows r and r + 8: the same swizzle
+            const int sw = q8_swizzle<D>(r);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              const int at = ((D / 64 * c + half) ^ sw) << 4;
+              const uint4 u = *reinterpret_cast<const uint4*>(k0 + at), v = *reinterpret_cast<const uint4*>(k0 + 8 * D + at);
+              const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t x0 = q8_word<FMT>(uw[k]), x1 = q8_word<FMT>(vw[k]);
+                const uint32_t a0 = q8_pair<FMT, 0>(x0), a1 = q8_pair<FMT, 0>(x1);
+                const uint32_t a2 = q8_pair<FMT, 1>(x0), a3 = q8_pair<FMT, 1>(x1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  const int at_q = n * KS + 4 * half + k;
+                  const uint2 q = NT <= 2 ? qf[NT <= 2 ? at_q : 0] : query[at_q * 32 + lane];
+                  mma_f16(sc[n], a0, a1, a2, a3, q.x, q.y);
+                }
+              }
+            }
+          }
+          // ---- softmax weights
+          const bool clear = slot0 + 15 <= x.ctx + x.j0 &&
+                             (a.c.window <= 0 || slot0 > x.ctx + x.j1 - a.c.window || slot0 + 15 < a.c.n_sink);
+          float ksc[NT][2];
+          bool over = false;
+          uint32_t hidden = 0u;                             // bit 4 n + k: element not seen by its row
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ksc[n][k] = cs[n][k] * ks;
+          if (!clear) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int slot = slot0 + r + 8 * (k >> 1), own = row_limit[8 * n + 2 * c + (k & 1)];
+                const bool seen = slot <= own && (a.c.window <= 0 || slot > own - a.c.window || slot < a.c.n_sink);
+                if (!seen) {
+                  hidden |= 1u << (4 * n + k);
+                  sc[n][k] = -INFINITY;
+                }
+              }
+            // (a scale of 0 or less does not occur; NaN stays with the rows that see the block)
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              sc[n][k] = hidden >> (4 * n + k) & 1u ? -INFINITY : sc[n][k] * ksc[n][k & 1];
+              over |= sc[n][k] > m[n][k & 1] + kTop;
+            }
+          const int ev = q8_exponent(vs) > 127 ? E : q8_exponent(vs);
+          const bool lift = ev > E + kScaleTop;
+          if (__any_sync(RQ_FULL_MASK, over) || lift) {
+            const float fe = lift ? q8_pow2(max(E - (ev - kScaleHead), -126)) : 1.f;
+            if (lift) E = ev - kScaleHead;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float v = fmaxf(sc[n][k], sc[n][k + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(RQ_FULL_MASK, v, o));
+                const float to = v > m[n][k] + kTop ? v : m[n][k];
+                const float f = ex2(m[n][k] - to);
+                m[n][k] = to;
+                l[n][k] *= f;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                  acc[n][i][k] *= f * fe;
+                  acc[n][i][k + 2] *= f * fe;
+                }
+              }
+          }
+          const float vsc = vs * q8_pow2(-E);
+          uint32_t b0[NT], b1[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              p[k] = ex2(sc[n][k] - m[n][k & 1]);
+              l[n][k & 1] += p[k];
+              p[k] = hidden >> (4 * n + k) & 1u ? 0.f : p[k] * vsc;
+            }
+            b0[n] = transposed(pack_half2(p[0], p[1]));
+            b1[n] = transposed(pack_half2(p[2], p[3]));
+          }
+          // ---- values
+          {
+            constexpr int W = D / 32;                       // words of a lane's channels of one row
+            uint32_t v[4][W];                               // slots 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = 16 * warp + 2 * c + (k & 1) + 8 * (k >> 1);
+              const uint8_t* const p = stage + kQ8Tile * D + row * D;
+              if (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p + ((r ^ q8_swizzle<D>(row)) << 4));
+                v[k][0] = u.x;
+                v[k][1] = u.y;
+                v[k][W - 2] = u.z;
+                v[k][W - 1] = u.w;
+              } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(p + (((r >> 1) ^ q8_swizzle<D>(row)) << 4) + (r & 1) * 8);
+                v[k][0] = u.x;
+                v[k][1] = u.y;
+              }
+              // slots behind the last new token may hold anything (a code that is not a number, too)
+              if (slot0 + 15 >= x.hi && slot0 - 16 * warp + row >= x.hi)
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[k][i] = 0u;
+#pragma unroll
+              for (int i = 0; i < W; ++i) v[k][i] = q8_word<FMT>(v[k][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              const uint32_t lo = __byte_perm(v[0][i / 2], v[1][i / 2], i & 1 ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(v[2][i / 2], v[3][i / 2], i & 1 ? 0x7362 : 0x5140);
+              const uint32_t a0 = q8_pair<FMT, 0>(lo), a1 = q8_pair<FMT, 1>(lo);
+              const uint32_t a2 = q8_pair<FMT, 0>(hi), a3 = q8_pair<FMT, 1>(hi);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(acc[n][i], a0, a1, a2, a3, b0[n], b1[n]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
+      }
+
+      // ---- the four warps' results joined, eight rows at a time
+      if (dead && lane == 0) atomicExch(&misc[0], 1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[n][k] += __shfl_xor_sync(RQ_FULL_MASK, l[n][k], o);
+          if (r == 0) stats[warp * L::kRows + 8 * n + 2 * c + k] = make_float2(m[n][k], l[n][k]);
+        }
+      if (lane == 0) misc[4 + warp] = E;
+      const bool whole = w.kt0 == 0 && w.T == x.V;
+      const int slot = 2 * me + (w.kt0 == 0 ? 1 : 0);
+      constexpr int CH = D / 16;                            // channels of a thread: row tid / 16
+      const int mr = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;
+      auto store = [&](int y, const float (&o)[CH], float inv) {
+        if (y >= x.rows) return;
+        const int j = (r0 + y) / a.G, hq = w.h * a.G + (r0 + y) % a.G;
+        uint16_t* const p = a.c.out + ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D + ch;
+        const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
+        uint32_t u[CH / 2];
+#pragma unroll
+        for (int k = 0; k < CH / 2; ++k) {
+          const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+          u[k] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        if (vec && CH == 8)
+          *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[CH / 2 - 2], u[CH / 2 - 1]);
+        else if (vec)
+          *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+        else
+#pragma unroll
+          for (int k = 0; k < CH / 2; ++k) {
+            p[2 * k] = uint16_t(u[k]);
+            p[2 * k + 1] = uint16_t(u[k] >> 16);
+          }
+      };
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        consumers_sync();
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * c + k) * L::kMergeRow + KS * 2 * r + 2 * i) =
+                make_float2(acc[n][i][k], acc[n][i][k + 2]);
+        consumers_sync();
+        const int y = 8 * n + mr;
+        float M = kNoMax, sum = 0.f, o[CH];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) o[k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) M = fmaxf(M, stats[k * L::kRows + y].x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 st = stats[k * L::kRows + y];
+          const float f = ex2(st.x - M), fe = f * q8_pow2(misc[4 + k]);
+          sum += f * st.y;
+          const float* const p = merge + (k * 8 + mr) * L::kMergeRow + ch;
+#pragma unroll
+          for (int z = 0; z < CH; ++z) o[z] = fmaf(fe, p[z], o[z]);
+        }
+        if (!x.ok || *reinterpret_cast<volatile int*>(&misc[0]) != 0) sum = __int_as_float(0x7fc00000);
+        if (whole) {
+          store(y, o, sum == 0.f ? 0.f : 1.f / sum);
+        } else {
+          float* const p = a.part + (int64_t(slot) * L::kRows + y) * D + ch;
+#pragma unroll
+          for (int z = 0; z < CH; z += 4) *reinterpret_cast<float4*>(p + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+          if (ch == 0) a.stats[int64_t(slot) * L::kRows + y] = make_float2(M, sum);
+        }
+      }
+      if (!whole) {
+        // the CTAs that share the unit: cut i lies at N i / used
+        const int64_t N = a.prefix[a.B];
+        const int used = *a.used;
+        const int first = int(((w.unit + 1) * used + N - 1) / N) - 1;
+        const int last = int(((w.unit + x.V) * used + N - 1) / N) - 1;
+        __threadfence();
+        consumers_sync();
+        if (threadIdx.x == 0) misc[1] = atomicAdd(a.tickets + first, 1u) == unsigned(last - first);
+        consumers_sync();
+        if (misc[1]) {
+          __threadfence();
+#pragma unroll 1
+          for (int n = 0; n < NT; ++n) {
+            const int y = 8 * n + mr;
+            if (y >= x.rows) break;
+            float M = kNoMax, sum = 0.f, o[CH];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) o[k] = 0.f;
+            for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(&a.stats[(2 * int64_t(k) + (k == first)) * L::kRows + y]).x);
+            for (int k = first; k <= last; ++k) {
+              const int64_t at = (2 * int64_t(k) + (k == first)) * L::kRows + y;
+              const float2 st = __ldcg(&a.stats[at]);
+              const float f = ex2(st.x - M);
+              sum += f * st.y;
+              const float* const p = a.part + at * D + ch;
+#pragma unroll
+              for (int z = 0; z < CH; z += 4) {
+                const float4 u = __ldcg(reinterpret_cast<const float4*>(p + z));
+                o[z] = fmaf(f, u.x, o[z]);
+                o[z + 1] = fmaf(f, u.y, o[z + 1]);
+                o[z + 2] = fmaf(f, u.z, o[z + 2]);
+                o[z + 3] = fmaf(f, u.w, o[z + 3]);
+              }
+            }
+            store(y, o, sum == 0.f ? 0.f : 1.f / sum);
+          }
+        }
+      }
+      consumers_sync();                                     // (the next segment overwrites what was read)
+    }
+    if (dead && threadIdx.x % 32 == 0) atomicOr(a.err, 1u);
+  }
+}
+
+// ------------------------------------------------------------------------------------- host
+
+struct StreamLayout {
+  int n_ctas, rows;
+  size_t tickets, prefix, cut, stats, part, total;
+};
+
+int tiles_of_rows(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+StreamLayout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx) {
+  StreamLayout x;
+  const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
+  const int nt = tiles_of_rows(rows > 32 ? 32 : int(rows));
+  x.rows = 8 * nt;
+  const int64_t tiles = (std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity) + kQ8Tile - 1) / kQ8Tile + 1;
+  const int64_t most = int64_t(s.batch) * s.n_kv_heads * ((rows + x.rows - 1) / x.rows) * tiles;
+  const int fit = std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas);
+  x.n_ctas = int(std::min<int64_t>(most, fit));
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  x.tickets = kWsHeaderBytes;
+  x.prefix = x.tickets + up(size_t(x.n_ctas) * 4);
+  x.cut = x.prefix + up((size_t(s.batch) + 1) * 8);
+  x.stats = x.cut + up((size_t(x.n_ctas) + 1) * sizeof(Cut));
+  x.part = x.stats + up(size_t(x.n_ctas) * 2 * x.rows * 8);
+  x.total = x.part + up(size_t(x.n_ctas) * 2 * x.rows * s.head_dim * 4);
+  return x;
+}
+
+template <int D, int NT, int FMT>
+cudaError_t launch(const StreamArgs& a, cudaStream_t stream) {
+  using L = StreamSmem<D, NT>;
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(q8_stream_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  });
+  if (e != cudaSuccess) return e;
+  q8_schedule_kernel<NT><<<1, 1024, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), 160, L::total, stream, a);
+}
+
+}  // namespace
+
+size_t q8_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx) {
+  size_t most = 0;     // (a call with fewer rows may have more CTAs, each with less to leave)
+  const int heads = s.n_q_heads / s.n_kv_heads;
+  for (int rows : {8, 16, 32}) {
+    const int n = std::min(n_new, std::max(1, rows / heads));
+    most = std::max(most, stream_layout(s, n, max_ctx).total);
+  }
+  return std::max(most, stream_layout(s, n_new, max_ctx).total);
+}
+
+cudaError_t launch_q8_attention(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                                const Q8Call& c, void* ws, cudaStream_t stream) {
+  const StreamLayout x = stream_layout(s, c.n_new, c.max_ctx);
+  char* const base = static_cast<char*>(ws);
+  StreamArgs a = {};
+  a.v = q8_view(s, cache, paging, c.loop);
+  a.c = c;
+  a.B = s.batch;
+  a.Hq = s.n_q_heads;
+  a.G = s.n_q_heads / s.n_kv_heads;
+  a.cap = s.capacity;
+  bool vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0;
+  for (int i = 0; i < 3; ++i) vec = vec && c.q_strides[i] % 8 == 0;
+  a.qvec = vec;
+  a.blocks = int((int64_t(c.n_new) * a.G + x.rows - 1) / x.rows);
+  a.scale_log2 = (s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim))) * kLog2e;
+  a.err = reinterpret_cast<unsigned*>(base);
+  a.used = reinterpret_cast<int32_t*>(base + 4);
+  a.tickets = reinterpret_cast<unsigned*>(base + x.tickets);
+  a.prefix = reinterpret_cast<int64_t*>(base + x.prefix);
+  a.cut = reinterpret_cast<Cut*>(base + x.cut);
+  a.stats = reinterpret_cast<float2*>(base + x.stats);
+  a.part = reinterpret_cast<float*>(base + x.part);
+  a.n_ctas = x.n_ctas;
+  const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
+  switch (x.rows) {
+    case 8:
+      return wide ? (i8 ? launch<128, 1, RQ_Q8_INT8>(a, stream) : launch<128, 1, RQ_Q8_E4M3>(a, stream))
+                  : (i8 ? launch<64, 1, RQ_Q8_INT8>(a, stream) : launch<64, 1, RQ_Q8_E4M3>(a, stream));
+    case 16:
+      return wide ? (i8 ? launch<128, 2, RQ_Q8_INT8>(a, stream) : launch<128, 2, RQ_Q8_E4M3>(a, stream))
+                  : (i8 ? launch<64, 2, RQ_Q8_INT8>(a, stream) : launch<64, 2, RQ_Q8_E4M3>(a, stream));
+    default:
+      return wide ? (i8 ? launch<128, 4, RQ_Q8_INT8>(a, stream) : launch<128, 4, RQ_Q8_E4M3>(a, stream))
+                  : (i8 ? launch<64, 4, RQ_Q8_INT8>(a, stream) : launch<64, 4, RQ_Q8_E4M3>(a, stream));
+  }
+}
+
+}  // namespace rq

@@ -1,7 +1,7 @@
 """Thin PyTorch binding of librq: argument marshalling only.
 
 Every step of encode and decode attention runs in the library's CUDA kernels; PyTorch
-provides device memory and the current stream.  Names follow the C ABI (include/rq.h).
+provides device memory and the current stream.  Names follow the C ABI (include/rq.h, include/rq_q8.h).
 """
 
 import ctypes
@@ -9,7 +9,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import RQ_MAX_LOOPS, RqCache, RqPaging, RqShape, RqSynthParams, check
+from ._lib import (RQ_MAX_LOOPS, RqCache, RqPaging, RqQ8Cache, RqQ8Shape, RqRope, RqShape,
+                   RqSynthParams, check)
 
 GROUP = 32
 
@@ -310,6 +311,149 @@ def paged_evict_compact(shape, cache, paging, to_shape, to_cache, to_paging, kee
         ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
         ctypes.byref(to_shape), ctypes.byref(to_cache.struct), ctypes.byref(to_paging),
         *_compact_args(shape, to_shape, keep, kept_lens, weights, to_weights, stream)))
+
+
+Q8_FORMATS = {"e4m3": 0, "int8": 1}
+
+
+def make_q8_shape(batch, n_q_heads, n_kv_heads, head_dim, n_loops, capacity, fmt="e4m3",
+                  softmax_scale=0.0):
+    """rq_q8_shape of one layer's 8-bit cache; fmt "e4m3" or "int8"."""
+    return RqQ8Shape(batch, n_q_heads, n_kv_heads, head_dim, n_loops, capacity, Q8_FORMATS[fmt],
+                     float(softmax_scale))
+
+
+def q8_cache_bytes(shape):
+    return int(_lib.lib().rq_q8_cache_bytes(ctypes.byref(shape)))
+
+
+def q8_paged_cache_bytes(shape, n_pages):
+    return int(_lib.lib().rq_q8_paged_cache_bytes(ctypes.byref(shape), int(n_pages)))
+
+
+class Q8Cache:
+    """One layer's 8-bit cache in device memory (include/rq_q8.h): codes uint8, 128-byte aligned,
+    [B][Hkv][capacity/64][loops][2][64][d], or [n_pages][Hkv]... in paged form, and scales fp32
+    [...][loops][2][4].  codes, scales: existing buffers of exactly these sizes to use instead of
+    new ones (kept alive here).  rows() gives the numbers that a cache holds."""
+
+    def __init__(self, shape, device="cuda", n_pages=None, codes=None, scales=None):
+        B, H, tiles, d, L = shape.batch, shape.n_kv_heads, shape.capacity // PAGE, shape.head_dim, shape.n_loops
+        self.shape, self.n_pages = shape, n_pages
+        lead = (B, H, tiles) if n_pages is None else (n_pages, H)
+        full = (*lead, L, 2, PAGE, d)
+        n = q8_cache_bytes(shape) if n_pages is None else q8_paged_cache_bytes(shape, n_pages)
+        assert n > 0
+        if codes is None:
+            codes = torch.zeros(n, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.ones(n // (4 * d * 4), dtype=torch.float32, device=codes.device)
+        assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.numel() == n
+        assert scales.dtype == torch.float32 and scales.is_contiguous() and scales.numel() * 16 * d == n
+        self.codes, self.scales = codes.view(full), scales.view(*lead, L, 2, 4)
+        self.struct = RqQ8Cache(self.codes.data_ptr(), self.scales.data_ptr())
+
+    def rows(self):
+        """The values in natural order, fp32 [...][loops][2][64][d] (to look at; nothing calls it)."""
+        s = self.shape
+        t = torch.arange(PAGE, device=self.codes.device).view(-1, 1)
+        c = torch.arange(s.head_dim // 16, device=self.codes.device).view(1, -1)
+        at = c ^ ((t & 7) if s.head_dim == 128 else (t // 2 & 3))
+        x = self.codes.unflatten(-1, (-1, 16))
+        x = x.gather(-2, at.unsqueeze(-1).expand(x.shape)).flatten(-2)
+        x = x.view(torch.int8 if s.format == Q8_FORMATS["int8"] else torch.float8_e4m3fn).float()
+        return (x.unflatten(-2, (4, 16)) * self.scales[..., None, None]).flatten(-3, -2)
+
+    def tensors(self):
+        return [self.codes, self.scales]
+
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def make_rope(table, interleaved=False, positions=None):
+    """rq_rope: table fp32 [n_pos][rot_dim/2][2] (cos, sin), positions int32 [B][n_new] or None (a
+    token's slot); the tensors are kept alive by the handle."""
+    assert table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and table.shape[2] == 2
+    assert positions is None or (positions.dtype == torch.int32 and positions.is_contiguous())
+    r = RqRope(table.data_ptr(), None if positions is None else positions.data_ptr(), table.shape[0],
+               2 * table.shape[1], int(interleaved))
+    r.tensors = (table, positions)
+    return r
+
+
+def _rope(rope, B, n):
+    if rope is None:
+        return None
+    positions = rope.tensors[1]
+    assert positions is None or tuple(positions.shape) == (B, n)
+    return ctypes.byref(rope)
+
+
+def _q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
+    B, n, two, loops, H, d = kv_new.shape
+    assert kv_new.dtype == torch.bfloat16 and (B, two, H, d) == (shape.batch, 2, shape.n_kv_heads, shape.head_dim)
+    st = kv_new.stride()
+    assert kv_new.numel() == 0 or st[5] == 1
+    assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
+    return (kv_new.data_ptr(), _I5(*st[:5]), int(loop_begin), loops, _i32(n_lens), n, _i32(ctx_lens),
+            _rope(rope, B, n), _stream(stream))
+
+
+def q8_append(shape, cache, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None, stream=None):
+    """rq_q8_append: kv_new bf16 [B][n][2][loops][Hkv][d] (any strides, channel stride 1) goes to the
+    slots from ctx_lens[b] on, of the loops from loop_begin on; n_lens int32 [B]; rope from make_rope."""
+    check("rq_q8_append", _lib.lib().rq_q8_append(
+        ctypes.byref(shape), ctypes.byref(cache.struct),
+        *_q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+
+
+def paged_q8_append(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None,
+                    stream=None):
+    """rq_paged_q8_append; the other arguments as in q8_append."""
+    check("rq_paged_q8_append", _lib.lib().rq_paged_q8_append(
+        ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
+        *_q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+
+
+def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
+    """rq_q8_workspace_bytes: workspace of q8_attention / paged_q8_attention calls of this shape with
+    at most these n_new and max_ctx."""
+    return int(_lib.lib().rq_q8_workspace_bytes(ctypes.byref(shape), int(n_new), int(max_ctx),
+                                                int(window), int(n_sink)))
+
+
+def _q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
+    B, n, Hq, d = q.shape
+    assert q.dtype == out.dtype == torch.bfloat16
+    assert (B, Hq, d) == (shape.batch, shape.n_q_heads, shape.head_dim)
+    qs = q.stride()
+    assert q.numel() == 0 or qs[3] == 1
+    assert out.is_contiguous() and out.shape == q.shape
+    assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
+    return (q.data_ptr(), _I3(*qs[:3]), int(loop), _i32(n_lens), n, _i32(ctx_lens), int(max_ctx),
+            int(window), int(n_sink), _rope(rope, B, n), out.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _stream(stream))
+
+
+def q8_attention(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None, window=0, n_sink=0,
+                 rope=None, stream=None):
+    """rq_q8_attention: q, out bf16 [B][n][Hq][d] (q any strides, channel stride 1) of the n tokens
+    that q8_append stored from ctx_lens[b] on; window 0: all slots up to a token's own, else its last
+    `window` and the first n_sink."""
+    check("rq_q8_attention", _lib.lib().rq_q8_attention(
+        ctypes.byref(shape), ctypes.byref(cache.struct),
+        *_q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+                            stream)))
+
+
+def paged_q8_attention(shape, cache, paging, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None, window=0,
+                       n_sink=0, rope=None, stream=None):
+    """rq_paged_q8_attention; the other arguments as in q8_attention."""
+    check("rq_paged_q8_attention", _lib.lib().rq_paged_q8_attention(
+        ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
+        *_q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+                            stream)))
 
 
 def synth_params(seed, layer, head_dim, n_kv_heads, dist, sigma, outlier_mult, outlier_table):
