@@ -21,7 +21,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["rq_api.cu", "rq_encode.cu", "rq_decode.cu", "rq_decode_mma.cu", "rq_decode_mma_paged.cu", "rq_bf16.cu",
            "rq_synth.cu", "rq_noalloc.cu", "rq_chunk.cu", "rq_chunk_mma.cu",
            "rq_chunk_mma_paged.cu", "rq_chunk_tc.cu",
-           "rq_chunk_fused.cu", "rq_evict.cu", "rq_q8_api.cu", "rq_q8_append.cu", "rq_q8_stream.cu"]
+           "rq_chunk_fused.cu", "rq_evict.cu", "rq_q8_api.cu", "rq_q8_append.cu", "rq_q8_stream.cu",
+           "rq_q8_rows.cu"]
 
 
 def nvcc():

@@ -132,9 +132,16 @@ struct Q8Call {          // an attention call, arguments as in include/rq_q8.h
   uint16_t* out;
 };
 
-size_t q8_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx);
+size_t q8_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink);
 cudaError_t launch_q8_attention(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
                                 const Q8Call& c, void* ws, cudaStream_t stream);
+// Few rows a kv-head (rq_q8_stream.cu), many (rq_q8_rows.cu); their workspaces.
+size_t q8_stream_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx);
+cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                             const Q8Call& c, void* ws, cudaStream_t stream);
+size_t q8_rows_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink);
+cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                           const Q8Call& c, void* ws, cudaStream_t stream);
 cudaError_t launch_q8_append(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
                              const uint16_t* kv_new, const int64_t strides[5], int loop_begin,
                              int loop_count, const int32_t* n_lens, int n_new, const int32_t* ctx_lens,

@@ -95,7 +95,7 @@ rq_status attention_common(const rq_q8_shape* s, const rq_q8_cache* cache, const
                   n_sink, {}, out};
   if ((st = check_rope(s, rope, c.rope)) != RQ_OK) return st;
   if (n_new == 0) return RQ_OK;
-  if (!ws || ws_bytes < rq::q8_workspace_bytes(*s, n_new, max_ctx)) return RQ_ERR_WORKSPACE;
+  if (!ws || ws_bytes < rq::q8_workspace_bytes(*s, n_new, max_ctx, window, n_sink)) return RQ_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RQ_ERR_WORKSPACE;
   // rows are read while others are written
   const uintptr_t o0 = reinterpret_cast<uintptr_t>(out);
@@ -142,7 +142,7 @@ rq_status rq_paged_q8_append(const rq_q8_shape* shape, const rq_q8_cache* cache,
 size_t rq_q8_workspace_bytes(const rq_q8_shape* s, int32_t n_new, int32_t max_ctx, int32_t window,
                              int32_t n_sink) {
   if (check_shape(s) != RQ_OK || check_sizes(s, n_new, max_ctx, window, n_sink) != RQ_OK) return 0;
-  return n_new == 0 ? size_t(rq::kWsHeaderBytes) : rq::q8_workspace_bytes(*s, n_new, max_ctx);
+  return n_new == 0 ? size_t(rq::kWsHeaderBytes) : rq::q8_workspace_bytes(*s, n_new, max_ctx, window, n_sink);
 }
 
 rq_status rq_q8_attention(const rq_q8_shape* shape, const rq_q8_cache* cache, const uint16_t* q,

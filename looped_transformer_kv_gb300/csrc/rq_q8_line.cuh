@@ -1,0 +1,242 @@
+// The line of an attention call over the 8-bit cache: for each sequence, for each block of rows and
+// kv-head, the key tiles that the block sees.  It is cut evenly for the CTAs that fit the GPU at once;
+// a unit (sequence, block, kv-head) that cuts divide leaves partial results in the workspace.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+#include "rq_kernels.h"
+#include "rq_launch.cuh"
+#include "rq_q8.cuh"
+
+namespace rq {
+
+struct Cut {           // a CTA's stretch of the line
+  int64_t pos, base;    // where it begins; where sequence b's units begin
+  int32_t b, pad;
+};
+
+struct Q8Line {
+  Q8View v;
+  Q8Call c;
+  int32_t B, Hq, G, cap, qvec;
+  int32_t blocks;        // blocks of rows, of n_new tokens
+  float scale_log2;
+  unsigned* err;         // workspace: error word, ...
+  int32_t* used;         // CTAs with work
+  unsigned* tickets;     // [CTA][n_tickets] of the unit that is cut at its end
+  int64_t* prefix;       // [B + 1] places of the sequences
+  Cut* cut;              // [CTA + 1]
+  float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l); or four floats each
+  float* part;           // ... their sums
+  int32_t n_ctas, n_tickets;
+  int32_t clear;         // the call's first launch
+};
+
+// The tiles of 64 slots that some new token of a sequence sees, as a list: 0 .. sink0 and then from
+// first0 on; and what a block of ROWS rows sees of it, in steps of KEYS keys.
+struct Rows {
+  int ctx, n, j0, j1;      // tokens of the block's rows
+  int rows;                // of the block
+  int sink0, first0, tiles, end;   // the list, its length, the slot behind its last
+  int sink, first, V, hi;  // steps 0 .. sink and from `first` on, V in all; the slot behind the block's last
+  bool ok;
+  __device__ __forceinline__ int step(int u) const { return u < sink ? u : first + u - sink; }     // the u-th step's place
+  __device__ __forceinline__ int tile(int v) const { return v < sink0 ? v : first0 + v - sink0; }  // tile at place v
+};
+
+__device__ __forceinline__ Rows sequence_of(const Q8Line& a, int b) {
+  Rows x;
+  x.ctx = a.c.ctx_lens[b];
+  x.n = a.c.n_lens ? a.c.n_lens[b] : a.c.n_new;
+  x.ok = x.ctx >= 0 && x.ctx <= a.c.max_ctx && x.n >= 0 && x.n <= a.c.n_new && x.ctx <= a.cap - x.n;
+  if (x.n < 0 || x.n > a.c.n_new) x.n = a.c.n_new;
+  x.sink0 = x.first0 = x.tiles = x.end = 0;
+  if (!x.ok || x.n == 0) return x;
+  const int lo = a.c.window > 0 ? max(0, x.ctx + 1 - a.c.window) : 0;
+  x.end = x.ctx + x.n;
+  x.first0 = lo / kQ8Tile;
+  x.sink0 = min((min(a.c.n_sink, lo) + kQ8Tile - 1) / kQ8Tile, x.first0);
+  x.tiles = x.sink0 + (x.end + kQ8Tile - 1) / kQ8Tile - x.first0;
+  return x;
+}
+
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Rows rows_of(const Q8Line& a, int b, int block) {
+  constexpr int K = KEYS / kQ8Tile;
+  Rows x = sequence_of(a, b);
+  const int r0 = block * ROWS;
+  x.rows = min(ROWS, x.n * a.G - r0);
+  x.sink = x.first = x.V = x.hi = 0;
+  if (x.rows <= 0) return x;
+  x.j0 = r0 / a.G;
+  x.j1 = (r0 + x.rows - 1) / a.G;
+  x.V = 1;                                                  // (bad lengths: one step, not read)
+  if (!x.ok) return x;
+  const int lo = a.c.window > 0 ? max(0, x.ctx + x.j0 + 1 - a.c.window) : 0, first = lo / kQ8Tile;
+  x.hi = x.ctx + x.j1 + 1;
+  // (sinks beyond sink0 only where the list begins at tile 0 without a gap: their places are their tiles)
+  const int sinks = min((min(a.c.n_sink, lo) + kQ8Tile - 1) / kQ8Tile, first);
+  x.first = (x.sink0 + first - x.first0) / K;
+  x.sink = min((sinks + K - 1) / K, x.first);
+  x.V = x.sink + (x.sink0 + (x.hi + kQ8Tile - 1) / kQ8Tile - x.first0 + K - 1) / K - x.first;
+  return x;
+}
+
+// One CTA: clears the error word and tickets, cuts the line.
+template <int ROWS, int KEYS>
+__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ Q8Line a) {
+  grid_next();
+  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0 && a.clear) *a.err = 0u;
+  for (int i = tid; i < a.n_ctas * a.n_tickets; i += 1024) a.tickets[i] = 0u;
+  int64_t run = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+    int64_t units = 0;
+    if (b0 + tid < a.B) {
+      for (int k = 0; k < a.blocks; ++k) {
+        const Rows x = rows_of<ROWS, KEYS>(a, b0 + tid, k);
+        bad |= !x.ok;
+        if (x.V == 0) break;
+        units += x.V;
+      }
+      units *= a.v.H;
+    }
+    int64_t sum = units;                                    // inclusive scan over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(RQ_FULL_MASK, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t before = run;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      run += warp_sum[w];
+    }
+    if (b0 + tid < a.B) a.prefix[b0 + tid] = before + sum - units;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.prefix[a.B] = run;
+    total = run;
+  }
+  bad = __syncthreads_or(bad);                              // (and the prefix is written)
+  if (bad && tid == 0) *a.err = 1u;
+  const int64_t N = total;
+  const int used = int(min(N, int64_t(a.n_ctas)));
+  if (tid == 0) *a.used = used;
+  for (int i = tid; i <= used; i += 1024) {
+    const int64_t pos = used ? N * i / used : 0;
+    int lo = 0, hi = a.B;                                   // the last sequence that begins at or before pos
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.prefix[mid] <= pos) lo = mid; else hi = mid;
+    }
+    a.cut[i] = {pos, a.prefix[lo], lo, 0};
+  }
+}
+
+// A CTA's segments in order.
+template <int ROWS, int KEYS>
+struct Walk {
+  const Q8Line& a;
+  int64_t pos, end, base;   // base: where the units of (b, block) begin
+  int b, block;
+  Rows x;
+  int h, kt0, T;
+  int64_t unit;             // the unit's place on the line
+  bool loaded;
+  __device__ __forceinline__ Walk(const Q8Line& args, const Cut& from, int64_t to)
+      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(0), loaded(false) {}
+  __device__ __forceinline__ bool next() {
+    if (pos >= end) return false;
+    for (;;) {
+      if (!loaded) {
+        x = rows_of<ROWS, KEYS>(a, b, block);
+        loaded = true;
+      }
+      const int64_t stop = base + int64_t(x.V) * a.v.H;
+      if (pos < stop) break;
+      base = stop;
+      loaded = false;
+      if (x.V == 0 || ++block == a.blocks) {
+        block = 0;
+        if (++b == a.B) return false;                       // (not with a sound schedule)
+      }
+    }
+    h = int((pos - base) / x.V);
+    unit = base + int64_t(h) * x.V;
+    kt0 = int(pos - unit);
+    T = int(min(int64_t(x.V - kt0), end - pos));
+    pos += T;
+    return true;
+  }
+  // The CTAs that share the unit (cut i lies at N i / used).
+  __device__ __forceinline__ void sharers(int& first, int& last) const {
+    const int64_t N = a.prefix[a.B];
+    const int used = *a.used;
+    first = int(((unit + 1) * used + N - 1) / N) - 1;
+    last = int(((unit + x.V) * used + N - 1) / N) - 1;
+  }
+};
+
+inline Q8Line q8_line(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging, const Q8Call& c,
+                      int rows) {
+  Q8Line a = {};
+  a.v = q8_view(s, cache, paging, c.loop);
+  a.c = c;
+  a.B = s.batch;
+  a.Hq = s.n_q_heads;
+  a.G = s.n_q_heads / s.n_kv_heads;
+  a.cap = s.capacity;
+  bool vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0;
+  for (int i = 0; i < 3; ++i) vec = vec && c.q_strides[i] % 8 == 0;
+  a.qvec = vec;
+  a.blocks = int((int64_t(c.n_new) * a.G + rows - 1) / rows);
+  a.scale_log2 = (s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim))) * kLog2e;
+  return a;
+}
+
+// Places in the workspace, and its size.
+struct Q8Layout {
+  int n_ctas;
+  size_t tickets, prefix, cut, stats, part, total;
+};
+
+inline Q8Layout q8_layout(const rq_q8_shape& s, int n_new, int max_ctx, int rows, int keys, int fit, int n_tickets) {
+  Q8Layout x;
+  const int64_t all = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
+  const int64_t tiles = (std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity) + keys - 1) / keys + 1;
+  const int64_t most = int64_t(s.batch) * s.n_kv_heads * ((all + rows - 1) / rows) * tiles;
+  x.n_ctas = int(std::min<int64_t>(most, fit));
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  x.tickets = kWsHeaderBytes;
+  x.prefix = x.tickets + up(size_t(x.n_ctas) * 4 * n_tickets);
+  x.cut = x.prefix + up((size_t(s.batch) + 1) * 8);
+  x.stats = x.cut + up((size_t(x.n_ctas) + 1) * sizeof(Cut));
+  x.part = x.stats + up(size_t(x.n_ctas) * 2 * rows * 16);
+  x.total = x.part + up(size_t(x.n_ctas) * 2 * rows * s.head_dim * 4);
+  return x;
+}
+
+inline void q8_place(Q8Line& a, const Q8Layout& x, void* ws, int n_tickets) {
+  char* const base = static_cast<char*>(ws);
+  a.err = reinterpret_cast<unsigned*>(base);
+  a.used = reinterpret_cast<int32_t*>(base + 4);
+  a.tickets = reinterpret_cast<unsigned*>(base + x.tickets);
+  a.prefix = reinterpret_cast<int64_t*>(base + x.prefix);
+  a.cut = reinterpret_cast<Cut*>(base + x.cut);
+  a.stats = reinterpret_cast<float2*>(base + x.stats);
+  a.part = reinterpret_cast<float*>(base + x.part);
+  a.n_ctas = x.n_ctas;
+  a.n_tickets = n_tickets;
+  a.clear = 1;
+}
+
+}  // namespace rq

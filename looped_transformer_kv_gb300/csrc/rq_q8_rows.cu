@@ -1,0 +1,839 @@
+// Attention over the 8-bit cache for many query rows (include/rq_q8.h) on the 5th-generation tensor
+// cores: blocks of 256 rows (two tiles of 128) share every tile of 128 keys.
+//
+//   S = Q K^T, O += P V as tcgen05 products of 128 x 128 tiles; S, P and O in tensor memory.
+// Codes become fp16 operands in shared memory, exactly: a key tile takes the largest of its blocks'
+// scales as its own, the codes of the others are multiplied by the power of two between them
+// (a block 2^-15 of the largest is still exact, smaller ones keep 2^-32 of the largest code).  V's tile
+// scale 2^e_V goes into the weights' exponent and is taken out of their sum again,
+//   P = 2^((S 2^e_K - R) c + e_V - h),  l += 2^-e_V sum P,
+// so that tiles of different scales need no rescaling of O.  R (a row's largest score, raw) and h are
+// raised when a weight would exceed 2^15, to make the largest 2^7.
+//
+// Many blocks of rows share a tile: its operands are then made once, in the workspace
+// (q8_image_kernel), and copied from there (IMG); else each block converts what it reads.
+//
+// Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; IMG: warp 9:
+// copies; else warps 12-15: codes from global memory (a tile ahead, in registers) to operands.
+// CTAs (one per SM) share the work by the line of rq_q8_line.cuh; the last CTA of a divided unit to
+// finish joins its partial results in order, each row tile for itself.
+#include "rq_q8_line.cuh"
+#include "rq_tc.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kKeys = 128, kRowTile = 128, kBlockRows = 2 * kRowTile;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMostCtas = 1024;
+using RowWalk = Walk<kBlockRows, kKeys>;
+
+template <int D>
+struct RowsSmem {
+  static constexpr int kTile = kKeys * D * 2;               // one K, V or Q tile
+  static constexpr int v = 0, k = 2 * kTile, q = 5 * kTile, exps = 7 * kTile;   // V first: see v_desc
+  static constexpr int row_exps = exps + 64;                // [8] K's and V's exponent of a tile
+  static constexpr int bars = row_exps + kBlockRows * 4;
+  static constexpr int kImage = 2 * kTile + 128;            // of a tile in the workspace
+  static constexpr int total = bars + 256 + 1024;           // + alignment of the base
+  static_assert(total <= 227 * 1024, "shared memory of one CTA");
+};
+
+// V tile as the product's B operand, channels contiguous: panels of 64 channels, rows of 128 bytes a
+// token; 8 tokens are 1024 bytes, panels kKeys * 128 bytes apart.
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(kKeys * 128 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void group_sync(int i) {         // 128 threads of softmax group 0 or 1
+  if (i == 0)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+__device__ __forceinline__ bool group_any(int i, bool x) {
+  uint32_t y;
+  if (i == 0)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(uint32_t(x)) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(uint32_t(x)) : "memory");
+  return y != 0u;
+}
+
+__device__ __forceinline__ uint32_t half2_pow2(int e) {     // 2^e twice, e <= 0; below 2^-24: 0
+  const uint32_t h = e >= -14 ? uint32_t(15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+  return h * 0x10001u;
+}
+
+// Two codes times the power of two f (bias: int8's -1152 f).
+template <int FMT, int HALF>
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t w, uint32_t f, uint32_t bias) {
+  uint32_t out;
+  if (FMT == RQ_Q8_INT8) {
+    const uint32_t t = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(out) : "r"(t), "r"(f), "r"(bias));
+  } else {
+    asm("mul.f16x2 %0, %1, %2;" : "=r"(out) : "r"(q8_pair<FMT, HALF>(w)), "r"(f));
+  }
+  return out;
+}
+
+// Bit y of the result: column y (0..31) lies in [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+
+struct RowsArgs : Q8Line {
+  uint8_t* images;       // operand tiles, [B][Hkv][list] of K, V, their exponents
+  int32_t list;          // of one unit, at most
+};
+
+// One key tile of 128 slots from codes to operands by 128 threads, a thread the same 16 channels of
+// every 16th (d = 64: 32nd) row.
+template <int D, int FMT>
+struct Converter {
+  static constexpr int CPR = D / 16;                         // 16-byte chunks of a row
+  static constexpr int PIECES = kKeys * CPR / 128;           // of a thread and K or V tile
+  const Q8Line& a;
+  const int tid, lane, row0, c, first;
+  const uint32_t panel;
+  int64_t rec[2];                                            // records of the tile's halves; -1: no page, -2: not there
+  float scale;                                               // lane l < 16: block l % 8 of K (l < 8) or V
+  uint32_t factor, lost;                                     // of take_scales: 2^(e - top) of the same; K's blocks to spoil
+  int v_from;                                                // V rows from here on hold nothing
+
+  // (rows of a thread's pieces differ by multiples of 16, so the chunk is the same; `first`: which half
+  // is stored first, so that neighbours meet distinct banks)
+  __device__ __forceinline__ Converter(const Q8Line& line, int t, int l)
+      : a(line), tid(t), lane(l), row0(t / CPR), c((t % CPR) ^ q8_swizzle<D>(t / CPR)),
+        first(D == 128 && c >= 4 ? 1 : 0), panel(uint32_t(c / 4) * (kKeys * 128)), scale(1.f), factor(0u), lost(0u), v_from(0) {}
+
+  __device__ __forceinline__ int64_t record(const Rows& x, int b, int h, int v) const {
+    if (v >= x.tiles) return -2;
+    const int64_t r = a.v.record(b, h, x.tile(v));
+    if (r == -1) atomicOr(a.err, 1u);
+    return r;
+  }
+  __device__ __forceinline__ void load(uint4 (&reg)[PIECES], int kv) const {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int half = p >= PIECES / 2;
+      reg[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (rec[half] >= 0)
+        reg[p] = __ldg(reinterpret_cast<const uint4*>(a.v.codes + rec[half] * a.v.rec_codes + kv * (kQ8Tile * D)) + tid +
+                       (p - half * (PIECES / 2)) * 128);
+    }
+  }
+  __device__ __forceinline__ void load_scales() {
+    const int64_t r = lane & 4 ? rec[1] : rec[0];
+    scale = r >= 0 && lane < 16 ? a.v.scales[r * a.v.rec_scales + (lane >> 3) * 4 + (lane & 3)] : 1.f;
+  }
+  // The tile's exponents of K and V, from its blocks that hold something; the tile begins at place v.
+  __device__ __forceinline__ int2 take_scales(const Rows& x, int v) {
+    const int half = lane >> 2 & 1;
+    const int64_t r = half ? rec[1] : rec[0];
+    const int left = v + half < x.tiles ? x.end - x.tile(v + half) * kQ8Tile : 0;   // slots of the half that hold something
+    const bool live = r >= 0 && (lane & 3) * kQ8Block < left && lane < 16;
+    const bool nan = live && !(scale < INFINITY);
+    const int e = live && !nan ? q8_exponent(scale) : -1000;
+    int top = e;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(RQ_FULL_MASK, top, o));
+    if (top == -1000) top = 0;
+    factor = e == -1000 ? 0u : half2_pow2(max(e - top, -30));
+    // (a scale that is not a number, K's or V's, spoils the scores: V then only meets weights of tokens
+    // that see the block)
+    const uint32_t nans = __ballot_sync(RQ_FULL_MASK, nan || (r == -1 && lane < 16));
+    lost = (nans | (nans >> 8)) & 255u;
+    // rows that hold something: the first half is full if there is a second
+    const int left0 = __shfl_sync(RQ_FULL_MASK, left, 0), left1 = __shfl_sync(RQ_FULL_MASK, left, 4);
+    v_from = v + 1 < x.tiles ? kQ8Tile + min(left1, kQ8Tile) : min(left0, kQ8Tile);
+    return make_int2(__shfl_sync(RQ_FULL_MASK, top, 0), __shfl_sync(RQ_FULL_MASK, top, 8));
+  }
+  // Operands of K or V.
+  __device__ __forceinline__ void put(const uint4 (&reg)[PIECES], uint8_t* tile, int kv) const {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int row = row0 + p * (128 / CPR), blk = row >> 4;
+      const uint32_t f = __shfl_sync(RQ_FULL_MASK, factor, 8 * kv + blk);
+      uint32_t bias;
+      asm("mul.f16x2 %0, %1, %2;" : "=r"(bias) : "r"(f), "r"(0xe480e480u));   // -1152 f
+      const uint32_t wd[4] = {reg[p].x, reg[p].y, reg[p].z, reg[p].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t y = q8_word<FMT>(wd[k]);
+        o[2 * k] = scaled_pair<FMT, 0>(y, f, bias);
+        o[2 * k + 1] = scaled_pair<FMT, 1>(y, f, bias);
+      }
+      const bool spoil = kv == 0 && (lost >> blk & 1u), none = kv == 1 && row >= v_from;
+      if (spoil || none)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = none ? 0u : 0x7fff7fffu;
+      uint8_t* const at = tile + panel;
+      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+      const int ch = 2 * (c & 3);
+      *reinterpret_cast<uint4*>(at + panel_offset(row, ch + first)) = first ? hi : lo;
+      *reinterpret_cast<uint4*>(at + panel_offset(row, ch + 1 - first)) = first ? lo : hi;
+    }
+  }
+};
+
+// Operand tiles of a whole call: 128 threads for K, 128 for V of one tile.
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ RowsArgs a) {
+  grid_wait();
+  grid_next();
+  const int kv = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const int u = int(blockIdx.x % unsigned(a.list));
+  const int unit = int(blockIdx.x / unsigned(a.list)), b = unit / a.v.H, h = unit % a.v.H;
+  const Rows x = sequence_of(a, b);
+  if (2 * u >= x.tiles) return;
+  Converter<D, FMT> to(a, threadIdx.x & 127, lane);
+  to.rec[0] = to.record(x, b, h, 2 * u);
+  to.rec[1] = to.record(x, b, h, 2 * u + 1);
+  uint4 reg[Converter<D, FMT>::PIECES];
+  to.load(reg, kv);
+  to.load_scales();
+  const int2 e = to.take_scales(x, 2 * u);
+  uint8_t* const image = a.images + (int64_t(unit) * a.list + u) * RowsSmem<D>::kImage;
+  to.put(reg, image + kv * RowsSmem<D>::kTile, kv);
+  if (threadIdx.x == 0) *reinterpret_cast<int2*>(image + 2 * RowsSmem<D>::kTile) = e;
+}
+
+// Exponents of tile t of the walk's segment.
+template <int D, typename W>
+__device__ __forceinline__ const int2* image_exps(const RowsArgs& a, const W& w, int t) {
+  return reinterpret_cast<const int2*>(a.images + ((int64_t(w.b) * a.v.H + w.h) * a.list + w.x.step(w.kt0 + t)) * RowsSmem<D>::kImage +
+                                       2 * RowsSmem<D>::kTile);
+}
+
+template <int D, int FMT, bool IMG>
+__global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __grid_constant__ RowsArgs a) {
+  grid_wait();
+  const int me = int(blockIdx.x);
+  if (me >= *a.used) return;
+  extern __shared__ uint8_t raw[];
+  using L = RowsSmem<D>;
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+  // barriers: K full [3], V full [2], step [8], S of row tile 0 [2], P ready [2], Q ready, drained.
+  // A step ends with the last row tile's scores of a tile (and the values of the tile before), or with
+  // the values of a segment's last tile: T + 1 steps for T tiles.  It frees K and V tiles.
+  const uint32_t bar0 = smem_u32(bars);
+  auto kfull = [&](int g) { return bar0 + 8 * (g % 3); };
+  auto vfull = [&](int g) { return bar0 + 8 * (3 + (g & 1)); };
+  auto step = [&](int n) { return bar0 + 8 * (5 + (n & 7)); };
+  auto sready = [&](int c) { return bar0 + 8 * (13 + (c & 1)); };
+  auto pready = [&](int i) { return bar0 + 8 * (15 + i); };
+  const uint32_t qready = bar0 + 8 * 17, drained = bar0 + 8 * 18;
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 19);
+  int* const last_one = reinterpret_cast<int*>(bars + 20);  // [row tile]
+  int2* const exps = reinterpret_cast<int2*>(smem + L::exps);        // [8] of tiles: K's, V's
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8) tc_alloc(smem_u32(tslot), 512);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(bar0 + 8 * i, IMG ? 1 : 128);
+    for (int i = 5; i < 15; ++i) mbar_init(bar0 + 8 * i, 1);
+    mbar_init(pready(0), kRowTile);
+    mbar_init(pready(1), kRowTile);
+    mbar_init(qready, kBlockRows);
+    mbar_init(drained, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const Cut from = a.cut[me];
+  RowWalk w(a, from, a.cut[me + 1].pos);
+  bool failed = false;
+
+  if (!IMG && warp >= 12) {                                  // ---- codes to operands
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    Converter<D, FMT> to(a, threadIdx.x - 384, lane);
+    constexpr int PIECES = Converter<D, FMT>::PIECES;
+    int g = 0, n0 = 0;                                       // tiles so far; g's step is n0 + g
+    int sk[3] = {-1, -1, -1};                                // steps that end with K tile g - 1, g - 2, g - 3
+    while (!failed && w.next()) {
+      const Rows& x = w.x;
+      if (!x.ok) continue;
+      uint4 kreg[PIECES], vreg[PIECES];
+      int64_t rec32 = -2;                                    // a lane's of 16 steps
+      auto load_records = [&](int t) {
+        const int u = t + lane / 2;
+        rec32 = u < w.T ? to.record(x, w.b, w.h, 2 * x.step(w.kt0 + u) + (lane & 1)) : -2;
+      };
+      auto aim = [&](int t) {
+        to.rec[0] = __shfl_sync(RQ_FULL_MASK, rec32, 2 * t & 31);
+        to.rec[1] = __shfl_sync(RQ_FULL_MASK, rec32, (2 * t + 1) & 31);
+      };
+      // K runs up to three tiles ahead of the scores, V one behind K: K0 V0 K1 V1 ...
+      load_records(0);
+      aim(0);
+      to.load(kreg, 0);
+      to.load_scales();
+      to.load(vreg, 1);
+      for (int t = 0; t < w.T; ++t, ++g) {
+        // scores of tile g - 3 done: K's place
+        if (g >= 3) failed = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(step(sk[2]), (sk[2] >> 3) & 1, kWaitNs));
+        if (failed) break;
+        const int2 e = to.take_scales(x, 2 * x.step(w.kt0 + t));
+        if (to.tid == 0) exps[g & 7] = e;
+        to.put(kreg, smem + L::k + (g % 3) * L::kTile, 0);
+        fence_async_smem();
+        mbar_arrive(kfull(g));
+        if (t + 1 < w.T) {
+          if (((t + 1) & 15) == 0) load_records(t + 1);
+          aim(t + 1);
+          to.load(kreg, 0);
+          to.load_scales();
+        }
+        // values of tile g - 2 done (the step after its scores'): V's place
+        if (g >= 2) failed = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(step(sk[1] + 1), ((sk[1] + 1) >> 3) & 1, kWaitNs));
+        if (failed) break;
+        to.put(vreg, smem + L::v + (g & 1) * L::kTile, 1);
+        fence_async_smem();
+        mbar_arrive(vfull(g));
+        if (t + 1 < w.T) to.load(vreg, 1);
+        sk[2] = sk[1];
+        sk[1] = sk[0];
+        sk[0] = n0 + g;
+      }
+      ++n0;
+    }
+  } else if (warp >= 8) {
+    if constexpr (IMG)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    const bool leader = elect_one();
+    if (IMG && warp == 9 && leader) {                        // ---- copies of operand tiles
+      int g = 0, n0 = 0, sk[3] = {-1, -1, -1};               // as the converting warps'
+      while (!failed && w.next()) {
+        if (!w.x.ok) continue;
+        const uint8_t* const unit = a.images + (int64_t(w.b) * a.v.H + w.h) * a.list * RowsSmem<D>::kImage;
+        for (int t = 0; t < w.T; ++t, ++g) {
+          const uint8_t* const tile = unit + w.x.step(w.kt0 + t) * int64_t(RowsSmem<D>::kImage);
+          if (g >= 3) failed = !mbar_wait_bounded(step(sk[2]), (sk[2] >> 3) & 1, kWaitNs);
+          if (failed) break;
+          mbar_arrive_expect_tx(kfull(g), L::kTile);
+          bulk_g2s(smem_u32(smem + L::k + (g % 3) * L::kTile), tile, L::kTile, kfull(g));
+          if (g >= 2) failed = !mbar_wait_bounded(step(sk[1] + 1), ((sk[1] + 1) >> 3) & 1, kWaitNs);
+          if (failed) {
+            ++g;
+            break;
+          }
+          mbar_arrive_expect_tx(vfull(g), L::kTile);
+          bulk_g2s(smem_u32(smem + L::v + (g & 1) * L::kTile), tile + L::kTile, L::kTile, vfull(g));
+          sk[2] = sk[1];
+          sk[1] = sk[0];
+          sk[0] = n0 + g;
+        }
+        ++n0;
+      }
+      // copies land before the CTA leaves
+      for (int k = max(0, g - 3); failed && k < g; ++k) mbar_wait_bounded(kfull(k), (k / 3) & 1, kWaitNs);
+      for (int k = max(0, g - 2); failed && k < g; ++k) mbar_wait_bounded(vfull(k), (k >> 1) & 1, kWaitNs);
+    } else if (warp == 8 && leader) {                        // ---- products
+      constexpr uint32_t ids = f16_idesc(kRowTile, kKeys), ido = f16_idesc(kRowTile, D) | (1u << 16);   // (B: channels contiguous)
+      int g = 0, c0 = 0, c1 = 0, n = 0, seg = 0;             // tiles; P's of row tile 0, 1; steps; segments
+      int s0 = 0;                                            // S's of row tile 0 with a row tile 1
+      bool good = true;
+      auto scores = [&](int i, int gk) {
+        const uint32_t q = smem_u32(smem + L::q + i * L::kTile), k = smem_u32(smem + L::k + (gk % 3) * L::kTile);
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y)
+          tc_mma(tmem + 128 * i, panel_desc(q + (y / 4) * (kRowTile * 128) + (y % 4) * 32),
+                 panel_desc(k + (y / 4) * (kKeys * 128) + (y % 4) * 32), ids, y > 0);
+      };
+      auto values = [&](int i, int gv, bool add) {
+        const uint32_t v = smem_u32(smem + L::v + (gv & 1) * L::kTile);
+#pragma unroll
+        for (int y = 0; y < kKeys / 16; ++y)
+          tc_mma_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * y, v_desc(v + y * 2048), ido, add || y > 0);
+      };
+      while (good && w.next()) {
+        if (!w.x.ok) continue;
+        const bool two = w.x.rows > kRowTile;
+        good = mbar_wait_bounded(kfull(g), (g / 3) & 1, kWaitNs) && mbar_wait_bounded(qready, seg & 1, kWaitNs);
+        ++seg;
+        tc_fence_after();
+        if (!good) break;
+        scores(0, g);
+        if (two) {
+          tc_commit(sready(s0++));
+          scores(1, g);
+        }
+        tc_commit(step(n++));
+        for (int j = 0; j < w.T && good; ++j, ++g) {
+          good = mbar_wait_bounded(vfull(g), (g >> 1) & 1, kWaitNs);
+          const bool more = j + 1 < w.T;
+          if (good && more) good = mbar_wait_bounded(kfull(g + 1), ((g + 1) / 3) & 1, kWaitNs);
+          if (!good) break;
+          good = mbar_wait_bounded(pready(0), c0++ & 1, kWaitNs);
+          if (!good) break;
+          tc_fence_after();
+          values(0, g, j > 0);
+          if (more) scores(0, g + 1);
+          if (two) {
+            if (more) tc_commit(sready(s0++));
+            good = mbar_wait_bounded(pready(1), c1++ & 1, kWaitNs);
+            if (!good) break;
+            tc_fence_after();
+            values(1, g, j > 0);
+            if (more) scores(1, g + 1);
+          }
+          tc_commit(step(n++));
+        }
+      }
+      if (!good) {                                           // nothing in flight when the CTA leaves
+        tc_commit(drained);
+        mbar_wait_bounded(drained, 0, kWaitNs);
+        failed = true;
+      }
+    }
+    __syncwarp();
+  } else {                                                   // ---- softmax
+    if constexpr (IMG)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int i = warp >> 2, r = threadIdx.x & (kRowTile - 1);
+    const uint32_t lanes = uint32_t(warp & 3) << 21;          // this warp's tensor-memory lanes
+    const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
+    float* const row_scale = reinterpret_cast<float*>(smem + L::row_exps) + i * kRowTile;
+    uint8_t* const img = smem + L::q + i * L::kTile;          // queries, then results going out
+    float4* const stats = reinterpret_cast<float4*>(a.stats);
+    int g = 0, n0 = 0, s0 = 0;
+    while (w.next()) {                                         // (failed: nothing is waited for any more, results are NaN)
+      const Rows& x = w.x;
+      const int r0 = w.block * kBlockRows + i * kRowTile;      // the row tile's first row
+      const bool two = x.rows > kRowTile, mine = i == 0 || two;
+      const int row = r0 + r;
+      // ---- queries to operands, 32 rows a warp
+      if (x.ok && !failed) {
+        if (mine) {
+          constexpr int LPR = D / 8, RPI = 32 / LPR;
+          const int qc = lane % LPR;
+#pragma unroll 2
+          for (int y = 0; y < 32 / RPI; ++y) {
+            const int rr = (warp & 3) * 32 + y * RPI + lane / LPR;
+            const bool live = i * kRowTile + rr < x.rows;
+            const int j = (r0 + rr) / a.G, hq = w.h * a.G + (r0 + rr) % a.G;
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = 0.f;
+            if (live) q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec, f);
+            bool out_of_table = false;
+            if (a.c.rope.table != nullptr) {
+              int p = -1;
+              if (live) {
+                p = a.c.rope.positions ? a.c.rope.positions[int64_t(w.b) * a.c.n_new + j] : x.ctx + j;
+                out_of_table = p < 0 || p >= a.c.rope.n_pos;
+                if (out_of_table) p = -1;
+              }
+              q8_rotate<D>(f, a.c.rope, p, lane);
+            }
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
+            const int ex = int(__float_as_uint(mx) >> 23);
+            const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);   // largest in [2^14, 2^15)
+            const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = pack_half2(f[2 * k] * up * up2, f[2 * k + 1] * up * up2);
+            *reinterpret_cast<uint4*>(img + (qc / 8) * (kRowTile * 128) + panel_offset(rr, qc % 8)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            if (qc == 0)
+              row_scale[rr] = out_of_table ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+          }
+          __syncwarp();
+        }
+        fence_async_smem();
+        mbar_arrive(qready);
+      }
+      // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
+      // of any size cancel without a residue
+      float R = -INFINITY, h = 0.f, l = 0.f, c = 0.f;
+      if (!mine) {                                             // no rows: only keeps step
+        if (!x.ok || failed) continue;
+        for (int t = 0; t <= w.T && !failed; ++t)
+          failed = !mbar_wait_bounded(step(n0 + g + t), ((n0 + g + t) >> 3) & 1, kWaitNs);
+        failed = group_any(i, failed);
+        g += w.T;
+        ++n0;
+        continue;
+      }
+      if (x.ok && !failed) {
+        c = row_scale[r];
+        if (c < 1.2e-38f) c = 1.2e-38f;                        // (above 0, so that -inf stays -inf)
+        const int own = x.ctx + min(row / a.G, x.n - 1);       // the row's own slot
+        const int own0 = x.ctx + r0 / a.G, own1 = x.ctx + min((r0 + kRowTile - 1) / a.G, x.j1);   // of the tile's rows
+        const int win = a.c.window > 0 ? a.c.window : 1 << 30, sinks = a.c.window > 0 ? a.c.n_sink : 0;
+        int2 ee32 = make_int2(0, 0);                           // (IMG) a lane's exponents of 32 tiles
+        for (int t = 0; t < w.T; ++t, ++g) {
+          const int n = n0 + g;
+          bool good;
+          if (i == 0 && two) {
+            good = mbar_wait_bounded(sready(s0), (s0 >> 1) & 1, kWaitNs);
+            ++s0;
+          } else {
+            good = mbar_wait_bounded(step(n), (n >> 3) & 1, kWaitNs);
+          }
+          if (__any_sync(RQ_FULL_MASK, !good)) {               // (the warp leaves as one)
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          int2 ee;
+          if constexpr (IMG) {
+            if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
+            ee = make_int2(__shfl_sync(RQ_FULL_MASK, ee32.x, t & 31), __shfl_sync(RQ_FULL_MASK, ee32.y, t & 31));
+          } else {
+            ee = exps[g & 7];
+          }
+          const float ke = q8_pow2(max(min(ee.x, 127), -126)), ev = float(ee.y);
+          uint32_t s[kKeys];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
+          tc_wait_ld();
+          // ---- what the row does not see
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int v = 2 * x.step(w.kt0 + t) + half;
+            const int at = v < x.tiles ? x.tile(v) * kQ8Tile : 1 << 30;        // (not there: behind every row)
+            if (at + 63 <= own0 && (at > own1 - win || at + 63 < sinks)) continue;
+            const int hi = own - at + 1, lo = own - win - at + 1, sk = min(sinks - at, hi);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t seen = range_bits(lo - 32 * q, hi - 32 * q) | range_bits(0, sk - 32 * q);
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (!(seen >> y & 1u)) s[half * 64 + 32 * q + y] = 0xff800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = __uint_as_float(s[y]);
+#pragma unroll
+          for (int y = 4; y + 4 < kKeys; y += 8)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
+#pragma unroll
+          for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ke;
+          const bool over = R == -INFINITY ? top > R : fmaf(top - R, c, ev - h) > kWeightTop;
+          if (__any_sync(RQ_FULL_MASK, over)) {
+            float f = 1.f;
+            if (over) {
+              const float hn = ev - kWeightHead;
+              f = R == -INFINITY ? 0.f : ex2(fmaf(R - top, c, h - hn));
+              R = top;
+              h = hn;
+            }
+            l *= f;
+            if (t > 0) {
+#pragma unroll 1
+              for (int y = 0; y < D / 16; ++y) {
+                uint32_t o[16];
+                tc_ld16(tO + 16 * y, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                tc_st16(tO + 16 * y, o);
+              }
+            }
+          }
+          const float r0x = R == -INFINITY ? 0.f : -R, hx = ev - h;
+          const uint64_t k2 = pack2(ke, ke), r2 = pack2(r0x, r0x), c2 = pack2(c, c), h2 = pack2(hx, hx);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t p[32];
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {
+              const int k = half * 64 + 2 * y;
+              float p0, p1;
+              unpack2(fma2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), k2, r2), c2, h2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+              p[y] = pack_half2(p0, p1);
+            }
+            tc_st32(tS + 32 * half, p);
+          }
+          float a0, a1;
+          unpack2(add2(sum[0], sum[1]), a0, a1);
+          l = fmaf(a0 + a1, q8_pow2(-max(min(ee.y, 126), -126)), l);
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(pready(i));
+        }
+        if (!failed) {
+          const int last_step = n0 + g;
+          failed = !mbar_wait_bounded(step(last_step), (last_step >> 3) & 1, kWaitNs);
+        }
+        ++n0;
+        failed = group_any(i, failed);                         // (the warps leave together: they share barriers)
+        tc_fence_after();
+      }
+      // ---- results (a wait that gave up: NaN)
+      const float nan = __int_as_float(0x7fc00000);
+      const bool there = x.ok && !failed;                      // O holds the segment's sums
+      bool whole = w.kt0 == 0 && w.T == x.V;
+      int from_cta = 0, to_cta = 0;
+      if (!whole) {
+        const int64_t at = 2 * int64_t(me) + (w.kt0 == 0 ? 1 : 0);
+        float* const part = a.part + (at * kBlockRows + i * kRowTile) * D;      // [D / 4][128 rows][4]
+        stats[at * kBlockRows + i * kRowTile + r] = make_float4(R * c, h, there ? l : nan, 0.f);
+#pragma unroll 1
+        for (int y = 0; y < D / 32; ++y) {
+          uint32_t o[32];
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] = 0u;
+          if (there) {
+            tc_ld32(tO + 32 * y, o);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            *reinterpret_cast<uint4*>(part + ((8 * y + z) * kRowTile + r) * 4) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        }
+        w.sharers(from_cta, to_cta);
+        __threadfence();
+        group_sync(i);
+        if (r == 0) last_one[i] = atomicAdd(a.tickets + 2 * from_cta + i, 1u) == unsigned(to_cta - from_cta);
+        group_sync(i);
+        if (last_one[i] == 0) {
+          tc_fence_before();
+          continue;
+        }
+        __threadfence();
+        // a part's weights are in units of 2^(st.x + st.y); nothing seen: st.x is -inf, st.z 0
+        float M = -INFINITY, H = 0.f;
+        for (int k = from_cta; k <= to_cta; ++k) {
+          const float4 st = __ldcg(&stats[(2 * int64_t(k) + (k == from_cta)) * kBlockRows + i * kRowTile + r]);
+          if (M == -INFINITY || (st.x - M) + (st.y - H) > 0.f) {
+            M = st.x;
+            H = st.y;
+          }
+        }
+        l = 0.f;
+        for (int k = from_cta; k <= to_cta; ++k) {
+          const float4 st = __ldcg(&stats[(2 * int64_t(k) + (k == from_cta)) * kBlockRows + i * kRowTile + r]);
+          l += st.z * (st.x == -INFINITY ? 0.f : ex2((st.x - M) + (st.y - H)));
+        }
+        R = M;
+        h = H;
+      }
+      constexpr int CR = D / 8;                                // 16-byte chunks of a row of bf16
+      const float inv = there ? (l == 0.f ? 0.f : 1.f / l) : nan;
+#pragma unroll 1
+      for (int y = 0; y < D / 32; ++y) {
+        float o[32];
+        if (whole) {
+          uint32_t u[32];
+#pragma unroll
+          for (int z = 0; z < 32; ++z) u[z] = 0u;
+          if (there) {
+            tc_ld32(tO + 32 * y, u);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] = __uint_as_float(u[z]);
+        } else {
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] = 0.f;
+          for (int k = from_cta; k <= to_cta; ++k) {
+            const int64_t at = 2 * int64_t(k) + (k == from_cta);
+            const float4 st = __ldcg(&stats[at * kBlockRows + i * kRowTile + r]);
+            const float f = st.x == -INFINITY ? 0.f : ex2((st.x - R) + (st.y - h));
+            const float* const part = a.part + (at * kBlockRows + i * kRowTile) * D;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(part + ((8 * y + z) * kRowTile + r) * 4));
+              o[4 * z] = fmaf(f, u.x, o[4 * z]);
+              o[4 * z + 1] = fmaf(f, u.y, o[4 * z + 1]);
+              o[4 * z + 2] = fmaf(f, u.z, o[4 * z + 2]);
+              o[4 * z + 3] = fmaf(f, u.w, o[4 * z + 3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 u = __floats2bfloat162_rn(o[8 * z + 2 * k] * inv, o[8 * z + 2 * k + 1] * inv);
+            p[k] = *reinterpret_cast<const uint32_t*>(&u);
+          }
+          *reinterpret_cast<uint4*>(img + r * (D * 2) + (((4 * y + z) ^ (r & (CR - 1))) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      __syncwarp();
+      const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
+#pragma unroll 4
+      for (int k = lane; k < 32 * CR; k += 32) {               // this warp's rows, 16 bytes a lane
+        const int rr = (warp & 3) * 32 + k / CR, cc = k % CR;
+        if (i * kRowTile + rr >= x.rows) continue;
+        const uint4 u = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
+        const int j = (r0 + rr) / a.G, hq = w.h * a.G + (r0 + rr) % a.G;
+        uint16_t* const o = a.c.out + ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D + 8 * cc;
+        if (vec) {
+          *reinterpret_cast<uint4*>(o) = u;
+        } else {
+          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            o[2 * z] = uint16_t(q[z]);
+            o[2 * z + 1] = uint16_t(q[z] >> 16);
+          }
+        }
+      }
+      __syncwarp();                                            // (the next queries overwrite the rows)
+      tc_fence_before();
+    }
+  }
+  if (__syncthreads_or(failed) && threadIdx.x == 0) atomicOr(a.err, 1u);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tc_free(tmem, 512);
+}
+
+// Bytes of the operand tiles of one sequence, and of one unit's list.
+template <typename Shape>
+int rows_list(const Shape& s, int n_new, int max_ctx, int window, int n_sink) {
+  int64_t slots = std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity), tiles = (slots + 63) / 64;
+  if (window > 0)      // sinks, the window and the new tokens, each from an edge of its own
+    tiles = std::min<int64_t>(tiles, (int64_t(n_sink) + 63) / 64 + (int64_t(window) + n_new + 63) / 64 + 1);
+  return int((tiles + 1) / 2);
+}
+
+struct RowsPlan {
+  Q8Layout line;
+  bool images;
+  int list, group;       // sequences handled together
+  size_t total;
+};
+
+constexpr size_t kGroupBytes = size_t(2) << 30;   // operand tiles of the sequences handled together
+// Blocks of rows from which the operand tiles are made once in the workspace.
+constexpr int kImageBlocks = 3;
+
+RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
+  RowsPlan p = {};
+  p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), 2);
+  p.total = p.line.total;
+  const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
+  p.images = rows > (kImageBlocks - 1) * kBlockRows;
+  p.group = s.batch;
+  if (!p.images) return p;
+  p.list = rows_list(s, n_new, max_ctx, window, n_sink);
+  const size_t per = size_t(s.n_kv_heads) * p.list * (s.head_dim == 128 ? RowsSmem<128>::kImage : RowsSmem<64>::kImage);
+  p.group = int(std::max<size_t>(1, std::min<size_t>(s.batch, kGroupBytes / per)));
+  p.total += std::min(per * size_t(s.batch), std::max(per, kGroupBytes));
+  return p;
+}
+
+template <int D, int FMT, bool IMG>
+cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
+  using L = RowsSmem<D>;
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+  });
+  if (e != cudaSuccess) return e;
+  q8_schedule_kernel<kBlockRows, kKeys><<<1, 1024, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * a.list), 256, 0, stream, a)) != cudaSuccess)
+    return e;
+  return launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a);
+}
+
+template <int D, int FMT>
+cudaError_t launch_either(const RowsArgs& a, bool images, cudaStream_t stream) {
+  return images ? launch<D, FMT, true>(a, stream) : launch<D, FMT, false>(a, stream);
+}
+
+}  // namespace
+
+size_t q8_rows_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
+  return rows_plan(s, n_new, max_ctx, window, n_sink).total;
+}
+
+cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                           const Q8Call& c, void* ws, cudaStream_t stream) {
+  const RowsPlan p = rows_plan(s, c.n_new, c.max_ctx, c.window, c.n_sink);
+  RowsArgs a = {};
+  static_cast<Q8Line&>(a) = q8_line(s, cache, paging, c, kBlockRows);
+  q8_place(a, p.line, ws, 2);
+  a.images = static_cast<uint8_t*>(ws) + p.line.total;
+  a.list = p.list;
+  for (int b0 = 0; b0 < s.batch; b0 += p.group) {            // (a group's kernels use the workspace after the one before)
+    RowsArgs g = a;
+    g.B = std::min(p.group, s.batch - b0);
+    g.clear = b0 == 0;
+    g.c.q += b0 * c.q_strides[0];
+    g.c.out += int64_t(b0) * c.n_new * s.n_q_heads * s.head_dim;
+    g.c.ctx_lens += b0;
+    if (c.n_lens) g.c.n_lens += b0;
+    if (c.rope.positions) g.c.rope.positions += int64_t(b0) * c.n_new;
+    if (paging) {
+      g.v.bt += int64_t(b0) * g.v.max_pages;
+    } else {
+      const int64_t records = int64_t(b0) * g.v.H * g.v.tiles;
+      g.v.codes += records * g.v.rec_codes;
+      g.v.scales += records * g.v.rec_scales;
+    }
+    cudaError_t e;
+    if (s.head_dim == 128)
+      e = s.format == RQ_Q8_INT8 ? launch_either<128, RQ_Q8_INT8>(g, p.images, stream) : launch_either<128, RQ_Q8_E4M3>(g, p.images, stream);
+    else
+      e = s.format == RQ_Q8_INT8 ? launch_either<64, RQ_Q8_INT8>(g, p.images, stream) : launch_either<64, RQ_Q8_E4M3>(g, p.images, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// -------------------------------------------------------------------------------- both kernels
+
+namespace {
+
+// Rows of a kv-head from which the tensor-core kernel is taken.
+constexpr int64_t kManyRows = 33;
+
+int64_t rows_of_call(const rq_q8_shape& s, int n_new) { return int64_t(n_new) * (s.n_q_heads / s.n_kv_heads); }
+
+}  // namespace
+
+// What a call takes, and never less than any call with fewer new tokens or a shorter context: few rows
+// may need more, as more CTAs share them.
+size_t q8_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
+  size_t most = 0;
+  const int heads = s.n_q_heads / s.n_kv_heads;
+  for (int rows : {8, 16, 32}) {
+    const int n = std::min(n_new, std::max(1, rows / heads));
+    if (rows_of_call(s, n) < kManyRows) most = std::max(most, q8_stream_workspace_bytes(s, n, max_ctx));
+  }
+  if (rows_of_call(s, n_new) >= kManyRows) most = std::max(most, q8_rows_workspace_bytes(s, n_new, max_ctx, window, n_sink));
+  return most;
+}
+
+cudaError_t launch_q8_attention(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                                const Q8Call& c, void* ws, cudaStream_t stream) {
+  return rows_of_call(s, c.n_new) >= kManyRows ? launch_q8_rows(s, cache, paging, c, ws, stream)
+                                               : launch_q8_stream(s, cache, paging, c, ws, stream);
+}
+
+}  // namespace rq

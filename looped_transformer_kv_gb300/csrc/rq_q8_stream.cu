@@ -8,15 +8,9 @@
 // merged once per segment.  m is raised when a score exceeds it by more than 8, E when a V scale
 // exceeds 2^(E + 7): weights stay below 2^15.
 //
-// The work is one line: for each sequence, for each block of rows and kv-head, its tiles.  It is cut
-// evenly for the CTAs that fit the GPU at once; a unit that a cut divides leaves partial results, and
-// the last of its CTAs to finish joins them in order.
-#include <algorithm>
-#include <cmath>
-
-#include "rq_kernels.h"
-#include "rq_launch.cuh"
-#include "rq_q8.cuh"
+// CTAs share the work by the line of rq_q8_line.cuh; the last CTA of a divided unit to finish joins
+// its partial results in order.
+#include "rq_q8_line.cuh"
 #include "rq_tc.cuh"
 
 namespace rq {
@@ -27,155 +21,6 @@ constexpr float kTop = 8.f;
 constexpr int kScaleTop = 7, kScaleHead = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
-
-struct Cut {
-  int64_t pos, base;    // where a CTA's stretch begins; where sequence b's units begin
-  int32_t b, pad;
-};
-
-struct StreamArgs {
-  Q8View v;
-  Q8Call c;
-  int32_t B, Hq, G, cap, qvec;
-  int32_t blocks;        // blocks of 8 NT rows, of n_new tokens
-  float scale_log2;
-  unsigned* err;         // workspace: error word, ...
-  int32_t* used;         // CTAs with work
-  unsigned* tickets;     // [CTA] of the unit that is cut at its end
-  int64_t* prefix;       // [B + 1] places of the sequences
-  Cut* cut;              // [CTA + 1]
-  float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l)
-  float* part;           // ... [rows][D]
-  int32_t n_ctas;
-};
-
-// What a block of rows sees: tiles 0 .. sink and from `first` on, V in all.
-struct Rows {
-  int ctx, n, j0, j1;    // tokens of the block's rows
-  int rows;              // of the block
-  int sink, first, V, hi;
-  bool ok;
-};
-
-template <int NT>
-__device__ __forceinline__ Rows rows_of(const StreamArgs& a, int b, int block) {
-  Rows x;
-  x.ctx = a.c.ctx_lens[b];
-  x.n = a.c.n_lens ? a.c.n_lens[b] : a.c.n_new;
-  x.ok = x.ctx >= 0 && x.ctx <= a.c.max_ctx && x.n >= 0 && x.n <= a.c.n_new && x.ctx <= a.cap - x.n;
-  if (x.n < 0 || x.n > a.c.n_new) x.n = a.c.n_new;
-  const int r0 = block * 8 * NT;
-  x.rows = min(8 * NT, x.n * a.G - r0);
-  x.sink = x.first = x.hi = 0;
-  x.V = 0;
-  if (x.rows <= 0) return x;
-  x.j0 = r0 / a.G;
-  x.j1 = (r0 + x.rows - 1) / a.G;
-  x.V = 1;                                                  // (bad lengths: one tile, not read)
-  if (!x.ok) return x;
-  const int lo = a.c.window > 0 ? max(0, x.ctx + x.j0 + 1 - a.c.window) : 0;
-  x.hi = x.ctx + x.j1 + 1;
-  x.first = lo / kQ8Tile;
-  x.sink = min((min(a.c.n_sink, lo) + kQ8Tile - 1) / kQ8Tile, x.first);
-  x.V = x.sink + (x.hi + kQ8Tile - 1) / kQ8Tile - x.first;
-  return x;
-}
-
-// One CTA: clears the error word and tickets, cuts the line.
-template <int NT>
-__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ StreamArgs a) {
-  grid_next();
-  __shared__ int64_t warp_sum[32];
-  __shared__ int64_t total;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) *a.err = 0u;
-  for (int i = tid; i < a.n_ctas; i += 1024) a.tickets[i] = 0u;
-  int64_t run = 0;
-  bool bad = false;
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
-    int64_t units = 0;
-    if (b0 + tid < a.B) {
-      for (int k = 0; k < a.blocks; ++k) {
-        const Rows x = rows_of<NT>(a, b0 + tid, k);
-        bad |= !x.ok;
-        if (x.V == 0) break;
-        units += x.V;
-      }
-      units *= a.v.H;
-    }
-    int64_t sum = units;                                    // inclusive scan over the block
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(RQ_FULL_MASK, sum, o);
-      if (lane >= o) sum += y;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    int64_t before = run;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warp_sum[w];
-      run += warp_sum[w];
-    }
-    if (b0 + tid < a.B) a.prefix[b0 + tid] = before + sum - units;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.prefix[a.B] = run;
-    total = run;
-  }
-  bad = __syncthreads_or(bad);                              // (and the prefix is written)
-  if (bad && tid == 0) *a.err = 1u;
-  const int64_t N = total;
-  const int used = int(min(N, int64_t(a.n_ctas)));
-  if (tid == 0) *a.used = used;
-  for (int i = tid; i <= used; i += 1024) {
-    const int64_t pos = used ? N * i / used : 0;
-    int lo = 0, hi = a.B;                                   // the last sequence that begins at or before pos
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.prefix[mid] <= pos) lo = mid; else hi = mid;
-    }
-    a.cut[i] = {pos, a.prefix[lo], lo, 0};
-  }
-}
-
-// A CTA's segments in order.
-template <int NT>
-struct Walk {
-  const StreamArgs& a;
-  int64_t pos, end, base;   // base: where the units of (b, block) begin
-  int b, block;
-  Rows x;
-  int h, kt0, T;
-  int64_t unit;             // the unit's place on the line
-  bool loaded;
-  __device__ __forceinline__ Walk(const StreamArgs& args, const Cut& from, int64_t to)
-      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(0), loaded(false) {}
-  __device__ __forceinline__ bool next() {
-    if (pos >= end) return false;
-    for (;;) {
-      if (!loaded) {
-        x = rows_of<NT>(a, b, block);
-        loaded = true;
-      }
-      const int64_t stop = base + int64_t(x.V) * a.v.H;
-      if (pos < stop) break;
-      base = stop;
-      loaded = false;
-      if (x.V == 0 || ++block == a.blocks) {
-        block = 0;
-        if (++b == a.B) return false;                       // (not with a sound schedule)
-      }
-    }
-    h = int((pos - base) / x.V);
-    unit = base + int64_t(h) * x.V;
-    kt0 = int(pos - unit);
-    T = int(min(int64_t(x.V - kt0), end - pos));
-    pos += T;
-    return true;
-  }
-  __device__ __forceinline__ int tile(int v) const { return v < x.sink ? v : x.first + v - x.sink; }
-};
 
 template <int D, int NT>
 struct StreamSmem {
@@ -203,7 +48,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ StreamArgs a) {
+__global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
   using L = StreamSmem<D, NT>;
   constexpr int KS = D / 16;                                // k-steps of a score, 16-channel tiles of O
   grid_wait();
@@ -227,7 +72,7 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
   }
   __syncthreads();
   const Cut from = a.cut[me];
-  Walk<NT> w(a, from, a.cut[me + 1].pos);
+  Walk<8 * NT, kQ8Tile> w(a, from, a.cut[me + 1].pos);
 
   if (warp == 4) {                                          // ---- copies
     int g = 0;
@@ -236,7 +81,7 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
       if (!w.x.ok) continue;
       for (int t0 = 0; t0 < w.T && good; t0 += 32) {
         int64_t rec = -1;
-        if (t0 + lane < w.T) rec = a.v.record(w.b, w.h, w.tile(w.kt0 + t0 + lane));
+        if (t0 + lane < w.T) rec = a.v.record(w.b, w.h, w.x.tile(w.x.step(w.kt0 + t0 + lane)));
         const int m = min(32, w.T - t0);
         for (int t = 0; t < m && good; ++t, ++g) {
           const int64_t r = __shfl_sync(RQ_FULL_MASK, rec, t);
@@ -347,7 +192,7 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
         if (!dead) dead = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(full(s), (g / L::kStages) & 1, kWaitNs));
         if (dead) continue;                                 // (the copies' warp gives up in its turn)
         const uint8_t* const stage = smem + s * L::kStage;
-        const int slot0 = w.tile(w.kt0 + t) * kQ8Tile + 16 * warp;
+        const int slot0 = x.tile(x.step(w.kt0 + t)) * kQ8Tile + 16 * warp;
         const int oldest = a.c.window > 0 ? x.ctx + x.j0 + 1 - a.c.window : 0;   // the first row's window
         if (slot0 < x.hi && (slot0 + 15 >= oldest || slot0 < a.c.n_sink)) {
           const float* const scales = reinterpret_cast<const float*>(stage + L::kCodes);
@@ -564,11 +409,8 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
         }
       }
       if (!whole) {
-        // the CTAs that share the unit: cut i lies at N i / used
-        const int64_t N = a.prefix[a.B];
-        const int used = *a.used;
-        const int first = int(((w.unit + 1) * used + N - 1) / N) - 1;
-        const int last = int(((w.unit + x.V) * used + N - 1) / N) - 1;
+        int first, last;                                    // the CTAs that share the unit
+        w.sharers(first, last);
         __threadfence();
         consumers_sync();
         if (threadIdx.x == 0) misc[1] = atomicAdd(a.tickets + first, 1u) == unsigned(last - first);
@@ -610,87 +452,42 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
 
 // ------------------------------------------------------------------------------------- host
 
-struct StreamLayout {
-  int n_ctas, rows;
-  size_t tickets, prefix, cut, stats, part, total;
-};
+int tiles_of_rows(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
-int tiles_of_rows(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-
-StreamLayout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx) {
-  StreamLayout x;
-  const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
-  const int nt = tiles_of_rows(rows > 32 ? 32 : int(rows));
-  x.rows = 8 * nt;
-  const int64_t tiles = (std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity) + kQ8Tile - 1) / kQ8Tile + 1;
-  const int64_t most = int64_t(s.batch) * s.n_kv_heads * ((rows + x.rows - 1) / x.rows) * tiles;
-  const int fit = std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas);
-  x.n_ctas = int(std::min<int64_t>(most, fit));
-  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  x.tickets = kWsHeaderBytes;
-  x.prefix = x.tickets + up(size_t(x.n_ctas) * 4);
-  x.cut = x.prefix + up((size_t(s.batch) + 1) * 8);
-  x.stats = x.cut + up((size_t(x.n_ctas) + 1) * sizeof(Cut));
-  x.part = x.stats + up(size_t(x.n_ctas) * 2 * x.rows * 8);
-  x.total = x.part + up(size_t(x.n_ctas) * 2 * x.rows * s.head_dim * 4);
-  return x;
+Q8Layout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx, int nt) {
+  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), 1);
 }
 
 template <int D, int NT, int FMT>
-cudaError_t launch(const StreamArgs& a, cudaStream_t stream) {
+cudaError_t launch(const Q8Line& a, cudaStream_t stream) {
   using L = StreamSmem<D, NT>;
   static OncePerDevice once;
   cudaError_t e = once([] {
     return cudaFuncSetAttribute(q8_stream_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  q8_schedule_kernel<NT><<<1, 1024, 0, stream>>>(a);
+  q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), 160, L::total, stream, a);
 }
 
 }  // namespace
 
-size_t q8_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx) {
-  size_t most = 0;     // (a call with fewer rows may have more CTAs, each with less to leave)
-  const int heads = s.n_q_heads / s.n_kv_heads;
-  for (int rows : {8, 16, 32}) {
-    const int n = std::min(n_new, std::max(1, rows / heads));
-    most = std::max(most, stream_layout(s, n, max_ctx).total);
-  }
-  return std::max(most, stream_layout(s, n_new, max_ctx).total);
+size_t q8_stream_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx) {
+  return stream_layout(s, n_new, max_ctx, tiles_of_rows(int64_t(n_new) * (s.n_q_heads / s.n_kv_heads))).total;
 }
 
-cudaError_t launch_q8_attention(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
-                                const Q8Call& c, void* ws, cudaStream_t stream) {
-  const StreamLayout x = stream_layout(s, c.n_new, c.max_ctx);
-  char* const base = static_cast<char*>(ws);
-  StreamArgs a = {};
-  a.v = q8_view(s, cache, paging, c.loop);
-  a.c = c;
-  a.B = s.batch;
-  a.Hq = s.n_q_heads;
-  a.G = s.n_q_heads / s.n_kv_heads;
-  a.cap = s.capacity;
-  bool vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0;
-  for (int i = 0; i < 3; ++i) vec = vec && c.q_strides[i] % 8 == 0;
-  a.qvec = vec;
-  a.blocks = int((int64_t(c.n_new) * a.G + x.rows - 1) / x.rows);
-  a.scale_log2 = (s.softmax_scale > 0.f ? s.softmax_scale : 1.0f / sqrtf(float(s.head_dim))) * kLog2e;
-  a.err = reinterpret_cast<unsigned*>(base);
-  a.used = reinterpret_cast<int32_t*>(base + 4);
-  a.tickets = reinterpret_cast<unsigned*>(base + x.tickets);
-  a.prefix = reinterpret_cast<int64_t*>(base + x.prefix);
-  a.cut = reinterpret_cast<Cut*>(base + x.cut);
-  a.stats = reinterpret_cast<float2*>(base + x.stats);
-  a.part = reinterpret_cast<float*>(base + x.part);
-  a.n_ctas = x.n_ctas;
+cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
+                             const Q8Call& c, void* ws, cudaStream_t stream) {
+  const int nt = tiles_of_rows(int64_t(c.n_new) * (s.n_q_heads / s.n_kv_heads));
+  Q8Line a = q8_line(s, cache, paging, c, 8 * nt);
+  q8_place(a, stream_layout(s, c.n_new, c.max_ctx, nt), ws, 1);
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
-  switch (x.rows) {
-    case 8:
+  switch (nt) {
+    case 1:
       return wide ? (i8 ? launch<128, 1, RQ_Q8_INT8>(a, stream) : launch<128, 1, RQ_Q8_E4M3>(a, stream))
                   : (i8 ? launch<64, 1, RQ_Q8_INT8>(a, stream) : launch<64, 1, RQ_Q8_E4M3>(a, stream));
-    case 16:
+    case 2:
       return wide ? (i8 ? launch<128, 2, RQ_Q8_INT8>(a, stream) : launch<128, 2, RQ_Q8_E4M3>(a, stream))
                   : (i8 ? launch<64, 2, RQ_Q8_INT8>(a, stream) : launch<64, 2, RQ_Q8_E4M3>(a, stream));
     default:

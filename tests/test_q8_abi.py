@@ -133,7 +133,10 @@ def test_a_workspace_serves_every_smaller_call(lib):
         assert by_n == sorted(by_n) and by_n[0] > 0
         by_ctx = [size(ctypes.byref(s), 3, c, 0, 0) for c in (0, 1, 64, 65, 1000, 8192, 1 << 15)]
         assert by_ctx == sorted(by_ctx)
-        assert size(ctypes.byref(s), 3, 1000, 77, 5) == size(ctypes.byref(s), 3, 1000, 0, 0)
+        by_n = [size(ctypes.byref(s), n, 20000, 300, 9) for n in (1, 16, 17, 33, 64, 65, 200, 257, 1025, 4096)]
+        assert by_n == sorted(by_n)
+        by_ctx = [size(ctypes.byref(s), 2000, c, w, 64) for w in (0, 500) for c in (0, 1, 64, 65, 1000, 8192, 1 << 15)]
+        assert by_ctx[:7] == sorted(by_ctx[:7]) and by_ctx[7:] == sorted(by_ctx[7:])
 
 
 def test_reference_codes_are_the_nearest():
