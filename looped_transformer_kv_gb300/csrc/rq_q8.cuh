@@ -42,33 +42,51 @@ __host__ __device__ __forceinline__ constexpr int q8_swizzle(int t) {
 }
 
 // 8 channels of a bf16 row.
-__device__ __forceinline__ void q8_load8(const uint16_t* p, bool vec, float (&f)[8]) {
-  if (vec) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ uint4 q8_load8(const uint16_t* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  } else {
+  for (int k = 0; k < 4; ++k) w[k] = uint32_t(p[2 * k]) | (uint32_t(p[2 * k + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void q8_floats(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = bf16_bits_to_float(p[k]);
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
   }
 }
 
-// Rotates a row held by D / 8 neighbouring lanes, 8 channels each.  Every lane of the warp calls it;
-// `pos` (the same in a row's lanes) below 0: the row is left alone.
+// The angles of a lane's 8 channels at a position, of a row held by D / 8 neighbouring lanes; below 0
+// (the same in a row's lanes): none.
+struct Q8Angles {
+  float4 a[4];           // (interleaved: two)
+  bool turned;
+};
 template <int D>
-__device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, int pos, int lane) {
-  const int c = lane % (D / 8);
-  const bool turned = pos >= 0 && 8 * c < rope.rot;
-  const float* const row = rope.table + int64_t(pos < 0 ? 0 : pos) * rope.rot;
+__device__ __forceinline__ Q8Angles q8_angles(const Q8Rope& rope, int pos, int lane) {
+  Q8Angles r;
+  const int c = lane % (D / 8), half = rope.rot / 16;      // half: lanes of the first channels of the pairs
+  r.turned = pos >= 0 && 8 * c < rope.rot;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.a[k] = make_float4(1.f, 0.f, 1.f, 0.f);
+  if (!r.turned) return r;
+  const float* const row = rope.table + int64_t(pos) * rope.rot + (rope.interleaved ? 8 * c : 16 * (c >= half ? c - half : c));
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < 2 || !rope.interleaved) r.a[k] = *reinterpret_cast<const float4*>(row + 4 * k);
+  return r;
+}
+
+// Rotates the row.  Every lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, const Q8Angles& r, int lane) {
   if (rope.interleaved) {
-    if (turned) {
+    if (r.turned) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 a = *reinterpret_cast<const float4*>(row + 8 * c + 4 * k);
+        const float4 a = r.a[k];
         const float x0 = f[4 * k], y0 = f[4 * k + 1], x1 = f[4 * k + 2], y1 = f[4 * k + 3];
         f[4 * k] = __fsub_rn(__fmul_rn(x0, a.x), __fmul_rn(y0, a.y));
         f[4 * k + 1] = __fadd_rn(__fmul_rn(y0, a.x), __fmul_rn(x0, a.y));
@@ -78,15 +96,15 @@ __device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, int
     }
     return;
   }
-  const int half = rope.rot / 16;                          // lanes of the first channels of the pairs
+  const int c = lane % (D / 8), half = rope.rot / 16;
   const bool second = c >= half;
   const int partner = lane - c + (8 * c < rope.rot ? (second ? c - half : c + half) : c);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float o0 = __shfl_sync(RQ_FULL_MASK, f[2 * k], partner);
     const float o1 = __shfl_sync(RQ_FULL_MASK, f[2 * k + 1], partner);
-    if (turned) {
-      const float4 a = *reinterpret_cast<const float4*>(row + 16 * (second ? c - half : c) + 4 * k);
+    if (r.turned) {
+      const float4 a = r.a[k];
       const float p0 = __fmul_rn(f[2 * k], a.x), p1 = __fmul_rn(f[2 * k + 1], a.z);
       const float r0 = __fmul_rn(o0, a.y), r1 = __fmul_rn(o1, a.w);
       f[2 * k] = second ? __fadd_rn(p0, r0) : __fsub_rn(p0, r0);

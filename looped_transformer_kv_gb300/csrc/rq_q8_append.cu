@@ -90,31 +90,40 @@ __global__ void __launch_bounds__(256) q8_append_kernel(const __grid_constant__ 
   const uint16_t* const src = a.kv + b * a.s0 + kv * a.s2 + l * a.s3 + h * a.s4 + 8 * c;
   float f[IT][8];
   uint32_t most = 0u;                                                // largest magnitude's fp32 bits
+  uint4 raw[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
     const int t = k0 + i * RPI + sub;
-    if (t >= t0 && t < t1) q8_load8(src + (t - ctx) * a.s1, a.vec, f[i]);
+    raw[i] = t >= t0 && t < t1 ? q8_load8(src + (t - ctx) * a.s1, a.vec) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int t = k0 + i * RPI + sub;
-    const bool live = t >= t0 && t < t1;
-    if (kv == 0 && a.rope.table != nullptr) {
-      int pos = -1;
-      if (live) {
-        pos = a.rope.positions ? a.rope.positions[int64_t(b) * a.n_new + t - ctx] : t;
-        if (pos < 0 || pos >= a.rope.n_pos) {
-          pos = -1;
-          most = 0x7fffffffu;                                        // as a row that is not finite
+  for (int i = 0; i < IT; ++i) q8_floats(raw[i], f[i]);
+  if (kv == 0 && a.rope.table != nullptr) {
+    constexpr int TOGETHER = 1;                                      // rows whose angles are loaded at once
+#pragma unroll
+    for (int i0 = 0; i0 < IT; i0 += TOGETHER) {
+      Q8Angles angles[TOGETHER];
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int t = k0 + (i0 + i) * RPI + sub;
+        int pos = -1;
+        if (t >= t0 && t < t1) {
+          pos = a.rope.positions ? a.rope.positions[int64_t(b) * a.n_new + t - ctx] : t;
+          if (pos < 0 || pos >= a.rope.n_pos) {
+            pos = -1;
+            most = 0x7fffffffu;                                      // as a row that is not finite
+          }
         }
+        angles[i] = q8_angles<D>(a.rope, pos, lane);
       }
-      q8_rotate<D>(f[i], a.rope, pos, lane);
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) q8_rotate<D>(f[i0 + i], a.rope, angles[i], lane);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(f[i][k]) & 0x7fffffffu);
-  }
   most = __reduce_max_sync(RQ_FULL_MASK, most);
 
   // the least exponent that holds them; bf16 bits: exponent field, 7 bits of the significand

@@ -13,8 +13,8 @@
 namespace rq {
 
 struct Cut {           // a CTA's stretch of the line
-  int64_t pos, base;    // where it begins; where sequence b's units begin
-  int32_t b, pad;
+  int64_t pos, base;    // where it begins; where the units of (sequence, block) begin
+  int32_t b, block;
 };
 
 struct Q8Line {
@@ -26,7 +26,7 @@ struct Q8Line {
   unsigned* err;         // workspace: error word, ...
   int32_t* used;         // CTAs with work
   unsigned* tickets;     // [CTA][n_tickets] of the unit that is cut at its end
-  int64_t* prefix;       // [B + 1] places of the sequences
+  int64_t* prefix;       // [B * blocks + 1] places of (sequence, block)
   Cut* cut;              // [CTA + 1]
   float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l); or four floats each
   float* part;           // ... their sums
@@ -89,22 +89,18 @@ template <int ROWS, int KEYS>
 __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ Q8Line a) {
   grid_next();
   __shared__ int64_t warp_sum[32];
-  __shared__ int64_t total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0 && a.clear) *a.err = 0u;
   for (int i = tid; i < a.n_ctas * a.n_tickets; i += 1024) a.tickets[i] = 0u;
+  const int64_t pairs = int64_t(a.B) * a.blocks;
   int64_t run = 0;
   bool bad = false;
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+  for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
     int64_t units = 0;
-    if (b0 + tid < a.B) {
-      for (int k = 0; k < a.blocks; ++k) {
-        const Rows x = rows_of<ROWS, KEYS>(a, b0 + tid, k);
-        bad |= !x.ok;
-        if (x.V == 0) break;
-        units += x.V;
-      }
-      units *= a.v.H;
+    if (p0 + tid < pairs) {
+      const Rows x = rows_of<ROWS, KEYS>(a, int((p0 + tid) / a.blocks), int((p0 + tid) % a.blocks));
+      bad |= !x.ok;
+      units = int64_t(x.V) * a.v.H;
     }
     int64_t sum = units;                                    // inclusive scan over the block
 #pragma unroll
@@ -115,30 +111,27 @@ __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant
     if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
     int64_t before = run;
+#pragma unroll
     for (int w = 0; w < 32; ++w) {
       if (w < warp) before += warp_sum[w];
       run += warp_sum[w];
     }
-    if (b0 + tid < a.B) a.prefix[b0 + tid] = before + sum - units;
+    if (p0 + tid < pairs) a.prefix[p0 + tid] = before + sum - units;
     __syncthreads();
   }
-  if (tid == 0) {
-    a.prefix[a.B] = run;
-    total = run;
-  }
+  if (tid == 0) a.prefix[pairs] = run;
   bad = __syncthreads_or(bad);                              // (and the prefix is written)
   if (bad && tid == 0) *a.err = 1u;
-  const int64_t N = total;
-  const int used = int(min(N, int64_t(a.n_ctas)));
+  const int used = int(min(run, int64_t(a.n_ctas)));
   if (tid == 0) *a.used = used;
   for (int i = tid; i <= used; i += 1024) {
-    const int64_t pos = used ? N * i / used : 0;
-    int lo = 0, hi = a.B;                                   // the last sequence that begins at or before pos
+    const int64_t pos = used ? run * i / used : 0;
+    int64_t lo = 0, hi = pairs;                             // the last pair that begins at or before pos
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
+      const int64_t mid = (lo + hi) / 2;
       if (a.prefix[mid] <= pos) lo = mid; else hi = mid;
     }
-    a.cut[i] = {pos, a.prefix[lo], lo, 0};
+    a.cut[i] = {pos, a.prefix[lo], int(lo / a.blocks), int(lo % a.blocks)};
   }
 }
 
@@ -153,7 +146,7 @@ struct Walk {
   int64_t unit;             // the unit's place on the line
   bool loaded;
   __device__ __forceinline__ Walk(const Q8Line& args, const Cut& from, int64_t to)
-      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(0), loaded(false) {}
+      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(from.block), loaded(false) {}
   __device__ __forceinline__ bool next() {
     if (pos >= end) return false;
     for (;;) {
@@ -179,7 +172,7 @@ struct Walk {
   }
   // The CTAs that share the unit (cut i lies at N i / used).
   __device__ __forceinline__ void sharers(int& first, int& last) const {
-    const int64_t N = a.prefix[a.B];
+    const int64_t N = a.prefix[int64_t(a.B) * a.blocks];
     const int used = *a.used;
     first = int(((unit + 1) * used + N - 1) / N) - 1;
     last = int(((unit + x.V) * used + N - 1) / N) - 1;
@@ -218,7 +211,7 @@ inline Q8Layout q8_layout(const rq_q8_shape& s, int n_new, int max_ctx, int rows
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   x.tickets = kWsHeaderBytes;
   x.prefix = x.tickets + up(size_t(x.n_ctas) * 4 * n_tickets);
-  x.cut = x.prefix + up((size_t(s.batch) + 1) * 8);
+  x.cut = x.prefix + up((size_t(s.batch) * size_t((all + rows - 1) / rows) + 1) * 8);
   x.stats = x.cut + up((size_t(x.n_ctas) + 1) * sizeof(Cut));
   x.part = x.stats + up(size_t(x.n_ctas) * 2 * rows * 16);
   x.total = x.part + up(size_t(x.n_ctas) * 2 * rows * s.head_dim * 4);

@@ -17,6 +17,8 @@
 // copies; else warps 12-15: codes from global memory (a tile ahead, in registers) to operands.
 // CTAs (one per SM) share the work by the line of rq_q8_line.cuh; the last CTA of a divided unit to
 // finish joins its partial results in order, each row tile for itself.
+#include <type_traits>
+
 #include "rq_q8_line.cuh"
 #include "rq_tc.cuh"
 
@@ -26,6 +28,7 @@ namespace {
 constexpr int kKeys = 128, kRowTile = 128, kBlockRows = 2 * kRowTile;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
+constexpr unsigned kQueryBlocks = 2;   // of q8_image_kernel, for a row tile
 using RowWalk = Walk<kBlockRows, kKeys>;
 
 template <int D>
@@ -34,7 +37,7 @@ struct RowsSmem {
   static constexpr int v = 0, k = 2 * kTile, q = 5 * kTile, exps = 7 * kTile;   // V first: see v_desc
   static constexpr int row_exps = exps + 64;                // [8] K's and V's exponent of a tile
   static constexpr int bars = row_exps + kBlockRows * 4;
-  static constexpr int kImage = 2 * kTile + 128;            // of a tile in the workspace
+  static constexpr int kImage = 2 * kTile + 128, kQueryImage = kTile + 4 * kRowTile;   // of tiles in the workspace
   static constexpr int total = bars + 256 + 1024;           // + alignment of the base
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
@@ -90,8 +93,62 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
 
 struct RowsArgs : Q8Line {
   uint8_t* images;       // operand tiles, [B][Hkv][list] of K, V, their exponents
-  int32_t list;          // of one unit, at most
+  uint8_t* queries;      // [B][Hkv][row_tiles] of rows, their factors
+  int32_t list, row_tiles;   // of one unit, at most
 };
+
+// Rows rr0 .. + ROWS of a tile of 128 query rows (row r0 of the sequence and on, `live` of them) to fp16
+// operands, each times a power of two that brings its largest element into [2^14, 2^15) (bf16 values are
+// exact then); factors: what a row's scores are multiplied by.  One warp.
+template <int D, int ROWS>
+__device__ __forceinline__ void put_queries(const Q8Line& a, const Rows& x, int b, int h, int r0, int rr0, int live,
+                                            uint8_t* tile, float* factors, int lane) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = ROWS / RPI, TOGETHER = 2;   // (rows whose loads are in flight)
+  const int qc = lane % LPR;
+#pragma unroll 1
+  for (int y0 = 0; y0 < IT; y0 += TOGETHER) {
+    uint4 raw[TOGETHER];
+    Q8Angles angles[TOGETHER];
+    bool lost[TOGETHER];
+#pragma unroll
+    for (int y = 0; y < TOGETHER; ++y) {
+      const int rr = rr0 + (y0 + y) * RPI + lane / LPR;
+      const int j = (r0 + rr) / a.G, hq = h * a.G + (r0 + rr) % a.G;
+      raw[y] = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < live) raw[y] = q8_load8(a.c.q + b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec);
+      lost[y] = false;
+      if (a.c.rope.table == nullptr) continue;
+      int p = -1;
+      if (rr < live) {
+        p = a.c.rope.positions ? a.c.rope.positions[int64_t(b) * a.c.n_new + j] : x.ctx + j;
+        lost[y] = p < 0 || p >= a.c.rope.n_pos;
+        if (lost[y]) p = -1;
+      }
+      angles[y] = q8_angles<D>(a.c.rope, p, lane);
+    }
+#pragma unroll
+    for (int y = 0; y < TOGETHER; ++y) {
+      const int rr = rr0 + (y0 + y) * RPI + lane / LPR;
+      float f[8];
+      q8_floats(raw[y], f);
+      if (a.c.rope.table != nullptr) q8_rotate<D>(f, a.c.rope, angles[y], lane);
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
+      const int ex = int(__float_as_uint(mx) >> 23);
+      const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
+      const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = pack_half2(f[2 * k] * up * up2, f[2 * k + 1] * up * up2);
+      *reinterpret_cast<uint4*>(tile + (qc / 8) * (kRowTile * 128) + panel_offset(rr, qc % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (qc == 0)
+        factors[rr] = lost[y] ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+    }
+  }
+}
 
 // One key tile of 128 slots from codes to operands by 128 threads, a thread the same 16 channels of
 // every 16th (d = 64: 32nd) row.
@@ -184,12 +241,30 @@ struct Converter {
   }
 };
 
-// Operand tiles of a whole call: 128 threads for K, 128 for V of one tile.
+// Operand tiles of a whole call: 128 threads for K, 128 for V of one key tile, or 8
+// rows of a query tile a warp.  Bound by HBM: 14,336 + 2,048 slots of 8 heads, 33 MB of codes to 67 MB of operands, in
+// 19 us.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(256, 4) q8_image_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
   grid_next();
-  const int kv = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  using L = RowsSmem<D>;
+  const int lane = threadIdx.x & 31;
+  const unsigned key_blocks = unsigned(a.B) * a.v.H * a.list;
+  if (blockIdx.x >= key_blocks) {                            // a part of a row tile
+    const unsigned block = blockIdx.x - key_blocks, tile = block / kQueryBlocks;
+    const int unit = int(tile / unsigned(a.row_tiles)), b = unit / a.v.H, h = unit % a.v.H;
+    const int t = int(tile % unsigned(a.row_tiles));
+    const Rows x = sequence_of(a, b);
+    const int live = x.ok ? x.n * a.G - t * kRowTile : 0;
+    if (live <= 0) return;
+    uint8_t* const image = a.queries + (int64_t(unit) * a.row_tiles + t) * L::kQueryImage;
+    constexpr int ROWS = kRowTile / kQueryBlocks / 8;
+    put_queries<D, ROWS>(a, x, b, h, t * kRowTile, (int(block % kQueryBlocks) * 8 + (threadIdx.x >> 5)) * ROWS, live, image,
+                         reinterpret_cast<float*>(image + L::kTile), lane);
+    return;
+  }
+  const int kv = threadIdx.x >> 7;
   const int u = int(blockIdx.x % unsigned(a.list));
   const int unit = int(blockIdx.x / unsigned(a.list)), b = unit / a.v.H, h = unit % a.v.H;
   const Rows x = sequence_of(a, b);
@@ -201,9 +276,9 @@ __global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ R
   to.load(reg, kv);
   to.load_scales();
   const int2 e = to.take_scales(x, 2 * u);
-  uint8_t* const image = a.images + (int64_t(unit) * a.list + u) * RowsSmem<D>::kImage;
-  to.put(reg, image + kv * RowsSmem<D>::kTile, kv);
-  if (threadIdx.x == 0) *reinterpret_cast<int2*>(image + 2 * RowsSmem<D>::kTile) = e;
+  uint8_t* const image = a.images + (int64_t(unit) * a.list + u) * L::kImage;
+  to.put(reg, image + kv * L::kTile, kv);
+  if (threadIdx.x == 0) *reinterpret_cast<int2*>(image + 2 * L::kTile) = e;
 }
 
 // Exponents of tile t of the walk's segment.
@@ -222,7 +297,8 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   using L = RowsSmem<D>;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  // barriers: K full [3], V full [2], step [8], S of row tile 0 [2], P ready [2], Q ready, drained.
+  // barriers: K full [3], V full [2], step [8], S of row tile 0 [2], P ready [row
+  // tile][half], Q ready, drained.
   // A step ends with the last row tile's scores of a tile (and the values of the tile before), or with
   // the values of a segment's last tile: T + 1 steps for T tiles.  It frees K and V tiles.
   const uint32_t bar0 = smem_u32(bars);
@@ -230,10 +306,10 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   auto vfull = [&](int g) { return bar0 + 8 * (3 + (g & 1)); };
   auto step = [&](int n) { return bar0 + 8 * (5 + (n & 7)); };
   auto sready = [&](int c) { return bar0 + 8 * (13 + (c & 1)); };
-  auto pready = [&](int i) { return bar0 + 8 * (15 + i); };
-  const uint32_t qready = bar0 + 8 * 17, drained = bar0 + 8 * 18;
-  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 19);
-  int* const last_one = reinterpret_cast<int*>(bars + 20);  // [row tile]
+  auto pready = [&](int i, int half) { return bar0 + 8 * (15 + 2 * i + half); };
+  const uint32_t qready = bar0 + 8 * 19, drained = bar0 + 8 * 20;
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 21);
+  int* const last_one = reinterpret_cast<int*>(bars + 22);  // [row tile]
   int2* const exps = reinterpret_cast<int2*>(smem + L::exps);        // [8] of tiles: K's, V's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -241,9 +317,8 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < 5; ++i) mbar_init(bar0 + 8 * i, IMG ? 1 : 128);
     for (int i = 5; i < 15; ++i) mbar_init(bar0 + 8 * i, 1);
-    mbar_init(pready(0), kRowTile);
-    mbar_init(pready(1), kRowTile);
-    mbar_init(qready, kBlockRows);
+    for (int i = 15; i < 19; ++i) mbar_init(bar0 + 8 * i, kRowTile);
+    mbar_init(qready, IMG ? 2 : kBlockRows);
     mbar_init(drained, 1);
     fence_mbar_init();
   }
@@ -353,11 +428,17 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
           tc_mma(tmem + 128 * i, panel_desc(q + (y / 4) * (kRowTile * 128) + (y % 4) * 32),
                  panel_desc(k + (y / 4) * (kKeys * 128) + (y % 4) * 32), ids, y > 0);
       };
-      auto values = [&](int i, int gv, bool add) {
+      auto values = [&](int i, int gv, int parity, bool add) {       // false: a wait gave up
         const uint32_t v = smem_u32(smem + L::v + (gv & 1) * L::kTile);
 #pragma unroll
-        for (int y = 0; y < kKeys / 16; ++y)
-          tc_mma_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * y, v_desc(v + y * 2048), ido, add || y > 0);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait_bounded(pready(i, half), parity, kWaitNs)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int y = 4 * half; y < 4 * half + 4; ++y)
+            tc_mma_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * y, v_desc(v + y * 2048), ido, add || y > 0);
+        }
+        return true;
       };
       while (good && w.next()) {
         if (!w.x.ok) continue;
@@ -377,17 +458,13 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
           const bool more = j + 1 < w.T;
           if (good && more) good = mbar_wait_bounded(kfull(g + 1), ((g + 1) / 3) & 1, kWaitNs);
           if (!good) break;
-          good = mbar_wait_bounded(pready(0), c0++ & 1, kWaitNs);
+          good = values(0, g, c0++ & 1, j > 0);
           if (!good) break;
-          tc_fence_after();
-          values(0, g, j > 0);
           if (more) scores(0, g + 1);
           if (two) {
             if (more) tc_commit(sready(s0++));
-            good = mbar_wait_bounded(pready(1), c1++ & 1, kWaitNs);
+            good = values(1, g, c1++ & 1, j > 0);
             if (!good) break;
-            tc_fence_after();
-            values(1, g, j > 0);
             if (more) scores(1, g + 1);
           }
           tc_commit(step(n++));
@@ -417,50 +494,25 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       const int r0 = w.block * kBlockRows + i * kRowTile;      // the row tile's first row
       const bool two = x.rows > kRowTile, mine = i == 0 || two;
       const int row = r0 + r;
-      // ---- queries to operands, 32 rows a warp
+      // ---- queries: operands, 32 rows a warp, or their copy
+      float factor = 0.f;
       if (x.ok && !failed) {
-        if (mine) {
-          constexpr int LPR = D / 8, RPI = 32 / LPR;
-          const int qc = lane % LPR;
-#pragma unroll 2
-          for (int y = 0; y < 32 / RPI; ++y) {
-            const int rr = (warp & 3) * 32 + y * RPI + lane / LPR;
-            const bool live = i * kRowTile + rr < x.rows;
-            const int j = (r0 + rr) / a.G, hq = w.h * a.G + (r0 + rr) % a.G;
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = 0.f;
-            if (live) q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec, f);
-            bool out_of_table = false;
-            if (a.c.rope.table != nullptr) {
-              int p = -1;
-              if (live) {
-                p = a.c.rope.positions ? a.c.rope.positions[int64_t(w.b) * a.c.n_new + j] : x.ctx + j;
-                out_of_table = p < 0 || p >= a.c.rope.n_pos;
-                if (out_of_table) p = -1;
-              }
-              q8_rotate<D>(f, a.c.rope, p, lane);
-            }
-            float mx = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
-            const int ex = int(__float_as_uint(mx) >> 23);
-            const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);   // largest in [2^14, 2^15)
-            const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = pack_half2(f[2 * k] * up * up2, f[2 * k + 1] * up * up2);
-            *reinterpret_cast<uint4*>(img + (qc / 8) * (kRowTile * 128) + panel_offset(rr, qc % 8)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            if (qc == 0)
-              row_scale[rr] = out_of_table ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+        if constexpr (IMG) {
+          const uint8_t* const image = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + r0 / kRowTile) * L::kQueryImage;
+          if (r == 0) {
+            mbar_arrive_expect_tx(qready, mine ? L::kTile : 0);
+            if (mine) bulk_g2s(smem_u32(img), image, L::kTile, qready);
           }
-          __syncwarp();
+          if (mine) factor = *reinterpret_cast<const float*>(image + L::kTile + 4 * r);
+        } else {
+          if (mine) {
+            put_queries<D, 32>(a, x, w.b, w.h, r0, (warp & 3) * 32, x.rows - i * kRowTile, img, row_scale, lane);
+            __syncwarp();
+            factor = row_scale[r];
+          }
+          fence_async_smem();
+          mbar_arrive(qready);
         }
-        fence_async_smem();
-        mbar_arrive(qready);
       }
       // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
       // of any size cancel without a residue
@@ -475,13 +527,28 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
         continue;
       }
       if (x.ok && !failed) {
-        c = row_scale[r];
+        c = factor;
         if (c < 1.2e-38f) c = 1.2e-38f;                        // (above 0, so that -inf stays -inf)
         const int own = x.ctx + min(row / a.G, x.n - 1);       // the row's own slot
         const int own0 = x.ctx + r0 / a.G, own1 = x.ctx + min((r0 + kRowTile - 1) / a.G, x.j1);   // of the tile's rows
         const int win = a.c.window > 0 ? a.c.window : 1 << 30, sinks = a.c.window > 0 ? a.c.n_sink : 0;
         int2 ee32 = make_int2(0, 0);                           // (IMG) a lane's exponents of 32 tiles
+        bool huge = false;                                     // scores beyond 2^20 in some row of the warp
         for (int t = 0; t < w.T; ++t, ++g) {
+          // ---- before the scores are there: the tile's exponents, and what of it the warp's rows see
+          int2 ee = make_int2(0, 0);
+          if constexpr (IMG) {
+            if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
+            ee = make_int2(__shfl_sync(RQ_FULL_MASK, ee32.x, t & 31), __shfl_sync(RQ_FULL_MASK, ee32.y, t & 31));
+          }
+          int at[2];
+          bool clear[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int v = 2 * x.step(w.kt0 + t) + half;
+            at[half] = v < x.tiles ? x.tile(v) * kQ8Tile : 1 << 30;            // (not there: behind every row)
+            clear[half] = at[half] + 63 <= own0 && (at[half] > own1 - win || at[half] + 63 < sinks);
+          }
           const int n = n0 + g;
           bool good;
           if (i == 0 && two) {
@@ -495,25 +562,16 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
             break;
           }
           tc_fence_after();
-          int2 ee;
-          if constexpr (IMG) {
-            if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
-            ee = make_int2(__shfl_sync(RQ_FULL_MASK, ee32.x, t & 31), __shfl_sync(RQ_FULL_MASK, ee32.y, t & 31));
-          } else {
-            ee = exps[g & 7];
-          }
-          const float ke = q8_pow2(max(min(ee.x, 127), -126)), ev = float(ee.y);
           uint32_t s[kKeys];
 #pragma unroll
           for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
+          if constexpr (!IMG) ee = exps[g & 7];
+          const float ke = q8_pow2(max(min(ee.x, 127), -126)), ev = float(ee.y);
           tc_wait_ld();
-          // ---- what the row does not see
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int v = 2 * x.step(w.kt0 + t) + half;
-            const int at = v < x.tiles ? x.tile(v) * kQ8Tile : 1 << 30;        // (not there: behind every row)
-            if (at + 63 <= own0 && (at > own1 - win || at + 63 < sinks)) continue;
-            const int hi = own - at + 1, lo = own - win - at + 1, sk = min(sinks - at, hi);
+            if (clear[half]) continue;
+            const int hi = own - at[half] + 1, lo = own - win - at[half] + 1, sk = min(sinks - at[half], hi);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const uint32_t seen = range_bits(lo - 32 * q, hi - 32 * q) | range_bits(0, sk - 32 * q);
@@ -543,6 +601,7 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
               h = hn;
             }
             l *= f;
+            huge = __any_sync(RQ_FULL_MASK, fabsf(R * c) > 0x1p20f && R != -INFINITY);
             if (t > 0) {
 #pragma unroll 1
               for (int y = 0; y < D / 16; ++y) {
@@ -555,30 +614,43 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
               }
             }
           }
-          const float r0x = R == -INFINITY ? 0.f : -R, hx = ev - h;
-          const uint64_t k2 = pack2(ke, ke), r2 = pack2(r0x, r0x), c2 = pack2(c, c), h2 = pack2(hx, hx);
+          // (huge scores: the difference first, exactly; one multiplication and addition would leave a
+          // residue of their last bits)
+          const float rz = R == -INFINITY ? 0.f : -R, hx = ev - h;
           uint64_t sum[2] = {0ull, 0ull};
+          auto weights = [&](auto exactly) {
+            constexpr bool EXACTLY = decltype(exactly)::value;
+            const float mul = EXACTLY ? c : ke * c, add = EXACTLY ? hx : fmaf(rz, c, hx);
+            const uint64_t k2 = pack2(ke, ke), r2 = pack2(rz, rz), c2 = pack2(mul, mul), h2 = pack2(add, add);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t p[32];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t p[32];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              const int k = half * 64 + 2 * y;
-              float p0, p1;
-              unpack2(fma2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), k2, r2), c2, h2), p0, p1);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-              sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
-              p[y] = pack_half2(p0, p1);
+              for (int y = 0; y < 32; ++y) {
+                const int k = half * 64 + 2 * y;
+                uint64_t z = pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                if (EXACTLY) z = fma2(z, k2, r2);
+                float p0, p1;
+                unpack2(fma2(z, c2, h2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+                p[y] = pack_half2(p0, p1);
+              }
+              tc_st32(tS + 32 * half, p);
+              // the values of the first 64 keys may begin
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive(pready(i, half));
             }
-            tc_st32(tS + 32 * half, p);
-          }
+          };
+          if (huge || ke < 0x1p-60f)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
           float a0, a1;
           unpack2(add2(sum[0], sum[1]), a0, a1);
           l = fmaf(a0 + a1, q8_pow2(-max(min(ee.y, 126), -126)), l);
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(pready(i));
         }
         if (!failed) {
           const int last_step = n0 + g;
@@ -701,7 +773,13 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
           }
         }
       }
-      __syncwarp();                                            // (the next queries overwrite the rows)
+      // (the next queries overwrite the rows; the copy's are the other proxy's)
+      if constexpr (IMG) {
+        fence_async_smem();
+        group_sync(i);
+      } else {
+        __syncwarp();
+      }
       tc_fence_before();
     }
   }
@@ -722,8 +800,9 @@ int rows_list(const Shape& s, int n_new, int max_ctx, int window, int n_sink) {
 
 struct RowsPlan {
   Q8Layout line;
-  bool images;
-  int list, group;       // sequences handled together
+  bool by_images;
+  int list, row_tiles, group;   // sequences handled together
+  size_t images, queries;       // bytes of a sequence's operand tiles
   size_t total;
 };
 
@@ -736,11 +815,15 @@ RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int
   p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), 2);
   p.total = p.line.total;
   const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
-  p.images = rows > (kImageBlocks - 1) * kBlockRows;
+  p.by_images = rows > (kImageBlocks - 1) * kBlockRows;
   p.group = s.batch;
-  if (!p.images) return p;
+  if (!p.by_images) return p;
   p.list = rows_list(s, n_new, max_ctx, window, n_sink);
-  const size_t per = size_t(s.n_kv_heads) * p.list * (s.head_dim == 128 ? RowsSmem<128>::kImage : RowsSmem<64>::kImage);
+  p.row_tiles = int((rows + kRowTile - 1) / kRowTile);
+  const bool wide = s.head_dim == 128;
+  p.images = size_t(s.n_kv_heads) * p.list * (wide ? RowsSmem<128>::kImage : RowsSmem<64>::kImage);
+  p.queries = size_t(s.n_kv_heads) * p.row_tiles * (wide ? RowsSmem<128>::kQueryImage : RowsSmem<64>::kQueryImage);
+  const size_t per = p.images + p.queries;
   p.group = int(std::max<size_t>(1, std::min<size_t>(s.batch, kGroupBytes / per)));
   p.total += std::min(per * size_t(s.batch), std::max(per, kGroupBytes));
   return p;
@@ -756,7 +839,7 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   q8_schedule_kernel<kBlockRows, kKeys><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * a.list), 256, 0, stream, a)) != cudaSuccess)
+  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * (unsigned(a.list) + kQueryBlocks * unsigned(a.row_tiles))), 256, 0, stream, a)) != cudaSuccess)
     return e;
   return launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a);
 }
@@ -780,6 +863,8 @@ cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const
   q8_place(a, p.line, ws, 2);
   a.images = static_cast<uint8_t*>(ws) + p.line.total;
   a.list = p.list;
+  a.row_tiles = p.row_tiles;
+  a.queries = a.images + p.images * size_t(p.group);
   for (int b0 = 0; b0 < s.batch; b0 += p.group) {            // (a group's kernels use the workspace after the one before)
     RowsArgs g = a;
     g.B = std::min(p.group, s.batch - b0);
@@ -798,9 +883,9 @@ cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const
     }
     cudaError_t e;
     if (s.head_dim == 128)
-      e = s.format == RQ_Q8_INT8 ? launch_either<128, RQ_Q8_INT8>(g, p.images, stream) : launch_either<128, RQ_Q8_E4M3>(g, p.images, stream);
+      e = s.format == RQ_Q8_INT8 ? launch_either<128, RQ_Q8_INT8>(g, p.by_images, stream) : launch_either<128, RQ_Q8_E4M3>(g, p.by_images, stream);
     else
-      e = s.format == RQ_Q8_INT8 ? launch_either<64, RQ_Q8_INT8>(g, p.images, stream) : launch_either<64, RQ_Q8_E4M3>(g, p.images, stream);
+      e = s.format == RQ_Q8_INT8 ? launch_either<64, RQ_Q8_INT8>(g, p.by_images, stream) : launch_either<64, RQ_Q8_E4M3>(g, p.by_images, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

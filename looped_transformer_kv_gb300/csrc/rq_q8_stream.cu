@@ -127,12 +127,12 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
         const int qc = threadIdx.x % LPR;
 #pragma unroll 1
         for (int y = threadIdx.x / LPR; y < L::kRows; y += AT) {
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = 0.f;
           const int j = (r0 + y) / a.G, hq = w.h * a.G + (r0 + y) % a.G;
           const bool live = y < x.rows;
-          if (live) q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec, f);
+          uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+          if (live) raw = q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec);
+          float f[8];
+          q8_floats(raw, f);
           bool lost = false;
           if (a.c.rope.table != nullptr) {
             int pos = -1;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
               lost = pos < 0 || pos >= a.c.rope.n_pos;
               if (lost) pos = -1;
             }
-            q8_rotate<D>(f, a.c.rope, pos, lane);
+            q8_rotate<D>(f, a.c.rope, q8_angles<D>(a.c.rope, pos, lane), lane);
           }
           float mx = 0.f;
 #pragma unroll
