@@ -47,8 +47,10 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
+// (more than 8 rows: accumulators take more registers than two CTAs of five warps leave, so three more
+// warps are launched that give theirs away)
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
+__global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
   using L = StreamSmem<D, NT>;
   constexpr int KS = D / 16;                                // k-steps of a score, 16-channel tiles of O
   grid_wait();
@@ -74,7 +76,9 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
   const Cut from = a.cut[me];
   Walk<8 * NT, kQ8Tile> w(a, from, a.cut[me + 1].pos);
 
-  if (warp == 4) {                                          // ---- copies
+  if (warp >= 4) {                                          // ---- copies
+    if constexpr (NT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp > 4) return;
     int g = 0;
     bool good = true;
     while (good && w.next()) {
@@ -110,6 +114,7 @@ __global__ void __launch_bounds__(160, StreamSmem<D, NT>::kCtas) q8_stream_kerne
       }
     }
   } else {                                                  // ---- products
+    if constexpr (NT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int r = lane >> 2, c = lane & 3;
     float* const merge = reinterpret_cast<float*>(smem + L::merge);
     uint2* const query = reinterpret_cast<uint2*>(smem + L::query);
@@ -468,7 +473,7 @@ cudaError_t launch(const Q8Line& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), 160, L::total, stream, a);
+  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), NT > 1 ? 256 : 160, L::total, stream, a);
 }
 
 }  // namespace
