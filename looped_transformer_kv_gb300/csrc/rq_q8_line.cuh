@@ -32,6 +32,7 @@ struct Q8Line {
   float* part;           // ... their sums
   int32_t n_ctas, n_tickets;
   int32_t clear;         // the call's first launch
+  int32_t own_cut;       // each CTA cuts for itself
 };
 
 // The tiles of 64 slots that some new token of a sequence sees, as a list: 0 .. sink0 and then from
@@ -135,19 +136,99 @@ __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant
   }
 }
 
-// A CTA's segments in order.
+// The same cut by a CTA of THREADS threads for itself, where there are at most kOwnCutPairs pairs; the
+// kernel before then only clears (q8_clear_kernel), and need not be waited for until the error word, the
+// tickets or partial results are used.
+constexpr int kOwnCutPairs = 640;
+
+struct OwnCut {
+  Cut from;
+  Rows rows;             // what the first (sequence, block) sees
+  int64_t to, N;         // where the stretch ends; the line's length
+  int32_t used;
+  int64_t warp_sum[8];
+};
+
+template <int ROWS, int KEYS, int THREADS>
+__device__ __forceinline__ bool own_cut(const Q8Line& a, OwnCut& out, int me) {   // whether some length is bad
+  constexpr int EACH = (kOwnCutPairs + THREADS - 1) / THREADS, WARPS = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = a.B * a.blocks;
+  int64_t run = 0;
+  int64_t before[EACH];
+  int units[EACH];
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    before[k] = run;
+    units[k] = 0;
+    if (k * THREADS >= pairs) continue;
+    const int p = tid + k * THREADS;
+    if (p < pairs) {
+      const Rows x = rows_of<ROWS, KEYS>(a, p / a.blocks, p % a.blocks);
+      bad |= !x.ok;
+      units[k] = x.V;
+    }
+    int64_t sum = int64_t(units[k]) * a.v.H;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(RQ_FULL_MASK, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) out.warp_sum[warp] = sum;
+    __syncthreads();
+    before[k] = run + sum - int64_t(units[k]) * a.v.H;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before[k] += out.warp_sum[w];
+      run += out.warp_sum[w];
+    }
+    __syncthreads();
+  }
+  const int used = int(min(run, int64_t(a.n_ctas)));
+  const int64_t pos = used ? run * me / used : 0;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k)
+    if (before[k] <= pos && pos < before[k] + int64_t(units[k]) * a.v.H) {
+      const int p = tid + k * THREADS;
+      out.from = {pos, before[k], p / a.blocks, p % a.blocks};
+      out.rows = rows_of<ROWS, KEYS>(a, p / a.blocks, p % a.blocks);
+    }
+  if (tid == 0) {
+    out.to = used ? run * (me + 1) / used : 0;
+    out.N = run;
+    out.used = used;
+  }
+  return __syncthreads_or(bad);
+}
+
+// A CTA's segments in order.  (No constructor: it may lie in shared memory, which keeps it out of the
+// registers of the threads that read it.)
 template <int ROWS, int KEYS>
 struct Walk {
-  const Q8Line& a;
   int64_t pos, end, base;   // base: where the units of (b, block) begin
-  int b, block;
-  Rows x;
-  int h, kt0, T;
   int64_t unit;             // the unit's place on the line
-  bool loaded;
-  __device__ __forceinline__ Walk(const Q8Line& args, const Cut& from, int64_t to)
-      : a(args), pos(from.pos), end(to), base(from.base), b(from.b), block(from.block), loaded(false) {}
-  __device__ __forceinline__ bool next() {
+  int b, block, h, kt0, T;
+  Rows x;
+  bool loaded, more;
+  __device__ __forceinline__ void begin(const Cut& from, int64_t to) {
+    pos = from.pos;
+    end = to;
+    base = from.base;
+    b = from.b;
+    block = from.block;
+    loaded = false;
+  }
+  __device__ __forceinline__ void begin(const OwnCut& cut) {
+    begin(cut.from, cut.to);
+    x = cut.rows;
+    loaded = true;
+  }
+  __device__ __forceinline__ bool next(const Q8Line& a) {
+    more = advance(a);
+    return more;
+  }
+  __device__ __forceinline__ bool advance(const Q8Line& a) {
     if (pos >= end) return false;
     for (;;) {
       if (!loaded) {
@@ -170,10 +251,8 @@ struct Walk {
     pos += T;
     return true;
   }
-  // The CTAs that share the unit (cut i lies at N i / used).
-  __device__ __forceinline__ void sharers(int& first, int& last) const {
-    const int64_t N = a.prefix[int64_t(a.B) * a.blocks];
-    const int used = *a.used;
+  // The CTAs that share the unit (cut i lies at N i / used; N: the line's length).
+  __device__ __forceinline__ void sharers(int64_t N, int used, int& first, int& last) const {
     first = int(((unit + 1) * used + N - 1) / N) - 1;
     last = int(((unit + x.V) * used + N - 1) / N) - 1;
   }

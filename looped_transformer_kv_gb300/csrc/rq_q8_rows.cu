@@ -36,9 +36,9 @@ struct RowsSmem {
   static constexpr int kTile = kKeys * D * 2;               // one K, V or Q tile
   static constexpr int v = 0, k = 2 * kTile, q = 5 * kTile, exps = 7 * kTile;   // V first: see v_desc
   static constexpr int row_exps = exps + 64;                // [8] K's and V's exponent of a tile
-  static constexpr int bars = row_exps + kBlockRows * 4;
+  static constexpr int bars = row_exps + kBlockRows * 4, walks = bars + 256;
   static constexpr int kImage = 2 * kTile + 128, kQueryImage = kTile + 4 * kRowTile;   // of tiles in the workspace
-  static constexpr int total = bars + 256 + 1024;           // + alignment of the base
+  static constexpr int total = walks + 4 * int(sizeof(RowWalk)) + 1024;   // + alignment of the base
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -327,16 +327,19 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const Cut from = a.cut[me];
-  RowWalk w(a, from, a.cut[me + 1].pos);
+  const int64_t to_pos = a.cut[me + 1].pos;
+  RowWalk* const walks = reinterpret_cast<RowWalk*>(smem + L::walks);           // of the softmax groups, products, copies
   bool failed = false;
 
   if (!IMG && warp >= 12) {                                  // ---- codes to operands
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    RowWalk w;
+    w.begin(from, to_pos);
     Converter<D, FMT> to(a, threadIdx.x - 384, lane);
     constexpr int PIECES = Converter<D, FMT>::PIECES;
     int g = 0, n0 = 0;                                       // tiles so far; g's step is n0 + g
     int sk[3] = {-1, -1, -1};                                // steps that end with K tile g - 1, g - 2, g - 3
-    while (!failed && w.next()) {
+    while (!failed && w.next(a)) {
       const Rows& x = w.x;
       if (!x.ok) continue;
       uint4 kreg[PIECES], vreg[PIECES];
@@ -390,8 +393,10 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const bool leader = elect_one();
     if (IMG && warp == 9 && leader) {                        // ---- copies of operand tiles
+      RowWalk& w = walks[3];
+      w.begin(from, to_pos);
       int g = 0, n0 = 0, sk[3] = {-1, -1, -1};               // as the converting warps'
-      while (!failed && w.next()) {
+      while (!failed && w.next(a)) {
         if (!w.x.ok) continue;
         const uint8_t* const unit = a.images + (int64_t(w.b) * a.v.H + w.h) * a.list * RowsSmem<D>::kImage;
         for (int t = 0; t < w.T; ++t, ++g) {
@@ -440,7 +445,9 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
         }
         return true;
       };
-      while (good && w.next()) {
+      RowWalk& w = walks[2];
+      w.begin(from, to_pos);
+      while (good && w.next(a)) {
         if (!w.x.ok) continue;
         const bool two = w.x.rows > kRowTile;
         good = mbar_wait_bounded(kfull(g), (g / 3) & 1, kWaitNs) && mbar_wait_bounded(qready, seg & 1, kWaitNs);
@@ -489,7 +496,13 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
     uint8_t* const img = smem + L::q + i * L::kTile;          // queries, then results going out
     float4* const stats = reinterpret_cast<float4*>(a.stats);
     int g = 0, n0 = 0, s0 = 0;
-    while (w.next()) {                                         // (failed: nothing is waited for any more, results are NaN)
+    RowWalk& w = walks[i];                                     // the group's first thread walks
+    if (r == 0) w.begin(from, to_pos);
+    for (;;) {                                                 // (failed: nothing is waited for any more, results are NaN)
+      group_sync(i);
+      if (r == 0) w.next(a);
+      group_sync(i);
+      if (!w.more) break;
       const Rows& x = w.x;
       const int r0 = w.block * kBlockRows + i * kRowTile;      // the row tile's first row
       const bool two = x.rows > kRowTile, mine = i == 0 || two;
@@ -682,7 +695,7 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
           for (int z = 0; z < 8; ++z)
             *reinterpret_cast<uint4*>(part + ((8 * y + z) * kRowTile + r) * 4) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
-        w.sharers(from_cta, to_cta);
+        w.sharers(a.prefix[int64_t(a.B) * a.blocks], *a.used, from_cta, to_cta);
         __threadfence();
         group_sync(i);
         if (r == 0) last_one[i] = atomicAdd(a.tickets + 2 * from_cta + i, 1u) == unsigned(to_cta - from_cta);
@@ -774,12 +787,8 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
         }
       }
       // (the next queries overwrite the rows; the copy's are the other proxy's)
-      if constexpr (IMG) {
-        fence_async_smem();
-        group_sync(i);
-      } else {
-        __syncwarp();
-      }
+      // (the walk's first barrier follows)
+      if constexpr (IMG) fence_async_smem();
       tc_fence_before();
     }
   }

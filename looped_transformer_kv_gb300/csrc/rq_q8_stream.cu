@@ -22,21 +22,28 @@ constexpr int kScaleTop = 7, kScaleHead = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
 
+// A divided unit: its rows, the CTAs that share it.
+struct Parted {
+  bool is;
+  int b, h, r0, rows, first, last;
+};
+
 template <int D, int NT>
 struct StreamSmem {
-  static constexpr int kCtas = NT == 1 ? 3 : 2;
+  static constexpr int kCtas = NT == 1 ? 3 : 2, kThreads = NT > 1 ? 256 : 160;
   static constexpr int kCodes = 2 * kQ8Tile * D, kStage = kCodes + 128;   // (scales: 32 bytes)
   static constexpr int kRows = 8 * NT, kMergeRow = D + 4;
   static constexpr int kMerge = 4 * 8 * kMergeRow * 4;
   static constexpr int kQuery = NT * (D / 16) * 32 * 8;
-  static constexpr int kFixed = kMerge + kQuery + 4 * kRows * 8 + kRows * 8 + 512;
+  static constexpr int kFixed = kMerge + kQuery + 4 * kRows * 8 + kRows * 8 + 768;
   static constexpr int kStages0 = (227 * 1024 / kCtas - 1024 - kFixed) / kStage;
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kQuery;
   static constexpr int row_scale = stats + 4 * kRows * 8, row_limit = row_scale + kRows * 4;
   static constexpr int bars = row_limit + kRows * 4, misc = bars + 16 * kStages;
-  static constexpr int total = misc + 16 * 4 + 4 * kStages + 128;   // + alignment of the base
-  static_assert(kStages >= 2 && misc % 8 == 0, "stages");
+  static constexpr int cut = misc + 16 * 4 + 4 * 8, parted = cut + int(sizeof(OwnCut)), walk = parted + 64;
+  static constexpr int total = walk + int(sizeof(Walk<8, kQ8Tile>)) + 128;   // + alignment of the base
+  static_assert(2 * sizeof(Parted) <= 64 && kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
 };
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -47,23 +54,96 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
+// CH channels of a unit's row y, times inv.
+template <int D, int CH>
+__device__ __forceinline__ void store_row(const Q8Line& a, int b, int h, int r0, int y, int rows, int ch, const float (&o)[CH], float inv) {
+  if (y >= rows) return;
+  const int j = (r0 + y) / a.G, hq = h * a.G + (r0 + y) % a.G;
+  uint16_t* const p = a.c.out + ((int64_t(b) * a.c.n_new + j) * a.Hq + hq) * D + ch;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
+  uint32_t u[CH / 2];
+#pragma unroll
+  for (int k = 0; k < CH / 2; ++k) {
+    const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    u[k] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  if (vec && CH == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[CH / 2 - 2], u[CH / 2 - 1]);
+  else if (vec)
+    *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+  else
+#pragma unroll
+    for (int k = 0; k < CH / 2; ++k) {
+      p[2 * k] = uint16_t(u[k]);
+      p[2 * k + 1] = uint16_t(u[k] >> 16);
+    }
+}
+
+// The parts of a divided unit in their order, the loads of four at a time.
+template <int D, int NT>
+__device__ __forceinline__ void join_parts(const Q8Line& a, const Parted& u, int row, int ch) {
+  constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = 4;
+#pragma unroll 1
+  for (int y = row; y < u.rows; y += 8) {
+    float M = kNoMax, sum = 0.f, o[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) o[k] = 0.f;
+#pragma unroll 1
+    for (int k0 = u.first; k0 <= u.last; k0 += TOGETHER) {
+      float2 st[TOGETHER];
+      float4 v[TOGETHER][CH / 4];
+#pragma unroll
+      for (int k = 0; k < TOGETHER; ++k) {
+        st[k] = make_float2(kNoMax, 0.f);
+        if (k0 + k > u.last) continue;
+        const int64_t at = (2 * int64_t(k0 + k) + (k0 + k == u.first)) * kRows + y;
+        st[k] = __ldcg(&a.stats[at]);
+#pragma unroll
+        for (int z = 0; z < CH / 4; ++z) v[k][z] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + ch) + z);
+      }
+      float to = M;
+#pragma unroll
+      for (int k = 0; k < TOGETHER; ++k) to = fmaxf(to, st[k].x);
+      const float f0 = ex2(M - to);
+      M = to;
+      sum *= f0;
+#pragma unroll
+      for (int z = 0; z < CH; ++z) o[z] *= f0;
+#pragma unroll
+      for (int k = 0; k < TOGETHER; ++k) {
+        if (k0 + k > u.last) continue;
+        const float f = ex2(st[k].x - M);
+        sum += f * st[k].y;
+#pragma unroll
+        for (int z = 0; z < CH / 4; ++z) {
+          o[4 * z] = fmaf(f, v[k][z].x, o[4 * z]);
+          o[4 * z + 1] = fmaf(f, v[k][z].y, o[4 * z + 1]);
+          o[4 * z + 2] = fmaf(f, v[k][z].z, o[4 * z + 2]);
+          o[4 * z + 3] = fmaf(f, v[k][z].w, o[4 * z + 3]);
+        }
+      }
+    }
+    store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+  }
+}
+
 // (more than 8 rows: accumulators take more registers than two CTAs of five warps leave, so three more
 // warps are launched that give theirs away)
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
+__global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
   using L = StreamSmem<D, NT>;
+  using StreamWalk = Walk<8 * NT, kQ8Tile>;
   constexpr int KS = D / 16;                                // k-steps of a score, 16-channel tiles of O
-  grid_wait();
   const int me = int(blockIdx.x);
-  if (me >= *a.used) return;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(smem + L::bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (L::kStages + s); };
-  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [1]: last of a unit, [4 ..]: a warp's E
+  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [1], [2]: last of a unit, [4 ..]: a warp's E
   int* const bad_page = misc + 16;                          // [stage]
+  OwnCut& cut = *reinterpret_cast<OwnCut*>(smem + L::cut);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(full(s), 1);
@@ -72,16 +152,37 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
     misc[0] = 0;
     fence_mbar_init();
   }
-  __syncthreads();
-  const Cut from = a.cut[me];
-  Walk<8 * NT, kQ8Tile> w(a, from, a.cut[me + 1].pos);
-
+  if (a.own_cut) {
+    const bool bad = own_cut<8 * NT, kQ8Tile, StreamSmem<D, NT>::kThreads>(a, cut, me);
+    if (bad && me == 0 && threadIdx.x == 0) {
+      grid_wait();
+      atomicOr(a.err, 1u);
+    }
+  } else {
+    grid_wait();
+    if (threadIdx.x == 0) {
+      cut.used = *a.used;
+      cut.N = a.prefix[int64_t(a.B) * a.blocks];
+      if (me < cut.used) {
+        cut.from = a.cut[me];
+        cut.to = a.cut[me + 1].pos;
+        cut.rows = rows_of<8 * NT, kQ8Tile>(a, cut.from.b, cut.from.block);
+      }
+    }
+    __syncthreads();
+  }
+  if (me >= cut.used) {
+    grid_wait();                                            // (the kernel before is complete when this one is)
+    return;
+  }
   if (warp >= 4) {                                          // ---- copies
     if constexpr (NT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp > 4) return;
+    StreamWalk w;
+    w.begin(cut);
     int g = 0;
     bool good = true;
-    while (good && w.next()) {
+    while (good && w.next(a)) {
       if (!w.x.ok) continue;
       for (int t0 = 0; t0 < w.T && good; t0 += 32) {
         int64_t rec = -1;
@@ -96,7 +197,10 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
           if (lane == 0) {
             const int64_t at = r < 0 ? w.h : r;             // (no page: page 0, and flagged)
             bad_page[s] = r < 0;
-            if (r < 0) atomicOr(a.err, 1u);
+            if (r < 0) {
+              grid_wait();
+              atomicOr(a.err, 1u);
+            }
             uint8_t* const stage = smem + s * L::kStage;
             mbar_arrive_expect_tx(full(s), L::kCodes + 32);
             bulk_g2s(smem_u32(stage), a.v.codes + at * a.v.rec_codes, L::kCodes, full(s));
@@ -110,6 +214,7 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
       for (int k = max(0, g - L::kStages); k < g; ++k) mbar_wait_bounded(full(k % L::kStages), (k / L::kStages) & 1, kWaitNs);
       if (lane == 0) {
         atomicExch(&misc[0], 1);
+        grid_wait();
         atomicOr(a.err, 1u);
       }
     }
@@ -121,9 +226,17 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
     float2* const stats = reinterpret_cast<float2*>(smem + L::stats);          // [warp][row]
     float* const row_scale = reinterpret_cast<float*>(smem + L::row_scale);
     int* const row_limit = reinterpret_cast<int*>(smem + L::row_limit);        // a row's own slot
+    constexpr int CH = D / 16;                              // channels of a thread that stores
+    Parted* const parted = reinterpret_cast<Parted*>(smem + L::parted);        // [0] at the stretch's begin, [1] at its end
+    if (threadIdx.x < 2) parted[threadIdx.x].is = false;
+    StreamWalk& w = *reinterpret_cast<StreamWalk*>(smem + L::walk);            // thread 0 walks
+    if (threadIdx.x == 0) w.begin(cut);
     int g = 0;
     bool dead = false;
-    while (w.next()) {
+    for (;;) {
+      if (threadIdx.x == 0) w.next(a);
+      consumers_sync();
+      if (!w.more) break;
       const Rows& x = w.x;
       const int r0 = w.block * L::kRows;
       // ---- the rows' queries as B fragments: (k-step, row) word pairs of the lanes that use them
@@ -354,30 +467,7 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
       if (lane == 0) misc[4 + warp] = E;
       const bool whole = w.kt0 == 0 && w.T == x.V;
       const int slot = 2 * me + (w.kt0 == 0 ? 1 : 0);
-      constexpr int CH = D / 16;                            // channels of a thread: row tid / 16
-      const int mr = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;
-      auto store = [&](int y, const float (&o)[CH], float inv) {
-        if (y >= x.rows) return;
-        const int j = (r0 + y) / a.G, hq = w.h * a.G + (r0 + y) % a.G;
-        uint16_t* const p = a.c.out + ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D + ch;
-        const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
-        uint32_t u[CH / 2];
-#pragma unroll
-        for (int k = 0; k < CH / 2; ++k) {
-          const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-          u[k] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-        if (vec && CH == 8)
-          *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[CH / 2 - 2], u[CH / 2 - 1]);
-        else if (vec)
-          *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-        else
-#pragma unroll
-          for (int k = 0; k < CH / 2; ++k) {
-            p[2 * k] = uint16_t(u[k]);
-            p[2 * k + 1] = uint16_t(u[k] >> 16);
-          }
-      };
+      const int mr = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;   // row, channels of a thread
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         consumers_sync();
@@ -405,7 +495,7 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
         }
         if (!x.ok || *reinterpret_cast<volatile int*>(&misc[0]) != 0) sum = __int_as_float(0x7fc00000);
         if (whole) {
-          store(y, o, sum == 0.f ? 0.f : 1.f / sum);
+          store_row<D, CH>(a, w.b, w.h, r0, y, x.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
         } else {
           float* const p = a.part + (int64_t(slot) * L::kRows + y) * D + ch;
 #pragma unroll
@@ -413,46 +503,37 @@ __global__ void __launch_bounds__(NT > 1 ? 256 : 160, StreamSmem<D, NT>::kCtas) 
           if (ch == 0) a.stats[int64_t(slot) * L::kRows + y] = make_float2(M, sum);
         }
       }
-      if (!whole) {
-        int first, last;                                    // the CTAs that share the unit
-        w.sharers(first, last);
-        __threadfence();
-        consumers_sync();
-        if (threadIdx.x == 0) misc[1] = atomicAdd(a.tickets + first, 1u) == unsigned(last - first);
-        consumers_sync();
-        if (misc[1]) {
-          __threadfence();
-#pragma unroll 1
-          for (int n = 0; n < NT; ++n) {
-            const int y = 8 * n + mr;
-            if (y >= x.rows) break;
-            float M = kNoMax, sum = 0.f, o[CH];
-#pragma unroll
-            for (int k = 0; k < CH; ++k) o[k] = 0.f;
-            for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(&a.stats[(2 * int64_t(k) + (k == first)) * L::kRows + y]).x);
-            for (int k = first; k <= last; ++k) {
-              const int64_t at = (2 * int64_t(k) + (k == first)) * L::kRows + y;
-              const float2 st = __ldcg(&a.stats[at]);
-              const float f = ex2(st.x - M);
-              sum += f * st.y;
-              const float* const p = a.part + at * D + ch;
-#pragma unroll
-              for (int z = 0; z < CH; z += 4) {
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(p + z));
-                o[z] = fmaf(f, u.x, o[z]);
-                o[z + 1] = fmaf(f, u.y, o[z + 1]);
-                o[z + 2] = fmaf(f, u.z, o[z + 2]);
-                o[z + 3] = fmaf(f, u.w, o[z + 3]);
-              }
-            }
-            store(y, o, sum == 0.f ? 0.f : 1.f / sum);
-          }
-        }
+      if (!whole && threadIdx.x == 0) {
+        Parted& p = parted[w.kt0 == 0];
+        p = {true, w.b, w.h, r0, x.rows, 0, 0};
+        w.sharers(cut.N, cut.used, p.first, p.last);
       }
       consumers_sync();                                     // (the next segment overwrites what was read)
     }
-    if (dead && threadIdx.x % 32 == 0) atomicOr(a.err, 1u);
+    // ---- divided units, at most two: the last of their CTAs joins the parts
+    grid_wait();
+    if (parted[0].is || parted[1].is) {
+      __threadfence();
+      consumers_sync();
+      if (threadIdx.x < 2) {
+        const Parted& p = parted[threadIdx.x];
+        misc[1 + threadIdx.x] = p.is && atomicAdd(a.tickets + p.first, 1u) == unsigned(p.last - p.first);
+      }
+      consumers_sync();
+      __threadfence();
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k)
+        if (misc[1 + k]) join_parts<D, NT>(a, parted[k], threadIdx.x >> 4, (threadIdx.x & 15) * CH);
+    }
+    if (dead && lane == 0) atomicOr(a.err, 1u);
   }
+}
+
+// Clears the error word and the tickets.
+__global__ void __launch_bounds__(256) q8_clear_kernel(unsigned* err, unsigned* tickets, int n) {
+  grid_next();
+  if (threadIdx.x == 0) *err = 0u;
+  for (int i = threadIdx.x; i < n; i += 256) tickets[i] = 0u;
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -471,9 +552,12 @@ cudaError_t launch(const Q8Line& a, cudaStream_t stream) {
     return cudaFuncSetAttribute(q8_stream_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
+  if (a.own_cut)
+    q8_clear_kernel<<<1, 256, 0, stream>>>(a.err, a.tickets, a.n_ctas);
+  else
+    q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), NT > 1 ? 256 : 160, L::total, stream, a);
+  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), L::kThreads, L::total, stream, a);
 }
 
 }  // namespace
@@ -487,6 +571,7 @@ cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, con
   const int nt = tiles_of_rows(int64_t(c.n_new) * (s.n_q_heads / s.n_kv_heads));
   Q8Line a = q8_line(s, cache, paging, c, 8 * nt);
   q8_place(a, stream_layout(s, c.n_new, c.max_ctx, nt), ws, 1);
+  a.own_cut = int64_t(a.B) * a.blocks <= kOwnCutPairs;
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
   switch (nt) {
     case 1:
