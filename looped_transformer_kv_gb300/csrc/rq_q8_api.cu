@@ -58,7 +58,7 @@ rq_status append_common(const rq_q8_shape* s, const rq_q8_cache* cache, const rq
   rq::Q8Rope r;
   if ((st = check_rope(s, rope, r)) != RQ_OK) return st;
   const int64_t blocks = (int64_t(n_new < s->capacity ? n_new : s->capacity) + 30) / 16;
-  if (int64_t(s->batch) * s->n_kv_heads > (int64_t(1) << 34) / (blocks * loop_count * 2)) return RQ_ERR_UNSUPPORTED;   // (grid.x)
+  if (int64_t(s->batch) * s->n_kv_heads > ((int64_t(1) << 31) - 1) / (blocks * loop_count * 2)) return RQ_ERR_UNSUPPORTED;   // (grid.x)
   if (n_new == 0) return RQ_OK;
   try {
     return from_cuda(rq::launch_q8_append(*s, *cache, paging, kv_new, strides, loop_begin, loop_count,

@@ -1,6 +1,6 @@
-// Appending to the 8-bit cache (include/rq_q8.h): a warp takes one block of 16 slots of one
-// (sequence, loop, kv-head, K or V).  D / 8 lanes hold a row, 8 channels each; the new rows are
-// loaded and rotated, their largest magnitude gives the scale, and the codes follow from registers.
+// Appending to the 8-bit cache (include/rq_q8.h): two warps (d = 64: one) take one block of 16 slots of one
+// (sequence, loop, kv-head, K or V); D / 8 lanes hold a row, 8 channels each.  The new rows are loaded and
+// rotated, their largest magnitude gives the scale, and the codes follow from registers.
 #include <algorithm>
 
 #include "rq_kernels.h"
@@ -28,12 +28,12 @@ __device__ __forceinline__ uint2 codes_of(const float (&f)[8], float inv) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (FMT == RQ_Q8_INT8) {
-      w[k] = 0u;
+      // under 2^23 + 2^22 a unit is worth 1: the sum's rounding is the code's, its low byte the code (a
+      // magnitude is at most 127.25 here)
+      uint32_t x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = max(-127, min(127, __float2int_rn(f[4 * k + i] * inv)));
-        w[k] |= (uint32_t(x) & 255u) << (8 * i);
-      }
+      for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(fmaf(f[4 * k + i], inv, 12582912.f));
+      w[k] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
     } else {
       const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k] * inv, f[4 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
       const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k + 2] * inv, f[4 * k + 3] * inv), __NV_SATFINITE, __NV_E4M3);
@@ -59,11 +59,20 @@ __device__ __forceinline__ void values_of(uint2 w, float (&f)[8]) {
   }
 }
 
+// The larger magnitude; not a number if either is none.
+__device__ __forceinline__ float larger(float m, float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
+  return y;
+}
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) q8_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = kQ8Block / RPI;   // lanes per row, rows at a time
-  const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(64, 16) q8_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int SPLIT = D / 64, LPR = D / 8, RPI = 32 / LPR, IT = kQ8Block / SPLIT / RPI;   // warps per block, lanes per row, rows at a time
+  __shared__ uint32_t halves[2];                                     // largest magnitude of a warp's rows
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR, half = warp % SPLIT;
+  const int sub = lane / LPR + half * (kQ8Block / 2);
+  int64_t u = int64_t(blockIdx.x) * (2 / SPLIT) + warp / SPLIT;
   if (u >= a.units) return;
   const int h = int(u % a.v.H);
   u /= a.v.H;
@@ -89,42 +98,44 @@ __global__ void __launch_bounds__(256) q8_append_kernel(const __grid_constant__ 
 
   const uint16_t* const src = a.kv + b * a.s0 + kv * a.s2 + l * a.s3 + h * a.s4 + 8 * c;
   float f[IT][8];
-  uint32_t most = 0u;                                                // largest magnitude's fp32 bits
+  float largest = 0.f;
   uint4 raw[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int t = k0 + i * RPI + sub;
     raw[i] = t >= t0 && t < t1 ? q8_load8(src + (t - ctx) * a.s1, a.vec) : make_uint4(0u, 0u, 0u, 0u);
   }
-#pragma unroll
-  for (int i = 0; i < IT; ++i) q8_floats(raw[i], f[i]);
   if (kv == 0 && a.rope.table != nullptr) {
-    constexpr int TOGETHER = 1;                                      // rows whose angles are loaded at once
 #pragma unroll
-    for (int i0 = 0; i0 < IT; i0 += TOGETHER) {
-      Q8Angles angles[TOGETHER];
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        const int t = k0 + (i0 + i) * RPI + sub;
-        int pos = -1;
-        if (t >= t0 && t < t1) {
-          pos = a.rope.positions ? a.rope.positions[int64_t(b) * a.n_new + t - ctx] : t;
-          if (pos < 0 || pos >= a.rope.n_pos) {
-            pos = -1;
-            most = 0x7fffffffu;                                      // as a row that is not finite
-          }
+    for (int i = 0; i < IT; ++i) {
+      const int t = k0 + i * RPI + sub;
+      int pos = -1;
+      if (t >= t0 && t < t1) {
+        pos = a.rope.positions ? a.rope.positions[int64_t(b) * a.n_new + t - ctx] : t;
+        if (pos < 0 || pos >= a.rope.n_pos) {
+          pos = -1;
+          largest = __int_as_float(0x7fc00000);                      // as a row that is not finite
         }
-        angles[i] = q8_angles<D>(a.rope, pos, lane);
       }
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) q8_rotate<D>(f[i0 + i], a.rope, angles[i], lane);
+      const Q8Angles angles = q8_angles<D>(a.rope, pos, lane);
+      q8_floats(raw[i], f[i]);
+      q8_rotate<D>(f[i], a.rope, angles, lane);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) q8_floats(raw[i], f[i]);
   }
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(f[i][k]) & 0x7fffffffu);
-  most = __reduce_max_sync(RQ_FULL_MASK, most);
+    for (int k = 0; k < 8; ++k) largest = larger(largest, f[i][k]);
+  // (a NaN's bits, without the sign, are above every number's)
+  uint32_t most = __reduce_max_sync(RQ_FULL_MASK, __float_as_uint(largest) & 0x7fffffffu);
+  if (SPLIT == 2) {
+    if (lane == 0) halves[warp] = most;
+    __syncthreads();
+    most = max(most, halves[warp ^ 1]);
+  }
 
   // the least exponent that holds them; bf16 bits: exponent field, 7 bits of the significand
   const uint32_t m16 = most < 0x7f800000u ? float_to_bf16_bits(__uint_as_float(most)) : 0x7f80u;
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(256) q8_append_kernel(const __grid_constant__ 
   const int e_old = k0 < ctx ? q8_exponent(was) : kQ8LeastExp;
   const bool bad = m16 >= 0x7f80u || e_old > 127;
   e = max(e, e_old);
-  if (lane == 0 && (k0 >= ctx || bad || e > e_old)) *scale = bad ? __int_as_float(0x7fc00000) : q8_pow2(e);
+  if (lane == 0 && half == 0 && (k0 >= ctx || bad || e > e_old)) *scale = bad ? __int_as_float(0x7fc00000) : q8_pow2(e);
   const float inv = bad ? 0.f : q8_pow2(-e);
 
   auto at = [&](int t) {
@@ -186,17 +197,18 @@ cudaError_t launch_q8_append(const rq_q8_shape& s, const rq_q8_cache& cache, con
   bool vec = (reinterpret_cast<uintptr_t>(kv_new) & 15) == 0;
   for (int i = 0; i < 5; ++i) vec = vec && strides[i] % 8 == 0;
   a.vec = vec;
-  const unsigned grid = unsigned((a.units + 7) / 8);
+  const int each = 128 / s.head_dim;                                 // units of a CTA
+  const unsigned grid = unsigned((a.units + each - 1) / each);
   if (s.head_dim == 128) {
     if (s.format == RQ_Q8_INT8)
-      q8_append_kernel<128, RQ_Q8_INT8><<<grid, 256, 0, stream>>>(a);
+      q8_append_kernel<128, RQ_Q8_INT8><<<grid, 64, 0, stream>>>(a);
     else
-      q8_append_kernel<128, RQ_Q8_E4M3><<<grid, 256, 0, stream>>>(a);
+      q8_append_kernel<128, RQ_Q8_E4M3><<<grid, 64, 0, stream>>>(a);
   } else {
     if (s.format == RQ_Q8_INT8)
-      q8_append_kernel<64, RQ_Q8_INT8><<<grid, 256, 0, stream>>>(a);
+      q8_append_kernel<64, RQ_Q8_INT8><<<grid, 64, 0, stream>>>(a);
     else
-      q8_append_kernel<64, RQ_Q8_E4M3><<<grid, 256, 0, stream>>>(a);
+      q8_append_kernel<64, RQ_Q8_E4M3><<<grid, 64, 0, stream>>>(a);
   }
   return cudaGetLastError();
 }

@@ -24,6 +24,13 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream):
+    """The same as a number, without a Stream object (4 us of a small call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def make_shape(batch, n_q_heads, n_kv_heads, head_dim, n_loops, capacity, res_bits,
                softmax_scale=0.0, group=GROUP):
     """rq_shape for one layer; res_bits lists the residual bits of loops 0..L-2."""
@@ -386,18 +393,25 @@ def _rope(rope, B, n):
     if rope is None:
         return None
     positions = rope.tensors[1]
-    assert positions is None or tuple(positions.shape) == (B, n)
+    assert positions is None or positions.shape == (B, n)
     return ctypes.byref(rope)
+
+
+def _lens(t, B):
+    """Address of an int32 [B] tensor, or None."""
+    if t is None:
+        return None
+    assert t.dtype == torch.int32 and t.numel() == B and t.is_contiguous()
+    return t.data_ptr()
 
 
 def _q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
     B, n, two, loops, H, d = kv_new.shape
+    s0, s1, s2, s3, s4, s5 = kv_new.stride()
     assert kv_new.dtype == torch.bfloat16 and (B, two, H, d) == (shape.batch, 2, shape.n_kv_heads, shape.head_dim)
-    st = kv_new.stride()
-    assert kv_new.numel() == 0 or st[5] == 1
-    assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
-    return (kv_new.data_ptr(), _I5(*st[:5]), int(loop_begin), loops, _i32(n_lens), n, _i32(ctx_lens),
-            _rope(rope, B, n), _stream(stream))
+    assert s5 == 1 or kv_new.numel() == 0
+    return (kv_new.data_ptr(), _I5(s0, s1, s2, s3, s4), loop_begin, loops, _lens(n_lens, B), n,
+            _lens(ctx_lens, B), _rope(rope, B, n), _raw_stream(stream))
 
 
 def q8_append(shape, cache, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None, stream=None):
@@ -425,15 +439,13 @@ def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
 
 def _q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
     B, n, Hq, d = q.shape
+    s0, s1, s2, s3 = q.stride()
     assert q.dtype == out.dtype == torch.bfloat16
     assert (B, Hq, d) == (shape.batch, shape.n_q_heads, shape.head_dim)
-    qs = q.stride()
-    assert q.numel() == 0 or qs[3] == 1
-    assert out.is_contiguous() and out.shape == q.shape
-    assert ctx_lens.numel() == B and (n_lens is None or n_lens.numel() == B)
-    return (q.data_ptr(), _I3(*qs[:3]), int(loop), _i32(n_lens), n, _i32(ctx_lens), int(max_ctx),
-            int(window), int(n_sink), _rope(rope, B, n), out.data_ptr(), ws.data_ptr(),
-            ws.numel() * ws.element_size(), _stream(stream))
+    assert s3 == 1 or q.numel() == 0
+    assert out.shape == q.shape and out.is_contiguous()
+    return (q.data_ptr(), _I3(s0, s1, s2), loop, _lens(n_lens, B), n, _lens(ctx_lens, B), max_ctx, window,
+            n_sink, _rope(rope, B, n), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
 
 
 def q8_attention(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None, window=0, n_sink=0,
