@@ -86,17 +86,16 @@ __device__ __forceinline__ Rows rows_of(const Q8Line& a, int b, int block) {
 }
 
 // One CTA: clears the error word and tickets, cuts the line.
-template <int ROWS, int KEYS>
-__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ Q8Line a) {
-  grid_next();
-  __shared__ int64_t warp_sum[32];
+template <int ROWS, int KEYS, int THREADS>
+__device__ __forceinline__ void cut_line(const Q8Line& a) {
+  __shared__ int64_t warp_sum[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0 && a.clear) *a.err = 0u;
-  for (int i = tid; i < a.n_ctas * a.n_tickets; i += 1024) a.tickets[i] = 0u;
+  for (int i = tid; i < a.n_ctas * a.n_tickets; i += THREADS) a.tickets[i] = 0u;
   const int64_t pairs = int64_t(a.B) * a.blocks;
   int64_t run = 0;
   bool bad = false;
-  for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
+  for (int64_t p0 = 0; p0 < pairs; p0 += THREADS) {
     int64_t units = 0;
     if (p0 + tid < pairs) {
       const Rows x = rows_of<ROWS, KEYS>(a, int((p0 + tid) / a.blocks), int((p0 + tid) % a.blocks));
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant
     __syncthreads();
     int64_t before = run;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += warp_sum[w];
       run += warp_sum[w];
     }
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant
   if (bad && tid == 0) *a.err = 1u;
   const int used = int(min(run, int64_t(a.n_ctas)));
   if (tid == 0) *a.used = used;
-  for (int i = tid; i <= used; i += 1024) {
+  for (int i = tid; i <= used; i += THREADS) {
     const int64_t pos = used ? run * i / used : 0;
     int64_t lo = 0, hi = pairs;                             // the last pair that begins at or before pos
     while (hi - lo > 1) {
@@ -134,6 +133,11 @@ __global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant
     }
     a.cut[i] = {pos, a.prefix[lo], int(lo / a.blocks), int(lo % a.blocks)};
   }
+}
+template <int ROWS, int KEYS>
+__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ Q8Line a) {
+  grid_next();
+  cut_line<ROWS, KEYS, 1024>(a);
 }
 
 // The same cut by a CTA of THREADS threads for itself, where there are at most kOwnCutPairs pairs; the

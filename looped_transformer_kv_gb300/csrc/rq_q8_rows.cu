@@ -28,7 +28,6 @@ namespace {
 constexpr int kKeys = 128, kRowTile = 128, kBlockRows = 2 * kRowTile;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
-constexpr unsigned kQueryBlocks = 2;   // of q8_image_kernel, for a row tile
 using RowWalk = Walk<kBlockRows, kKeys>;
 
 template <int D>
@@ -103,7 +102,7 @@ struct RowsArgs : Q8Line {
 template <int D, int ROWS>
 __device__ __forceinline__ void put_queries(const Q8Line& a, const Rows& x, int b, int h, int r0, int rr0, int live,
                                             uint8_t* tile, float* factors, int lane) {
-  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = ROWS / RPI, TOGETHER = 2;   // (rows whose loads are in flight)
+  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = ROWS / RPI, TOGETHER = IT < 2 ? IT : 2;   // (rows whose loads are in flight)
   const int qc = lane % LPR;
 #pragma unroll 1
   for (int y0 = 0; y0 < IT; y0 += TOGETHER) {
@@ -241,30 +240,35 @@ struct Converter {
   }
 };
 
-// Operand tiles of a whole call: 128 threads for K, 128 for V of one key tile, or 8
-// rows of a query tile a warp.  Bound by HBM: 14,336 + 2,048 slots of 8 heads, 33 MB of codes to 67 MB of operands, in
-// 19 us.
+// The schedule, and beside it the operand tiles of the queries: a row tile a CTA, 16
+// rows a warp.
+template <int D>
+__global__ void __launch_bounds__(256, 4) q8_query_kernel(const __grid_constant__ RowsArgs a) {
+  grid_next();
+  using L = RowsSmem<D>;
+  if (blockIdx.x == 0) {
+    cut_line<kBlockRows, kKeys, 256>(a);
+    return;
+  }
+  const unsigned tile = blockIdx.x - 1;
+  const int unit = int(tile / unsigned(a.row_tiles)), b = unit / a.v.H, h = unit % a.v.H;
+  const int t = int(tile % unsigned(a.row_tiles));
+  const Rows x = sequence_of(a, b);
+  const int live = x.ok ? x.n * a.G - t * kRowTile : 0;
+  if (live <= 0) return;
+  uint8_t* const image = a.queries + (int64_t(unit) * a.row_tiles + t) * L::kQueryImage;
+  put_queries<D, 16>(a, x, b, h, t * kRowTile, int(threadIdx.x >> 5) * 16, live, image, reinterpret_cast<float*>(image + L::kTile),
+                    threadIdx.x & 31);
+}
+
+// Operand tiles of K and V: 128 threads each for one key tile.  Bound by HBM: 14,336 + 2,048 slots of 8
+// heads, 33 MB of codes to 67 MB of operands, in 19 us.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256, 4) q8_image_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
   grid_next();
   using L = RowsSmem<D>;
-  const int lane = threadIdx.x & 31;
-  const unsigned key_blocks = unsigned(a.B) * a.v.H * a.list;
-  if (blockIdx.x >= key_blocks) {                            // a part of a row tile
-    const unsigned block = blockIdx.x - key_blocks, tile = block / kQueryBlocks;
-    const int unit = int(tile / unsigned(a.row_tiles)), b = unit / a.v.H, h = unit % a.v.H;
-    const int t = int(tile % unsigned(a.row_tiles));
-    const Rows x = sequence_of(a, b);
-    const int live = x.ok ? x.n * a.G - t * kRowTile : 0;
-    if (live <= 0) return;
-    uint8_t* const image = a.queries + (int64_t(unit) * a.row_tiles + t) * L::kQueryImage;
-    constexpr int ROWS = kRowTile / kQueryBlocks / 8;
-    put_queries<D, ROWS>(a, x, b, h, t * kRowTile, (int(block % kQueryBlocks) * 8 + (threadIdx.x >> 5)) * ROWS, live, image,
-                         reinterpret_cast<float*>(image + L::kTile), lane);
-    return;
-  }
-  const int kv = threadIdx.x >> 7;
+  const int lane = threadIdx.x & 31, kv = threadIdx.x >> 7;
   const int u = int(blockIdx.x % unsigned(a.list));
   const int unit = int(blockIdx.x / unsigned(a.list)), b = unit / a.v.H, h = unit % a.v.H;
   const Rows x = sequence_of(a, b);
@@ -768,13 +772,15 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       }
       __syncwarp();
       const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
+      // place of the row that this lane stands for (the rows of the warp in turn, below)
+      const int j = row / a.G, hq = w.h * a.G + row % a.G;
+      const int64_t place = ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D;
 #pragma unroll 4
       for (int k = lane; k < 32 * CR; k += 32) {               // this warp's rows, 16 bytes a lane
         const int rr = (warp & 3) * 32 + k / CR, cc = k % CR;
+        uint16_t* const o = a.c.out + __shfl_sync(RQ_FULL_MASK, place, k / CR) + 8 * cc;
         if (i * kRowTile + rr >= x.rows) continue;
         const uint4 u = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
-        const int j = (r0 + rr) / a.G, hq = w.h * a.G + (r0 + rr) % a.G;
-        uint16_t* const o = a.c.out + ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D + 8 * cc;
         if (vec) {
           *reinterpret_cast<uint4*>(o) = u;
         } else {
@@ -846,9 +852,12 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
     return cudaFuncSetAttribute(q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  q8_schedule_kernel<kBlockRows, kKeys><<<1, 1024, 0, stream>>>(a);
+  if (IMG)
+    q8_query_kernel<D><<<1 + unsigned(a.B) * a.v.H * unsigned(a.row_tiles), 256, 0, stream>>>(a);
+  else
+    q8_schedule_kernel<kBlockRows, kKeys><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * (unsigned(a.list) + kQueryBlocks * unsigned(a.row_tiles))), 256, 0, stream, a)) != cudaSuccess)
+  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * unsigned(a.list)), 256, 0, stream, a)) != cudaSuccess)
     return e;
   return launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a);
 }
