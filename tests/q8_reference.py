@@ -112,11 +112,12 @@ def append(codes, scales, kv, ctx, fmt):
 
 def rows_of(codes, scales, n, d, fmt):
     """Values [2][n][d] of the first n slots, from codes [tiles][2][64 d] and scales [tiles][2][4]."""
+    t = np.arange(n)
+    at = np.stack([place(x, d) for x in range(64)])[t % 64]                  # [n][d]
     out = np.zeros((2, n, d))
-    for t in range(n):
-        for which in (0, 1):
-            by = codes[t // 64, which, place(t, d)]
-            out[which, t] = value_of(by, fmt) * float(scales[t // 64, which, t % 64 // 16])
+    for which in (0, 1):
+        by = np.take_along_axis(codes[t // 64, which], at, 1)
+        out[which] = value_of(by, fmt) * scales[t // 64, which, t % 64 // 16].astype(np.float64)[:, None]
     return out
 
 

@@ -11,7 +11,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
-    from looped_transformer_kv_gb300 import rq
+    import looped_transformer_kv_gb300 as rq
+    from looped_transformer_kv_gb300.rq import advance_ctx
 
 MARK = 776.0      # what outputs hold before a call
 
@@ -396,3 +397,322 @@ def test_window(window, sinks, n):
     c.attend()
     c.table.copy_(keep)
     c.check()
+
+
+LONG = [
+    # B, Hq, H, d, fmt, ctx, n_new, n_lens, more: units that several CTAs share
+    (2, 2, 1, 128, "e4m3", [9000, 2111], 1, None, dict(rot=128, fill=False)),
+    (1, 16, 2, 128, "int8", [7001], 2, None, dict(paged=True, fill=False)),
+    (2, 8, 1, 64, "int8", [5000, 130], 4, [4, 3], dict(rot=64, fill=False)),
+    (1, 4, 1, 128, "e4m3", [6000], 40, None, dict(rot=64, fill=False)),
+    (2, 4, 1, 64, "e4m3", [100, 3000], 300, [300, 222], dict(paged=True, fill=False)),
+    (1, 8, 1, 128, "int8", [3333], 200, None, dict(rot=128, window=1000, sinks=70, fill=False)),
+    (1, 2, 1, 128, "e4m3", [20000], 3, None, dict(window=5000, sinks=200, fill=False, paged=True)),
+]
+
+
+def fill_cache(c, seed=0):
+    """Random codes and scales (2^-6 .. 2^-3) in every slot of a case's cache, on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randint(0, 127, c.cache.codes.shape, generator=g, device="cuda", dtype=torch.uint8)
+    codes |= torch.randint(0, 2, codes.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    if c.fmt == "e4m3":        # below 16, no NaN
+        codes &= 0xd7
+    c.cache.codes.copy_(codes)
+    c.cache.scales.copy_(2.0 ** torch.randint(-6, -2, c.cache.scales.shape, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("B,Hq,H,d,fmt,ctx,n,lens,more", LONG)
+def test_long_contexts(B, Hq, H, d, fmt, ctx, n, lens, more):
+    c = Case(B, Hq, H, d, fmt, ctx, n, lens, **more)
+    fill_cache(c)
+    c.append()
+    c.attend()
+    c.check()
+
+
+def test_a_run_of_tokens_as_a_serving_loop_makes_it():
+    """A prompt in two chunks, drafted tokens, single tokens: append, attend, advance, on one paged cache;
+    every output against the reference over the cache as it is then."""
+    c = Case(2, 8, 2, 128, "e4m3", [0, 0], 200, cap=512, rot=128, paged=True, max_ctx=400)
+    rng = np.random.default_rng(3)
+    for n in (200, 75, 5, 1, 1, 1):
+        c.n_new, c.lens = n, [n, n]
+        c.kv_host = torch.from_numpy(rng.standard_normal((2, n, 2, 1, 2, 128)).astype(np.float32)).bfloat16()
+        c.q_host = torch.from_numpy(rng.standard_normal((2, n, 8, 128)).astype(np.float32)).bfloat16()
+        c.q, c.out = c.q_host.cuda(), torch.full((2, n, 8, 128), MARK, dtype=torch.bfloat16, device="cuda")
+        c.append(kv=c.kv_host.cuda())
+        c.append_reference()
+        c.same_cache()
+        c.attend()
+        c.check()
+        advance_ctx(c.ctx_lens, n, c.cap)
+        c.ctx = [x + n for x in c.ctx]
+    assert c.ctx_lens.tolist() == [283, 283]
+
+
+@pytest.mark.parametrize("n", [1, 3, 40, 300])
+def test_bad_lengths_and_pages(n):
+    """A sequence with bad lengths, and tokens that see a bad page, are NaN; the others are as ever."""
+    def case():
+        c = Case(4, 2, 2, 64, "e4m3", [130, 64, 200, 10], n, paged=True, max_ctx=200, cap=576)
+        c.append()
+        return c
+
+    c = case()
+    c.attend()
+    c.check()
+    clean = c.out.clone()
+    for what, value, b in (("ctx", -1, 1), ("ctx", 201, 3), ("ctx", 577, 0), ("n", -1, 2), ("n", n + 1, 0)):
+        d = case()
+        lens = torch.full((4,), n, dtype=torch.int32).cuda()
+        d.n_lens = lens
+        (d.ctx_lens if what == "ctx" else lens)[b] = value
+        d.attend()
+        assert d.error_word() != 0
+        assert torch.isnan(d.out[b].float()).all()
+        others = [x for x in range(4) if x != b]
+        assert torch.isfinite(d.out[others].float()).all()
+        np.testing.assert_allclose(d.out[others].float().cpu(), clean[others].float().cpu(), rtol=2.0 ** -7, atol=1e-3)
+    for bad in (-1, 1 << 30):
+        d = case()
+        d.table[2, 1] = bad           # slots 64..127 of sequence 2: all of its tokens see them
+        d.attend()
+        assert d.error_word() != 0 and torch.isnan(d.out[2].float()).all()
+        assert torch.isfinite(d.out[[0, 1, 3]].float()).all()
+
+
+def test_no_new_tokens():
+    for n in (1, 40, 600):
+        c = Case(3, 2, 1, 64, "int8", [5, 0, 70], n, [0, 0, 0], cap=704)
+        c.append()
+        c.same_cache()
+        c.attend()
+        torch.cuda.synchronize()
+        assert c.error_word() == 0 and (c.out == MARK).all()
+    c = Case(3, 2, 1, 64, "int8", [5, 0, 70], 1)
+    rq.q8_append(c.shape, c.cache, c.kv[:, :0], 0, c.ctx_lens)
+    rq.q8_attention(c.shape, c.cache, c.q[:, :0], 0, c.ctx_lens, 70, c.out[:, :0], c.ws)
+    c.same_cache()
+
+
+@pytest.mark.parametrize("n,heads", [(1, 1), (1, 3), (2, 1)])
+def test_wide_batches(n, heads):
+    """More sequences than a CTA cuts for itself, many of them without tokens."""
+    B = 1500
+    rng = np.random.default_rng(5)
+    ctx = rng.integers(0, 150, B).tolist()
+    lens = rng.integers(0, n + 1, B).tolist()
+    c = Case(B, heads, 1, 64, "e4m3", ctx, n, lens, cap=192, fill=False)
+    fill_cache(c)
+    c.append()
+    c.attend()
+    c.check()
+
+
+@pytest.mark.parametrize("n", [1, 4, 50, 300])
+def test_blocks_of_very_different_sizes(n):
+    """V's and K's scales from 2^-100 (zeros) over 2^-20 to 2^10 in one context."""
+    c = Case(1, 2, 1, 128, "int8", [400], n, cap=704)
+    rng = np.random.default_rng(9)
+    rows = rng.standard_normal((400, 2, 128)).astype(np.float32)
+    size = np.repeat(2.0 ** rng.integers(-20, 3, (25, 2)), 16, 0)[:400]
+    size[rng.integers(0, 25, 4) * 16 + 3] *= 0
+    rows *= size[:, :, None]
+    rows[96:112, 1] = 0
+    rows[200:, 1] *= 2.0 ** 8
+    R.append(c.codes[0, 0, :, 0], c.scales[0, 0, :, 0], torch.from_numpy(rows).bfloat16().float().numpy(), 0, "int8")
+    c.put()
+    c.append()
+    c.attend()
+    c.check()
+
+
+@pytest.mark.parametrize("n", [1, 50, 300])
+def test_huge_scores_pick_one_slot(n):
+    """Scores of 1e25: the weights are 0 and 1, and the output one value row."""
+    c = Case(1, 1, 1, 128, "e4m3", [200], n, size=1e25, cap=512)
+    c.append()
+    c.attend()
+    codes, scales = c.get()
+    k, v = R.rows_of(codes[0, 0, :, 0], scales[0, 0, :, 0], 200 + n, 128, "e4m3")
+    s = c.q_host[0, :, 0].double().numpy() @ k.T
+    s[np.arange(200 + n)[None] > 200 + np.arange(n)[:, None]] = -np.inf
+    best = s.argmax(1)
+    # (rows whose two largest scores are closer than the fp32 sums' rounding may go either way)
+    top = np.sort(s, 1)[:, -2:]
+    sure = top[:, 1] - top[:, 0] > 2.0 ** -15 * np.abs(c.q_host[0, :, 0].double().numpy()).sum(1) * np.abs(k).max()
+    assert sure.sum() >= n / 2
+    out = c.out[0, :, 0].double().cpu().numpy()
+    assert (np.abs(out - v[best])[sure] <= 2.0 ** -8 * np.abs(v[best])[sure] * 1.01 + 2.0 ** -10 * np.abs(v).max()).all()
+
+
+def test_same_call_same_bits_and_any_larger_workspace():
+    for n in (1, 5, 60, 400):
+        c = Case(2, 4, 2, 64, "e4m3", [900, 333], n, rot=64, fill=False)
+        fill_cache(c)
+        c.append()
+        c.attend()
+        first = c.out.clone()
+        c.ws = torch.full((rq.q8_workspace_bytes(c.shape, n + 700, c.max_ctx, 0, 0),), 255, dtype=torch.uint8).cuda()
+        c.out.fill_(MARK)
+        c.attend()
+        assert torch.equal(first, c.out)
+        c.check()
+
+
+def test_unaligned_outputs_and_inputs():
+    for n in (1, 20, 300):
+        c = Case(1, 3, 1, 128, "int8", [77], n, spread=True, cap=384)
+        buf = torch.full((n * 3 * 128 + 9,), MARK, dtype=torch.bfloat16, device="cuda")
+        c.out = buf[5:5 + n * 3 * 128].view(1, n, 3, 128)
+        c.append()
+        c.attend()
+        c.check()
+        assert (buf[:5] == MARK).all() and (buf[-4:] == MARK).all()
+
+
+def test_broadcast_queries():
+    """Strides of 0: one query row for all heads and tokens."""
+    c = Case(2, 4, 2, 64, "e4m3", [50, 9], 3)
+    c.append()
+    c.q = c.q[:1, :1, :1].expand(2, 3, 4, 64)
+    c.q_host = c.q.cpu()
+    c.attend()
+    c.check()
+
+
+def test_two_calls_at_once_on_side_streams():
+    cases = [Case(2, 8, 2, 128, "e4m3", [3000, 900], n, rot=128, fill=False, seed=n) for n in (1, 30, 300)]
+    for c in cases:
+        fill_cache(c, c.n_new)
+        c.append()
+        c.attend()
+    torch.cuda.synchronize()
+    want = [c.out.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for c in cases:
+        c.out.fill_(MARK)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            c.append(stream=s)
+            c.attend(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert c.error_word() == 0 and torch.equal(c.out, w)
+
+
+def test_a_captured_step_replayed():
+    """Append, attend and advance in one graph: replays leave the same bits as eager steps."""
+    def build():
+        c = Case(2, 4, 2, 128, "int8", [60, 3], 1, rot=128, cap=256, max_ctx=255)
+        return c
+
+    eager, graphed = build(), build()
+
+    def step(c):
+        c.append()
+        c.attend()
+        advance_ctx(c.ctx_lens, 1, c.cap)
+
+    outs = []
+    for _ in range(40):
+        step(eager)
+        outs.append(eager.out.clone())
+    graphed.append()      # (once before the capture: the same call again leaves the same bits)
+    graphed.attend()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graphed)
+    for i in range(40):
+        g.replay()
+        assert torch.equal(graphed.out, outs[i]), i
+    assert torch.equal(eager.cache.codes, graphed.cache.codes)
+    assert eager.ctx_lens.tolist() == graphed.ctx_lens.tolist() == [100, 43]
+    assert graphed.error_word() == 0
+
+
+@pytest.mark.parametrize("n", [1, 20, 150, 300])
+def test_captured_chunks(n):
+    c = Case(2, 4, 1, 64, "e4m3", [500, 77], n, rot=64, cap=832, fill=False)
+    fill_cache(c)
+    c.append()
+    c.attend()
+    torch.cuda.synchronize()
+    want = c.out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append()
+        c.attend()
+        c.attend()
+    c.out.fill_(MARK)
+    for _ in range(3):
+        g.replay()
+    assert torch.equal(c.out, want) and c.error_word() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of 5.4 GB (16 loops, 1,310,720 slots): the last slots, through a window, by each kernel."""
+    L, cap = 16, 5 << 18
+    shape = rq.make_q8_shape(1, 2, 2, 64, L, cap, "e4m3")
+    cache = rq.Q8Cache(shape)
+    assert cache.codes.numel() > 1 << 32
+    cache.codes.fill_(255)
+    for n in (1, 30, 600):
+        ctx = cap - 700
+        c = Case(1, 2, 2, 64, "e4m3", [40], n, rot=64, cap=704, window=30, positions=[list(range(n))])
+        kv = torch.full((1, n, 2, L, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        kv[:, :, :, L - 1] = c.kv[:, :, :, 0]
+        lens = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+        rq.q8_append(shape, cache, kv[:, :, :, L - 1:], L - 1, lens, rope=c.rope)
+        ws = torch.empty(rq.q8_workspace_bytes(shape, n, ctx, 30, 0), dtype=torch.uint8, device="cuda")
+        out = torch.full((1, n, 2, 64), MARK, dtype=torch.bfloat16, device="cuda")
+        # slots before the new ones hold nothing: a window of 1 sees a token's own slot
+        rq.q8_attention(shape, cache, c.q, L - 1, lens, ctx, out, ws, window=1, rope=c.rope)
+        t = ctx + np.arange(n)
+        codes = cache.codes[0, :, ctx // 64:-(-(ctx + n) // 64), L - 1, 1].flatten(2).cpu().numpy()
+        scales = cache.scales[0, :, ctx // 64:-(-(ctx + n) // 64), L - 1, 1].cpu().numpy()
+        for h in (0, 1):
+            v = np.stack([R.value_of(codes[h, x // 64 - ctx // 64, R.place(x, 64)], "e4m3") *
+                          float(scales[h, x // 64 - ctx // 64, x % 64 // 16]) for x in t])
+            got = out[0, :, h].float().cpu().numpy()
+            assert (np.abs(got - v) <= 2.0 ** -8 * np.abs(v) + 2.0 ** -10 * np.abs(v) + 1e-30).all()
+        assert int(ws[:4].view(torch.int32).item()) == 0
+    del cache
+    torch.cuda.empty_cache()
+
+
+def test_sequences_in_groups():
+    """Operand tiles of more than 2 GB: sequences are handled in groups; each as it is alone, and a bad
+    length in any of them is told."""
+    B, H, ctx, n = 9, 16, 30000, 520
+    cap = 30592
+    shape, one = (rq.make_q8_shape(b, H, H, 128, 1, cap, "int8") for b in (B, 1))
+    cache = rq.Q8Cache(shape)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    cache.codes.random_(generator=g)
+    cache.scales.fill_(2.0 ** -7)
+    q = torch.randn(B, n, H, 128, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([ctx - 3000 * b for b in range(B)], dtype=torch.int32, device="cuda")
+    need = rq.q8_workspace_bytes(shape, n, ctx, 0, 0)
+    assert need > 2 << 30
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, MARK)
+    rq.q8_attention(shape, cache, q, 0, lens, ctx, out, ws)
+    assert int(ws[:4].view(torch.int32).item()) == 0
+    for b in (0, 4, 8):
+        alone = rq.Q8Cache(one, codes=cache.codes[b].reshape(-1), scales=cache.scales[b].reshape(-1))
+        got = torch.full_like(q[:1], MARK)
+        rq.q8_attention(one, alone, q[b:b + 1], 0, lens[b:b + 1].clone(), ctx, got, ws)
+        # the same products; parts joined elsewhere (fp32), results rounded to bf16
+        torch.testing.assert_close(out[b:b + 1].float(), got.float(), rtol=2.0 ** -7, atol=1e-4)
+    for b in (0, 8):
+        bad = lens.clone()
+        bad[b] = ctx + 1
+        rq.q8_attention(shape, cache, q, 0, bad, ctx, out, ws)
+        assert int(ws[:4].view(torch.int32).item()) != 0
+        assert torch.isnan(out[b].float()).all() and torch.isfinite(out[4].float()).all()
+    del cache, ws
+    torch.cuda.empty_cache()
