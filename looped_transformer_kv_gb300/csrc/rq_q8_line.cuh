@@ -33,6 +33,7 @@ struct Q8Line {
   int32_t n_ctas, n_tickets;
   int32_t clear;         // the call's first launch
   int32_t own_cut;       // each CTA cuts for itself
+  int32_t least;         // steps of a CTA
 };
 
 // The tiles of 64 slots that some new token of a sequence sees, as a list: 0 .. sink0 and then from
@@ -41,6 +42,7 @@ struct Rows {
   int ctx, n, j0, j1;      // tokens of the block's rows
   int rows;                // of the block
   int sink0, first0, tiles, end;   // the list, its length, the slot behind its last
+  int oldest;              // slots before this one are seen as sinks only
   int sink, first, V, hi;  // steps 0 .. sink and from `first` on, V in all; the slot behind the block's last
   bool ok;
   __device__ __forceinline__ int step(int u) const { return u < sink ? u : first + u - sink; }     // the u-th step's place
@@ -53,10 +55,11 @@ __device__ __forceinline__ Rows sequence_of(const Q8Line& a, int b) {
   x.n = a.c.n_lens ? a.c.n_lens[b] : a.c.n_new;
   x.ok = x.ctx >= 0 && x.ctx <= a.c.max_ctx && x.n >= 0 && x.n <= a.c.n_new && x.ctx <= a.cap - x.n;
   if (x.n < 0 || x.n > a.c.n_new) x.n = a.c.n_new;
-  x.sink0 = x.first0 = x.tiles = x.end = 0;
+  x.sink0 = x.first0 = x.tiles = x.end = x.oldest = 0;
   if (!x.ok || x.n == 0) return x;
   const int lo = a.c.window > 0 ? max(0, x.ctx + 1 - a.c.window) : 0;
   x.end = x.ctx + x.n;
+  x.oldest = lo;
   x.first0 = lo / kQ8Tile;
   x.sink0 = min((min(a.c.n_sink, lo) + kQ8Tile - 1) / kQ8Tile, x.first0);
   x.tiles = x.sink0 + (x.end + kQ8Tile - 1) / kQ8Tile - x.first0;
@@ -83,6 +86,11 @@ __device__ __forceinline__ Rows rows_of(const Q8Line& a, int b, int block) {
   x.sink = min((sinks + K - 1) / K, x.first);
   x.V = x.sink + (x.sink0 + (x.hi + kQ8Tile - 1) / kQ8Tile - x.first0 + K - 1) / K - x.first;
   return x;
+}
+
+// CTAs that share a line of N steps: `least` steps each where there are few.
+__device__ __forceinline__ int ctas_used(const Q8Line& a, int64_t N) {
+  return int(min((N + a.least - 1) / a.least, int64_t(a.n_ctas)));
 }
 
 // One CTA: clears the error word and tickets, cuts the line.
@@ -122,7 +130,7 @@ __device__ __forceinline__ void cut_line(const Q8Line& a) {
   if (tid == 0) a.prefix[pairs] = run;
   bad = __syncthreads_or(bad);                              // (and the prefix is written)
   if (bad && tid == 0) *a.err = 1u;
-  const int used = int(min(run, int64_t(a.n_ctas)));
+  const int used = ctas_used(a, run);
   if (tid == 0) *a.used = used;
   for (int i = tid; i <= used; i += THREADS) {
     const int64_t pos = used ? run * i / used : 0;
@@ -189,7 +197,7 @@ __device__ __forceinline__ bool own_cut(const Q8Line& a, OwnCut& out, int me) { 
     }
     __syncthreads();
   }
-  const int used = int(min(run, int64_t(a.n_ctas)));
+  const int used = ctas_used(a, run);
   const int64_t pos = used ? run * me / used : 0;
 #pragma unroll
   for (int k = 0; k < EACH; ++k)
@@ -313,6 +321,7 @@ inline void q8_place(Q8Line& a, const Q8Layout& x, void* ws, int n_tickets) {
   a.n_ctas = x.n_ctas;
   a.n_tickets = n_tickets;
   a.clear = 1;
+  a.least = 1;
 }
 
 }  // namespace rq

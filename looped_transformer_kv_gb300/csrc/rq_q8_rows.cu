@@ -15,8 +15,8 @@
 //
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; IMG: warp 9:
 // copies; else warps 12-15: codes from global memory (a tile ahead, in registers) to operands.
-// CTAs (one per SM) share the work by the line of rq_q8_line.cuh; the last CTA of a divided unit to
-// finish joins its partial results in order, each row tile for itself.
+// CTAs (one per SM) share the work by the line of rq_q8_line.cuh; q8_join_kernel joins the partial results
+// of divided units (in this kernel the code for it cost the main loop its registers: 460 against 375 us).
 #include <type_traits>
 
 #include "rq_q8_line.cuh"
@@ -161,13 +161,13 @@ struct Converter {
   int64_t rec[2];                                            // records of the tile's halves; -1: no page, -2: not there
   float scale;                                               // lane l < 16: block l % 8 of K (l < 8) or V
   uint32_t factor, lost;                                     // of take_scales: 2^(e - top) of the same; K's blocks to spoil
-  int v_from;                                                // V rows from here on hold nothing
+  int at[2], end, oldest;                                    // slots of the halves' first rows; what is seen
 
   // (rows of a thread's pieces differ by multiples of 16, so the chunk is the same; `first`: which half
   // is stored first, so that neighbours meet distinct banks)
   __device__ __forceinline__ Converter(const Q8Line& line, int t, int l)
       : a(line), tid(t), lane(l), row0(t / CPR), c((t % CPR) ^ q8_swizzle<D>(t / CPR)),
-        first(D == 128 && c >= 4 ? 1 : 0), panel(uint32_t(c / 4) * (kKeys * 128)), scale(1.f), factor(0u), lost(0u), v_from(0) {}
+        first(D == 128 && c >= 4 ? 1 : 0), panel(uint32_t(c / 4) * (kKeys * 128)), scale(1.f), factor(0u), lost(0u) {}
 
   __device__ __forceinline__ int64_t record(const Rows& x, int b, int h, int v) const {
     if (v >= x.tiles) return -2;
@@ -193,8 +193,12 @@ struct Converter {
   __device__ __forceinline__ int2 take_scales(const Rows& x, int v) {
     const int half = lane >> 2 & 1;
     const int64_t r = half ? rec[1] : rec[0];
-    const int left = v + half < x.tiles ? x.end - x.tile(v + half) * kQ8Tile : 0;   // slots of the half that hold something
-    const bool live = r >= 0 && (lane & 3) * kQ8Block < left && lane < 16;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) at[k] = v + k < x.tiles ? x.tile(v + k) * kQ8Tile : 1 << 30;   // (not there: behind the end)
+    end = x.end;
+    oldest = x.oldest;
+    const int first = (half ? at[1] : at[0]) + (lane & 3) * kQ8Block;          // the block's first slot
+    const bool live = r >= 0 && lane < 16 && first < end && (first + kQ8Block > oldest || first < a.c.n_sink);
     const bool nan = live && !(scale < INFINITY);
     const int e = live && !nan ? q8_exponent(scale) : -1000;
     int top = e;
@@ -206,9 +210,6 @@ struct Converter {
     // that see the block)
     const uint32_t nans = __ballot_sync(RQ_FULL_MASK, nan || (r == -1 && lane < 16));
     lost = (nans | (nans >> 8)) & 255u;
-    // rows that hold something: the first half is full if there is a second
-    const int left0 = __shfl_sync(RQ_FULL_MASK, left, 0), left1 = __shfl_sync(RQ_FULL_MASK, left, 4);
-    v_from = v + 1 < x.tiles ? kQ8Tile + min(left1, kQ8Tile) : min(left0, kQ8Tile);
     return make_int2(__shfl_sync(RQ_FULL_MASK, top, 0), __shfl_sync(RQ_FULL_MASK, top, 8));
   }
   // Operands of K or V.
@@ -227,7 +228,10 @@ struct Converter {
         o[2 * k] = scaled_pair<FMT, 0>(y, f, bias);
         o[2 * k + 1] = scaled_pair<FMT, 1>(y, f, bias);
       }
-      const bool spoil = kv == 0 && (lost >> blk & 1u), none = kv == 1 && row >= v_from;
+      // (slots that no token sees may hold anything, in V codes that are not numbers too)
+      const int slot = (row < kQ8Tile ? at[0] : at[1]) + row % kQ8Tile;
+      const bool spoil = kv == 0 && (lost >> blk & 1u);
+      const bool none = kv == 1 && (slot >= end || (slot < oldest && slot >= a.c.n_sink));
       if (spoil || none)
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = none ? 0u : 0x7fff7fffu;
@@ -292,9 +296,31 @@ __device__ __forceinline__ const int2* image_exps(const RowsArgs& a, const W& w,
                                        2 * RowsSmem<D>::kTile);
 }
 
+// Place of 8 channels of a row among a row tile's results on their way out.
+template <int D>
+__device__ __forceinline__ int result_place(int r, int chunk) {
+  return r * (D * 2) + ((chunk ^ (r & (D / 8 - 1))) << 4);
+}
+__device__ __forceinline__ uint4 bf16_row(const float (&v)[8], float inv) {
+  uint32_t p[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 u = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+    p[k] = *reinterpret_cast<const uint32_t*>(&u);
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+// A divided unit: its first row, the CTAs that share it.  By the CTA where it begins; no rows: none does.
+struct Parted {
+  int b, h, r0, rows, first, last, pad[2];
+};
+constexpr int kTickets = sizeof(Parted) / 4;                // (they lie where other kernels count)
+
 template <int D, int FMT, bool IMG>
 __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
+  grid_next();
   const int me = int(blockIdx.x);
   if (me >= *a.used) return;
   extern __shared__ uint8_t raw[];
@@ -313,7 +339,6 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   auto pready = [&](int i, int half) { return bar0 + 8 * (15 + 2 * i + half); };
   const uint32_t qready = bar0 + 8 * 19, drained = bar0 + 8 * 20;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 21);
-  int* const last_one = reinterpret_cast<int*>(bars + 22);  // [row tile]
   int2* const exps = reinterpret_cast<int2*>(smem + L::exps);        // [8] of tiles: K's, V's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -680,12 +705,14 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       // ---- results (a wait that gave up: NaN)
       const float nan = __int_as_float(0x7fc00000);
       const bool there = x.ok && !failed;                      // O holds the segment's sums
-      bool whole = w.kt0 == 0 && w.T == x.V;
-      int from_cta = 0, to_cta = 0;
+      const bool whole = w.kt0 == 0 && w.T == x.V;
+      const bool valid = i * kRowTile + r < x.rows;
       if (!whole) {
-        const int64_t at = 2 * int64_t(me) + (w.kt0 == 0 ? 1 : 0);
-        float* const part = a.part + (at * kBlockRows + i * kRowTile) * D;      // [D / 4][128 rows][4]
-        stats[at * kBlockRows + i * kRowTile + r] = make_float4(R * c, h, there ? l : nan, 0.f);
+        int first, last;
+        w.sharers(a.prefix[int64_t(a.B) * a.blocks], *a.used, first, last);
+        const int64_t at = (2 * int64_t(me) + (w.kt0 == 0)) * kBlockRows + i * kRowTile;
+        float* const part = a.part + at * D;                   // [D / 4][128 rows][4]
+        stats[at + r] = make_float4(R * c, h, there ? l : nan, 0.f);
 #pragma unroll 1
         for (int y = 0; y < D / 32; ++y) {
           uint32_t o[32];
@@ -695,90 +722,44 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
             tc_ld32(tO + 32 * y, o);
             tc_wait_ld();
           }
+          if (!valid) continue;
 #pragma unroll
           for (int z = 0; z < 8; ++z)
             *reinterpret_cast<uint4*>(part + ((8 * y + z) * kRowTile + r) * 4) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
-        w.sharers(a.prefix[int64_t(a.B) * a.blocks], *a.used, from_cta, to_cta);
-        __threadfence();
-        group_sync(i);
-        if (r == 0) last_one[i] = atomicAdd(a.tickets + 2 * from_cta + i, 1u) == unsigned(to_cta - from_cta);
-        group_sync(i);
-        if (last_one[i] == 0) {
-          tc_fence_before();
-          continue;
-        }
-        __threadfence();
-        // a part's weights are in units of 2^(st.x + st.y); nothing seen: st.x is -inf, st.z 0
-        float M = -INFINITY, H = 0.f;
-        for (int k = from_cta; k <= to_cta; ++k) {
-          const float4 st = __ldcg(&stats[(2 * int64_t(k) + (k == from_cta)) * kBlockRows + i * kRowTile + r]);
-          if (M == -INFINITY || (st.x - M) + (st.y - H) > 0.f) {
-            M = st.x;
-            H = st.y;
-          }
-        }
-        l = 0.f;
-        for (int k = from_cta; k <= to_cta; ++k) {
-          const float4 st = __ldcg(&stats[(2 * int64_t(k) + (k == from_cta)) * kBlockRows + i * kRowTile + r]);
-          l += st.z * (st.x == -INFINITY ? 0.f : ex2((st.x - M) + (st.y - H)));
-        }
-        R = M;
-        h = H;
+        if (i == 0 && r == 0 && w.kt0 == 0)                     // (told by the CTA where the unit begins)
+          reinterpret_cast<Parted*>(a.tickets)[me] = {w.b, w.h, w.block * kBlockRows, x.rows, first, last, {0, 0}};
+        tc_fence_before();
+        continue;
       }
       constexpr int CR = D / 8;                                // 16-byte chunks of a row of bf16
       const float inv = there ? (l == 0.f ? 0.f : 1.f / l) : nan;
 #pragma unroll 1
       for (int y = 0; y < D / 32; ++y) {
-        float o[32];
-        if (whole) {
-          uint32_t u[32];
+        uint32_t o[32];
 #pragma unroll
-          for (int z = 0; z < 32; ++z) u[z] = 0u;
-          if (there) {
-            tc_ld32(tO + 32 * y, u);
-            tc_wait_ld();
-          }
-#pragma unroll
-          for (int z = 0; z < 32; ++z) o[z] = __uint_as_float(u[z]);
-        } else {
-#pragma unroll
-          for (int z = 0; z < 32; ++z) o[z] = 0.f;
-          for (int k = from_cta; k <= to_cta; ++k) {
-            const int64_t at = 2 * int64_t(k) + (k == from_cta);
-            const float4 st = __ldcg(&stats[at * kBlockRows + i * kRowTile + r]);
-            const float f = st.x == -INFINITY ? 0.f : ex2((st.x - R) + (st.y - h));
-            const float* const part = a.part + (at * kBlockRows + i * kRowTile) * D;
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const float4 u = __ldcg(reinterpret_cast<const float4*>(part + ((8 * y + z) * kRowTile + r) * 4));
-              o[4 * z] = fmaf(f, u.x, o[4 * z]);
-              o[4 * z + 1] = fmaf(f, u.y, o[4 * z + 1]);
-              o[4 * z + 2] = fmaf(f, u.z, o[4 * z + 2]);
-              o[4 * z + 3] = fmaf(f, u.w, o[4 * z + 3]);
-            }
-          }
+        for (int z = 0; z < 32; ++z) o[z] = 0u;
+        if (there) {
+          tc_ld32(tO + 32 * y, o);
+          tc_wait_ld();
         }
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          uint32_t p[4];
+          float v[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 u = __floats2bfloat162_rn(o[8 * z + 2 * k] * inv, o[8 * z + 2 * k + 1] * inv);
-            p[k] = *reinterpret_cast<const uint32_t*>(&u);
-          }
-          *reinterpret_cast<uint4*>(img + r * (D * 2) + (((4 * y + z) ^ (r & (CR - 1))) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+          for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[8 * z + k]);
+          *reinterpret_cast<uint4*>(img + result_place<D>(r, 4 * y + z)) = bf16_row(v, inv);
         }
       }
       __syncwarp();
       const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
       // place of the row that this lane stands for (the rows of the warp in turn, below)
       const int j = row / a.G, hq = w.h * a.G + row % a.G;
-      const int64_t place = ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D;
+      const int64_t out_row = ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D;
 #pragma unroll 4
       for (int k = lane; k < 32 * CR; k += 32) {               // this warp's rows, 16 bytes a lane
         const int rr = (warp & 3) * 32 + k / CR, cc = k % CR;
-        uint16_t* const o = a.c.out + __shfl_sync(RQ_FULL_MASK, place, k / CR) + 8 * cc;
+        uint16_t* const o = a.c.out + __shfl_sync(RQ_FULL_MASK, out_row, k / CR) + 8 * cc;
         if (i * kRowTile + rr >= x.rows) continue;
         const uint4 u = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
         if (vec) {
@@ -804,6 +785,80 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   if (warp == 8) tc_free(tmem, 512);
 }
 
+// The divided units: a CTA joins 32 rows of one, a thread 16 channels of a row, its parts in order and the
+// loads of four at a time.  A part's weights are in units of 2^(st.x + st.y), its sum is st.z; nothing
+// seen: st.x is -inf.
+template <int D>
+__global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ RowsArgs a) {
+  grid_wait();
+  const Parted u = reinterpret_cast<const Parted*>(a.tickets)[blockIdx.x];
+  const int row = int(blockIdx.y) * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  if (row >= u.rows) return;
+  const float4* const stats = reinterpret_cast<const float4*>(a.stats);
+  const int tile = row / kRowTile * kRowTile, r = row % kRowTile;
+  auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kBlockRows + tile; };
+  float M = -INFINITY, h = 0.f, sum = 0.f, o[16];
+#pragma unroll
+  for (int z = 0; z < 16; ++z) o[z] = 0.f;
+  for (int k = u.first; k <= u.last; k += 4) {
+    float4 st[4], v[4][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      st[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (k + e > u.last) continue;
+      st[e] = stats[place(k + e) + r];
+      const float4* const part = reinterpret_cast<const float4*>(a.part + place(k + e) * D) + 4 * y * kRowTile + r;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) v[e][z] = part[z * kRowTile];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (k + e > u.last) continue;
+      float f = 1.f, f0 = 1.f;                               // of this part, and of those before
+      if (st[e].x == -INFINITY) {
+        f = 0.f;
+      } else {
+        const float d = M == -INFINITY ? 1.f : (st[e].x - M) + (st[e].y - h);
+        if (!(d <= 0.f)) {
+          f0 = M == -INFINITY ? 0.f : ex2(-d);
+          M = st[e].x;
+          h = st[e].y;
+        } else {
+          f = ex2(d);
+        }
+      }
+      sum = fmaf(f, st[e].z, sum * f0);                      // (a part that gave up is NaN)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        o[4 * z] = fmaf(f, v[e][z].x, o[4 * z] * f0);
+        o[4 * z + 1] = fmaf(f, v[e][z].y, o[4 * z + 1] * f0);
+        o[4 * z + 2] = fmaf(f, v[e][z].z, o[4 * z + 2] * f0);
+        o[4 * z + 3] = fmaf(f, v[e][z].w, o[4 * z + 3] * f0);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int j = (u.r0 + row) / a.G, hq = u.h * a.G + (u.r0 + row) % a.G;
+  uint16_t* const to = a.c.out + ((int64_t(u.b) * a.c.n_new + j) * a.Hq + hq) * D + 16 * y;
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    float w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = o[8 * z + k];
+    const uint4 q = bf16_row(w, inv);
+    if ((reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0) {
+      *reinterpret_cast<uint4*>(to + 8 * z) = q;
+    } else {
+      const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        to[8 * z + 2 * k] = uint16_t(p[k]);
+        to[8 * z + 2 * k + 1] = uint16_t(p[k] >> 16);
+      }
+    }
+  }
+}
+
 // Bytes of the operand tiles of one sequence, and of one unit's list.
 template <typename Shape>
 int rows_list(const Shape& s, int n_new, int max_ctx, int window, int n_sink) {
@@ -827,7 +882,7 @@ constexpr int kImageBlocks = 3;
 
 RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
   RowsPlan p = {};
-  p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), 2);
+  p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), kTickets);
   p.total = p.line.total;
   const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
   p.by_images = rows > (kImageBlocks - 1) * kBlockRows;
@@ -859,7 +914,10 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * unsigned(a.list)), 256, 0, stream, a)) != cudaSuccess)
     return e;
-  return launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a);
+  if ((e = launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a)) != cudaSuccess)
+    return e;
+  const int rows = int(std::min<int64_t>(kBlockRows, int64_t(a.c.n_new) * a.G));
+  return launch_after(true, q8_join_kernel<D>, dim3(unsigned(a.n_ctas), unsigned((rows + 31) / 32)), 2 * D, 0, stream, a);
 }
 
 template <int D, int FMT>
@@ -878,7 +936,8 @@ cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const
   const RowsPlan p = rows_plan(s, c.n_new, c.max_ctx, c.window, c.n_sink);
   RowsArgs a = {};
   static_cast<Q8Line&>(a) = q8_line(s, cache, paging, c, kBlockRows);
-  q8_place(a, p.line, ws, 2);
+  q8_place(a, p.line, ws, kTickets);
+  a.least = 2;
   a.images = static_cast<uint8_t*>(ws) + p.line.total;
   a.list = p.list;
   a.row_tiles = p.row_tiles;

@@ -21,6 +21,7 @@ constexpr float kTop = 8.f;
 constexpr int kScaleTop = 7, kScaleHead = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
+constexpr int kJoin = 16;             // parts joined at once
 
 // A divided unit: its rows, the CTAs that share it.
 struct Parted {
@@ -46,13 +47,14 @@ struct StreamSmem {
   static_assert(2 * sizeof(Parted) <= 64 && kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // CH channels of a unit's row y, times inv.
 template <int D, int CH>
@@ -79,51 +81,91 @@ __device__ __forceinline__ void store_row(const Q8Line& a, int b, int h, int r0,
     }
 }
 
-// The parts of a divided unit in their order, the loads of four at a time.
+// Parts of CTAs k0, k0 + stride .. <= k1 of a divided unit joined, by 128 threads: 16 a row (CH channels
+// each), the eight groups on eight rows, or on parts of fewer rows; each takes its parts in order, the
+// loads of two or four at a time.  Into the first one's place (`last` false), or out.
 template <int D, int NT>
-__device__ __forceinline__ void join_parts(const Q8Line& a, const Parted& u, int row, int ch) {
-  constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = 4;
+__device__ __forceinline__ void join_parts(const Q8Line& a, const Parted& u, int k0, int k1, int stride, bool last, float* buffer) {
+  constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = NT > 1 ? 4 : 2, kRow = D + 2;
+  const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;
+  const int rows = u.rows > 4 ? 8 : u.rows > 2 ? 4 : u.rows, groups = 8 / rows;   // at a time; groups of a row
+  auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kRows; };
 #pragma unroll 1
-  for (int y = row; y < u.rows; y += 8) {
+  for (int y0 = 0; y0 < u.rows; y0 += rows) {
+    const int y = y0 + group % rows, mine = group / rows;
     float M = kNoMax, sum = 0.f, o[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) o[k] = 0.f;
 #pragma unroll 1
-    for (int k0 = u.first; k0 <= u.last; k0 += TOGETHER) {
+    for (int k = k0 + mine * stride; y < u.rows && mine < groups && k <= k1; k += TOGETHER * groups * stride) {
       float2 st[TOGETHER];
       float4 v[TOGETHER][CH / 4];
 #pragma unroll
-      for (int k = 0; k < TOGETHER; ++k) {
-        st[k] = make_float2(kNoMax, 0.f);
-        if (k0 + k > u.last) continue;
-        const int64_t at = (2 * int64_t(k0 + k) + (k0 + k == u.first)) * kRows + y;
-        st[k] = __ldcg(&a.stats[at]);
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int ki = k + i * groups * stride;
+        st[i] = make_float2(kNoMax, 0.f);
+        if (ki > k1) continue;
+        st[i] = __ldcg(&a.stats[place(ki) + y]);
 #pragma unroll
-        for (int z = 0; z < CH / 4; ++z) v[k][z] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + ch) + z);
+        for (int z = 0; z < CH / 4; ++z) v[i][z] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(ki) + y) * D + ch) + z);
       }
       float to = M;
 #pragma unroll
-      for (int k = 0; k < TOGETHER; ++k) to = fmaxf(to, st[k].x);
+      for (int i = 0; i < TOGETHER; ++i) to = fmaxf(to, st[i].x);
       const float f0 = ex2(M - to);
       M = to;
       sum *= f0;
 #pragma unroll
       for (int z = 0; z < CH; ++z) o[z] *= f0;
 #pragma unroll
-      for (int k = 0; k < TOGETHER; ++k) {
-        if (k0 + k > u.last) continue;
-        const float f = ex2(st[k].x - M);
-        sum += f * st[k].y;
+      for (int i = 0; i < TOGETHER; ++i) {
+        if (k + i * groups * stride > k1) continue;
+        const float f = ex2(st[i].x - M);
+        sum += f * st[i].y;
 #pragma unroll
         for (int z = 0; z < CH / 4; ++z) {
-          o[4 * z] = fmaf(f, v[k][z].x, o[4 * z]);
-          o[4 * z + 1] = fmaf(f, v[k][z].y, o[4 * z + 1]);
-          o[4 * z + 2] = fmaf(f, v[k][z].z, o[4 * z + 2]);
-          o[4 * z + 3] = fmaf(f, v[k][z].w, o[4 * z + 3]);
+          o[4 * z] = fmaf(f, v[i][z].x, o[4 * z]);
+          o[4 * z + 1] = fmaf(f, v[i][z].y, o[4 * z + 1]);
+          o[4 * z + 2] = fmaf(f, v[i][z].z, o[4 * z + 2]);
+          o[4 * z + 3] = fmaf(f, v[i][z].w, o[4 * z + 3]);
         }
       }
     }
-    store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (groups > 1) {                                       // the groups of a row, in order
+      float* const at = buffer + group * kRow;
+#pragma unroll
+      for (int z = 0; z < CH; ++z) at[2 + ch + z] = o[z];
+      if (ch == 0) {
+        at[0] = M;
+        at[1] = sum;
+      }
+      consumers_sync();
+      if (mine == 0) {
+        float to = kNoMax;
+        for (int i = 0; i < groups; ++i) to = fmaxf(to, buffer[(group + i * rows) * kRow]);
+        M = to;
+        sum = 0.f;
+#pragma unroll
+        for (int z = 0; z < CH; ++z) o[z] = 0.f;
+        for (int i = 0; i < groups; ++i) {
+          const float* const from = buffer + (group + i * rows) * kRow;
+          const float f = ex2(from[0] - M);
+          sum += f * from[1];
+#pragma unroll
+          for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[2 + ch + z], o[z]);
+        }
+      }
+    }
+    consumers_sync();                                       // (every part of these rows is read)
+    if (mine != 0 || y >= u.rows) continue;
+    if (last) {
+      store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+    } else {
+      float* const p = a.part + (place(k0) + y) * D + ch;
+#pragma unroll
+      for (int z = 0; z < CH; z += 4) *reinterpret_cast<float4*>(p + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+      if (ch == 0) a.stats[place(k0) + y] = make_float2(M, sum);
+    }
   }
 }
 
@@ -432,8 +474,9 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
                 v[k][0] = u.x;
                 v[k][1] = u.y;
               }
-              // slots behind the last new token may hold anything (a code that is not a number, too)
-              if (slot0 + 15 >= x.hi && slot0 - 16 * warp + row >= x.hi)
+              // slots that no row sees may hold anything (a code that is not a number, too)
+              const int slot = slot0 - 16 * warp + row;
+              if (!clear && (slot >= x.hi || (slot < oldest && slot >= a.c.n_sink)))
 #pragma unroll
                 for (int i = 0; i < W; ++i) v[k][i] = 0u;
 #pragma unroll
@@ -513,17 +556,35 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
     // ---- divided units, at most two: the last of their CTAs joins the parts
     grid_wait();
     if (parted[0].is || parted[1].is) {
+      // units of many CTAs: kJoin neighbours are joined first, by the last of them
       __threadfence();
       consumers_sync();
       if (threadIdx.x < 2) {
         const Parted& p = parted[threadIdx.x];
-        misc[1 + threadIdx.x] = p.is && atomicAdd(a.tickets + p.first, 1u) == unsigned(p.last - p.first);
+        const bool many = p.last - p.first >= kJoin;
+        const int k0 = many ? p.first + (me - p.first) / kJoin * kJoin : p.first, k1 = many ? min(k0 + kJoin - 1, p.last) : p.last;
+        misc[1 + threadIdx.x] = p.is && atomicAdd(a.tickets + (many ? a.n_ctas : 0) + k0, 1u) == unsigned(k1 - k0);
       }
       consumers_sync();
       __threadfence();
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k)
-        if (misc[1 + k]) join_parts<D, NT>(a, parted[k], threadIdx.x >> 4, (threadIdx.x & 15) * CH);
+      for (int k = 0; k < 2; ++k) {
+        if (!misc[1 + k]) continue;
+        const Parted& p = parted[k];
+        if (p.last - p.first >= kJoin) {
+          const int k0 = p.first + (me - p.first) / kJoin * kJoin;
+          join_parts<D, NT>(a, p, k0, min(k0 + kJoin - 1, p.last), 1, false, merge);
+          __threadfence();
+          consumers_sync();
+          if (threadIdx.x == 0) misc[3] = atomicAdd(a.tickets + p.first, 1u) == unsigned((p.last - p.first) / kJoin);
+          consumers_sync();
+          if (!misc[3]) continue;
+          __threadfence();
+          join_parts<D, NT>(a, p, p.first, p.last, kJoin, true, merge);
+        } else {
+          join_parts<D, NT>(a, p, p.first, p.last, 1, true, merge);
+        }
+      }
     }
     if (dead && lane == 0) atomicOr(a.err, 1u);
   }
@@ -541,7 +602,7 @@ __global__ void __launch_bounds__(256) q8_clear_kernel(unsigned* err, unsigned* 
 int tiles_of_rows(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 Q8Layout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx, int nt) {
-  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), 1);
+  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), 2);
 }
 
 template <int D, int NT, int FMT>
@@ -553,7 +614,7 @@ cudaError_t launch(const Q8Line& a, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   if (a.own_cut)
-    q8_clear_kernel<<<1, 256, 0, stream>>>(a.err, a.tickets, a.n_ctas);
+    q8_clear_kernel<<<1, 256, 0, stream>>>(a.err, a.tickets, 2 * a.n_ctas);
   else
     q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -570,7 +631,7 @@ cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, con
                              const Q8Call& c, void* ws, cudaStream_t stream) {
   const int nt = tiles_of_rows(int64_t(c.n_new) * (s.n_q_heads / s.n_kv_heads));
   Q8Line a = q8_line(s, cache, paging, c, 8 * nt);
-  q8_place(a, stream_layout(s, c.n_new, c.max_ctx, nt), ws, 1);
+  q8_place(a, stream_layout(s, c.n_new, c.max_ctx, nt), ws, 2);
   a.own_cut = int64_t(a.B) * a.blocks <= kOwnCutPairs;
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
   switch (nt) {

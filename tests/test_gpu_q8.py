@@ -229,7 +229,7 @@ def test_append_token_by_token(fmt, d):
         c.append(kv=kv.cuda())
         c.append_reference()
         c.same_cache()
-        rq.advance_ctx(c.ctx_lens, 1, c.cap)
+        advance_ctx(c.ctx_lens, 1, c.cap)
         c.ctx = [x + 1 for x in c.ctx]
 
 
