@@ -10,11 +10,11 @@
 // so that tiles of different scales need no rescaling of O.  R (a row's largest score, raw) and h are
 // raised when a weight would exceed 2^15, to make the largest 2^7.
 //
-// Many blocks of rows share a tile: its operands are then made once, in the workspace
-// (q8_image_kernel), and copied from there (IMG); else each block converts what it reads.
+// The operands are made once, in the workspace (q8_query_kernel, q8_image_kernel), and copied from there.
+// (A kernel that converted what it read, without the workspace, was slower from 33 rows on: its loads and
+// conversions took registers from the softmax, 67 against 33 us for 260 rows after 500 slots.)
 //
-// Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; IMG: warp 9:
-// copies; else warps 12-15: codes from global memory (a tile ahead, in registers) to operands.
+// Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; warp 9: copies.
 // CTAs (one per SM) share the work by the line of rq_q8_line.cuh; q8_join_kernel joins the partial results
 // of divided units (in this kernel the code for it cost the main loop its registers: 460 against 375 us).
 #include <type_traits>
@@ -33,9 +33,8 @@ using RowWalk = Walk<kBlockRows, kKeys>;
 template <int D>
 struct RowsSmem {
   static constexpr int kTile = kKeys * D * 2;               // one K, V or Q tile
-  static constexpr int v = 0, k = 2 * kTile, q = 5 * kTile, exps = 7 * kTile;   // V first: see v_desc
-  static constexpr int row_exps = exps + 64;                // [8] K's and V's exponent of a tile
-  static constexpr int bars = row_exps + kBlockRows * 4, walks = bars + 256;
+  static constexpr int v = 0, k = 2 * kTile, q = 5 * kTile;   // V first: see v_desc
+  static constexpr int bars = 7 * kTile, walks = bars + 256;
   static constexpr int kImage = 2 * kTile + 128, kQueryImage = kTile + 4 * kRowTile;   // of tiles in the workspace
   static constexpr int total = walks + 4 * int(sizeof(RowWalk)) + 1024;   // + alignment of the base
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
@@ -317,8 +316,8 @@ struct Parted {
 };
 constexpr int kTickets = sizeof(Parted) / 4;                // (they lie where other kernels count)
 
-template <int D, int FMT, bool IMG>
-__global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __grid_constant__ RowsArgs a) {
+template <int D>
+__global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
   grid_next();
   const int me = int(blockIdx.x);
@@ -339,15 +338,14 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   auto pready = [&](int i, int half) { return bar0 + 8 * (15 + 2 * i + half); };
   const uint32_t qready = bar0 + 8 * 19, drained = bar0 + 8 * 20;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 21);
-  int2* const exps = reinterpret_cast<int2*>(smem + L::exps);        // [8] of tiles: K's, V's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 8) tc_alloc(smem_u32(tslot), 512);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 5; ++i) mbar_init(bar0 + 8 * i, IMG ? 1 : 128);
+    for (int i = 0; i < 5; ++i) mbar_init(bar0 + 8 * i, 1);
     for (int i = 5; i < 15; ++i) mbar_init(bar0 + 8 * i, 1);
     for (int i = 15; i < 19; ++i) mbar_init(bar0 + 8 * i, kRowTile);
-    mbar_init(qready, IMG ? 2 : kBlockRows);
+    mbar_init(qready, 2);
     mbar_init(drained, 1);
     fence_mbar_init();
   }
@@ -360,71 +358,14 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
   RowWalk* const walks = reinterpret_cast<RowWalk*>(smem + L::walks);           // of the softmax groups, products, copies
   bool failed = false;
 
-  if (!IMG && warp >= 12) {                                  // ---- codes to operands
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    RowWalk w;
-    w.begin(from, to_pos);
-    Converter<D, FMT> to(a, threadIdx.x - 384, lane);
-    constexpr int PIECES = Converter<D, FMT>::PIECES;
-    int g = 0, n0 = 0;                                       // tiles so far; g's step is n0 + g
-    int sk[3] = {-1, -1, -1};                                // steps that end with K tile g - 1, g - 2, g - 3
-    while (!failed && w.next(a)) {
-      const Rows& x = w.x;
-      if (!x.ok) continue;
-      uint4 kreg[PIECES], vreg[PIECES];
-      int64_t rec32 = -2;                                    // a lane's of 16 steps
-      auto load_records = [&](int t) {
-        const int u = t + lane / 2;
-        rec32 = u < w.T ? to.record(x, w.b, w.h, 2 * x.step(w.kt0 + u) + (lane & 1)) : -2;
-      };
-      auto aim = [&](int t) {
-        to.rec[0] = __shfl_sync(RQ_FULL_MASK, rec32, 2 * t & 31);
-        to.rec[1] = __shfl_sync(RQ_FULL_MASK, rec32, (2 * t + 1) & 31);
-      };
-      // K runs up to three tiles ahead of the scores, V one behind K: K0 V0 K1 V1 ...
-      load_records(0);
-      aim(0);
-      to.load(kreg, 0);
-      to.load_scales();
-      to.load(vreg, 1);
-      for (int t = 0; t < w.T; ++t, ++g) {
-        // scores of tile g - 3 done: K's place
-        if (g >= 3) failed = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(step(sk[2]), (sk[2] >> 3) & 1, kWaitNs));
-        if (failed) break;
-        const int2 e = to.take_scales(x, 2 * x.step(w.kt0 + t));
-        if (to.tid == 0) exps[g & 7] = e;
-        to.put(kreg, smem + L::k + (g % 3) * L::kTile, 0);
-        fence_async_smem();
-        mbar_arrive(kfull(g));
-        if (t + 1 < w.T) {
-          if (((t + 1) & 15) == 0) load_records(t + 1);
-          aim(t + 1);
-          to.load(kreg, 0);
-          to.load_scales();
-        }
-        // values of tile g - 2 done (the step after its scores'): V's place
-        if (g >= 2) failed = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(step(sk[1] + 1), ((sk[1] + 1) >> 3) & 1, kWaitNs));
-        if (failed) break;
-        to.put(vreg, smem + L::v + (g & 1) * L::kTile, 1);
-        fence_async_smem();
-        mbar_arrive(vfull(g));
-        if (t + 1 < w.T) to.load(vreg, 1);
-        sk[2] = sk[1];
-        sk[1] = sk[0];
-        sk[0] = n0 + g;
-      }
-      ++n0;
-    }
-  } else if (warp >= 8) {
-    if constexpr (IMG)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const bool leader = elect_one();
-    if (IMG && warp == 9 && leader) {                        // ---- copies of operand tiles
+    if (warp == 9 && leader) {                        // ---- copies of operand tiles
       RowWalk& w = walks[3];
       w.begin(from, to_pos);
-      int g = 0, n0 = 0, sk[3] = {-1, -1, -1};               // as the converting warps'
+      int g = 0, n0 = 0;                                     // tiles so far; g's step is n0 + g
+      int sk[3] = {-1, -1, -1};                              // steps that end with K tile g - 1, g - 2, g - 3
       while (!failed && w.next(a)) {
         if (!w.x.ok) continue;
         const uint8_t* const unit = a.images + (int64_t(w.b) * a.v.H + w.h) * a.list * RowsSmem<D>::kImage;
@@ -514,14 +455,10 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
     }
     __syncwarp();
   } else {                                                   // ---- softmax
-    if constexpr (IMG)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int i = warp >> 2, r = threadIdx.x & (kRowTile - 1);
     const uint32_t lanes = uint32_t(warp & 3) << 21;          // this warp's tensor-memory lanes
     const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
-    float* const row_scale = reinterpret_cast<float*>(smem + L::row_exps) + i * kRowTile;
     uint8_t* const img = smem + L::q + i * L::kTile;          // queries, then results going out
     float4* const stats = reinterpret_cast<float4*>(a.stats);
     int g = 0, n0 = 0, s0 = 0;
@@ -536,25 +473,15 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       const int r0 = w.block * kBlockRows + i * kRowTile;      // the row tile's first row
       const bool two = x.rows > kRowTile, mine = i == 0 || two;
       const int row = r0 + r;
-      // ---- queries: operands, 32 rows a warp, or their copy
+      // ---- queries
       float factor = 0.f;
       if (x.ok && !failed) {
-        if constexpr (IMG) {
-          const uint8_t* const image = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + r0 / kRowTile) * L::kQueryImage;
-          if (r == 0) {
-            mbar_arrive_expect_tx(qready, mine ? L::kTile : 0);
-            if (mine) bulk_g2s(smem_u32(img), image, L::kTile, qready);
-          }
-          if (mine) factor = *reinterpret_cast<const float*>(image + L::kTile + 4 * r);
-        } else {
-          if (mine) {
-            put_queries<D, 32>(a, x, w.b, w.h, r0, (warp & 3) * 32, x.rows - i * kRowTile, img, row_scale, lane);
-            __syncwarp();
-            factor = row_scale[r];
-          }
-          fence_async_smem();
-          mbar_arrive(qready);
+        const uint8_t* const image = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + r0 / kRowTile) * L::kQueryImage;
+        if (r == 0) {
+          mbar_arrive_expect_tx(qready, mine ? L::kTile : 0);
+          if (mine) bulk_g2s(smem_u32(img), image, L::kTile, qready);
         }
+        if (mine) factor = *reinterpret_cast<const float*>(image + L::kTile + 4 * r);
       }
       // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
       // of any size cancel without a residue
@@ -574,15 +501,12 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
         const int own = x.ctx + min(row / a.G, x.n - 1);       // the row's own slot
         const int own0 = x.ctx + r0 / a.G, own1 = x.ctx + min((r0 + kRowTile - 1) / a.G, x.j1);   // of the tile's rows
         const int win = a.c.window > 0 ? a.c.window : 1 << 30, sinks = a.c.window > 0 ? a.c.n_sink : 0;
-        int2 ee32 = make_int2(0, 0);                           // (IMG) a lane's exponents of 32 tiles
+        int2 ee32 = make_int2(0, 0);                           // a lane's exponents of 32 tiles
         bool huge = false;                                     // scores beyond 2^20 in some row of the warp
         for (int t = 0; t < w.T; ++t, ++g) {
           // ---- before the scores are there: the tile's exponents, and what of it the warp's rows see
-          int2 ee = make_int2(0, 0);
-          if constexpr (IMG) {
-            if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
-            ee = make_int2(__shfl_sync(RQ_FULL_MASK, ee32.x, t & 31), __shfl_sync(RQ_FULL_MASK, ee32.y, t & 31));
-          }
+          if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
+          const int2 ee = make_int2(__shfl_sync(RQ_FULL_MASK, ee32.x, t & 31), __shfl_sync(RQ_FULL_MASK, ee32.y, t & 31));
           int at[2];
           bool clear[2];
 #pragma unroll
@@ -607,7 +531,6 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
           uint32_t s[kKeys];
 #pragma unroll
           for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
-          if constexpr (!IMG) ee = exps[g & 7];
           const float ke = q8_pow2(max(min(ee.x, 127), -126)), ev = float(ee.y);
           tc_wait_ld();
 #pragma unroll
@@ -775,7 +698,7 @@ __global__ void __launch_bounds__(IMG ? 384 : 512, 1) q8_rows_kernel(const __gri
       }
       // (the next queries overwrite the rows; the copy's are the other proxy's)
       // (the walk's first barrier follows)
-      if constexpr (IMG) fence_async_smem();
+      fence_async_smem();
       tc_fence_before();
     }
   }
@@ -870,24 +793,18 @@ int rows_list(const Shape& s, int n_new, int max_ctx, int window, int n_sink) {
 
 struct RowsPlan {
   Q8Layout line;
-  bool by_images;
   int list, row_tiles, group;   // sequences handled together
   size_t images, queries;       // bytes of a sequence's operand tiles
   size_t total;
 };
 
 constexpr size_t kGroupBytes = size_t(2) << 30;   // operand tiles of the sequences handled together
-// Blocks of rows from which the operand tiles are made once in the workspace.
-constexpr int kImageBlocks = 3;
 
 RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
   RowsPlan p = {};
   p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), kTickets);
   p.total = p.line.total;
   const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
-  p.by_images = rows > (kImageBlocks - 1) * kBlockRows;
-  p.group = s.batch;
-  if (!p.by_images) return p;
   p.list = rows_list(s, n_new, max_ctx, window, n_sink);
   p.row_tiles = int((rows + kRowTile - 1) / kRowTile);
   const bool wide = s.head_dim == 128;
@@ -899,30 +816,21 @@ RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int
   return p;
 }
 
-template <int D, int FMT, bool IMG>
+template <int D, int FMT>
 cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
   using L = RowsSmem<D>;
   static OncePerDevice once;
   cudaError_t e = once([] {
-    return cudaFuncSetAttribute(q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+    return cudaFuncSetAttribute(q8_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  if (IMG)
-    q8_query_kernel<D><<<1 + unsigned(a.B) * a.v.H * unsigned(a.row_tiles), 256, 0, stream>>>(a);
-  else
-    q8_schedule_kernel<kBlockRows, kKeys><<<1, 1024, 0, stream>>>(a);
+  q8_query_kernel<D><<<1 + unsigned(a.B) * a.v.H * unsigned(a.row_tiles), 256, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (IMG && (e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * unsigned(a.list)), 256, 0, stream, a)) != cudaSuccess)
-    return e;
-  if ((e = launch_after(true, q8_rows_kernel<D, IMG ? 0 : FMT, IMG>, dim3(unsigned(a.n_ctas)), IMG ? 384 : 512, L::total, stream, a)) != cudaSuccess)
-    return e;
+  e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * unsigned(a.list)), 256, 0, stream, a);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_after(true, q8_rows_kernel<D>, dim3(unsigned(a.n_ctas)), 384, L::total, stream, a)) != cudaSuccess) return e;
   const int rows = int(std::min<int64_t>(kBlockRows, int64_t(a.c.n_new) * a.G));
   return launch_after(true, q8_join_kernel<D>, dim3(unsigned(a.n_ctas), unsigned((rows + 31) / 32)), 2 * D, 0, stream, a);
-}
-
-template <int D, int FMT>
-cudaError_t launch_either(const RowsArgs& a, bool images, cudaStream_t stream) {
-  return images ? launch<D, FMT, true>(a, stream) : launch<D, FMT, false>(a, stream);
 }
 
 }  // namespace
@@ -960,9 +868,9 @@ cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const
     }
     cudaError_t e;
     if (s.head_dim == 128)
-      e = s.format == RQ_Q8_INT8 ? launch_either<128, RQ_Q8_INT8>(g, p.by_images, stream) : launch_either<128, RQ_Q8_E4M3>(g, p.by_images, stream);
+      e = s.format == RQ_Q8_INT8 ? launch<128, RQ_Q8_INT8>(g, stream) : launch<128, RQ_Q8_E4M3>(g, stream);
     else
-      e = s.format == RQ_Q8_INT8 ? launch_either<64, RQ_Q8_INT8>(g, p.by_images, stream) : launch_either<64, RQ_Q8_E4M3>(g, p.by_images, stream);
+      e = s.format == RQ_Q8_INT8 ? launch<64, RQ_Q8_INT8>(g, stream) : launch<64, RQ_Q8_E4M3>(g, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
