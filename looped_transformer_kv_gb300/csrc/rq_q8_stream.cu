@@ -8,8 +8,9 @@
 // merged once per segment.  m is raised when a score exceeds it by more than 8, E when a V scale
 // exceeds 2^(E + 7): weights stay below 2^15.
 //
-// CTAs share the work by the line of rq_q8_line.cuh; the last CTA of a divided unit to finish joins
-// its partial results in order.
+// CTAs share the work by the line of rq_q8_line.cuh; q8_stream_join_kernel joins the partial results of
+// divided units, and the queries' operands are made by the kernel before (q8_prepare_kernel): code for
+// either in this kernel costs its loop registers (verification of 8 tokens: 121 us).
 #include "rq_q8_line.cuh"
 #include "rq_tc.cuh"
 
@@ -21,13 +22,16 @@ constexpr float kTop = 8.f;
 constexpr int kScaleTop = 7, kScaleHead = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
-constexpr int kJoin = 16;             // parts joined at once
 
-// A divided unit: its rows, the CTAs that share it.
-struct Parted {
-  bool is;
-  int b, h, r0, rows, first, last;
+struct StreamArgs : Q8Line {
+  uint8_t* queries;      // [B][Hkv][blocks] of StreamSmem::kQuery bytes
 };
+
+// A divided unit: its rows, the CTAs that share it.  By the CTA where it begins; no rows: none does.
+struct Parted {
+  int b, h, r0, rows, first, last, pad[2];
+};
+constexpr int kTickets = sizeof(Parted) / 4;   // (they lie where tickets would)
 
 template <int D, int NT>
 struct StreamSmem {
@@ -35,18 +39,18 @@ struct StreamSmem {
   static constexpr int kCodes = 2 * kQ8Tile * D, kStage = kCodes + 128;   // (scales: 32 bytes)
   static constexpr int kRows = 8 * NT, kMergeRow = D + 4;
   static constexpr int kMerge = 4 * 8 * kMergeRow * 4;
-  static constexpr int kQuery = NT * (D / 16) * 32 * 8;
-  static constexpr int kFixed = kMerge + kQuery + 4 * kRows * 8 + kRows * 8 + 768;
+  static constexpr int kFragments = NT * (D / 16) * 32 * 8;
+  static constexpr int kQuery = kFragments + kRows * 8;     // of a unit: B fragments, factors, own slots
+  static constexpr int kHeld = NT > 2 ? kQuery : kRows * 8;  // of it in shared memory
+  static constexpr int kFixed = kMerge + kHeld + 4 * kRows * 8 + 768;
   static constexpr int kStages0 = (227 * 1024 / kCtas - 1024 - kFixed) / kStage;
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-  static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kQuery;
-  static constexpr int row_scale = stats + 4 * kRows * 8, row_limit = row_scale + kRows * 4;
-  static constexpr int bars = row_limit + kRows * 4, misc = bars + 16 * kStages;
-  static constexpr int cut = misc + 16 * 4 + 4 * 8, parted = cut + int(sizeof(OwnCut)), walk = parted + 64;
-  static constexpr int total = walk + int(sizeof(Walk<8, kQ8Tile>)) + 128;   // + alignment of the base
-  static_assert(2 * sizeof(Parted) <= 64 && kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
+  static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kHeld;
+  static constexpr int bars = stats + 4 * kRows * 8, misc = bars + 16 * kStages;
+  static constexpr int cut = misc + 16 * 4 + 4 * 8, walk = cut + int(sizeof(OwnCut));
+  static constexpr int total = walk + int(sizeof(Walk<8, kQ8Tile>)) + 128;
+  static_assert(kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
 };
-
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -81,98 +85,156 @@ __device__ __forceinline__ void store_row(const Q8Line& a, int b, int h, int r0,
     }
 }
 
-// Parts of CTAs k0, k0 + stride .. <= k1 of a divided unit joined, by 128 threads: 16 a row (CH channels
-// each), the eight groups on eight rows, or on parts of fewer rows; each takes its parts in order, the
-// loads of two or four at a time.  Into the first one's place (`last` false), or out.
+// The kernel before: clears the error word and what tells of divided units (or cuts the line), and makes
+// the queries' operands, a CTA a unit: B fragments, (k-step, row) word pairs of the lanes that use them.
 template <int D, int NT>
-__device__ __forceinline__ void join_parts(const Q8Line& a, const Parted& u, int k0, int k1, int stride, bool last, float* buffer) {
-  constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = NT > 1 ? 4 : 2, kRow = D + 2;
-  const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;
-  const int rows = u.rows > 4 ? 8 : u.rows > 2 ? 4 : u.rows, groups = 8 / rows;   // at a time; groups of a row
-  auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kRows; };
-#pragma unroll 1
-  for (int y0 = 0; y0 < u.rows; y0 += rows) {
-    const int y = y0 + group % rows, mine = group / rows;
-    float M = kNoMax, sum = 0.f, o[CH];
-#pragma unroll
-    for (int k = 0; k < CH; ++k) o[k] = 0.f;
-#pragma unroll 1
-    for (int k = k0 + mine * stride; y < u.rows && mine < groups && k <= k1; k += TOGETHER * groups * stride) {
-      float2 st[TOGETHER];
-      float4 v[TOGETHER][CH / 4];
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        const int ki = k + i * groups * stride;
-        st[i] = make_float2(kNoMax, 0.f);
-        if (ki > k1) continue;
-        st[i] = __ldcg(&a.stats[place(ki) + y]);
-#pragma unroll
-        for (int z = 0; z < CH / 4; ++z) v[i][z] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(ki) + y) * D + ch) + z);
-      }
-      float to = M;
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) to = fmaxf(to, st[i].x);
-      const float f0 = ex2(M - to);
-      M = to;
-      sum *= f0;
-#pragma unroll
-      for (int z = 0; z < CH; ++z) o[z] *= f0;
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        if (k + i * groups * stride > k1) continue;
-        const float f = ex2(st[i].x - M);
-        sum += f * st[i].y;
-#pragma unroll
-        for (int z = 0; z < CH / 4; ++z) {
-          o[4 * z] = fmaf(f, v[i][z].x, o[4 * z]);
-          o[4 * z + 1] = fmaf(f, v[i][z].y, o[4 * z + 1]);
-          o[4 * z + 2] = fmaf(f, v[i][z].z, o[4 * z + 2]);
-          o[4 * z + 3] = fmaf(f, v[i][z].w, o[4 * z + 3]);
-        }
-      }
-    }
-    if (groups > 1) {                                       // the groups of a row, in order
-      float* const at = buffer + group * kRow;
-#pragma unroll
-      for (int z = 0; z < CH; ++z) at[2 + ch + z] = o[z];
-      if (ch == 0) {
-        at[0] = M;
-        at[1] = sum;
-      }
-      consumers_sync();
-      if (mine == 0) {
-        float to = kNoMax;
-        for (int i = 0; i < groups; ++i) to = fmaxf(to, buffer[(group + i * rows) * kRow]);
-        M = to;
-        sum = 0.f;
-#pragma unroll
-        for (int z = 0; z < CH; ++z) o[z] = 0.f;
-        for (int i = 0; i < groups; ++i) {
-          const float* const from = buffer + (group + i * rows) * kRow;
-          const float f = ex2(from[0] - M);
-          sum += f * from[1];
-#pragma unroll
-          for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[2 + ch + z], o[z]);
-        }
-      }
-    }
-    consumers_sync();                                       // (every part of these rows is read)
-    if (mine != 0 || y >= u.rows) continue;
-    if (last) {
-      store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+__global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__ StreamArgs a) {
+  grid_next();
+  using L = StreamSmem<D, NT>;
+  if (blockIdx.x == 0) {
+    if (a.own_cut) {
+      if (threadIdx.x == 0) *a.err = 0u;
+      for (int i = threadIdx.x; i < a.n_ctas * kTickets; i += 128) a.tickets[i] = 0u;
     } else {
-      float* const p = a.part + (place(k0) + y) * D + ch;
+      cut_line<8 * NT, kQ8Tile, 128>(a);
+    }
+    return;
+  }
+  constexpr int KS = D / 16, LPR = D / 8, AT = 128 / LPR;   // lanes per row, rows at a time
+  const unsigned unit = blockIdx.x - 1;
+  const int block = int(unit % unsigned(a.blocks)), bh = int(unit / unsigned(a.blocks)), b = bh / a.v.H, h = bh % a.v.H;
+  const Rows x = rows_of<8 * NT, kQ8Tile>(a, b, block);
+  if (x.rows <= 0 || !x.ok) return;
+  uint8_t* const to = a.queries + int64_t(unit) * L::kQuery;
+  uint2* const query = reinterpret_cast<uint2*>(to);
+  float* const row_scale = reinterpret_cast<float*>(to + L::kFragments);
+  int* const row_limit = reinterpret_cast<int*>(row_scale + L::kRows);         // a row's own slot
+  const int r0 = block * L::kRows, qc = threadIdx.x % LPR, lane = threadIdx.x & 31;
 #pragma unroll
-      for (int z = 0; z < CH; z += 4) *reinterpret_cast<float4*>(p + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
-      if (ch == 0) a.stats[place(k0) + y] = make_float2(M, sum);
+  for (int y0 = 0; y0 < L::kRows; y0 += AT) {
+    const int y = y0 + threadIdx.x / LPR, j = (r0 + y) / a.G, hq = h * a.G + (r0 + y) % a.G;
+    const bool live = y < x.rows;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (live) raw = q8_load8(a.c.q + b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec);
+    float f[8];
+    bool lost = false;
+    if (a.c.rope.table != nullptr) {
+      int pos = -1;
+      if (live) {
+        pos = a.c.rope.positions ? a.c.rope.positions[int64_t(b) * a.c.n_new + j] : x.ctx + j;
+        lost = pos < 0 || pos >= a.c.rope.n_pos;
+        if (lost) pos = -1;
+      }
+      const Q8Angles angles = q8_angles<D>(a.c.rope, pos, lane);
+      q8_floats(raw, f);
+      q8_rotate<D>(f, a.c.rope, angles, lane);
+    } else {
+      q8_floats(raw, f);
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
+    // a power of two brings the row's largest element into [2^14, 2^15): bf16 values are exact
+    const int ex = int(__float_as_uint(mx) >> 23);
+    const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
+    const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
+    if (y >= L::kRows) continue;
+    const int nt = y >> 3, n = y & 7;
+    const int cc = D == 128 ? qc >> 2 : qc >> 1, s = D == 128 ? 2 * (qc & 3) : 2 * (qc & 1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      query[(nt * KS + s + k) * 32 + 4 * n + cc] =
+          make_uint2(pack_half2(f[4 * k] * up * up2, f[4 * k + 1] * up * up2),
+                     pack_half2(f[4 * k + 2] * up * up2, f[4 * k + 3] * up * up2));
+    if (qc == 0) {
+      row_scale[y] = lost ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+      row_limit[y] = x.ctx + min(j, x.n - 1);
     }
   }
+}
+
+// The parts of a divided unit: two rows a CTA, 16 threads (CH channels each) a row and group; the groups of
+// a row take every groups-th part, the loads of four at a time, and are joined in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_constant__ StreamArgs a) {
+  grid_wait();
+  const Parted u = reinterpret_cast<const Parted*>(a.tickets)[blockIdx.x];
+  const int y0 = int(blockIdx.y) * 2;
+  if (y0 >= u.rows) return;
+  constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = 4, kRow = D + 4;
+  __shared__ float buffer[16 * kRow];
+  const int left = u.rows - y0, rows = min(left, 2), groups = 16 / rows;   // rows here; groups of a row
+  const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH, y = y0 + group % rows, mine = group / rows;
+  auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kRows + y; };
+  float M = kNoMax, sum = 0.f, o[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) o[k] = 0.f;
+#pragma unroll 1
+  for (int k = u.first + mine; y < u.rows && k <= u.last; k += TOGETHER * groups) {
+    float2 st[TOGETHER];
+    float4 v[TOGETHER][CH / 4];
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) {
+      const int ki = k + i * groups;
+      st[i] = make_float2(kNoMax, 0.f);
+      if (ki > u.last) continue;
+      st[i] = a.stats[place(ki)];
+#pragma unroll
+      for (int z = 0; z < CH / 4; ++z) v[i][z] = *(reinterpret_cast<const float4*>(a.part + place(ki) * D + ch) + z);
+    }
+    float to = M;
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) to = fmaxf(to, st[i].x);
+    const float f0 = ex2(M - to);
+    M = to;
+    sum *= f0;
+#pragma unroll
+    for (int z = 0; z < CH; ++z) o[z] *= f0;
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) {
+      if (k + i * groups > u.last) continue;
+      const float f = ex2(st[i].x - M);
+      sum += f * st[i].y;
+#pragma unroll
+      for (int z = 0; z < CH / 4; ++z) {
+        o[4 * z] = fmaf(f, v[i][z].x, o[4 * z]);
+        o[4 * z + 1] = fmaf(f, v[i][z].y, o[4 * z + 1]);
+        o[4 * z + 2] = fmaf(f, v[i][z].z, o[4 * z + 2]);
+        o[4 * z + 3] = fmaf(f, v[i][z].w, o[4 * z + 3]);
+      }
+    }
+  }
+  float* const at = buffer + group * kRow;
+#pragma unroll
+  for (int z = 0; z < CH; ++z) at[2 + ch + z] = o[z];
+  if (ch == 0) {
+    at[0] = M;
+    at[1] = sum;
+  }
+  __syncthreads();
+  if (mine != 0 || y >= u.rows) return;
+  const int filled = min(groups, u.last - u.first + 1);     // (the others have no part)
+  for (int i = 0; i < filled; ++i) M = fmaxf(M, buffer[(group + i * rows) * kRow]);
+  sum = 0.f;
+#pragma unroll
+  for (int z = 0; z < CH; ++z) o[z] = 0.f;
+  for (int i = 0; i < filled; ++i) {
+    const float* const from = buffer + (group + i * rows) * kRow;
+    const float f = ex2(from[0] - M);
+    sum += f * from[1];
+#pragma unroll
+    for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[2 + ch + z], o[z]);
+  }
+  store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
 }
 
 // (more than 8 rows: accumulators take more registers than two CTAs of five warps leave, so three more
 // warps are launched that give theirs away)
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ Q8Line a) {
+__global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>::kCtas) q8_stream_kernel(const __grid_constant__ StreamArgs a) {
+  grid_next();
   using L = StreamSmem<D, NT>;
   using StreamWalk = Walk<8 * NT, kQ8Tile>;
   constexpr int KS = D / 16;                                // k-steps of a score, 16-channel tiles of O
@@ -183,7 +245,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
   const uint32_t bar0 = smem_u32(smem + L::bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (L::kStages + s); };
-  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [1], [2]: last of a unit, [4 ..]: a warp's E
+  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [4 ..]: a warp's E
   int* const bad_page = misc + 16;                          // [stage]
   OwnCut& cut = *reinterpret_cast<OwnCut*>(smem + L::cut);
   if (threadIdx.x == 0) {
@@ -264,13 +326,12 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
     if constexpr (NT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int r = lane >> 2, c = lane & 3;
     float* const merge = reinterpret_cast<float*>(smem + L::merge);
-    uint2* const query = reinterpret_cast<uint2*>(smem + L::query);
     float2* const stats = reinterpret_cast<float2*>(smem + L::stats);          // [warp][row]
-    float* const row_scale = reinterpret_cast<float*>(smem + L::row_scale);
-    int* const row_limit = reinterpret_cast<int*>(smem + L::row_limit);        // a row's own slot
+    uint8_t* const held = smem + L::query;                  // what is held of the unit's queries: all, or factors and own slots
+    const uint2* const query = reinterpret_cast<const uint2*>(held);
+    const float* const row_scale = reinterpret_cast<const float*>(held + L::kHeld - L::kRows * 8);
+    const int* const row_limit = reinterpret_cast<const int*>(row_scale + L::kRows);   // a row's own slot
     constexpr int CH = D / 16;                              // channels of a thread that stores
-    Parted* const parted = reinterpret_cast<Parted*>(smem + L::parted);        // [0] at the stretch's begin, [1] at its end
-    if (threadIdx.x < 2) parted[threadIdx.x].is = false;
     StreamWalk& w = *reinterpret_cast<StreamWalk*>(smem + L::walk);            // thread 0 walks
     if (threadIdx.x == 0) w.begin(cut);
     int g = 0;
@@ -281,50 +342,15 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
       if (!w.more) break;
       const Rows& x = w.x;
       const int r0 = w.block * L::kRows;
-      // ---- the rows' queries as B fragments: (k-step, row) word pairs of the lanes that use them
-      if (x.ok) {
-        constexpr int LPR = D / 8, AT = 128 / LPR;          // lanes per row, rows at a time
-        const int qc = threadIdx.x % LPR;
-#pragma unroll 1
-        for (int y = threadIdx.x / LPR; y < L::kRows; y += AT) {
-          const int j = (r0 + y) / a.G, hq = w.h * a.G + (r0 + y) % a.G;
-          const bool live = y < x.rows;
-          uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-          if (live) raw = q8_load8(a.c.q + w.b * a.c.q_strides[0] + j * a.c.q_strides[1] + hq * a.c.q_strides[2] + 8 * qc, a.qvec);
-          float f[8];
-          q8_floats(raw, f);
-          bool lost = false;
-          if (a.c.rope.table != nullptr) {
-            int pos = -1;
-            if (live) {
-              pos = a.c.rope.positions ? a.c.rope.positions[int64_t(w.b) * a.c.n_new + j] : x.ctx + j;
-              lost = pos < 0 || pos >= a.c.rope.n_pos;
-              if (lost) pos = -1;
-            }
-            q8_rotate<D>(f, a.c.rope, q8_angles<D>(a.c.rope, pos, lane), lane);
-          }
-          float mx = 0.f;
+      const uint8_t* const queries = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.blocks + w.block) * L::kQuery;
+      grid_wait();                                          // (the queries are there)
+      if (x.ok)
+        for (int k = threadIdx.x; k < L::kHeld / 8; k += 128)
+          reinterpret_cast<uint2*>(held)[k] = __ldcg(reinterpret_cast<const uint2*>(queries + L::kQuery - L::kHeld) + k);
+      uint2 qf[NT <= 2 ? NT * KS : 1];                      // (more rows: read again for every tile)
+      if (NT <= 2)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
-          // a power of two brings the row's largest element into [2^14, 2^15): bf16 values are exact
-          const int ex = int(__float_as_uint(mx) >> 23);
-          const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
-          const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
-          const int nt = y >> 3, n = y & 7;
-          const int cc = D == 128 ? qc >> 2 : qc >> 1, s = D == 128 ? 2 * (qc & 3) : 2 * (qc & 1);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            query[(nt * KS + s + k) * 32 + 4 * n + cc] =
-                make_uint2(pack_half2(f[4 * k] * up * up2, f[4 * k + 1] * up * up2),
-                           pack_half2(f[4 * k + 2] * up * up2, f[4 * k + 3] * up * up2));
-          if (qc == 0) {
-            row_scale[y] = lost ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
-            row_limit[y] = x.ctx + min(j, x.n - 1);
-          }
-        }
-      }
+        for (int k = 0; k < NT * KS; ++k) qf[k] = x.ok ? __ldcg(reinterpret_cast<const uint2*>(queries) + k * 32 + lane) : make_uint2(0u, 0u);
       consumers_sync();
 
       float acc[NT][KS][4], m[NT][2], l[NT][2], cs[NT][2];
@@ -342,10 +368,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
       }
       int E = -120;
-      uint2 qf[NT <= 2 ? NT * KS : 1];                      // (more rows: read again for every tile)
-      if (NT <= 2)
-#pragma unroll
-        for (int k = 0; k < NT * KS; ++k) qf[k] = query[k * 32 + lane];
+
 
       for (int t = 0; x.ok && t < w.T; ++t, ++g) {
         const int s = g % L::kStages;
@@ -546,55 +569,16 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           if (ch == 0) a.stats[int64_t(slot) * L::kRows + y] = make_float2(M, sum);
         }
       }
-      if (!whole && threadIdx.x == 0) {
-        Parted& p = parted[w.kt0 == 0];
-        p = {true, w.b, w.h, r0, x.rows, 0, 0};
-        w.sharers(cut.N, cut.used, p.first, p.last);
+      if (!whole && w.kt0 == 0 && threadIdx.x == 0) {       // (told by the CTA where the unit begins)
+        int first, last;
+        w.sharers(cut.N, cut.used, first, last);
+        reinterpret_cast<Parted*>(a.tickets)[me] = {w.b, w.h, r0, x.rows, first, last, {0, 0}};
       }
       consumers_sync();                                     // (the next segment overwrites what was read)
     }
-    // ---- divided units, at most two: the last of their CTAs joins the parts
     grid_wait();
-    if (parted[0].is || parted[1].is) {
-      // units of many CTAs: kJoin neighbours are joined first, by the last of them
-      __threadfence();
-      consumers_sync();
-      if (threadIdx.x < 2) {
-        const Parted& p = parted[threadIdx.x];
-        const bool many = p.last - p.first >= kJoin;
-        const int k0 = many ? p.first + (me - p.first) / kJoin * kJoin : p.first, k1 = many ? min(k0 + kJoin - 1, p.last) : p.last;
-        misc[1 + threadIdx.x] = p.is && atomicAdd(a.tickets + (many ? a.n_ctas : 0) + k0, 1u) == unsigned(k1 - k0);
-      }
-      consumers_sync();
-      __threadfence();
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        if (!misc[1 + k]) continue;
-        const Parted& p = parted[k];
-        if (p.last - p.first >= kJoin) {
-          const int k0 = p.first + (me - p.first) / kJoin * kJoin;
-          join_parts<D, NT>(a, p, k0, min(k0 + kJoin - 1, p.last), 1, false, merge);
-          __threadfence();
-          consumers_sync();
-          if (threadIdx.x == 0) misc[3] = atomicAdd(a.tickets + p.first, 1u) == unsigned((p.last - p.first) / kJoin);
-          consumers_sync();
-          if (!misc[3]) continue;
-          __threadfence();
-          join_parts<D, NT>(a, p, p.first, p.last, kJoin, true, merge);
-        } else {
-          join_parts<D, NT>(a, p, p.first, p.last, 1, true, merge);
-        }
-      }
-    }
     if (dead && lane == 0) atomicOr(a.err, 1u);
   }
-}
-
-// Clears the error word and the tickets.
-__global__ void __launch_bounds__(256) q8_clear_kernel(unsigned* err, unsigned* tickets, int n) {
-  grid_next();
-  if (threadIdx.x == 0) *err = 0u;
-  for (int i = threadIdx.x; i < n; i += 256) tickets[i] = 0u;
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -602,36 +586,44 @@ __global__ void __launch_bounds__(256) q8_clear_kernel(unsigned* err, unsigned* 
 int tiles_of_rows(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 Q8Layout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx, int nt) {
-  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), 2);
+  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), kTickets);
+}
+
+size_t query_bytes(const rq_q8_shape& s, int n_new, int nt) {
+  const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads), blocks = (rows + 8 * nt - 1) / (8 * nt);
+  return size_t(s.batch) * s.n_kv_heads * blocks * (size_t(nt) * (s.head_dim / 16) * 256 + size_t(8 * nt) * 8);
 }
 
 template <int D, int NT, int FMT>
-cudaError_t launch(const Q8Line& a, cudaStream_t stream) {
+cudaError_t launch(const StreamArgs& a, cudaStream_t stream) {
   using L = StreamSmem<D, NT>;
   static OncePerDevice once;
   cudaError_t e = once([] {
     return cudaFuncSetAttribute(q8_stream_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  if (a.own_cut)
-    q8_clear_kernel<<<1, 256, 0, stream>>>(a.err, a.tickets, 2 * a.n_ctas);
-  else
-    q8_schedule_kernel<8 * NT, kQ8Tile><<<1, 1024, 0, stream>>>(a);
+  q8_prepare_kernel<D, NT><<<1 + unsigned(a.B) * a.v.H * a.blocks, 128, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), L::kThreads, L::total, stream, a);
+  if ((e = launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), L::kThreads, L::total, stream, a)) != cudaSuccess) return e;
+  const int rows = int(std::min<int64_t>(8 * NT, int64_t(a.c.n_new) * a.G));
+  return launch_after(true, q8_stream_join_kernel<D, NT>, dim3(unsigned(a.n_ctas), unsigned((rows + 1) / 2)), 256, 0, stream, a);
 }
 
 }  // namespace
 
 size_t q8_stream_workspace_bytes(const rq_q8_shape& s, int n_new, int max_ctx) {
-  return stream_layout(s, n_new, max_ctx, tiles_of_rows(int64_t(n_new) * (s.n_q_heads / s.n_kv_heads))).total;
+  const int nt = tiles_of_rows(int64_t(n_new) * (s.n_q_heads / s.n_kv_heads));
+  return stream_layout(s, n_new, max_ctx, nt).total + query_bytes(s, n_new, nt);
 }
 
 cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_paging* paging,
                              const Q8Call& c, void* ws, cudaStream_t stream) {
   const int nt = tiles_of_rows(int64_t(c.n_new) * (s.n_q_heads / s.n_kv_heads));
-  Q8Line a = q8_line(s, cache, paging, c, 8 * nt);
-  q8_place(a, stream_layout(s, c.n_new, c.max_ctx, nt), ws, 2);
+  StreamArgs a = {};
+  static_cast<Q8Line&>(a) = q8_line(s, cache, paging, c, 8 * nt);
+  const Q8Layout x = stream_layout(s, c.n_new, c.max_ctx, nt);
+  q8_place(a, x, ws, kTickets);
+  a.queries = static_cast<uint8_t*>(ws) + x.total;
   a.own_cut = int64_t(a.B) * a.blocks <= kOwnCutPairs;
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
   switch (nt) {
