@@ -98,6 +98,7 @@ __device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, con
   }
   const int c = lane % (D / 8), half = rope.rot / 16;
   const bool second = c >= half;
+  const float sign = second ? 1.f : -1.f;
   const int partner = lane - c + (8 * c < rope.rot ? (second ? c - half : c + half) : c);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -105,10 +106,9 @@ __device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, con
     const float o1 = __shfl_sync(RQ_FULL_MASK, f[2 * k + 1], partner);
     if (r.turned) {
       const float4 a = r.a[k];
-      const float p0 = __fmul_rn(f[2 * k], a.x), p1 = __fmul_rn(f[2 * k + 1], a.z);
-      const float r0 = __fmul_rn(o0, a.y), r1 = __fmul_rn(o1, a.w);
-      f[2 * k] = second ? __fadd_rn(p0, r0) : __fsub_rn(p0, r0);
-      f[2 * k + 1] = second ? __fadd_rn(p1, r1) : __fsub_rn(p1, r1);
+      // (a product with 1 or -1 is exact: the sum's is the only rounding of the last step)
+      f[2 * k] = __fmaf_rn(__fmul_rn(o0, a.y), sign, __fmul_rn(f[2 * k], a.x));
+      f[2 * k + 1] = __fmaf_rn(__fmul_rn(o1, a.w), sign, __fmul_rn(f[2 * k + 1], a.z));
     }
   }
 }

@@ -1,6 +1,10 @@
 // Appending to the 8-bit cache (include/rq_q8.h): two warps (d = 64: one) take one block of 16 slots of one
 // (sequence, loop, kv-head, K or V); D / 8 lanes hold a row, 8 channels each.  The new rows are loaded and
 // rotated, their largest magnitude gives the scale, and the codes follow from registers.
+//
+// Bound by instructions and occupancy (issue slots 73 % used): 1,024 tokens of 4 x 16 heads and 4 loops in 41 us
+// without rotation, 4.9 TB/s, 57 us rotated.  A whole block a warp took 110 registers and 51 us (75 rotated);
+// blocks of 256 threads, whose warps end together, 46 (77).
 #include <algorithm>
 
 #include "rq_kernels.h"
@@ -59,10 +63,10 @@ __device__ __forceinline__ void values_of(uint2 w, float (&f)[8]) {
   }
 }
 
-// The larger magnitude; not a number if either is none.
+// The larger magnitude (of any sign); not a number if either is none.
 __device__ __forceinline__ float larger(float m, float x) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(x));
   return y;
 }
 

@@ -10,7 +10,12 @@
 //
 // CTAs share the work by the line of rq_q8_line.cuh; q8_stream_join_kernel joins the partial results of
 // divided units, and the queries' operands are made by the kernel before (q8_prepare_kernel): code for
-// either in this kernel costs its loop registers (verification of 8 tokens: 121 us).
+// either in this kernel costs its loop registers (verification of 8 tokens: 121 us against 109).
+//
+// One row or a few: bound by HBM while it streams (16 x 16 heads: 7.3 TB/s from 8,192 to 16,384 slots), by
+// launches, first tiles and joins at short contexts (4,096 slots in 55 us, 40 at a copy's rate).  32 rows: by
+// the latency of each warp's scores, softmax and values, two warps a scheduler (8 x 8 heads after 16,384
+// slots in 109 us).
 #include "rq_q8_line.cuh"
 #include "rq_tc.cuh"
 
