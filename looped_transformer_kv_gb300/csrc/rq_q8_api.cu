@@ -91,8 +91,9 @@ rq_status attention_common(const rq_q8_shape* s, const rq_q8_cache* cache, const
   if ((st = check_sizes(s, n_new, max_ctx, window, n_sink)) != RQ_OK) return st;
   const int64_t extents[3] = {s->batch, n_new, s->n_q_heads};
   if (!rq::strides_ok(q_strides, extents, 3)) return RQ_ERR_INVALID_ARG;
-  rq::Q8Call c = {q, {q_strides[0], q_strides[1], q_strides[2]}, loop, n_lens, n_new, ctx_lens, max_ctx, window,
-                  n_sink, {}, out};
+  const int32_t most = 1 << 30;                             // (as many slots as there can be)
+  rq::Q8Call c = {q, {q_strides[0], q_strides[1], q_strides[2]}, loop, n_lens, n_new, ctx_lens, max_ctx,
+                  window < most ? window : most, n_sink < most ? n_sink : most, {}, out};
   if ((st = check_rope(s, rope, c.rope)) != RQ_OK) return st;
   if (n_new == 0) return RQ_OK;
   if (!ws || ws_bytes < rq::q8_workspace_bytes(*s, n_new, max_ctx, window, n_sink)) return RQ_ERR_WORKSPACE;

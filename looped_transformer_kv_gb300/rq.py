@@ -389,29 +389,32 @@ def make_rope(table, interleaved=False, positions=None):
     return r
 
 
-def _rope(rope, B, n):
+def _rope(rope, B, n, dev):
     if rope is None:
         return None
-    positions = rope.tensors[1]
-    assert positions is None or positions.shape == (B, n)
+    table, positions = rope.tensors
+    assert table.get_device() == dev
+    assert positions is None or (positions.shape == (B, n) and positions.get_device() == dev)
     return ctypes.byref(rope)
 
 
-def _lens(t, B):
+def _lens(t, B, dev):
     """Address of an int32 [B] tensor, or None."""
     if t is None:
         return None
-    assert t.dtype == torch.int32 and t.numel() == B and t.is_contiguous()
+    assert t.dtype == torch.int32 and t.numel() == B and t.is_contiguous() and t.get_device() == dev
     return t.data_ptr()
 
 
-def _q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
+def _q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
     B, n, two, loops, H, d = kv_new.shape
+    dev = torch._C._cuda_getDevice()      # every tensor lies on the current device
+    assert kv_new.get_device() == cache.codes.get_device() == cache.scales.get_device() == dev
     s0, s1, s2, s3, s4, s5 = kv_new.stride()
     assert kv_new.dtype == torch.bfloat16 and (B, two, H, d) == (shape.batch, 2, shape.n_kv_heads, shape.head_dim)
     assert s5 == 1 or kv_new.numel() == 0
-    return (kv_new.data_ptr(), _I5(s0, s1, s2, s3, s4), loop_begin, loops, _lens(n_lens, B), n,
-            _lens(ctx_lens, B), _rope(rope, B, n), _raw_stream(stream))
+    return (kv_new.data_ptr(), _I5(s0, s1, s2, s3, s4), loop_begin, loops, _lens(n_lens, B, dev), n,
+            _lens(ctx_lens, B, dev), _rope(rope, B, n, dev), _raw_stream(stream))
 
 
 def q8_append(shape, cache, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None, stream=None):
@@ -419,7 +422,7 @@ def q8_append(shape, cache, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None
     slots from ctx_lens[b] on, of the loops from loop_begin on; n_lens int32 [B]; rope from make_rope."""
     check("rq_q8_append", _lib.lib().rq_q8_append(
         ctypes.byref(shape), ctypes.byref(cache.struct),
-        *_q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+        *_q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
 
 
 def paged_q8_append(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None,
@@ -427,7 +430,7 @@ def paged_q8_append(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens=N
     """rq_paged_q8_append; the other arguments as in q8_append."""
     check("rq_paged_q8_append", _lib.lib().rq_paged_q8_append(
         ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
-        *_q8_append_args(shape, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+        *_q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
 
 
 def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
@@ -437,15 +440,18 @@ def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
                                                 int(window), int(n_sink)))
 
 
-def _q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
+def _q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
     B, n, Hq, d = q.shape
+    dev = torch._C._cuda_getDevice()
+    assert (q.get_device() == out.get_device() == ws.get_device() == cache.codes.get_device() ==
+            cache.scales.get_device() == dev)
     s0, s1, s2, s3 = q.stride()
     assert q.dtype == out.dtype == torch.bfloat16
     assert (B, Hq, d) == (shape.batch, shape.n_q_heads, shape.head_dim)
     assert s3 == 1 or q.numel() == 0
     assert out.shape == q.shape and out.is_contiguous()
-    return (q.data_ptr(), _I3(s0, s1, s2), loop, _lens(n_lens, B), n, _lens(ctx_lens, B), max_ctx, window,
-            n_sink, _rope(rope, B, n), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    return (q.data_ptr(), _I3(s0, s1, s2), loop, _lens(n_lens, B, dev), n, _lens(ctx_lens, B, dev), max_ctx, window,
+            n_sink, _rope(rope, B, n, dev), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
 
 
 def q8_attention(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None, window=0, n_sink=0,
@@ -455,7 +461,7 @@ def q8_attention(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None,
     `window` and the first n_sink."""
     check("rq_q8_attention", _lib.lib().rq_q8_attention(
         ctypes.byref(shape), ctypes.byref(cache.struct),
-        *_q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+        *_q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
                             stream)))
 
 
@@ -464,7 +470,7 @@ def paged_q8_attention(shape, cache, paging, q, loop, ctx_lens, max_ctx, out, ws
     """rq_paged_q8_attention; the other arguments as in q8_attention."""
     check("rq_paged_q8_attention", _lib.lib().rq_paged_q8_attention(
         ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
-        *_q8_attention_args(shape, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+        *_q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
                             stream)))
 
 

@@ -716,3 +716,46 @@ def test_sequences_in_groups():
         assert torch.isnan(out[b].float()).all() and torch.isfinite(out[4].float()).all()
     del cache, ws
     torch.cuda.empty_cache()
+
+
+def test_the_largest_windows_and_sinks():
+    """Windows and sinks beyond any context: everything is seen."""
+    for n in (1, 40):
+        c = Case(1, 2, 1, 64, "e4m3", [300], n)
+        c.append()
+        c.attend()
+        want = c.out.clone()
+        for window, sinks in (((1 << 31) - 1, 0), ((1 << 31) - 1, (1 << 31) - 1), (1 << 30, 5), (1, (1 << 31) - 1)):
+            c.ws = torch.empty(rq.q8_workspace_bytes(c.shape, n, c.max_ctx, window, sinks), dtype=torch.uint8, device="cuda")
+            c.out.fill_(MARK)
+            c.attend(window=window, n_sink=sinks)
+            assert torch.equal(c.out, want), (n, window, sinks)
+
+
+def test_zero_queries_and_zero_states():
+    """Rows of zeros: equal weights, outputs the mean; a cache of zeros: zeros."""
+    for n in (1, 9, 50):
+        c = Case(1, 4, 1, 128, "int8", [100], n)
+        c.append()
+        c.q_host[:] = 0
+        c.q = c.q_host.cuda()
+        c.attend()
+        c.check()
+        z = Case(1, 4, 1, 128, "int8", [0], n)
+        z.append(kv=torch.zeros_like(z.kv))
+        assert (z.cache.scales[0, 0, 0, 0, :, 0] == 2.0 ** -100).all()
+        z.attend()
+        assert (z.out == 0).all()
+
+
+def test_tensors_elsewhere_are_refused():
+    c = Case(1, 2, 1, 64, "e4m3", [5], 2, rot=64)
+    with pytest.raises(AssertionError):
+        rq.q8_append(c.shape, c.cache, c.kv.cpu(), 0, c.ctx_lens)
+    with pytest.raises(AssertionError):
+        rq.q8_append(c.shape, c.cache, c.kv, 0, c.ctx_lens.cpu())
+    with pytest.raises(AssertionError):
+        rq.q8_append(c.shape, c.cache, c.kv, 0, c.ctx_lens, rope=rq.make_rope(torch.zeros(8, 32, 2)))
+    for q, out, ws in ((c.q.cpu(), c.out, c.ws), (c.q, c.out.cpu(), c.ws), (c.q, c.out, c.ws.cpu())):
+        with pytest.raises(AssertionError):
+            rq.q8_attention(c.shape, c.cache, q, 0, c.ctx_lens, 5, out, ws)
