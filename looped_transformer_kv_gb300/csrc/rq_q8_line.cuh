@@ -17,6 +17,10 @@ struct Cut {           // a CTA's stretch of the line
   int32_t b, block;
 };
 
+struct Parted {        // a divided unit: its rows, the CTAs that share it; no rows: there is none
+  int32_t b, h, r0, rows, first, last;
+};
+
 struct Q8Line {
   Q8View v;
   Q8Call c;
@@ -25,15 +29,16 @@ struct Q8Line {
   float scale_log2;
   unsigned* err;         // workspace: error word, ...
   int32_t* used;         // CTAs with work
-  unsigned* tickets;     // [CTA][n_tickets] of the unit that is cut at its end
+  Parted* parted;        // [CTA] the unit that begins in its stretch and goes on behind it
   int64_t* prefix;       // [B * blocks + 1] places of (sequence, block)
   Cut* cut;              // [CTA + 1]
   float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l); or four floats each
   float* part;           // ... their sums
-  int32_t n_ctas, n_tickets;
+  int32_t n_ctas;
   int32_t clear;         // the call's first launch
   int32_t own_cut;       // each CTA cuts for itself
   int32_t least;         // steps of a CTA
+  int32_t whole;         // (own_cut) units are not divided
 };
 
 // The tiles of 64 slots that some new token of a sequence sees, as a list: 0 .. sink0 and then from
@@ -93,13 +98,13 @@ __device__ __forceinline__ int ctas_used(const Q8Line& a, int64_t N) {
   return int(min((N + a.least - 1) / a.least, int64_t(a.n_ctas)));
 }
 
-// One CTA: clears the error word and tickets, cuts the line.
+// One CTA: clears the error word and what tells of divided units, cuts the line.
 template <int ROWS, int KEYS, int THREADS>
 __device__ __forceinline__ void cut_line(const Q8Line& a) {
   __shared__ int64_t warp_sum[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0 && a.clear) *a.err = 0u;
-  for (int i = tid; i < a.n_ctas * a.n_tickets; i += THREADS) a.tickets[i] = 0u;
+  for (int i = tid; i < a.n_ctas; i += THREADS) a.parted[i].rows = 0;
   const int64_t pairs = int64_t(a.B) * a.blocks;
   int64_t run = 0;
   bool bad = false;
@@ -142,15 +147,10 @@ __device__ __forceinline__ void cut_line(const Q8Line& a) {
     a.cut[i] = {pos, a.prefix[lo], int(lo / a.blocks), int(lo % a.blocks)};
   }
 }
-template <int ROWS, int KEYS>
-__global__ void __launch_bounds__(1024) q8_schedule_kernel(const __grid_constant__ Q8Line a) {
-  grid_next();
-  cut_line<ROWS, KEYS, 1024>(a);
-}
 
 // The same cut by a CTA of THREADS threads for itself, where there are at most kOwnCutPairs pairs; the
-// kernel before then only clears (q8_clear_kernel), and need not be waited for until the error word, the
-// tickets or partial results are used.
+// kernel before then does not cut, and need not be waited for until the error word or
+// the workspace is used.
 constexpr int kOwnCutPairs = 640;
 
 struct OwnCut {
@@ -198,16 +198,20 @@ __device__ __forceinline__ bool own_cut(const Q8Line& a, OwnCut& out, int me) { 
     __syncthreads();
   }
   const int used = ctas_used(a, run);
-  const int64_t pos = used ? run * me / used : 0;
+  const int64_t pos = used ? run * me / used : 0, to = used ? run * (me + 1) / used : 0;
 #pragma unroll
-  for (int k = 0; k < EACH; ++k)
-    if (before[k] <= pos && pos < before[k] + int64_t(units[k]) * a.v.H) {
-      const int p = tid + k * THREADS;
-      out.from = {pos, before[k], p / a.blocks, p % a.blocks};
+  for (int k = 0; k < EACH; ++k) {
+    const int p = tid + k * THREADS;
+    const int64_t stop = before[k] + int64_t(units[k]) * a.v.H;
+    // (whole: a cut inside a unit moves to its end)
+    auto cut_at = [&](int64_t x) { return a.whole ? before[k] + (x - before[k] + units[k] - 1) / units[k] * units[k] : x; };
+    if (before[k] <= pos && pos < stop) {
+      out.from = {cut_at(pos), before[k], p / a.blocks, p % a.blocks};
       out.rows = rows_of<ROWS, KEYS>(a, p / a.blocks, p % a.blocks);
     }
+    if (before[k] < to && to <= stop) out.to = cut_at(to);
+  }
   if (tid == 0) {
-    out.to = used ? run * (me + 1) / used : 0;
     out.N = run;
     out.used = used;
   }
@@ -290,18 +294,18 @@ inline Q8Line q8_line(const rq_q8_shape& s, const rq_q8_cache& cache, const rq_p
 // Places in the workspace, and its size.
 struct Q8Layout {
   int n_ctas;
-  size_t tickets, prefix, cut, stats, part, total;
+  size_t parted, prefix, cut, stats, part, total;
 };
 
-inline Q8Layout q8_layout(const rq_q8_shape& s, int n_new, int max_ctx, int rows, int keys, int fit, int n_tickets) {
+inline Q8Layout q8_layout(const rq_q8_shape& s, int n_new, int max_ctx, int rows, int keys, int fit) {
   Q8Layout x;
   const int64_t all = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
   const int64_t tiles = (std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity) + keys - 1) / keys + 1;
   const int64_t most = int64_t(s.batch) * s.n_kv_heads * ((all + rows - 1) / rows) * tiles;
   x.n_ctas = int(std::min<int64_t>(most, fit));
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  x.tickets = kWsHeaderBytes;
-  x.prefix = x.tickets + up(size_t(x.n_ctas) * 4 * n_tickets);
+  x.parted = kWsHeaderBytes;
+  x.prefix = x.parted + up(size_t(x.n_ctas) * sizeof(Parted));
   x.cut = x.prefix + up((size_t(s.batch) * size_t((all + rows - 1) / rows) + 1) * 8);
   x.stats = x.cut + up((size_t(x.n_ctas) + 1) * sizeof(Cut));
   x.part = x.stats + up(size_t(x.n_ctas) * 2 * rows * 16);
@@ -309,17 +313,16 @@ inline Q8Layout q8_layout(const rq_q8_shape& s, int n_new, int max_ctx, int rows
   return x;
 }
 
-inline void q8_place(Q8Line& a, const Q8Layout& x, void* ws, int n_tickets) {
+inline void q8_place(Q8Line& a, const Q8Layout& x, void* ws) {
   char* const base = static_cast<char*>(ws);
   a.err = reinterpret_cast<unsigned*>(base);
   a.used = reinterpret_cast<int32_t*>(base + 4);
-  a.tickets = reinterpret_cast<unsigned*>(base + x.tickets);
+  a.parted = reinterpret_cast<Parted*>(base + x.parted);
   a.prefix = reinterpret_cast<int64_t*>(base + x.prefix);
   a.cut = reinterpret_cast<Cut*>(base + x.cut);
   a.stats = reinterpret_cast<float2*>(base + x.stats);
   a.part = reinterpret_cast<float*>(base + x.part);
   a.n_ctas = x.n_ctas;
-  a.n_tickets = n_tickets;
   a.clear = 1;
   a.least = 1;
 }

@@ -312,12 +312,6 @@ __device__ __forceinline__ uint4 bf16_row(const float (&v)[8], float inv) {
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// A divided unit: its first row, the CTAs that share it.  By the CTA where it begins; no rows: none does.
-struct Parted {
-  int b, h, r0, rows, first, last, pad[2];
-};
-constexpr int kTickets = sizeof(Parted) / 4;                // (they lie where other kernels count)
-
 template <int D>
 __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
@@ -653,7 +647,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
             *reinterpret_cast<uint4*>(part + ((8 * y + z) * kRowTile + r) * 4) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
         if (i == 0 && r == 0 && w.kt0 == 0)                     // (told by the CTA where the unit begins)
-          reinterpret_cast<Parted*>(a.tickets)[me] = {w.b, w.h, w.block * kBlockRows, x.rows, first, last, {0, 0}};
+          a.parted[me] = {w.b, w.h, w.block * kBlockRows, x.rows, first, last};
         tc_fence_before();
         continue;
       }
@@ -716,7 +710,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
 template <int D>
 __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
-  const Parted u = reinterpret_cast<const Parted*>(a.tickets)[blockIdx.x];
+  const Parted u = a.parted[blockIdx.x];
   const int row = int(blockIdx.y) * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
   if (row >= u.rows) return;
   const float4* const stats = reinterpret_cast<const float4*>(a.stats);
@@ -804,7 +798,7 @@ constexpr size_t kGroupBytes = size_t(2) << 30;   // operand tiles of the sequen
 
 RowsPlan rows_plan(const rq_q8_shape& s, int n_new, int max_ctx, int window, int n_sink) {
   RowsPlan p = {};
-  p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas), kTickets);
+  p.line = q8_layout(s, n_new, max_ctx, kBlockRows, kKeys, std::min(device_sm_count(), kMostCtas));
   p.total = p.line.total;
   const int64_t rows = int64_t(n_new) * (s.n_q_heads / s.n_kv_heads);
   p.list = rows_list(s, n_new, max_ctx, window, n_sink);
@@ -846,7 +840,7 @@ cudaError_t launch_q8_rows(const rq_q8_shape& s, const rq_q8_cache& cache, const
   const RowsPlan p = rows_plan(s, c.n_new, c.max_ctx, c.window, c.n_sink);
   RowsArgs a = {};
   static_cast<Q8Line&>(a) = q8_line(s, cache, paging, c, kBlockRows);
-  q8_place(a, p.line, ws, kTickets);
+  q8_place(a, p.line, ws);
   a.least = 2;
   a.images = static_cast<uint8_t*>(ws) + p.line.total;
   a.list = p.list;

@@ -32,12 +32,6 @@ struct StreamArgs : Q8Line {
   uint8_t* queries;      // [B][Hkv][blocks] of StreamSmem::kQuery bytes
 };
 
-// A divided unit: its rows, the CTAs that share it.  By the CTA where it begins; no rows: none does.
-struct Parted {
-  int b, h, r0, rows, first, last, pad[2];
-};
-constexpr int kTickets = sizeof(Parted) / 4;   // (they lie where tickets would)
-
 template <int D, int NT>
 struct StreamSmem {
   static constexpr int kCtas = NT == 1 ? 3 : 2, kThreads = NT > 1 ? 256 : 160;
@@ -99,7 +93,7 @@ __global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__
   if (blockIdx.x == 0) {
     if (a.own_cut) {
       if (threadIdx.x == 0) *a.err = 0u;
-      for (int i = threadIdx.x; i < a.n_ctas * kTickets; i += 128) a.tickets[i] = 0u;
+      for (int i = threadIdx.x; i < a.n_ctas; i += 128) a.parted[i].rows = 0;
     } else {
       cut_line<8 * NT, kQ8Tile, 128>(a);
     }
@@ -165,7 +159,7 @@ __global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__
 template <int D, int NT>
 __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_constant__ StreamArgs a) {
   grid_wait();
-  const Parted u = reinterpret_cast<const Parted*>(a.tickets)[blockIdx.x];
+  const Parted u = a.parted[blockIdx.x];
   const int y0 = int(blockIdx.y) * 2;
   if (y0 >= u.rows) return;
   constexpr int CH = D / 16, kRows = 8 * NT, TOGETHER = 4, kRow = D + 4;
@@ -577,7 +571,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
       if (!whole && w.kt0 == 0 && threadIdx.x == 0) {       // (told by the CTA where the unit begins)
         int first, last;
         w.sharers(cut.N, cut.used, first, last);
-        reinterpret_cast<Parted*>(a.tickets)[me] = {w.b, w.h, r0, x.rows, first, last, {0, 0}};
+        a.parted[me] = {w.b, w.h, r0, x.rows, first, last};
       }
       consumers_sync();                                     // (the next segment overwrites what was read)
     }
@@ -591,7 +585,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
 int tiles_of_rows(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 Q8Layout stream_layout(const rq_q8_shape& s, int n_new, int max_ctx, int nt) {
-  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas), kTickets);
+  return q8_layout(s, n_new, max_ctx, 8 * nt, kQ8Tile, std::min(device_sm_count() * (nt == 1 ? 3 : 2), kMostCtas));
 }
 
 size_t query_bytes(const rq_q8_shape& s, int n_new, int nt) {
@@ -610,8 +604,25 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t stream) {
   q8_prepare_kernel<D, NT><<<1 + unsigned(a.B) * a.v.H * a.blocks, 128, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_after(true, q8_stream_kernel<D, NT, FMT>, dim3(unsigned(a.n_ctas)), L::kThreads, L::total, stream, a)) != cudaSuccess) return e;
+  if (a.whole) return cudaSuccess;                          // (nothing to join)
   const int rows = int(std::min<int64_t>(8 * NT, int64_t(a.c.n_new) * a.G));
   return launch_after(true, q8_stream_join_kernel<D, NT>, dim3(unsigned(a.n_ctas), unsigned((rows + 1) / 2)), 256, 0, stream, a);
+}
+
+// Whether units stay whole, which saves the launch that joins their parts.  That launch costs what about
+// four more tiles on a CTA cost, a fourth of it where few units leave most CTAs idle; and no more than
+// eight tiles, as one long sequence among short ones is then a CTA's.  After 250 slots, 16 heads each:
+// 16 sequences 16.1 -> 12.4 us, 8 14.1 -> 11.9; 32 sequences of 8 heads with 16 rows each 24.9 -> 15.3.
+// Against the rule: 8 heads after 500 slots 9.3 -> 12.0, 512 heads 22.6 -> 25.7.
+bool whole_units(const StreamArgs& a) {
+  int64_t tiles = (std::min<int64_t>(int64_t(a.c.max_ctx) + a.c.n_new, a.cap) + kQ8Tile - 1) / kQ8Tile;
+  if (a.c.window > 0) {
+    const int64_t sinks = (int64_t(a.c.n_sink) + kQ8Tile - 1) / kQ8Tile;
+    tiles = std::min(tiles, sinks + (int64_t(a.c.window) + a.c.n_new + kQ8Tile - 1) / kQ8Tile + 1);
+  }
+  const int64_t units = int64_t(a.B) * a.v.H * a.blocks, ctas = a.n_ctas;
+  const int64_t whole = (units + ctas - 1) / ctas * tiles, divided = (units * tiles + ctas - 1) / ctas;
+  return tiles <= 8 && whole - divided <= (4 * units >= ctas ? 4 : 1);
 }
 
 }  // namespace
@@ -627,9 +638,10 @@ cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, con
   StreamArgs a = {};
   static_cast<Q8Line&>(a) = q8_line(s, cache, paging, c, 8 * nt);
   const Q8Layout x = stream_layout(s, c.n_new, c.max_ctx, nt);
-  q8_place(a, x, ws, kTickets);
+  q8_place(a, x, ws);
   a.queries = static_cast<uint8_t*>(ws) + x.total;
   a.own_cut = int64_t(a.B) * a.blocks <= kOwnCutPairs;
+  a.whole = a.own_cut && whole_units(a);
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;
   switch (nt) {
     case 1:

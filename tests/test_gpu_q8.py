@@ -510,6 +510,34 @@ def test_wide_batches(n, heads):
     c.check()
 
 
+SHORT = [
+    # B, Hq, H, d, fmt, longest, n_new, more
+    (4, 8, 8, 128, "e4m3", 63, 1, {}),
+    (40, 16, 16, 64, "int8", 380, 1, dict(rot=64)),
+    (28, 16, 16, 128, "e4m3", 500, 1, dict(paged=True)),
+    (40, 24, 24, 64, "e4m3", 200, 1, {}),
+    (70, 16, 4, 64, "int8", 250, 4, dict(rot=32)),
+    (90, 8, 2, 128, "e4m3", 300, 5, dict(paged=True, rot=128)),
+    (40, 16, 2, 64, "int8", 120, 4, dict(spread=True)),
+    (60, 4, 4, 64, "e4m3", 900, 1, dict(window=150, sinks=70, paged=True)),
+    (60, 8, 4, 128, "int8", 700, 6, dict(window=33)),
+]
+
+
+@pytest.mark.parametrize("B,Hq,H,d,fmt,longest,n,more", SHORT)
+def test_many_short_sequences(B, Hq, H, d, fmt, longest, n, more):
+    """Contexts so short that no unit is divided, of all lengths, some without tokens."""
+    rng = np.random.default_rng(B + n)
+    ctx = rng.integers(0, longest + 1, B)
+    ctx[B // 3] = longest
+    ctx[: B // 4 : 5] = 0
+    c = Case(B, Hq, H, d, fmt, ctx.tolist(), n, rng.integers(0, n + 1, B).tolist(), fill=False, **more)
+    fill_cache(c)
+    c.append()
+    c.attend()
+    c.check()
+
+
 @pytest.mark.parametrize("n", [1, 4, 50, 300])
 def test_blocks_of_very_different_sizes(n):
     """V's and K's scales from 2^-100 (zeros) over 2^-20 to 2^10 in one context."""
