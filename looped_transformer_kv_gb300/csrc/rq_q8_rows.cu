@@ -173,7 +173,10 @@ struct Converter {
   __device__ __forceinline__ int64_t record(const Rows& x, int b, int h, int v) const {
     if (v >= x.tiles) return -2;
     const int64_t r = a.v.record(b, h, x.tile(v));
-    if (r == -1) atomicOr(a.err, 1u);
+    if (r == -1) {
+      grid_wait();                                           // (the kernel before clears it)
+      atomicOr(a.err, 1u);
+    }
     return r;
   }
   __device__ __forceinline__ void load(uint4 (&reg)[PIECES], int kv) const {
@@ -245,8 +248,10 @@ struct Converter {
   }
 };
 
-// The schedule, and beside it the operand tiles of the queries: a row tile a CTA, 16
-// rows a warp.
+// The schedule, and beside it the operand tiles of the queries, kQueryRows rows a warp (bound by the
+// latency of angles and queries: with 16 rows a warp, four rounds, 17 tokens of 3 sequences 15.7 us, with four 14.0).
+constexpr int kQueryRows = 4, kQueryParts = kRowTile / (8 * kQueryRows);   // CTAs of a row tile
+
 template <int D>
 __global__ void __launch_bounds__(256, 4) q8_query_kernel(const __grid_constant__ RowsArgs a) {
   grid_next();
@@ -255,29 +260,32 @@ __global__ void __launch_bounds__(256, 4) q8_query_kernel(const __grid_constant_
     cut_line<kBlockRows, kKeys, 256>(a);
     return;
   }
-  const unsigned tile = blockIdx.x - 1;
+  const unsigned tile = (blockIdx.x - 1) / kQueryParts, part = (blockIdx.x - 1) % kQueryParts;
   const int unit = int(tile / unsigned(a.row_tiles)), b = unit / a.v.H, h = unit % a.v.H;
   const int t = int(tile % unsigned(a.row_tiles));
   const Rows x = sequence_of(a, b);
   const int live = x.ok ? x.n * a.G - t * kRowTile : 0;
   if (live <= 0) return;
   uint8_t* const image = a.queries + (int64_t(unit) * a.row_tiles + t) * L::kQueryImage;
-  put_queries<D, 16>(a, x, b, h, t * kRowTile, int(threadIdx.x >> 5) * 16, live, image, reinterpret_cast<float*>(image + L::kTile),
-                    threadIdx.x & 31);
+  put_queries<D, kQueryRows>(a, x, b, h, t * kRowTile, int(part * 8 + (threadIdx.x >> 5)) * kQueryRows, live, image,
+                             reinterpret_cast<float*>(image + L::kTile), threadIdx.x & 31);
 }
 
-// Operand tiles of K and V: 128 threads each for one key tile.  Bound by HBM: 14,336 + 2,048 slots of 8
+// Operand tiles of K and V: 128 threads each for one key tile.  They need nothing of the queries' kernel and
+// run beside it; it is complete when this one is.  Bound by HBM: 14,336 + 2,048 slots of 8
 // heads, 33 MB of codes to 67 MB of operands, in 19 us.
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ RowsArgs a) {
-  grid_wait();
   grid_next();
   using L = RowsSmem<D>;
   const int lane = threadIdx.x & 31, kv = threadIdx.x >> 7;
   const int u = int(blockIdx.x % unsigned(a.list));
   const int unit = int(blockIdx.x / unsigned(a.list)), b = unit / a.v.H, h = unit % a.v.H;
   const Rows x = sequence_of(a, b);
-  if (2 * u >= x.tiles) return;
+  if (2 * u >= x.tiles) {
+    grid_wait();
+    return;
+  }
   Converter<D, FMT> to(a, threadIdx.x & 127, lane);
   to.rec[0] = to.record(x, b, h, 2 * u);
   to.rec[1] = to.record(x, b, h, 2 * u + 1);
@@ -288,6 +296,7 @@ __global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ R
   uint8_t* const image = a.images + (int64_t(unit) * a.list + u) * L::kImage;
   to.put(reg, image + kv * L::kTile, kv);
   if (threadIdx.x == 0) *reinterpret_cast<int2*>(image + 2 * L::kTile) = e;
+  grid_wait();
 }
 
 // Exponents of tile t of the walk's segment.
@@ -820,7 +829,7 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t stream) {
     return cudaFuncSetAttribute(q8_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
   });
   if (e != cudaSuccess) return e;
-  q8_query_kernel<D><<<1 + unsigned(a.B) * a.v.H * unsigned(a.row_tiles), 256, 0, stream>>>(a);
+  q8_query_kernel<D><<<1 + unsigned(a.B) * a.v.H * unsigned(a.row_tiles) * kQueryParts, 256, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after(true, q8_image_kernel<D, FMT>, dim3(unsigned(a.B) * a.v.H * unsigned(a.list)), 256, 0, stream, a);
   if (e != cudaSuccess) return e;
