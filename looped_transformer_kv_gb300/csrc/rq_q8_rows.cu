@@ -306,10 +306,9 @@ __device__ __forceinline__ const int2* image_exps(const RowsArgs& a, const W& w,
                                        2 * RowsSmem<D>::kTile);
 }
 
-// Place of 8 channels of a row among a row tile's results on their way out.
-template <int D>
-__device__ __forceinline__ int result_place(int r, int chunk) {
-  return r * (D * 2) + ((chunk ^ (r & (D / 8 - 1))) << 4);
+__device__ __forceinline__ void store32(void* to, const uint4& a, const uint4& b) {   // 32 bytes, aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
 }
 __device__ __forceinline__ uint4 bf16_row(const float (&v)[8], float inv) {
   uint32_t p[4];
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
     for (int i = 0; i < 5; ++i) mbar_init(bar0 + 8 * i, 1);
     for (int i = 5; i < 15; ++i) mbar_init(bar0 + 8 * i, 1);
     for (int i = 15; i < 19; ++i) mbar_init(bar0 + 8 * i, kRowTile);
-    mbar_init(qready, 2);
+    mbar_init(qready, 3);                                    // the copy, both softmax groups
     mbar_init(drained, 1);
     fence_mbar_init();
   }
@@ -369,17 +368,30 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
     if (warp == 9 && leader) {                        // ---- copies of operand tiles
       RowWalk& w = walks[3];
       w.begin(from, to_pos);
+      int seg = 0;                                           // segments whose queries are on their way
       int g = 0, n0 = 0;                                     // tiles so far; g's step is n0 + g
       int sk[3] = {-1, -1, -1};                              // steps that end with K tile g - 1, g - 2, g - 3
       while (!failed && w.next(a)) {
         if (!w.x.ok) continue;
         const uint8_t* const unit = a.images + (int64_t(w.b) * a.v.H + w.h) * a.list * RowsSmem<D>::kImage;
+        const uint8_t* const queries = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + w.block * (kBlockRows / kRowTile)) * L::kQueryImage;
+        const int row_tiles = w.x.rows > kRowTile ? 2 : 1;
         for (int t = 0; t < w.T; ++t, ++g) {
           const uint8_t* const tile = unit + w.x.step(w.kt0 + t) * int64_t(RowsSmem<D>::kImage);
           if (g >= 3) failed = !mbar_wait_bounded(step(sk[2]), (sk[2] >> 3) & 1, kWaitNs);
           if (failed) break;
           mbar_arrive_expect_tx(kfull(g), L::kTile);
           bulk_g2s(smem_u32(smem + L::k + (g % 3) * L::kTile), tile, L::kTile, kfull(g));
+          if (t == 0) {                                      // queries, once the last scores need those before no more
+            if (g > 0) failed = !mbar_wait_bounded(step(sk[0]), (sk[0] >> 3) & 1, kWaitNs);
+            if (failed) {
+              ++g;
+              break;
+            }
+            mbar_arrive_expect_tx(qready, row_tiles * L::kTile);
+            for (int i = 0; i < row_tiles; ++i) bulk_g2s(smem_u32(smem + L::q + i * L::kTile), queries + i * L::kQueryImage, L::kTile, qready);
+            ++seg;
+          }
           if (g >= 2) failed = !mbar_wait_bounded(step(sk[1] + 1), ((sk[1] + 1) >> 3) & 1, kWaitNs);
           if (failed) {
             ++g;
@@ -396,6 +408,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
       // copies land before the CTA leaves
       for (int k = max(0, g - 3); failed && k < g; ++k) mbar_wait_bounded(kfull(k), (k / 3) & 1, kWaitNs);
       for (int k = max(0, g - 2); failed && k < g; ++k) mbar_wait_bounded(vfull(k), (k >> 1) & 1, kWaitNs);
+      if (failed && seg > 0) mbar_wait_bounded(qready, (seg - 1) & 1, kWaitNs);
     } else if (warp == 8 && leader) {                        // ---- products
       constexpr uint32_t ids = f16_idesc(kRowTile, kKeys), ido = f16_idesc(kRowTile, D) | (1u << 16);   // (B: channels contiguous)
       int g = 0, c0 = 0, c1 = 0, n = 0, seg = 0;             // tiles; P's of row tile 0, 1; steps; segments
@@ -464,7 +477,6 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
     const int i = warp >> 2, r = threadIdx.x & (kRowTile - 1);
     const uint32_t lanes = uint32_t(warp & 3) << 21;          // this warp's tensor-memory lanes
     const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
-    uint8_t* const img = smem + L::q + i * L::kTile;          // queries, then results going out
     float4* const stats = reinterpret_cast<float4*>(a.stats);
     int g = 0, n0 = 0, s0 = 0;
     RowWalk& w = walks[i];                                     // the group's first thread walks
@@ -478,14 +490,10 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
       const int r0 = w.block * kBlockRows + i * kRowTile;      // the row tile's first row
       const bool two = x.rows > kRowTile, mine = i == 0 || two;
       const int row = r0 + r;
-      // ---- queries
       float factor = 0.f;
       if (x.ok && !failed) {
         const uint8_t* const image = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + r0 / kRowTile) * L::kQueryImage;
-        if (r == 0) {
-          mbar_arrive_expect_tx(qready, mine ? L::kTile : 0);
-          if (mine) bulk_g2s(smem_u32(img), image, L::kTile, qready);
-        }
+        if (r == 0) mbar_arrive(qready);                       // (the products keep to a segment with both groups)
         if (mine) factor = *reinterpret_cast<const float*>(image + L::kTile + 4 * r);
       }
       // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
@@ -660,8 +668,9 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         tc_fence_before();
         continue;
       }
-      constexpr int CR = D / 8;                                // 16-byte chunks of a row of bf16
       const float inv = there ? (l == 0.f ? 0.f : 1.f / l) : nan;
+      uint16_t* const out = a.c.out + ((int64_t(w.b) * a.c.n_new + row / a.G) * a.Hq + w.h * a.G + row % a.G) * D;
+      const uintptr_t odd = reinterpret_cast<uintptr_t>(a.c.out) & 31;
 #pragma unroll 1
       for (int y = 0; y < D / 32; ++y) {
         uint32_t o[32];
@@ -671,39 +680,35 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
           tc_ld32(tO + 32 * y, o);
           tc_wait_ld();
         }
+        if (!valid) continue;
+        uint4 q[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           float v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[8 * z + k]);
-          *reinterpret_cast<uint4*>(img + result_place<D>(r, 4 * y + z)) = bf16_row(v, inv);
+          q[z] = bf16_row(v, inv);
         }
-      }
-      __syncwarp();
-      const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
-      // place of the row that this lane stands for (the rows of the warp in turn, below)
-      const int j = row / a.G, hq = w.h * a.G + row % a.G;
-      const int64_t out_row = ((int64_t(w.b) * a.c.n_new + j) * a.Hq + hq) * D;
-#pragma unroll 4
-      for (int k = lane; k < 32 * CR; k += 32) {               // this warp's rows, 16 bytes a lane
-        const int rr = (warp & 3) * 32 + k / CR, cc = k % CR;
-        uint16_t* const o = a.c.out + __shfl_sync(RQ_FULL_MASK, out_row, k / CR) + 8 * cc;
-        if (i * kRowTile + rr >= x.rows) continue;
-        const uint4 u = *reinterpret_cast<const uint4*>(img + rr * (D * 2) + ((cc ^ (rr & (CR - 1))) << 4));
-        if (vec) {
-          *reinterpret_cast<uint4*>(o) = u;
+        if (odd == 0) {                                        // (whole sectors)
+          store32(out + 32 * y, q[0], q[1]);
+          store32(out + 32 * y + 16, q[2], q[3]);
         } else {
-          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            o[2 * z] = uint16_t(q[z]);
-            o[2 * z + 1] = uint16_t(q[z] >> 16);
+            uint16_t* const to = out + 32 * y + 8 * z;
+            if (odd == 16) {
+              *reinterpret_cast<uint4*>(to) = q[z];
+              continue;
+            }
+            const uint32_t u[4] = {q[z].x, q[z].y, q[z].z, q[z].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              to[2 * k] = uint16_t(u[k]);
+              to[2 * k + 1] = uint16_t(u[k] >> 16);
+            }
           }
         }
       }
-      // (the next queries overwrite the rows; the copy's are the other proxy's)
-      // (the walk's first barrier follows)
-      fence_async_smem();
       tc_fence_before();
     }
   }
