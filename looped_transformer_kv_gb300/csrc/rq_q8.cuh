@@ -49,6 +49,10 @@ __device__ __forceinline__ uint4 q8_load8(const uint16_t* p, bool vec) {
   for (int k = 0; k < 4; ++k) w[k] = uint32_t(p[2 * k]) | (uint32_t(p[2 * k + 1]) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ uint2 q8_load4(const uint16_t* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint2*>(p);
+  return make_uint2(uint32_t(p[0]) | (uint32_t(p[1]) << 16), uint32_t(p[2]) | (uint32_t(p[3]) << 16));
+}
 __device__ __forceinline__ void q8_floats(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -79,6 +83,13 @@ __device__ __forceinline__ Q8Angles q8_angles(const Q8Rope& rope, int pos, int l
   return r;
 }
 
+// Rotates a pair; each product and sum is rounded.
+__device__ __forceinline__ void q8_turn(float& x, float& y, float c, float s) {
+  const float x0 = x, y0 = y;
+  x = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(y0, s));
+  y = __fadd_rn(__fmul_rn(y0, c), __fmul_rn(x0, s));
+}
+
 // Rotates the row.  Every lane of the warp calls it.
 template <int D>
 __device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, const Q8Angles& r, int lane) {
@@ -86,12 +97,8 @@ __device__ __forceinline__ void q8_rotate(float (&f)[8], const Q8Rope& rope, con
     if (r.turned) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 a = r.a[k];
-        const float x0 = f[4 * k], y0 = f[4 * k + 1], x1 = f[4 * k + 2], y1 = f[4 * k + 3];
-        f[4 * k] = __fsub_rn(__fmul_rn(x0, a.x), __fmul_rn(y0, a.y));
-        f[4 * k + 1] = __fadd_rn(__fmul_rn(y0, a.x), __fmul_rn(x0, a.y));
-        f[4 * k + 2] = __fsub_rn(__fmul_rn(x1, a.z), __fmul_rn(y1, a.w));
-        f[4 * k + 3] = __fadd_rn(__fmul_rn(y1, a.z), __fmul_rn(x1, a.w));
+        q8_turn(f[4 * k], f[4 * k + 1], r.a[k].x, r.a[k].y);
+        q8_turn(f[4 * k + 2], f[4 * k + 3], r.a[k].z, r.a[k].w);
       }
     }
     return;
