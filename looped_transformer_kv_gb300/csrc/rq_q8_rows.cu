@@ -16,7 +16,7 @@
 //
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; warp 9: copies.
 // Bound by a row tile's chain, softmax and then products, two tiles taking turns: 2,048 tokens of 32 heads
-// after 14,336 slots in 344 us, 1,500 TFLOP/s.
+// after 14,336 slots in 338 us, 1,520 TFLOP/s.
 // CTAs (one per SM) share the work by the line of rq_q8_line.cuh; q8_join_kernel joins the partial results
 // of divided units (in this kernel the code for it cost the main loop its registers: 460 against 375 us).
 #include <type_traits>
@@ -270,9 +270,10 @@ struct Converter {
   }
 };
 
-// The schedule, and beside it the operand tiles of the queries, kQueryRows rows a warp (bound by the
-// latency of angles and queries: with 16 rows a warp, four rounds, 17 tokens of 3 sequences 15.7 us, with four 14.0).
-constexpr int kQueryRows = 4, kQueryParts = kRowTile / (8 * kQueryRows);   // CTAs of a row tile
+// The schedule, and beside it the operand tiles of the queries, kQueryRows rows a warp.  (Small calls wait
+// for a warp's rounds of loads, large ones for CTAs that begin: with 4, 8 and 16 rows a warp 17 tokens of 3
+// sequences take 14.1, 14.3 and 15.0 us, 1,023 tokens of 4 x 16 heads 72, 71 and 71.)
+constexpr int kQueryRows = 8, kQueryParts = kRowTile / (8 * kQueryRows);   // CTAs of a row tile
 
 template <int D>
 __global__ void __launch_bounds__(256, 4) q8_query_kernel(const __grid_constant__ RowsArgs a) {
