@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
     const uint32_t lanes = uint32_t(warp & 3) << 21;          // this warp's tensor-memory lanes
     const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
     float4* const stats = reinterpret_cast<float4*>(a.stats);
-    int g = 0, n0 = 0, s0 = 0;
+    int g = 0, n0 = 0, s0 = 0, seg = 0;
     RowWalk& w = walks[i];                                     // the group's first thread walks
     if (r == 0) w.begin(from, to_pos);
     for (;;) {                                                 // (failed: nothing is waited for any more, results are NaN)
@@ -518,15 +518,17 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         const uint8_t* const image = a.queries + ((int64_t(w.b) * a.v.H + w.h) * a.row_tiles + r0 / kRowTile) * L::kQueryImage;
         if (r == 0) mbar_arrive(qready);                       // (the products keep to a segment with both groups)
         if (mine) factor = *reinterpret_cast<const float*>(image + L::kTile + 4 * r);
+        // Group 1 has segments without rows, in which nothing ties it to the products' steps: it waits for
+        // its segment to begin, a phase whose successor needs its own arrival.  (The steps' ring tells one
+        // lap from the next but not from the one after: it could neither run ahead nor poll along.)
+        if (i == 1) failed = group_any(1, !mbar_wait_bounded(qready, seg & 1, kWaitNs));
+        ++seg;
       }
       // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
       // of any size cancel without a residue
       float R = -INFINITY, h = 0.f, l = 0.f, c = 0.f;
-      if (!mine) {                                             // no rows: only keeps step
+      if (!mine) {                                             // no rows
         if (!x.ok || failed) continue;
-        for (int t = 0; t <= w.T && !failed; ++t)
-          failed = !mbar_wait_bounded(step(n0 + g + t), ((n0 + g + t) >> 3) & 1, kWaitNs);
-        failed = group_any(i, failed);
         g += w.T;
         ++n0;
         continue;
