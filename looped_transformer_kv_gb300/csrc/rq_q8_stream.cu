@@ -3,10 +3,12 @@
 //
 //   S[t, r] = q_r . K_t on mma.sync, M = a warp's 16 slots, N = 8 rows; one scale per warp and tile
 //   (a block of 16 slots is a warp's share), so scores are S * scale_K * (softmax scale of the row).
-//   w = 2^(S - m) scale_V 2^-E, fp16; O[ch, r] += V^T w on mma.sync, M = 16 channels, K = the slots.
-// A warp keeps its own m and l (rows), E (all) and accumulators over its slots; the four warps are
-// merged once per segment.  m is raised when a score exceeds it by more than 8, E when a V scale
-// exceeds 2^(E + 7): weights stay below 2^15.
+//   w = 2^(S - m) scale_V 2^-h, fp16; O[ch, r] += V^T w on mma.sync, M = 16 channels, K = the slots.
+// A warp keeps its own m, l, h (rows) and accumulators over its slots; the four warps are merged once per
+// segment.  m is raised when a score exceeds it by more than 8.  h is one number E for all rows, 2^-3 of the
+// first V scale, while V scales stay within 2^4 of that: weights then reach 2^-1 and stay below 2^15.  From
+// the first other scale on every row has its own (`heights`), raised as w exceeds 2^15, to make it 2^7: what a
+// row does not see, or gives no weight, takes nothing from its other weights' 11 bits.
 //
 // CTAs share the work by the line of rq_q8_line.cuh; q8_stream_join_kernel joins the partial results of
 // divided units, and the queries' operands are made by the kernel before (q8_prepare_kernel): code for
@@ -16,6 +18,8 @@
 // launches, first tiles and joins at short contexts (4,096 slots in 55 us, 40 at a copy's rate).  32 rows: by
 // the latency of each warp's scores, softmax and values, two warps a scheduler (8 x 8 heads after 16,384
 // slots in 109 us).
+#include <type_traits>
+
 #include "rq_q8_line.cuh"
 #include "rq_tc.cuh"
 
@@ -24,7 +28,8 @@ namespace {
 
 constexpr float kNoMax = -1e30f;      // m of a row that has seen nothing
 constexpr float kTop = 8.f;
-constexpr int kScaleTop = 7, kScaleHead = 6;
+constexpr int kScaleBelow = 3, kScaleRange = 4;   // E: below the first V scale; how far others may be from that
+constexpr int kNoScale = -1000;       // E before the first V scale
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
 
@@ -41,11 +46,11 @@ struct StreamSmem {
   static constexpr int kFragments = NT * (D / 16) * 32 * 8;
   static constexpr int kQuery = kFragments + kRows * 8;     // of a unit: B fragments, factors, own slots
   static constexpr int kHeld = NT > 2 ? kQuery : kRows * 8;  // of it in shared memory
-  static constexpr int kFixed = kMerge + kHeld + 4 * kRows * 8 + 768;
+  static constexpr int kFixed = kMerge + kHeld + 4 * kRows * 12 + 768;
   static constexpr int kStages0 = (227 * 1024 / kCtas - 1024 - kFixed) / kStage;
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kHeld;
-  static constexpr int bars = stats + 4 * kRows * 8, misc = bars + 16 * kStages;
+  static constexpr int heights = stats + 4 * kRows * 8, bars = heights + 4 * kRows * 4, misc = bars + 16 * kStages;
   static constexpr int cut = misc + 16 * 4 + 4 * 8, walk = cut + int(sizeof(OwnCut));
   static constexpr int total = walk + int(sizeof(Walk<8, kQ8Tile>)) + 128;
   static_assert(kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
   const uint32_t bar0 = smem_u32(smem + L::bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (L::kStages + s); };
-  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up, [4 ..]: a warp's E
+  int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up
   int* const bad_page = misc + 16;                          // [stage]
   OwnCut& cut = *reinterpret_cast<OwnCut*>(smem + L::cut);
   if (threadIdx.x == 0) {
@@ -326,6 +331,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
     const int r = lane >> 2, c = lane & 3;
     float* const merge = reinterpret_cast<float*>(smem + L::merge);
     float2* const stats = reinterpret_cast<float2*>(smem + L::stats);          // [warp][row]
+    float* const heights = reinterpret_cast<float*>(smem + L::heights) + warp * L::kRows;   // h of this warp's rows
     uint8_t* const held = smem + L::query;                  // what is held of the unit's queries: all, or factors and own slots
     const uint2* const query = reinterpret_cast<const uint2*>(held);
     const float* const row_scale = reinterpret_cast<const float*>(held + L::kHeld - L::kRows * 8);
@@ -366,10 +372,12 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
       }
-      int E = -120;
-
-
-      for (int t = 0; x.ok && t < w.T; ++t, ++g) {
+      int E = kNoScale, t = 0;
+      // Tiles from t on; without APART up to one whose V scale is out of E's range.  (Two loops: as one, with
+      // the rows' h behind a branch, verification of 8 tokens took 121 us, now 112.)
+      auto tiles = [&](auto apart) {
+      constexpr bool APART = decltype(apart)::value;
+      for (; x.ok && t < w.T; ++t, ++g) {
         const int s = g % L::kStages;
         if (!dead) dead = !__all_sync(RQ_FULL_MASK, mbar_wait_bounded(full(s), (g / L::kStages) & 1, kWaitNs));
         if (dead) continue;                                 // (the copies' warp gives up in its turn)
@@ -440,39 +448,59 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
               sc[n][k] = hidden >> (4 * n + k) & 1u ? -INFINITY : sc[n][k] * ksc[n][k & 1];
               over |= sc[n][k] > m[n][k & 1] + kTop;
             }
-          const int ev = q8_exponent(vs) > 127 ? E : q8_exponent(vs);
-          const bool lift = ev > E + kScaleTop;
-          if (__any_sync(RQ_FULL_MASK, over) || lift) {
-            const float fe = lift ? q8_pow2(max(E - (ev - kScaleHead), -126)) : 1.f;
-            if (lift) E = ev - kScaleHead;
+          const int ev = q8_exponent(vs);
+          const bool lost = ev > 127, far = !APART && unsigned(ev - E - kScaleBelow + kScaleRange) > 2u * kScaleRange;
+          const float evf = lost ? vs : float(ev);          // (NaN where the scale is)
+          if (APART)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                over |= (sc[n][k] - m[n][k & 1]) + (evf - heights[8 * n + 2 * c + (k & 1)]) > kWeightTop;
+          if (__any_sync(RQ_FULL_MASK, over) || far) {
+            if (far && !lost) {
+              if (E != kNoScale) return;                    // (here and not before the scores, which need not wait for it)
+              E = ev - kScaleBelow;
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
+                const float h = APART ? heights[8 * n + 2 * c + k] : 0.f;
+                if (APART) __syncwarp();                    // (read before one lane of the row's writes)
                 float v = fmaxf(sc[n][k], sc[n][k + 2]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(RQ_FULL_MASK, v, o));
                 const float to = v > m[n][k] + kTop ? v : m[n][k];
                 const float f = ex2(m[n][k] - to);
+                float fa = f;                               // of the accumulators, whose unit is 2^(m + h)
+                if (APART && (v > m[n][k] + kTop || (v - m[n][k]) + (evf - h) > kWeightTop)) {
+                  const float hn = fmaxf(h + (m[n][k] - to), evf + (v - to) - kWeightHead);   // (evf NaN: the first)
+                  fa = ex2((m[n][k] - to) + (h - hn));
+                  if (r == 0) heights[8 * n + 2 * c + k] = hn;
+                }
                 m[n][k] = to;
                 l[n][k] *= f;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
-                  acc[n][i][k] *= f * fe;
-                  acc[n][i][k + 2] *= f * fe;
+                  acc[n][i][k] *= fa;
+                  acc[n][i][k + 2] *= fa;
                 }
               }
+            if (APART) __syncwarp();
           }
-          const float vsc = vs * q8_pow2(-E);
           uint32_t b0[NT], b1[NT];
+          const float vsc = APART ? 1.f : vs * q8_pow2(-E);   // (E == kNoScale: vs is not a number)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              p[k] = ex2(sc[n][k] - m[n][k & 1]);
+              const float z = sc[n][k] - m[n][k & 1];
+              p[k] = ex2(z);
               l[n][k & 1] += p[k];
-              p[k] = hidden >> (4 * n + k) & 1u ? 0.f : p[k] * vsc;
+              p[k] = APART ? ex2(z + (evf - heights[8 * n + 2 * c + (k & 1)])) : p[k] * vsc;
+              if (hidden >> (4 * n + k) & 1u) p[k] = 0.f;
             }
             b0[n] = transposed(pack_half2(p[0], p[1]));
             b1[n] = transposed(pack_half2(p[2], p[3]));
@@ -518,6 +546,11 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(s));
       }
+      };
+      tiles(std::false_type{});
+      if (lane < L::kRows) heights[lane] = float(E);        // (E == kNoScale: acc is 0)
+      __syncwarp();
+      tiles(std::true_type{});
 
       // ---- the four warps' results joined, eight rows at a time
       if (dead && lane == 0) atomicExch(&misc[0], 1);
@@ -529,9 +562,9 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           for (int o = 4; o < 32; o <<= 1) l[n][k] += __shfl_xor_sync(RQ_FULL_MASK, l[n][k], o);
           if (r == 0) stats[warp * L::kRows + 8 * n + 2 * c + k] = make_float2(m[n][k], l[n][k]);
         }
-      if (lane == 0) misc[4 + warp] = E;
       const bool whole = w.kt0 == 0 && w.T == x.V;
       const int slot = 2 * me + (w.kt0 == 0 ? 1 : 0);
+      const float* const all_heights = reinterpret_cast<const float*>(smem + L::heights);
       const int mr = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH;   // row, channels of a thread
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -552,7 +585,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 st = stats[k * L::kRows + y];
-          const float f = ex2(st.x - M), fe = f * q8_pow2(misc[4 + k]);
+          const float f = ex2(st.x - M), fe = f * ex2(all_heights[k * L::kRows + y]);
           sum += f * st.y;
           const float* const p = merge + (k * 8 + mr) * L::kMergeRow + ch;
 #pragma unroll

@@ -8,9 +8,7 @@ import q8_reference as R
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-if torch.cuda.is_available():
-    import looped_transformer_kv_gb300 as rq  # noqa: F401
-    from test_gpu_q8 import MARK, Case, fill_cache
+from test_gpu_q8 import MARK, Case, fill_cache  # noqa: E402
 
 
 @pytest.mark.parametrize("B,n,longest", [(60, 40, 600), (60, 100, 2500), (60, 300, 900), (12, 300, 6000)])
@@ -27,3 +25,127 @@ def test_row_tiles_without_rows(B, n, longest):
         c.out.fill_(MARK)
         c.attend()
     c.check()
+
+
+class Hand(Case):
+    """One sequence whose rows are given, the same for all H kv-heads: k, v [ctx + n][d], q [n][G][d].  (With
+    one head a context is divided among CTAs, with many a CTA walks it.)"""
+
+    def __init__(self, k, v, q, fmt, H=1, **more):
+        n, G, d = q.shape
+        ctx = len(k) - n
+        super().__init__(1, G * H, H, d, fmt, [ctx], n, fill=False, **more)
+        kv = torch.from_numpy(np.stack([k, v], 1).astype(np.float32)).bfloat16()
+        R.append(self.codes[0, 0, :, 0], self.scales[0, 0, :, 0], kv[:ctx].float().numpy(), 0, fmt)
+        self.codes[:], self.scales[:] = self.codes[:, :1], self.scales[:, :1]
+        self.put()
+        self.kv_host = kv[ctx:].view(1, n, 2, 1, 1, d).expand(1, n, 2, 1, H, d).contiguous()
+        self.q_host = torch.from_numpy(np.concatenate([q] * H, 1).astype(np.float32)).bfloat16()[None].contiguous()
+        self.kv, self.q = self.kv_host.cuda(), self.q_host.cuda()
+
+    def run(self):
+        self.append()
+        self.attend()
+        assert self.error_word() == 0
+        return self
+
+
+def close(c, tokens=slice(None)):
+    """Outputs of a case of one sequence against the reference over the cache that the GPU holds.
+
+    Everything goes by what a row sees and how much it weighs.  A score's error e: the fp32 sum of d products
+    and its scaling, (d + 8) 2^-23 of its sum |q k|; the row's reference is subtracted, and the exponents of
+    scales (at most 2^8 in all) added, in fp32: 2^-23 of the largest such sum among slots that matter, and
+    2^-15.  A weight is off by expm1(e), and so is its share of the sum.  Times its block's scale it is
+    rounded to fp16: 2^-11 of itself, or 2^-24 of the largest product of weight and scale that the row sees
+    (which is 2^-1 or more in units where fp16's last half step is 2^-25); fp32 sums (T / 16 + 64) 2^-23,
+    twice; the result 2^-8 of itself."""
+    codes, scales = c.get()
+    assert (codes == codes[:, :1]).all() and ((scales == scales[:, :1]) | np.isnan(scales)).all()
+    G, d, m, ctx = c.Hq // c.H, c.d, c.n_new, c.ctx[0]
+    T = ctx + m
+    out = c.out.double().cpu().numpy().reshape(m, c.H, G, d)
+    k, v = R.rows_of(codes[0, 0, :, 0], scales[0, 0, :, 0], T, d, c.fmt)
+    q = c.q_host[0, :, :G].double().numpy()
+    block = np.repeat(scales[0, 0, :, 0, 1].reshape(-1).astype(np.float64), 16)[:T]
+    own, t = (ctx + np.arange(m))[:, None], np.arange(T)[None]
+    seen = t <= own
+    if c.window:
+        seen &= (t > own - c.window) | (t < c.sinks)
+    s = np.einsum("jgd,td->jgt", q, k) * c.scale
+    s = np.where(seen[:, None], s, -np.inf)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    ref = np.einsum("jgt,td->jgd", p, v)
+    pv = np.einsum("jgt,td->jgd", p, np.abs(v))
+    mag = np.einsum("jgd,td->jgt", np.abs(q), np.abs(k)) * c.scale * seen[:, None]
+    best = np.where(p > 1e-9, mag, 0).max(-1, keepdims=True)
+    u = p * np.expm1(np.minimum((mag + best) * (d + 8) * 2.0 ** -23 + 2.0 ** -15, 60))
+    assert np.median(u[tokens].sum(-1)) < 2.0 ** -6                        # (the test means something)
+    tol = 2 * (np.einsum("jgt,td->jgd", u, np.abs(v)) + np.abs(ref) * u.sum(-1)[..., None])
+    tol += pv * (2.0 ** -11 + 2 * (T / 16 + 64) * 2.0 ** -23)
+    most = (p * block).max(-1)[..., None]
+    tol += 2.0 ** -24 * most * np.einsum("jt,td->jd", seen.astype(np.float64), np.abs(v) / block[:, None])[:, None]
+    tol += 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-37
+    worst = (np.abs(out - ref[:, None]) / tol[:, None])[tokens].max()
+    assert worst <= 1, worst
+
+
+FEW = [(2, 1), (2, 4), (4, 4), (8, 4)]          # tokens, query heads: 2, 8, 16, 32 rows
+ONE = [(1, 1), (1, 8)]
+
+
+def normal(seed, *shape):
+    return np.random.default_rng(seed).standard_normal(shape)
+
+
+def slots_of(n, T=200):
+    """A context for n new tokens of which the last begins a block of 16 slots."""
+    return -(-(T + n) // 16) * 16 + 1
+
+
+def aimed(seed, n, G, d):
+    """Queries that lie along one direction, and the direction."""
+    u = normal(seed, d)
+    u /= np.linalg.norm(u)
+    return 8 * u + 0.1 * normal(seed + 1, n, G, d), u
+
+
+@pytest.mark.parametrize("far", [12, 30, 60, 100])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", FEW)
+def test_the_last_token_s_large_value_changes_no_earlier_output(n, G, fmt, far, H):
+    T, d = slots_of(n), 128 if n % 8 else 64
+    k, v, q = normal(1, T, d) / 2, normal(2, T, d), normal(3, n, G, d)
+    v[-1] *= 2.0 ** far
+    close(Hand(k, v, q, fmt, H).run())
+
+
+@pytest.mark.parametrize("far", [12, 30, 60, 100])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", FEW)
+def test_a_large_value_that_left_the_window(n, G, far, H):
+    """Only the first token's window reaches the slot; the other slots of its block are out of every window."""
+    window, d = 289, 128 if n % 8 else 64
+    ctx = 600 + 15 - (600 + 1 - window) % 16
+    assert (ctx + 1 - window) % 16 == 15
+    T = ctx + n
+    k, v, q = normal(27, T, d) / 2, normal(28, T, d), normal(29, n, G, d)
+    v[ctx + 1 - window] *= 2.0 ** far
+    close(Hand(k, v, q, "e4m3" if far % 4 else "int8", H, window=window).run())
+
+
+@pytest.mark.parametrize("far", [12, 30, 38])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", ONE + FEW)
+def test_large_values_of_no_weight(n, G, fmt, far, H):
+    """A block whose values are 2^far larger at weights of e^-60."""
+    T, d = slots_of(n, 300), 128 if n % 8 else 64
+    q, u = aimed(4, n, G, d)
+    k, v = normal(5, T, d) / 4, normal(6, T, d)
+    for block in (slice(32, 48), slice(192, 208)):
+        k[block] = -60 * d ** 0.5 / 8 * u + normal(7, 16, d) / 4
+        v[block] *= 2.0 ** far
+    close(Hand(k, v, q, fmt, H).run())
