@@ -26,7 +26,7 @@
 namespace rq {
 namespace {
 
-constexpr float kNoMax = -1e30f;      // m of a row that has seen nothing
+constexpr float kNoMax = -3.402823466e38f;   // m of a row that has seen nothing: no finite score is below it
 constexpr float kTop = 8.f;
 constexpr int kScaleBelow = 3, kScaleRange = 4;   // E: below the first V scale; how far others may be from that
 constexpr int kNoScale = -1000;       // E before the first V scale

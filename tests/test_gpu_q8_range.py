@@ -92,6 +92,7 @@ def close(c, tokens=slice(None)):
 
 
 FEW = [(2, 1), (2, 4), (4, 4), (8, 4)]          # tokens, query heads: 2, 8, 16, 32 rows
+MANY = [(40, 1), (64, 4), (300, 1)]
 ONE = [(1, 1), (1, 8)]
 
 
@@ -149,3 +150,20 @@ def test_large_values_of_no_weight(n, G, fmt, far, H):
         k[block] = -60 * d ** 0.5 / 8 * u + normal(7, 16, d) / 4
         v[block] *= 2.0 ** far
     close(Hand(k, v, q, fmt, H).run())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
+def test_scores_far_below_zero(n, G, fmt, H):
+    """All scores near -1e32, one the largest by far: the output is its value row."""
+    T, d = n + 150, 64
+    q = np.zeros((n, G, d))
+    q[:, :, 5] = 2.0 ** 50
+    k = np.zeros((T, d))
+    k[:, 5] = -2.0 ** 60 * (1.5 + np.arange(T) % 7 / 8)
+    k[3, 5] = -2.0 ** 60
+    c = Hand(k, normal(11, T, d), q, fmt, H).run()
+    codes, scales = c.get()
+    v = R.rows_of(codes[0, 0, :, 0], scales[0, 0, :, 0], T, d, fmt)[1][3]
+    assert (np.abs(c.out[0].double().cpu().numpy() - v) <= 2.0 ** -8 * np.abs(v)).all()
