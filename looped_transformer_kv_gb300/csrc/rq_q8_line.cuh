@@ -32,7 +32,7 @@ struct Q8Line {
   Parted* parted;        // [CTA] the unit that begins in its stretch and goes on behind it
   int64_t* prefix;       // [B * blocks + 1] places of (sequence, block)
   Cut* cut;              // [CTA + 1]
-  float2* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] (m, l); or four floats each
+  float4* stats;         // [2 CTA + (0: the unit began before, 1: goes on)][rows] maxima, sums, units
   float* part;           // ... their sums
   int32_t n_ctas;
   int32_t clear;         // the call's first launch
@@ -320,7 +320,7 @@ inline void q8_place(Q8Line& a, const Q8Layout& x, void* ws) {
   a.parted = reinterpret_cast<Parted*>(base + x.parted);
   a.prefix = reinterpret_cast<int64_t*>(base + x.prefix);
   a.cut = reinterpret_cast<Cut*>(base + x.cut);
-  a.stats = reinterpret_cast<float2*>(base + x.stats);
+  a.stats = reinterpret_cast<float4*>(base + x.stats);
   a.part = reinterpret_cast<float*>(base + x.part);
   a.n_ctas = x.n_ctas;
   a.clear = 1;

@@ -500,7 +500,6 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
     const int i = warp >> 2, r = threadIdx.x & (kRowTile - 1);
     const uint32_t lanes = uint32_t(warp & 3) << 21;          // this warp's tensor-memory lanes
     const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + 128 * i + lanes;
-    float4* const stats = reinterpret_cast<float4*>(a.stats);
     int g = 0, n0 = 0, s0 = 0, seg = 0;
     RowWalk& w = walks[i];                                     // the group's first thread walks
     if (r == 0) w.begin(from, to_pos);
@@ -673,7 +672,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         w.sharers(a.prefix[int64_t(a.B) * a.blocks], *a.used, first, last);
         const int64_t at = (2 * int64_t(me) + (w.kt0 == 0)) * kBlockRows + i * kRowTile;
         float* const part = a.part + at * D;                   // [D / 4][128 rows][4]
-        stats[at + r] = make_float4(R * c, h, there ? l : nan, 0.f);
+        a.stats[at + r] = make_float4(R * c, h, there ? l : nan, 0.f);
 #pragma unroll 1
         for (int y = 0; y < D / 32; ++y) {
           uint32_t o[32];
@@ -752,7 +751,6 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
   const Parted u = a.parted[blockIdx.x];
   const int row = int(blockIdx.y) * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
   if (row >= u.rows) return;
-  const float4* const stats = reinterpret_cast<const float4*>(a.stats);
   const int tile = row / kRowTile * kRowTile, r = row % kRowTile;
   auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kBlockRows + tile; };
   float M = -INFINITY, h = 0.f, sum = 0.f, o[16];
@@ -764,7 +762,7 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
     for (int e = 0; e < 4; ++e) {
       st[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       if (k + e > u.last) continue;
-      st[e] = stats[place(k + e) + r];
+      st[e] = a.stats[place(k + e) + r];
       const float4* const part = reinterpret_cast<const float4*>(a.part + place(k + e) * D) + 4 * y * kRowTile + r;
 #pragma unroll
       for (int z = 0; z < 4; ++z) v[e][z] = part[z * kRowTile];

@@ -29,7 +29,7 @@ namespace {
 constexpr float kNoMax = -3.402823466e38f;   // m of a row that has seen nothing: no finite score is below it
 constexpr float kTop = 8.f;
 constexpr int kScaleBelow = 3, kScaleRange = 4;   // E: below the first V scale; how far others may be from that
-constexpr int kNoScale = -1000;       // E before the first V scale
+constexpr int kNoScale = -1000;       // E before the first V scale (and h of sums that hold nothing)
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
 
@@ -64,17 +64,18 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// CH channels of a unit's row y, times inv.
+// CH channels of a unit's row y, times inv 2^unit (the unit last, in two steps: it brings back V's size).
 template <int D, int CH>
-__device__ __forceinline__ void store_row(const Q8Line& a, int b, int h, int r0, int y, int rows, int ch, const float (&o)[CH], float inv) {
+__device__ __forceinline__ void store_row(const Q8Line& a, int b, int h, int r0, int y, int rows, int ch, const float (&o)[CH], float inv, float unit) {
   if (y >= rows) return;
   const int j = (r0 + y) / a.G, hq = h * a.G + (r0 + y) % a.G;
   uint16_t* const p = a.c.out + ((int64_t(b) * a.c.n_new + j) * a.Hq + hq) * D + ch;
   const bool vec = (reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0;
   uint32_t u[CH / 2];
+  const float up = ex2(0.5f * unit);
 #pragma unroll
   for (int k = 0; k < CH / 2; ++k) {
-    const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv * up * up, o[2 * k + 1] * inv * up * up);
     u[k] = *reinterpret_cast<const uint32_t*>(&z);
   }
   if (vec && CH == 8)
@@ -160,7 +161,22 @@ __global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__
 }
 
 // The parts of a divided unit: two rows a CTA, 16 threads (CH channels each) a row and group; the groups of
-// a row take every groups-th part, the loads of four at a time, and are joined in order.
+// a row take every groups-th part, the loads of four at a time, and are joined in order.  A part (m, l, h):
+// its weights' sum l is in units of 2^m, the sums with the values in units of 2^(m + h).  Both are joined
+// under the largest unit of their kind, (Mo, h) for the second: V's size would not fit beside a weight's.
+struct Join {
+  float M, sum, Mo, h;
+  // The second unit becomes (m, hn) if that is larger; what the sums before are multiplied by.
+  __device__ __forceinline__ float raise(float m, float hn) {
+    const float d = (m - Mo) + (hn - h);
+    if (!(d > 0.f)) return 1.f;
+    Mo = m;
+    h = hn;
+    return ex2(-d);
+  }
+  __device__ __forceinline__ float factor(float m, float hn) const { return ex2((m - Mo) + (hn - h)); }
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_constant__ StreamArgs a) {
   grid_wait();
@@ -172,35 +188,38 @@ __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_consta
   const int left = u.rows - y0, rows = min(left, 2), groups = 16 / rows;   // rows here; groups of a row
   const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH, y = y0 + group % rows, mine = group / rows;
   auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kRows + y; };
-  float M = kNoMax, sum = 0.f, o[CH];
+  Join x = {kNoMax, 0.f, kNoMax, kNoScale};
+  float o[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) o[k] = 0.f;
 #pragma unroll 1
   for (int k = u.first + mine; y < u.rows && k <= u.last; k += TOGETHER * groups) {
-    float2 st[TOGETHER];
+    float4 st[TOGETHER];
     float4 v[TOGETHER][CH / 4];
 #pragma unroll
     for (int i = 0; i < TOGETHER; ++i) {
       const int ki = k + i * groups;
-      st[i] = make_float2(kNoMax, 0.f);
+      st[i] = make_float4(kNoMax, 0.f, kNoScale, 0.f);
       if (ki > u.last) continue;
       st[i] = a.stats[place(ki)];
 #pragma unroll
       for (int z = 0; z < CH / 4; ++z) v[i][z] = *(reinterpret_cast<const float4*>(a.part + place(ki) * D + ch) + z);
     }
-    float to = M;
+    float to = x.M, f0 = 1.f;
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) to = fmaxf(to, st[i].x);
-    const float f0 = ex2(M - to);
-    M = to;
-    sum *= f0;
+    for (int i = 0; i < TOGETHER; ++i) {
+      to = fmaxf(to, st[i].x);
+      f0 *= x.raise(st[i].x, st[i].z);
+    }
+    x.sum *= ex2(x.M - to);
+    x.M = to;
 #pragma unroll
     for (int z = 0; z < CH; ++z) o[z] *= f0;
 #pragma unroll
     for (int i = 0; i < TOGETHER; ++i) {
       if (k + i * groups > u.last) continue;
-      const float f = ex2(st[i].x - M);
-      sum += f * st[i].y;
+      const float f = x.factor(st[i].x, st[i].z);
+      x.sum += ex2(st[i].x - x.M) * st[i].y;
 #pragma unroll
       for (int z = 0; z < CH / 4; ++z) {
         o[4 * z] = fmaf(f, v[i][z].x, o[4 * z]);
@@ -212,26 +231,32 @@ __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_consta
   }
   float* const at = buffer + group * kRow;
 #pragma unroll
-  for (int z = 0; z < CH; ++z) at[2 + ch + z] = o[z];
+  for (int z = 0; z < CH; ++z) at[4 + ch + z] = o[z];
   if (ch == 0) {
-    at[0] = M;
-    at[1] = sum;
+    at[0] = x.M;
+    at[1] = x.sum;
+    at[2] = x.Mo;
+    at[3] = x.h;
   }
   __syncthreads();
   if (mine != 0 || y >= u.rows) return;
   const int filled = min(groups, u.last - u.first + 1);     // (the others have no part)
-  for (int i = 0; i < filled; ++i) M = fmaxf(M, buffer[(group + i * rows) * kRow]);
-  sum = 0.f;
+  for (int i = 0; i < filled; ++i) {
+    const float* const from = buffer + (group + i * rows) * kRow;
+    x.M = fmaxf(x.M, from[0]);
+    x.raise(from[2], from[3]);
+  }
+  x.sum = 0.f;
 #pragma unroll
   for (int z = 0; z < CH; ++z) o[z] = 0.f;
   for (int i = 0; i < filled; ++i) {
     const float* const from = buffer + (group + i * rows) * kRow;
-    const float f = ex2(from[0] - M);
-    sum += f * from[1];
+    const float f = x.factor(from[2], from[3]);
+    x.sum += ex2(from[0] - x.M) * from[1];
 #pragma unroll
-    for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[2 + ch + z], o[z]);
+    for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[4 + ch + z], o[z]);
   }
-  store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+  store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, x.sum == 0.f ? 0.f : 1.f / x.sum, (x.Mo - x.M) + x.h);
 }
 
 // (more than 8 rows: accumulators take more registers than two CTAs of five warps leave, so three more
@@ -577,7 +602,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
                 make_float2(acc[n][i][k], acc[n][i][k + 2]);
         consumers_sync();
         const int y = 8 * n + mr;
-        float M = kNoMax, sum = 0.f, o[CH];
+        float M = kNoMax, sum = 0.f, H = -INFINITY, z4[4], o[CH];   // z4: a warp's unit against 2^M
 #pragma unroll
         for (int k = 0; k < CH; ++k) o[k] = 0.f;
 #pragma unroll
@@ -585,20 +610,25 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 st = stats[k * L::kRows + y];
-          const float f = ex2(st.x - M), fe = f * ex2(all_heights[k * L::kRows + y]);
-          sum += f * st.y;
+          sum += ex2(st.x - M) * st.y;
+          z4[k] = (st.x - M) + all_heights[k * L::kRows + y];
+          H = fmaxf(H, z4[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float fe = ex2(z4[k] - H);
           const float* const p = merge + (k * 8 + mr) * L::kMergeRow + ch;
 #pragma unroll
           for (int z = 0; z < CH; ++z) o[z] = fmaf(fe, p[z], o[z]);
         }
         if (!x.ok || *reinterpret_cast<volatile int*>(&misc[0]) != 0) sum = __int_as_float(0x7fc00000);
         if (whole) {
-          store_row<D, CH>(a, w.b, w.h, r0, y, x.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum);
+          store_row<D, CH>(a, w.b, w.h, r0, y, x.rows, ch, o, sum == 0.f ? 0.f : 1.f / sum, H);
         } else {
           float* const p = a.part + (int64_t(slot) * L::kRows + y) * D + ch;
 #pragma unroll
           for (int z = 0; z < CH; z += 4) *reinterpret_cast<float4*>(p + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
-          if (ch == 0) a.stats[int64_t(slot) * L::kRows + y] = make_float2(M, sum);
+          if (ch == 0) a.stats[int64_t(slot) * L::kRows + y] = make_float4(M, sum, H, 0.f);
         }
       }
       if (!whole && w.kt0 == 0 && threadIdx.x == 0) {       // (told by the CTA where the unit begins)

@@ -152,6 +152,20 @@ def test_large_values_of_no_weight(n, G, fmt, far, H):
     close(Hand(k, v, q, fmt, H).run())
 
 
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", ONE + FEW)
+def test_values_of_many_sizes(n, G, H):
+    """Every block of values of another size, 2^-90 to 2^100, its weights such that each matters somewhere."""
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        T, d = slots_of(n, 700), 128
+        q, u = aimed(8 + seed, n, G, d)
+        far = np.repeat(rng.integers(-90, 101, T // 16 + 1), 16)[:T] if seed else np.repeat(rng.permutation(T // 16 + 1) % 40 * 5 - 90, 16)[:T]
+        k = normal(9 + seed, T, d) / 4 - (far * np.log(2.0) * d ** 0.5 / 8)[:, None] * u / 2 ** (seed % 2)
+        v = normal(10 + seed, T, d) * 2.0 ** far[:, None]
+        close(Hand(k, v, q, "int8" if seed % 2 else "e4m3", H).run())
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("H", [1, 128])
 @pytest.mark.parametrize("n,G", ONE + FEW + MANY)
@@ -167,3 +181,14 @@ def test_scores_far_below_zero(n, G, fmt, H):
     codes, scales = c.get()
     v = R.rows_of(codes[0, 0, :, 0], scales[0, 0, :, 0], T, d, fmt)[1][3]
     assert (np.abs(c.out[0].double().cpu().numpy() - v) <= 2.0 ** -8 * np.abs(v)).all()
+
+
+@pytest.mark.parametrize("T", [100, 3000])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
+def test_values_near_the_largest(n, G, fmt, T):
+    """Values up to 3e38: a weighted mean is no larger."""
+    T, d = T + n, 64
+    k, v, q = normal(24, T, d) / 2, np.clip(normal(25, T, d), -1, 1) * 2.98e38, normal(26, n, G, d)
+    v[:, :8] = np.abs(v[:, :8])
+    close(Hand(k, v, q, fmt).run())
