@@ -549,9 +549,10 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
                 v[k][0] = u.x;
                 v[k][1] = u.y;
               }
-              // slots that no row sees may hold anything (a code that is not a number, too)
+              // slots that no row sees, and what was read for a bad page, may hold anything (a code that is
+              // not a number, too); rows that see none of it stay clean
               const int slot = slot0 - 16 * warp + row;
-              if (!clear && (slot >= x.hi || (slot < oldest && slot >= a.c.n_sink)))
+              if (!clear && (slot >= x.hi || (slot < oldest && slot >= a.c.n_sink) || bad_page[s] != 0))
 #pragma unroll
                 for (int i = 0; i < W; ++i) v[k][i] = 0u;
 #pragma unroll

@@ -192,3 +192,22 @@ def test_values_near_the_largest(n, G, fmt, T):
     k, v, q = normal(24, T, d) / 2, np.clip(normal(25, T, d), -1, 1) * 2.98e38, normal(26, n, G, d)
     v[:, :8] = np.abs(v[:, :8])
     close(Hand(k, v, q, fmt).run())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,Hq", [(5, 1), (5, 4), (40, 1)])
+def test_a_bad_page_spoils_only_tokens_that_see_it(n, Hq, fmt):
+    """Whatever lies in the pool's first page."""
+    c = next(c for c in (Case(1, Hq, 1, 64, fmt, [62], n, paged=True, seed=s) for s in range(99)) if not (c.table == 0).any())
+    c.append()
+    c.attend()
+    c.check()
+    want = c.out.clone()
+    c.cache.codes[0] = 255
+    c.cache.scales[0] = 1.0
+    c.table[0, 1] = -1
+    c.attend()
+    assert c.error_word() != 0
+    assert torch.isnan(c.out[0, 2:].float()).all()
+    # (the products are the same; a unit may be divided elsewhere)
+    torch.testing.assert_close(c.out[0, :2].float(), want[0, :2].float(), rtol=2.0 ** -7, atol=1e-4)
