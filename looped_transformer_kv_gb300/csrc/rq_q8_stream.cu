@@ -51,7 +51,7 @@ struct StreamSmem {
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int merge = kStages * kStage, query = merge + kMerge, stats = query + kHeld;
   static constexpr int heights = stats + 4 * kRows * 8, bars = heights + 4 * kRows * 4, misc = bars + 16 * kStages;
-  static constexpr int cut = misc + 16 * 4 + 4 * 8, walk = cut + int(sizeof(OwnCut));
+  static constexpr int cut = misc + 16, walk = cut + int(sizeof(OwnCut));
   static constexpr int total = walk + int(sizeof(Walk<8, kQ8Tile>)) + 128;
   static_assert(kStages >= 2 && cut % 8 == 0 && total <= 227 * 1024 / kCtas - 1024, "shared memory");
 };
@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (L::kStages + s); };
   int* const misc = reinterpret_cast<int*>(smem + L::misc); // [0]: gave up
-  int* const bad_page = misc + 16;                          // [stage]
   OwnCut& cut = *reinterpret_cast<OwnCut*>(smem + L::cut);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -327,17 +326,21 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           if (n > 0) good = mbar_wait_bounded(empty(s), (n - 1) & 1, kWaitNs);
           good = __all_sync(RQ_FULL_MASK, good);
           if (!good) break;
-          if (lane == 0) {
-            const int64_t at = r < 0 ? w.h : r;             // (no page: page 0, and flagged)
-            bad_page[s] = r < 0;
-            if (r < 0) {
+          uint8_t* const stage = smem + s * L::kStage;
+          if (r < 0) {                                      // no page: zeros under scales that are not numbers
+            for (int k = lane; k < L::kCodes / 16; k += 32) reinterpret_cast<uint4*>(stage)[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (lane < 8) reinterpret_cast<float*>(stage + L::kCodes)[lane] = __int_as_float(0x7fc00000);
+            fence_async_smem();                             // (a later copy writes there)
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(full(s));
               grid_wait();
               atomicOr(a.err, 1u);
             }
-            uint8_t* const stage = smem + s * L::kStage;
+          } else if (lane == 0) {
             mbar_arrive_expect_tx(full(s), L::kCodes + 32);
-            bulk_g2s(smem_u32(stage), a.v.codes + at * a.v.rec_codes, L::kCodes, full(s));
-            bulk_g2s(smem_u32(stage + L::kCodes), a.v.scales + at * a.v.rec_scales, 32, full(s));
+            bulk_g2s(smem_u32(stage), a.v.codes + r * a.v.rec_codes, L::kCodes, full(s));
+            bulk_g2s(smem_u32(stage + L::kCodes), a.v.scales + r * a.v.rec_scales, 32, full(s));
           }
           __syncwarp();
         }
@@ -411,9 +414,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
         const int oldest = a.c.window > 0 ? x.ctx + x.j0 + 1 - a.c.window : 0;   // the first row's window
         if (slot0 < x.hi && (slot0 + 15 >= oldest || slot0 < a.c.n_sink)) {
           const float* const scales = reinterpret_cast<const float*>(stage + L::kCodes);
-          const bool no_page = bad_page[s] != 0;
-          const float ks = no_page ? __int_as_float(0x7fc00000) : scales[warp];
-          const float vs = no_page ? __int_as_float(0x7fc00000) : scales[4 + warp];
+          const float ks = scales[warp], vs = scales[4 + warp];
           // ---- scores
           float sc[NT][4];
 #pragma unroll
@@ -549,10 +550,9 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
                 v[k][0] = u.x;
                 v[k][1] = u.y;
               }
-              // slots that no row sees, and what was read for a bad page, may hold anything (a code that is
-              // not a number, too); rows that see none of it stay clean
+              // slots that no row sees may hold anything (a code that is not a number, too)
               const int slot = slot0 - 16 * warp + row;
-              if (!clear && (slot >= x.hi || (slot < oldest && slot >= a.c.n_sink) || bad_page[s] != 0))
+              if (!clear && (slot >= x.hi || (slot < oldest && slot >= a.c.n_sink)))
 #pragma unroll
                 for (int i = 0; i < W; ++i) v[k][i] = 0u;
 #pragma unroll
