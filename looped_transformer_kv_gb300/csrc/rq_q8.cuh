@@ -11,6 +11,7 @@ namespace rq {
 
 constexpr int kQ8Tile = 64, kQ8Block = 16;
 constexpr int kQ8LeastExp = -100;   // exponent of the smallest scale
+constexpr int kMostUp = 110;        // exponent of what brings queries into fp16's range, at most
 
 struct Q8View {          // one loop's part of a cache
   uint8_t* codes;        // + loop * 2 * 64 * d

@@ -6,9 +6,11 @@
 // scales as its own, the codes of the others are multiplied by the power of two between them
 // (a block 2^-15 of the largest is still exact, smaller ones keep 2^-32 of the largest code).  V's tile
 // scale 2^e_V goes into the weights' exponent and is taken out of their sum again,
-//   P = 2^((S 2^e_K - R) c + e_V - h),  l += 2^-e_V sum P,
-// so that tiles of different scales need no rescaling of O.  R (a row's largest score, raw) and h are
-// raised when a weight would exceed 2^15, to make the largest 2^7.
+//   P = 2^((S 2^(e_K - e_q) - R) c + e_V - h),  l += 2^-e_V sum P,
+// so that tiles of different scales need no rescaling of O; 2^e_q is what brought the row's query into
+// fp16's range.  R (a row's largest q K) and h are raised when a weight would exceed 2^15, to make the
+// largest 2^7.  Tiles whose exponents do not allow the products to be drawn together, and rows of huge
+// scores, take another loop over the scores (`careful`).
 //
 // The operands are made once, in the workspace (q8_query_kernel, q8_image_kernel), and copied from there.
 // (A kernel that converted what it read, without the workspace, was slower from 33 rows on: its loads and
@@ -99,7 +101,7 @@ struct RowsArgs : Q8Line {
 
 // Rows rr0 .. + ROWS of a tile of 128 query rows (row r0 of the sequence and on, `live` of them) to fp16
 // operands, each times a power of two that brings its largest element into [2^14, 2^15) (bf16 values are
-// exact then); factors: what a row's scores are multiplied by.  One warp; a lane holds two runs of four
+// exact then; at most 2^kMostUp); factors: its inverse.  One warp; a lane holds two runs of four
 // channels that are turned into each other, so that it reads no angle that another lane reads (eight
 // neighbouring channels a lane, partners by shuffles: 1,023 tokens of 4 x 16 heads in 19 us, now 13).
 template <int D, int ROWS>
@@ -155,7 +157,7 @@ __device__ __forceinline__ void put_queries(const Q8Line& a, const Rows& x, int 
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
       const int ex = int(__float_as_uint(mx) >> 23);
-      const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
+      const int e = mx == 0.f || ex == 255 ? 0 : min(141 - ex, kMostUp);
       const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
       uint32_t o[4];
 #pragma unroll
@@ -167,7 +169,7 @@ __device__ __forceinline__ void put_queries(const Q8Line& a, const Rows& x, int 
             make_uint2(o[2 * k], o[2 * k + 1]);
       }
       if (qc == 0)
-        factors[rr] = lost[y] ? __int_as_float(0x7fc00000) : a.scale_log2 * q8_pow2(-(e >> 1)) * q8_pow2(-(e - (e >> 1)));
+        factors[rr] = lost[y] ? __int_as_float(0x7fc00000) : q8_pow2(-e);
     }
   }
 }
@@ -523,9 +525,8 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         if (i == 1) failed = group_any(1, !mbar_wait_bounded(qready, seg & 1, kWaitNs));
         ++seg;
       }
-      // weights are 2^((S 2^e_K - R) c + e_V - h): the product with a power of two is exact, so that scores
-      // of any size cancel without a residue
-      float R = -INFINITY, h = 0.f, l = 0.f, c = 0.f;
+      const float c = a.scale_log2;
+      float R = -INFINITY, h = 0.f, l = 0.f;
       if (!mine) {                                             // no rows
         if (!x.ok || failed) continue;
         g += w.T;
@@ -533,8 +534,11 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         continue;
       }
       if (x.ok && !failed) {
-        c = factor;
-        if (c < 1.2e-38f) c = 1.2e-38f;                        // (above 0, so that -inf stays -inf)
+        // exponents of a tile's K for which 2^(e_K - e_q) and its product with c are far from fp32's ends
+        // for all rows of the warp: from ke_min to ke_max
+        const int fe = q8_exponent(factor);
+        const bool tame = c > 0x1p-30f && c < 0x1p30f;
+        const int ke_min = tame ? -90 - __reduce_min_sync(RQ_FULL_MASK, fe) : 1, ke_max = tame ? 90 - __reduce_max_sync(RQ_FULL_MASK, fe) : 0;
         const int own = x.ctx + min(row / a.G, x.n - 1);       // the row's own slot
         const int own0 = x.ctx + r0 / a.G, own1 = x.ctx + min((r0 + kRowTile - 1) / a.G, x.j1);   // of the tile's rows
         const int win = a.c.window > 0 ? a.c.window : 1 << 30, sinks = a.c.window > 0 ? a.c.n_sink : 0;
@@ -565,36 +569,23 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
             break;
           }
           tc_fence_after();
-          uint32_t s[kKeys];
+          const float ev = float(ee.y);
+          // O, whose unit changes with h and R, times f (a lane's row); every lane of the warp calls it
+          auto rescale = [&](float f) {
+            if (t == 0) return;
+#pragma unroll 1
+            for (int y = 0; y < D / 16; ++y) {
+              uint32_t o[16];
+              tc_ld16(tO + 16 * y, o);
+              tc_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
-          const float ke = q8_pow2(max(min(ee.x, 127), -126)), ev = float(ee.y);
-          tc_wait_ld();
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (clear[half]) continue;
-            const int hi = own - at[half] + 1, lo = own - win - at[half] + 1, sk = min(sinks - at[half], hi);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t seen = range_bits(lo - 32 * q, hi - 32 * q) | range_bits(0, sk - 32 * q);
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (!(seen >> y & 1u)) s[half * 64 + 32 * q + y] = 0xff800000u;
+              for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+              tc_st16(tO + 16 * y, o);
             }
-          }
-          float mx[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = __uint_as_float(s[y]);
-#pragma unroll
-          for (int y = 4; y + 4 < kKeys; y += 8)
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
-#pragma unroll
-          for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ke;
-          const bool over = R == -INFINITY ? top > R : fmaf(top - R, c, ev - h) > kWeightTop;
-          if (__any_sync(RQ_FULL_MASK, over)) {
+          };
+          auto raise = [&](float top) {
+            const bool over = R == -INFINITY ? top > R : fmaf(top - R, c, ev - h) > kWeightTop;
+            if (!__any_sync(RQ_FULL_MASK, over)) return;
             float f = 1.f;
             if (over) {
               const float hn = ev - kWeightHead;
@@ -604,55 +595,112 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
             }
             l *= f;
             huge = __any_sync(RQ_FULL_MASK, fabsf(R * c) > 0x1p20f && R != -INFINITY);
-            if (t > 0) {
-#pragma unroll 1
-              for (int y = 0; y < D / 16; ++y) {
-                uint32_t o[16];
-                tc_ld16(tO + 16 * y, o);
-                tc_wait_ld();
+            rescale(f);
+          };
+          auto weights_there = [&](int half) {                 // the values of its 64 keys may begin
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(pready(i, half));
+          };
+          auto seen_by = [&](int half, int q) {                // bit y: the row sees key 64 half + 32 q + y
+            const int first = (half ? at[1] : at[0]) + 32 * q, hi = own - first + 1, lo = hi - win, sk = sinks - first;
+            return range_bits(lo, hi) | range_bits(0, min(sk, hi));
+          };
+          float sum01 = 0.f;
+          bool slow = ee.x < ke_min || ee.x > ke_max;
+          if (!slow) {
+            uint32_t s[kKeys];
 #pragma unroll
-                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-                tc_st16(tO + 16 * y, o);
-              }
-            }
-          }
-          // (huge scores: the difference first, exactly; one multiplication and addition would leave a
-          // residue of their last bits)
-          const float rz = R == -INFINITY ? 0.f : -R, hx = ev - h;
-          uint64_t sum[2] = {0ull, 0ull};
-          auto weights = [&](auto exactly) {
-            constexpr bool EXACTLY = decltype(exactly)::value;
-            const float mul = EXACTLY ? c : ke * c, add = EXACTLY ? hx : fmaf(rz, c, hx);
-            const uint64_t k2 = pack2(ke, ke), r2 = pack2(rz, rz), c2 = pack2(mul, mul), h2 = pack2(add, add);
+            for (int y = 0; y < 4; ++y) tc_ld32(tS + 32 * y, s + 32 * y);
+            const float kq = q8_pow2(ee.x) * factor;
+            tc_wait_ld();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t p[32];
+              if (clear[half]) continue;
 #pragma unroll
-              for (int y = 0; y < 32; ++y) {
-                const int k = half * 64 + 2 * y;
-                uint64_t z = pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                if (EXACTLY) z = fma2(z, k2, r2);
-                float p0, p1;
-                unpack2(fma2(z, c2, h2), p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
-                p[y] = pack_half2(p0, p1);
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t seen = seen_by(half, q);
+#pragma unroll
+                for (int y = 0; y < 32; ++y)
+                  if (!(seen >> y & 1u)) s[half * 64 + 32 * q + y] = 0xff800000u;
               }
-              tc_st32(tS + 32 * half, p);
-              // the values of the first 64 keys may begin
-              tc_wait_st();
-              tc_fence_before();
-              mbar_arrive(pready(i, half));
             }
-          };
-          if (huge || ke < 0x1p-60f)
-            weights(std::true_type{});
-          else
-            weights(std::false_type{});
-          float a0, a1;
-          unpack2(add2(sum[0], sum[1]), a0, a1);
-          l = fmaf(a0 + a1, q8_pow2(-max(min(ee.y, 126), -126)), l);
+            float mx[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = __uint_as_float(s[y]);
+#pragma unroll
+            for (int y = 4; y + 4 < kKeys; y += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
+#pragma unroll
+            for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
+            raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq);
+            slow = huge;
+            if (!slow) {
+              const float mul = kq * c, add = fmaf(R == -INFINITY ? 0.f : -R, c, ev - h);
+              const uint64_t c2 = pack2(mul, mul), h2 = pack2(add, add);
+              uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t p[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                  const int k = half * 64 + 2 * y;
+                  float p0, p1;
+                  unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, h2), p0, p1);
+                  p0 = ex2(p0);
+                  p1 = ex2(p1);
+                  sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+                  p[y] = pack_half2(p0, p1);
+                }
+                tc_st32(tS + 32 * half, p);
+                weights_there(half);
+              }
+              float a0, a1;
+              unpack2(add2(sum[0], sum[1]), a0, a1);
+              sum01 = a0 + a1;
+            }
+          }
+          if (slow) {
+            // careful: scores as q K (the power of two in two steps, of the same direction), and differences
+            // before the product with c, exactly: scores of any size cancel without a residue.  Twice over the
+            // scores in tensor memory, 32 keys at a time (the weights of some lie where only scores did that
+            // were read before).
+            const int x2 = ee.x + fe;
+            const float k1 = q8_pow2(x2 >> 1), k2 = q8_pow2(x2 - (x2 >> 1)) + (factor - factor);   // (no number: stays so)
+            auto scores = [&](int y, float (&z)[32]) {
+              uint32_t s[32];
+              tc_ld32(tS + 32 * y, s);
+              const uint32_t seen = (y >> 1 ? clear[1] : clear[0]) ? ~0u : seen_by(y >> 1, y & 1);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) z[k] = seen >> k & 1u ? __uint_as_float(s[k]) * k1 * k2 : -INFINITY;
+            };
+            float top = -INFINITY, z[32];
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y) {
+              scores(y, z);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) top = fmaxf(top, z[k]);
+            }
+            raise(top);
+            const float r = R == -INFINITY ? 0.f : R;
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y) {
+              scores(y, z);
+              uint32_t p[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float p0 = ex2(fmaf(z[2 * k] - r, c, ev - h)), p1 = ex2(fmaf(z[2 * k + 1] - r, c, ev - h));
+                sum01 += p0 + p1;
+                p[k] = pack_half2(p0, p1);
+              }
+              tc_st16(tS + 16 * y, p);
+              if (y & 1) weights_there(y >> 1);
+            }
+          }
+          l = fmaf(sum01, q8_pow2(-max(min(ee.y, 126), -126)), l);
         }
         if (!failed) {
           const int last_step = n0 + g;

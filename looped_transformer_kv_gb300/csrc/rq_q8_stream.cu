@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__
     for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(RQ_FULL_MASK, mx, o));
     // a power of two brings the row's largest element into [2^14, 2^15): bf16 values are exact
     const int ex = int(__float_as_uint(mx) >> 23);
-    const int e = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);
+    const int e = mx == 0.f || ex == 255 ? 0 : min(141 - ex, kMostUp);
     const float up = q8_pow2(e >> 1), up2 = q8_pow2(e - (e >> 1));
     if (y >= L::kRows) continue;
     const int nt = y >> 3, n = y & 7;

@@ -183,6 +183,19 @@ def test_scores_far_below_zero(n, G, fmt, H):
     assert (np.abs(c.out[0].double().cpu().numpy() - v) <= 2.0 ** -8 * np.abs(v)).all()
 
 
+SIZES = [(-90, -50, 0.0), (-80, -45, 0.0), (0, -50, 2.0 ** -80), (-60, -60, 2.0 ** -20), (-100, -100, 0.0), (100, -98, 0.0), (-98, 100, 0.0),
+         (-105, 106, 0.0), (-112, 112, 0.0), (-118, 117, 0.0), (-30, 110, 2.0 ** -81), (110, -20, 2.0 ** -92)]
+
+
+@pytest.mark.parametrize("qe,ke,scale", SIZES)
+@pytest.mark.parametrize("n,G", ONE[:1] + FEW[1:] + MANY)
+def test_sizes_of_queries_and_keys(n, G, qe, ke, scale):
+    """Queries of 2^qe and keys of 2^ke, whose scores are moderate."""
+    T, d = n + 280, 128 if n % 8 else 64
+    k, v, q = normal(12, T, d) * 2.0 ** ke, normal(13, T, d), normal(14, n, G, d) * 2.0 ** qe
+    close(Hand(k, v, q, "int8" if n % 3 else "e4m3", scale=scale).run())
+
+
 @pytest.mark.parametrize("T", [100, 3000])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("n,G", ONE + FEW + MANY)
