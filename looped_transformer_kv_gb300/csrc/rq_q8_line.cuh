@@ -9,8 +9,12 @@
 #include "rq_kernels.h"
 #include "rq_launch.cuh"
 #include "rq_q8.cuh"
+#include "rq_tc.cuh"
 
 namespace rq {
+
+constexpr float kNoMax = -3.402823466e38f;   // m of a row that has seen nothing: no finite score is below it
+constexpr int kNoScale = -1000;              // h of sums that hold nothing
 
 struct Cut {           // a CTA's stretch of the line
   int64_t pos, base;    // where it begins; where the units of (sequence, block) begin
@@ -217,6 +221,25 @@ __device__ __forceinline__ bool own_cut(const Q8Line& a, OwnCut& out, int me) { 
   }
   return __syncthreads_or(bad);
 }
+
+// The parts of a divided unit's row, joined.  A part (m, l, h): its weights' sum l is in units of 2^m, the
+// sums with the values in units of 2^(m + h).  Both are joined under the largest unit of their kind, (Mo, h)
+// for the second: V's size would not fit beside a weight's.
+struct Join {
+  float M, sum, Mo, h;
+  __device__ __forceinline__ static Join none() { return {kNoMax, 0.f, kNoMax, float(kNoScale)}; }
+  // The second unit becomes (m, hn) if that is larger; what the sums before are multiplied by.
+  __device__ __forceinline__ float raise(float m, float hn) {
+    const float d = (m - Mo) + (hn - h);
+    if (!(d > 0.f)) return 1.f;
+    Mo = m;
+    h = hn;
+    return ex2(-d);
+  }
+  __device__ __forceinline__ float factor(float m, float hn) const { return ex2((m - Mo) + (hn - h)); }
+  __device__ __forceinline__ float inverse() const { return sum == 0.f ? 0.f : 1.f / sum; }
+  __device__ __forceinline__ float unit() const { return (Mo - M) + h; }
+};
 
 // A CTA's segments in order.  (No constructor: it may lie in shared memory, which keeps it out of the
 // registers of the threads that read it.)

@@ -6,11 +6,12 @@
 // scales as its own, the codes of the others are multiplied by the power of two between them
 // (a block 2^-15 of the largest is still exact, smaller ones keep 2^-32 of the largest code).  V's tile
 // scale 2^e_V goes into the weights' exponent and is taken out of their sum again,
-//   P = 2^((S 2^(e_K - e_q) - R) c + e_V - h),  l += 2^-e_V sum P,
+//   P = 2^((S 2^(e_K - e_q) - R) c + e_V - h),  l += 2^(h - e_V) sum P,
 // so that tiles of different scales need no rescaling of O; 2^e_q is what brought the row's query into
 // fp16's range.  R (a row's largest q K) and h are raised when a weight would exceed 2^15, to make the
-// largest 2^7.  Tiles whose exponents do not allow the products to be drawn together, and rows of huge
-// scores, take another loop over the scores (`careful`).
+// largest 2^7.  Tiles whose exponents do not allow the products to be drawn together, tiles of a V so small
+// beside another's that weights would leave fp32's range before they are summed, and rows of huge scores
+// take another loop over the scores (`careful`).
 //
 // The operands are made once, in the workspace (q8_query_kernel, q8_image_kernel), and copied from there.
 // (A kernel that converted what it read, without the workspace, was slower from 33 rows on: its loads and
@@ -29,6 +30,7 @@
 namespace rq {
 namespace {
 
+constexpr int kFarBelow = 40;         // V's exponent below a row's h: weights of 2^-86 are still summed
 constexpr int kKeys = 128, kRowTile = 128, kBlockRows = 2 * kRowTile;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
@@ -335,11 +337,11 @@ __device__ __forceinline__ void store32(void* to, const uint4& a, const uint4& b
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                :: "l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
 }
-__device__ __forceinline__ uint4 bf16_row(const float (&v)[8], float inv) {
+__device__ __forceinline__ uint4 bf16_row(const float (&v)[8], float inv, float up) {   // times inv up^2
   uint32_t p[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 u = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+    const __nv_bfloat162 u = __floats2bfloat162_rn(v[2 * k] * inv * up * up, v[2 * k + 1] * inv * up * up);
     p[k] = *reinterpret_cast<const uint32_t*>(&u);
   }
   return make_uint4(p[0], p[1], p[2], p[3]);
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         const int win = a.c.window > 0 ? a.c.window : 1 << 30, sinks = a.c.window > 0 ? a.c.n_sink : 0;
         int2 ee32 = make_int2(0, 0);                           // a lane's exponents of 32 tiles
         bool huge = false;                                     // scores beyond 2^20 in some row of the warp
+        int h_top = kNoScale;                                  // the largest h of the warp's rows
         for (int t = 0; t < w.T; ++t, ++g) {
           // ---- before the scores are there: the tile's exponents, and what of it the warp's rows see
           if ((t & 31) == 0) ee32 = t + lane < w.T ? *image_exps<D>(a, w, t + lane) : make_int2(0, 0);
@@ -583,19 +586,29 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
               tc_st16(tO + 16 * y, o);
             }
           };
-          auto raise = [&](float top) {
-            const bool over = R == -INFINITY ? top > R : fmaf(top - R, c, ev - h) > kWeightTop;
+          // before weights of up to 2^sum_top (their sum's units) and 2^kWeightTop
+          auto raise = [&](float top, float sum_top) {
+            const float a = top - R;
+            const bool over = R == -INFINITY ? top > R : a * c > sum_top || fmaf(a, c, ev - h) > kWeightTop;
             if (!__any_sync(RQ_FULL_MASK, over)) return;
-            float f = 1.f;
+            float f = 1.f, fo = 1.f;                           // of l, and of O
             if (over) {
-              const float hn = ev - kWeightHead;
-              f = R == -INFINITY ? 0.f : ex2(fmaf(R - top, c, h - hn));
-              R = top;
-              h = hn;
+              const float Rn = fmaxf(R, top), hn = fmaf(top - Rn, c, ev - kWeightHead);
+              if (R == -INFINITY) {
+                f = fo = 0.f;
+                h = hn;
+              } else {
+                const float d = (R - Rn) * c, h0 = h;
+                h = fmaxf(hn, h + d);
+                f = ex2(d);
+                fo = ex2(d + (h0 - h));
+              }
+              R = Rn;
             }
             l *= f;
             huge = __any_sync(RQ_FULL_MASK, fabsf(R * c) > 0x1p20f && R != -INFINITY);
-            rescale(f);
+            h_top = __reduce_max_sync(RQ_FULL_MASK, R == -INFINITY ? kNoScale : int(ceilf(h)));
+            rescale(fo);
           };
           auto weights_there = [&](int half) {                 // the values of its 64 keys may begin
             tc_wait_st();
@@ -606,8 +619,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
             const int first = (half ? at[1] : at[0]) + 32 * q, hi = own - first + 1, lo = hi - win, sk = sinks - first;
             return range_bits(lo, hi) | range_bits(0, min(sk, hi));
           };
-          float sum01 = 0.f;
-          bool slow = ee.x < ke_min || ee.x > ke_max;
+          bool slow = ee.x < ke_min || ee.x > ke_max || ee.y < h_top - kFarBelow;
           if (!slow) {
             uint32_t s[kKeys];
 #pragma unroll
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
                 mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
 #pragma unroll
             for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
-            raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq);
+            raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq, INFINITY);
             slow = huge;
             if (!slow) {
               const float mul = kq * c, add = fmaf(R == -INFINITY ? 0.f : -R, c, ev - h);
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
               }
               float a0, a1;
               unpack2(add2(sum[0], sum[1]), a0, a1);
-              sum01 = a0 + a1;
+              l = fmaf(a0 + a1, ex2(h - ev), l);               // (h - ev: kFarBelow at most)
             }
           }
           if (slow) {
@@ -684,7 +696,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
 #pragma unroll
               for (int k = 0; k < 32; ++k) top = fmaxf(top, z[k]);
             }
-            raise(top);
+            raise(top, kWeightTop);
             const float r = R == -INFINITY ? 0.f : R;
 #pragma unroll 1
             for (int y = 0; y < 4; ++y) {
@@ -692,15 +704,14 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
               uint32_t p[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                const float p0 = ex2(fmaf(z[2 * k] - r, c, ev - h)), p1 = ex2(fmaf(z[2 * k + 1] - r, c, ev - h));
-                sum01 += p0 + p1;
-                p[k] = pack_half2(p0, p1);
+                const float a0 = (z[2 * k] - r) * c, a1 = (z[2 * k + 1] - r) * c;
+                l += ex2(a0) + ex2(a1);
+                p[k] = pack_half2(ex2(a0 + (ev - h)), ex2(a1 + (ev - h)));
               }
               tc_st16(tS + 16 * y, p);
               if (y & 1) weights_there(y >> 1);
             }
           }
-          l = fmaf(sum01, q8_pow2(-max(min(ee.y, 126), -126)), l);
         }
         if (!failed) {
           const int last_step = n0 + g;
@@ -740,7 +751,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
         tc_fence_before();
         continue;
       }
-      const float inv = there ? (l == 0.f ? 0.f : 1.f / l) : nan;
+      const float inv = there ? (l == 0.f ? 0.f : 1.f / l) : nan, up = ex2(0.5f * h);
       uint16_t* const out = a.c.out + ((int64_t(w.b) * a.c.n_new + row / a.G) * a.Hq + w.h * a.G + row % a.G) * D;
       const uintptr_t odd = reinterpret_cast<uintptr_t>(a.c.out) & 31;
 #pragma unroll 1
@@ -759,7 +770,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
           float v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[8 * z + k]);
-          q[z] = bf16_row(v, inv);
+          q[z] = bf16_row(v, inv, up);
         }
         if (odd == 0) {                                        // (whole sectors)
           store32(out + 32 * y, q[0], q[1]);
@@ -791,8 +802,7 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
 }
 
 // The divided units: a CTA joins 32 rows of one, a thread 16 channels of a row, its parts in order and the
-// loads of four at a time.  A part's weights are in units of 2^(st.x + st.y), its sum is st.z; nothing
-// seen: st.x is -inf.
+// loads of four at a time.  A part's m is st.x (-inf: nothing seen), h st.y, l st.z.
 template <int D>
 __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ RowsArgs a) {
   grid_wait();
@@ -801,14 +811,15 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
   if (row >= u.rows) return;
   const int tile = row / kRowTile * kRowTile, r = row % kRowTile;
   auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kBlockRows + tile; };
-  float M = -INFINITY, h = 0.f, sum = 0.f, o[16];
+  Join x = Join::none();
+  float o[16];
 #pragma unroll
   for (int z = 0; z < 16; ++z) o[z] = 0.f;
   for (int k = u.first; k <= u.last; k += 4) {
     float4 st[4], v[4][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      st[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      st[e] = make_float4(-INFINITY, float(kNoScale), 0.f, 0.f);
       if (k + e > u.last) continue;
       st[e] = a.stats[place(k + e) + r];
       const float4* const part = reinterpret_cast<const float4*>(a.part + place(k + e) * D) + 4 * y * kRowTile + r;
@@ -818,20 +829,10 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (k + e > u.last) continue;
-      float f = 1.f, f0 = 1.f;                               // of this part, and of those before
-      if (st[e].x == -INFINITY) {
-        f = 0.f;
-      } else {
-        const float d = M == -INFINITY ? 1.f : (st[e].x - M) + (st[e].y - h);
-        if (!(d <= 0.f)) {
-          f0 = M == -INFINITY ? 0.f : ex2(-d);
-          M = st[e].x;
-          h = st[e].y;
-        } else {
-          f = ex2(d);
-        }
-      }
-      sum = fmaf(f, st[e].z, sum * f0);                      // (a part that gave up is NaN)
+      const float to = fmaxf(x.M, st[e].x);
+      x.sum = fmaf(ex2(st[e].x - to), st[e].z, x.sum * ex2(x.M - to));   // (a part that gave up is NaN)
+      x.M = to;
+      const float f0 = x.raise(st[e].x, st[e].y), f = x.factor(st[e].x, st[e].y);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         o[4 * z] = fmaf(f, v[e][z].x, o[4 * z] * f0);
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
       }
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = x.inverse(), up = ex2(0.5f * x.unit());
   const int j = (u.r0 + row) / a.G, hq = u.h * a.G + (u.r0 + row) % a.G;
   uint16_t* const to = a.c.out + ((int64_t(u.b) * a.c.n_new + j) * a.Hq + hq) * D + 16 * y;
 #pragma unroll
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
     float w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = o[8 * z + k];
-    const uint4 q = bf16_row(w, inv);
+    const uint4 q = bf16_row(w, inv, up);
     if ((reinterpret_cast<uintptr_t>(a.c.out) & 15) == 0) {
       *reinterpret_cast<uint4*>(to + 8 * z) = q;
     } else {

@@ -26,10 +26,8 @@
 namespace rq {
 namespace {
 
-constexpr float kNoMax = -3.402823466e38f;   // m of a row that has seen nothing: no finite score is below it
 constexpr float kTop = 8.f;
 constexpr int kScaleBelow = 3, kScaleRange = 4;   // E: below the first V scale; how far others may be from that
-constexpr int kNoScale = -1000;       // E before the first V scale (and h of sums that hold nothing)
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMostCtas = 1024;
 
@@ -161,22 +159,7 @@ __global__ void __launch_bounds__(128) q8_prepare_kernel(const __grid_constant__
 }
 
 // The parts of a divided unit: two rows a CTA, 16 threads (CH channels each) a row and group; the groups of
-// a row take every groups-th part, the loads of four at a time, and are joined in order.  A part (m, l, h):
-// its weights' sum l is in units of 2^m, the sums with the values in units of 2^(m + h).  Both are joined
-// under the largest unit of their kind, (Mo, h) for the second: V's size would not fit beside a weight's.
-struct Join {
-  float M, sum, Mo, h;
-  // The second unit becomes (m, hn) if that is larger; what the sums before are multiplied by.
-  __device__ __forceinline__ float raise(float m, float hn) {
-    const float d = (m - Mo) + (hn - h);
-    if (!(d > 0.f)) return 1.f;
-    Mo = m;
-    h = hn;
-    return ex2(-d);
-  }
-  __device__ __forceinline__ float factor(float m, float hn) const { return ex2((m - Mo) + (hn - h)); }
-};
-
+// a row take every groups-th part, the loads of four at a time, and are joined in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_constant__ StreamArgs a) {
   grid_wait();
@@ -188,7 +171,7 @@ __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_consta
   const int left = u.rows - y0, rows = min(left, 2), groups = 16 / rows;   // rows here; groups of a row
   const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * CH, y = y0 + group % rows, mine = group / rows;
   auto place = [&](int k) { return (2 * int64_t(k) + (k == u.first)) * kRows + y; };
-  Join x = {kNoMax, 0.f, kNoMax, kNoScale};
+  Join x = Join::none();
   float o[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) o[k] = 0.f;
@@ -256,7 +239,7 @@ __global__ void __launch_bounds__(256) q8_stream_join_kernel(const __grid_consta
 #pragma unroll
     for (int z = 0; z < CH; ++z) o[z] = fmaf(f, from[4 + ch + z], o[z]);
   }
-  store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, x.sum == 0.f ? 0.f : 1.f / x.sum, (x.Mo - x.M) + x.h);
+  store_row<D, CH>(a, u.b, u.h, u.r0, y, u.rows, ch, o, x.inverse(), x.unit());
 }
 
 // (more than 8 rows: accumulators take more registers than two CTAs of five warps leave, so three more

@@ -196,6 +196,21 @@ def test_sizes_of_queries_and_keys(n, G, qe, ke, scale):
     close(Hand(k, v, q, "int8" if n % 3 else "e4m3", scale=scale).run())
 
 
+@pytest.mark.parametrize("far", [20, 28, 34, 60, 110])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
+def test_zeros_beside_large_values(n, G, first, far, H):
+    """Slots of zero values keep their weight in the sum beside values of 2^far."""
+    T, d = n + 512, 64
+    k, v, q = normal(15, T, d) / 2, normal(16, T, d) * 2.0 ** far, normal(17, n, G, d)
+    if first:
+        v[:256] = 0
+    else:
+        v[128:384] = 0
+    close(Hand(k, v, q, "int8" if far % 4 else "e4m3", H).run())
+
+
 @pytest.mark.parametrize("T", [100, 3000])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("n,G", ONE + FEW + MANY)
