@@ -2,10 +2,10 @@
 // cores: blocks of 256 rows (two tiles of 128) share every tile of 128 keys.
 //
 //   S = Q K^T, O += P V as tcgen05 products of 128 x 128 tiles; S, P and O in tensor memory.
-// Codes become fp16 operands in shared memory, exactly: a key tile takes the largest of its blocks'
-// scales as its own, the codes of the others are multiplied by the power of two between them
-// (a block 2^-15 of the largest is still exact, smaller ones keep 2^-32 of the largest code).  V's tile
-// scale 2^e_V goes into the weights' exponent and is taken out of their sum again,
+// Codes become fp16 operands exactly: a key tile takes the largest of its blocks' scales as its own, the
+// codes of the others are multiplied by the power of two between them, down to 2^-kFold; in a tile whose
+// scales lie further apart codes stay as they are, and scores and weights get their block's scale one by one
+// (`careful`).  V's tile scale 2^e_V goes into the weights' exponent and is taken out of their sum again,
 //   P = 2^((S 2^(e_K - e_q) - R) c + e_V - h),  l += 2^(h - e_V) sum P,
 // so that tiles of different scales need no rescaling of O; 2^e_q is what brought the row's query into
 // fp16's range.  R (a row's largest q K) and h are raised when a weight would exceed 2^15, to make the
@@ -30,6 +30,8 @@
 namespace rq {
 namespace {
 
+constexpr int kFold = 8;              // exponents of a tile's scales, at most, that go into its operands
+constexpr int kApart = 4096;          // added to K's exponent of a tile whose scales do not
 constexpr int kFarBelow = 40;         // V's exponent below a row's h: weights of 2^-86 are still summed
 constexpr int kKeys = 128, kRowTile = 128, kBlockRows = 2 * kRowTile;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -70,10 +72,7 @@ __device__ __forceinline__ bool group_any(int i, bool x) {
   return y != 0u;
 }
 
-__device__ __forceinline__ uint32_t half2_pow2(int e) {     // 2^e twice, e <= 0; below 2^-24: 0
-  const uint32_t h = e >= -14 ? uint32_t(15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
-  return h * 0x10001u;
-}
+__device__ __forceinline__ uint32_t half2_pow2(int e) { return (uint32_t(15 + e) << 10) * 0x10001u; }   // 2^e twice, -14 <= e
 
 // Two codes times the power of two f (bias: int8's -1152 f).
 template <int FMT, int HALF>
@@ -187,14 +186,15 @@ struct Converter {
   const uint32_t panel;
   int64_t rec[2];                                            // records of the tile's halves; -1: no page, -2: not there
   float scale;                                               // lane l < 16: block l % 8 of K (l < 8) or V
-  uint32_t factor, lost;                                     // of take_scales: 2^(e - top) of the same; K's blocks to spoil
+  uint32_t factor, lost;                                     // of take_scales: 2^(e - top) of the same (1: not folded); K's blocks to spoil
+  uint32_t exps;                                             // ... lane 4 k of the first 16: exponents of four blocks, a byte each
   int at[2], end, oldest;                                    // slots of the halves' first rows; what is seen
 
   // (rows of a thread's pieces differ by multiples of 16, so the chunk is the same; `first`: which half
   // is stored first, so that neighbours meet distinct banks)
   __device__ __forceinline__ Converter(const Q8Line& line, int t, int l)
       : a(line), tid(t), lane(l), row0(t / CPR), c((t % CPR) ^ q8_swizzle<D>(t / CPR)),
-        first(D == 128 && c >= 4 ? 1 : 0), panel(uint32_t(c / 4) * (kKeys * 128)), scale(1.f), factor(0u), lost(0u) {}
+        first(D == 128 && c >= 4 ? 1 : 0), panel(uint32_t(c / 4) * (kKeys * 128)), scale(1.f), factor(0u), lost(0u), exps(0u) {}
 
   __device__ __forceinline__ int64_t record(const Rows& x, int b, int h, int v) const {
     if (v >= x.tiles) return -2;
@@ -231,16 +231,24 @@ struct Converter {
     const bool live = r >= 0 && lane < 16 && first < end && (first + kQ8Block > oldest || first < a.c.n_sink);
     const bool nan = live && !(scale < INFINITY);
     const int e = live && !nan ? q8_exponent(scale) : -1000;
-    int top = e;
+    int top = e, least = e == -1000 ? 1000 : e;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(RQ_FULL_MASK, top, o));
-    if (top == -1000) top = 0;
-    factor = e == -1000 ? 0u : half2_pow2(max(e - top, -30));
+    for (int o = 1; o < 8; o <<= 1) {
+      top = max(top, __shfl_xor_sync(RQ_FULL_MASK, top, o));
+      least = min(least, __shfl_xor_sync(RQ_FULL_MASK, least, o));
+    }
+    if (top == -1000) top = least = 0;
+    const bool folded = top - least <= kFold;
+    factor = e == -1000 ? 0u : half2_pow2(folded ? e - top : 0);
+    exps = uint32_t((folded || e == -1000 ? top : e) & 255) << (8 * (lane & 3));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) exps |= __shfl_xor_sync(RQ_FULL_MASK, exps, o);
+    const int apart = __any_sync(RQ_FULL_MASK, !folded) ? kApart : 0;
     // (a scale that is not a number, K's or V's, spoils the scores: V then only meets weights of tokens
     // that see the block)
     const uint32_t nans = __ballot_sync(RQ_FULL_MASK, nan || (r == -1 && lane < 16));
     lost = (nans | (nans >> 8)) & 255u;
-    return make_int2(__shfl_sync(RQ_FULL_MASK, top, 0), __shfl_sync(RQ_FULL_MASK, top, 8));
+    return make_int2(__shfl_sync(RQ_FULL_MASK, top, 0) + apart, __shfl_sync(RQ_FULL_MASK, top, 8));
   }
   // Operands of K or V.
   __device__ __forceinline__ void put(const uint4 (&reg)[PIECES], uint8_t* tile, int kv) const {
@@ -323,10 +331,12 @@ __global__ void __launch_bounds__(256) q8_image_kernel(const __grid_constant__ R
   uint8_t* const image = a.images + (int64_t(unit) * a.list + u) * L::kImage;
   to.put(reg, image + kv * L::kTile, kv);
   if (threadIdx.x == 0) *reinterpret_cast<int2*>(image + 2 * L::kTile) = e;
+  if (threadIdx.x < 16 && (threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t*>(image + 2 * L::kTile + 16 + threadIdx.x) = to.exps;
   grid_wait();
 }
 
-// Exponents of tile t of the walk's segment.
+// Exponents of tile t of the walk's segment: K's (and whether its blocks lie apart) and V's; 16 bytes on,
+// those of its blocks, a byte each.
 template <int D, typename W>
 __device__ __forceinline__ const int2* image_exps(const RowsArgs& a, const W& w, int t) {
   return reinterpret_cast<const int2*>(a.images + ((int64_t(w.b) * a.v.H + w.h) * a.list + w.x.step(w.kt0 + t)) * RowsSmem<D>::kImage +
@@ -586,14 +596,11 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
               tc_st16(tO + 16 * y, o);
             }
           };
-          // before weights of up to 2^sum_top (their sum's units) and 2^kWeightTop
-          auto raise = [&](float top, float sum_top) {
-            const float a = top - R;
-            const bool over = R == -INFINITY ? top > R : a * c > sum_top || fmaf(a, c, ev - h) > kWeightTop;
-            if (!__any_sync(RQ_FULL_MASK, over)) return;
+          // rows of `over` get Rn for R, and an h that makes the largest of 2^(wn - h) 2^kWeightHead
+          auto raise = [&](bool over, float Rn, float wn) {
             float f = 1.f, fo = 1.f;                           // of l, and of O
             if (over) {
-              const float Rn = fmaxf(R, top), hn = fmaf(top - Rn, c, ev - kWeightHead);
+              const float hn = wn - kWeightHead;
               if (R == -INFINITY) {
                 f = fo = 0.f;
                 h = hn;
@@ -647,7 +654,12 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
                 mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 4])));
 #pragma unroll
             for (int y = kKeys - 4; y < kKeys; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
-            raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq, INFINITY);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq;
+            const bool over = R == -INFINITY ? top > R : fmaf(top - R, c, ev - h) > kWeightTop;
+            if (__any_sync(RQ_FULL_MASK, over)) {
+              const float Rn = fmaxf(R, top);
+              raise(over, Rn, fmaf(top - Rn, c, ev));
+            }
             slow = huge;
             if (!slow) {
               const float mul = kq * c, add = fmaf(R == -INFINITY ? 0.f : -R, c, ev - h);
@@ -676,27 +688,43 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
           }
           if (slow) {
             // careful: scores as q K (the power of two in two steps, of the same direction), and differences
-            // before the product with c, exactly: scores of any size cancel without a residue.  Twice over the
-            // scores in tensor memory, 32 keys at a time (the weights of some lie where only scores did that
-            // were read before).
-            const int x2 = ee.x + fe;
-            const float k1 = q8_pow2(x2 >> 1), k2 = q8_pow2(x2 - (x2 >> 1)) + (factor - factor);   // (no number: stays so)
+            // before the product with c, exactly: scores of any size cancel without a residue.  Every block has
+            // its own exponents.  Twice over the scores in tensor memory, 32 keys at a time (the weights of some
+            // lie where only scores did that were read before).
+            const uint4 eb = *reinterpret_cast<const uint4*>(image_exps<D>(a, w, t) + 2);
+            auto exponent = [](uint32_t lo, uint32_t hi, int b) { return int((b & 4 ? hi : lo) << (24 - 8 * (b & 3))) >> 24; };
             auto scores = [&](int y, float (&z)[32]) {
               uint32_t s[32];
               tc_ld32(tS + 32 * y, s);
               const uint32_t seen = (y >> 1 ? clear[1] : clear[0]) ? ~0u : seen_by(y >> 1, y & 1);
               tc_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) z[k] = seen >> k & 1u ? __uint_as_float(s[k]) * k1 * k2 : -INFINITY;
+              for (int b = 0; b < 2; ++b) {
+                const int x2 = exponent(eb.x, eb.y, 2 * y + b) + fe;
+                const float k1 = q8_pow2(x2 >> 1), k2 = q8_pow2(x2 - (x2 >> 1)) + (factor - factor);   // (no number: stays so)
+#pragma unroll
+                for (int k = 16 * b; k < 16 * b + 16; ++k) z[k] = seen >> k & 1u ? __uint_as_float(s[k]) * k1 * k2 : -INFINITY;
+              }
             };
-            float top = -INFINITY, z[32];
+            float Rn = R, wn = -INFINITY, z[32];               // the largest score; of the blocks' weights, against Rn
 #pragma unroll 1
             for (int y = 0; y < 4; ++y) {
               scores(y, z);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) top = fmaxf(top, z[k]);
+              for (int b = 0; b < 2; ++b) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 16 * b; k < 16 * b + 16; ++k) top = fmaxf(top, z[k]);
+                if (top > Rn) {
+                  wn += (Rn - top) * c;
+                  Rn = top;
+                }
+                wn = fmaxf(wn, fmaf(top - Rn, c, float(exponent(eb.z, eb.w, 2 * y + b))));   // (nothing so far: the first)
+              }
             }
-            raise(top, kWeightTop);
+            const float up = (Rn - R) * c;
+            const bool over = R == -INFINITY ? Rn > R : up > kWeightTop || wn + up - h > kWeightTop;
+            if (__any_sync(RQ_FULL_MASK, over)) raise(over, Rn, wn);
             const float r = R == -INFINITY ? 0.f : R;
 #pragma unroll 1
             for (int y = 0; y < 4; ++y) {
@@ -705,8 +733,9 @@ __global__ void __launch_bounds__(384, 1) q8_rows_kernel(const __grid_constant__
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float a0 = (z[2 * k] - r) * c, a1 = (z[2 * k + 1] - r) * c;
+                const float eh = float(exponent(eb.z, eb.w, 2 * y + k / 8)) - h;
                 l += ex2(a0) + ex2(a1);
-                p[k] = pack_half2(ex2(a0 + (ev - h)), ex2(a1 + (ev - h)));
+                p[k] = pack_half2(ex2(a0 + eh), ex2(a1 + eh));
               }
               tc_st16(tS + 16 * y, p);
               if (y & 1) weights_there(y >> 1);

@@ -115,7 +115,7 @@ def aimed(seed, n, G, d):
 @pytest.mark.parametrize("far", [12, 30, 60, 100])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("H", [1, 128])
-@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("n,G", FEW + MANY)
 def test_the_last_token_s_large_value_changes_no_earlier_output(n, G, fmt, far, H):
     T, d = slots_of(n), 128 if n % 8 else 64
     k, v, q = normal(1, T, d) / 2, normal(2, T, d), normal(3, n, G, d)
@@ -125,7 +125,7 @@ def test_the_last_token_s_large_value_changes_no_earlier_output(n, G, fmt, far, 
 
 @pytest.mark.parametrize("far", [12, 30, 60, 100])
 @pytest.mark.parametrize("H", [1, 128])
-@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("n,G", FEW + MANY)
 def test_a_large_value_that_left_the_window(n, G, far, H):
     """Only the first token's window reaches the slot; the other slots of its block are out of every window."""
     window, d = 289, 128 if n % 8 else 64
@@ -140,7 +140,7 @@ def test_a_large_value_that_left_the_window(n, G, far, H):
 @pytest.mark.parametrize("far", [12, 30, 38])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("H", [1, 128])
-@pytest.mark.parametrize("n,G", ONE + FEW)
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
 def test_large_values_of_no_weight(n, G, fmt, far, H):
     """A block whose values are 2^far larger at weights of e^-60."""
     T, d = slots_of(n, 300), 128 if n % 8 else 64
@@ -153,7 +153,7 @@ def test_large_values_of_no_weight(n, G, fmt, far, H):
 
 
 @pytest.mark.parametrize("H", [1, 128])
-@pytest.mark.parametrize("n,G", ONE + FEW)
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
 def test_values_of_many_sizes(n, G, H):
     """Every block of values of another size, 2^-90 to 2^100, its weights such that each matters somewhere."""
     for seed in range(4):
@@ -209,6 +209,31 @@ def test_zeros_beside_large_values(n, G, first, far, H):
     else:
         v[128:384] = 0
     close(Hand(k, v, q, "int8" if far % 4 else "e4m3", H).run())
+
+
+@pytest.mark.parametrize("far", [10, 16, 25, 30, 60])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", FEW + MANY)
+def test_the_last_token_s_large_key_changes_no_earlier_output(n, G, far, H):
+    T, d = slots_of(n), 128 if n % 8 else 64
+    k, v, q = normal(18, T, d), normal(19, T, d), normal(20, n, G, d)
+    k[-1] *= 2.0 ** far
+    v[-1] *= 2.0 ** far
+    close(Hand(k, v, q, "e4m3" if far % 4 else "int8", H).run(), slice(0, n - 1))
+
+
+@pytest.mark.parametrize("far", [10, 16, 25, 30, 60])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H", [1, 128])
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
+def test_large_keys_of_no_weight(n, G, fmt, far, H):
+    """A block of keys 2^far larger that point away from the queries: the other keys' scores decide."""
+    T, d = slots_of(n, 300), 128 if n % 8 else 64
+    q, u = aimed(21, n, G, d)
+    k, v = normal(22, T, d), normal(23, T, d)
+    for block in (slice(16, 32), slice(208, 224)):
+        k[block] = -u * d ** 0.5 * 2.0 ** far
+    close(Hand(k, v, q, fmt, H).run())
 
 
 @pytest.mark.parametrize("T", [100, 3000])
