@@ -131,6 +131,7 @@ def make_paging(block_table, n_pages):
     g.block_table = block_table.data_ptr()
     g.max_pages = block_table.shape[1]
     g.n_pages = int(n_pages)
+    g.sequences, g.device = block_table.shape[0], block_table.get_device()
     return g
 
 
@@ -346,7 +347,7 @@ class Q8Cache:
 
     def __init__(self, shape, device="cuda", n_pages=None, codes=None, scales=None):
         B, H, tiles, d, L = shape.batch, shape.n_kv_heads, shape.capacity // PAGE, shape.head_dim, shape.n_loops
-        self.shape, self.n_pages = shape, n_pages
+        self.shape, self.n_pages, self.key = shape, n_pages, bytes(shape)
         lead = (B, H, tiles) if n_pages is None else (n_pages, H)
         full = (*lead, L, 2, PAGE, d)
         n = q8_cache_bytes(shape) if n_pages is None else q8_paged_cache_bytes(shape, n_pages)
@@ -406,9 +407,28 @@ def _lens(t, B, dev):
     return t.data_ptr()
 
 
-def _q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
+def _q8_fits(shape, cache, paging):
+    """The library sees bare pointers: what a call of this shape reads and writes lies in the cache."""
+    if paging is None:
+        assert cache.n_pages is None, "a paged cache in a contiguous call"
+    else:
+        assert cache.n_pages is not None, "a contiguous cache in a paged call"
+        assert paging.n_pages <= cache.n_pages, "more pages than the cache has"
+        assert paging.sequences >= shape.batch, "fewer block-table rows than sequences"
+    if bytes(shape) == cache.key:
+        return
+    own = RqQ8Shape.from_buffer_copy(cache.key)
+    assert ((shape.n_kv_heads, shape.head_dim, shape.n_loops, shape.format) ==
+            (own.n_kv_heads, own.head_dim, own.n_loops, own.format)), "another layout than the cache's"
+    # (a pool serves any batch and any length; a contiguous cache its first sequences)
+    assert paging is not None or (shape.capacity == own.capacity and shape.batch <= own.batch), "a larger shape than the cache's"
+
+
+def _q8_append_args(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens, rope, stream):
+    _q8_fits(shape, cache, paging)
     B, n, two, loops, H, d = kv_new.shape
     dev = torch._C._cuda_getDevice()      # every tensor lies on the current device
+    assert paging is None or paging.device == dev
     assert kv_new.get_device() == cache.codes.get_device() == cache.scales.get_device() == dev
     s0, s1, s2, s3, s4, s5 = kv_new.stride()
     assert kv_new.dtype == torch.bfloat16 and (B, two, H, d) == (shape.batch, 2, shape.n_kv_heads, shape.head_dim)
@@ -422,7 +442,7 @@ def q8_append(shape, cache, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None
     slots from ctx_lens[b] on, of the loops from loop_begin on; n_lens int32 [B]; rope from make_rope."""
     check("rq_q8_append", _lib.lib().rq_q8_append(
         ctypes.byref(shape), ctypes.byref(cache.struct),
-        *_q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+        *_q8_append_args(shape, cache, None, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
 
 
 def paged_q8_append(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens=None, rope=None,
@@ -430,7 +450,7 @@ def paged_q8_append(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens=N
     """rq_paged_q8_append; the other arguments as in q8_append."""
     check("rq_paged_q8_append", _lib.lib().rq_paged_q8_append(
         ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
-        *_q8_append_args(shape, cache, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
+        *_q8_append_args(shape, cache, paging, kv_new, loop_begin, ctx_lens, n_lens, rope, stream)))
 
 
 def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
@@ -440,16 +460,18 @@ def q8_workspace_bytes(shape, n_new, max_ctx, window=0, n_sink=0):
                                                 int(window), int(n_sink)))
 
 
-def _q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
+def _q8_attention_args(shape, cache, paging, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope, stream):
+    _q8_fits(shape, cache, paging)
     B, n, Hq, d = q.shape
     dev = torch._C._cuda_getDevice()
+    assert paging is None or paging.device == dev
     assert (q.get_device() == out.get_device() == ws.get_device() == cache.codes.get_device() ==
             cache.scales.get_device() == dev)
     s0, s1, s2, s3 = q.stride()
     assert q.dtype == out.dtype == torch.bfloat16
     assert (B, Hq, d) == (shape.batch, shape.n_q_heads, shape.head_dim)
     assert s3 == 1 or q.numel() == 0
-    assert out.shape == q.shape and out.is_contiguous()
+    assert out.shape == q.shape and out.is_contiguous() and ws.is_contiguous()
     return (q.data_ptr(), _I3(s0, s1, s2), loop, _lens(n_lens, B, dev), n, _lens(ctx_lens, B, dev), max_ctx, window,
             n_sink, _rope(rope, B, n, dev), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
 
@@ -461,7 +483,7 @@ def q8_attention(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens=None,
     `window` and the first n_sink."""
     check("rq_q8_attention", _lib.lib().rq_q8_attention(
         ctypes.byref(shape), ctypes.byref(cache.struct),
-        *_q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+        *_q8_attention_args(shape, cache, None, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
                             stream)))
 
 
@@ -470,7 +492,7 @@ def paged_q8_attention(shape, cache, paging, q, loop, ctx_lens, max_ctx, out, ws
     """rq_paged_q8_attention; the other arguments as in q8_attention."""
     check("rq_paged_q8_attention", _lib.lib().rq_paged_q8_attention(
         ctypes.byref(shape), ctypes.byref(cache.struct), ctypes.byref(paging),
-        *_q8_attention_args(shape, cache, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
+        *_q8_attention_args(shape, cache, paging, q, loop, ctx_lens, max_ctx, out, ws, n_lens, window, n_sink, rope,
                             stream)))
 
 
