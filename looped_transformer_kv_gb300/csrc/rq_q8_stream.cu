@@ -33,6 +33,7 @@ constexpr int kMostCtas = 1024;
 
 struct StreamArgs : Q8Line {
   uint8_t* queries;      // [B][Hkv][blocks] of StreamSmem::kQuery bytes
+  float tame_ks;         // K scales up to which their products with rows' factors stay in fp32's range
 };
 
 template <int D, int NT>
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
       }
       int E = kNoScale, t = 0;
-      // Tiles from t on; without APART up to one whose V scale is out of E's range.  (Two loops: as one, with
+      // Tiles from t on; without APART up to one whose V scale is out of E's range, or whose K scale is huge.  (Two loops: as one, with
       // the rows' h behind a branch, verification of 8 tokens took 121 us, now 112.)
       auto tiles = [&](auto apart) {
       constexpr bool APART = decltype(apart)::value;
@@ -436,6 +437,17 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) ksc[n][k] = cs[n][k] * ks;
+          if (APART && ks > a.tame_ks) {                    // (both factors huge: one by one, so that 0 stays 0)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (ksc[n][k] == INFINITY) {
+                  sc[n][k] *= cs[n][k];
+                  sc[n][k + 2] *= cs[n][k];
+                  ksc[n][k] = ks;
+                }
+          }
           if (!clear) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
               over |= sc[n][k] > m[n][k & 1] + kTop;
             }
           const int ev = q8_exponent(vs);
-          const bool lost = ev > 127, far = !APART && unsigned(ev - E - kScaleBelow + kScaleRange) > 2u * kScaleRange;
+          const bool lost = ev > 127, far = !APART && (unsigned(ev - E - kScaleBelow + kScaleRange) > 2u * kScaleRange || ks > a.tame_ks);
           const float evf = lost ? vs : float(ev);          // (NaN where the scale is)
           if (APART)
 #pragma unroll
@@ -468,7 +480,7 @@ __global__ void __launch_bounds__(StreamSmem<D, NT>::kThreads, StreamSmem<D, NT>
                 over |= (sc[n][k] - m[n][k & 1]) + (evf - heights[8 * n + 2 * c + (k & 1)]) > kWeightTop;
           if (__any_sync(RQ_FULL_MASK, over) || far) {
             if (far && !lost) {
-              if (E != kNoScale) return;                    // (here and not before the scores, which need not wait for it)
+              if (E != kNoScale || ks > a.tame_ks) return;  // (here and not before the scores, which need not wait for it)
               E = ev - kScaleBelow;
             }
 #pragma unroll
@@ -687,6 +699,7 @@ cudaError_t launch_q8_stream(const rq_q8_shape& s, const rq_q8_cache& cache, con
   const Q8Layout x = stream_layout(s, c.n_new, c.max_ctx, nt);
   q8_place(a, x, ws);
   a.queries = static_cast<uint8_t*>(ws) + x.total;
+  a.tame_ks = a.scale_log2 <= 64.f ? 256.f : 0.f;           // (factors: 2^113 scale_log2 at most)
   a.own_cut = int64_t(a.B) * a.blocks <= kOwnCutPairs;
   a.whole = a.own_cut && whole_units(a);
   const bool i8 = s.format == RQ_Q8_INT8, wide = s.head_dim == 128;

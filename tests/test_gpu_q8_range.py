@@ -264,3 +264,16 @@ def test_a_bad_page_spoils_only_tokens_that_see_it(n, Hq, fmt):
     assert torch.isnan(c.out[0, 2:].float()).all()
     # (the products are the same; a unit may be divided elsewhere)
     torch.testing.assert_close(c.out[0, :2].float(), want[0, :2].float(), rtol=2.0 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("qe,ke", [(100, 60), (120, 118), (126, 2), (2, 118), (-110, -90)])
+@pytest.mark.parametrize("n,G", ONE + FEW + MANY)
+def test_queries_and_keys_without_a_common_channel(n, G, qe, ke):
+    """Scores of exactly 0, whatever the sizes; some queries are zeros."""
+    T, d = n + 100, 64
+    k, v, q = normal(30, T, d) * 2.0 ** ke, normal(31, T, d), normal(32, n, G, d) * 2.0 ** qe
+    k, q = np.clip(k, -3e38, 3e38), np.clip(q, -3e38, 3e38)
+    k[:, ::2] = 0
+    q[:, :, 1::2] = 0
+    q[-16:, ::2] = 0
+    close(Hand(k, v, q, "int8" if ke % 4 else "e4m3").run())
