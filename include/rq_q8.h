@@ -110,14 +110,19 @@ rq_status rq_paged_q8_append(const rq_q8_shape* shape, const rq_q8_cache* cache,
  *              as n_new), ctx_len + n_len beyond the capacity, a bad block-table entry of a tile that is
  *              seen, or a pipeline wait that gave up; outputs of the sequences (of a bad page: of the
  *              tokens that see it) concerned are NaN.  Calls that share a workspace must not overlap on
- *              the GPU.
+ *              the GPU.  Up to 32 rows a kv-head (n_new * Hq / Hkv) it takes some MB; from 33 on it holds
+ *              fp16 operands, the queries' and twice the bytes of the loop's codes that are seen, for as many
+ *              sequences at a time as 2 GB hold, for one at least (a million slots of 8 heads of 128: 4.3 GB)
  * Only tiles that some new token sees are read; block-table entries of others may be anything, so
  * pages that fell out of the window may be given away.
  * Sizes: n_new * (Hq / Hkv) <= 2^22, B * Hkv * ceil(n_new * (Hq / Hkv) / 32) * (capacity / 64 + 1) <= 2^40,
  * B * Hq * n_new <= 2^31 (RQ_ERR_UNSUPPORTED).
- * Precision: codes enter the products exactly, scores, statistics and accumulators are fp32.  A
- * query is exact without rotation; rotated, and a softmax weight, is rounded once to fp16 (2^-11 of
- * itself).  No atomics on results: the same call gives the same bits. */
+ * Precision: codes enter the products exactly; q . k, its product with softmax_scale, statistics and
+ * accumulators are fp32.  A rotated query's element is rounded once to fp16 (2^-11 of itself); of any
+ * query, elements below 2^-31 of their row's largest to 2^-39 of that, and rows below 2^-96 to 2^-135.  A
+ * softmax weight times its block's V scale is rounded once to fp16: 2^-11 of itself, or 2^-24 of the largest
+ * such product that the row sees.  What a row does not see takes no bits from it.  No atomics on results:
+ * the same call gives the same bits. */
 size_t rq_q8_workspace_bytes(const rq_q8_shape* shape, int32_t n_new, int32_t max_ctx,
                              int32_t window, int32_t n_sink);
 rq_status rq_q8_attention(const rq_q8_shape* shape, const rq_q8_cache* cache, const uint16_t* q,

@@ -4,7 +4,8 @@
 //
 // Bound by instructions and occupancy (issue slots 73 % used): 1,024 tokens of 4 x 16 heads and 4 loops in 41 us
 // without rotation, 4.9 TB/s, 57 us rotated.  A whole block a warp took 110 registers and 51 us (75 rotated);
-// blocks of 256 threads, whose warps end together, 46 (77).
+// blocks of 256 threads, whose warps end together, 46 (77).  Head dim 64 takes a whole block a warp and spills
+// some 25 registers for it.
 #include <algorithm>
 
 #include "rq_kernels.h"

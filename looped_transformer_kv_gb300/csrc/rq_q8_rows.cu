@@ -19,7 +19,7 @@
 //
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row; warp 8: products; warp 9: copies.
 // Bound by a row tile's chain, softmax and then products, two tiles taking turns: 2,048 tokens of 32 heads
-// after 14,336 slots in 338 us, 1,520 TFLOP/s.
+// after 14,336 slots in 331 us, 1,560 TFLOP/s.
 // CTAs (one per SM) share the work by the line of rq_q8_line.cuh; q8_join_kernel joins the partial results
 // of divided units (in this kernel the code for it cost the main loop its registers: 460 against 375 us).
 #include <type_traits>
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(2 * D) q8_join_kernel(const __grid_constant__ 
   }
 }
 
-// Bytes of the operand tiles of one sequence, and of one unit's list.
+// Key tiles of one unit's list, at most.
 template <typename Shape>
 int rows_list(const Shape& s, int n_new, int max_ctx, int window, int n_sink) {
   int64_t slots = std::min<int64_t>(int64_t(max_ctx) + n_new, s.capacity), tiles = (slots + 63) / 64;

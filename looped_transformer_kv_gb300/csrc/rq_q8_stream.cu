@@ -17,7 +17,7 @@
 // One row or a few: bound by HBM while it streams (16 x 16 heads: 7.3 TB/s from 8,192 to 16,384 slots), by
 // launches, first tiles and joins at short contexts (4,096 slots in 55 us, 40 at a copy's rate).  32 rows: by
 // the latency of each warp's scores, softmax and values, two warps a scheduler (8 x 8 heads after 16,384
-// slots in 109 us).
+// slots in 107 us).
 #include <type_traits>
 
 #include "rq_q8_line.cuh"
